@@ -404,6 +404,195 @@ ssd_status ssd_chain_states(const float *contrib, const float *log_decay, const 
                             int nranges, int batch, int nheads, int headdim, int dstate,
                             float *entering, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The steps of a layer around such a recurrence: the root-mean-square norm
+ * with the residual's addition, the matrix product with bias, activation and
+ * residual in its epilogue, and a gated linear recurrence that is elementwise
+ * over the channels.  Each is given forward and backward.  The pages do not
+ * build them; the formulas below are their definition.
+ *
+ * Matrices are row-major with unit-stride columns; an argument `name_stride`
+ * is the distance of two rows in elements (at least the row's width), so a
+ * column range of a wider matrix can be passed as it lies.  Arrays without a
+ * stride argument are contiguous.  Outputs must not overlap inputs unless an
+ * entry point says so.  Pointers need the alignment of their element type (4
+ * bytes for E4M3 rows read by ssd_linear_fwd); 16-byte aligned pointers and
+ * strides take the vector paths.  Sums, statistics, states and gradients in
+ * flight are fp32; each output is rounded once.
+ *
+ * Root-mean-square norm of the residual stream s = x + residual:
+ *     s = x + residual            (s = x when residual is NULL)
+ *     rstd = (mean_j s_j^2 + eps)^(-1/2)          over the row's `width` values
+ *     y_j = s_j rstd weight_j
+ * computed from the unrounded s.
+ *   x             x_dtype (SSD_F32 or SSD_BF16) [rows][width], x_stride.
+ *   residual      stream_dtype [rows][width], residual_stride, or NULL.
+ *                 stream_dtype is x_dtype or SSD_F32.
+ *   weight        float [width].  eps >= 0.
+ *   y             out_dtype [rows][width]: SSD_F32, SSD_BF16, or SSD_FP8_E4M3
+ *                 with one scale a row: scale = max_j |y_j| / 448 (1 for a row
+ *                 of zeros), y holds y_j / scale rounded to nearest even.
+ *   residual_out  stream_dtype [rows][width]: s.  Required with a residual
+ *                 (may be the residual itself), ignored without.
+ *   rstd          float [rows].  scale: float [rows], required for 8-bit
+ *                 outputs, ignored otherwise.
+ * rows == 0 enqueues nothing.  SSD_ERR_INVALID_ARG for null pointers, width
+ * <= 0, rows < 0, strides below width, eps < 0 or NaN; SSD_ERR_UNSUPPORTED
+ * for other types, rows >= 2^31 or width >= 2^24. */
+ssd_status ssd_rmsnorm_fwd(const void *x, const void *residual, const float *weight, float eps,
+                           ssd_dtype x_dtype, ssd_dtype stream_dtype, ssd_dtype out_dtype,
+                           long long rows, int width, long long x_stride,
+                           long long residual_stride, void *y, void *residual_out, float *rstd,
+                           float *scale, cudaStream_t stream);
+
+/* Gradients of ssd_rmsnorm_fwd.  With e_j = dy_j weight_j:
+ *     ds_j = dresidual_j + rstd (e_j - s_j rstd^2 mean_i(e_i s_i))
+ *     dweight_j = sum over rows of dy_j s_j rstd
+ * ds is the gradient of x and of the residual alike.  An 8-bit output is
+ * treated as the unrounded one: dy is the gradient of y.
+ *   dy          dtype (SSD_F32 or SSD_BF16) [rows][width], dy_stride.
+ *   s           stream_dtype (dtype or SSD_F32) [rows][width], s_stride: the
+ *               residual_out of the forward call (or its x).
+ *   rstd        float [rows], of the forward call.
+ *   dresidual   stream_dtype [rows][width], dresidual_stride: the gradient
+ *               that reached residual_out from elsewhere, or NULL.
+ *   dx          dtype [rows][width].  ds: stream_dtype [rows][width], or NULL.
+ *   dweight     float [width]; the sum's order is fixed for given sizes.
+ *   workspace   ssd_rmsnorm_bwd_workspace_bytes() bytes, 16-byte aligned.
+ * Errors as ssd_rmsnorm_fwd, and SSD_ERR_WORKSPACE.  rows == 0 writes zeros
+ * to dweight. */
+ssd_status ssd_rmsnorm_bwd(const void *dy, const void *s, const float *weight, const float *rstd,
+                           const void *dresidual, ssd_dtype dtype, ssd_dtype stream_dtype,
+                           long long rows, int width, long long dy_stride, long long s_stride,
+                           long long dresidual_stride, void *dx, void *ds, float *dweight,
+                           void *workspace, size_t workspace_bytes, cudaStream_t stream);
+/* Workspace of ssd_rmsnorm_bwd on the current device; (size_t)-1 for invalid sizes. */
+size_t ssd_rmsnorm_bwd_workspace_bytes(long long rows, int width);
+
+/* The activation of ssd_linear_fwd: p, p / (1 + e^-p), p (1 + erf(p / sqrt 2)) / 2, max(p, 0). */
+typedef enum {
+    SSD_ACT_NONE = 0,
+    SSD_ACT_SILU = 1,
+    SSD_ACT_GELU = 2,
+    SSD_ACT_RELU = 3
+} ssd_activation;
+
+/* Matrix product with its epilogue:
+ *     p[m][n] = (sum_k x[m][k] w[n][k]) x_scale[m] w_scale[n] + bias[n]
+ *     y[m][n] = act(p[m][n]) + residual[m][n]
+ *   x           in_dtype [tokens][inner], x_stride.
+ *   w           in_dtype [features][inner].
+ *   x_scale     float [tokens], w_scale float [features]: required for
+ *               SSD_FP8_E4M3 (ssd_rmsnorm_fwd writes such rows), NULL otherwise.
+ *   bias        float [features] or NULL.
+ *   residual    out_dtype [tokens][features], residual_stride, or NULL.
+ *   y           out_dtype [tokens][features], y_stride.  out_dtype: SSD_BF16
+ *               or SSD_F32 for bf16 and fp8 inputs, SSD_F32 for fp32 inputs.
+ *               y may be the residual itself (same pointer and stride).
+ *   preact      p, contiguous, SSD_F32 for fp32 inputs and SSD_BF16 otherwise,
+ *               or NULL: what ssd_linear_bwd needs of the forward call.
+ *   workspace   ssd_linear_workspace_bytes() bytes, 256-byte aligned (may be
+ *               NULL when that is 0).
+ * bf16 and fp8 inputs whose rows start on 16-byte boundaries run on the
+ * tensor cores (products of the inputs as they are, fp32 sums); fp32 inputs
+ * and other alignments in fp32 multiply-adds.  tokens == 0 enqueues nothing.
+ * SSD_ERR_INVALID_ARG for null pointers, sizes, strides or enums out of range;
+ * SSD_ERR_UNSUPPORTED for type combinations not listed and for sizes of 2^31 - 256
+ * tokens or 2^22 features or more. */
+ssd_status ssd_linear_fwd(const void *x, const float *x_scale, const void *w,
+                          const float *w_scale, const float *bias, const void *residual,
+                          ssd_activation activation, ssd_dtype in_dtype, ssd_dtype out_dtype,
+                          long long tokens, int features, int inner, long long x_stride,
+                          long long residual_stride, void *y, long long y_stride, void *preact,
+                          void *workspace, size_t workspace_bytes, cudaStream_t stream);
+size_t ssd_linear_workspace_bytes(ssd_dtype in_dtype, long long tokens, int features, int inner);
+
+/* Gradients of ssd_linear_fwd (fp32 or bf16 inputs).  With dp = dy act'(preact):
+ *     dx[m][k] = sum_n dp[m][n] w[n][k]
+ *     dw[n][k] = sum_m dp[m][n] x[m][k]
+ *     dbias[n] = sum_m dp[m][n]
+ * (the residual's gradient is dy itself).  dp is rounded to dtype before the
+ * two products and not before dbias.
+ *   dy          dtype [tokens][features], dy_stride.
+ *   preact      dtype [tokens][features], contiguous; NULL with SSD_ACT_NONE.
+ *   dx          dtype [tokens][inner], contiguous, or NULL: not wanted.
+ *   dw          dtype [features][inner], contiguous, or NULL.
+ *   dbias       float [features] or NULL.
+ *   workspace   ssd_linear_bwd_workspace_bytes() bytes, 256-byte aligned.
+ * tokens == 0 writes zeros to dw and dbias.  Sums run in an order fixed for
+ * given sizes.  Errors as ssd_linear_fwd, and SSD_ERR_WORKSPACE; here inner
+ * too stays below 2^22. */
+ssd_status ssd_linear_bwd(const void *dy, const void *x, const void *w, const void *preact,
+                          ssd_activation activation, ssd_dtype dtype, long long tokens,
+                          int features, int inner, long long dy_stride, long long x_stride,
+                          void *dx, void *dw, float *dbias, void *workspace,
+                          size_t workspace_bytes, cudaStream_t stream);
+size_t ssd_linear_bwd_workspace_bytes(ssd_dtype dtype, ssd_activation activation,
+                                      long long tokens, int features, int inner);
+
+/* Gated linear recurrence, elementwise over `width` channels:
+ *     f_t = sigmoid(g_t)
+ *     h_t = f_t h_{t-1} + (1 - f_t) x_t
+ *     y_t = h_t silu(z_t)                  (y_t = h_t when z is NULL)
+ * over nseq sequences laid end to end on one axis of `tokens` tokens.
+ *   x, g, z, y   dtype (SSD_F32 or SSD_BF16) [tokens][width], each with its
+ *                row stride.
+ *   length       tokens of each sequence (tokens = nseq * length), when
+ *                cu_seqlens_host is NULL.
+ *   cu_seqlens_host, cu_seqlens_dev   offsets of sequences of any lengths
+ *                (nseq + 1 ints, host and device copies) as in
+ *                ssd_scan_fwd_varlen; both or neither.  `length` is then ignored.
+ *   init_state   float [nseq][width] or NULL (zeros).
+ *   final_state  float [nseq][width] or NULL.  An empty sequence's final state
+ *                is its initial one.
+ *   checkpoints  float [ceil(tokens / 64)][width] or NULL: the state before
+ *                tokens 0, 64, 128, ... of the token axis (a sequence's first
+ *                token has its initial state there): what ssd_gated_scan_bwd
+ *                needs of the forward call.
+ *   workspace    ssd_gated_scan_workspace_bytes() bytes, 256-byte aligned (may
+ *                be NULL when that is 0); no initialisation needed.
+ * SSD_ERR_INVALID_ARG for null pointers, sizes <= 0 (length 0 is allowed),
+ * strides below width or offsets that do not start at 0 or decrease;
+ * SSD_ERR_UNSUPPORTED for other types, width >= 2^21, or 2^31 - 2048 tokens or more. */
+ssd_status ssd_gated_scan_fwd(const void *x, const void *g, const void *z, ssd_dtype dtype,
+                              int nseq, int length, const int *cu_seqlens_host,
+                              const int *cu_seqlens_dev, int width, long long x_stride,
+                              long long g_stride, long long z_stride, const float *init_state,
+                              void *y, long long y_stride, float *final_state,
+                              float *checkpoints, void *workspace, size_t workspace_bytes,
+                              cudaStream_t stream);
+size_t ssd_gated_scan_workspace_bytes(ssd_dtype dtype, long long tokens, int width);
+
+/* Gradients of ssd_gated_scan_fwd.  With dh_t = dy_t silu(z_t), plus dfinal at
+ * a sequence's last token, and lam_t = dh_t + f_{t+1} lam_{t+1} inside it:
+ *     dx_t = (1 - f_t) lam_t
+ *     dg_t = lam_t (h_{t-1} - x_t) f_t (1 - f_t)
+ *     dz_t = dy_t h_t silu'(z_t)
+ *     dinit = f_0 lam_0                     (dfinal for an empty sequence)
+ * x, g, z, init_state, offsets and checkpoints as in (and of) the forward call.
+ *   dy, dx, dg, dz   dtype [tokens][width] with row strides; dz is required
+ *                    with z and ignored without.
+ *   dfinal, dinit    float [nseq][width] or NULL.
+ *   workspace        ssd_gated_scan_workspace_bytes() bytes.
+ * h is recomputed in fp32 from the checkpoints. */
+ssd_status ssd_gated_scan_bwd(const void *dy, const void *x, const void *g, const void *z,
+                              ssd_dtype dtype, int nseq, int length, const int *cu_seqlens_host,
+                              const int *cu_seqlens_dev, int width, long long dy_stride,
+                              long long x_stride, long long g_stride, long long z_stride,
+                              const float *init_state, const float *checkpoints,
+                              const float *dfinal, void *dx, long long dx_stride, void *dg,
+                              long long dg_stride, void *dz, long long dz_stride, float *dinit,
+                              void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* One token of the gated recurrence: state float [rows][width], read and
+ * updated in place; x, g, z (or NULL) and y dtype [rows][width], x, g and z
+ * with row strides.  y may be x, g or z itself when that is contiguous.  rows
+ * == 0 enqueues nothing. */
+ssd_status ssd_gated_state_update(float *state, const void *x, const void *g, const void *z,
+                                  ssd_dtype dtype, long long rows, int width, long long x_stride,
+                                  long long g_stride, long long z_stride, void *y,
+                                  cudaStream_t stream);
+
 /* Human-readable name of a status code (static storage). */
 const char *ssd_status_string(ssd_status s);
 

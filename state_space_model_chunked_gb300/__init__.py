@@ -13,6 +13,16 @@ cannot load, every call raises.
     y = state_update(state, x, dt, A, B, C, D)          # state updated in place
     y = state_update_multi(state, x, dt, A, B, C, D)    # T tokens [b,T,H,P] in one call
     pipe = HostScanPipeline(); pipe.submit(..., out=(y_host, final_host))  # host tensors
+
+The steps of a layer around such a recurrence, each with its gradients:
+
+    y, stream, rstd, scale = rmsnorm_fwd(x, weight, residual)          # scale: 8-bit outputs
+    dx, dstream, dweight = rmsnorm_bwd(dy, stream, weight, rstd, dstream)
+    y = linear_fwd(x, w, bias, residual, activation="silu")            # bf16, f32, or E4M3 with scales
+    dx, dw, dbias = linear_bwd(dy, x, w, preact, activation="silu")
+    y, final = gated_scan_fwd(x, g, z, init_state)                     # also packed sequences
+    dx, dg, dz, dinit = gated_scan_bwd(dy, x, g, checkpoints, z, init_state, dfinal)
+    y = gated_state_update(state, x, g, z)                             # one token, state in place
 """
 from __future__ import annotations
 
@@ -43,4 +53,19 @@ from ._binding import (  # noqa: F401
     fp8_e4m3_to_bf16,
     range_log_decay,
     chain_states,
+)
+from .layer_ops import (  # noqa: F401
+    ACTIVATIONS,
+    GATED_SCAN_CHECKPOINT,
+    gated_scan_bwd,
+    gated_scan_fwd,
+    gated_scan_workspace_bytes,
+    gated_state_update,
+    linear_bwd,
+    linear_bwd_workspace_bytes,
+    linear_fwd,
+    linear_workspace_bytes,
+    rmsnorm_bwd,
+    rmsnorm_bwd_workspace_bytes,
+    rmsnorm_fwd,
 )

@@ -33,6 +33,17 @@ EXPORTED_SYMBOLS = (
     "ssd_fp8_e4m3_to_bf16",
     "ssd_range_log_decay",
     "ssd_chain_states",
+    "ssd_rmsnorm_fwd",
+    "ssd_rmsnorm_bwd",
+    "ssd_rmsnorm_bwd_workspace_bytes",
+    "ssd_linear_fwd",
+    "ssd_linear_workspace_bytes",
+    "ssd_linear_bwd",
+    "ssd_linear_bwd_workspace_bytes",
+    "ssd_gated_scan_fwd",
+    "ssd_gated_scan_bwd",
+    "ssd_gated_scan_workspace_bytes",
+    "ssd_gated_state_update",
 )
 
 ALGO_AUTO, ALGO_SIMT, ALGO_TCGEN05 = 0, 1, 2
@@ -126,6 +137,31 @@ def load():
         lib.ssd_range_log_decay.argtypes = [_vp, _vp, _vp, _int, _int, _int, _vp, _vp]
         lib.ssd_chain_states.restype = _int
         lib.ssd_chain_states.argtypes = [_vp, _vp, _vp] + [_int] * 5 + [_vp, _vp]
+        ll, f32 = ctypes.c_longlong, ctypes.c_float
+        layer = {
+            "ssd_rmsnorm_fwd": [_vp, _vp, _vp, f32, _int, _int, _int, ll, _int, ll, ll, _vp, _vp,
+                                _vp, _vp, _vp],
+            "ssd_rmsnorm_bwd": [_vp] * 5 + [_int, _int, ll, _int, ll, ll, ll] + [_vp] * 4 +
+                               [_sz, _vp],
+            "ssd_rmsnorm_bwd_workspace_bytes": [ll, _int],
+            "ssd_linear_fwd": [_vp] * 6 + [_int] * 3 + [ll, _int, _int, ll, ll, _vp, ll, _vp, _vp,
+                                                        _sz, _vp],
+            "ssd_linear_workspace_bytes": [_int, ll, _int, _int],
+            "ssd_linear_bwd": [_vp] * 4 + [_int, _int, ll, _int, _int, ll, ll] + [_vp] * 4 +
+                              [_sz, _vp],
+            "ssd_linear_bwd_workspace_bytes": [_int, _int, ll, _int, _int],
+            "ssd_gated_scan_fwd": [_vp] * 3 + [_int] * 3 + [_vp, _vp, _int, ll, ll, ll, _vp, _vp,
+                                                            ll, _vp, _vp, _vp, _sz, _vp],
+            "ssd_gated_scan_bwd": [_vp] * 4 + [_int] * 3 + [_vp, _vp, _int, ll, ll, ll, ll, _vp,
+                                                            _vp, _vp, _vp, ll, _vp, ll, _vp, ll,
+                                                            _vp, _vp, _sz, _vp],
+            "ssd_gated_scan_workspace_bytes": [_int, ll, _int],
+            "ssd_gated_state_update": [_vp] * 4 + [_int, ll, _int, ll, ll, ll, _vp, _vp],
+        }
+        for name, args in layer.items():
+            fn = getattr(lib, name)
+            fn.restype = _sz if name.endswith("_bytes") else _int
+            fn.argtypes = args
         _lib = lib
         return lib
 

@@ -241,6 +241,8 @@ size_t scan_workspace(int batch, int seqlen, int nheads, int headdim, int dstate
 }  // namespace
 
 SsdDebug ssd_debug_config() { return g_debug; }
+unsigned int *ssd_device_error_word() { return device_error_word(); }
+int ssd_sm_count() { return current_sm_count(); }
 
 extern "C" {
 

@@ -115,3 +115,116 @@ cudaError_t ssd_launch_scan_tc(const SsdTcPlan &plan, const void *x, const float
                                void *workspace, unsigned int *err, const SsdFuse &fuse,
                                SsdProfileEvents prof, cudaStream_t stream,
                                const int *cu_dev = nullptr);
+
+// ------------------------------------------------ the steps around the scan
+// What the layer's other kernels share with the ABI layer: the current
+// device's error word and its number of SMs.
+unsigned int *ssd_device_error_word();
+int ssd_sm_count();
+
+// Element types of the layer's operators.
+enum SsdElt { SSD_ELT_F32 = 0, SSD_ELT_BF16 = 1, SSD_ELT_E4M3 = 2 };
+
+// Root-mean-square norm (rmsnorm.cu).  `in`: the type of x (forward) and of dy
+// and dx (backward); `stream_type`: that of the residual stream.
+struct SsdNormFwd {
+    const void *x, *residual;
+    const float *weight;
+    float eps;
+    SsdElt in, stream_type, out;
+    long long rows;
+    int width;
+    long long x_stride, residual_stride;
+    void *y, *residual_out;
+    float *rstd, *scale;
+};
+cudaError_t ssd_launch_rmsnorm_fwd(const SsdNormFwd &a, int sms, cudaStream_t stream);
+
+struct SsdNormBwd {
+    const void *dy, *s, *dresidual;
+    const float *weight, *rstd;
+    SsdElt in, stream_type;
+    long long rows;
+    int width;
+    long long dy_stride, s_stride, dresidual_stride;
+    void *dx, *ds;
+    float *dweight;
+};
+size_t ssd_rmsnorm_bwd_workspace(long long rows, int width, int sms);
+cudaError_t ssd_launch_rmsnorm_bwd(const SsdNormBwd &a, float *partial, int sms,
+                                   cudaStream_t stream);
+
+// Gated linear recurrence (gated_scan.cu) over `tokens` tokens laid end to
+// end: nseq sequences of `length` tokens each, or, with cu (device, nseq + 1
+// offsets), of any lengths.
+constexpr int kSsdCheckpointTokens = 64;
+struct SsdGated {
+    const void *x, *g, *z;
+    const float *init;
+    bool bf16;
+    long long tokens;
+    int nseq, length, width;
+    const int *cu;
+    long long x_stride, g_stride, z_stride;
+};
+struct SsdGatedFwd {
+    SsdGated in;
+    void *y;
+    long long y_stride;
+    float *final_state, *checkpoints;
+};
+struct SsdGatedBwd {
+    SsdGated in;
+    const void *dy;
+    const float *dfinal, *checkpoints;
+    long long dy_stride, dx_stride, dg_stride, dz_stride;
+    void *dx, *dg, *dz;
+    float *dinit;
+};
+cudaError_t ssd_launch_gated_fwd(const SsdGatedFwd &a, int sms, cudaStream_t stream);
+cudaError_t ssd_launch_gated_bwd(const SsdGatedBwd &a, int sms, cudaStream_t stream);
+struct SsdGatedStep {
+    float *state;
+    const void *x, *g, *z;
+    bool bf16;
+    long long rows;
+    int width;
+    long long x_stride, g_stride, z_stride;
+    void *y;
+};
+cudaError_t ssd_launch_gated_step(const SsdGatedStep &a, cudaStream_t stream);
+
+// Matrix product with a fused epilogue: out[m][n] = act(sum_k A(m,k) B(n,k)
+// * a_scale[m] * b_scale[n] + bias[n]) + residual[m][n].
+enum class SsdAct { none = 0, silu = 1, gelu = 2, relu = 3 };
+struct SsdProduct {
+    // element (row, k) of A at a[row * a_row + k * a_col]; one of the two
+    // strides is 1.  B likewise by its rows n.
+    const void *a, *b;
+    SsdElt in;
+    long long m, n, k;
+    long long a_row, a_col, b_row, b_col;
+    const float *a_scale, *b_scale, *bias;
+    const void *residual;        // of the output's type
+    long long residual_row;
+    SsdAct act;
+    void *out, *preact;          // preact: of type preact_type, rows of n values, or null
+    SsdElt out_type, preact_type;
+    long long out_row;
+};
+cudaError_t ssd_launch_product_simt(const SsdProduct &p, cudaStream_t stream);
+
+// dp = dy act'(preact) (dp null: not stored) and the column sums of dp
+// (dbias null: none; `partial` holds ssd_act_bwd_workspace bytes).
+struct SsdActBwd {
+    const void *dy, *preact;
+    SsdElt type;
+    SsdAct act;
+    long long rows;
+    int width;
+    long long dy_stride;
+    void *dp;
+    float *dbias;
+};
+size_t ssd_act_bwd_workspace(long long rows, int width, int sms);
+cudaError_t ssd_launch_act_bwd(const SsdActBwd &a, float *partial, int sms, cudaStream_t stream);

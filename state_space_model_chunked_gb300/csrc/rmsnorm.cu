@@ -1,0 +1,386 @@
+// Root-mean-square norm of s = x + residual, forward (with an 8-bit output
+// and its row scales) and backward.
+//
+//   s = x + r,  rstd = (mean_j s_j^2 + eps)^(-1/2),  y_j = s_j rstd w_j
+//   8 bits: scale = max_j |y_j| / 448 (1 for a row of zeros), q = e4m3(y / scale)
+//   backward, with e_j = dy_j w_j:
+//     ds_j = ds_out_j + rstd (e_j - s_j rstd^2 mean_i(e_i s_i))
+//     dw_j = sum over rows of dy_j s_j rstd
+//
+// Both are bound by memory: every value is read once and written once, the
+// sums stay in fp32, and each result is rounded once.  One CTA holds one row
+// in registers (kC runs of V values a thread), so the row's sum and the row's
+// largest |s w| come from one pass and one barrier: max |y| = rstd max |s w|.
+#include "launch.h"
+#include "vec.cuh"
+
+namespace {
+
+constexpr float kE4m3Max = 448.f;
+constexpr int kMostWarps = 16;      // a row's CTA: 128 registers a thread
+constexpr int kRuns8 = 4, kRuns1 = 16;   // most runs a thread, of 8 values and of one
+
+// The CTA's sum and maximum over its warps (any number of them up to 32).
+__device__ __forceinline__ void cta_sum_max(float &sum, float &mx, float (*buf)[32]) {
+    sum = ssd_warp_sum(sum);
+    mx = ssd_warp_max(mx);
+    const int warps = blockDim.x >> 5;
+    if (warps == 1) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) {
+        buf[0][warp] = sum;
+        buf[1][warp] = mx;
+    }
+    __syncthreads();
+    sum = ssd_warp_sum(lane < warps ? buf[0][lane] : 0.f);
+    mx = ssd_warp_max(lane < warps ? buf[1][lane] : 0.f);
+}
+
+// The scale of an 8-bit row and the rounding of one of its values.  Below
+// 1e-30 the reciprocal of the scale would leave fp32's range, so those rows
+// divide.
+struct RowScale {
+    float scale, inv;
+    bool tiny;
+    __device__ __forceinline__ explicit RowScale(float amax) {
+        scale = amax == 0.f ? 1.f : amax / kE4m3Max;
+        tiny = scale < 1e-30f;
+        inv = 1.f / scale;
+    }
+    __device__ __forceinline__ float apply(float y) const { return tiny ? y / scale : y * inv; }
+};
+
+template <typename TX, typename TR, typename TO, int V, int kC>
+__global__ void __launch_bounds__(32 * kMostWarps) rmsnorm_fwd_kernel(const SsdNormFwd a) {
+    __shared__ float buf[2][32];
+    constexpr bool kFp8 = sizeof(TO) == 1;
+    const long long row = blockIdx.x;
+    const TX *x = static_cast<const TX *>(a.x) + row * a.x_stride;
+    const TR *r = a.residual ? static_cast<const TR *>(a.residual) + row * a.residual_stride
+                             : nullptr;
+    const int nvec = a.width / V;
+    SsdRaw<TX, V> xr[kC];
+    SsdRaw<TR, V> rr[kC];
+#pragma unroll
+    for (int c = 0; c < kC; ++c) {
+        const int i = threadIdx.x + c * blockDim.x;
+        if (i < nvec) {
+            xr[c].load_cs(x + (size_t)i * V);
+            if (r) rr[c].load_cs(r + (size_t)i * V);
+        } else {
+            xr[c].zero();
+        }
+        if (!r || i >= nvec) rr[c].zero();
+    }
+    float s[kC][V], sum = 0.f, mx = 0.f;
+#pragma unroll
+    for (int c = 0; c < kC; ++c) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            s[c][k] = r ? xr[c].get(k) + rr[c].get(k) : xr[c].get(k);
+            sum += s[c][k] * s[c][k];
+        }
+        if constexpr (kFp8) {
+            const int i = threadIdx.x + c * blockDim.x;
+            if (i < nvec) {
+#pragma unroll
+                for (int k = 0; k < V; ++k)
+                    mx = fmaxf(mx, fabsf(s[c][k] * __ldg(a.weight + (size_t)i * V + k)));
+            }
+        }
+    }
+    if (r) {
+        TR *so = static_cast<TR *>(a.residual_out) + row * a.width;
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+            const int i = threadIdx.x + c * blockDim.x;
+            if (i < nvec) ssd_store_vec<V>(so + (size_t)i * V, s[c]);
+        }
+    }
+    cta_sum_max(sum, mx, buf);
+    const float rstd = rsqrtf(sum / (float)a.width + a.eps);
+    const RowScale q(kFp8 ? mx * rstd : 0.f);
+    if (threadIdx.x == 0) {
+        a.rstd[row] = rstd;
+        if constexpr (kFp8) a.scale[row] = q.scale;
+    }
+    TO *y = static_cast<TO *>(a.y) + row * a.width;
+#pragma unroll
+    for (int c = 0; c < kC; ++c) {
+        const int i = threadIdx.x + c * blockDim.x;
+        if (i >= nvec) continue;
+        float o[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            o[k] = s[c][k] * rstd * __ldg(a.weight + (size_t)i * V + k);
+            if constexpr (kFp8) o[k] = q.apply(o[k]);
+        }
+        ssd_store_vec<V>(y + (size_t)i * V, o);
+    }
+}
+
+// Rows too wide for the registers of a CTA: two passes over the row, the
+// second one out of L2.
+template <typename TX, typename TR, typename TO>
+__global__ void rmsnorm_fwd_wide_kernel(const SsdNormFwd a) {
+    __shared__ float buf[2][32];
+    constexpr bool kFp8 = sizeof(TO) == 1;
+    const long long row = blockIdx.x;
+    const TX *x = static_cast<const TX *>(a.x) + row * a.x_stride;
+    const TR *r = a.residual ? static_cast<const TR *>(a.residual) + row * a.residual_stride
+                             : nullptr;
+    float sum = 0.f, mx = 0.f;
+    for (int i = threadIdx.x; i < a.width; i += blockDim.x) {
+        const float s = r ? ssd_ld(x + i) + ssd_ld(r + i) : ssd_ld(x + i);
+        sum += s * s;
+        if constexpr (kFp8) mx = fmaxf(mx, fabsf(s * a.weight[i]));
+    }
+    cta_sum_max(sum, mx, buf);
+    const float rstd = rsqrtf(sum / (float)a.width + a.eps);
+    const RowScale q(kFp8 ? mx * rstd : 0.f);
+    if (threadIdx.x == 0) {
+        a.rstd[row] = rstd;
+        if constexpr (kFp8) a.scale[row] = q.scale;
+    }
+    TR *so = static_cast<TR *>(a.residual_out) + (r ? row * a.width : 0);
+    TO *y = static_cast<TO *>(a.y) + row * a.width;
+    for (int i = threadIdx.x; i < a.width; i += blockDim.x) {
+        const float s = r ? ssd_ld(x + i) + ssd_ld(r + i) : ssd_ld(x + i);
+        float o[1] = {s * rstd * a.weight[i]};
+        if constexpr (kFp8) o[0] = q.apply(o[0]);
+        ssd_store_vec<1>(y + i, o);
+        if (r) ssd_st(so + i, s);
+    }
+}
+
+// ------------------------------------------------------------------ backward
+// A CTA walks the rows b, b + grid, ...; each thread keeps its columns' share
+// of dw in registers over all of them and writes it once, as row b of the
+// partial sums that rmsnorm_dw_kernel adds.
+template <typename T, typename TS, int V, int kC>
+__global__ void __launch_bounds__(32 * kMostWarps)
+rmsnorm_bwd_kernel(const SsdNormBwd a, float *__restrict__ partial) {
+    __shared__ float buf[2][2][32];
+    const int nvec = a.width / V;
+    float dw[kC][V];
+#pragma unroll
+    for (int c = 0; c < kC; ++c)
+#pragma unroll
+        for (int k = 0; k < V; ++k) dw[c][k] = 0.f;
+    int turn = 0;
+    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+        const T *dy = static_cast<const T *>(a.dy) + row * a.dy_stride;
+        const TS *s = static_cast<const TS *>(a.s) + row * a.s_stride;
+        const TS *dres = a.dresidual
+                             ? static_cast<const TS *>(a.dresidual) + row * a.dresidual_stride
+                             : nullptr;
+        const float rstd = a.rstd[row];
+        SsdRaw<T, V> yr[kC];
+        SsdRaw<TS, V> sr[kC], dr[kC];
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+            const int i = threadIdx.x + c * blockDim.x;
+            if (i < nvec) {
+                yr[c].load_cs(dy + (size_t)i * V);
+                sr[c].load_cs(s + (size_t)i * V);
+                if (dres) dr[c].load_cs(dres + (size_t)i * V);
+            } else {
+                yr[c].zero();
+                sr[c].zero();
+            }
+            if (!dres || i >= nvec) dr[c].zero();
+        }
+        float e[kC][V], sum = 0.f, unused = 0.f;
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+            const int i = threadIdx.x + c * blockDim.x;
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const float dyv = yr[c].get(k), sv = sr[c].get(k);
+                e[c][k] = i < nvec ? dyv * __ldg(a.weight + (size_t)i * V + k) : 0.f;
+                sum += e[c][k] * sv;
+                dw[c][k] += dyv * (sv * rstd);
+            }
+        }
+        cta_sum_max(sum, unused, buf[turn]);
+        const float m = sum / (float)a.width * rstd * rstd;
+        T *dx = static_cast<T *>(a.dx) + row * a.width;
+        TS *ds = a.ds ? static_cast<TS *>(a.ds) + row * a.width : nullptr;
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+            const int i = threadIdx.x + c * blockDim.x;
+            if (i >= nvec) continue;
+            float o[V];
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                o[k] = rstd * (e[c][k] - sr[c].get(k) * m);
+                if (dres) o[k] += dr[c].get(k);
+            }
+            ssd_store_vec<V>(dx + (size_t)i * V, o);
+            if (ds) ssd_store_vec<V>(ds + (size_t)i * V, o);
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < kC; ++c) {
+        const int i = threadIdx.x + c * blockDim.x;
+        if (i < nvec) ssd_store_vec<V>(partial + (size_t)blockIdx.x * a.width + (size_t)i * V, dw[c]);
+    }
+}
+
+// Rows too wide for a CTA's registers: the sums per row, then the columns.
+template <typename T, typename TS>
+__global__ void rmsnorm_bwd_wide_kernel(const SsdNormBwd a) {
+    __shared__ float buf[2][32];
+    const long long row = blockIdx.x;
+    const T *dy = static_cast<const T *>(a.dy) + row * a.dy_stride;
+    const TS *s = static_cast<const TS *>(a.s) + row * a.s_stride;
+    const TS *dres = a.dresidual ? static_cast<const TS *>(a.dresidual) + row * a.dresidual_stride
+                                 : nullptr;
+    const float rstd = a.rstd[row];
+    float sum = 0.f, unused = 0.f;
+    for (int i = threadIdx.x; i < a.width; i += blockDim.x)
+        sum += ssd_ld(dy + i) * a.weight[i] * ssd_ld(s + i);
+    cta_sum_max(sum, unused, buf);
+    const float m = sum / (float)a.width * rstd * rstd;
+    T *dx = static_cast<T *>(a.dx) + row * a.width;
+    TS *ds = a.ds ? static_cast<TS *>(a.ds) + row * a.width : nullptr;
+    for (int i = threadIdx.x; i < a.width; i += blockDim.x) {
+        float o = rstd * (ssd_ld(dy + i) * a.weight[i] - ssd_ld(s + i) * m);
+        if (dres) o += ssd_ld(dres + i);
+        ssd_st(dx + i, o);
+        if (ds) ssd_st(ds + i, o);
+    }
+}
+template <typename T, typename TS>
+__global__ void rmsnorm_dw_wide_kernel(const SsdNormBwd a, float *__restrict__ partial) {
+    const int j = blockIdx.y * blockDim.x + threadIdx.x;
+    if (j >= a.width) return;
+    float acc = 0.f;
+    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x)
+        acc += ssd_ld(static_cast<const T *>(a.dy) + row * a.dy_stride + j) *
+               (ssd_ld(static_cast<const TS *>(a.s) + row * a.s_stride + j) * a.rstd[row]);
+    partial[(size_t)blockIdx.x * a.width + j] = acc;
+}
+
+// out[j] = sum over the n partial rows, in a fixed order: 32 x 32 threads take
+// 32 columns, each of the 32 thread rows every 32nd partial row.
+__global__ void __launch_bounds__(1024)
+rmsnorm_dw_kernel(const float *__restrict__ partial, int n, int width, float *__restrict__ out) {
+    __shared__ float part[32][33];
+    const int j = blockIdx.x * 32 + threadIdx.x;
+    float acc = 0.f;
+    if (j < width)
+        for (int r = threadIdx.y; r < n; r += 32) acc += partial[(size_t)r * width + j];
+    part[threadIdx.y][threadIdx.x] = acc;
+    __syncthreads();
+    const float v = ssd_warp_sum(part[threadIdx.x][threadIdx.y]);
+    const int jo = blockIdx.x * 32 + threadIdx.y;
+    if (threadIdx.x == 0 && jo < width) out[jo] = v;
+}
+
+// Threads and runs a thread for one row: at most kC runs of V values, a power
+// of two of warps; 0 warps when the row does not fit.
+struct RowShape {
+    int warps, runs;
+};
+RowShape row_shape(int width, int V, int most_runs, bool few_rows) {
+    const int nvec = (width + V - 1) / V;
+    // few rows leave SMs idle: one run a thread, so the row is read in one step
+    const int want = few_rows ? 1 : most_runs;
+    int w = 1;
+    while (w < kMostWarps && (long long)w * 32 * want < nvec) w *= 2;
+    const int runs = (nvec + w * 32 - 1) / (w * 32);
+    return {runs <= most_runs ? w : 0, runs};
+}
+
+bool vec8(const void *p, long long stride, int size) {
+    return p == nullptr || (((uintptr_t)p & 15u) == 0 && (stride * size) % 16 == 0);
+}
+
+template <typename TX, typename TR, typename TO>
+cudaError_t launch_fwd(const SsdNormFwd &a, int sms, cudaStream_t stream) {
+    const bool v8 = a.width % 8 == 0 && vec8(a.x, a.x_stride, sizeof(TX)) &&
+                    vec8(a.residual, a.residual_stride, sizeof(TR)) &&
+                    vec8(a.residual_out, a.width, sizeof(TR)) && ((uintptr_t)a.y & 7u) == 0 &&
+                    vec8(sizeof(TO) == 1 ? nullptr : a.y, a.width, sizeof(TO));
+    const unsigned rows = (unsigned)a.rows;
+    const RowShape sh = row_shape(a.width, v8 ? 8 : 1, v8 ? kRuns8 : kRuns1, a.rows <= sms);
+    if (sh.warps == 0) {
+        rmsnorm_fwd_wide_kernel<TX, TR, TO><<<rows, 1024, 0, stream>>>(a);
+    } else if (v8) {
+        switch (sh.runs) {
+            case 1: rmsnorm_fwd_kernel<TX, TR, TO, 8, 1><<<rows, 32 * sh.warps, 0, stream>>>(a); break;
+            case 2: rmsnorm_fwd_kernel<TX, TR, TO, 8, 2><<<rows, 32 * sh.warps, 0, stream>>>(a); break;
+            case 3: rmsnorm_fwd_kernel<TX, TR, TO, 8, 3><<<rows, 32 * sh.warps, 0, stream>>>(a); break;
+            default: rmsnorm_fwd_kernel<TX, TR, TO, 8, 4><<<rows, 32 * sh.warps, 0, stream>>>(a); break;
+        }
+    } else {
+        rmsnorm_fwd_kernel<TX, TR, TO, 1, kRuns1><<<rows, 32 * sh.warps, 0, stream>>>(a);
+    }
+    return cudaGetLastError();
+}
+
+template <typename TX, typename TR>
+cudaError_t launch_fwd_out(const SsdNormFwd &a, int sms, cudaStream_t stream) {
+    switch (a.out) {
+        case SSD_ELT_F32: return launch_fwd<TX, TR, float>(a, sms, stream);
+        case SSD_ELT_BF16: return launch_fwd<TX, TR, __nv_bfloat16>(a, sms, stream);
+        default: return launch_fwd<TX, TR, __nv_fp8_e4m3>(a, sms, stream);
+    }
+}
+
+// CTAs of the backward pass: enough to fill the SMs, few enough that the
+// partial sums of dw stay small next to the rows.
+int bwd_ctas(long long rows, int sms) {
+    const long long most = 4ll * sms;
+    return (int)(rows < most ? rows : most);
+}
+
+template <typename T, typename TS>
+cudaError_t launch_bwd(const SsdNormBwd &a, float *partial, int sms, cudaStream_t stream) {
+    const bool v8 = a.width % 8 == 0 && vec8(a.dy, a.dy_stride, sizeof(T)) &&
+                    vec8(a.s, a.s_stride, sizeof(TS)) &&
+                    vec8(a.dresidual, a.dresidual_stride, sizeof(TS)) &&
+                    vec8(a.dx, a.width, sizeof(T)) && vec8(a.ds, a.width, sizeof(TS));
+    const RowShape sh = row_shape(a.width, v8 ? 8 : 1, v8 ? kRuns8 : kRuns1, a.rows <= sms);
+    int n = bwd_ctas(a.rows, sms);
+    if (sh.warps == 0) {
+        rmsnorm_bwd_wide_kernel<T, TS><<<(unsigned)a.rows, 1024, 0, stream>>>(a);
+        const dim3 grid((unsigned)n, (unsigned)((a.width + 255) / 256));
+        rmsnorm_dw_wide_kernel<T, TS><<<grid, 256, 0, stream>>>(a, partial);
+    } else if (v8) {
+        switch (sh.runs) {
+            case 1: rmsnorm_bwd_kernel<T, TS, 8, 1><<<n, 32 * sh.warps, 0, stream>>>(a, partial); break;
+            case 2: rmsnorm_bwd_kernel<T, TS, 8, 2><<<n, 32 * sh.warps, 0, stream>>>(a, partial); break;
+            case 3: rmsnorm_bwd_kernel<T, TS, 8, 3><<<n, 32 * sh.warps, 0, stream>>>(a, partial); break;
+            default: rmsnorm_bwd_kernel<T, TS, 8, 4><<<n, 32 * sh.warps, 0, stream>>>(a, partial); break;
+        }
+    } else {
+        rmsnorm_bwd_kernel<T, TS, 1, kRuns1><<<n, 32 * sh.warps, 0, stream>>>(a, partial);
+    }
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    rmsnorm_dw_kernel<<<(unsigned)((a.width + 31) / 32), dim3(32, 32), 0, stream>>>(
+        partial, n, a.width, a.dweight);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t ssd_launch_rmsnorm_fwd(const SsdNormFwd &a, int sms, cudaStream_t stream) {
+    if (a.in == SSD_ELT_F32) return launch_fwd_out<float, float>(a, sms, stream);
+    if (a.stream_type == SSD_ELT_F32) return launch_fwd_out<__nv_bfloat16, float>(a, sms, stream);
+    return launch_fwd_out<__nv_bfloat16, __nv_bfloat16>(a, sms, stream);
+}
+
+size_t ssd_rmsnorm_bwd_workspace(long long rows, int width, int sms) {
+    return (size_t)bwd_ctas(rows, sms) * (size_t)width * sizeof(float);
+}
+
+cudaError_t ssd_launch_rmsnorm_bwd(const SsdNormBwd &a, float *partial, int sms,
+                                   cudaStream_t stream) {
+    if (a.in == SSD_ELT_F32) return launch_bwd<float, float>(a, partial, sms, stream);
+    if (a.stream_type == SSD_ELT_F32)
+        return launch_bwd<__nv_bfloat16, float>(a, partial, sms, stream);
+    return launch_bwd<__nv_bfloat16, __nv_bfloat16>(a, partial, sms, stream);
+}
