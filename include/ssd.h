@@ -553,7 +553,10 @@ size_t ssd_linear_bwd_workspace_bytes(ssd_dtype dtype, ssd_activation activation
  *                be NULL when that is 0); no initialisation needed.
  * SSD_ERR_INVALID_ARG for null pointers, sizes <= 0 (length 0 is allowed),
  * strides below width or offsets that do not start at 0 or decrease;
- * SSD_ERR_UNSUPPORTED for other types, width >= 2^21, or 2^31 - 2048 tokens or more. */
+ * SSD_ERR_UNSUPPORTED for other types, width >= 2^21, 2^31 - 2048 tokens or
+ * more, or tokens * width of about 2^42 or more.  A call of more than 64 tokens
+ * joins its parts on the device by waits that are bounded in time; one that
+ * runs out is reported by ssd_last_device_error(). */
 ssd_status ssd_gated_scan_fwd(const void *x, const void *g, const void *z, ssd_dtype dtype,
                               int nseq, int length, const int *cu_seqlens_host,
                               const int *cu_seqlens_dev, int width, long long x_stride,

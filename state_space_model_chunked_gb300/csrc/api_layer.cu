@@ -65,6 +65,11 @@ ssd_status check_sequences(int nseq, int length, const int *host, const int *dev
     return *tokens < (1ll << 31) - 2048 ? SSD_OK : SSD_ERR_UNSUPPORTED;
 }
 
+// Sizes the recurrence's grid can number (tiles of 64 tokens by blocks of 32 channels).
+bool gated_handled(long long tokens, int width) {
+    return width < (1 << 21) && (tokens / 64 + 1) * (width / 32 + 1) < (1ll << 31);
+}
+
 // What the recurrence's two directions share.
 ssd_status gated_input(const void *x, const void *g, const void *z, ssd_dtype dtype, int nseq,
                        int length, const int *host, const int *dev, int width, long long x_stride,
@@ -73,7 +78,7 @@ ssd_status gated_input(const void *x, const void *g, const void *z, ssd_dtype dt
     if (!float_type(dtype)) return SSD_ERR_UNSUPPORTED;
     const ssd_status st = check_sequences(nseq, length, host, dev, &out->tokens);
     if (st != SSD_OK) return st;
-    if (width >= (1 << 21)) return SSD_ERR_UNSUPPORTED;
+    if (!gated_handled(out->tokens, width)) return SSD_ERR_UNSUPPORTED;
     const size_t n = size_of(dtype);
     if (out->tokens > 0 && (!array(x, n) || !array(g, n))) return SSD_ERR_INVALID_ARG;
     if (!maybe(z, n) || !maybe(init, 4)) return SSD_ERR_INVALID_ARG;
@@ -268,9 +273,9 @@ ssd_status ssd_linear_bwd(const void *dy, const void *x, const void *w, const vo
 
 size_t ssd_gated_scan_workspace_bytes(ssd_dtype dtype, long long tokens, int width) {
     if (!float_type(dtype) || tokens < 0 || tokens >= (1ll << 31) - 2048 || width <= 0 ||
-        width >= (1 << 21))
+        !gated_handled(tokens, width))
         return kBad;
-    return 0;
+    return ssd_gated_workspace(tokens, width);
 }
 
 ssd_status ssd_gated_scan_fwd(const void *x, const void *g, const void *z, ssd_dtype dtype,
@@ -281,20 +286,20 @@ ssd_status ssd_gated_scan_fwd(const void *x, const void *g, const void *z, ssd_d
                               float *checkpoints, void *workspace, size_t workspace_bytes,
                               cudaStream_t stream) {
     SsdGatedFwd a{};
-    const ssd_status st =
+    ssd_status st =
         gated_input(x, g, z, dtype, nseq, length, cu_seqlens_host, cu_seqlens_dev, width, x_stride,
                     g_stride, z_stride, init_state, &a.in);
     if (st != SSD_OK) return st;
     if (a.in.tokens > 0 && !array(y, size_of(dtype))) return SSD_ERR_INVALID_ARG;
     if (y_stride < width || !maybe(final_state, 4) || !maybe(checkpoints, 4))
         return SSD_ERR_INVALID_ARG;
-    (void)workspace;
-    (void)workspace_bytes;
+    st = check_workspace(workspace, workspace_bytes, ssd_gated_workspace(a.in.tokens, width), 256);
+    if (st != SSD_OK) return st;
     a.y = y;
     a.y_stride = y_stride;
     a.final_state = final_state;
     a.checkpoints = checkpoints;
-    return launched(ssd_launch_gated_fwd(a, ssd_sm_count(), stream));
+    return launched(ssd_launch_gated_fwd(a, workspace, ssd_device_error_word(), stream));
 }
 
 ssd_status ssd_gated_scan_bwd(const void *dy, const void *x, const void *g, const void *z,
@@ -306,7 +311,7 @@ ssd_status ssd_gated_scan_bwd(const void *dy, const void *x, const void *g, cons
                               long long dg_stride, void *dz, long long dz_stride, float *dinit,
                               void *workspace, size_t workspace_bytes, cudaStream_t stream) {
     SsdGatedBwd a{};
-    const ssd_status st =
+    ssd_status st =
         gated_input(x, g, z, dtype, nseq, length, cu_seqlens_host, cu_seqlens_dev, width, x_stride,
                     g_stride, z_stride, init_state, &a.in);
     if (st != SSD_OK) return st;
@@ -317,8 +322,8 @@ ssd_status ssd_gated_scan_bwd(const void *dy, const void *x, const void *g, cons
     if (dy_stride < width || dx_stride < width || dg_stride < width || (z && dz_stride < width) ||
         !maybe(dfinal, 4) || !maybe(dinit, 4))
         return SSD_ERR_INVALID_ARG;
-    (void)workspace;
-    (void)workspace_bytes;
+    st = check_workspace(workspace, workspace_bytes, ssd_gated_workspace(a.in.tokens, width), 256);
+    if (st != SSD_OK) return st;
     a.dy = dy;
     a.dfinal = dfinal;
     a.checkpoints = checkpoints;
@@ -330,7 +335,7 @@ ssd_status ssd_gated_scan_bwd(const void *dy, const void *x, const void *g, cons
     a.dg = dg;
     a.dz = dz;
     a.dinit = dinit;
-    return launched(ssd_launch_gated_bwd(a, ssd_sm_count(), stream));
+    return launched(ssd_launch_gated_bwd(a, workspace, ssd_device_error_word(), stream));
 }
 
 ssd_status ssd_gated_state_update(float *state, const void *x, const void *g, const void *z,

@@ -32,75 +32,506 @@ struct Gate {
 };
 __device__ __forceinline__ float sigmoidf(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 
-__device__ __forceinline__ void seq_range(const SsdGated &a, int s, long long &t0, long long &t1) {
-    t0 = a.cu ? a.cu[s] : (long long)s * a.length;
-    t1 = a.cu ? a.cu[s + 1] : t0 + a.length;
+// ------------------------------------------------------------- tiles and joins
+// The token axis is cut into tiles, one CTA a tile and block of 32 V channels:
+// each of 8 warps holds kTok consecutive tokens of it in registers, a lane V
+// channels.  A run of tokens acts on the state that enters it as h -> A h + H,
+// so the warps' (A, H) are joined through shared memory and the tiles' through
+// global memory in one pass over the data:
+//
+//   a tile publishes its own (A, H) as soon as its loads have landed, then
+//   walks back over its predecessors' until one has published the state that
+//   leaves it, and publishes its own leaving state.
+//
+// Tiles are handed out by a counter in the order of the walk, so a tile waits
+// only for tiles that already run; every wait is bounded in time.
+//
+// A run that holds a sequence boundary is cut: what leaves it does not depend
+// on what enters, and nothing is multiplied across the cut (0 times a NaN of
+// the sequence before would reach the next one).  A cut tile publishes its
+// leaving state at once.
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kFwdTok = 16, kBwdTok = 8;
+constexpr int kFwdTile = kWarps * kFwdTok, kBwdTile = kWarps * kBwdTok;
+static_assert(kBwdTile == kEvery, "a backward tile starts from a kept state");
+static_assert(kEvery % kFwdTok == 0, "kept states are those that enter a warp's run");
+constexpr unsigned kNone = 0, kRun = 1, kState = 2;    // what a tile has published
+
+// Global memory of the joins: per (tile, block of channels) a word, per (tile,
+// channel) the run (A, H) and the state behind it.
+struct Joins {
+    unsigned *ticket, *word;
+    float2 *run;
+    float *state;
+    unsigned *err;
+    unsigned long long wait_ns;
+    int withhold;           // test hook: the walk's first tile publishes nothing
+};
+
+__device__ __forceinline__ unsigned ld_acquire(const unsigned *p) {
+    unsigned v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_release(unsigned *p, unsigned v) {
+    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
-template <typename T>
-__global__ void __launch_bounds__(128) gated_fwd_kernel(const SsdGatedFwd a) {
-    const int c = blockIdx.x * 128 + threadIdx.x, s = blockIdx.y;
-    if (c >= a.in.width) return;
-    long long t0, t1;
-    seq_range(a.in, s, t0, t1);
-    float h = a.in.init ? a.in.init[(size_t)s * a.in.width + c] : 0.f;
-    for (long long t = t0; t < t1; ++t) {
-        if (a.checkpoints && t % kEvery == 0) a.checkpoints[(size_t)(t / kEvery) * a.in.width + c] = h;
-        const float x = ssd_ld(static_cast<const T *>(a.in.x) + t * a.in.x_stride + c);
-        const Gate f(ssd_ld(static_cast<const T *>(a.in.g) + t * a.in.g_stride + c));
-        h = f.keep * h + f.drop * x;
-        float y = h;
-        if (a.in.z) {
-            const float z = ssd_ld(static_cast<const T *>(a.in.z) + t * a.in.z_stride + c);
-            y = h * z * sigmoidf(z);
-        }
-        ssd_st(static_cast<T *>(a.y) + t * a.y_stride + c, y);
-    }
-    if (a.final_state) a.final_state[(size_t)s * a.in.width + c] = h;
+// One warp publishes a tile's word after its lanes' values.
+__device__ __forceinline__ void publish(unsigned *word, unsigned v) {
+    __threadfence();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) st_release(word, v);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(128) gated_bwd_kernel(const SsdGatedBwd a) {
-    const int c = blockIdx.x * 128 + threadIdx.x, s = blockIdx.y;
-    if (c >= a.in.width) return;
-    long long t0, t1;
-    seq_range(a.in, s, t0, t1);
-    const float init = a.in.init ? a.in.init[(size_t)s * a.in.width + c] : 0.f;
-    float carry = a.dfinal ? a.dfinal[(size_t)s * a.in.width + c] : 0.f;   // f_{t+1} lam_{t+1}
-    float before[kEvery];
-    for (long long e = t1; e > t0;) {
-        // the block of tokens [b, e) that starts at a kept state or at the sequence's start
-        long long b = (e - 1) / kEvery * kEvery;
-        float h = b >= t0 ? a.checkpoints[(size_t)(b / kEvery) * a.in.width + c] : init;
-        if (b < t0) b = t0;
-        for (long long t = b; t < e; ++t) {
-            before[t - b] = h;
-            const float x = ssd_ld(static_cast<const T *>(a.in.x) + t * a.in.x_stride + c);
-            const Gate f(ssd_ld(static_cast<const T *>(a.in.g) + t * a.in.g_stride + c));
-            h = f.keep * h + f.drop * x;
-        }
-        for (long long t = e - 1; t >= b; --t) {
-            const float x = ssd_ld(static_cast<const T *>(a.in.x) + t * a.in.x_stride + c);
-            const Gate f(ssd_ld(static_cast<const T *>(a.in.g) + t * a.in.g_stride + c));
-            const float keep = f.keep, drop = f.drop;
-            float dh = ssd_ld(static_cast<const T *>(a.dy) + t * a.dy_stride + c);
-            if (a.in.z) {
-                const float z = ssd_ld(static_cast<const T *>(a.in.z) + t * a.in.z_stride + c);
-                const float sig = sigmoidf(z);
-                const float ht = keep * before[t - b] + drop * x;
-                ssd_st(static_cast<T *>(a.dz) + t * a.dz_stride + c,
-                       dh * ht * sig * (1.f + z * (1.f - sig)));
-                dh *= z * sig;
+// The state that enters tile number `at` of the walk (at > 0), for this lane's
+// V channels from c: one warp, predecessors at - 1, at - 2, ... of the walk.
+// The words of 32 of them are polled at a time.
+template <int V>
+__device__ __forceinline__ void walk_back(const Joins &j, int at, int blocks, int block, int width,
+                                          int c, float (&h)[V]) {
+    const int lane = threadIdx.x & 31;
+    float A[V], H[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) A[k] = 1.f, H[k] = 0.f;
+    for (int p = at - 1;; p -= 32) {
+        const int mine = p - lane;
+        const unsigned *word = j.word + (size_t)(mine < 0 ? 0 : mine) * blocks + block;
+        unsigned states, runs;
+        unsigned long long t0 = 0;
+        for (;;) {
+            const unsigned v = mine < 0 ? kRun : ld_acquire(word);
+            states = __ballot_sync(0xffffffffu, v == kState);
+            runs = __ballot_sync(0xffffffffu, v != kNone);
+            // tiles before the nearest state (all 32 without one) must have their runs
+            const unsigned need = states ? (states & -states) - 1 : 0xffffffffu;
+            if ((runs & need) == need) break;
+            unsigned long long now;
+            asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+            if (t0 == 0) t0 = now;
+            if (__shfl_sync(0xffffffffu, now - t0 > j.wait_ns, 0)) {    // lane 0's clock decides
+                if (lane == 0) ssd_report(j.err, SSD_DEVERR_TIMEOUT);
+#pragma unroll
+                for (int k = 0; k < V; ++k) h[k] = 0.f;
+                return;
             }
-            const float lam = dh + carry;
-            ssd_st(static_cast<T *>(a.dx) + t * a.dx_stride + c, drop * lam);
-            ssd_st(static_cast<T *>(a.dg) + t * a.dg_stride + c,
-                   lam * (before[t - b] - x) * keep * drop);
-            carry = keep * lam;
         }
-        e = b;
+        const int n = states ? __ffs(states) - 1 : 32;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            if (c < width) {
+                const float2 *r = j.run + (size_t)(p - i) * width + c;
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    const float2 v = __ldcg(r + k);
+                    H[k] += A[k] * v.y;
+                    A[k] *= v.x;
+                }
+            }
+        }
+        if (states || p - 32 < 0) {
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+                h[k] = states && c < width
+                           ? A[k] * __ldcg(j.state + (size_t)(p - n) * width + c + k) + H[k]
+                           : H[k];
+            return;
+        }
     }
-    if (a.dinit) a.dinit[(size_t)s * a.in.width + c] = carry;
+}
+
+// Which sequence each of a warp's tokens belongs to (lane i: token t0 + i, i < n)
+// and which of them begin or end one.
+struct Marks {
+    int seq;
+    unsigned starts, ends;
+};
+__device__ __forceinline__ Marks marks(const SsdGated &a, long long t0, int n) {
+    const int lane = threadIdx.x & 31;
+    const long long t = t0 + lane;
+    const bool in = lane < n && t < a.tokens;
+    Marks m;
+    m.seq = 0;
+    bool start = false, end = false;
+    if (in) {
+        if (a.cu) {
+            int lo = 0, hi = a.nseq - 1;    // the last s with cu[s] <= t
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (__ldg(a.cu + mid) <= t) lo = mid;
+                else hi = mid - 1;
+            }
+            m.seq = lo;
+            start = __ldg(a.cu + lo) == t;
+            end = __ldg(a.cu + lo + 1) == t + 1;
+        } else {
+            m.seq = (int)t / a.length;
+            const int off = (int)t - m.seq * a.length;
+            start = off == 0;
+            end = off == a.length - 1;
+        }
+    }
+    m.starts = __ballot_sync(0xffffffffu, start);
+    m.ends = __ballot_sync(0xffffffffu, end);
+    return m;
+}
+
+// Empty sequences hand `in` (zeros without one) on to `out`; the CTAs of one
+// tile do this for all of them.
+template <int V>
+__device__ __forceinline__ void pass_empty(const SsdGated &a, const float *in, float *out, int c) {
+    if (!out || c >= a.width) return;
+    for (int s = threadIdx.x >> 5; s < a.nseq; s += kWarps) {
+        const bool empty = a.cu ? __ldg(a.cu + s) == __ldg(a.cu + s + 1) : a.length == 0;
+        if (!empty) continue;
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+            out[(size_t)s * a.width + c + k] = in ? in[(size_t)s * a.width + c + k] : 0.f;
+    }
+}
+
+template <int V>
+__device__ __forceinline__ void load_f32(const float *p, bool on, float (&v)[V]) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) v[k] = on ? p[k] : 0.f;
+}
+
+// The CTA's place: number in the walk, and block of channels.
+template <bool kJoin>
+__device__ __forceinline__ void place(const Joins &j, int blocks, int &at, int &block) {
+    if constexpr (kJoin) {
+        __shared__ unsigned ticket;
+        if (threadIdx.x == 0) ticket = atomicAdd(j.ticket, 1u);
+        __syncthreads();
+        at = ticket / blocks;
+        block = ticket % blocks;
+    } else {
+        at = 0;
+        block = blockIdx.x;
+    }
+}
+
+// The (A, H) of the CTA's warps in the order of the walk, and what enters the
+// tile, in shared memory.
+template <int V>
+struct Runs {
+    float A[kWarps][32 * V], H[kWarps][32 * V], in[32 * V];
+    bool cut[kWarps];
+};
+
+// Joins the warps' runs and, with kJoin, the tiles': on return h is the state
+// that enters this warp's run (`place` = its number in the walk's order).
+template <int V, bool kJoin>
+__device__ __forceinline__ void join(Runs<V> &r, const Joins &j, int at, int blocks, int block,
+                                     int width, int c, int place, bool cut, const float (&A)[V],
+                                     const float (&H)[V], float (&h)[V]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        r.A[place][lane * V + k] = A[k];
+        r.H[place][lane * V + k] = H[k];
+    }
+    if (lane == 0) r.cut[place] = cut;
+    __syncthreads();
+    float pA[V];            // the runs in front of this one
+    bool pcut = false;
+#pragma unroll
+    for (int k = 0; k < V; ++k) h[k] = 0.f, pA[k] = 1.f;
+    for (int w = 0; w < place; ++w) {
+        const bool wcut = r.cut[w];
+        pcut |= wcut;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const float wa = r.A[w][lane * V + k], wh = r.H[w][lane * V + k];
+            h[k] = wcut ? wh : wa * h[k] + wh;
+            pA[k] *= wa;
+        }
+    }
+    if constexpr (kJoin) {
+        if (place == kWarps - 1) {
+            const bool tcut = pcut || cut, on = c < width;
+            float in[V], tA[V], tH[V];
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                tA[k] = A[k] * pA[k];
+                tH[k] = cut ? H[k] : A[k] * h[k] + H[k];
+                in[k] = 0.f;
+            }
+            unsigned *word = j.word + (size_t)at * blocks + block;
+            const size_t slot = (size_t)at * width + c;
+            const bool say = !(j.withhold && at == 0);
+            if (at == 0 || tcut) {
+                if (on && say) {
+#pragma unroll
+                    for (int k = 0; k < V; ++k) j.state[slot + k] = tH[k];
+                }
+                if (say) publish(word, kState);
+            } else {
+                if (on) {
+#pragma unroll
+                    for (int k = 0; k < V; ++k) j.run[slot + k] = make_float2(tA[k], tH[k]);
+                }
+                publish(word, kRun);
+            }
+            if (at > 0) {
+                walk_back<V>(j, at, blocks, block, width, c, in);
+                if (!tcut) {
+                    if (on) {
+#pragma unroll
+                        for (int k = 0; k < V; ++k) j.state[slot + k] = tA[k] * in[k] + tH[k];
+                    }
+                    publish(word, kState);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < V; ++k) r.in[lane * V + k] = in[k];
+        }
+        __syncthreads();
+        if (!pcut) {
+#pragma unroll
+            for (int k = 0; k < V; ++k) h[k] += pA[k] * r.in[lane * V + k];
+        }
+    }
+}
+
+template <typename T, int V, int kTok>
+__device__ __forceinline__ void load_run(SsdRaw<T, V> (&raw)[kTok], const void *base,
+                                         long long stride, long long t0, int n, int c, bool on) {
+    const T *p = static_cast<const T *>(base) + t0 * stride + c;
+#pragma unroll
+    for (int i = 0; i < kTok; ++i) {
+        if (on && i < n) raw[i].load_cs(p + i * stride);
+        else raw[i].zero();
+    }
+}
+
+template <typename T, int V, bool kGate, bool kJoin>
+__global__ void __launch_bounds__(kThreads, 2)
+gated_fwd_kernel(const SsdGatedFwd a, const Joins joins, int blocks) {
+    __shared__ Runs<V> runs;
+    int at, block;
+    place<kJoin>(joins, blocks, at, block);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int width = a.in.width, c = (block * 32 + lane) * V;
+    const bool on = c < width;
+    const long long t0 = (long long)at * kFwdTile + warp * kFwdTok;
+    const int n = (int)max(0ll, min((long long)kFwdTok, a.in.tokens - t0));
+
+    SsdRaw<T, V> graw[kFwdTok], xraw[kFwdTok], zraw[kGate ? kFwdTok : 1];
+    load_run<T, V>(graw, a.in.g, a.in.g_stride, t0, n, c, on);
+    load_run<T, V>(xraw, a.in.x, a.in.x_stride, t0, n, c, on);
+    if constexpr (kGate) load_run<T, V>(zraw, a.in.z, a.in.z_stride, t0, n, c, on);
+    const Marks m = marks(a.in, t0, kFwdTok);
+    if (at == 0) pass_empty<V>(a.in, a.in.init, a.final_state, c);
+
+    float keep[kFwdTok][V], u[kFwdTok][V], A[V], H[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) A[k] = 1.f, H[k] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kFwdTok; ++i) {
+        const bool start = (m.starts >> i) & 1u;
+        float first[V];
+        if (start) {
+            const int seq = __shfl_sync(0xffffffffu, m.seq, i);
+            load_f32<V>(a.in.init + (size_t)seq * width + c, on && a.in.init != nullptr, first);
+        }
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const Gate f(graw[i].get(k));
+            keep[i][k] = f.keep;
+            u[i][k] = f.drop * xraw[i].get(k);
+            if (start) {
+                u[i][k] += f.keep * first[k];
+                A[k] = 0.f;
+                H[k] = u[i][k];
+            } else if (i < n) {
+                A[k] *= f.keep;
+                H[k] = f.keep * H[k] + u[i][k];
+            }
+        }
+    }
+    float h[V];
+    join<V, kJoin>(runs, joins, at, blocks, block, width, c, warp, m.starts != 0, A, H, h);
+
+    if (a.checkpoints && n > 0 && t0 % kEvery == 0) {
+        float before[V];
+        const int seq = __shfl_sync(0xffffffffu, m.seq, 0);
+        if (m.starts & 1u) {
+            load_f32<V>(a.in.init + (size_t)seq * width + c, on && a.in.init != nullptr, before);
+        } else {
+#pragma unroll
+            for (int k = 0; k < V; ++k) before[k] = h[k];
+        }
+        if (on) ssd_store_vec<V>(a.checkpoints + (size_t)(t0 / kEvery) * width + c, before);
+    }
+    T *y = static_cast<T *>(a.y) + t0 * a.y_stride + c;
+#pragma unroll
+    for (int i = 0; i < kFwdTok; ++i) {
+        if (i < n) {
+            const bool start = (m.starts >> i) & 1u;
+            float o[V];
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                h[k] = start ? u[i][k] : keep[i][k] * h[k] + u[i][k];
+                o[k] = h[k];
+                if constexpr (kGate) {
+                    const float z = zraw[i].get(k);
+                    o[k] *= z * sigmoidf(z);
+                }
+            }
+            if (on) ssd_store_vec<V>(y + i * a.y_stride, o);
+            if (((m.ends >> i) & 1u) && a.final_state) {
+                const int seq = __shfl_sync(0xffffffffu, m.seq, i);
+                if (on) ssd_store_vec<V>(a.final_state + (size_t)seq * width + c, h);
+            }
+        }
+    }
+}
+
+// Backward: the same joins from the last tile to the first, on the gradient
+// that a token hands to the one before it, mu_t = f_t lam_t: mu -> A mu + M
+// over a run.  h is recomputed inside the tile from its kept state.
+template <typename T, int V, bool kGate, bool kJoin>
+__global__ void __launch_bounds__(kThreads, 2)
+gated_bwd_kernel(const SsdGatedBwd a, const Joins joins, int blocks, int tiles) {
+    __shared__ Runs<V> runs;
+    __shared__ float fA[kWarps][32 * V], fH[kWarps][32 * V];
+    __shared__ bool fcut[kWarps];
+    int at, block;
+    place<kJoin>(joins, blocks, at, block);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int width = a.in.width, c = (block * 32 + lane) * V;
+    const bool on = c < width;
+    const int tile = tiles - 1 - at;
+    const long long t0 = (long long)tile * kBwdTile + warp * kBwdTok;
+    const int n = (int)max(0ll, min((long long)kBwdTok, a.in.tokens - t0));
+
+    SsdRaw<T, V> graw[kBwdTok], xraw[kBwdTok], yraw[kBwdTok], zraw[kGate ? kBwdTok : 1];
+    load_run<T, V>(graw, a.in.g, a.in.g_stride, t0, n, c, on);
+    load_run<T, V>(yraw, a.dy, a.dy_stride, t0, n, c, on);
+    if constexpr (kGate) load_run<T, V>(zraw, a.in.z, a.in.z_stride, t0, n, c, on);
+    load_run<T, V>(xraw, a.in.x, a.in.x_stride, t0, n, c, on);
+    float h[V];         // the state that enters the tile
+    load_f32<V>(a.checkpoints + (size_t)tile * width + c, on && a.in.tokens > 0, h);
+    const Marks m = marks(a.in, t0, kBwdTok);
+    if (at == 0) pass_empty<V>(a.in, a.dfinal, a.dinit, c);
+
+    // the run forward (A, H) and backward (A, M)
+    float keep[kBwdTok][V], drop[kBwdTok][V], dh[kBwdTok][V], A[V], H[V], M[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) A[k] = 1.f, H[k] = 0.f, M[k] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kBwdTok; ++i) {
+        const bool start = (m.starts >> i) & 1u;
+        float first[V];
+        if (start) {
+            const int seq = __shfl_sync(0xffffffffu, m.seq, i);
+            load_f32<V>(a.in.init + (size_t)seq * width + c, on && a.in.init != nullptr, first);
+        }
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const Gate f(graw[i].get(k));
+            keep[i][k] = f.keep;
+            drop[i][k] = f.drop;
+            const float u = f.drop * xraw[i].get(k);
+            if (start) {
+                A[k] = 0.f;
+                H[k] = f.keep * first[k] + u;
+            } else if (i < n) {
+                A[k] *= f.keep;
+                H[k] = f.keep * H[k] + u;
+            }
+        }
+    }
+#pragma unroll
+    for (int i = kBwdTok - 1; i >= 0; --i) {
+        float last[V];
+        const bool end = (m.ends >> i) & 1u;
+        if (end) {
+            const int seq = __shfl_sync(0xffffffffu, m.seq, i);
+            load_f32<V>(a.dfinal + (size_t)seq * width + c, on && a.dfinal != nullptr, last);
+        }
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            dh[i][k] = yraw[i].get(k);
+            if constexpr (kGate) {
+                const float z = zraw[i].get(k);
+                dh[i][k] *= z * sigmoidf(z);
+            }
+            if (end) dh[i][k] += last[k];
+            if (i < n) {
+                const bool start = (m.starts >> i) & 1u;
+                const float lam = end ? dh[i][k] : dh[i][k] + M[k];
+                M[k] = start ? 0.f : keep[i][k] * lam;
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        fA[warp][lane * V + k] = A[k];
+        fH[warp][lane * V + k] = H[k];
+    }
+    if (lane == 0) fcut[warp] = m.starts != 0;
+    float mu[V];
+    join<V, kJoin>(runs, joins, at, blocks, block, width, c, kWarps - 1 - warp, m.starts != 0, A, M,
+                   mu);
+    for (int w = 0; w < warp; ++w) {
+        const bool wcut = fcut[w];
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+            h[k] = wcut ? fH[w][lane * V + k] : fA[w][lane * V + k] * h[k] + fH[w][lane * V + k];
+    }
+
+    // forward: the state before each token, and dz
+    float before[kBwdTok][V];
+    T *dz = kGate ? static_cast<T *>(a.dz) + t0 * a.dz_stride + c : nullptr;
+#pragma unroll
+    for (int i = 0; i < kBwdTok; ++i) {
+        if (i < n) {
+            if ((m.starts >> i) & 1u) {
+                const int seq = __shfl_sync(0xffffffffu, m.seq, i);
+                load_f32<V>(a.in.init + (size_t)seq * width + c, on && a.in.init != nullptr, h);
+            }
+            float o[V];
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                before[i][k] = h[k];
+                h[k] = keep[i][k] * h[k] + drop[i][k] * xraw[i].get(k);
+                if constexpr (kGate) {
+                    const float z = zraw[i].get(k), sig = sigmoidf(z);
+                    o[k] = yraw[i].get(k) * h[k] * sig * (1.f + z * (1.f - sig));
+                }
+            }
+            if constexpr (kGate) {
+                if (on) ssd_store_vec<V>(dz + i * a.dz_stride, o);
+            }
+        }
+    }
+    // backward
+    T *dx = static_cast<T *>(a.dx) + t0 * a.dx_stride + c;
+    T *dg = static_cast<T *>(a.dg) + t0 * a.dg_stride + c;
+#pragma unroll
+    for (int i = kBwdTok - 1; i >= 0; --i) {
+        if (i < n) {
+            const bool end = (m.ends >> i) & 1u;
+            float ox[V], og[V];
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const float lam = end ? dh[i][k] : dh[i][k] + mu[k];
+                ox[k] = drop[i][k] * lam;
+                og[k] = lam * (before[i][k] - xraw[i].get(k)) * keep[i][k] * drop[i][k];
+                mu[k] = keep[i][k] * lam;
+            }
+            if (on) {
+                ssd_store_vec<V>(dx + i * a.dx_stride, ox);
+                ssd_store_vec<V>(dg + i * a.dg_stride, og);
+            }
+            if (((m.starts >> i) & 1u) && a.dinit) {
+                const int seq = __shfl_sync(0xffffffffu, m.seq, i);
+                if (on) ssd_store_vec<V>(a.dinit + (size_t)seq * width + c, mu);
+            }
+        }
+    }
 }
 
 // One token of every (row, channel): the state is read and written in place.
@@ -123,18 +554,117 @@ __global__ void __launch_bounds__(256) gated_step_kernel(const SsdGatedStep a) {
 
 }  // namespace
 
-cudaError_t ssd_launch_gated_fwd(const SsdGatedFwd &a, int, cudaStream_t stream) {
-    const dim3 grid((unsigned)((a.in.width + 127) / 128), (unsigned)a.in.nseq);
-    if (a.in.bf16) gated_fwd_kernel<__nv_bfloat16><<<grid, 128, 0, stream>>>(a);
-    else gated_fwd_kernel<float><<<grid, 128, 0, stream>>>(a);
+// Channels a lane: two when every row of every array starts on a boundary of
+// two elements (4-byte loads in bf16: a warp reads whole 128-byte lines), else one.
+static bool pairs(bool bf16, int width, const void *p, long long stride) {
+    return p == nullptr || (width % 2 == 0 && stride % 2 == 0 &&
+                            ((uintptr_t)p & (bf16 ? 3u : 7u)) == 0);
+}
+static bool pairs_in(const SsdGated &a) {
+    return pairs(a.bf16, a.width, a.x, a.x_stride) && pairs(a.bf16, a.width, a.g, a.g_stride) &&
+           pairs(a.bf16, a.width, a.z, a.z_stride) && pairs(false, a.width, a.init, 0);
+}
+
+// Tiles of a walk (at least one: it also hands on the empty sequences' states).
+static int tiles_of(long long tokens, int tile) {
+    return tokens > 0 ? (int)((tokens + tile - 1) / tile) : 1;
+}
+
+static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+// The joins' memory for the smaller (backward) tiles and for one channel a
+// lane covers both directions: a ticket and the words, the runs, the states.
+size_t ssd_gated_workspace(long long tokens, int width) {
+    const size_t tiles = tiles_of(tokens, kBwdTile);
+    if (tiles == 1) return 0;
+    const size_t blocks = (width + 31) / 32;
+    return up256(4 + 4 * tiles * blocks) + up256(8 * tiles * (size_t)width) +
+           up256(4 * tiles * (size_t)width);
+}
+
+// Carves the joins out of the workspace and clears the words.
+static cudaError_t joins_of(void *workspace, int tiles, int blocks, int width, unsigned *err,
+                            cudaStream_t stream, Joins *j) {
+    const SsdDebug dbg = ssd_debug_config();
+    char *ws = static_cast<char *>(workspace);
+    const size_t words = up256(4 + 4 * (size_t)tiles * blocks);
+    j->ticket = reinterpret_cast<unsigned *>(ws);
+    j->word = j->ticket + 1;
+    j->run = reinterpret_cast<float2 *>(ws + words);
+    j->state = reinterpret_cast<float *>(ws + words + up256(8 * (size_t)tiles * width));
+    j->err = err;
+    j->wait_ns = dbg.wait_ns;
+    j->withhold = dbg.fault == kSsdFaultWithholdSignal;
+    return cudaMemsetAsync(ws, 0, 4 + 4 * (size_t)tiles * blocks, stream);
+}
+
+template <typename T, int V, bool kGate>
+static cudaError_t launch_fwd(const SsdGatedFwd &a, void *ws, unsigned *err, cudaStream_t stream) {
+    const int tiles = tiles_of(a.in.tokens, kFwdTile), blocks = (a.in.width + 32 * V - 1) / (32 * V);
+    Joins j{};
+    if (tiles == 1) {
+        gated_fwd_kernel<T, V, kGate, false><<<blocks, kThreads, 0, stream>>>(a, j, blocks);
+        return cudaGetLastError();
+    }
+    const cudaError_t e = joins_of(ws, tiles, blocks, a.in.width, err, stream, &j);
+    if (e != cudaSuccess) return e;
+    gated_fwd_kernel<T, V, kGate, true>
+        <<<(unsigned)((size_t)tiles * blocks), kThreads, 0, stream>>>(a, j, blocks);
     return cudaGetLastError();
 }
 
-cudaError_t ssd_launch_gated_bwd(const SsdGatedBwd &a, int, cudaStream_t stream) {
-    const dim3 grid((unsigned)((a.in.width + 127) / 128), (unsigned)a.in.nseq);
-    if (a.in.bf16) gated_bwd_kernel<__nv_bfloat16><<<grid, 128, 0, stream>>>(a);
-    else gated_bwd_kernel<float><<<grid, 128, 0, stream>>>(a);
+template <typename T, int V, bool kGate>
+static cudaError_t launch_bwd(const SsdGatedBwd &a, void *ws, unsigned *err, cudaStream_t stream) {
+    const int tiles = tiles_of(a.in.tokens, kBwdTile), blocks = (a.in.width + 32 * V - 1) / (32 * V);
+    Joins j{};
+    if (tiles == 1) {
+        gated_bwd_kernel<T, V, kGate, false><<<blocks, kThreads, 0, stream>>>(a, j, blocks, tiles);
+        return cudaGetLastError();
+    }
+    const cudaError_t e = joins_of(ws, tiles, blocks, a.in.width, err, stream, &j);
+    if (e != cudaSuccess) return e;
+    gated_bwd_kernel<T, V, kGate, true>
+        <<<(unsigned)((size_t)tiles * blocks), kThreads, 0, stream>>>(a, j, blocks, tiles);
     return cudaGetLastError();
+}
+
+cudaError_t ssd_launch_gated_fwd(const SsdGatedFwd &a, void *ws, unsigned *err,
+                                 cudaStream_t stream) {
+    const bool two = pairs_in(a.in) && pairs(a.in.bf16, a.in.width, a.y, a.y_stride) &&
+                     pairs(false, a.in.width, a.final_state, 0) &&
+                     pairs(false, a.in.width, a.checkpoints, 0);
+    const bool gate = a.in.z != nullptr;
+    if (a.in.bf16) {
+        using T = __nv_bfloat16;
+        if (two) return gate ? launch_fwd<T, 2, true>(a, ws, err, stream)
+                             : launch_fwd<T, 2, false>(a, ws, err, stream);
+        return gate ? launch_fwd<T, 1, true>(a, ws, err, stream)
+                    : launch_fwd<T, 1, false>(a, ws, err, stream);
+    }
+    if (two) return gate ? launch_fwd<float, 2, true>(a, ws, err, stream)
+                         : launch_fwd<float, 2, false>(a, ws, err, stream);
+    return gate ? launch_fwd<float, 1, true>(a, ws, err, stream)
+                : launch_fwd<float, 1, false>(a, ws, err, stream);
+}
+
+cudaError_t ssd_launch_gated_bwd(const SsdGatedBwd &a, void *ws, unsigned *err,
+                                 cudaStream_t stream) {
+    const bool bf16 = a.in.bf16, gate = a.in.z != nullptr;
+    const int w = a.in.width;
+    const bool two = pairs_in(a.in) && pairs(bf16, w, a.dy, a.dy_stride) &&
+                     pairs(bf16, w, a.dx, a.dx_stride) && pairs(bf16, w, a.dg, a.dg_stride) &&
+                     (!gate || pairs(bf16, w, a.dz, a.dz_stride)) && pairs(false, w, a.dinit, 0);
+    if (bf16) {
+        using T = __nv_bfloat16;
+        if (two) return gate ? launch_bwd<T, 2, true>(a, ws, err, stream)
+                             : launch_bwd<T, 2, false>(a, ws, err, stream);
+        return gate ? launch_bwd<T, 1, true>(a, ws, err, stream)
+                    : launch_bwd<T, 1, false>(a, ws, err, stream);
+    }
+    if (two) return gate ? launch_bwd<float, 2, true>(a, ws, err, stream)
+                         : launch_bwd<float, 2, false>(a, ws, err, stream);
+    return gate ? launch_bwd<float, 1, true>(a, ws, err, stream)
+                : launch_bwd<float, 1, false>(a, ws, err, stream);
 }
 
 cudaError_t ssd_launch_gated_step(const SsdGatedStep &a, cudaStream_t stream) {

@@ -245,11 +245,15 @@ def _check_scan(x, g, z, init, cu, d, packed, rng):
     cut = (lambda t: t) if packed else (lambda t: None if t is None else t.unflatten(0, (n, -1)))
     y, f, kept = ssd.gated_scan_fwd(cut(x), cut(g), cut(z), init, return_checkpoints=True, **kw)
     assert y.dtype == DT[d] and f.dtype == torch.float32
-    assert rel(host(y).reshape(yr.shape), yr) <= BAR[d] and rel(host(f), fr) <= BAR["f32"]
-    assert rel(host(kept), before[::64]) <= BAR["f32"]
+    # states are one sum a channel: held against the size of their terms, which may cancel
+    _, _, fsize, ksize = ref.gated_fwd(np.abs(hx), hg, None, np.abs(hi), cu)
+    assert rel(host(y).reshape(yr.shape), yr) <= BAR[d]
+    assert np.linalg.norm(host(f) - fr) <= BAR["f32"] * np.linalg.norm(fsize)
+    assert np.linalg.norm(host(kept) - before[::64]) <= BAR["f32"] * np.linalg.norm(ksize[::64])
     y2, f2 = ssd.gated_scan_fwd(cut(x), cut(g), cut(z), init, **kw)
     # the order of the sums may follow the progress of other blocks: both results are held to the bar
-    assert rel(host(y2).reshape(yr.shape), yr) <= BAR[d] and rel(host(f2), fr) <= BAR["f32"]
+    assert rel(host(y2).reshape(yr.shape), yr) <= BAR[d]
+    assert np.linalg.norm(host(f2) - fr) <= BAR["f32"] * np.linalg.norm(fsize)
     dy, dfinal = tens(rng, x.shape, d), tens(rng, (n, width))
     dxr, dgr, dzr, dir_ = ref.gated_bwd(host(dy), hx, hg, hz, hi, host(dfinal), cu)
     dx, dg, dz, di = ssd.gated_scan_bwd(cut(dy), cut(x), cut(g), kept, cut(z), init, dfinal, **kw)
