@@ -2,6 +2,7 @@
 // validated by the ABI layer before any of these is called.
 #pragma once
 
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 
@@ -82,6 +83,9 @@ cudaError_t ssd_launch_scan_simt(const void *x, const float *dt, const float *A,
                                  int batch, int L, int H, int P, int N, int G,
                                  const SsdFuse &fuse, const int *cu, SsdProfileEvents prof,
                                  cudaStream_t stream);
+
+// The driver's cuTensorMapEncodeTiled (null when it has none).
+PFN_cuTensorMapEncodeTiled_v12000 ssd_tensor_map_encoder();
 
 // Tensor-core (tcgen05/TMEM/TMA) chunked scan.
 struct SsdTcPlan {
@@ -217,6 +221,9 @@ struct SsdProduct {
     long long out_row;
 };
 cudaError_t ssd_launch_product_simt(const SsdProduct &p, cudaStream_t stream);
+bool ssd_product_tc_handles(const SsdProduct &p);
+cudaError_t ssd_launch_product_tc(const SsdProduct &p, int sms, unsigned *err,
+                                  cudaStream_t stream);
 
 // dp = dy act'(preact) (dp null: not stored) and the column sums of dp
 // (dbias null: none; `partial` holds ssd_act_bwd_workspace bytes).

@@ -1,0 +1,534 @@
+// The matrix product on the 5th-generation tensor cores, bf16 or E4M3 inputs:
+//
+//   out[m][n] = act(sum_k A(m,k) B(n,k) a_scale[m] b_scale[n] + bias[n]) + residual[m][n]
+//
+// A CTA computes tiles of 128 x kBN: a producer warp brings 128-byte-wide
+// blocks of both operands into a ring of shared-memory stages by TMA (rows
+// past an end read as zero), an issuer warp multiplies them into a TMEM
+// accumulator, and eight epilogue warps read that back, one TMEM lane (a row
+// of A) a thread, and apply scales, bias, activation and residual on the way
+// to global memory.
+//   Operands lie with k contiguous (K-major) or with their rows contiguous
+// (MN-major, the gradients' transposed operands); both use 128-byte swizzled
+// tiles.  kSwap takes the weights as A and the tokens as B, for few tokens:
+// then a lane is a feature, and the rows of B are only as many as needed.
+//   Without kSplit a CTA walks over tiles with two accumulators, so a tile's
+// epilogue runs under the next one's products.  With kSplit the k axis of one
+// tile is split over a cluster of CTAs and their sums are joined through
+// distributed shared memory, in rank order.
+#include <cuda.h>
+
+#include "act.cuh"
+#include "launch.h"
+#include "ptx.cuh"
+#include "vec.cuh"
+
+using namespace ssdptx;
+
+namespace {
+
+constexpr int kBM = 128;
+constexpr int kRowBytes = 128;                  // a block's k extent
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (2 + kEpiWarps);  // producer, issuer, epilogue
+constexpr uint32_t kABytes = kBM * kRowBytes;
+constexpr uint32_t kRingBytes = 196608;
+constexpr uint32_t kCtrlBytes = 1024;
+constexpr int kMaxStages = 12;
+
+constexpr uint32_t stage_bytes(int bn) { return kABytes + bn * kRowBytes; }
+constexpr int stages(int bn) {
+    return kRingBytes / stage_bytes(bn) < kMaxStages ? kRingBytes / stage_bytes(bn) : kMaxStages;
+}
+constexpr uint32_t smem_bytes(int bn) { return kCtrlBytes + stages(bn) * stage_bytes(bn); }
+constexpr uint32_t tmem_cols(int bn, bool split) {
+    const int want = split ? bn : 2 * bn;
+    return want <= 32 ? 32 : want <= 64 ? 64 : want <= 128 ? 128 : want <= 256 ? 256 : 512;
+}
+
+struct Args {
+    SsdProduct p;           // rows of A are p.m, or (kSwap) p.n
+    int row_tiles, col_tiles, kblocks;
+    bool vec;               // 16-byte rows of out, preact and residual
+    unsigned *err;
+    unsigned long long wait_ns;
+};
+
+struct Ctrl {
+    uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
+    uint32_t tmem;
+    int abort;
+};
+static_assert(sizeof(Ctrl) <= kCtrlBytes, "control block");
+
+// A wait that another role's failure also ends; the first to run out reports.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Ctrl *ctl, const Args &a) {
+    const uint32_t b = smem_u32(bar);
+    if (mbar_try_wait(b, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        if (mbar_try_wait(b, parity)) return true;
+        if (*reinterpret_cast<volatile int *>(&ctl->abort)) return false;
+        if (globaltimer_ns() - t0 > a.wait_ns) {
+            *reinterpret_cast<volatile int *>(&ctl->abort) = 1;
+            ssd_report(a.err, SSD_DEVERR_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+// The same by a whole warp, which goes on or gives up as one.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Ctrl *ctl, const Args &a) {
+    return __all_sync(0xffffffffu, wait(bar, parity, ctl, a));
+}
+
+// Tiles in groups of 16 row tiles, column by column: the CTAs that run at one
+// time share rows of both operands in L2.
+__device__ __forceinline__ void tile_at(const Args &a, int t, int &row, int &col) {
+    constexpr int kGroup = 16;
+    const int per = kGroup * a.col_tiles, g = t / per, first = g * kGroup;
+    const int rows = min(kGroup, a.row_tiles - first);
+    row = first + (t - g * per) % rows;
+    col = (t - g * per) / rows;
+}
+
+__device__ __forceinline__ void act_all(float (&v)[8], SsdAct act) {
+    switch (act) {
+        case SsdAct::silu:
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = ssd_act(v[i], SsdAct::silu);
+            break;
+        case SsdAct::gelu:
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = ssd_act(v[i], SsdAct::gelu);
+            break;
+        case SsdAct::relu:
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = ssd_act(v[i], SsdAct::relu);
+            break;
+        default: break;
+    }
+}
+
+__device__ __forceinline__ float load_one(const void *p, long long i, SsdElt t) {
+    return t == SSD_ELT_F32 ? static_cast<const float *>(p)[i]
+                            : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
+}
+__device__ __forceinline__ void store_one(void *p, long long i, SsdElt t, float v) {
+    if (t == SSD_ELT_F32) static_cast<float *>(p)[i] = v;
+    else static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
+}
+
+// Eight columns n .. n + 7 of row m (m in range; n < p.n).
+__device__ __forceinline__ void finish_row8(const Args &a, long long m, long long n, float (&v)[8]) {
+    const SsdProduct &p = a.p;
+    const bool whole = a.vec && n + 8 <= p.n;
+    if (p.a_scale) {
+        const float s = __ldg(p.a_scale + m);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= n + i < p.n ? s * __ldg(p.b_scale + n + i) : 0.f;
+    }
+    if (p.bias) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += n + i < p.n ? __ldg(p.bias + n + i) : 0.f;
+    }
+    if (p.preact) {
+        if (whole) {
+            ssd_store_vec<8>(static_cast<__nv_bfloat16 *>(p.preact) + m * p.n + n, v);
+        } else {
+            for (int i = 0; i < 8 && n + i < p.n; ++i)
+                store_one(p.preact, m * p.n + n + i, SSD_ELT_BF16, v[i]);
+        }
+    }
+    act_all(v, p.act);
+    const long long ro = m * p.residual_row + n, oo = m * p.out_row + n;
+    if (p.residual) {
+        if (!whole) {
+            for (int i = 0; i < 8 && n + i < p.n; ++i) v[i] += load_one(p.residual, ro + i, p.out_type);
+        } else if (p.out_type == SSD_ELT_F32) {
+            SsdRaw<float, 8> r;
+            r.load(static_cast<const float *>(p.residual) + ro);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += r.get(i);
+        } else {
+            SsdRaw<__nv_bfloat16, 8> r;
+            r.load(static_cast<const __nv_bfloat16 *>(p.residual) + ro);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += r.get(i);
+        }
+    }
+    if (!whole) {
+        for (int i = 0; i < 8 && n + i < p.n; ++i) store_one(p.out, oo + i, p.out_type, v[i]);
+    } else if (p.out_type == SSD_ELT_F32) {
+        ssd_store_vec<8>(static_cast<float *>(p.out) + oo, v);
+    } else {
+        ssd_store_vec<8>(static_cast<__nv_bfloat16 *>(p.out) + oo, v);
+    }
+}
+
+// One value: token m, feature n (lanes are consecutive features).
+__device__ __forceinline__ void finish_one(const SsdProduct &p, long long m, long long n, float v) {
+    if (p.a_scale) v *= __ldg(p.a_scale + m) * __ldg(p.b_scale + n);
+    if (p.bias) v += __ldg(p.bias + n);
+    if (p.preact) store_one(p.preact, m * p.n + n, SSD_ELT_BF16, v);
+    v = ssd_act(v, p.act);
+    if (p.residual) v += load_one(p.residual, m * p.residual_row + n, p.out_type);
+    store_one(p.out, m * p.out_row + n, p.out_type, v);
+}
+
+// One k block of both operands into a stage.  Coordinates are (k, row) for a
+// K-major operand and (row, k) for an MN-major one, whose 64 x 64 boxes lie
+// one after another.
+template <int kBN, bool kAmn, bool kBmn, bool kFp8>
+__device__ __forceinline__ void load_stage(const CUtensorMap *ma, const CUtensorMap *mb,
+                                           uint32_t dst, uint32_t bar, int kb, int row, int col) {
+    constexpr int kK = kFp8 ? 128 : 64;
+    mbar_arrive_expect_tx(bar, stage_bytes(kBN));
+    if constexpr (kAmn) {
+#pragma unroll
+        for (int i = 0; i < kBM / 64; ++i)
+            tma_load_2d(dst + i * 8192, ma, bar, row * kBM + i * 64, kb * kK);
+    } else {
+        tma_load_2d(dst, ma, bar, kb * kK, row * kBM);
+    }
+    if constexpr (kBmn) {
+#pragma unroll
+        for (int i = 0; i < kBN / 64; ++i)
+            tma_load_2d(dst + kABytes + i * 8192, mb, bar, col * kBN + i * 64, kb * kK);
+    } else {
+        tma_load_2d(dst + kABytes, mb, bar, kb * kK, col * kBN);
+    }
+}
+
+template <int kBN, bool kAmn, bool kBmn, bool kFp8, bool kSwap, bool kSplit>
+__global__ void __launch_bounds__(kThreads, 1)
+product_tc_kernel(const __grid_constant__ CUtensorMap map_a,
+                  const __grid_constant__ CUtensorMap map_b, const __grid_constant__ Args a) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    constexpr int kStages = stages(kBN);
+    constexpr uint32_t kStage = stage_bytes(kBN), kCols = tmem_cols(kBN, kSplit);
+    Ctrl *ctl = reinterpret_cast<Ctrl *>(smem);
+    const uint32_t ring = smem_u32(smem) + kCtrlBytes;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool misplaced = (ring & 1023u) != 0u;    // the same in every CTA of the grid
+    if (misplaced) {
+        if (threadIdx.x == 0) ssd_report(a.err, SSD_DEVERR_SMEM_ALIGN);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(smem_u32(&ctl->full[i]), 1);
+            mbar_init(smem_u32(&ctl->empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&ctl->acc_full[i]), 1);
+            mbar_init(smem_u32(&ctl->acc_empty[i]), kEpiWarps);
+        }
+        mbar_init(smem_u32(&ctl->drain), 1);
+        ctl->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&ctl->tmem), kCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem;
+
+    // this CTA's tiles and, with kSplit, its part of the k blocks
+    const int ntiles = a.row_tiles * a.col_tiles;
+    const int rank = kSplit ? (int)cluster_rank() : 0, ranks = kSplit ? (int)cluster_size() : 1;
+    const int first = kSplit ? (int)blockIdx.x / ranks : (int)blockIdx.x;
+    const int step = kSplit ? ntiles : (int)gridDim.x;
+    const int kb0 = kSplit ? (int)((long long)a.kblocks * rank / ranks) : 0;
+    const int kb1 = kSplit ? (int)((long long)a.kblocks * (rank + 1) / ranks) : a.kblocks;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            tma_prefetch_desc(&map_a);
+            tma_prefetch_desc(&map_b);
+            uint32_t n = 0;             // blocks issued so far
+            bool ok = true;
+            for (int t = first; ok && t < ntiles; t += step) {
+                int row, col;
+                tile_at(a, t, row, col);
+                for (int kb = kb0; kb < kb1; ++kb, ++n) {
+                    const uint32_t s = n % kStages, turn = n / kStages;
+                    if (turn > 0 && !wait(&ctl->empty[s], (turn - 1) & 1, ctl, a)) {
+                        ok = false;
+                        break;
+                    }
+                    load_stage<kBN, kAmn, kBmn, kFp8>(&map_a, &map_b, ring + s * kStage,
+                                                      smem_u32(&ctl->full[s]), kb, row, col);
+                }
+            }
+            if (!ok) {                  // let the copies in flight land before the CTA ends
+                for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i)
+                    mbar_wait(smem_u32(&ctl->full[i % kStages]), (i / kStages) & 1, a.wait_ns);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t kId = kFp8 ? idesc_e4m3_f32(kBM, kBN)
+                                          : idesc_bf16_f32(kBM, kBN, kAmn, kBmn);
+            const uint64_t ad = kAmn ? smem_desc(ring, 8192, 1024, kSwizzle128B)
+                                     : smem_desc(ring, 16, 1024, kSwizzle128B);
+            const uint64_t bd = kBmn ? smem_desc(ring + kABytes, 8192, 1024, kSwizzle128B)
+                                     : smem_desc(ring + kABytes, 16, 1024, kSwizzle128B);
+            // a step's 32 bytes of k in a K-major row; 16 rows of k when MN-major
+            constexpr uint64_t kAStep = kAmn ? 2048 >> 4 : 32 >> 4;
+            constexpr uint64_t kBStep = kBmn ? 2048 >> 4 : 32 >> 4;
+            uint32_t n = 0, tiles = 0;
+            bool ok = true;
+            for (int t = first; ok && t < ntiles; t += step, ++tiles) {
+                const uint32_t buf = tiles & 1, turn = tiles >> 1;
+                const uint32_t d = tmem + (kSplit ? 0 : buf * kBN);
+                if (turn > 0 && !wait(&ctl->acc_empty[buf], (turn - 1) & 1, ctl, a)) break;
+                tc_fence_after();
+                for (int kb = kb0; kb < kb1; ++kb, ++n) {
+                    const uint32_t s = n % kStages;
+                    if (!wait(&ctl->full[s], (n / kStages) & 1, ctl, a)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t off = (uint64_t)(s * kStage) >> 4;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (kFp8)
+                            mma_ss_fp8(d, ad + off + i * kAStep, bd + off + i * kBStep, kId,
+                                       kb > kb0 || i > 0);
+                        else
+                            mma_ss(d, ad + off + i * kAStep, bd + off + i * kBStep, kId,
+                                   kb > kb0 || i > 0);
+                    }
+                    mma_commit(smem_u32(&ctl->empty[s]));
+                }
+                if (ok) mma_commit(smem_u32(&ctl->acc_full[buf]));
+            }
+            // every product has ended before the accumulators are freed
+            mma_commit(smem_u32(&ctl->drain));
+            mbar_wait(smem_u32(&ctl->drain), 0, a.wait_ns);
+        }
+    } else {
+        // a warp reads the 32 TMEM lanes of its number modulo 4; the two warps
+        // of a quarter share its columns
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        if constexpr (!kSplit) {
+            uint32_t tiles = 0;
+            for (int t = first; t < ntiles; t += step, ++tiles) {
+                const uint32_t buf = tiles & 1, turn = tiles >> 1;
+                int row, col;
+                tile_at(a, t, row, col);
+                if (!wait_warp(&ctl->acc_full[buf], turn & 1, ctl, a)) break;
+                tc_fence_after();
+                const long long m = (long long)row * kBM + quarter * 32 + lane;
+                const long long n0 = (long long)col * kBN;
+#pragma unroll
+                for (int c = half * 32; c < kBN; c += 64) {
+                    uint32_t r[32];
+                    tmem_ld32(tmem + lanes + buf * kBN + c, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8) {
+                        float v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[j + i]);
+                        if (m < a.p.m && n0 + c + j < a.p.n) finish_row8(a, m, n0 + c + j, v);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ctl->acc_empty[buf]));
+            }
+        } else {
+            // the partial sums, column by column, over the ring (every copy into
+            // it has been read: the last product waited for them)
+            if (wait_warp(&ctl->acc_full[0], 0, ctl, a)) {
+                tc_fence_after();
+                float *part = reinterpret_cast<float *>(smem + kCtrlBytes);
+#pragma unroll
+                for (int c = half * 16; c < kBN; c += 32) {
+                    uint32_t r[16];
+                    tmem_ld16(tmem + lanes + c, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        part[(c + i) * kBM + quarter * 32 + lane] = __uint_as_float(r[i]);
+                }
+                tc_fence_before();
+            }
+        }
+    }
+    if constexpr (kSplit) {
+        __syncwarp();
+        cluster_sync_all();
+        if (warp >= 2 && !ctl->abort) {
+            const int quarter = warp & 3, half = (warp - 2) >> 2;
+            const int r = quarter * 32 + lane;
+            int row, col;
+            tile_at(a, first, row, col);
+            const uint32_t part = smem_u32(smem) + kCtrlBytes;
+            uint32_t peer[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) peer[k] = cluster_map(part, k < ranks ? k : 0);
+            if constexpr (kSwap) {
+                // this rank's share of the columns (tokens)
+                const long long n = (long long)row * kBM + r;
+                for (int c = rank * 2 + half; c < kBN; c += 2 * ranks) {
+                    const long long m = (long long)col * kBN + c;
+                    float v = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (k < ranks) v += cluster_ld_f32(peer[k] + (c * kBM + r) * 4);
+                    if (m < a.p.m && n < a.p.n) finish_one(a.p, m, n, v);
+                }
+            } else {
+                const long long m = (long long)row * kBM + r;
+                for (int c = (rank * 2 + half) * 8; c < kBN; c += 16 * ranks) {
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        v[i] = 0.f;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (k < ranks) v[i] += cluster_ld_f32(peer[k] + ((c + i) * kBM + r) * 4);
+                    }
+                    const long long n = (long long)col * kBN + c;
+                    if (m < a.p.m && n < a.p.n) finish_row8(a, m, n, v);
+                }
+            }
+        }
+        __syncwarp();
+        cluster_sync_all();     // nobody leaves while its sums are being read
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(tmem, kCols);
+}
+
+// ------------------------------------------------------------------ host
+// A 2-D map of an operand: `rows` rows of k values.  K-major: boxes of 128
+// bytes of k by `box_rows`; MN-major: 64 rows by 64 values of k.
+bool operand_map(CUtensorMap *map, const void *base, bool fp8, bool mn, long long rows,
+                 long long k, long long stride, int box_rows) {
+    const auto enc = ssd_tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t size = fp8 ? 1 : 2;
+    const cuuint64_t dims[2] = {(cuuint64_t)(mn ? rows : k), (cuuint64_t)(mn ? k : rows)};
+    const cuuint64_t strides[1] = {(cuuint64_t)stride * size};
+    const cuuint32_t box[2] = {(cuuint32_t)(mn ? 64 : kRowBytes / size),
+                               (cuuint32_t)(mn ? 64 : box_rows)};
+    const cuuint32_t es[2] = {1, 1};
+    return enc(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+               const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool on_16(const void *p, long long stride, int size) {
+    return ((uintptr_t)p & 15u) == 0 && (stride * size) % 16 == 0;
+}
+
+template <int kBN, bool kAmn, bool kBmn, bool kFp8, bool kSwap, bool kSplit>
+cudaError_t launch(const SsdProduct &p, int sms, int ranks, unsigned *err, cudaStream_t stream) {
+    constexpr uint32_t kSmem = smem_bytes(kBN);
+    const long long rows = kSwap ? p.n : p.m, cols = kSwap ? p.m : p.n;
+    const void *rp = kSwap ? p.b : p.a, *cp = kSwap ? p.a : p.b;
+    const long long rs = kSwap ? p.b_row : (kAmn ? p.a_col : p.a_row);
+    const long long cs = kSwap ? p.a_row : (kBmn ? p.b_col : p.b_row);
+    Args a{};
+    a.p = p;
+    a.row_tiles = (int)((rows + kBM - 1) / kBM);
+    a.col_tiles = (int)((cols + kBN - 1) / kBN);
+    a.kblocks = (int)((p.k + (kFp8 ? 127 : 63)) / (kFp8 ? 128 : 64));
+    const int so = p.out_type == SSD_ELT_F32 ? 4 : 2;
+    a.vec = on_16(p.out, p.out_row, so) && (!p.residual || on_16(p.residual, p.residual_row, so)) &&
+            (!p.preact || on_16(p.preact, p.n, 2));
+    a.err = err;
+    a.wait_ns = ssd_debug_config().wait_ns;
+    CUtensorMap ma, mb;
+    if (!operand_map(&ma, rp, kFp8, kAmn, rows, p.k, rs, kBM) ||
+        !operand_map(&mb, cp, kFp8, kBmn, cols, p.k, cs, kBN))
+        return cudaErrorInvalidValue;
+    const auto kernel = product_tc_kernel<kBN, kAmn, kBmn, kFp8, kSwap, kSplit>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    const long long tiles = (long long)a.row_tiles * a.col_tiles;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(kSplit ? tiles * ranks : (tiles < sms ? tiles : sms)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kSplit ? ranks : 1;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = kSplit ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, ma, mb, a);
+}
+
+// Ranks of a split: enough clusters to fill the SMs, at least four k blocks a
+// rank, at most eight (portable cluster size).
+int split_ranks(long long tiles, long long kblocks, int sms) {
+    int r = 1;
+    while (r < 8 && tiles * r * 2 <= sms + sms / 8 && kblocks / (2 * r) >= 4) r *= 2;
+    return r;
+}
+
+template <bool kFp8>
+cudaError_t few_tokens(const SsdProduct &p, int sms, unsigned *err, cudaStream_t stream) {
+    const long long kb = (p.k + (kFp8 ? 127 : 63)) / (kFp8 ? 128 : 64);
+    const int ranks = split_ranks((p.n + kBM - 1) / kBM, kb, sms);
+    if (p.m <= 16) return launch<16, false, false, kFp8, true, true>(p, sms, ranks, err, stream);
+    if (p.m <= 32) return launch<32, false, false, kFp8, true, true>(p, sms, ranks, err, stream);
+    if (p.m <= 64) return launch<64, false, false, kFp8, true, true>(p, sms, ranks, err, stream);
+    return launch<128, false, false, kFp8, true, true>(p, sms, ranks, err, stream);
+}
+
+template <bool kAmn, bool kBmn, bool kFp8>
+cudaError_t many(const SsdProduct &p, int sms, unsigned *err, cudaStream_t stream) {
+    const long long kb = (p.k + (kFp8 ? 127 : 63)) / (kFp8 ? 128 : 64);
+    const long long rt = (p.m + kBM - 1) / kBM, ct = (p.n + 127) / 128;
+    // fewer tiles than half the SMs: split k
+    if (rt * ct * 2 <= sms + sms / 8)
+        return launch<128, kAmn, kBmn, kFp8, false, true>(p, sms, split_ranks(rt * ct, kb, sms), err,
+                                                         stream);
+    const long long wide = rt * ((p.n + 255) / 256);
+    if (wide >= sms) return launch<256, kAmn, kBmn, kFp8, false, false>(p, sms, 1, err, stream);
+    return launch<128, kAmn, kBmn, kFp8, false, false>(p, sms, 1, err, stream);
+}
+
+}  // namespace
+
+// Both operands' rows on 16-byte boundaries, sizes within a map's and a grid's range.
+bool ssd_product_tc_handles(const SsdProduct &p) {
+    if (p.in == SSD_ELT_F32) return false;
+    const int size = p.in == SSD_ELT_E4M3 ? 1 : 2;
+    const bool amn = p.a_row == 1 && p.a_col != 1, bmn = p.b_row == 1 && p.b_col != 1;
+    if (size == 1 && (amn || bmn)) return false;
+    if (amn && !bmn) return false;      // no caller multiplies so
+    const long long as = amn ? p.a_col : p.a_row, bs = bmn ? p.b_col : p.b_row;
+    if (!on_16(p.a, as, size) || !on_16(p.b, bs, size)) return false;
+    const long long tiles = ((p.m + 127) / 128) * ((p.n + 127) / 128);
+    return tiles < (1ll << 27) && as < (1ll << 36) && bs < (1ll << 36) && p.k < (1ll << 31);
+}
+
+cudaError_t ssd_launch_product_tc(const SsdProduct &p, int sms, unsigned *err,
+                                  cudaStream_t stream) {
+    const bool amn = p.a_row == 1 && p.a_col != 1, bmn = p.b_row == 1 && p.b_col != 1;
+    if (amn) return many<true, true, false>(p, sms, err, stream);
+    if (bmn) return many<false, true, false>(p, sms, err, stream);
+    const bool few = p.m <= 128;
+    if (p.in == SSD_ELT_E4M3)
+        return few ? few_tokens<true>(p, sms, err, stream)
+                   : many<false, false, true>(p, sms, err, stream);
+    return few ? few_tokens<false>(p, sms, err, stream)
+               : many<false, false, false>(p, sms, err, stream);
+}

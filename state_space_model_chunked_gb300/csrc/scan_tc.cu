@@ -1353,7 +1353,9 @@ ssd_tc_segment_pass_kernel(__nv_bfloat16 *__restrict__ ws_state, const float *__
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+}  // namespace
+
+PFN_cuTensorMapEncodeTiled_v12000 ssd_tensor_map_encoder() {
     std::call_once(g_encode_once, [] {
         void *fn = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -1365,11 +1367,13 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     return g_encode;
 }
 
+namespace {
+
 // 4-D bf16 map over [batch][L][d1][inner] with a box of 64 x 1 x 128 x 1,
 // 128-byte swizzle; out-of-range tokens read as zero.
 bool make_map(CUtensorMap *m, const void *base, uint64_t inner, uint64_t d1, uint64_t L,
               uint64_t batch) {
-    auto enc = encoder();
+    auto enc = ssd_tensor_map_encoder();
     if (!enc) return false;
     cuuint64_t dims[4] = {inner, d1, L, batch};
     cuuint64_t strides[3] = {inner * 2, inner * d1 * 2, inner * d1 * L * 2};
@@ -1515,7 +1519,7 @@ SsdTcPlan ssd_tc_plan(int batch, int L, int H, int P, int N, int G, int num_sms)
     SsdTcPlan p{};
     p.launches = 1;
     p.supported = P == kP && N == kN && num_sms > 0 && batch > 0 && L > 0 && H > 0 && G > 0 &&
-                  H % G == 0 && encoder() != nullptr;
+                  H % G == 0 && ssd_tensor_map_encoder() != nullptr;
     if (!p.supported) return p;
     p.heads_per_cta = ((H / G) % 2 == 0) ? 2 : 1;
     p.tiles = (L + kTile - 1) / kTile;
@@ -1573,7 +1577,7 @@ SsdTcPlan ssd_tc_plan_varlen(int nseq, const int *cu, int H, int P, int N, int G
     SsdTcPlan p{};
     p.launches = 1;
     p.supported = P == kP && N == kN && num_sms > 0 && nseq > 0 && cu != nullptr && H > 0 &&
-                  G > 0 && H % G == 0 && encoder() != nullptr;
+                  G > 0 && H % G == 0 && ssd_tensor_map_encoder() != nullptr;
     if (!p.supported) return p;
     int max_tiles = 0;
     for (int s = 0; s < nseq; ++s) {
