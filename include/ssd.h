@@ -491,8 +491,6 @@ typedef enum {
  *               y may be the residual itself (same pointer and stride).
  *   preact      p, contiguous, SSD_F32 for fp32 inputs and SSD_BF16 otherwise,
  *               or NULL: what ssd_linear_bwd needs of the forward call.
- *   workspace   ssd_linear_workspace_bytes() bytes, 256-byte aligned (may be
- *               NULL when that is 0).
  * bf16 and fp8 inputs whose rows start on 16-byte boundaries run on the
  * tensor cores (products of the inputs as they are, fp32 sums); fp32 inputs
  * and other alignments in fp32 multiply-adds.  tokens == 0 enqueues nothing.
@@ -504,8 +502,7 @@ ssd_status ssd_linear_fwd(const void *x, const float *x_scale, const void *w,
                           ssd_activation activation, ssd_dtype in_dtype, ssd_dtype out_dtype,
                           long long tokens, int features, int inner, long long x_stride,
                           long long residual_stride, void *y, long long y_stride, void *preact,
-                          void *workspace, size_t workspace_bytes, cudaStream_t stream);
-size_t ssd_linear_workspace_bytes(ssd_dtype in_dtype, long long tokens, int features, int inner);
+                          cudaStream_t stream);
 
 /* Gradients of ssd_linear_fwd (fp32 or bf16 inputs).  With dp = dy act'(preact):
  *     dx[m][k] = sum_n dp[m][n] w[n][k]

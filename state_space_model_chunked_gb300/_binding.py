@@ -37,7 +37,6 @@ EXPORTED_SYMBOLS = (
     "ssd_rmsnorm_bwd",
     "ssd_rmsnorm_bwd_workspace_bytes",
     "ssd_linear_fwd",
-    "ssd_linear_workspace_bytes",
     "ssd_linear_bwd",
     "ssd_linear_bwd_workspace_bytes",
     "ssd_gated_scan_fwd",
@@ -81,6 +80,8 @@ def load():
     """Load libssd.so (built in-tree by state_space_model_chunked_gb300.build).
     Raises if it is missing: there is no fallback path."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -144,9 +145,7 @@ def load():
             "ssd_rmsnorm_bwd": [_vp] * 5 + [_int, _int, ll, _int, ll, ll, ll] + [_vp] * 4 +
                                [_sz, _vp],
             "ssd_rmsnorm_bwd_workspace_bytes": [ll, _int],
-            "ssd_linear_fwd": [_vp] * 6 + [_int] * 3 + [ll, _int, _int, ll, ll, _vp, ll, _vp, _vp,
-                                                        _sz, _vp],
-            "ssd_linear_workspace_bytes": [_int, ll, _int, _int],
+            "ssd_linear_fwd": [_vp] * 6 + [_int] * 3 + [ll, _int, _int, ll, ll, _vp, ll, _vp, _vp],
             "ssd_linear_bwd": [_vp] * 4 + [_int, _int, ll, _int, _int, ll, ll] + [_vp] * 4 +
                               [_sz, _vp],
             "ssd_linear_bwd_workspace_bytes": [_int, _int, ll, _int, _int],

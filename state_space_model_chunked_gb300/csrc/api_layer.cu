@@ -163,17 +163,12 @@ ssd_status ssd_rmsnorm_bwd(const void *dy, const void *s, const float *weight, c
     return launched(ssd_launch_rmsnorm_bwd(a, static_cast<float *>(workspace), sms, stream));
 }
 
-size_t ssd_linear_workspace_bytes(ssd_dtype in_dtype, long long tokens, int features, int inner) {
-    if (check_linear(in_dtype, tokens, features, inner) != SSD_OK) return kBad;
-    return 0;
-}
-
 ssd_status ssd_linear_fwd(const void *x, const float *x_scale, const void *w,
                           const float *w_scale, const float *bias, const void *residual,
                           ssd_activation activation, ssd_dtype in_dtype, ssd_dtype out_dtype,
                           long long tokens, int features, int inner, long long x_stride,
                           long long residual_stride, void *y, long long y_stride, void *preact,
-                          void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+                          cudaStream_t stream) {
     const ssd_status st = check_linear(in_dtype, tokens, features, inner);
     if (st != SSD_OK) return st;
     if (!known_type(out_dtype) || !valid_activation(activation)) return SSD_ERR_INVALID_ARG;
@@ -190,8 +185,6 @@ ssd_status ssd_linear_fwd(const void *x, const float *x_scale, const void *w,
         return SSD_ERR_INVALID_ARG;
     if (x_stride < inner || y_stride < features || (residual && residual_stride < features))
         return SSD_ERR_INVALID_ARG;
-    (void)workspace;
-    (void)workspace_bytes;
     SsdProduct p{x, w, elt(in_dtype), tokens, features, inner, x_stride, 1, inner, 1, x_scale,
                  w_scale, bias, residual, residual_stride, (SsdAct)(int)activation, y, preact,
                  elt(out_dtype), in_dtype == SSD_F32 ? SSD_ELT_F32 : SSD_ELT_BF16, y_stride};

@@ -36,30 +36,35 @@ def _activation(name):
     return code
 
 
+# The checks below are one expression a tensor on the way that passes: a call of
+# one token is as long as its marshalling.
 def _cuda(t, name):
+    """The tensor's device index."""
     if t is None:
         raise ValueError(f"{name} is required")
-    if not t.is_cuda:
+    index = t.get_device()
+    if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
+    return index
 
 
-def _like(t, name, dtype, device, shape):
-    if t.dtype != dtype:
+def _refuse(t, name, dtype, index, shape):
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _full(t, name, dtype, device, shape):
+def _full(t, name, dtype, index, shape):
     """Address of a contiguous array (None: no array)."""
     if t is None:
         return None
-    _like(t, name, dtype, device, shape)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if (t.dtype is not dtype or t.get_device() != index or t.shape != shape
+            or not t.is_contiguous()):
+        _refuse(t, name, dtype, index, shape)
     return t.data_ptr()
 
 
@@ -88,35 +93,48 @@ def _row_stride(t, name):
     return row
 
 
-def _rows(t, name, dtype, device, shape):
+def _rows(t, name, dtype, index, shape):
     """(address, row stride) of a matrix (None: no matrix)."""
     if t is None:
         return None, 0
-    _like(t, name, dtype, device, shape)
+    if t.dtype is not dtype or t.get_device() != index or t.shape != shape:
+        _refuse(t, name, dtype, index, shape)
+    if t.is_contiguous() and t.dim() > 1:
+        return t.data_ptr(), shape[-1]
     return t.data_ptr(), _row_stride(t, name)
 
 
-def _call(device, fn, *args):
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
+def _call(index, fn, *args):
     """The C call on the device's current stream; `args` without the stream."""
-    index = device.index
-    if index == torch.cuda.current_device():
-        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if index == _current_device():
+        rc = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+        with torch.cuda.device(index):
+            rc = fn(*args, _raw_stream(index))
     if rc:
         _check(fn.__name__, rc)
 
 
-def _size(device, fn, *args):
-    if device.index == torch.cuda.current_device():
+def _size(index, fn, *args):
+    if index == _current_device():
         n = fn(*args)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             n = fn(*args)
     if n == _BAD:
         raise SsdError(fn.__name__, 1, "invalid sizes")
     return n
+
+
+def _index(device):
+    if device is None:
+        return torch.cuda.current_device()
+    device = torch.device(device)
+    return torch.cuda.current_device() if device.index is None else device.index
 
 
 def _scratch(workspace, need, device):
@@ -125,6 +143,8 @@ def _scratch(workspace, need, device):
         return None, None, 0
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif workspace.device != device:
+        raise ValueError(f"workspace is on {workspace.device}, expected {device}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -147,14 +167,14 @@ def rmsnorm_fwd(x, weight, residual=None, *, eps=1e-5, out_dtype=None, y=None, r
     Returns (y, residual_out = s in the residual's dtype or None, rstd [...]
     f32, scale [...] f32 or None).  residual_out may be the residual itself."""
     lib = load()
-    dev = _cuda(x, "x")
+    at, dev = _cuda(x, "x"), x.device
     shape, rows_shape, width = x.shape, x.shape[:-1], x.shape[-1]
     out_dtype = x.dtype if out_dtype is None else out_dtype
     xc, oc = _code(x.dtype, "x"), _code(out_dtype, "out_dtype")
     xp, xs = x.data_ptr(), _row_stride(x, "x")
     rp, rs, sc = None, 0, xc
     if residual is not None:
-        rp, rs = _rows(residual, "residual", residual.dtype, dev, shape)
+        rp, rs = _rows(residual, "residual", residual.dtype, at, shape)
         sc = _code(residual.dtype, "residual")
         if residual_out is None:
             residual_out = torch.empty(shape, dtype=residual.dtype, device=dev)
@@ -168,18 +188,17 @@ def rmsnorm_fwd(x, weight, residual=None, *, eps=1e-5, out_dtype=None, y=None, r
         scale = None
     elif scale is None:
         scale = torch.empty(rows_shape, dtype=_F32, device=dev)
-    _call(dev, lib.ssd_rmsnorm_fwd, xp, rp, _full(weight, "weight", _F32, dev, (width,)), eps, xc,
-          sc, oc, _count(rows_shape), width, xs, rs, _full(y, "y", out_dtype, dev, shape),
+    _call(at, lib.ssd_rmsnorm_fwd, xp, rp, _full(weight, "weight", _F32, at, (width,)), eps, xc,
+          sc, oc, _count(rows_shape), width, xs, rs, _full(y, "y", out_dtype, at, shape),
           _full(residual_out, "residual_out", residual.dtype if residual is not None else None,
-                dev, shape),
-          _full(rstd, "rstd", _F32, dev, rows_shape), _full(scale, "scale", _F32, dev, rows_shape))
+                at, shape),
+          _full(rstd, "rstd", _F32, at, rows_shape), _full(scale, "scale", _F32, at, rows_shape))
     return y, residual_out, rstd, scale
 
 
 def rmsnorm_bwd_workspace_bytes(rows, width, device=None):
     """Workspace bytes of rmsnorm_bwd on the device."""
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    return _size(dev, load().ssd_rmsnorm_bwd_workspace_bytes, rows, width)
+    return _size(_index(device), load().ssd_rmsnorm_bwd_workspace_bytes, rows, width)
 
 
 def rmsnorm_bwd(dy, s, weight, rstd, dresidual=None, *, dx=None, ds=None, dweight=None,
@@ -190,12 +209,12 @@ def rmsnorm_bwd(dy, s, weight, rstd, dresidual=None, *, dx=None, ds=None, dweigh
     in dy's dtype and of the residual in s's (one tensor when those agree),
     and of the weight, f32."""
     lib = load()
-    dev = _cuda(dy, "dy")
+    at, dev = _cuda(dy, "dy"), dy.device
     shape, width = dy.shape, dy.shape[-1]
     yc = _code(dy.dtype, "dy")
     yp, ys = dy.data_ptr(), _row_stride(dy, "dy")
-    sp, ss = _rows(s, "s", s.dtype, dev, shape)
-    dp, dstride = _rows(dresidual, "dresidual", s.dtype, dev, shape)
+    sp, ss = _rows(s, "s", s.dtype, at, shape)
+    dp, dstride = _rows(dresidual, "dresidual", s.dtype, at, shape)
     rows = _count(shape[:-1])
     if dx is None:
         dx = torch.empty(shape, dtype=dy.dtype, device=dev)
@@ -207,33 +226,25 @@ def rmsnorm_bwd(dy, s, weight, rstd, dresidual=None, *, dx=None, ds=None, dweigh
         ds = torch.empty(shape, dtype=s.dtype, device=dev)
     if dweight is None:
         dweight = torch.empty((width,), dtype=_F32, device=dev)
-    need = _size(dev, lib.ssd_rmsnorm_bwd_workspace_bytes, rows, width)
+    need = _size(at, lib.ssd_rmsnorm_bwd_workspace_bytes, rows, width)
     _keep, wp, wb = _scratch(workspace, need, dev)
-    _call(dev, lib.ssd_rmsnorm_bwd, yp, sp, _full(weight, "weight", _F32, dev, (width,)),
-          _full(rstd, "rstd", _F32, dev, shape[:-1]), dp, yc, _code(s.dtype, "s"), rows, width, ys,
-          ss, dstride, _full(dx, "dx", dy.dtype, dev, shape),
-          None if one else _full(ds, "ds", s.dtype, dev, shape),
-          _full(dweight, "dweight", _F32, dev, (width,)), wp, wb)
+    _call(at, lib.ssd_rmsnorm_bwd, yp, sp, _full(weight, "weight", _F32, at, (width,)),
+          _full(rstd, "rstd", _F32, at, shape[:-1]), dp, yc, _code(s.dtype, "s"), rows, width, ys,
+          ss, dstride, _full(dx, "dx", dy.dtype, at, shape),
+          None if one else _full(ds, "ds", s.dtype, at, shape),
+          _full(dweight, "dweight", _F32, at, (width,)), wp, wb)
     return dx, dx if one else ds, dweight
 
 
 # -------------------------------------------------------------------- product
-def linear_workspace_bytes(dtype, tokens, features, inner, device=None):
-    """Workspace bytes of linear_fwd for inputs of the dtype on the device."""
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    return _size(dev, load().ssd_linear_workspace_bytes, _code(dtype, "dtype"), tokens, features,
-                 inner)
-
-
 def linear_bwd_workspace_bytes(dtype, tokens, features, inner, activation=None, device=None):
     """Workspace bytes of linear_bwd on the device."""
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    return _size(dev, load().ssd_linear_bwd_workspace_bytes, _code(dtype, "dtype"),
+    return _size(_index(device), load().ssd_linear_bwd_workspace_bytes, _code(dtype, "dtype"),
                  _activation(activation), tokens, features, inner)
 
 
 def linear_fwd(x, w, bias=None, residual=None, *, activation=None, x_scale=None, w_scale=None,
-               out_dtype=None, y=None, preact=None, return_preact=False, workspace=None):
+               out_dtype=None, y=None, preact=None, return_preact=False):
     """y = act(x w^T * x_scale[:, None] * w_scale + bias) + residual.
 
     x [..., inner] and w [features, inner]: f32, bf16, or float8_e4m3fn with
@@ -243,7 +254,7 @@ def linear_fwd(x, w, bias=None, residual=None, *, activation=None, x_scale=None,
     residual itself.  Returns y, or (y, preact) with return_preact: the values
     before the activation, which linear_bwd needs."""
     lib = load()
-    dev = _cuda(x, "x")
+    at, dev = _cuda(x, "x"), x.device
     act = _activation(activation)
     xc = _code(x.dtype, "x")
     lead, inner = x.shape[:-1], x.shape[-1]
@@ -255,20 +266,18 @@ def linear_fwd(x, w, bias=None, residual=None, *, activation=None, x_scale=None,
     out_dtype = kept if out_dtype is None else out_dtype
     oc = _code(out_dtype, "out_dtype")
     shape = lead + (features,)
-    rp, rs = _rows(residual, "residual", out_dtype, dev, shape)
+    rp, rs = _rows(residual, "residual", out_dtype, at, shape)
     if y is None:
         y = torch.empty(shape, dtype=out_dtype, device=dev)
-    yp, ys = _rows(y, "y", out_dtype, dev, shape)
+    yp, ys = _rows(y, "y", out_dtype, at, shape)
     if return_preact and preact is None:
         preact = torch.empty(shape, dtype=kept, device=dev)
     tokens = _count(lead)
-    need = _size(dev, lib.ssd_linear_workspace_bytes, xc, tokens, features, inner)
-    _keep, wp, wb = _scratch(workspace, need, dev)
-    _call(dev, lib.ssd_linear_fwd, xp, _full(x_scale, "x_scale", _F32, dev, lead),
-          _full(w, "w", x.dtype, dev, (features, inner)),
-          _full(w_scale, "w_scale", _F32, dev, (features,)),
-          _full(bias, "bias", _F32, dev, (features,)), rp, act, xc, oc, tokens, features, inner,
-          xs, rs, yp, ys, _full(preact, "preact", kept, dev, shape), wp, wb)
+    _call(at, lib.ssd_linear_fwd, xp, _full(x_scale, "x_scale", _F32, at, lead),
+          _full(w, "w", x.dtype, at, (features, inner)),
+          _full(w_scale, "w_scale", _F32, at, (features,)),
+          _full(bias, "bias", _F32, at, (features,)), rp, act, xc, oc, tokens, features, inner,
+          xs, rs, yp, ys, _full(preact, "preact", kept, at, shape))
     return (y, preact) if return_preact else y
 
 
@@ -279,13 +288,13 @@ def linear_bwd(dy, x, w, preact=None, *, activation=None, bias=True, need_dx=Tru
     (dx, dw, dbias): in dy's dtype, dy's dtype and f32; None for what is not
     wanted (need_dx, need_dw, bias).  The residual's gradient is dy."""
     lib = load()
-    dev = _cuda(dy, "dy")
+    at, dev = _cuda(dy, "dy"), dy.device
     act = _activation(activation)
     dt, code = dy.dtype, _code(dy.dtype, "dy")
     lead, features = dy.shape[:-1], dy.shape[-1]
     inner = x.shape[-1]
     yp, ys = dy.data_ptr(), _row_stride(dy, "dy")
-    xp, xs = _rows(x, "x", dt, dev, lead + (inner,))
+    xp, xs = _rows(x, "x", dt, at, lead + (inner,))
     tokens = _count(lead)
     if need_dx and dx is None:
         dx = torch.empty(lead + (inner,), dtype=dt, device=dev)
@@ -293,20 +302,19 @@ def linear_bwd(dy, x, w, preact=None, *, activation=None, bias=True, need_dx=Tru
         dw = torch.empty((features, inner), dtype=dt, device=dev)
     if bias and dbias is None:
         dbias = torch.empty((features,), dtype=_F32, device=dev)
-    need = _size(dev, lib.ssd_linear_bwd_workspace_bytes, code, act, tokens, features, inner)
+    need = _size(at, lib.ssd_linear_bwd_workspace_bytes, code, act, tokens, features, inner)
     _keep, wp, wb = _scratch(workspace, need, dev)
-    _call(dev, lib.ssd_linear_bwd, yp, xp, _full(w, "w", dt, dev, (features, inner)),
-          _full(preact, "preact", dt, dev, dy.shape), act, code, tokens, features, inner, ys, xs,
-          _full(dx, "dx", dt, dev, lead + (inner,)), _full(dw, "dw", dt, dev, (features, inner)),
-          _full(dbias, "dbias", _F32, dev, (features,)), wp, wb)
+    _call(at, lib.ssd_linear_bwd, yp, xp, _full(w, "w", dt, at, (features, inner)),
+          _full(preact, "preact", dt, at, dy.shape), act, code, tokens, features, inner, ys, xs,
+          _full(dx, "dx", dt, at, lead + (inner,)), _full(dw, "dw", dt, at, (features, inner)),
+          _full(dbias, "dbias", _F32, at, (features,)), wp, wb)
     return dx, dw, dbias
 
 
 # ----------------------------------------------------------------- recurrence
 def gated_scan_workspace_bytes(dtype, tokens, width, device=None):
     """Workspace bytes of gated_scan_fwd and gated_scan_bwd on the device."""
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    return _size(dev, load().ssd_gated_scan_workspace_bytes, _code(dtype, "dtype"), tokens, width)
+    return _size(_index(device), load().ssd_gated_scan_workspace_bytes, _code(dtype, "dtype"), tokens, width)
 
 
 def _sequences(x, name, cu_seqlens, cu_seqlens_dev):
@@ -324,7 +332,7 @@ def _sequences(x, name, cu_seqlens, cu_seqlens_dev):
         raise ValueError(f"cu_seqlens ends at {int(cu[-1])}, {name} holds {x.shape[0]} tokens")
     if cu_seqlens_dev is None:
         cu_seqlens_dev = torch.from_numpy(cu).to(x.device)
-    dev_ptr = _full(cu_seqlens_dev, "cu_seqlens_dev", torch.int32, x.device, (cu.size,))
+    dev_ptr = _full(cu_seqlens_dev, "cu_seqlens_dev", torch.int32, x.get_device(), (cu.size,))
     return cu.size - 1, 0, cu_ptr, dev_ptr, x.shape[0], (cu, cu_seqlens_dev)
 
 
@@ -341,26 +349,26 @@ def gated_scan_fwd(x, g, z=None, init_state=None, *, cu_seqlens=None, cu_seqlens
     [ceil(tokens / 64), width] f32 that gated_scan_bwd needs with
     return_checkpoints."""
     lib = load()
-    dev = _cuda(x, "x")
+    at, dev = _cuda(x, "x"), x.device
     code, shape, width = _code(x.dtype, "x"), x.shape, x.shape[-1]
     nseq, length, cu_ptr, cu_dev, tokens, _keep_cu = _sequences(x, "x", cu_seqlens, cu_seqlens_dev)
     xs = _row_stride(x, "x")
-    gp, gs = _rows(g, "g", x.dtype, dev, shape)
-    zp, zs = _rows(z, "z", x.dtype, dev, shape)
+    gp, gs = _rows(g, "g", x.dtype, at, shape)
+    zp, zs = _rows(z, "z", x.dtype, at, shape)
     if y is None:
         y = torch.empty(shape, dtype=x.dtype, device=dev)
-    yp, ys = _rows(y, "y", x.dtype, dev, shape)
+    yp, ys = _rows(y, "y", x.dtype, at, shape)
     if final_state is None and return_final:
         final_state = torch.empty((nseq, width), dtype=_F32, device=dev)
     kept = (-(-tokens // GATED_SCAN_CHECKPOINT), width)
     if checkpoints is None and return_checkpoints:
         checkpoints = torch.empty(kept, dtype=_F32, device=dev)
-    need = _size(dev, lib.ssd_gated_scan_workspace_bytes, code, tokens, width)
+    need = _size(at, lib.ssd_gated_scan_workspace_bytes, code, tokens, width)
     _keep, wp, wb = _scratch(workspace, need, dev)
-    _call(dev, lib.ssd_gated_scan_fwd, x.data_ptr(), gp, zp, code, nseq, length, cu_ptr, cu_dev,
-          width, xs, gs, zs, _full(init_state, "init_state", _F32, dev, (nseq, width)), yp, ys,
-          _full(final_state, "final_state", _F32, dev, (nseq, width)),
-          _full(checkpoints, "checkpoints", _F32, dev, kept), wp, wb)
+    _call(at, lib.ssd_gated_scan_fwd, x.data_ptr(), gp, zp, code, nseq, length, cu_ptr, cu_dev,
+          width, xs, gs, zs, _full(init_state, "init_state", _F32, at, (nseq, width)), yp, ys,
+          _full(final_state, "final_state", _F32, at, (nseq, width)),
+          _full(checkpoints, "checkpoints", _F32, at, kept), wp, wb)
     return (y, final_state, checkpoints) if return_checkpoints else (y, final_state)
 
 
@@ -372,13 +380,13 @@ def gated_scan_bwd(dy, x, g, checkpoints, z=None, init_state=None, dfinal=None, 
     and the checkpoints it returned.  dx, dg and dz may be column ranges of one
     matrix.  Returns (dx, dg, dz or None, dinit [nseq, width] f32 or None)."""
     lib = load()
-    dev = _cuda(x, "x")
+    at, dev = _cuda(x, "x"), x.device
     code, shape, width = _code(x.dtype, "x"), x.shape, x.shape[-1]
     nseq, length, cu_ptr, cu_dev, tokens, _keep_cu = _sequences(x, "x", cu_seqlens, cu_seqlens_dev)
     xs = _row_stride(x, "x")
-    yp, ys = _rows(dy, "dy", x.dtype, dev, shape)
-    gp, gs = _rows(g, "g", x.dtype, dev, shape)
-    zp, zs = _rows(z, "z", x.dtype, dev, shape)
+    yp, ys = _rows(dy, "dy", x.dtype, at, shape)
+    gp, gs = _rows(g, "g", x.dtype, at, shape)
+    zp, zs = _rows(z, "z", x.dtype, at, shape)
     if dx is None:
         dx = torch.empty(shape, dtype=x.dtype, device=dev)
     if dg is None:
@@ -387,21 +395,21 @@ def gated_scan_bwd(dy, x, g, checkpoints, z=None, init_state=None, dfinal=None, 
         dz = None
     elif dz is None:
         dz = torch.empty(shape, dtype=x.dtype, device=dev)
-    dxp, dxs = _rows(dx, "dx", x.dtype, dev, shape)
-    dgp, dgs = _rows(dg, "dg", x.dtype, dev, shape)
-    dzp, dzs = _rows(dz, "dz", x.dtype, dev, shape)
+    dxp, dxs = _rows(dx, "dx", x.dtype, at, shape)
+    dgp, dgs = _rows(dg, "dg", x.dtype, at, shape)
+    dzp, dzs = _rows(dz, "dz", x.dtype, at, shape)
     if dinit is None and return_dinit:
         dinit = torch.empty((nseq, width), dtype=_F32, device=dev)
     kept = (-(-tokens // GATED_SCAN_CHECKPOINT), width)
     if checkpoints is None:
         raise ValueError("checkpoints is required")
-    need = _size(dev, lib.ssd_gated_scan_workspace_bytes, code, tokens, width)
+    need = _size(at, lib.ssd_gated_scan_workspace_bytes, code, tokens, width)
     _keep, wp, wb = _scratch(workspace, need, dev)
-    _call(dev, lib.ssd_gated_scan_bwd, yp, x.data_ptr(), gp, zp, code, nseq, length, cu_ptr, cu_dev,
-          width, ys, xs, gs, zs, _full(init_state, "init_state", _F32, dev, (nseq, width)),
-          _full(checkpoints, "checkpoints", _F32, dev, kept),
-          _full(dfinal, "dfinal", _F32, dev, (nseq, width)), dxp, dxs, dgp, dgs, dzp, dzs,
-          _full(dinit, "dinit", _F32, dev, (nseq, width)), wp, wb)
+    _call(at, lib.ssd_gated_scan_bwd, yp, x.data_ptr(), gp, zp, code, nseq, length, cu_ptr, cu_dev,
+          width, ys, xs, gs, zs, _full(init_state, "init_state", _F32, at, (nseq, width)),
+          _full(checkpoints, "checkpoints", _F32, at, kept),
+          _full(dfinal, "dfinal", _F32, at, (nseq, width)), dxp, dxs, dgp, dgs, dzp, dzs,
+          _full(dinit, "dinit", _F32, at, (nseq, width)), wp, wb)
     return dx, dg, dz, dinit
 
 
@@ -409,16 +417,16 @@ def gated_state_update(state, x, g, z=None, *, y=None):
     """One token of the gated recurrence: state [..., width] f32, updated in
     place; x, g, z [..., width] f32 or bf16.  Returns y in x's dtype."""
     lib = load()
-    dev = _cuda(x, "x")
+    at, dev = _cuda(x, "x"), x.device
     code, shape = _code(x.dtype, "x"), x.shape
     xs = _row_stride(x, "x")
-    gp, gs = _rows(g, "g", x.dtype, dev, shape)
-    zp, zs = _rows(z, "z", x.dtype, dev, shape)
+    gp, gs = _rows(g, "g", x.dtype, at, shape)
+    zp, zs = _rows(z, "z", x.dtype, at, shape)
     if state is None:
         raise ValueError("state is required")
     if y is None:
         y = torch.empty(shape, dtype=x.dtype, device=dev)
-    _call(dev, lib.ssd_gated_state_update, _full(state, "state", _F32, dev, shape), x.data_ptr(),
+    _call(at, lib.ssd_gated_state_update, _full(state, "state", _F32, at, shape), x.data_ptr(),
           gp, zp, code, _count(shape[:-1]), shape[-1], xs, gs, zs,
-          _full(y, "y", x.dtype, dev, shape))
+          _full(y, "y", x.dtype, at, shape))
     return y
