@@ -41,7 +41,7 @@ __device__ __forceinline__ float sigmoidf(float z) { return __fdividef(1.f, 1.f 
 //
 //   a tile publishes its own (A, H) as soon as its loads have landed, then
 //   walks back over its predecessors' until one has published the state that
-//   leaves it, and publishes its own leaving state.
+//   leaves it, and replaces its (A, H) by its own leaving state.
 //
 // Tiles are handed out by a counter in the order of the walk, so a tile waits
 // only for tiles that already run; every wait is bounded in time.
@@ -55,89 +55,116 @@ constexpr int kFwdTok = 16, kBwdTok = 8;
 constexpr int kFwdTile = kWarps * kFwdTok, kBwdTile = kWarps * kBwdTok;
 static_assert(kBwdTile == kEvery, "a backward tile starts from a kept state");
 static_assert(kEvery % kFwdTok == 0, "kept states are those that enter a warp's run");
-constexpr unsigned kNone = 0, kRun = 1, kState = 2;    // what a tile has published
 
-// Global memory of the joins: per (tile, block of channels) a word, per (tile,
-// channel) the run (A, H) and the state behind it.
+// What a tile tells the tiles after it, per channel: one 64-bit word, written
+// and read whole, so it needs no flag, no fence and no second trip to L2.  The
+// low half is A of a run, or -1 for a state, or all ones: nothing yet (A of a
+// run is in [0, 1] or the canonical NaN); the high half is H or the state.
+// The words and the ticket are set to all ones before the kernel.
 struct Joins {
-    unsigned *ticket, *word;
-    float2 *run;
-    float *state;
+    unsigned *ticket;
+    uint2 *word;            // [tiles][width]
     unsigned *err;
     unsigned long long wait_ns;
     int withhold;           // test hook: the walk's first tile publishes nothing
 };
+constexpr unsigned kUnset = 0xffffffffu;
 
-__device__ __forceinline__ unsigned ld_acquire(const unsigned *p) {
-    unsigned v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-    return v;
-}
-__device__ __forceinline__ void st_release(unsigned *p, unsigned v) {
-    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
-}
-
-// One warp publishes a tile's word after its lanes' values.
-__device__ __forceinline__ void publish(unsigned *word, unsigned v) {
-    __threadfence();
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) st_release(word, v);
-}
-
-// The state that enters tile number `at` of the walk (at > 0), for this lane's
-// V channels from c: one warp, predecessors at - 1, at - 2, ... of the walk.
-// The words of 32 of them are polled at a time.
+// One lane's V words.
 template <int V>
-__device__ __forceinline__ void walk_back(const Joins &j, int at, int blocks, int block, int width,
-                                          int c, float (&h)[V]) {
-    const int lane = threadIdx.x & 31;
-    float A[V], H[V];
-#pragma unroll
-    for (int k = 0; k < V; ++k) A[k] = 1.f, H[k] = 0.f;
-    for (int p = at - 1;; p -= 32) {
-        const int mine = p - lane;
-        const unsigned *word = j.word + (size_t)(mine < 0 ? 0 : mine) * blocks + block;
-        unsigned states, runs;
-        unsigned long long t0 = 0;
-        for (;;) {
-            const unsigned v = mine < 0 ? kRun : ld_acquire(word);
-            states = __ballot_sync(0xffffffffu, v == kState);
-            runs = __ballot_sync(0xffffffffu, v != kNone);
-            // tiles before the nearest state (all 32 without one) must have their runs
-            const unsigned need = states ? (states & -states) - 1 : 0xffffffffu;
-            if ((runs & need) == need) break;
-            unsigned long long now;
-            asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
-            if (t0 == 0) t0 = now;
-            if (__shfl_sync(0xffffffffu, now - t0 > j.wait_ns, 0)) {    // lane 0's clock decides
-                if (lane == 0) ssd_report(j.err, SSD_DEVERR_TIMEOUT);
-#pragma unroll
-                for (int k = 0; k < V; ++k) h[k] = 0.f;
-                return;
-            }
-        }
-        const int n = states ? __ffs(states) - 1 : 32;
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            if (c < width) {
-                const float2 *r = j.run + (size_t)(p - i) * width + c;
-#pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    const float2 v = __ldcg(r + k);
-                    H[k] += A[k] * v.y;
-                    A[k] *= v.x;
-                }
-            }
-        }
-        if (states || p - 32 < 0) {
-#pragma unroll
-            for (int k = 0; k < V; ++k)
-                h[k] = states && c < width
-                           ? A[k] * __ldcg(j.state + (size_t)(p - n) * width + c + k) + H[k]
-                           : H[k];
-            return;
+struct Words {
+    uint2 w[V];
+    __device__ __forceinline__ void load(const uint2 *p) {
+        if constexpr (V == 2) {
+            unsigned long long a, b;
+            asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];"
+                         : "=l"(a), "=l"(b) : "l"(p) : "memory");
+            w[0] = make_uint2((unsigned)a, (unsigned)(a >> 32));
+            w[1] = make_uint2((unsigned)b, (unsigned)(b >> 32));
+        } else {
+            unsigned long long a;
+            asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(a) : "l"(p) : "memory");
+            w[0] = make_uint2((unsigned)a, (unsigned)(a >> 32));
         }
     }
+    __device__ __forceinline__ void store(uint2 *p) const {
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+            asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(p + k),
+                         "l"((unsigned long long)w[k].x | ((unsigned long long)w[k].y << 32))
+                         : "memory");
+    }
+    __device__ __forceinline__ bool set() const {
+        bool all = true;
+#pragma unroll
+        for (int k = 0; k < V; ++k) all &= w[k].x != kUnset;
+        return all;
+    }
+};
+
+template <int V>
+__device__ __forceinline__ void publish_run(uint2 *p, const float (&A)[V], const float (&H)[V]) {
+    Words<V> m;
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+        m.w[k] = make_uint2(A[k] == A[k] ? __float_as_uint(A[k]) : 0x7fffffffu,
+                            __float_as_uint(H[k]));
+    m.store(p);
+}
+template <int V>
+__device__ __forceinline__ void publish_state(uint2 *p, const float (&h)[V]) {
+    Words<V> m;
+#pragma unroll
+    for (int k = 0; k < V; ++k) m.w[k] = make_uint2(__float_as_uint(-1.f), __float_as_uint(h[k]));
+    m.store(p);
+}
+
+// The state that enters tile number `at` of the walk (at > 0) in a lane's V
+// channels: back over the tiles at - 1, at - 2, ... to the nearest state, four
+// words under way at a time.
+template <int V>
+__device__ __forceinline__ void walk_back(const Joins &j, int at, int width, int c, float (&h)[V]) {
+    constexpr int kAhead = 4;
+    float A[V], H[V];
+    bool done[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) A[k] = 1.f, H[k] = 0.f, done[k] = false;
+    unsigned long long t0 = 0;
+    bool open = true;
+    for (int p = at - 1; open && p >= 0; p -= kAhead) {
+        Words<V> m[kAhead];
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q)
+            m[q].load(j.word + (size_t)max(p - q, 0) * width + c);
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) {
+            if (!open || p - q < 0) continue;
+            while (!m[q].set()) {
+                unsigned long long now;
+                asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+                if (t0 == 0) t0 = now;
+                if (now - t0 > j.wait_ns) {
+                    ssd_report(j.err, SSD_DEVERR_TIMEOUT);
+                    open = false;
+                    break;
+                }
+                m[q].load(j.word + (size_t)(p - q) * width + c);
+            }
+            if (!open) continue;
+            open = false;
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                if (done[k]) continue;
+                const float a = __uint_as_float(m[q].w[k].x), v = __uint_as_float(m[q].w[k].y);
+                H[k] += A[k] * v;
+                done[k] = a < 0.f;
+                A[k] *= a;
+                open |= !done[k];
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < V; ++k) h[k] = H[k];
 }
 
 // Which sequence each of a warp's tokens belongs to (lane i: token t0 + i, i < n)
@@ -201,7 +228,7 @@ template <bool kJoin>
 __device__ __forceinline__ void place(const Joins &j, int blocks, int &at, int &block) {
     if constexpr (kJoin) {
         __shared__ unsigned ticket;
-        if (threadIdx.x == 0) ticket = atomicAdd(j.ticket, 1u);
+        if (threadIdx.x == 0) ticket = atomicAdd(j.ticket, 1u) + 1u;    // from all ones: 0, 1, ...
         __syncthreads();
         at = ticket / blocks;
         block = ticket % blocks;
@@ -222,8 +249,7 @@ struct Runs {
 // Joins the warps' runs and, with kJoin, the tiles': on return h is the state
 // that enters this warp's run (`place` = its number in the walk's order).
 template <int V, bool kJoin>
-__device__ __forceinline__ void join(Runs<V> &r, const Joins &j, int at, int blocks, int block,
-                                     int width, int c, int place, bool cut, const float (&A)[V],
+__device__ __forceinline__ void join(Runs<V> &r, const Joins &j, int at, int width, int c, int place, bool cut, const float (&A)[V],
                                      const float (&H)[V], float (&h)[V]) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -257,32 +283,24 @@ __device__ __forceinline__ void join(Runs<V> &r, const Joins &j, int at, int blo
                 tH[k] = cut ? H[k] : A[k] * h[k] + H[k];
                 in[k] = 0.f;
             }
-            unsigned *word = j.word + (size_t)at * blocks + block;
-            const size_t slot = (size_t)at * width + c;
-            const bool say = !(j.withhold && at == 0);
-            if (at == 0 || tcut) {
-                if (on && say) {
-#pragma unroll
-                    for (int k = 0; k < V; ++k) j.state[slot + k] = tH[k];
+            if (on) {
+                uint2 *word = j.word + (size_t)at * width + c;
+                if (at == 0 || tcut) {
+                    if (!(j.withhold && at == 0)) publish_state<V>(word, tH);
+                } else {
+                    publish_run<V>(word, tA, tH);
                 }
-                if (say) publish(word, kState);
-            } else {
-                if (on) {
+                if (at > 0) {
+                    walk_back<V>(j, at, width, c, in);
+                    if (!tcut) {
+                        float out[V];
 #pragma unroll
-                    for (int k = 0; k < V; ++k) j.run[slot + k] = make_float2(tA[k], tH[k]);
-                }
-                publish(word, kRun);
-            }
-            if (at > 0) {
-                walk_back<V>(j, at, blocks, block, width, c, in);
-                if (!tcut) {
-                    if (on) {
-#pragma unroll
-                        for (int k = 0; k < V; ++k) j.state[slot + k] = tA[k] * in[k] + tH[k];
+                        for (int k = 0; k < V; ++k) out[k] = tA[k] * in[k] + tH[k];
+                        publish_state<V>(word, out);
                     }
-                    publish(word, kState);
                 }
             }
+            __syncwarp();
 #pragma unroll
             for (int k = 0; k < V; ++k) r.in[lane * V + k] = in[k];
         }
@@ -351,7 +369,7 @@ gated_fwd_kernel(const SsdGatedFwd a, const Joins joins, int blocks) {
         }
     }
     float h[V];
-    join<V, kJoin>(runs, joins, at, blocks, block, width, c, warp, m.starts != 0, A, H, h);
+    join<V, kJoin>(runs, joins, at, width, c, warp, m.starts != 0, A, H, h);
 
     if (a.checkpoints && n > 0 && t0 % kEvery == 0) {
         float before[V];
@@ -473,7 +491,7 @@ gated_bwd_kernel(const SsdGatedBwd a, const Joins joins, int blocks, int tiles) 
     }
     if (lane == 0) fcut[warp] = m.starts != 0;
     float mu[V];
-    join<V, kJoin>(runs, joins, at, blocks, block, width, c, kWarps - 1 - warp, m.starts != 0, A, M,
+    join<V, kJoin>(runs, joins, at, width, c, kWarps - 1 - warp, m.starts != 0, A, M,
                    mu);
     for (int w = 0; w < warp; ++w) {
         const bool wcut = fcut[w];
@@ -572,30 +590,28 @@ static int tiles_of(long long tokens, int tile) {
 
 static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-// The joins' memory for the smaller (backward) tiles and for one channel a
-// lane covers both directions: a ticket and the words, the runs, the states.
+// The joins' memory, sized for the smaller (backward) tiles: a ticket, then a
+// word for every (tile, channel).
+constexpr size_t kTicketBytes = 256;
+static size_t joins_bytes(int tiles, int width) {
+    return kTicketBytes + sizeof(uint2) * (size_t)tiles * (size_t)width;
+}
 size_t ssd_gated_workspace(long long tokens, int width) {
-    const size_t tiles = tiles_of(tokens, kBwdTile);
-    if (tiles == 1) return 0;
-    const size_t blocks = (width + 31) / 32;
-    return up256(4 + 4 * tiles * blocks) + up256(8 * tiles * (size_t)width) +
-           up256(4 * tiles * (size_t)width);
+    const int tiles = tiles_of(tokens, kBwdTile);
+    return tiles == 1 ? 0 : up256(joins_bytes(tiles, width));
 }
 
-// Carves the joins out of the workspace and clears the words.
-static cudaError_t joins_of(void *workspace, int tiles, int blocks, int width, unsigned *err,
+// Carves the joins out of the workspace and sets them to all ones.
+static cudaError_t joins_of(void *workspace, int tiles, int width, unsigned *err,
                             cudaStream_t stream, Joins *j) {
     const SsdDebug dbg = ssd_debug_config();
     char *ws = static_cast<char *>(workspace);
-    const size_t words = up256(4 + 4 * (size_t)tiles * blocks);
     j->ticket = reinterpret_cast<unsigned *>(ws);
-    j->word = j->ticket + 1;
-    j->run = reinterpret_cast<float2 *>(ws + words);
-    j->state = reinterpret_cast<float *>(ws + words + up256(8 * (size_t)tiles * width));
+    j->word = reinterpret_cast<uint2 *>(ws + kTicketBytes);
     j->err = err;
     j->wait_ns = dbg.wait_ns;
     j->withhold = dbg.fault == kSsdFaultWithholdSignal;
-    return cudaMemsetAsync(ws, 0, 4 + 4 * (size_t)tiles * blocks, stream);
+    return cudaMemsetAsync(ws, 0xff, joins_bytes(tiles, width), stream);
 }
 
 template <typename T, int V, bool kGate>
@@ -606,7 +622,7 @@ static cudaError_t launch_fwd(const SsdGatedFwd &a, void *ws, unsigned *err, cud
         gated_fwd_kernel<T, V, kGate, false><<<blocks, kThreads, 0, stream>>>(a, j, blocks);
         return cudaGetLastError();
     }
-    const cudaError_t e = joins_of(ws, tiles, blocks, a.in.width, err, stream, &j);
+    const cudaError_t e = joins_of(ws, tiles, a.in.width, err, stream, &j);
     if (e != cudaSuccess) return e;
     gated_fwd_kernel<T, V, kGate, true>
         <<<(unsigned)((size_t)tiles * blocks), kThreads, 0, stream>>>(a, j, blocks);
@@ -621,7 +637,7 @@ static cudaError_t launch_bwd(const SsdGatedBwd &a, void *ws, unsigned *err, cud
         gated_bwd_kernel<T, V, kGate, false><<<blocks, kThreads, 0, stream>>>(a, j, blocks, tiles);
         return cudaGetLastError();
     }
-    const cudaError_t e = joins_of(ws, tiles, blocks, a.in.width, err, stream, &j);
+    const cudaError_t e = joins_of(ws, tiles, a.in.width, err, stream, &j);
     if (e != cudaSuccess) return e;
     gated_bwd_kernel<T, V, kGate, true>
         <<<(unsigned)((size_t)tiles * blocks), kThreads, 0, stream>>>(a, j, blocks, tiles);
