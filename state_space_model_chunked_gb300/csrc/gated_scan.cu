@@ -8,29 +8,118 @@
 //   dx_t = (1 - f_t) lam_t,      dg_t = lam_t (h_{t-1} - x_t) f_t (1 - f_t),
 //   dz_t = dy_t h_t silu'(z_t),  dinit = f_0 lam_0.
 //
-// f and 1 - f = sigmoid(-g) each keep their full relative precision; states and gradients are carried in fp32.
+// f and 1 - f = sigmoid(-g) each keep their full relative precision; states
+// and gradients are carried in fp32.
 #include "launch.h"
+#include "ptx.cuh"
 #include "vec.cuh"
 
 namespace {
 
 constexpr int kEvery = kSsdCheckpointTokens;
 
-// f = sigmoid(g) and 1 - f = sigmoid(-g).  The smaller of the two is
-// e / (1 + e) with e = e^-|g|, to a few 2^-23 of itself; the larger is 1 minus
-// it, rounded to nearest: its error has no sign, so it does not add up along a
-// memory of thousands of tokens (1 / (1 + e) from the approximate reciprocal
-// erred to one side and did).
-struct Gate {
-    float keep, drop;
-    __device__ __forceinline__ explicit Gate(float g) {
-        const float e = __expf(-fabsf(g));
-        const float small = __fdividef(e, 1.f + e), big = 1.f - small;
-        keep = g >= 0.f ? big : small;
-        drop = g >= 0.f ? small : big;
-    }
+// A lane's V channels: pairs go through the packed fp32 instructions.
+template <int V>
+struct Val {
+    float v[V];
+    __device__ __forceinline__ float &operator[](int k) { return v[k]; }
+    __device__ __forceinline__ float operator[](int k) const { return v[k]; }
 };
-__device__ __forceinline__ float sigmoidf(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+template <int V>
+__device__ __forceinline__ Val<V> all(float a) {
+    Val<V> r;
+#pragma unroll
+    for (int k = 0; k < V; ++k) r[k] = a;
+    return r;
+}
+template <int V>
+__device__ __forceinline__ Val<V> fma(const Val<V> &a, const Val<V> &b, const Val<V> &c) {
+    Val<V> r;
+    if constexpr (V == 2) {
+        const float2 d = ssdptx::ffma2(make_float2(a[0], a[1]), make_float2(b[0], b[1]),
+                                       make_float2(c[0], c[1]));
+        r[0] = d.x, r[1] = d.y;
+    } else {
+        r[0] = fmaf(a[0], b[0], c[0]);
+    }
+    return r;
+}
+template <int V>
+__device__ __forceinline__ Val<V> operator*(const Val<V> &a, const Val<V> &b) {
+    Val<V> r;
+    if constexpr (V == 2) {
+        const float2 d = ssdptx::fmul2(make_float2(a[0], a[1]), make_float2(b[0], b[1]));
+        r[0] = d.x, r[1] = d.y;
+    } else {
+        r[0] = a[0] * b[0];
+    }
+    return r;
+}
+template <int V>
+__device__ __forceinline__ Val<V> operator+(const Val<V> &a, const Val<V> &b) {
+    Val<V> r;
+    if constexpr (V == 2) {
+        const float2 d = ssdptx::fadd2(make_float2(a[0], a[1]), make_float2(b[0], b[1]));
+        r[0] = d.x, r[1] = d.y;
+    } else {
+        r[0] = a[0] + b[0];
+    }
+    return r;
+}
+template <int V>
+__device__ __forceinline__ Val<V> operator-(const Val<V> &a, const Val<V> &b) {
+    return fma(b, all<V>(-1.f), a);
+}
+template <typename T, int V>
+__device__ __forceinline__ Val<V> value(const SsdRaw<T, V> &raw) {
+    Val<V> r;
+#pragma unroll
+    for (int k = 0; k < V; ++k) r[k] = raw.get(k);
+    return r;
+}
+
+// e = exp(-|v|) and 1 / (1 + e): a pair shares one reciprocal (the product of
+// both denominators is in [1, 4]), which relieves the special-function unit,
+// the recurrence's narrowest pipe.
+template <int V>
+__device__ __forceinline__ void exp_inv(const Val<V> &v, Val<V> &e, Val<V> &inv) {
+    Val<V> d;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        e[k] = ssdptx::ex2_approx(fabsf(v[k]) * -1.44269504f);
+        d[k] = 1.f + e[k];
+    }
+    if constexpr (V == 2) {
+        const float r = ssdptx::rcp_approx(d[0] * d[1]);
+        inv[0] = r * d[1], inv[1] = r * d[0];
+    } else {
+        inv[0] = ssdptx::rcp_approx(d[0]);
+    }
+}
+// f = sigmoid(g) and 1 - f = sigmoid(-g).  The smaller of the two is
+// e / (1 + e), to a few 2^-23 of itself; the larger is 1 minus it, rounded to
+// nearest: its error has no sign, so it does not add up along a memory of
+// thousands of tokens (1 / (1 + e) from the approximate reciprocal erred to one
+// side and did).
+template <int V>
+__device__ __forceinline__ void gate(const Val<V> &g, Val<V> &keep, Val<V> &drop) {
+    Val<V> e, inv;
+    exp_inv(g, e, inv);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        const float small = e[k] * inv[k], big = 1.f - small;
+        keep[k] = g[k] >= 0.f ? big : small;
+        drop[k] = g[k] >= 0.f ? small : big;
+    }
+}
+template <int V>
+__device__ __forceinline__ Val<V> sigmoid(const Val<V> &z) {
+    Val<V> e, s;
+    exp_inv(z, e, s);
+#pragma unroll
+    for (int k = 0; k < V; ++k) s[k] *= z[k] >= 0.f ? 1.f : e[k];
+    return s;
+}
 
 // ------------------------------------------------------------- tiles and joins
 // The token axis is cut into tiles, one CTA a tile and block of 32 V channels:
@@ -103,7 +192,7 @@ struct Words {
 };
 
 template <int V>
-__device__ __forceinline__ void publish_run(uint2 *p, const float (&A)[V], const float (&H)[V]) {
+__device__ __forceinline__ void publish_run(uint2 *p, const Val<V> &A, const Val<V> &H) {
     Words<V> m;
 #pragma unroll
     for (int k = 0; k < V; ++k)
@@ -112,7 +201,7 @@ __device__ __forceinline__ void publish_run(uint2 *p, const float (&A)[V], const
     m.store(p);
 }
 template <int V>
-__device__ __forceinline__ void publish_state(uint2 *p, const float (&h)[V]) {
+__device__ __forceinline__ void publish_state(uint2 *p, const Val<V> &h) {
     Words<V> m;
 #pragma unroll
     for (int k = 0; k < V; ++k) m.w[k] = make_uint2(__float_as_uint(-1.f), __float_as_uint(h[k]));
@@ -123,7 +212,7 @@ __device__ __forceinline__ void publish_state(uint2 *p, const float (&h)[V]) {
 // channels: back over the tiles at - 1, at - 2, ... to the nearest state, four
 // words under way at a time.
 template <int V>
-__device__ __forceinline__ void walk_back(const Joins &j, int at, int width, int c, float (&h)[V]) {
+__device__ __forceinline__ void walk_back(const Joins &j, int at, int width, int c, Val<V> &h) {
     constexpr int kAhead = 4;
     float A[V], H[V];
     bool done[V];
@@ -246,11 +335,15 @@ struct Runs {
     bool cut[kWarps];
 };
 
-// Joins the warps' runs and, with kJoin, the tiles': on return h is the state
-// that enters this warp's run (`place` = its number in the walk's order).
+// Joins the runs: `place` is the warp's number in the walk's order, h becomes
+// the state that enters its run if nothing entered the tile, pA what the
+// entering state is multiplied by on the way.  With kJoin the last warp then
+// walks back over the tiles, so join_end (after whatever needs no entering
+// state) waits for it and adds it in.
 template <int V, bool kJoin>
-__device__ __forceinline__ void join(Runs<V> &r, const Joins &j, int at, int width, int c, int place, bool cut, const float (&A)[V],
-                                     const float (&H)[V], float (&h)[V]) {
+__device__ __forceinline__ void join_begin(Runs<V> &r, const Joins &j, int at, int width, int c,
+                                           int place, bool cut, const Val<V> &A, const Val<V> &H,
+                                           Val<V> &h, Val<V> &pA, bool &pcut) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
@@ -259,31 +352,24 @@ __device__ __forceinline__ void join(Runs<V> &r, const Joins &j, int at, int wid
     }
     if (lane == 0) r.cut[place] = cut;
     __syncthreads();
-    float pA[V];            // the runs in front of this one
-    bool pcut = false;
-#pragma unroll
-    for (int k = 0; k < V; ++k) h[k] = 0.f, pA[k] = 1.f;
+    pcut = false;
+    h = all<V>(0.f);
+    pA = all<V>(1.f);
     for (int w = 0; w < place; ++w) {
         const bool wcut = r.cut[w];
         pcut |= wcut;
+        Val<V> wa, wh;
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const float wa = r.A[w][lane * V + k], wh = r.H[w][lane * V + k];
-            h[k] = wcut ? wh : wa * h[k] + wh;
-            pA[k] *= wa;
-        }
+        for (int k = 0; k < V; ++k) wa[k] = r.A[w][lane * V + k], wh[k] = r.H[w][lane * V + k];
+        h = wcut ? wh : fma(wa, h, wh);
+        pA = pA * wa;
     }
     if constexpr (kJoin) {
         if (place == kWarps - 1) {
-            const bool tcut = pcut || cut, on = c < width;
-            float in[V], tA[V], tH[V];
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                tA[k] = A[k] * pA[k];
-                tH[k] = cut ? H[k] : A[k] * h[k] + H[k];
-                in[k] = 0.f;
-            }
-            if (on) {
+            const bool tcut = pcut || cut;
+            Val<V> in = all<V>(0.f);
+            const Val<V> tA = A * pA, tH = cut ? H : fma(A, h, H);
+            if (c < width) {
                 uint2 *word = j.word + (size_t)at * width + c;
                 if (at == 0 || tcut) {
                     if (!(j.withhold && at == 0)) publish_state<V>(word, tH);
@@ -292,35 +378,58 @@ __device__ __forceinline__ void join(Runs<V> &r, const Joins &j, int at, int wid
                 }
                 if (at > 0) {
                     walk_back<V>(j, at, width, c, in);
-                    if (!tcut) {
-                        float out[V];
-#pragma unroll
-                        for (int k = 0; k < V; ++k) out[k] = tA[k] * in[k] + tH[k];
-                        publish_state<V>(word, out);
-                    }
+                    if (!tcut) publish_state<V>(word, fma(tA, in, tH));
                 }
             }
             __syncwarp();
 #pragma unroll
             for (int k = 0; k < V; ++k) r.in[lane * V + k] = in[k];
         }
+    }
+}
+template <int V, bool kJoin>
+__device__ __forceinline__ void join_end(const Runs<V> &r, const Val<V> &pA, bool pcut, Val<V> &h) {
+    if constexpr (kJoin) {
         __syncthreads();
         if (!pcut) {
+            Val<V> in;
 #pragma unroll
-            for (int k = 0; k < V; ++k) h[k] += pA[k] * r.in[lane * V + k];
+            for (int k = 0; k < V; ++k) in[k] = r.in[(threadIdx.x & 31) * V + k];
+            h = fma(pA, in, h);
         }
     }
 }
 
+// kTok tokens of one array.  whole: all of them, in all of the warp's lanes.
 template <typename T, int V, int kTok>
 __device__ __forceinline__ void load_run(SsdRaw<T, V> (&raw)[kTok], const void *base,
-                                         long long stride, long long t0, int n, int c, bool on) {
+                                         long long stride, long long t0, int n, int c, bool on,
+                                         bool whole) {
     const T *p = static_cast<const T *>(base) + t0 * stride + c;
+    if (whole) {
 #pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-        if (on && i < n) raw[i].load_cs(p + i * stride);
-        else raw[i].zero();
+        for (int i = 0; i < kTok; ++i, p += stride) raw[i].load_cs(p);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kTok; ++i, p += stride) {
+            raw[i].zero();
+            if (on && i < n) raw[i].load_cs(p);
+        }
     }
+}
+
+// Runs `body` as its plain form where a warp's tokens hold no sequence boundary
+// and no end of the arrays, which leaves the tests for them out.
+struct Plain {
+    static constexpr bool kOn = true;
+};
+struct General {
+    static constexpr bool kOn = false;
+};
+template <typename F>
+__device__ __forceinline__ void by_form(bool plain, F &&body) {
+    if (plain) body(Plain{});
+    else body(General{});
 }
 
 template <typename T, int V, bool kGate, bool kJoin>
@@ -334,81 +443,76 @@ gated_fwd_kernel(const SsdGatedFwd a, const Joins joins, int blocks) {
     const bool on = c < width;
     const long long t0 = (long long)at * kFwdTile + warp * kFwdTok;
     const int n = (int)max(0ll, min((long long)kFwdTok, a.in.tokens - t0));
+    const bool whole = n == kFwdTok && __all_sync(0xffffffffu, on);
 
     SsdRaw<T, V> graw[kFwdTok], xraw[kFwdTok], zraw[kGate ? kFwdTok : 1];
-    load_run<T, V>(graw, a.in.g, a.in.g_stride, t0, n, c, on);
-    load_run<T, V>(xraw, a.in.x, a.in.x_stride, t0, n, c, on);
-    if constexpr (kGate) load_run<T, V>(zraw, a.in.z, a.in.z_stride, t0, n, c, on);
+    load_run<T, V>(graw, a.in.g, a.in.g_stride, t0, n, c, on, whole);
+    load_run<T, V>(xraw, a.in.x, a.in.x_stride, t0, n, c, on, whole);
+    if constexpr (kGate) load_run<T, V>(zraw, a.in.z, a.in.z_stride, t0, n, c, on, whole);
     const Marks m = marks(a.in, t0, kFwdTok);
+    const bool plain = whole && (m.starts | m.ends) == 0;
     if (at == 0) pass_empty<V>(a.in, a.in.init, a.final_state, c);
 
-    float keep[kFwdTok][V], u[kFwdTok][V], A[V], H[V];
+    Val<V> keep[kFwdTok], u[kFwdTok], A = all<V>(1.f), H = all<V>(0.f);
+    by_form(plain, [&](auto form) {
+        constexpr bool kPlain = decltype(form)::kOn;
 #pragma unroll
-    for (int k = 0; k < V; ++k) A[k] = 1.f, H[k] = 0.f;
-#pragma unroll
-    for (int i = 0; i < kFwdTok; ++i) {
-        const bool start = (m.starts >> i) & 1u;
-        float first[V];
-        if (start) {
-            const int seq = __shfl_sync(0xffffffffu, m.seq, i);
-            load_f32<V>(a.in.init + (size_t)seq * width + c, on && a.in.init != nullptr, first);
-        }
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const Gate f(graw[i].get(k));
-            keep[i][k] = f.keep;
-            u[i][k] = f.drop * xraw[i].get(k);
-            if (start) {
-                u[i][k] += f.keep * first[k];
-                A[k] = 0.f;
-                H[k] = u[i][k];
-            } else if (i < n) {
-                A[k] *= f.keep;
-                H[k] = f.keep * H[k] + u[i][k];
+        for (int i = 0; i < kFwdTok; ++i) {
+            Val<V> drop;
+            gate(value(graw[i]), keep[i], drop);
+            u[i] = drop * value(xraw[i]);
+            if (!kPlain && ((m.starts >> i) & 1u)) {
+                const int seq = __shfl_sync(0xffffffffu, m.seq, i);
+                Val<V> first;
+                load_f32<V>(a.in.init + (size_t)seq * width + c, on && a.in.init != nullptr,
+                            first.v);
+                u[i] = fma(keep[i], first, u[i]);
+                A = all<V>(0.f);
+                H = u[i];
+            } else if (kPlain || i < n) {
+                A = A * keep[i];
+                H = fma(keep[i], H, u[i]);
             }
         }
-    }
-    float h[V];
-    join<V, kJoin>(runs, joins, at, width, c, warp, m.starts != 0, A, H, h);
+    });
+    Val<V> h, pA;
+    bool pcut;
+    join_begin<V, kJoin>(runs, joins, at, width, c, warp, m.starts != 0, A, H, h, pA, pcut);
+    join_end<V, kJoin>(runs, pA, pcut, h);
 
     if (a.checkpoints && n > 0 && t0 % kEvery == 0) {
-        float before[V];
+        Val<V> before = h;
         const int seq = __shfl_sync(0xffffffffu, m.seq, 0);
-        if (m.starts & 1u) {
-            load_f32<V>(a.in.init + (size_t)seq * width + c, on && a.in.init != nullptr, before);
-        } else {
-#pragma unroll
-            for (int k = 0; k < V; ++k) before[k] = h[k];
-        }
-        if (on) ssd_store_vec<V>(a.checkpoints + (size_t)(t0 / kEvery) * width + c, before);
+        if (m.starts & 1u)
+            load_f32<V>(a.in.init + (size_t)seq * width + c, on && a.in.init != nullptr, before.v);
+        if (on) ssd_store_vec<V>(a.checkpoints + (size_t)(t0 / kEvery) * width + c, before.v);
     }
-    T *y = static_cast<T *>(a.y) + t0 * a.y_stride + c;
+    by_form(plain, [&](auto form) {
+        constexpr bool kPlain = decltype(form)::kOn;
+        T *y = static_cast<T *>(a.y) + t0 * a.y_stride + c;
 #pragma unroll
-    for (int i = 0; i < kFwdTok; ++i) {
-        if (i < n) {
-            const bool start = (m.starts >> i) & 1u;
-            float o[V];
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                h[k] = start ? u[i][k] : keep[i][k] * h[k] + u[i][k];
-                o[k] = h[k];
-                if constexpr (kGate) {
-                    const float z = zraw[i].get(k);
-                    o[k] *= z * sigmoidf(z);
-                }
+        for (int i = 0; i < kFwdTok; ++i, y += a.y_stride) {
+            if (!kPlain && i >= n) continue;
+            h = !kPlain && ((m.starts >> i) & 1u) ? u[i] : fma(keep[i], h, u[i]);
+            Val<V> o = h;
+            if constexpr (kGate) {
+                const Val<V> z = value(zraw[i]);
+                o = h * (z * sigmoid(z));
             }
-            if (on) ssd_store_vec<V>(y + i * a.y_stride, o);
-            if (((m.ends >> i) & 1u) && a.final_state) {
+            if (kPlain || on) ssd_store_vec<V>(y, o.v);
+            if (!kPlain && ((m.ends >> i) & 1u) && a.final_state) {
                 const int seq = __shfl_sync(0xffffffffu, m.seq, i);
-                if (on) ssd_store_vec<V>(a.final_state + (size_t)seq * width + c, h);
+                if (on) ssd_store_vec<V>(a.final_state + (size_t)seq * width + c, h.v);
             }
         }
-    }
+    });
 }
 
 // Backward: the same joins from the last tile to the first, on the gradient
 // that a token hands to the one before it, mu_t = f_t lam_t: mu -> A mu + M
-// over a run.  h is recomputed inside the tile from its kept state.
+// over a run.  h is recomputed inside the tile from its kept state while the
+// walk is under way; with s = sigmoid(z), dh = dy z s:
+// dz = dy h s (1 + z (1 - s)) = h (s (dy - dh) + dh).
 template <typename T, int V, bool kGate, bool kJoin>
 __global__ void __launch_bounds__(kThreads, 2)
 gated_bwd_kernel(const SsdGatedBwd a, const Joins joins, int blocks, int tiles) {
@@ -423,133 +527,124 @@ gated_bwd_kernel(const SsdGatedBwd a, const Joins joins, int blocks, int tiles) 
     const int tile = tiles - 1 - at;
     const long long t0 = (long long)tile * kBwdTile + warp * kBwdTok;
     const int n = (int)max(0ll, min((long long)kBwdTok, a.in.tokens - t0));
+    const bool whole = n == kBwdTok && __all_sync(0xffffffffu, on);
 
     SsdRaw<T, V> graw[kBwdTok], xraw[kBwdTok], yraw[kBwdTok], zraw[kGate ? kBwdTok : 1];
-    load_run<T, V>(graw, a.in.g, a.in.g_stride, t0, n, c, on);
-    load_run<T, V>(yraw, a.dy, a.dy_stride, t0, n, c, on);
-    if constexpr (kGate) load_run<T, V>(zraw, a.in.z, a.in.z_stride, t0, n, c, on);
-    load_run<T, V>(xraw, a.in.x, a.in.x_stride, t0, n, c, on);
-    float h[V];         // the state that enters the tile
-    load_f32<V>(a.checkpoints + (size_t)tile * width + c, on && a.in.tokens > 0, h);
+    load_run<T, V>(graw, a.in.g, a.in.g_stride, t0, n, c, on, whole);
+    load_run<T, V>(yraw, a.dy, a.dy_stride, t0, n, c, on, whole);
+    if constexpr (kGate) load_run<T, V>(zraw, a.in.z, a.in.z_stride, t0, n, c, on, whole);
+    load_run<T, V>(xraw, a.in.x, a.in.x_stride, t0, n, c, on, whole);
+    Val<V> h;           // the state that enters the tile
+    load_f32<V>(a.checkpoints + (size_t)tile * width + c, on && a.in.tokens > 0, h.v);
     const Marks m = marks(a.in, t0, kBwdTok);
+    const bool plain = whole && (m.starts | m.ends) == 0;
     if (at == 0) pass_empty<V>(a.in, a.dfinal, a.dinit, c);
 
     // the run forward (A, H) and backward (A, M)
-    float keep[kBwdTok][V], drop[kBwdTok][V], dh[kBwdTok][V], A[V], H[V], M[V];
+    Val<V> keep[kBwdTok], drop[kBwdTok], dh[kBwdTok], sig[kGate ? kBwdTok : 1];
+    Val<V> A = all<V>(1.f), H = all<V>(0.f), M = all<V>(0.f);
+    by_form(plain, [&](auto form) {
+        constexpr bool kPlain = decltype(form)::kOn;
 #pragma unroll
-    for (int k = 0; k < V; ++k) A[k] = 1.f, H[k] = 0.f, M[k] = 0.f;
-#pragma unroll
-    for (int i = 0; i < kBwdTok; ++i) {
-        const bool start = (m.starts >> i) & 1u;
-        float first[V];
-        if (start) {
-            const int seq = __shfl_sync(0xffffffffu, m.seq, i);
-            load_f32<V>(a.in.init + (size_t)seq * width + c, on && a.in.init != nullptr, first);
-        }
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const Gate f(graw[i].get(k));
-            keep[i][k] = f.keep;
-            drop[i][k] = f.drop;
-            const float u = f.drop * xraw[i].get(k);
-            if (start) {
-                A[k] = 0.f;
-                H[k] = f.keep * first[k] + u;
-            } else if (i < n) {
-                A[k] *= f.keep;
-                H[k] = f.keep * H[k] + u;
+        for (int i = 0; i < kBwdTok; ++i) {
+            gate(value(graw[i]), keep[i], drop[i]);
+            const Val<V> u = drop[i] * value(xraw[i]);
+            if (!kPlain && ((m.starts >> i) & 1u)) {
+                const int seq = __shfl_sync(0xffffffffu, m.seq, i);
+                Val<V> first;
+                load_f32<V>(a.in.init + (size_t)seq * width + c, on && a.in.init != nullptr,
+                            first.v);
+                A = all<V>(0.f);
+                H = fma(keep[i], first, u);
+            } else if (kPlain || i < n) {
+                A = A * keep[i];
+                H = fma(keep[i], H, u);
             }
         }
-    }
 #pragma unroll
-    for (int i = kBwdTok - 1; i >= 0; --i) {
-        float last[V];
-        const bool end = (m.ends >> i) & 1u;
-        if (end) {
-            const int seq = __shfl_sync(0xffffffffu, m.seq, i);
-            load_f32<V>(a.dfinal + (size_t)seq * width + c, on && a.dfinal != nullptr, last);
-        }
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-            dh[i][k] = yraw[i].get(k);
+        for (int i = kBwdTok - 1; i >= 0; --i) {
+            dh[i] = value(yraw[i]);
             if constexpr (kGate) {
-                const float z = zraw[i].get(k);
-                dh[i][k] *= z * sigmoidf(z);
+                const Val<V> z = value(zraw[i]);
+                sig[i] = sigmoid(z);
+                dh[i] = dh[i] * (z * sig[i]);
             }
-            if (end) dh[i][k] += last[k];
-            if (i < n) {
-                const bool start = (m.starts >> i) & 1u;
-                const float lam = end ? dh[i][k] : dh[i][k] + M[k];
-                M[k] = start ? 0.f : keep[i][k] * lam;
+            if (!kPlain && i >= n) continue;
+            Val<V> lam = dh[i] + M;
+            if (!kPlain && ((m.ends >> i) & 1u)) {
+                const int seq = __shfl_sync(0xffffffffu, m.seq, i);
+                load_f32<V>(a.dfinal + (size_t)seq * width + c, on && a.dfinal != nullptr, lam.v);
+                lam = dh[i] + lam;
             }
+            M = !kPlain && ((m.starts >> i) & 1u) ? all<V>(0.f) : keep[i] * lam;
         }
-    }
+    });
 #pragma unroll
     for (int k = 0; k < V; ++k) {
         fA[warp][lane * V + k] = A[k];
         fH[warp][lane * V + k] = H[k];
     }
     if (lane == 0) fcut[warp] = m.starts != 0;
-    float mu[V];
-    join<V, kJoin>(runs, joins, at, width, c, kWarps - 1 - warp, m.starts != 0, A, M,
-                   mu);
-    for (int w = 0; w < warp; ++w) {
-        const bool wcut = fcut[w];
-#pragma unroll
-        for (int k = 0; k < V; ++k)
-            h[k] = wcut ? fH[w][lane * V + k] : fA[w][lane * V + k] * h[k] + fH[w][lane * V + k];
-    }
+    Val<V> mu, pA;
+    bool pcut;
+    join_begin<V, kJoin>(runs, joins, at, width, c, kWarps - 1 - warp, m.starts != 0, A, M, mu, pA,
+                         pcut);
 
     // forward: the state before each token, and dz
-    float before[kBwdTok][V];
-    T *dz = kGate ? static_cast<T *>(a.dz) + t0 * a.dz_stride + c : nullptr;
+    for (int w = 0; w < warp; ++w) {
+        Val<V> wa, wh;
 #pragma unroll
-    for (int i = 0; i < kBwdTok; ++i) {
-        if (i < n) {
-            if ((m.starts >> i) & 1u) {
+        for (int k = 0; k < V; ++k) wa[k] = fA[w][lane * V + k], wh[k] = fH[w][lane * V + k];
+        h = fcut[w] ? wh : fma(wa, h, wh);
+    }
+    Val<V> before[kBwdTok];
+    by_form(plain, [&](auto form) {
+        constexpr bool kPlain = decltype(form)::kOn;
+        [[maybe_unused]] T *dz = kGate ? static_cast<T *>(a.dz) + t0 * a.dz_stride + c : nullptr;
+#pragma unroll
+        for (int i = 0; i < kBwdTok; ++i) {
+            if (!kPlain && i >= n) continue;
+            if (!kPlain && ((m.starts >> i) & 1u)) {
                 const int seq = __shfl_sync(0xffffffffu, m.seq, i);
-                load_f32<V>(a.in.init + (size_t)seq * width + c, on && a.in.init != nullptr, h);
+                load_f32<V>(a.in.init + (size_t)seq * width + c, on && a.in.init != nullptr, h.v);
             }
-            float o[V];
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                before[i][k] = h[k];
-                h[k] = keep[i][k] * h[k] + drop[i][k] * xraw[i].get(k);
-                if constexpr (kGate) {
-                    const float z = zraw[i].get(k), sig = sigmoidf(z);
-                    o[k] = yraw[i].get(k) * h[k] * sig * (1.f + z * (1.f - sig));
-                }
-            }
+            before[i] = h;
+            h = fma(keep[i], h, drop[i] * value(xraw[i]));
             if constexpr (kGate) {
-                if (on) ssd_store_vec<V>(dz + i * a.dz_stride, o);
+                const Val<V> o = h * fma(sig[i], value(yraw[i]) - dh[i], dh[i]);
+                if (kPlain || on) ssd_store_vec<V>(dz, o.v);
+                dz += a.dz_stride;
             }
         }
-    }
+    });
+    join_end<V, kJoin>(runs, pA, pcut, mu);
     // backward
-    T *dx = static_cast<T *>(a.dx) + t0 * a.dx_stride + c;
-    T *dg = static_cast<T *>(a.dg) + t0 * a.dg_stride + c;
+    by_form(plain, [&](auto form) {
+        constexpr bool kPlain = decltype(form)::kOn;
+        T *dx = static_cast<T *>(a.dx) + (t0 + kBwdTok - 1) * a.dx_stride + c;
+        T *dg = static_cast<T *>(a.dg) + (t0 + kBwdTok - 1) * a.dg_stride + c;
 #pragma unroll
-    for (int i = kBwdTok - 1; i >= 0; --i) {
-        if (i < n) {
-            const bool end = (m.ends >> i) & 1u;
-            float ox[V], og[V];
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const float lam = end ? dh[i][k] : dh[i][k] + mu[k];
-                ox[k] = drop[i][k] * lam;
-                og[k] = lam * (before[i][k] - xraw[i].get(k)) * keep[i][k] * drop[i][k];
-                mu[k] = keep[i][k] * lam;
-            }
-            if (on) {
-                ssd_store_vec<V>(dx + i * a.dx_stride, ox);
-                ssd_store_vec<V>(dg + i * a.dg_stride, og);
-            }
-            if (((m.starts >> i) & 1u) && a.dinit) {
+        for (int i = kBwdTok - 1; i >= 0; --i, dx -= a.dx_stride, dg -= a.dg_stride) {
+            if (!kPlain && i >= n) continue;
+            Val<V> lam = dh[i] + mu;
+            if (!kPlain && ((m.ends >> i) & 1u)) {
                 const int seq = __shfl_sync(0xffffffffu, m.seq, i);
-                if (on) ssd_store_vec<V>(a.dinit + (size_t)seq * width + c, mu);
+                load_f32<V>(a.dfinal + (size_t)seq * width + c, on && a.dfinal != nullptr, lam.v);
+                lam = dh[i] + lam;
+            }
+            const Val<V> ox = drop[i] * lam;
+            mu = keep[i] * lam;
+            const Val<V> og = (mu * drop[i]) * (before[i] - value(xraw[i]));
+            if (kPlain || on) {
+                ssd_store_vec<V>(dx, ox.v);
+                ssd_store_vec<V>(dg, og.v);
+            }
+            if (!kPlain && ((m.starts >> i) & 1u) && a.dinit) {
+                const int seq = __shfl_sync(0xffffffffu, m.seq, i);
+                if (on) ssd_store_vec<V>(a.dinit + (size_t)seq * width + c, mu.v);
             }
         }
-    }
+    });
 }
 
 // One token of every (row, channel): the state is read and written in place.
@@ -558,14 +653,16 @@ __global__ void __launch_bounds__(256) gated_step_kernel(const SsdGatedStep a) {
     const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= (size_t)a.rows * a.width) return;
     const size_t r = i / a.width, c = i % a.width;
-    const Gate f(ssd_ld(static_cast<const T *>(a.g) + r * a.g_stride + c));
+    const Val<1> g{{ssd_ld(static_cast<const T *>(a.g) + r * a.g_stride + c)}};
     const float x = ssd_ld(static_cast<const T *>(a.x) + r * a.x_stride + c);
-    const float h = f.keep * a.state[i] + f.drop * x;
+    Val<1> keep, drop;
+    gate(g, keep, drop);
+    const float h = keep[0] * a.state[i] + drop[0] * x;
     a.state[i] = h;
     float y = h;
     if (a.z) {
-        const float z = ssd_ld(static_cast<const T *>(a.z) + r * a.z_stride + c);
-        y = h * z * sigmoidf(z);
+        const Val<1> z{{ssd_ld(static_cast<const T *>(a.z) + r * a.z_stride + c)}};
+        y = h * (z[0] * sigmoid(z)[0]);
     }
     ssd_st(static_cast<T *>(a.y) + i, y);
 }
