@@ -294,7 +294,7 @@ ssd_status ssd_gated_scan_fwd(const void *x, const void *g, const void *z, ssd_d
     a.y_stride = y_stride;
     a.final_state = final_state;
     a.checkpoints = checkpoints;
-    return launched(ssd_launch_gated_fwd(a, workspace, ssd_device_error_word(), stream));
+    return launched(ssd_launch_gated_fwd(a, ssd_sm_count(), workspace, ssd_device_error_word(), stream));
 }
 
 ssd_status ssd_gated_scan_bwd(const void *dy, const void *x, const void *g, const void *z,
@@ -330,7 +330,7 @@ ssd_status ssd_gated_scan_bwd(const void *dy, const void *x, const void *g, cons
     a.dg = dg;
     a.dz = dz;
     a.dinit = dinit;
-    return launched(ssd_launch_gated_bwd(a, workspace, ssd_device_error_word(), stream));
+    return launched(ssd_launch_gated_bwd(a, ssd_sm_count(), workspace, ssd_device_error_word(), stream));
 }
 
 ssd_status ssd_gated_state_update(float *state, const void *x, const void *g, const void *z,

@@ -78,52 +78,37 @@ __device__ __forceinline__ Val<V> value(const SsdRaw<T, V> &raw) {
     return r;
 }
 
-// e = exp(-|v|) and 1 / (1 + e): a pair shares one reciprocal (the product of
-// both denominators is in [1, 4]), which relieves the special-function unit,
-// the recurrence's narrowest pipe.
-template <int V>
-__device__ __forceinline__ void exp_inv(const Val<V> &v, Val<V> &e, Val<V> &inv) {
-    Val<V> d;
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-        e[k] = ssdptx::ex2_approx(fabsf(v[k]) * -1.44269504f);
-        d[k] = 1.f + e[k];
-    }
-    if constexpr (V == 2) {
-        const float r = ssdptx::rcp_approx(d[0] * d[1]);
-        inv[0] = r * d[1], inv[1] = r * d[0];
-    } else {
-        inv[0] = ssdptx::rcp_approx(d[0]);
-    }
-}
-// f = sigmoid(g) and 1 - f = sigmoid(-g).  The smaller of the two is
-// e / (1 + e), to a few 2^-23 of itself; the larger is 1 minus it, rounded to
-// nearest: its error has no sign, so it does not add up along a memory of
-// thousands of tokens (1 / (1 + e) from the approximate reciprocal erred to one
-// side and did).
+constexpr float kLog2e = 1.44269504f;
+
+// f = sigmoid(g) and 1 - f = sigmoid(-g).  With e = e^-|g| the smaller of the
+// two is e / (1 + e), to a few 2^-23 of itself; the larger is 1 minus it,
+// rounded to nearest: its error has no sign, so it does not add up along a
+// memory of thousands of tokens (1 / (1 + e) from the approximate reciprocal
+// erred to one side and did).  Sharing one reciprocal between a lane's pair of
+// channels takes more instructions than it saves (603 against 574 us forward,
+// 65536 x 5120): the special-function unit is not what bounds this.
 template <int V>
 __device__ __forceinline__ void gate(const Val<V> &g, Val<V> &keep, Val<V> &drop) {
-    Val<V> e, inv;
-    exp_inv(g, e, inv);
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-        const float small = e[k] * inv[k], big = 1.f - small;
+        const float e = ssdptx::ex2_approx(fabsf(g[k]) * -kLog2e);
+        const float small = e * ssdptx::rcp_approx(1.f + e), big = 1.f - small;
         keep[k] = g[k] >= 0.f ? big : small;
         drop[k] = g[k] >= 0.f ? small : big;
     }
 }
 template <int V>
 __device__ __forceinline__ Val<V> sigmoid(const Val<V> &z) {
-    Val<V> e, s;
-    exp_inv(z, e, s);
+    Val<V> s;
 #pragma unroll
-    for (int k = 0; k < V; ++k) s[k] *= z[k] >= 0.f ? 1.f : e[k];
+    for (int k = 0; k < V; ++k)
+        s[k] = ssdptx::rcp_approx(1.f + ssdptx::ex2_approx(z[k] * -kLog2e));
     return s;
 }
 
 // ------------------------------------------------------------- tiles and joins
 // The token axis is cut into tiles, one CTA a tile and block of 32 V channels:
-// each of 8 warps holds kTok consecutive tokens of it in registers, a lane V
+// each of its warps holds kTok consecutive tokens of it in registers, a lane V
 // channels.  A run of tokens acts on the state that enters it as h -> A h + H,
 // so the warps' (A, H) are joined through shared memory and the tiles' through
 // global memory in one pass over the data:
@@ -139,9 +124,9 @@ __device__ __forceinline__ Val<V> sigmoid(const Val<V> &z) {
 // on what enters, and nothing is multiplied across the cut (0 times a NaN of
 // the sequence before would reach the next one).  A cut tile publishes its
 // leaving state at once.
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kFwdTok = 16, kBwdTok = 8;
-constexpr int kFwdTile = kWarps * kFwdTok, kBwdTile = kWarps * kBwdTok;
+constexpr int kFwdWarps = 4, kFwdTok = 16, kFwdCtas = 4;
+constexpr int kBwdWarps = 8, kBwdTok = 8, kBwdCtas = 2;
+constexpr int kFwdTile = kFwdWarps * kFwdTok, kBwdTile = kBwdWarps * kBwdTok;
 static_assert(kBwdTile == kEvery, "a backward tile starts from a kept state");
 static_assert(kEvery % kFwdTok == 0, "kept states are those that enter a warp's run");
 
@@ -297,7 +282,7 @@ __device__ __forceinline__ Marks marks(const SsdGated &a, long long t0, int n) {
 template <int V>
 __device__ __forceinline__ void pass_empty(const SsdGated &a, const float *in, float *out, int c) {
     if (!out || c >= a.width) return;
-    for (int s = threadIdx.x >> 5; s < a.nseq; s += kWarps) {
+    for (int s = threadIdx.x >> 5; s < a.nseq; s += blockDim.x >> 5) {
         const bool empty = a.cu ? __ldg(a.cu + s) == __ldg(a.cu + s + 1) : a.length == 0;
         if (!empty) continue;
 #pragma unroll
@@ -319,8 +304,9 @@ __device__ __forceinline__ void place(const Joins &j, int blocks, int &at, int &
         __shared__ unsigned ticket;
         if (threadIdx.x == 0) ticket = atomicAdd(j.ticket, 1u) + 1u;    // from all ones: 0, 1, ...
         __syncthreads();
-        at = ticket / blocks;
-        block = ticket % blocks;
+        const unsigned t = __shfl_sync(0xffffffffu, ticket, 0);     // one value in the warp
+        at = t / blocks;
+        block = t % blocks;
     } else {
         at = 0;
         block = blockIdx.x;
@@ -329,21 +315,28 @@ __device__ __forceinline__ void place(const Joins &j, int blocks, int &at, int &
 
 // The (A, H) of the CTA's warps in the order of the walk, and what enters the
 // tile, in shared memory.
-template <int V>
+template <int V, int kWarps>
 struct Runs {
     float A[kWarps][32 * V], H[kWarps][32 * V], in[32 * V];
     bool cut[kWarps];
 };
 
-// Joins the runs: `place` is the warp's number in the walk's order, h becomes
-// the state that enters its run if nothing entered the tile, pA what the
-// entering state is multiplied by on the way.  With kJoin the last warp then
-// walks back over the tiles, so join_end (after whatever needs no entering
-// state) waits for it and adds it in.
-template <int V, bool kJoin>
-__device__ __forceinline__ void join_begin(Runs<V> &r, const Joins &j, int at, int width, int c,
-                                           int place, bool cut, const Val<V> &A, const Val<V> &H,
-                                           Val<V> &h, Val<V> &pA, bool &pcut) {
+// Joins the runs in three steps.  join_begin: the warps' runs through shared
+// memory; with kJoin the last warp of the walk publishes the tile's.  Then every
+// warp does what needs no entering state.  join_walk: the last warp walks back
+// over the tiles.  join_end: what it found enters every warp's run.
+template <int V>
+struct Entering {
+    Val<V> h;               // the state that enters the warp's run if nothing entered the tile
+    Val<V> A;               // what the tile's entering state is multiplied by on the way
+    bool cut;               // a boundary lies in between
+    Val<V> tA, tH;          // the last warp: the tile's run
+    bool tcut;
+};
+template <int V, int kWarps, bool kJoin>
+__device__ __forceinline__ Entering<V> join_begin(Runs<V, kWarps> &r, const Joins &j, int at,
+                                                  int width, int c, int place, bool cut,
+                                                  const Val<V> &A, const Val<V> &H) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
@@ -352,52 +345,60 @@ __device__ __forceinline__ void join_begin(Runs<V> &r, const Joins &j, int at, i
     }
     if (lane == 0) r.cut[place] = cut;
     __syncthreads();
-    pcut = false;
-    h = all<V>(0.f);
-    pA = all<V>(1.f);
+    Entering<V> e{all<V>(0.f), all<V>(1.f), false, {}, {}, false};
     for (int w = 0; w < place; ++w) {
         const bool wcut = r.cut[w];
-        pcut |= wcut;
+        e.cut |= wcut;
         Val<V> wa, wh;
 #pragma unroll
         for (int k = 0; k < V; ++k) wa[k] = r.A[w][lane * V + k], wh[k] = r.H[w][lane * V + k];
-        h = wcut ? wh : fma(wa, h, wh);
-        pA = pA * wa;
+        e.h = wcut ? wh : fma(wa, e.h, wh);
+        e.A = e.A * wa;
     }
     if constexpr (kJoin) {
         if (place == kWarps - 1) {
-            const bool tcut = pcut || cut;
-            Val<V> in = all<V>(0.f);
-            const Val<V> tA = A * pA, tH = cut ? H : fma(A, h, H);
+            e.tcut = e.cut || cut;
+            e.tA = A * e.A;
+            e.tH = cut ? H : fma(A, e.h, H);
             if (c < width) {
                 uint2 *word = j.word + (size_t)at * width + c;
-                if (at == 0 || tcut) {
-                    if (!(j.withhold && at == 0)) publish_state<V>(word, tH);
+                if (at == 0 || e.tcut) {
+                    if (!(j.withhold && at == 0)) publish_state<V>(word, e.tH);
                 } else {
-                    publish_run<V>(word, tA, tH);
-                }
-                if (at > 0) {
-                    walk_back<V>(j, at, width, c, in);
-                    if (!tcut) publish_state<V>(word, fma(tA, in, tH));
+                    publish_run<V>(word, e.tA, e.tH);
                 }
             }
-            __syncwarp();
-#pragma unroll
-            for (int k = 0; k < V; ++k) r.in[lane * V + k] = in[k];
         }
     }
+    return e;
 }
-template <int V, bool kJoin>
-__device__ __forceinline__ void join_end(const Runs<V> &r, const Val<V> &pA, bool pcut, Val<V> &h) {
+template <int V, int kWarps, bool kJoin>
+__device__ __forceinline__ void join_walk(Runs<V, kWarps> &r, const Joins &j, int at, int width,
+                                          int c, int place, const Entering<V> &e) {
+    if constexpr (kJoin) {
+        if (place != kWarps - 1) return;
+        Val<V> in = all<V>(0.f);
+        if (at > 0 && c < width) {
+            walk_back<V>(j, at, width, c, in);
+            if (!e.tcut) publish_state<V>(j.word + (size_t)at * width + c, fma(e.tA, in, e.tH));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < V; ++k) r.in[(threadIdx.x & 31) * V + k] = in[k];
+    }
+}
+template <int V, int kWarps, bool kJoin>
+__device__ __forceinline__ Val<V> join_end(const Runs<V, kWarps> &r, const Entering<V> &e) {
     if constexpr (kJoin) {
         __syncthreads();
-        if (!pcut) {
+        if (!e.cut) {
             Val<V> in;
 #pragma unroll
             for (int k = 0; k < V; ++k) in[k] = r.in[(threadIdx.x & 31) * V + k];
-            h = fma(pA, in, h);
+            return fma(e.A, in, e.h);
         }
     }
+    return e.h;
 }
 
 // kTok tokens of one array.  whole: all of them, in all of the warp's lanes.
@@ -405,16 +406,34 @@ template <typename T, int V, int kTok>
 __device__ __forceinline__ void load_run(SsdRaw<T, V> (&raw)[kTok], const void *base,
                                          long long stride, long long t0, int n, int c, bool on,
                                          bool whole) {
-    const T *p = static_cast<const T *>(base) + t0 * stride + c;
+    // a row's address is one value in the warp, a lane adds its channel to it
+    const T *p = static_cast<const T *>(base) + t0 * stride;
     if (whole) {
 #pragma unroll
-        for (int i = 0; i < kTok; ++i, p += stride) raw[i].load_cs(p);
+        for (int i = 0; i < kTok; ++i) raw[i].load_cs(p + i * stride + (unsigned)c);
     } else {
 #pragma unroll
-        for (int i = 0; i < kTok; ++i, p += stride) {
+        for (int i = 0; i < kTok; ++i) {
             raw[i].zero();
-            if (on && i < n) raw[i].load_cs(p);
+            if (on && i < n) raw[i].load_cs(p + i * stride + (unsigned)c);
         }
+    }
+}
+
+// Asks L2 for one array's rows of the tile from t0: a generation of CTAs ahead
+// of their use, so their loads find them there.  A thread takes rows in turn.
+template <typename T, int V, int kTile>
+__device__ __forceinline__ void prefetch_tile(const void *base, long long stride, long long t0,
+                                              long long tokens, int c0, int width) {
+    const int bytes = min(32 * V, width - c0) * (int)sizeof(T);
+    for (int i = threadIdx.x; i < kTile; i += blockDim.x) {
+        if (t0 + i < 0 || t0 + i >= tokens) continue;
+        const char *p = reinterpret_cast<const char *>(static_cast<const T *>(base) +
+                                                       (t0 + i) * stride + c0);
+        for (int b = 0; b < bytes; b += 128)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p + b));
+        if (((uintptr_t)p & 127u) != 0)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p + bytes - 1));
     }
 }
 
@@ -433,12 +452,12 @@ __device__ __forceinline__ void by_form(bool plain, F &&body) {
 }
 
 template <typename T, int V, bool kGate, bool kJoin>
-__global__ void __launch_bounds__(kThreads, 2)
-gated_fwd_kernel(const SsdGatedFwd a, const Joins joins, int blocks) {
-    __shared__ Runs<V> runs;
+__global__ void __launch_bounds__(32 * kFwdWarps, kFwdCtas)
+gated_fwd_kernel(const SsdGatedFwd a, const Joins joins, int blocks, int ahead) {
+    __shared__ Runs<V, kFwdWarps> runs;
     int at, block;
     place<kJoin>(joins, blocks, at, block);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int width = a.in.width, c = (block * 32 + lane) * V;
     const bool on = c < width;
     const long long t0 = (long long)at * kFwdTile + warp * kFwdTok;
@@ -449,6 +468,14 @@ gated_fwd_kernel(const SsdGatedFwd a, const Joins joins, int blocks) {
     load_run<T, V>(graw, a.in.g, a.in.g_stride, t0, n, c, on, whole);
     load_run<T, V>(xraw, a.in.x, a.in.x_stride, t0, n, c, on, whole);
     if constexpr (kGate) load_run<T, V>(zraw, a.in.z, a.in.z_stride, t0, n, c, on, whole);
+    if constexpr (kJoin) {
+        const long long tn = (long long)(at + ahead) * kFwdTile;
+        const int c0 = block * 32 * V;
+        prefetch_tile<T, V, kFwdTile>(a.in.g, a.in.g_stride, tn, a.in.tokens, c0, width);
+        prefetch_tile<T, V, kFwdTile>(a.in.x, a.in.x_stride, tn, a.in.tokens, c0, width);
+        if constexpr (kGate)
+            prefetch_tile<T, V, kFwdTile>(a.in.z, a.in.z_stride, tn, a.in.tokens, c0, width);
+    }
     const Marks m = marks(a.in, t0, kFwdTok);
     const bool plain = whole && (m.starts | m.ends) == 0;
     if (at == 0) pass_empty<V>(a.in, a.in.init, a.final_state, c);
@@ -475,10 +502,18 @@ gated_fwd_kernel(const SsdGatedFwd a, const Joins joins, int blocks) {
             }
         }
     });
-    Val<V> h, pA;
-    bool pcut;
-    join_begin<V, kJoin>(runs, joins, at, width, c, warp, m.starts != 0, A, H, h, pA, pcut);
-    join_end<V, kJoin>(runs, pA, pcut, h);
+    const Entering<V> e = join_begin<V, kFwdWarps, kJoin>(runs, joins, at, width, c, warp,
+                                                          m.starts != 0, A, H);
+    Val<V> silu[kGate ? kFwdTok : 1];
+    if constexpr (kGate) {
+#pragma unroll
+        for (int i = 0; i < kFwdTok; ++i) {
+            const Val<V> z = value(zraw[i]);
+            silu[i] = z * sigmoid(z);
+        }
+    }
+    join_walk<V, kFwdWarps, kJoin>(runs, joins, at, width, c, warp, e);
+    Val<V> h = join_end<V, kFwdWarps, kJoin>(runs, e);
 
     if (a.checkpoints && n > 0 && t0 % kEvery == 0) {
         Val<V> before = h;
@@ -489,17 +524,14 @@ gated_fwd_kernel(const SsdGatedFwd a, const Joins joins, int blocks) {
     }
     by_form(plain, [&](auto form) {
         constexpr bool kPlain = decltype(form)::kOn;
-        T *y = static_cast<T *>(a.y) + t0 * a.y_stride + c;
+        T *y = static_cast<T *>(a.y) + t0 * a.y_stride;
 #pragma unroll
-        for (int i = 0; i < kFwdTok; ++i, y += a.y_stride) {
+        for (int i = 0; i < kFwdTok; ++i) {
             if (!kPlain && i >= n) continue;
             h = !kPlain && ((m.starts >> i) & 1u) ? u[i] : fma(keep[i], h, u[i]);
             Val<V> o = h;
-            if constexpr (kGate) {
-                const Val<V> z = value(zraw[i]);
-                o = h * (z * sigmoid(z));
-            }
-            if (kPlain || on) ssd_store_vec<V>(y, o.v);
+            if constexpr (kGate) o = h * silu[i];
+            if (kPlain || on) ssd_store_vec<V>(y + i * a.y_stride + (unsigned)c, o.v);
             if (!kPlain && ((m.ends >> i) & 1u) && a.final_state) {
                 const int seq = __shfl_sync(0xffffffffu, m.seq, i);
                 if (on) ssd_store_vec<V>(a.final_state + (size_t)seq * width + c, h.v);
@@ -514,14 +546,14 @@ gated_fwd_kernel(const SsdGatedFwd a, const Joins joins, int blocks) {
 // walk is under way; with s = sigmoid(z), dh = dy z s:
 // dz = dy h s (1 + z (1 - s)) = h (s (dy - dh) + dh).
 template <typename T, int V, bool kGate, bool kJoin>
-__global__ void __launch_bounds__(kThreads, 2)
-gated_bwd_kernel(const SsdGatedBwd a, const Joins joins, int blocks, int tiles) {
-    __shared__ Runs<V> runs;
-    __shared__ float fA[kWarps][32 * V], fH[kWarps][32 * V];
-    __shared__ bool fcut[kWarps];
+__global__ void __launch_bounds__(32 * kBwdWarps, kBwdCtas)
+gated_bwd_kernel(const SsdGatedBwd a, const Joins joins, int blocks, int tiles, int ahead) {
+    __shared__ Runs<V, kBwdWarps> runs;
+    __shared__ float fA[kBwdWarps][32 * V], fH[kBwdWarps][32 * V];
+    __shared__ bool fcut[kBwdWarps];
     int at, block;
     place<kJoin>(joins, blocks, at, block);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int width = a.in.width, c = (block * 32 + lane) * V;
     const bool on = c < width;
     const int tile = tiles - 1 - at;
@@ -536,6 +568,15 @@ gated_bwd_kernel(const SsdGatedBwd a, const Joins joins, int blocks, int tiles) 
     load_run<T, V>(xraw, a.in.x, a.in.x_stride, t0, n, c, on, whole);
     Val<V> h;           // the state that enters the tile
     load_f32<V>(a.checkpoints + (size_t)tile * width + c, on && a.in.tokens > 0, h.v);
+    if constexpr (kJoin) {
+        const long long tn = (long long)(tile - ahead) * kBwdTile;
+        const int c0 = block * 32 * V;
+        prefetch_tile<T, V, kBwdTile>(a.in.g, a.in.g_stride, tn, a.in.tokens, c0, width);
+        prefetch_tile<T, V, kBwdTile>(a.dy, a.dy_stride, tn, a.in.tokens, c0, width);
+        if constexpr (kGate)
+            prefetch_tile<T, V, kBwdTile>(a.in.z, a.in.z_stride, tn, a.in.tokens, c0, width);
+        prefetch_tile<T, V, kBwdTile>(a.in.x, a.in.x_stride, tn, a.in.tokens, c0, width);
+    }
     const Marks m = marks(a.in, t0, kBwdTok);
     const bool plain = whole && (m.starts | m.ends) == 0;
     if (at == 0) pass_empty<V>(a.in, a.dfinal, a.dinit, c);
@@ -585,10 +626,8 @@ gated_bwd_kernel(const SsdGatedBwd a, const Joins joins, int blocks, int tiles) 
         fH[warp][lane * V + k] = H[k];
     }
     if (lane == 0) fcut[warp] = m.starts != 0;
-    Val<V> mu, pA;
-    bool pcut;
-    join_begin<V, kJoin>(runs, joins, at, width, c, kWarps - 1 - warp, m.starts != 0, A, M, mu, pA,
-                         pcut);
+    const Entering<V> e = join_begin<V, kBwdWarps, kJoin>(
+        runs, joins, at, width, c, kBwdWarps - 1 - warp, m.starts != 0, A, M);
 
     // forward: the state before each token, and dz
     for (int w = 0; w < warp; ++w) {
@@ -600,7 +639,7 @@ gated_bwd_kernel(const SsdGatedBwd a, const Joins joins, int blocks, int tiles) 
     Val<V> before[kBwdTok];
     by_form(plain, [&](auto form) {
         constexpr bool kPlain = decltype(form)::kOn;
-        [[maybe_unused]] T *dz = kGate ? static_cast<T *>(a.dz) + t0 * a.dz_stride + c : nullptr;
+        [[maybe_unused]] T *dz = kGate ? static_cast<T *>(a.dz) + t0 * a.dz_stride : nullptr;
 #pragma unroll
         for (int i = 0; i < kBwdTok; ++i) {
             if (!kPlain && i >= n) continue;
@@ -612,19 +651,19 @@ gated_bwd_kernel(const SsdGatedBwd a, const Joins joins, int blocks, int tiles) 
             h = fma(keep[i], h, drop[i] * value(xraw[i]));
             if constexpr (kGate) {
                 const Val<V> o = h * fma(sig[i], value(yraw[i]) - dh[i], dh[i]);
-                if (kPlain || on) ssd_store_vec<V>(dz, o.v);
-                dz += a.dz_stride;
+                if (kPlain || on) ssd_store_vec<V>(dz + i * a.dz_stride + (unsigned)c, o.v);
             }
         }
     });
-    join_end<V, kJoin>(runs, pA, pcut, mu);
+    join_walk<V, kBwdWarps, kJoin>(runs, joins, at, width, c, kBwdWarps - 1 - warp, e);
+    Val<V> mu = join_end<V, kBwdWarps, kJoin>(runs, e);
     // backward
     by_form(plain, [&](auto form) {
         constexpr bool kPlain = decltype(form)::kOn;
-        T *dx = static_cast<T *>(a.dx) + (t0 + kBwdTok - 1) * a.dx_stride + c;
-        T *dg = static_cast<T *>(a.dg) + (t0 + kBwdTok - 1) * a.dg_stride + c;
+        T *dx = static_cast<T *>(a.dx) + t0 * a.dx_stride;
+        T *dg = static_cast<T *>(a.dg) + t0 * a.dg_stride;
 #pragma unroll
-        for (int i = kBwdTok - 1; i >= 0; --i, dx -= a.dx_stride, dg -= a.dg_stride) {
+        for (int i = kBwdTok - 1; i >= 0; --i) {
             if (!kPlain && i >= n) continue;
             Val<V> lam = dh[i] + mu;
             if (!kPlain && ((m.ends >> i) & 1u)) {
@@ -636,8 +675,8 @@ gated_bwd_kernel(const SsdGatedBwd a, const Joins joins, int blocks, int tiles) 
             mu = keep[i] * lam;
             const Val<V> og = (mu * drop[i]) * (before[i] - value(xraw[i]));
             if (kPlain || on) {
-                ssd_store_vec<V>(dx, ox.v);
-                ssd_store_vec<V>(dg, og.v);
+                ssd_store_vec<V>(dx + i * a.dx_stride + (unsigned)c, ox.v);
+                ssd_store_vec<V>(dg + i * a.dg_stride + (unsigned)c, og.v);
             }
             if (!kPlain && ((m.starts >> i) & 1u) && a.dinit) {
                 const int seq = __shfl_sync(0xffffffffu, m.seq, i);
@@ -687,14 +726,14 @@ static int tiles_of(long long tokens, int tile) {
 
 static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-// The joins' memory, sized for the smaller (backward) tiles: a ticket, then a
+// The joins' memory, sized for the smaller tiles: a ticket, then a
 // word for every (tile, channel).
 constexpr size_t kTicketBytes = 256;
 static size_t joins_bytes(int tiles, int width) {
     return kTicketBytes + sizeof(uint2) * (size_t)tiles * (size_t)width;
 }
 size_t ssd_gated_workspace(long long tokens, int width) {
-    const int tiles = tiles_of(tokens, kBwdTile);
+    const int tiles = tiles_of(tokens, kBwdTile < kFwdTile ? kBwdTile : kFwdTile);
     return tiles == 1 ? 0 : up256(joins_bytes(tiles, width));
 }
 
@@ -712,36 +751,38 @@ static cudaError_t joins_of(void *workspace, int tiles, int width, unsigned *err
 }
 
 template <typename T, int V, bool kGate>
-static cudaError_t launch_fwd(const SsdGatedFwd &a, void *ws, unsigned *err, cudaStream_t stream) {
+static cudaError_t launch_fwd(const SsdGatedFwd &a, int sms, void *ws, unsigned *err, cudaStream_t stream) {
     const int tiles = tiles_of(a.in.tokens, kFwdTile), blocks = (a.in.width + 32 * V - 1) / (32 * V);
     Joins j{};
     if (tiles == 1) {
-        gated_fwd_kernel<T, V, kGate, false><<<blocks, kThreads, 0, stream>>>(a, j, blocks);
+        gated_fwd_kernel<T, V, kGate, false><<<blocks, 32 * kFwdWarps, 0, stream>>>(a, j, blocks, 0);
         return cudaGetLastError();
     }
     const cudaError_t e = joins_of(ws, tiles, a.in.width, err, stream, &j);
     if (e != cudaSuccess) return e;
     gated_fwd_kernel<T, V, kGate, true>
-        <<<(unsigned)((size_t)tiles * blocks), kThreads, 0, stream>>>(a, j, blocks);
+        <<<(unsigned)((size_t)tiles * blocks), 32 * kFwdWarps, 0, stream>>>(
+            a, j, blocks, (sms * kFwdCtas + blocks - 1) / blocks);
     return cudaGetLastError();
 }
 
 template <typename T, int V, bool kGate>
-static cudaError_t launch_bwd(const SsdGatedBwd &a, void *ws, unsigned *err, cudaStream_t stream) {
+static cudaError_t launch_bwd(const SsdGatedBwd &a, int sms, void *ws, unsigned *err, cudaStream_t stream) {
     const int tiles = tiles_of(a.in.tokens, kBwdTile), blocks = (a.in.width + 32 * V - 1) / (32 * V);
     Joins j{};
     if (tiles == 1) {
-        gated_bwd_kernel<T, V, kGate, false><<<blocks, kThreads, 0, stream>>>(a, j, blocks, tiles);
+        gated_bwd_kernel<T, V, kGate, false><<<blocks, 32 * kBwdWarps, 0, stream>>>(a, j, blocks, tiles, 0);
         return cudaGetLastError();
     }
     const cudaError_t e = joins_of(ws, tiles, a.in.width, err, stream, &j);
     if (e != cudaSuccess) return e;
     gated_bwd_kernel<T, V, kGate, true>
-        <<<(unsigned)((size_t)tiles * blocks), kThreads, 0, stream>>>(a, j, blocks, tiles);
+        <<<(unsigned)((size_t)tiles * blocks), 32 * kBwdWarps, 0, stream>>>(
+            a, j, blocks, tiles, (sms * kBwdCtas + blocks - 1) / blocks);
     return cudaGetLastError();
 }
 
-cudaError_t ssd_launch_gated_fwd(const SsdGatedFwd &a, void *ws, unsigned *err,
+cudaError_t ssd_launch_gated_fwd(const SsdGatedFwd &a, int sms, void *ws, unsigned *err,
                                  cudaStream_t stream) {
     const bool two = pairs_in(a.in) && pairs(a.in.bf16, a.in.width, a.y, a.y_stride) &&
                      pairs(false, a.in.width, a.final_state, 0) &&
@@ -749,18 +790,18 @@ cudaError_t ssd_launch_gated_fwd(const SsdGatedFwd &a, void *ws, unsigned *err,
     const bool gate = a.in.z != nullptr;
     if (a.in.bf16) {
         using T = __nv_bfloat16;
-        if (two) return gate ? launch_fwd<T, 2, true>(a, ws, err, stream)
-                             : launch_fwd<T, 2, false>(a, ws, err, stream);
-        return gate ? launch_fwd<T, 1, true>(a, ws, err, stream)
-                    : launch_fwd<T, 1, false>(a, ws, err, stream);
+        if (two) return gate ? launch_fwd<T, 2, true>(a, sms, ws, err, stream)
+                             : launch_fwd<T, 2, false>(a, sms, ws, err, stream);
+        return gate ? launch_fwd<T, 1, true>(a, sms, ws, err, stream)
+                    : launch_fwd<T, 1, false>(a, sms, ws, err, stream);
     }
-    if (two) return gate ? launch_fwd<float, 2, true>(a, ws, err, stream)
-                         : launch_fwd<float, 2, false>(a, ws, err, stream);
-    return gate ? launch_fwd<float, 1, true>(a, ws, err, stream)
-                : launch_fwd<float, 1, false>(a, ws, err, stream);
+    if (two) return gate ? launch_fwd<float, 2, true>(a, sms, ws, err, stream)
+                         : launch_fwd<float, 2, false>(a, sms, ws, err, stream);
+    return gate ? launch_fwd<float, 1, true>(a, sms, ws, err, stream)
+                : launch_fwd<float, 1, false>(a, sms, ws, err, stream);
 }
 
-cudaError_t ssd_launch_gated_bwd(const SsdGatedBwd &a, void *ws, unsigned *err,
+cudaError_t ssd_launch_gated_bwd(const SsdGatedBwd &a, int sms, void *ws, unsigned *err,
                                  cudaStream_t stream) {
     const bool bf16 = a.in.bf16, gate = a.in.z != nullptr;
     const int w = a.in.width;
@@ -769,15 +810,15 @@ cudaError_t ssd_launch_gated_bwd(const SsdGatedBwd &a, void *ws, unsigned *err,
                      (!gate || pairs(bf16, w, a.dz, a.dz_stride)) && pairs(false, w, a.dinit, 0);
     if (bf16) {
         using T = __nv_bfloat16;
-        if (two) return gate ? launch_bwd<T, 2, true>(a, ws, err, stream)
-                             : launch_bwd<T, 2, false>(a, ws, err, stream);
-        return gate ? launch_bwd<T, 1, true>(a, ws, err, stream)
-                    : launch_bwd<T, 1, false>(a, ws, err, stream);
+        if (two) return gate ? launch_bwd<T, 2, true>(a, sms, ws, err, stream)
+                             : launch_bwd<T, 2, false>(a, sms, ws, err, stream);
+        return gate ? launch_bwd<T, 1, true>(a, sms, ws, err, stream)
+                    : launch_bwd<T, 1, false>(a, sms, ws, err, stream);
     }
-    if (two) return gate ? launch_bwd<float, 2, true>(a, ws, err, stream)
-                         : launch_bwd<float, 2, false>(a, ws, err, stream);
-    return gate ? launch_bwd<float, 1, true>(a, ws, err, stream)
-                : launch_bwd<float, 1, false>(a, ws, err, stream);
+    if (two) return gate ? launch_bwd<float, 2, true>(a, sms, ws, err, stream)
+                         : launch_bwd<float, 2, false>(a, sms, ws, err, stream);
+    return gate ? launch_bwd<float, 1, true>(a, sms, ws, err, stream)
+                : launch_bwd<float, 1, false>(a, sms, ws, err, stream);
 }
 
 cudaError_t ssd_launch_gated_step(const SsdGatedStep &a, cudaStream_t stream) {

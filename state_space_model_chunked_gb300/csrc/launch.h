@@ -187,9 +187,9 @@ struct SsdGatedBwd {
 };
 // ws: ssd_gated_workspace bytes; err: the device error word of bounded waits.
 size_t ssd_gated_workspace(long long tokens, int width);
-cudaError_t ssd_launch_gated_fwd(const SsdGatedFwd &a, void *ws, unsigned *err,
+cudaError_t ssd_launch_gated_fwd(const SsdGatedFwd &a, int sms, void *ws, unsigned *err,
                                  cudaStream_t stream);
-cudaError_t ssd_launch_gated_bwd(const SsdGatedBwd &a, void *ws, unsigned *err,
+cudaError_t ssd_launch_gated_bwd(const SsdGatedBwd &a, int sms, void *ws, unsigned *err,
                                  cudaStream_t stream);
 struct SsdGatedStep {
     float *state;
