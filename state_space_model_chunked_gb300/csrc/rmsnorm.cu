@@ -8,9 +8,11 @@
 //     dw_j = sum over rows of dy_j s_j rstd
 //
 // Both are bound by memory: every value is read once and written once, the
-// sums stay in fp32, and each result is rounded once.  One CTA holds one row
-// in registers (kC runs of V values a thread), so the row's sum and the row's
-// largest |s w| come from one pass and one barrier: max |y| = rstd max |s w|.
+// sums stay in fp32, and each result is rounded once.  A CTA walks over rows,
+// one at a time in registers (kC runs of V values a thread) with the next
+// row's loads under way, and keeps its columns' weights in registers; the
+// row's sum and its largest |s w| come from one pass and one barrier:
+// max |y| = rstd max |s w|.
 #include "launch.h"
 #include "vec.cuh"
 
@@ -18,22 +20,27 @@ namespace {
 
 constexpr float kE4m3Max = 448.f;
 constexpr int kMostWarps = 16;      // a row's CTA: 128 registers a thread
-constexpr int kRuns8 = 4, kRuns1 = 16;   // most runs a thread, of 8 values and of one
+// most runs a thread: of 8 values (forward, backward) and of one
+constexpr int kRuns8 = 4, kBwdRuns8 = 2, kRuns1 = 16;
+// runs wanted a thread where there are rows enough, and warps an SM holds
+constexpr int kFwdRuns = 4, kFwdWarpsSm = 16;
+constexpr int kBwdRuns = 1, kBwdWarpsSm = 16;
 
-// The CTA's sum and maximum over its warps (any number of them up to 32).
+// The CTA's sum, and with kMax its maximum, over its warps (any number of them up to 32).
+template <bool kMax>
 __device__ __forceinline__ void cta_sum_max(float &sum, float &mx, float (*buf)[32]) {
     sum = ssd_warp_sum(sum);
-    mx = ssd_warp_max(mx);
+    if constexpr (kMax) mx = ssd_warp_max(mx);
     const int warps = blockDim.x >> 5;
     if (warps == 1) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0) {
         buf[0][warp] = sum;
-        buf[1][warp] = mx;
+        if constexpr (kMax) buf[1][warp] = mx;
     }
     __syncthreads();
     sum = ssd_warp_sum(lane < warps ? buf[0][lane] : 0.f);
-    mx = ssd_warp_max(lane < warps ? buf[1][lane] : 0.f);
+    if constexpr (kMax) mx = ssd_warp_max(lane < warps ? buf[1][lane] : 0.f);
 }
 
 // The scale of an 8-bit row and the rounding of one of its values.  Below
@@ -50,72 +57,101 @@ struct RowScale {
     __device__ __forceinline__ float apply(float y) const { return tiny ? y / scale : y * inv; }
 };
 
-template <typename TX, typename TR, typename TO, int V, int kC>
-__global__ void __launch_bounds__(32 * kMostWarps) rmsnorm_fwd_kernel(const SsdNormFwd a) {
-    __shared__ float buf[2][32];
-    constexpr bool kFp8 = sizeof(TO) == 1;
-    const long long row = blockIdx.x;
-    const TX *x = static_cast<const TX *>(a.x) + row * a.x_stride;
-    const TR *r = a.residual ? static_cast<const TR *>(a.residual) + row * a.residual_stride
-                             : nullptr;
-    const int nvec = a.width / V;
-    SsdRaw<TX, V> xr[kC];
-    SsdRaw<TR, V> rr[kC];
-#pragma unroll
-    for (int c = 0; c < kC; ++c) {
-        const int i = threadIdx.x + c * blockDim.x;
-        if (i < nvec) {
-            xr[c].load_cs(x + (size_t)i * V);
-            if (r) rr[c].load_cs(r + (size_t)i * V);
-        } else {
-            xr[c].zero();
-        }
-        if (!r || i >= nvec) rr[c].zero();
-    }
-    float s[kC][V], sum = 0.f, mx = 0.f;
-#pragma unroll
-    for (int c = 0; c < kC; ++c) {
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-            s[c][k] = r ? xr[c].get(k) + rr[c].get(k) : xr[c].get(k);
-            sum += s[c][k] * s[c][k];
-        }
-        if constexpr (kFp8) {
-            const int i = threadIdx.x + c * blockDim.x;
-            if (i < nvec) {
-#pragma unroll
-                for (int k = 0; k < V; ++k)
-                    mx = fmaxf(mx, fabsf(s[c][k] * __ldg(a.weight + (size_t)i * V + k)));
-            }
-        }
-    }
-    if (r) {
-        TR *so = static_cast<TR *>(a.residual_out) + row * a.width;
+// kC runs of V values of a row: run c of this thread starts at value
+// (threadIdx.x + c * blockDim.x) * V; runs past the row read as zero.
+template <typename T, int V, int kC>
+struct Row {
+    SsdRaw<T, V> run[kC];
+    __device__ __forceinline__ void load(const T *row, int nvec, bool on) {
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
             const int i = threadIdx.x + c * blockDim.x;
-            if (i < nvec) ssd_store_vec<V>(so + (size_t)i * V, s[c]);
+            run[c].zero();
+            if (on && i < nvec) run[c].load_cs(row + (size_t)i * V);
         }
     }
-    cta_sum_max(sum, mx, buf);
-    const float rstd = rsqrtf(sum / (float)a.width + a.eps);
-    const RowScale q(kFp8 ? mx * rstd : 0.f);
-    if (threadIdx.x == 0) {
-        a.rstd[row] = rstd;
-        if constexpr (kFp8) a.scale[row] = q.scale;
-    }
-    TO *y = static_cast<TO *>(a.y) + row * a.width;
+};
+template <int V, int kC>
+__device__ __forceinline__ void load_weight(const float *weight, int nvec, float (&w)[kC][V]) {
 #pragma unroll
     for (int c = 0; c < kC; ++c) {
         const int i = threadIdx.x + c * blockDim.x;
-        if (i >= nvec) continue;
-        float o[V];
+        SsdRaw<float, V> r;
+        r.zero();
+        if (i < nvec) r.load(weight + (size_t)i * V);
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            o[k] = s[c][k] * rstd * __ldg(a.weight + (size_t)i * V + k);
-            if constexpr (kFp8) o[k] = q.apply(o[k]);
+        for (int k = 0; k < V; ++k) w[c][k] = r.get(k);
+    }
+}
+
+template <typename TX, typename TR, typename TO, int V, int kC>
+__global__ void __launch_bounds__(32 * kMostWarps) rmsnorm_fwd_kernel(const SsdNormFwd a) {
+    __shared__ float buf[2][2][32];
+    constexpr bool kFp8 = sizeof(TO) == 1;
+    const int nvec = a.width / V;
+    const bool res = a.residual != nullptr;
+    const TX *x = static_cast<const TX *>(a.x);
+    const TR *r = static_cast<const TR *>(a.residual);
+    Row<TX, V, kC> xr;
+    Row<TR, V, kC> rr;
+    long long row = blockIdx.x;
+    xr.load(x + row * a.x_stride, nvec, true);
+    rr.load(r + row * a.residual_stride, nvec, res);
+    float w[kC][V];
+    load_weight<V, kC>(a.weight, nvec, w);
+    for (int turn = 0; row < a.rows; turn ^= 1) {
+        float s[kC][V], sum = 0.f, mx = 0.f;
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                s[c][k] = xr.run[c].get(k);
+                if (res) s[c][k] += rr.run[c].get(k);
+                sum += s[c][k] * s[c][k];
+            }
         }
-        ssd_store_vec<V>(y + (size_t)i * V, o);
+        const long long next = row + gridDim.x;
+        if (next < a.rows) {
+            xr.load(x + next * a.x_stride, nvec, true);
+            rr.load(r + next * a.residual_stride, nvec, res);
+        }
+        if (res) {
+            TR *so = static_cast<TR *>(a.residual_out) + row * a.width;
+#pragma unroll
+            for (int c = 0; c < kC; ++c) {
+                const int i = threadIdx.x + c * blockDim.x;
+                if (i < nvec) ssd_store_vec<V>(so + (size_t)i * V, s[c]);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                s[c][k] *= w[c][k];
+                if constexpr (kFp8) mx = fmaxf(mx, fabsf(s[c][k]));
+            }
+        }
+        cta_sum_max<kFp8>(sum, mx, buf[turn]);
+        const float rstd = rsqrtf(sum / (float)a.width + a.eps);
+        const RowScale q(kFp8 ? mx * rstd : 0.f);
+        if (threadIdx.x == 0) {
+            a.rstd[row] = rstd;
+            if constexpr (kFp8) a.scale[row] = q.scale;
+        }
+        TO *y = static_cast<TO *>(a.y) + row * a.width;
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+            const int i = threadIdx.x + c * blockDim.x;
+            if (i >= nvec) continue;
+            float o[V];
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                o[k] = s[c][k] * rstd;
+                if constexpr (kFp8) o[k] = q.apply(o[k]);
+            }
+            ssd_store_vec<V>(y + (size_t)i * V, o);
+        }
+        row = next;
     }
 }
 
@@ -135,7 +171,7 @@ __global__ void rmsnorm_fwd_wide_kernel(const SsdNormFwd a) {
         sum += s * s;
         if constexpr (kFp8) mx = fmaxf(mx, fabsf(s * a.weight[i]));
     }
-    cta_sum_max(sum, mx, buf);
+    cta_sum_max<kFp8>(sum, mx, buf);
     const float rstd = rsqrtf(sum / (float)a.width + a.eps);
     const RowScale q(kFp8 ? mx * rstd : 0.f);
     if (threadIdx.x == 0) {
@@ -162,48 +198,47 @@ __global__ void __launch_bounds__(32 * kMostWarps)
 rmsnorm_bwd_kernel(const SsdNormBwd a, float *__restrict__ partial) {
     __shared__ float buf[2][2][32];
     const int nvec = a.width / V;
-    float dw[kC][V];
+    const bool res = a.dresidual != nullptr;
+    const T *dy = static_cast<const T *>(a.dy);
+    const TS *st = static_cast<const TS *>(a.s), *dres = static_cast<const TS *>(a.dresidual);
+    Row<T, V, kC> yr;
+    Row<TS, V, kC> sr, dr;
+    long long row = blockIdx.x;
+    yr.load(dy + row * a.dy_stride, nvec, true);
+    sr.load(st + row * a.s_stride, nvec, true);
+    dr.load(dres + row * a.dresidual_stride, nvec, res);
+    float rstd = a.rstd[row];
+    float w[kC][V], dw[kC][V];
+    load_weight<V, kC>(a.weight, nvec, w);
 #pragma unroll
     for (int c = 0; c < kC; ++c)
 #pragma unroll
         for (int k = 0; k < V; ++k) dw[c][k] = 0.f;
-    int turn = 0;
-    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
-        const T *dy = static_cast<const T *>(a.dy) + row * a.dy_stride;
-        const TS *s = static_cast<const TS *>(a.s) + row * a.s_stride;
-        const TS *dres = a.dresidual
-                             ? static_cast<const TS *>(a.dresidual) + row * a.dresidual_stride
-                             : nullptr;
-        const float rstd = a.rstd[row];
-        SsdRaw<T, V> yr[kC];
-        SsdRaw<TS, V> sr[kC], dr[kC];
+    for (int turn = 0; row < a.rows; turn ^= 1) {
+        // e = dy w, v = s rstd, and what came from elsewhere
+        float e[kC][V], v[kC][V], d[kC][V], sum = 0.f, unused = 0.f;
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
-            const int i = threadIdx.x + c * blockDim.x;
-            if (i < nvec) {
-                yr[c].load_cs(dy + (size_t)i * V);
-                sr[c].load_cs(s + (size_t)i * V);
-                if (dres) dr[c].load_cs(dres + (size_t)i * V);
-            } else {
-                yr[c].zero();
-                sr[c].zero();
-            }
-            if (!dres || i >= nvec) dr[c].zero();
-        }
-        float e[kC][V], sum = 0.f, unused = 0.f;
-#pragma unroll
-        for (int c = 0; c < kC; ++c) {
-            const int i = threadIdx.x + c * blockDim.x;
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-                const float dyv = yr[c].get(k), sv = sr[c].get(k);
-                e[c][k] = i < nvec ? dyv * __ldg(a.weight + (size_t)i * V + k) : 0.f;
-                sum += e[c][k] * sv;
-                dw[c][k] += dyv * (sv * rstd);
+                const float dyv = yr.run[c].get(k);
+                v[c][k] = sr.run[c].get(k) * rstd;
+                d[c][k] = dr.run[c].get(k);
+                e[c][k] = dyv * w[c][k];
+                sum += e[c][k] * v[c][k];
+                dw[c][k] += dyv * v[c][k];
             }
         }
-        cta_sum_max(sum, unused, buf[turn]);
-        const float m = sum / (float)a.width * rstd * rstd;
+        const float scale = rstd;
+        const long long next = row + gridDim.x;
+        if (next < a.rows) {
+            yr.load(dy + next * a.dy_stride, nvec, true);
+            sr.load(st + next * a.s_stride, nvec, true);
+            dr.load(dres + next * a.dresidual_stride, nvec, res);
+            rstd = a.rstd[next];
+        }
+        cta_sum_max<false>(sum, unused, buf[turn]);
+        const float mean = sum / (float)a.width;
         T *dx = static_cast<T *>(a.dx) + row * a.width;
         TS *ds = a.ds ? static_cast<TS *>(a.ds) + row * a.width : nullptr;
 #pragma unroll
@@ -212,13 +247,11 @@ rmsnorm_bwd_kernel(const SsdNormBwd a, float *__restrict__ partial) {
             if (i >= nvec) continue;
             float o[V];
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-                o[k] = rstd * (e[c][k] - sr[c].get(k) * m);
-                if (dres) o[k] += dr[c].get(k);
-            }
+            for (int k = 0; k < V; ++k) o[k] = scale * (e[c][k] - v[c][k] * mean) + d[c][k];
             ssd_store_vec<V>(dx + (size_t)i * V, o);
             if (ds) ssd_store_vec<V>(ds + (size_t)i * V, o);
         }
+        row = next;
     }
 #pragma unroll
     for (int c = 0; c < kC; ++c) {
@@ -240,7 +273,7 @@ __global__ void rmsnorm_bwd_wide_kernel(const SsdNormBwd a) {
     float sum = 0.f, unused = 0.f;
     for (int i = threadIdx.x; i < a.width; i += blockDim.x)
         sum += ssd_ld(dy + i) * a.weight[i] * ssd_ld(s + i);
-    cta_sum_max(sum, unused, buf);
+    cta_sum_max<false>(sum, unused, buf);
     const float m = sum / (float)a.width * rstd * rstd;
     T *dx = static_cast<T *>(a.dx) + row * a.width;
     TS *ds = a.ds ? static_cast<TS *>(a.ds) + row * a.width : nullptr;
@@ -278,19 +311,24 @@ rmsnorm_dw_kernel(const float *__restrict__ partial, int n, int width, float *__
     if (threadIdx.x == 0 && jo < width) out[jo] = v;
 }
 
-// Threads and runs a thread for one row: at most kC runs of V values, a power
-// of two of warps; 0 warps when the row does not fit.
+// Threads and runs a thread for one row: at most `most_runs` runs of V values a
+// thread (`want` where the warps allow it), a power of two of warps; 0 warps
+// when the row does not fit.
 struct RowShape {
     int warps, runs;
 };
-RowShape row_shape(int width, int V, int most_runs, bool few_rows) {
+RowShape row_shape(int width, int V, int most_runs, int want) {
     const int nvec = (width + V - 1) / V;
-    // few rows leave SMs idle: one run a thread, so the row is read in one step
-    const int want = few_rows ? 1 : most_runs;
     int w = 1;
     while (w < kMostWarps && (long long)w * 32 * want < nvec) w *= 2;
     const int runs = (nvec + w * 32 - 1) / (w * 32);
     return {runs <= most_runs ? w : 0, runs};
+}
+
+// CTAs of a walk over rows: as many as the SMs hold at once.
+unsigned walkers(long long rows, int sms, int ctas) {
+    const long long n = (long long)sms * ctas;
+    return (unsigned)(rows < n ? rows : n);
 }
 
 bool vec8(const void *p, long long stride, int size) {
@@ -299,14 +337,16 @@ bool vec8(const void *p, long long stride, int size) {
 
 template <typename TX, typename TR, typename TO>
 cudaError_t launch_fwd(const SsdNormFwd &a, int sms, cudaStream_t stream) {
-    const bool v8 = a.width % 8 == 0 && vec8(a.x, a.x_stride, sizeof(TX)) &&
+    const bool v8 = a.width % 8 == 0 && vec8(a.weight, 0, 4) && vec8(a.x, a.x_stride, sizeof(TX)) &&
                     vec8(a.residual, a.residual_stride, sizeof(TR)) &&
                     vec8(a.residual_out, a.width, sizeof(TR)) && ((uintptr_t)a.y & 7u) == 0 &&
                     vec8(sizeof(TO) == 1 ? nullptr : a.y, a.width, sizeof(TO));
-    const unsigned rows = (unsigned)a.rows;
-    const RowShape sh = row_shape(a.width, v8 ? 8 : 1, v8 ? kRuns8 : kRuns1, a.rows <= sms);
+    // few rows leave SMs idle: one run a thread, so the row is read in one step
+    const RowShape sh = row_shape(a.width, v8 ? 8 : 1, v8 ? kRuns8 : kRuns1,
+                                  a.rows <= sms ? 1 : (v8 ? kFwdRuns : kRuns1));
+    const unsigned rows = walkers(a.rows, sms, kFwdWarpsSm / (sh.warps ? sh.warps : 1));
     if (sh.warps == 0) {
-        rmsnorm_fwd_wide_kernel<TX, TR, TO><<<rows, 1024, 0, stream>>>(a);
+        rmsnorm_fwd_wide_kernel<TX, TR, TO><<<(unsigned)a.rows, 1024, 0, stream>>>(a);
     } else if (v8) {
         switch (sh.runs) {
             case 1: rmsnorm_fwd_kernel<TX, TR, TO, 8, 1><<<rows, 32 * sh.warps, 0, stream>>>(a); break;
@@ -329,21 +369,21 @@ cudaError_t launch_fwd_out(const SsdNormFwd &a, int sms, cudaStream_t stream) {
     }
 }
 
-// CTAs of the backward pass: enough to fill the SMs, few enough that the
-// partial sums of dw stay small next to the rows.
-int bwd_ctas(long long rows, int sms) {
-    const long long most = 4ll * sms;
-    return (int)(rows < most ? rows : most);
+// CTAs, and so rows of partial sums, of the backward pass: by the warps that a
+// row of this width takes with vectors (a row without them takes fewer CTAs).
+int bwd_ctas(long long rows, int width, int sms) {
+    const RowShape sh = row_shape(width, 8, kBwdRuns8, kBwdRuns);
+    return (int)walkers(rows, sms, sh.warps ? kBwdWarpsSm / sh.warps : 2);
 }
 
 template <typename T, typename TS>
 cudaError_t launch_bwd(const SsdNormBwd &a, float *partial, int sms, cudaStream_t stream) {
-    const bool v8 = a.width % 8 == 0 && vec8(a.dy, a.dy_stride, sizeof(T)) &&
+    const bool v8 = a.width % 8 == 0 && vec8(a.weight, 0, 4) && vec8(a.dy, a.dy_stride, sizeof(T)) &&
                     vec8(a.s, a.s_stride, sizeof(TS)) &&
                     vec8(a.dresidual, a.dresidual_stride, sizeof(TS)) &&
                     vec8(a.dx, a.width, sizeof(T)) && vec8(a.ds, a.width, sizeof(TS));
-    const RowShape sh = row_shape(a.width, v8 ? 8 : 1, v8 ? kRuns8 : kRuns1, a.rows <= sms);
-    int n = bwd_ctas(a.rows, sms);
+    const RowShape sh = row_shape(a.width, v8 ? 8 : 1, v8 ? kBwdRuns8 : kRuns1, v8 ? kBwdRuns : kRuns1);
+    const int n = bwd_ctas(a.rows, a.width, sms);
     if (sh.warps == 0) {
         rmsnorm_bwd_wide_kernel<T, TS><<<(unsigned)a.rows, 1024, 0, stream>>>(a);
         const dim3 grid((unsigned)n, (unsigned)((a.width + 255) / 256));
@@ -351,9 +391,7 @@ cudaError_t launch_bwd(const SsdNormBwd &a, float *partial, int sms, cudaStream_
     } else if (v8) {
         switch (sh.runs) {
             case 1: rmsnorm_bwd_kernel<T, TS, 8, 1><<<n, 32 * sh.warps, 0, stream>>>(a, partial); break;
-            case 2: rmsnorm_bwd_kernel<T, TS, 8, 2><<<n, 32 * sh.warps, 0, stream>>>(a, partial); break;
-            case 3: rmsnorm_bwd_kernel<T, TS, 8, 3><<<n, 32 * sh.warps, 0, stream>>>(a, partial); break;
-            default: rmsnorm_bwd_kernel<T, TS, 8, 4><<<n, 32 * sh.warps, 0, stream>>>(a, partial); break;
+            default: rmsnorm_bwd_kernel<T, TS, 8, 2><<<n, 32 * sh.warps, 0, stream>>>(a, partial); break;
         }
     } else {
         rmsnorm_bwd_kernel<T, TS, 1, kRuns1><<<n, 32 * sh.warps, 0, stream>>>(a, partial);
@@ -374,7 +412,7 @@ cudaError_t ssd_launch_rmsnorm_fwd(const SsdNormFwd &a, int sms, cudaStream_t st
 }
 
 size_t ssd_rmsnorm_bwd_workspace(long long rows, int width, int sms) {
-    return (size_t)bwd_ctas(rows, sms) * (size_t)width * sizeof(float);
+    return (size_t)bwd_ctas(rows, width, sms) * (size_t)width * sizeof(float);
 }
 
 cudaError_t ssd_launch_rmsnorm_bwd(const SsdNormBwd &a, float *partial, int sms,
