@@ -21,7 +21,7 @@ LIB = os.path.join(OUT_DIR, "libssd.so")
 OBJ_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.cu", "decode.cu", "scan_simt.cu", "scan_tc.cu", "scan_static.cu", "widen.cu",
            "seqshard.cu", "api_layer.cu", "rmsnorm.cu", "gated_scan.cu", "linear_simt.cu",
-           "linear_tc.cu"]
+           "linear_tc.cu", "linear_gemv.cu", "linear_few.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

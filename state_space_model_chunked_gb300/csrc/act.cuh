@@ -3,10 +3,17 @@
 #pragma once
 
 #include "launch.h"
+#include "ptx.cuh"
+
+// 1 / (1 + e^-p) by the hardware's exponential and reciprocal (a few 2^-23);
+// e^-p past fp32's range gives 0.
+__device__ __forceinline__ float ssd_sigmoid(float p) {
+    return ssdptx::rcp_approx(1.f + ssdptx::ex2_approx(p * -1.44269504f));
+}
 
 __device__ __forceinline__ float ssd_act(float p, SsdAct act) {
     switch (act) {
-        case SsdAct::silu: return ssd_silu(p);
+        case SsdAct::silu: return p * ssd_sigmoid(p);
         case SsdAct::gelu: return 0.5f * p * (1.f + erff(p * 0.70710678f));
         case SsdAct::relu: return p < 0.f ? 0.f : p;
         default: return p;
@@ -16,7 +23,7 @@ __device__ __forceinline__ float ssd_act(float p, SsdAct act) {
 __device__ __forceinline__ float ssd_act_slope(float p, SsdAct act) {
     switch (act) {
         case SsdAct::silu: {
-            const float sig = __fdividef(1.f, 1.f + __expf(-p));
+            const float sig = ssd_sigmoid(p);
             return sig * (1.f + p * (1.f - sig));
         }
         case SsdAct::gelu:
@@ -25,4 +32,23 @@ __device__ __forceinline__ float ssd_act_slope(float p, SsdAct act) {
         case SsdAct::relu: return p > 0.f ? 1.f : 0.f;
         default: return 1.f;
     }
+}
+
+// Single elements of the product's output types, and the epilogue of one of its
+// values: token m, feature n.
+__device__ __forceinline__ float ssd_elt_load(const void *p, long long i, SsdElt t) {
+    return t == SSD_ELT_F32 ? static_cast<const float *>(p)[i]
+                            : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
+}
+__device__ __forceinline__ void ssd_elt_store(void *p, long long i, SsdElt t, float v) {
+    if (t == SSD_ELT_F32) static_cast<float *>(p)[i] = v;
+    else static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
+}
+__device__ __forceinline__ void ssd_finish(const SsdProduct &p, long long m, long long n, float v) {
+    if (p.a_scale) v *= __ldg(p.a_scale + m) * __ldg(p.b_scale + n);
+    if (p.bias) v += __ldg(p.bias + n);
+    if (p.preact) ssd_elt_store(p.preact, m * p.n + n, p.preact_type, v);
+    v = ssd_act(v, p.act);
+    if (p.residual) v += ssd_elt_load(p.residual, m * p.residual_row + n, p.out_type);
+    ssd_elt_store(p.out, m * p.out_row + n, p.out_type, v);
 }

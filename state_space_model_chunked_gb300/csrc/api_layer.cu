@@ -46,6 +46,8 @@ bool valid_activation(ssd_activation a) { return a >= SSD_ACT_NONE && a <= SSD_A
 
 // The product on the path its types and alignments take.
 cudaError_t launch_product(const SsdProduct &p, cudaStream_t stream) {
+    if (ssd_product_few_handles(p)) return ssd_launch_product_few(p, ssd_sm_count(), stream);
+    if (ssd_product_gemv_handles(p)) return ssd_launch_product_gemv(p, stream);
     if (ssd_product_tc_handles(p))
         return ssd_launch_product_tc(p, ssd_sm_count(), ssd_device_error_word(), stream);
     return ssd_launch_product_simt(p, stream);

@@ -221,6 +221,10 @@ struct SsdProduct {
     long long out_row;
 };
 cudaError_t ssd_launch_product_simt(const SsdProduct &p, cudaStream_t stream);
+bool ssd_product_few_handles(const SsdProduct &p);
+cudaError_t ssd_launch_product_few(const SsdProduct &p, int sms, cudaStream_t stream);
+bool ssd_product_gemv_handles(const SsdProduct &p);
+cudaError_t ssd_launch_product_gemv(const SsdProduct &p, cudaStream_t stream);
 bool ssd_product_tc_handles(const SsdProduct &p);
 cudaError_t ssd_launch_product_tc(const SsdProduct &p, int sms, unsigned *err,
                                   cudaStream_t stream);

@@ -15,19 +15,11 @@
 namespace {
 
 constexpr int kTile = 64, kStep = 16;
+constexpr int kAhead = 4;      // rows of the gradients' pass under way in a thread
 
 __device__ __forceinline__ float ld(const float *p) { return *p; }
 __device__ __forceinline__ float ld(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
 __device__ __forceinline__ float ld(const __nv_fp8_e4m3 *p) { return float(*p); }
-
-__device__ __forceinline__ float ld_any(const void *p, long long i, SsdElt t) {
-    return t == SSD_ELT_F32 ? static_cast<const float *>(p)[i]
-                            : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
-}
-__device__ __forceinline__ void st_any(void *p, long long i, SsdElt t, float v) {
-    if (t == SSD_ELT_F32) static_cast<float *>(p)[i] = v;
-    else static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
-}
 
 // kStep x kTile values of one operand, row-major by k in shared memory.  The
 // thread order follows the operand's unit stride, so loads are coalesced.
@@ -73,58 +65,105 @@ __global__ void __launch_bounds__(256) product_simt_kernel(const SsdProduct p) {
         for (int j = 0; j < 4; ++j) {
             const long long n = n0 + 4 * tx + j;
             if (n >= p.n) break;
-            float v = acc[i][j];
-            if (p.a_scale) v *= p.a_scale[m] * p.b_scale[n];
-            if (p.bias) v += p.bias[n];
-            if (p.preact) st_any(p.preact, m * p.n + n, p.preact_type, v);
-            v = ssd_act(v, p.act);
-            if (p.residual) v += ld_any(p.residual, m * p.residual_row + n, p.out_type);
-            st_any(p.out, m * p.out_row + n, p.out_type, v);
+            ssd_finish(p, m, n, acc[i][j]);
         }
     }
 }
 
-// dp = dy act'(p) and its column sums.  32 x 8 threads take 32 columns of the
-// rows b, b + grid, ... ; the sums of each block of rows go to `partial`.
-template <typename T>
+// dp = dy act'(p) and its column sums: bound by memory.  32 x 8 threads take
+// 32 V columns of the rows b, b + grid, ... ; a thread's sums stay in registers,
+// each block of rows' go to `partial`.
+template <typename T, int V>
 __global__ void __launch_bounds__(256) act_bwd_kernel(const SsdActBwd a, float *partial) {
-    __shared__ float part[8][33];
-    const int j = blockIdx.x * 32 + threadIdx.x;
-    float acc = 0.f;
+    __shared__ float part[8][32 * V + 1];
+    const int j = (blockIdx.x * 32 + threadIdx.x) * V;
+    float acc[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) acc[k] = 0.f;
     if (j < a.width) {
-        for (long long r = (long long)blockIdx.y * 8 + threadIdx.y; r < a.rows;
-             r += (long long)gridDim.y * 8) {
-            float v = ssd_ld(static_cast<const T *>(a.dy) + r * a.dy_stride + j);
-            if (a.preact)
-                v *= ssd_act_slope(ssd_ld(static_cast<const T *>(a.preact) + r * a.width + j), a.act);
-            if (a.dp) ssd_st(static_cast<T *>(a.dp) + r * a.width + j, v);
-            acc += v;
+        const T *dy = static_cast<const T *>(a.dy) + j, *pre = static_cast<const T *>(a.preact) + j;
+        const long long step = (long long)gridDim.y * 8;
+        for (long long r = (long long)blockIdx.y * 8 + threadIdx.y; r < a.rows; r += kAhead * step) {
+            SsdRaw<T, V> d[kAhead], p[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const long long ru = r + u * step;
+                d[u].zero();
+                p[u].zero();
+                if (ru >= a.rows) continue;
+                d[u].load_cs(dy + ru * a.dy_stride);
+                if (a.preact) p[u].load_cs(pre + ru * a.width);
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const long long ru = r + u * step;
+                if (ru >= a.rows) continue;
+                float v[V];
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    v[k] = d[u].get(k);
+                    if (a.preact) v[k] *= ssd_act_slope(p[u].get(k), a.act);
+                    acc[k] += v[k];
+                }
+                if (a.dp) ssd_store_vec<V>(static_cast<T *>(a.dp) + ru * a.width + j, v);
+            }
         }
     }
     if (!partial) return;
-    part[threadIdx.y][threadIdx.x] = acc;
+#pragma unroll
+    for (int k = 0; k < V; ++k) part[threadIdx.y][threadIdx.x * V + k] = acc[k];
     __syncthreads();
-    if (threadIdx.y == 0 && j < a.width) {
+    for (int i = threadIdx.y * 32 + threadIdx.x; i < 32 * V; i += 256) {
+        const int col = blockIdx.x * 32 * V + i;
         float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += part[i][threadIdx.x];
-        partial[(size_t)blockIdx.y * a.width + j] = s;
+        for (int y = 0; y < 8; ++y) s += part[y][i];
+        if (col < a.width) partial[(size_t)blockIdx.y * a.width + col] = s;
     }
 }
 
+// out[j] = the sum over n partial rows in a fixed order: 32 x 8 threads take 32
+// columns, each thread row every 8th partial row.
 __global__ void __launch_bounds__(256)
 column_sum_kernel(const float *__restrict__ partial, int n, int width, float *__restrict__ out) {
-    const int j = blockIdx.x * 256 + threadIdx.x;
-    if (j >= width) return;
+    __shared__ float part[8][32];
+    const int j = blockIdx.x * 32 + threadIdx.x;
     float s = 0.f;
-    for (int r = 0; r < n; ++r) s += partial[(size_t)r * width + j];
-    out[j] = s;
+    if (j < width) {
+#pragma unroll 4
+        for (int r = threadIdx.y; r < n; r += 8) s += partial[(size_t)r * width + j];
+    }
+    part[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.y == 0 && j < width) {
+        s = 0.f;
+#pragma unroll
+        for (int y = 0; y < 8; ++y) s += part[y][threadIdx.x];
+        out[j] = s;
+    }
 }
 
+// Blocks of rows: eight CTAs an SM, whatever vectors the arrays allow.
 int act_bwd_rows(long long rows, int width, int sms) {
-    const long long cols = (width + 31) / 32;
+    const long long cols = (width + 255) / 256;
     const long long want = (8ll * sms + cols - 1) / cols, most = (rows + 7) / 8;
     return (int)(want < most ? want : most);
+}
+
+template <typename T>
+cudaError_t launch_act_bwd(const SsdActBwd &a, float *partial, int n, cudaStream_t stream) {
+    const auto on_16 = [](const void *p, long long stride) {
+        return !p || (((uintptr_t)p & 15u) == 0 && (stride * sizeof(T)) % 16 == 0);
+    };
+    const dim3 block(32, 8);
+    if (on_16(a.dy, a.dy_stride) && on_16(a.preact, a.width) && on_16(a.dp, a.width) &&
+        a.width % 8 == 0)
+        act_bwd_kernel<T, 8><<<dim3((unsigned)((a.width + 255) / 256), (unsigned)n), block, 0,
+                               stream>>>(a, partial);
+    else
+        act_bwd_kernel<T, 1><<<dim3((unsigned)((a.width + 31) / 32), (unsigned)n), block, 0,
+                               stream>>>(a, partial);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -145,13 +184,12 @@ size_t ssd_act_bwd_workspace(long long rows, int width, int sms) {
 
 cudaError_t ssd_launch_act_bwd(const SsdActBwd &a, float *partial, int sms, cudaStream_t stream) {
     const int n = act_bwd_rows(a.rows, a.width, sms);
-    const dim3 grid((unsigned)((a.width + 31) / 32), (unsigned)n), block(32, 8);
     float *part = a.dbias ? partial : nullptr;
-    if (a.type == SSD_ELT_F32) act_bwd_kernel<float><<<grid, block, 0, stream>>>(a, part);
-    else act_bwd_kernel<__nv_bfloat16><<<grid, block, 0, stream>>>(a, part);
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = a.type == SSD_ELT_F32
+                              ? launch_act_bwd<float>(a, part, n, stream)
+                              : launch_act_bwd<__nv_bfloat16>(a, part, n, stream);
     if (e != cudaSuccess || !a.dbias) return e;
-    column_sum_kernel<<<(unsigned)((a.width + 255) / 256), 256, 0, stream>>>(partial, n, a.width,
-                                                                            a.dbias);
+    column_sum_kernel<<<(unsigned)((a.width + 31) / 32), dim3(32, 8), 0, stream>>>(partial, n,
+                                                                                 a.width, a.dbias);
     return cudaGetLastError();
 }

@@ -18,6 +18,8 @@
 // distributed shared memory, in rank order.
 #include <cuda.h>
 
+#include <algorithm>
+
 #include "act.cuh"
 #include "launch.h"
 #include "ptx.cuh"
@@ -49,7 +51,7 @@ constexpr uint32_t tmem_cols(int bn, bool split) {
 struct Args {
     SsdProduct p;           // rows of A are p.m, or (kSwap) p.n
     int row_tiles, col_tiles, kblocks;
-    bool vec;               // 16-byte rows of out, preact and residual
+    bool vec;               // 16-byte rows of out, preact, residual; bias and b_scale on 16 bytes
     unsigned *err;
     unsigned long long wait_ns;
 };
@@ -92,88 +94,85 @@ __device__ __forceinline__ void tile_at(const Args &a, int t, int &row, int &col
     col = (t - g * per) / rows;
 }
 
-__device__ __forceinline__ void act_all(float (&v)[8], SsdAct act) {
+template <SsdAct kAct, int N>
+__device__ __forceinline__ void act_each(float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = ssd_act(v[i], kAct);
+}
+template <int N>
+__device__ __forceinline__ void act_all(float (&v)[N], SsdAct act) {
     switch (act) {
-        case SsdAct::silu:
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = ssd_act(v[i], SsdAct::silu);
-            break;
-        case SsdAct::gelu:
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = ssd_act(v[i], SsdAct::gelu);
-            break;
-        case SsdAct::relu:
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = ssd_act(v[i], SsdAct::relu);
-            break;
+        case SsdAct::silu: act_each<SsdAct::silu>(v); break;
+        case SsdAct::gelu: act_each<SsdAct::gelu>(v); break;
+        case SsdAct::relu: act_each<SsdAct::relu>(v); break;
         default: break;
     }
 }
 
-__device__ __forceinline__ float load_one(const void *p, long long i, SsdElt t) {
-    return t == SSD_ELT_F32 ? static_cast<const float *>(p)[i]
-                            : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
-}
-__device__ __forceinline__ void store_one(void *p, long long i, SsdElt t, float v) {
-    if (t == SSD_ELT_F32) static_cast<float *>(p)[i] = v;
-    else static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
+__device__ __forceinline__ float4 cols4(const float *p, long long n) {
+    return __ldg(reinterpret_cast<const float4 *>(p + n));
 }
 
-// Eight columns n .. n + 7 of row m (m in range; n < p.n).
-__device__ __forceinline__ void finish_row8(const Args &a, long long m, long long n, float (&v)[8]) {
+// One value, for the edges: out of line, so the epilogue's code stays small.
+__device__ __noinline__ void finish_edge(const SsdProduct &p, long long m, long long n, float v) {
+    if (m < p.m && n < p.n) ssd_finish(p, m, n, v);
+}
+
+// N columns n .. n + N - 1 of row m.  Rows of 16-byte vectors and all columns in
+// range: whole vectors, the residual's asked for first; else value by value.
+template <typename TO, int N>
+__device__ __forceinline__ void finish_cols(const Args &a, long long m, long long n, float scale,
+                                            float (&v)[N]) {
     const SsdProduct &p = a.p;
-    const bool whole = a.vec && n + 8 <= p.n;
-    if (p.a_scale) {
-        const float s = __ldg(p.a_scale + m);
+    if (!a.vec || n + N > p.n) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= n + i < p.n ? s * __ldg(p.b_scale + n + i) : 0.f;
+        for (int i = 0; i < N; ++i) finish_edge(p, m, n + i, v[i]);
+        return;
+    }
+    if (m >= p.m) return;
+    const TO *res = static_cast<const TO *>(p.residual) + m * p.residual_row + n;
+    SsdRaw<TO, 8> r[N / 8];
+    if (p.residual) {
+#pragma unroll
+        for (int j = 0; j < N / 8; ++j) r[j].load(res + 8 * j);
+    }
+    if (p.a_scale) {
+#pragma unroll
+        for (int j = 0; j < N; j += 4) {
+            const float4 s = cols4(p.b_scale, n + j);
+            v[j] *= scale * s.x, v[j + 1] *= scale * s.y;
+            v[j + 2] *= scale * s.z, v[j + 3] *= scale * s.w;
+        }
     }
     if (p.bias) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += n + i < p.n ? __ldg(p.bias + n + i) : 0.f;
-    }
-    if (p.preact) {
-        if (whole) {
-            ssd_store_vec<8>(static_cast<__nv_bfloat16 *>(p.preact) + m * p.n + n, v);
-        } else {
-            for (int i = 0; i < 8 && n + i < p.n; ++i)
-                store_one(p.preact, m * p.n + n + i, SSD_ELT_BF16, v[i]);
+        for (int j = 0; j < N; j += 4) {
+            const float4 b = cols4(p.bias, n + j);
+            v[j] += b.x, v[j + 1] += b.y, v[j + 2] += b.z, v[j + 3] += b.w;
         }
     }
+    const auto store = [&](auto *out) {
+#pragma unroll
+        for (int j = 0; j < N / 8; ++j) {
+            float o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = v[8 * j + i];
+            ssd_store_vec<8>(out + 8 * j, o);
+        }
+    };
+    if (p.preact) store(static_cast<__nv_bfloat16 *>(p.preact) + m * p.n + n);
     act_all(v, p.act);
-    const long long ro = m * p.residual_row + n, oo = m * p.out_row + n;
     if (p.residual) {
-        if (!whole) {
-            for (int i = 0; i < 8 && n + i < p.n; ++i) v[i] += load_one(p.residual, ro + i, p.out_type);
-        } else if (p.out_type == SSD_ELT_F32) {
-            SsdRaw<float, 8> r;
-            r.load(static_cast<const float *>(p.residual) + ro);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += r.get(i);
-        } else {
-            SsdRaw<__nv_bfloat16, 8> r;
-            r.load(static_cast<const __nv_bfloat16 *>(p.residual) + ro);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += r.get(i);
-        }
+        for (int i = 0; i < N; ++i) v[i] += r[i / 8].get(i % 8);
     }
-    if (!whole) {
-        for (int i = 0; i < 8 && n + i < p.n; ++i) store_one(p.out, oo + i, p.out_type, v[i]);
-    } else if (p.out_type == SSD_ELT_F32) {
-        ssd_store_vec<8>(static_cast<float *>(p.out) + oo, v);
-    } else {
-        ssd_store_vec<8>(static_cast<__nv_bfloat16 *>(p.out) + oo, v);
-    }
+    store(static_cast<TO *>(p.out) + m * p.out_row + n);
 }
-
-// One value: token m, feature n (lanes are consecutive features).
-__device__ __forceinline__ void finish_one(const SsdProduct &p, long long m, long long n, float v) {
-    if (p.a_scale) v *= __ldg(p.a_scale + m) * __ldg(p.b_scale + n);
-    if (p.bias) v += __ldg(p.bias + n);
-    if (p.preact) store_one(p.preact, m * p.n + n, SSD_ELT_BF16, v);
-    v = ssd_act(v, p.act);
-    if (p.residual) v += load_one(p.residual, m * p.residual_row + n, p.out_type);
-    store_one(p.out, m * p.out_row + n, p.out_type, v);
+template <int N>
+__device__ __forceinline__ void finish(const Args &a, long long m, long long n, float scale,
+                                       float (&v)[N]) {
+    if (a.p.out_type == SSD_ELT_F32) finish_cols<float>(a, m, n, scale, v);
+    else finish_cols<__nv_bfloat16>(a, m, n, scale, v);
 }
 
 // One k block of both operands into a stage.  Coordinates are (k, row) for a
@@ -327,22 +326,25 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a,
                 tc_fence_after();
                 const long long m = (long long)row * kBM + quarter * 32 + lane;
                 const long long n0 = (long long)col * kBN;
-#pragma unroll
+                const float scale = a.p.a_scale && m < a.p.m ? __ldg(a.p.a_scale + m) : 1.f;
+                // one copy of the code for all of a warp's columns: unrolled, the
+                // epilogue outgrows the instruction cache (1320 against 1120 us for
+                // 65536 x 5120 -> 2560)
+#pragma unroll 1
                 for (int c = half * 32; c < kBN; c += 64) {
                     uint32_t r[32];
                     tmem_ld32(tmem + lanes + buf * kBN + c, r);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
-                        float v[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[j + i]);
-                        if (m < a.p.m && n0 + c + j < a.p.n) finish_row8(a, m, n0 + c + j, v);
+                    tmem_ld_wait(r);
+                    if (c + 64 >= kBN) {        // the last of the accumulator has been read
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&ctl->acc_empty[buf]));
                     }
+                    float v[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+                    finish(a, m, n0 + c, scale, v);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&ctl->acc_empty[buf]));
             }
         } else {
             // the partial sums, column by column, over the ring (every copy into
@@ -354,7 +356,7 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a,
                 for (int c = half * 16; c < kBN; c += 32) {
                     uint32_t r[16];
                     tmem_ld16(tmem + lanes + c, r);
-                    tmem_ld_wait();
+                    tmem_ld_wait(r);
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         part[(c + i) * kBM + quarter * 32 + lane] = __uint_as_float(r[i]);
@@ -384,10 +386,11 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a,
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
                         if (k < ranks) v += cluster_ld_f32(peer[k] + (c * kBM + r) * 4);
-                    if (m < a.p.m && n < a.p.n) finish_one(a.p, m, n, v);
+                    if (m < a.p.m && n < a.p.n) ssd_finish(a.p, m, n, v);
                 }
             } else {
                 const long long m = (long long)row * kBM + r;
+                const float scale = a.p.a_scale && m < a.p.m ? __ldg(a.p.a_scale + m) : 1.f;
                 for (int c = (rank * 2 + half) * 8; c < kBN; c += 16 * ranks) {
                     float v[8];
 #pragma unroll
@@ -398,7 +401,7 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a,
                             if (k < ranks) v[i] += cluster_ld_f32(peer[k] + ((c + i) * kBM + r) * 4);
                     }
                     const long long n = (long long)col * kBN + c;
-                    if (m < a.p.m && n < a.p.n) finish_row8(a, m, n, v);
+                    finish(a, m, n, scale, v);
                 }
             }
         }
@@ -448,7 +451,7 @@ cudaError_t launch(const SsdProduct &p, int sms, int ranks, unsigned *err, cudaS
     a.kblocks = (int)((p.k + (kFp8 ? 127 : 63)) / (kFp8 ? 128 : 64));
     const int so = p.out_type == SSD_ELT_F32 ? 4 : 2;
     a.vec = on_16(p.out, p.out_row, so) && (!p.residual || on_16(p.residual, p.residual_row, so)) &&
-            (!p.preact || on_16(p.preact, p.n, 2));
+            (!p.preact || on_16(p.preact, p.n, 2)) && on_16(p.bias, 0, 4) && on_16(p.b_scale, 0, 4);
     a.err = err;
     a.wait_ns = ssd_debug_config().wait_ns;
     CUtensorMap ma, mb;
@@ -474,22 +477,19 @@ cudaError_t launch(const SsdProduct &p, int sms, int ranks, unsigned *err, cudaS
     return cudaLaunchKernelEx(&cfg, kernel, ma, mb, a);
 }
 
-// Ranks of a split: enough clusters to fill the SMs, at least four k blocks a
+// Ranks of a split: as many as the SMs hold at once, at least two k blocks a
 // rank, at most eight (portable cluster size).
 int split_ranks(long long tiles, long long kblocks, int sms) {
-    int r = 1;
-    while (r < 8 && tiles * r * 2 <= sms + sms / 8 && kblocks / (2 * r) >= 4) r *= 2;
-    return r;
+    const long long r = std::min(std::min(sms / tiles, kblocks / 2), 8ll);
+    return r < 1 ? 1 : (int)r;
 }
 
 template <bool kFp8>
 cudaError_t few_tokens(const SsdProduct &p, int sms, unsigned *err, cudaStream_t stream) {
     const long long kb = (p.k + (kFp8 ? 127 : 63)) / (kFp8 ? 128 : 64);
     const int ranks = split_ranks((p.n + kBM - 1) / kBM, kb, sms);
-    if (p.m <= 16) return launch<16, false, false, kFp8, true, true>(p, sms, ranks, err, stream);
     if (p.m <= 32) return launch<32, false, false, kFp8, true, true>(p, sms, ranks, err, stream);
-    if (p.m <= 64) return launch<64, false, false, kFp8, true, true>(p, sms, ranks, err, stream);
-    return launch<128, false, false, kFp8, true, true>(p, sms, ranks, err, stream);
+    return launch<64, false, false, kFp8, true, true>(p, sms, ranks, err, stream);
 }
 
 template <bool kAmn, bool kBmn, bool kFp8>
@@ -525,7 +525,7 @@ cudaError_t ssd_launch_product_tc(const SsdProduct &p, int sms, unsigned *err,
     const bool amn = p.a_row == 1 && p.a_col != 1, bmn = p.b_row == 1 && p.b_col != 1;
     if (amn) return many<true, true, false>(p, sms, err, stream);
     if (bmn) return many<false, true, false>(p, sms, err, stream);
-    const bool few = p.m <= 128;
+    const bool few = p.m <= 64;
     if (p.in == SSD_ELT_E4M3)
         return few ? few_tokens<true>(p, sms, err, stream)
                    : many<false, false, true>(p, sms, err, stream);

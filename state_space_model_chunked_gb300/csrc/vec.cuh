@@ -1,6 +1,6 @@
-// Runs of V consecutive values of an array as fp32 in registers: V = 8, 4 or
-// 2 move as one aligned vector of at most 16 bytes each (the caller has
-// checked the alignment), V = 1 as a scalar.
+// Runs of V consecutive values of an array as fp32 in registers: V = 16, 8, 4
+// or 2 move as aligned vectors of at most 16 bytes each (the caller has checked
+// the alignment), V = 1 as a scalar.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -10,6 +10,8 @@
 
 template <int kBytes>
 struct SsdWord;
+template <>
+struct SsdWord<1> { using type = uint8_t; };
 template <>
 struct SsdWord<2> { using type = uint16_t; };
 template <>
