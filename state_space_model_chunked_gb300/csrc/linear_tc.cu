@@ -19,6 +19,8 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <atomic>
+#include <limits>
 
 #include "act.cuh"
 #include "launch.h"
@@ -347,19 +349,21 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a,
                 }
             }
         } else {
-            // the partial sums, column by column, over the ring (every copy into
+            // the partial sums, four columns a row together, over the ring (every copy into
             // it has been read: the last product waited for them)
             if (wait_warp(&ctl->acc_full[0], 0, ctl, a)) {
                 tc_fence_after();
-                float *part = reinterpret_cast<float *>(smem + kCtrlBytes);
-#pragma unroll
+                float4 *part = reinterpret_cast<float4 *>(smem + kCtrlBytes);
+#pragma unroll 1
                 for (int c = half * 16; c < kBN; c += 32) {
                     uint32_t r[16];
                     tmem_ld16(tmem + lanes + c, r);
                     tmem_ld_wait(r);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        part[(c + i) * kBM + quarter * 32 + lane] = __uint_as_float(r[i]);
+                    for (int i = 0; i < 16; i += 4)
+                        part[(c + i) / 4 * kBM + quarter * 32 + lane] =
+                            make_float4(__uint_as_float(r[i]), __uint_as_float(r[i + 1]),
+                                        __uint_as_float(r[i + 2]), __uint_as_float(r[i + 3]));
                 }
                 tc_fence_before();
             }
@@ -377,31 +381,39 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a,
             uint32_t peer[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) peer[k] = cluster_map(part, k < ranks ? k : 0);
-            if constexpr (kSwap) {
-                // this rank's share of the columns (tokens)
-                const long long n = (long long)row * kBM + r;
-                for (int c = rank * 2 + half; c < kBN; c += 2 * ranks) {
-                    const long long m = (long long)col * kBN + c;
-                    float v = 0.f;
+            // columns c .. c + 3 of this thread's row, summed over the ranks in order
+            const auto sum4 = [&](int c) {
+                float4 q[8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (k < ranks) v += cluster_ld_f32(peer[k] + (c * kBM + r) * 4);
-                    if (m < a.p.m && n < a.p.n) ssd_finish(a.p, m, n, v);
+                for (int k = 0; k < 8; ++k)
+                    if (k < ranks) q[k] = cluster_ld_f32x4(peer[k] + (c / 4 * kBM + r) * 16);
+                float4 v = q[0];
+#pragma unroll
+                for (int k = 1; k < 8; ++k)
+                    if (k < ranks) v.x += q[k].x, v.y += q[k].y, v.z += q[k].z, v.w += q[k].w;
+                return v;
+            };
+            if constexpr (kSwap) {
+                // this rank's share of the columns (tokens), four at a time
+                const long long n = (long long)row * kBM + r;
+#pragma unroll 1
+                for (int c = (rank * 2 + half) * 4; c < kBN; c += 8 * ranks) {
+                    const long long m = (long long)col * kBN + c;
+                    if (m >= a.p.m) break;
+                    const float4 s = sum4(c);
+                    const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (m + i < a.p.m && n < a.p.n) ssd_finish(a.p, m + i, n, v[i]);
                 }
             } else {
                 const long long m = (long long)row * kBM + r;
                 const float scale = a.p.a_scale && m < a.p.m ? __ldg(a.p.a_scale + m) : 1.f;
+#pragma unroll 1
                 for (int c = (rank * 2 + half) * 8; c < kBN; c += 16 * ranks) {
-                    float v[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        v[i] = 0.f;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (k < ranks) v[i] += cluster_ld_f32(peer[k] + ((c + i) * kBM + r) * 4);
-                    }
-                    const long long n = (long long)col * kBN + c;
-                    finish(a, m, n, scale, v);
+                    const float4 lo = sum4(c), hi = sum4(c + 4);
+                    float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                    finish(a, m, (long long)col * kBN + c, scale, v);
                 }
             }
         }
@@ -437,8 +449,32 @@ bool on_16(const void *p, long long stride, int size) {
     return ((uintptr_t)p & 15u) == 0 && (stride * size) % 16 == 0;
 }
 
+// Ranks of a split: the largest cluster of which the device holds one for every
+// tile at once (clusters do not span the SMs' groups, so that is fewer than the
+// SMs over the ranks: with 20 tiles, seven ranks took two waves), of at least two
+// k blocks a rank, at most eight (portable cluster size).
+template <typename Kernel>
+int split_ranks(Kernel kernel, cudaLaunchConfig_t cfg, long long tiles, long long kblocks) {
+    static std::atomic<int> most[9];        // clusters of r CTAs at once, plus one; 0: not asked yet
+    for (int r = 8; r > 1; --r) {
+        if (kblocks < 2 * r) continue;
+        int n = most[r].load(std::memory_order_relaxed) - 1;
+        if (n < 0) {
+            cfg.gridDim = dim3((unsigned)r);
+            cfg.attrs->val.clusterDim.x = r;
+            if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+                (void)cudaGetLastError();
+                n = 0;
+            }
+            most[r].store(n + 1, std::memory_order_relaxed);
+        }
+        if (tiles <= n) return r;
+    }
+    return 1;
+}
+
 template <int kBN, bool kAmn, bool kBmn, bool kFp8, bool kSwap, bool kSplit>
-cudaError_t launch(const SsdProduct &p, int sms, int ranks, unsigned *err, cudaStream_t stream) {
+cudaError_t launch(const SsdProduct &p, int sms, unsigned *err, cudaStream_t stream) {
     constexpr uint32_t kSmem = smem_bytes(kBN);
     const long long rows = kSwap ? p.n : p.m, cols = kSwap ? p.m : p.n;
     const void *rp = kSwap ? p.b : p.a, *cp = kSwap ? p.a : p.b;
@@ -463,46 +499,48 @@ cudaError_t launch(const SsdProduct &p, int sms, int ranks, unsigned *err, cudaS
     if (e != cudaSuccess) return e;
     const long long tiles = (long long)a.row_tiles * a.col_tiles;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(kSplit ? tiles * ranks : (tiles < sms ? tiles : sms)));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kSplit ? ranks : 1;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    attr[0].val.clusterDim.x = attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = kSplit ? 1 : 0;
+    const int ranks = kSplit ? split_ranks(kernel, cfg, tiles, a.kblocks) : 1;
+    attr[0].val.clusterDim.x = ranks;
+    cfg.gridDim = dim3((unsigned)(kSplit ? tiles * ranks : (tiles < sms ? tiles : sms)));
     return cudaLaunchKernelEx(&cfg, kernel, ma, mb, a);
-}
-
-// Ranks of a split: as many as the SMs hold at once, at least two k blocks a
-// rank, at most eight (portable cluster size).
-int split_ranks(long long tiles, long long kblocks, int sms) {
-    const long long r = std::min(std::min(sms / tiles, kblocks / 2), 8ll);
-    return r < 1 ? 1 : (int)r;
 }
 
 template <bool kFp8>
 cudaError_t few_tokens(const SsdProduct &p, int sms, unsigned *err, cudaStream_t stream) {
-    const long long kb = (p.k + (kFp8 ? 127 : 63)) / (kFp8 ? 128 : 64);
-    const int ranks = split_ranks((p.n + kBM - 1) / kBM, kb, sms);
-    if (p.m <= 32) return launch<32, false, false, kFp8, true, true>(p, sms, ranks, err, stream);
-    return launch<64, false, false, kFp8, true, true>(p, sms, ranks, err, stream);
+    if (p.m <= 32) return launch<32, false, false, kFp8, true, true>(p, sms, err, stream);
+    return launch<64, false, false, kFp8, true, true>(p, sms, err, stream);
 }
 
+// Tiles of 128 or of 256 columns, k split or not, by the time each would take: a
+// k block of the narrow tile takes 3/5 of the wide one's (0.20 and 0.34 us in
+// bf16), a split about 10 of the wide one's on top, for its barriers and the
+// exchange of sums; a split has as many ranks as 7/8 of the SMs allow (clusters
+// do not fill all of them), the others ceil(tiles / SMs) rounds.
 template <bool kAmn, bool kBmn, bool kFp8>
 cudaError_t many(const SsdProduct &p, int sms, unsigned *err, cudaStream_t stream) {
+    const long long rt = (p.m + kBM - 1) / kBM;
+    const long long narrow = rt * ((p.n + 127) / 128), wide = rt * ((p.n + 255) / 256);
     const long long kb = (p.k + (kFp8 ? 127 : 63)) / (kFp8 ? 128 : 64);
-    const long long rt = (p.m + kBM - 1) / kBM, ct = (p.n + 127) / 128;
-    // fewer tiles than half the SMs: split k
-    if (rt * ct * 2 <= sms + sms / 8)
-        return launch<128, kAmn, kBmn, kFp8, false, true>(p, sms, split_ranks(rt * ct, kb, sms), err,
-                                                         stream);
-    const long long wide = rt * ((p.n + 255) / 256);
-    if (wide >= sms) return launch<256, kAmn, kBmn, kFp8, false, false>(p, sms, 1, err, stream);
-    return launch<128, kAmn, kBmn, kFp8, false, false>(p, sms, 1, err, stream);
+    const auto rounds = [&](long long tiles) { return (tiles + sms - 1) / sms * kb; };
+    const auto split = [&](long long tiles) {
+        const long long r = std::min({sms * 7ll / 8 / tiles, kb / 2, 8ll});
+        return r < 2 ? std::numeric_limits<long long>::max() / 8 : (kb + r - 1) / r;
+    };
+    const long long t[4] = {3 * rounds(narrow), 5 * rounds(wide), 3 * split(narrow) + 50,
+                            5 * split(wide) + 50};
+    const int best = (int)(std::min_element(t, t + 4) - t);
+    if (best == 0) return launch<128, kAmn, kBmn, kFp8, false, false>(p, sms, err, stream);
+    if (best == 1) return launch<256, kAmn, kBmn, kFp8, false, false>(p, sms, err, stream);
+    if (best == 2) return launch<128, kAmn, kBmn, kFp8, false, true>(p, sms, err, stream);
+    return launch<256, kAmn, kBmn, kFp8, false, true>(p, sms, err, stream);
 }
 
 }  // namespace
