@@ -11,10 +11,27 @@ __device__ __forceinline__ float ssd_sigmoid(float p) {
     return ssdptx::rcp_approx(1.f + ssdptx::ex2_approx(p * -1.44269504f));
 }
 
+// The normal distribution's density at p, and its tail beyond |p|: 1 - Phi(|p|) =
+// (a1 t + a2 t^2 + a3 t^3 + a4 t^4 + a5 t^5) e^(-p^2/2) / 2, t = 1 / (1 + b |p| / sqrt 2),
+// Abramowitz and Stegun's 7.1.26 (error of erf below 1.5e-7).  erff takes three
+// times the instructions and bound the activation's backward pass.
+struct SsdNormal {
+    float density, below;       // below = Phi(p)
+    __device__ __forceinline__ explicit SsdNormal(float p) {
+        const float t = ssdptx::rcp_approx(1.f + 0.3275911f * 0.70710678f * fabsf(p));
+        const float e = ssdptx::ex2_approx(p * p * (-0.5f * 1.44269504f));
+        const float q = 0.5f * e * t *
+                        (0.254829592f +
+                         t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
+        density = 0.39894228f * e;
+        below = p < 0.f ? q : 1.f - q;
+    }
+};
+
 __device__ __forceinline__ float ssd_act(float p, SsdAct act) {
     switch (act) {
         case SsdAct::silu: return p * ssd_sigmoid(p);
-        case SsdAct::gelu: return 0.5f * p * (1.f + erff(p * 0.70710678f));
+        case SsdAct::gelu: return p * SsdNormal(p).below;
         case SsdAct::relu: return p < 0.f ? 0.f : p;
         default: return p;
     }
@@ -26,9 +43,10 @@ __device__ __forceinline__ float ssd_act_slope(float p, SsdAct act) {
             const float sig = ssd_sigmoid(p);
             return sig * (1.f + p * (1.f - sig));
         }
-        case SsdAct::gelu:
-            return 0.5f * (1.f + erff(p * 0.70710678f)) +
-                   p * 0.39894228f * __expf(-0.5f * p * p);
+        case SsdAct::gelu: {
+            const SsdNormal f(p);
+            return f.below + p * f.density;
+        }
         case SsdAct::relu: return p > 0.f ? 1.f : 0.f;
         default: return 1.f;
     }

@@ -241,5 +241,8 @@ struct SsdActBwd {
     void *dp;
     float *dbias;
 };
+// out[j] = the sum of column j over n rows of `width` floats (linear_simt.cu).
+cudaError_t ssd_launch_column_sum(const float *partial, int n, int width, float *out,
+                                  cudaStream_t stream);
 size_t ssd_act_bwd_workspace(long long rows, int width, int sms);
 cudaError_t ssd_launch_act_bwd(const SsdActBwd &a, float *partial, int sms, cudaStream_t stream);

@@ -122,25 +122,22 @@ __global__ void __launch_bounds__(256) act_bwd_kernel(const SsdActBwd a, float *
     }
 }
 
-// out[j] = the sum over n partial rows in a fixed order: 32 x 8 threads take 32
-// columns, each thread row every 8th partial row.
-__global__ void __launch_bounds__(256)
+// out[j] = the sum over n partial rows in a fixed order: 32 x 32 threads take 32
+// columns, each thread row every 32nd partial row.
+__global__ void __launch_bounds__(1024)
 column_sum_kernel(const float *__restrict__ partial, int n, int width, float *__restrict__ out) {
-    __shared__ float part[8][32];
+    __shared__ float part[32][33];
     const int j = blockIdx.x * 32 + threadIdx.x;
-    float s = 0.f;
+    float acc = 0.f;
     if (j < width) {
-#pragma unroll 4
-        for (int r = threadIdx.y; r < n; r += 8) s += partial[(size_t)r * width + j];
+#pragma unroll 8
+        for (int r = threadIdx.y; r < n; r += 32) acc += partial[(size_t)r * width + j];
     }
-    part[threadIdx.y][threadIdx.x] = s;
+    part[threadIdx.y][threadIdx.x] = acc;
     __syncthreads();
-    if (threadIdx.y == 0 && j < width) {
-        s = 0.f;
-#pragma unroll
-        for (int y = 0; y < 8; ++y) s += part[y][threadIdx.x];
-        out[j] = s;
-    }
+    const float v = ssd_warp_sum(part[threadIdx.x][threadIdx.y]);
+    const int jo = blockIdx.x * 32 + threadIdx.y;
+    if (threadIdx.x == 0 && jo < width) out[jo] = v;
 }
 
 // Blocks of rows: eight CTAs an SM, whatever vectors the arrays allow.
@@ -189,7 +186,12 @@ cudaError_t ssd_launch_act_bwd(const SsdActBwd &a, float *partial, int sms, cuda
                               ? launch_act_bwd<float>(a, part, n, stream)
                               : launch_act_bwd<__nv_bfloat16>(a, part, n, stream);
     if (e != cudaSuccess || !a.dbias) return e;
-    column_sum_kernel<<<(unsigned)((a.width + 31) / 32), dim3(32, 8), 0, stream>>>(partial, n,
-                                                                                 a.width, a.dbias);
+    return ssd_launch_column_sum(partial, n, a.width, a.dbias, stream);
+}
+
+cudaError_t ssd_launch_column_sum(const float *partial, int n, int width, float *out,
+                                  cudaStream_t stream) {
+    column_sum_kernel<<<(unsigned)((width + 31) / 32), dim3(32, 32), 0, stream>>>(partial, n, width,
+                                                                                out);
     return cudaGetLastError();
 }

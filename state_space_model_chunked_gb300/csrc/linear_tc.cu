@@ -44,7 +44,6 @@ constexpr uint32_t stage_bytes(int bn) { return kABytes + bn * kRowBytes; }
 constexpr int stages(int bn) {
     return kRingBytes / stage_bytes(bn) < kMaxStages ? kRingBytes / stage_bytes(bn) : kMaxStages;
 }
-constexpr uint32_t smem_bytes(int bn) { return kCtrlBytes + stages(bn) * stage_bytes(bn); }
 constexpr uint32_t tmem_cols(int bn, bool split) {
     const int want = split ? bn : 2 * bn;
     return want <= 32 ? 32 : want <= 64 ? 64 : want <= 128 ? 128 : want <= 256 ? 256 : 512;
@@ -86,10 +85,10 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Ctrl *
     return __all_sync(0xffffffffu, wait(bar, parity, ctl, a));
 }
 
-// Tiles in groups of 16 row tiles, column by column: the CTAs that run at one
+// Tiles in groups of 8 row tiles, column by column: the CTAs that run at one
 // time share rows of both operands in L2.
 __device__ __forceinline__ void tile_at(const Args &a, int t, int &row, int &col) {
-    constexpr int kGroup = 16;
+    constexpr int kGroup = 8;
     const int per = kGroup * a.col_tiles, g = t / per, first = g * kGroup;
     const int rows = min(kGroup, a.row_tiles - first);
     row = first + (t - g * per) % rows;
@@ -111,8 +110,31 @@ __device__ __forceinline__ void act_all(float (&v)[N], SsdAct act) {
     }
 }
 
-__device__ __forceinline__ float4 cols4(const float *p, long long n) {
-    return __ldg(reinterpret_cast<const float4 *>(p + n));
+// The bias and scale of a warp's half of a tile's columns (32 of every 64), in
+// shared memory of its own, so that no barrier stands between it and the others.
+struct Columns {
+    float bias[128], scale[128];
+};
+constexpr uint32_t kColumnBytes = kEpiWarps * sizeof(Columns);
+constexpr uint32_t smem_bytes(int bn) {
+    return kCtrlBytes + stages(bn) * stage_bytes(bn) + kColumnBytes;
+}
+
+// The warp fetches its columns before the tile's products are complete; zeros past
+// the last column.
+template <int kBN>
+__device__ __forceinline__ void fetch_columns(const Args &a, Columns *cols, int half, long long n0) {
+    if (!a.p.bias && !a.p.a_scale) return;
+    const int lane = threadIdx.x & 31;
+    __syncwarp();               // the tile before has been read
+#pragma unroll
+    for (int k = 0; k < kBN / 64; ++k) {
+        const long long n = n0 + half * 32 + k * 64 + lane;
+        const bool in = n < a.p.n;
+        cols->bias[k * 32 + lane] = a.p.bias && in ? __ldg(a.p.bias + n) : 0.f;
+        cols->scale[k * 32 + lane] = a.p.a_scale && in ? __ldg(a.p.b_scale + n) : 0.f;
+    }
+    __syncwarp();
 }
 
 // One value, for the edges: out of line, so the epilogue's code stays small.
@@ -120,61 +142,178 @@ __device__ __noinline__ void finish_edge(const SsdProduct &p, long long m, long 
     if (m < p.m && n < p.n) ssd_finish(p, m, n, v);
 }
 
-// N columns n .. n + N - 1 of row m.  Rows of 16-byte vectors and all columns in
-// range: whole vectors, the residual's asked for first; else value by value.
+// N columns n .. n + N - 1 of row m, their bias and scale at `bias` and `scale`.
+// Rows of 16-byte vectors and all columns in range: whole vectors; else value by
+// value.  `r`: the residual's values, if whole.
 template <typename TO, int N>
-__device__ __forceinline__ void finish_cols(const Args &a, long long m, long long n, float scale,
-                                            float (&v)[N]) {
-    const SsdProduct &p = a.p;
-    if (!a.vec || n + N > p.n) {
+struct RowPart {
+    SsdRaw<TO, 8> residual[N / 8];
+    bool whole;
+    __device__ __forceinline__ void ask(const Args &a, long long m, long long n) {
+        whole = a.vec && n + N <= a.p.n;
+        if (!whole || m >= a.p.m || !a.p.residual) return;
+        const TO *res = static_cast<const TO *>(a.p.residual) + m * a.p.residual_row + n;
 #pragma unroll
-        for (int i = 0; i < N; ++i) finish_edge(p, m, n + i, v[i]);
-        return;
+        for (int j = 0; j < N / 8; ++j) residual[j].load(res + 8 * j);
     }
-    if (m >= p.m) return;
-    const TO *res = static_cast<const TO *>(p.residual) + m * p.residual_row + n;
-    SsdRaw<TO, 8> r[N / 8];
-    if (p.residual) {
+    __device__ __forceinline__ void finish(const Args &a, long long m, long long n, float row_scale,
+                                           const float *bias, const float *scale, float (&v)[N]) {
+        const SsdProduct &p = a.p;
+        if (!whole) {
 #pragma unroll
-        for (int j = 0; j < N / 8; ++j) r[j].load(res + 8 * j);
-    }
-    if (p.a_scale) {
-#pragma unroll
-        for (int j = 0; j < N; j += 4) {
-            const float4 s = cols4(p.b_scale, n + j);
-            v[j] *= scale * s.x, v[j + 1] *= scale * s.y;
-            v[j + 2] *= scale * s.z, v[j + 3] *= scale * s.w;
+            for (int i = 0; i < N; ++i) finish_edge(p, m, n + i, v[i]);
+            return;
         }
-    }
-    if (p.bias) {
+        if (m >= p.m) return;
+        if (p.a_scale) {
 #pragma unroll
-        for (int j = 0; j < N; j += 4) {
-            const float4 b = cols4(p.bias, n + j);
-            v[j] += b.x, v[j + 1] += b.y, v[j + 2] += b.z, v[j + 3] += b.w;
+            for (int j = 0; j < N; j += 4) {
+                const float4 s = *reinterpret_cast<const float4 *>(scale + j);
+                v[j] *= row_scale * s.x, v[j + 1] *= row_scale * s.y;
+                v[j + 2] *= row_scale * s.z, v[j + 3] *= row_scale * s.w;
+            }
         }
-    }
-    const auto store = [&](auto *out) {
+        if (p.bias) {
 #pragma unroll
-        for (int j = 0; j < N / 8; ++j) {
-            float o[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = v[8 * j + i];
-            ssd_store_vec<8>(out + 8 * j, o);
+            for (int j = 0; j < N; j += 4) {
+                const float4 b = *reinterpret_cast<const float4 *>(bias + j);
+                v[j] += b.x, v[j + 1] += b.y, v[j + 2] += b.z, v[j + 3] += b.w;
+            }
         }
-    };
-    if (p.preact) store(static_cast<__nv_bfloat16 *>(p.preact) + m * p.n + n);
-    act_all(v, p.act);
-    if (p.residual) {
+        const auto store = [&](auto *out) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += r[i / 8].get(i % 8);
+            for (int j = 0; j < N / 8; ++j) {
+                float o[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = v[8 * j + i];
+                ssd_store_vec<8>(out + 8 * j, o);
+            }
+        };
+        if (p.preact) store(static_cast<__nv_bfloat16 *>(p.preact) + m * p.n + n);
+        act_all(v, p.act);
+        if (p.residual) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += residual[i / 8].get(i % 8);
+        }
+        store(static_cast<TO *>(p.out) + m * p.out_row + n);
     }
-    store(static_cast<TO *>(p.out) + m * p.out_row + n);
+};
+
+// A warp's half of the columns of an accumulator tile (acc: the tile's first
+// column in the warp's lanes) to global memory, row m of the output a lane.
+// `ready` waits for the accumulator, `read` runs once it may be written again.
+// One copy of the code for all columns: unrolled, the epilogue outgrows the
+// instruction cache (1320 against 1120 us for 65536 x 5120 -> 2560).  Laying the
+// rows out in shared memory for coalesced stores took longer, not shorter (1000
+// against 977 us): the products keep shared memory busy.
+template <typename TO, int kBN, typename F, typename G>
+__device__ __forceinline__ bool drain(const Args &a, const Columns *cols, uint32_t acc, int half,
+                                      long long m, long long n0, F &&ready, G &&read) {
+    const float scale = a.p.a_scale && m < a.p.m ? __ldg(a.p.a_scale + m) : 1.f;
+    RowPart<TO, 32> part;
+    part.ask(a, m, n0 + half * 32);
+    if (!ready()) return false;
+    tc_fence_after();
+#pragma unroll 1
+    for (int c = half * 32; c < kBN; c += 64) {
+        if (c >= 64) part.ask(a, m, n0 + c);
+        uint32_t r[32];
+        tmem_ld32(acc + c, r);
+        tmem_ld_wait(r);
+        if (c + 64 >= kBN) {
+            tc_fence_before();
+            __syncwarp();
+            read();
+        }
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+        part.finish(a, m, n0 + c, scale, cols->bias + c / 64 * 32, cols->scale + c / 64 * 32, v);
+    }
+    return true;
 }
-template <int N>
-__device__ __forceinline__ void finish(const Args &a, long long m, long long n, float scale,
-                                       float (&v)[N]) {
-    if (a.p.out_type == SSD_ELT_F32) finish_cols<float>(a, m, n, scale, v);
-    else finish_cols<__nv_bfloat16>(a, m, n, scale, v);
+template <int kBN, typename F, typename G>
+__device__ __forceinline__ bool drain_accumulator(const Args &a, Columns *cols, uint32_t acc,
+                                                  int half, long long m, long long n0, F &&ready,
+                                                  G &&read) {
+    fetch_columns<kBN>(a, cols, half, n0);
+    return a.p.out_type == SSD_ELT_F32
+               ? drain<float, kBN>(a, cols, acc, half, m, n0, ready, read)
+               : drain<__nv_bfloat16, kBN>(a, cols, acc, half, m, n0, ready, read);
+}
+
+// ------------------------------------------------------------ split of k: the exchange
+// A rank's partial sums over the ring, four columns of a row together: column c of
+// row r is component c % 4 of vector c / 4 * kBM + r, so that a warp's accesses,
+// here and in another rank's shared memory, are whole vectors without conflicts.
+template <int kBN>
+__device__ __forceinline__ void store_sums(uint8_t *ring, uint32_t acc, int r, int half) {
+    float4 *part = reinterpret_cast<float4 *>(ring);
+    tc_fence_after();
+#pragma unroll 1
+    for (int c = half * 16; c < kBN; c += 32) {
+        uint32_t v[16];
+        tmem_ld16(acc + c, v);
+        tmem_ld_wait(v);
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+            part[(c + i) / 4 * kBM + r] =
+                make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]),
+                            __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
+    }
+    tc_fence_before();
+}
+
+// Rank `rank` of `ranks` adds its share of the columns over all ranks, in order,
+// and finishes them.  Rank k's sums lie at `ring` in the cluster's CTA
+// k * stride + offset.  r: this thread's row of the tile, m0 and n0 its first row
+// and column (with kSwap: first feature and token).
+template <int kBN, bool kSwap>
+__device__ __forceinline__ void finish_split(const Args &a, uint32_t ring, int r, int half,
+                                             int rank, int ranks, int stride, int offset,
+                                             long long row0, long long col0) {
+    uint32_t peer[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) peer[k] = cluster_map(ring, (k < ranks ? k : 0) * stride + offset);
+    const auto sum4 = [&](int c) {
+        float4 q[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < ranks) q[k] = cluster_ld_f32x4(peer[k] + (c / 4 * kBM + r) * 16);
+        float4 v = q[0];
+#pragma unroll
+        for (int k = 1; k < 8; ++k)
+            if (k < ranks) v.x += q[k].x, v.y += q[k].y, v.z += q[k].z, v.w += q[k].w;
+        return v;
+    };
+    if constexpr (kSwap) {
+        const long long n = row0 + r;
+#pragma unroll 1
+        for (int c = (rank * 2 + half) * 4; c < kBN; c += 8 * ranks) {
+            const long long m = col0 + c;
+            if (m >= a.p.m) break;
+            const float4 s = sum4(c);
+            const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (m + i < a.p.m && n < a.p.n) ssd_finish(a.p, m + i, n, v[i]);
+        }
+    } else {
+        const long long m = row0 + r;
+        const float scale = a.p.a_scale && m < a.p.m ? __ldg(a.p.a_scale + m) : 1.f;
+#pragma unroll 1
+        for (int c = (rank * 2 + half) * 8; c < kBN; c += 16 * ranks) {
+            const long long n = col0 + c;
+            const float4 lo = sum4(c), hi = sum4(c + 4);
+            float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            const auto last = [&](auto part) {
+                part.ask(a, m, n);
+                part.finish(a, m, n, scale, a.p.bias + n, a.p.b_scale + n, v);
+            };
+            if (a.p.out_type == SSD_ELT_F32) last(RowPart<float, 8>{});
+            else last(RowPart<__nv_bfloat16, 8>{});
+        }
+    }
 }
 
 // One k block of both operands into a stage.  Coordinates are (k, row) for a
@@ -318,104 +457,38 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a,
         // of a quarter share its columns
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        Columns *cols =
+            reinterpret_cast<Columns *>(smem + kCtrlBytes + kStages * kStage) + (warp - 2);
         if constexpr (!kSplit) {
             uint32_t tiles = 0;
             for (int t = first; t < ntiles; t += step, ++tiles) {
                 const uint32_t buf = tiles & 1, turn = tiles >> 1;
                 int row, col;
                 tile_at(a, t, row, col);
-                if (!wait_warp(&ctl->acc_full[buf], turn & 1, ctl, a)) break;
-                tc_fence_after();
-                const long long m = (long long)row * kBM + quarter * 32 + lane;
-                const long long n0 = (long long)col * kBN;
-                const float scale = a.p.a_scale && m < a.p.m ? __ldg(a.p.a_scale + m) : 1.f;
-                // one copy of the code for all of a warp's columns: unrolled, the
-                // epilogue outgrows the instruction cache (1320 against 1120 us for
-                // 65536 x 5120 -> 2560)
-#pragma unroll 1
-                for (int c = half * 32; c < kBN; c += 64) {
-                    uint32_t r[32];
-                    tmem_ld32(tmem + lanes + buf * kBN + c, r);
-                    tmem_ld_wait(r);
-                    if (c + 64 >= kBN) {        // the last of the accumulator has been read
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&ctl->acc_empty[buf]));
-                    }
-                    float v[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-                    finish(a, m, n0 + c, scale, v);
-                }
+                if (!drain_accumulator<kBN>(
+                        a, cols, tmem + lanes + buf * kBN, half,
+                        (long long)row * kBM + quarter * 32 + lane, (long long)col * kBN,
+                        [&]() { return wait_warp(&ctl->acc_full[buf], turn & 1, ctl, a); },
+                        [&]() {
+                            if (lane == 0) mbar_arrive(smem_u32(&ctl->acc_empty[buf]));
+                        }))
+                    break;
             }
         } else {
-            // the partial sums, four columns a row together, over the ring (every copy into
-            // it has been read: the last product waited for them)
-            if (wait_warp(&ctl->acc_full[0], 0, ctl, a)) {
-                tc_fence_after();
-                float4 *part = reinterpret_cast<float4 *>(smem + kCtrlBytes);
-#pragma unroll 1
-                for (int c = half * 16; c < kBN; c += 32) {
-                    uint32_t r[16];
-                    tmem_ld16(tmem + lanes + c, r);
-                    tmem_ld_wait(r);
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4)
-                        part[(c + i) / 4 * kBM + quarter * 32 + lane] =
-                            make_float4(__uint_as_float(r[i]), __uint_as_float(r[i + 1]),
-                                        __uint_as_float(r[i + 2]), __uint_as_float(r[i + 3]));
-                }
-                tc_fence_before();
-            }
+            // every copy into the ring has been read: the last product waited for them
+            if (wait_warp(&ctl->acc_full[0], 0, ctl, a))
+                store_sums<kBN>(smem + kCtrlBytes, tmem + lanes, quarter * 32 + lane, half);
         }
     }
     if constexpr (kSplit) {
         __syncwarp();
         cluster_sync_all();
         if (warp >= 2 && !ctl->abort) {
-            const int quarter = warp & 3, half = (warp - 2) >> 2;
-            const int r = quarter * 32 + lane;
             int row, col;
             tile_at(a, first, row, col);
-            const uint32_t part = smem_u32(smem) + kCtrlBytes;
-            uint32_t peer[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) peer[k] = cluster_map(part, k < ranks ? k : 0);
-            // columns c .. c + 3 of this thread's row, summed over the ranks in order
-            const auto sum4 = [&](int c) {
-                float4 q[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (k < ranks) q[k] = cluster_ld_f32x4(peer[k] + (c / 4 * kBM + r) * 16);
-                float4 v = q[0];
-#pragma unroll
-                for (int k = 1; k < 8; ++k)
-                    if (k < ranks) v.x += q[k].x, v.y += q[k].y, v.z += q[k].z, v.w += q[k].w;
-                return v;
-            };
-            if constexpr (kSwap) {
-                // this rank's share of the columns (tokens), four at a time
-                const long long n = (long long)row * kBM + r;
-#pragma unroll 1
-                for (int c = (rank * 2 + half) * 4; c < kBN; c += 8 * ranks) {
-                    const long long m = (long long)col * kBN + c;
-                    if (m >= a.p.m) break;
-                    const float4 s = sum4(c);
-                    const float v[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (m + i < a.p.m && n < a.p.n) ssd_finish(a.p, m + i, n, v[i]);
-                }
-            } else {
-                const long long m = (long long)row * kBM + r;
-                const float scale = a.p.a_scale && m < a.p.m ? __ldg(a.p.a_scale + m) : 1.f;
-#pragma unroll 1
-                for (int c = (rank * 2 + half) * 8; c < kBN; c += 16 * ranks) {
-                    const float4 lo = sum4(c), hi = sum4(c + 4);
-                    float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-                    finish(a, m, (long long)col * kBN + c, scale, v);
-                }
-            }
+            finish_split<kBN, kSwap>(a, smem_u32(smem) + kCtrlBytes, (warp & 3) * 32 + lane,
+                                     (warp - 2) >> 2, rank, ranks, 1, 0, (long long)row * kBM,
+                                     (long long)col * kBN);
         }
         __syncwarp();
         cluster_sync_all();     // nobody leaves while its sums are being read
@@ -424,6 +497,181 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a,
     tc_fence_before();
     __syncthreads();
     if (warp == 1) tmem_dealloc(tmem, kCols);
+}
+
+// A pair of CTAs computes tiles of 256 x 256: each brings its 128 rows of A and of
+// B, so an SM takes in 32 KB of operands a k block where a 128 x 256 tile of its
+// own takes 48: the SM's 64 bytes a clock from L2 then last as long as the products
+// (512 clocks a block), instead of half as long again.  The even CTA's issuer
+// multiplies for both; its `full` barriers count both CTAs' bytes, its
+// `acc_empty` ones both CTAs' epilogue warps.
+constexpr int kPairBN = 256;
+constexpr uint32_t kPairStage = 2 * kABytes;
+constexpr int kPairStages = kRingBytes / kPairStage;
+static_assert(kPairStages <= kMaxStages, "stages");
+
+template <bool kAmn, bool kBmn, bool kFp8, bool kSplit>
+__global__ void __launch_bounds__(kThreads, 1)
+product_pair_kernel(const __grid_constant__ CUtensorMap map_a,
+                    const __grid_constant__ CUtensorMap map_b, const __grid_constant__ Args a) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    constexpr int kK = kFp8 ? 128 : 64;
+    Ctrl *ctl = reinterpret_cast<Ctrl *>(smem);
+    const uint32_t ring = smem_u32(smem) + kCtrlBytes;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // the pair's place in the cluster (its part of k), this CTA's in the pair
+    const int in_cluster = (int)cluster_rank(), leader = in_cluster & ~1, rank = in_cluster & 1;
+    const int part = in_cluster / 2, parts = kSplit ? (int)cluster_size() / 2 : 1;
+    const bool misplaced = (ring & 1023u) != 0u;    // the same in every CTA of the grid
+    if (misplaced) {
+        if (threadIdx.x == 0) ssd_report(a.err, SSD_DEVERR_SMEM_ALIGN);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kPairStages; ++i) {
+            mbar_init(smem_u32(&ctl->full[i]), 1);
+            mbar_init(smem_u32(&ctl->empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&ctl->acc_full[i]), 1);
+            mbar_init(smem_u32(&ctl->acc_empty[i]), 2 * kEpiWarps);
+        }
+        mbar_init(smem_u32(&ctl->drain), 1);
+        ctl->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(&ctl->tmem), 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();         // both CTAs' barriers and tensor memory stand
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem;
+    const int ntiles = a.row_tiles * a.col_tiles, step = kSplit ? ntiles : (int)gridDim.x / 2;
+    const int first = blockIdx.x / (2 * parts);
+    const int kb0 = (int)((long long)a.kblocks * part / parts);
+    const int kb1 = (int)((long long)a.kblocks * (part + 1) / parts);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            tma_prefetch_desc(&map_a);
+            tma_prefetch_desc(&map_b);
+            uint32_t n = 0;
+            bool ok = true;
+            for (int t = first; ok && t < ntiles; t += step) {
+                int row, col;
+                tile_at(a, t, row, col);
+                const int ar = row * 256 + rank * 128, br = col * 256 + rank * 128;
+                for (int kb = kSplit ? kb0 : 0; kb < (kSplit ? kb1 : a.kblocks); ++kb, ++n) {
+                    const uint32_t s = n % kPairStages, turn = n / kPairStages;
+                    if (turn > 0 && !wait(&ctl->empty[s], (turn - 1) & 1, ctl, a)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t own = smem_u32(&ctl->full[s]), bar = cluster_map(own, leader);
+                    const uint32_t dst = ring + s * kPairStage;
+                    if (rank == 0) mbar_arrive_expect_tx(own, 2 * kPairStage);
+                    if constexpr (kAmn) {
+                        tma_load_2d_pair(dst, &map_a, bar, ar, kb * kK);
+                        tma_load_2d_pair(dst + 8192, &map_a, bar, ar + 64, kb * kK);
+                    } else {
+                        tma_load_2d_pair(dst, &map_a, bar, kb * kK, ar);
+                    }
+                    if constexpr (kBmn) {
+                        tma_load_2d_pair(dst + kABytes, &map_b, bar, br, kb * kK);
+                        tma_load_2d_pair(dst + kABytes + 8192, &map_b, bar, br + 64, kb * kK);
+                    } else {
+                        tma_load_2d_pair(dst + kABytes, &map_b, bar, kb * kK, br);
+                    }
+                }
+            }
+            if (!ok && rank == 0) {     // let both CTAs' copies in flight land
+                for (uint32_t i = n > kPairStages ? n - kPairStages : 0; i < n; ++i)
+                    mbar_wait(smem_u32(&ctl->full[i % kPairStages]), (i / kPairStages) & 1, a.wait_ns);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            constexpr uint32_t kId = kFp8 ? idesc_e4m3_f32(256, kPairBN)
+                                          : idesc_bf16_f32(256, kPairBN, kAmn, kBmn);
+            const uint64_t ad = smem_desc(ring, kAmn ? 8192 : 16, 1024, kSwizzle128B);
+            const uint64_t bd = smem_desc(ring + kABytes, kBmn ? 8192 : 16, 1024, kSwizzle128B);
+            constexpr uint64_t kAStep = kAmn ? 2048 >> 4 : 32 >> 4;
+            constexpr uint64_t kBStep = kBmn ? 2048 >> 4 : 32 >> 4;
+            const uint16_t both = (uint16_t)(3u << leader);
+            uint32_t n = 0, tiles = 0;
+            bool ok = true;
+            for (int t = first; ok && t < ntiles; t += step, ++tiles) {
+                const uint32_t buf = tiles & 1, turn = tiles >> 1;
+                const uint32_t d = tmem + buf * kPairBN;
+                if (turn > 0 && !wait(&ctl->acc_empty[buf], (turn - 1) & 1, ctl, a)) break;
+                tc_fence_after();
+                for (int kb = kSplit ? kb0 : 0; kb < (kSplit ? kb1 : a.kblocks); ++kb, ++n) {
+                    const uint32_t s = n % kPairStages;
+                    if (!wait(&ctl->full[s], (n / kPairStages) & 1, ctl, a)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t off = (uint64_t)(s * kPairStage) >> 4;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        mma_ss_pair<kFp8>(d, ad + off + i * kAStep, bd + off + i * kBStep, kId,
+                                          kb > (kSplit ? kb0 : 0) || i > 0);
+                    mma_commit_pair(smem_u32(&ctl->empty[s]), both);
+                }
+                if (ok) mma_commit_pair(smem_u32(&ctl->acc_full[buf]), both);
+            }
+            // every product has ended before the accumulators are freed
+            mma_commit_pair(smem_u32(&ctl->drain), both);
+            mbar_wait(smem_u32(&ctl->drain), 0, a.wait_ns);
+        }
+    } else {
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        Columns *cols =
+            reinterpret_cast<Columns *>(smem + kCtrlBytes + kPairStages * kPairStage) + (warp - 2);
+        if constexpr (kSplit) {
+            if (wait_warp(&ctl->acc_full[0], 0, ctl, a))
+                store_sums<kPairBN>(smem + kCtrlBytes, tmem + lanes, quarter * 32 + lane, half);
+        }
+        uint32_t tiles = 0;
+        for (int t = first; !kSplit && t < ntiles; t += step, ++tiles) {
+            const uint32_t buf = tiles & 1, turn = tiles >> 1;
+            int row, col;
+            tile_at(a, t, row, col);
+            if (!drain_accumulator<kPairBN>(
+                    a, cols, tmem + lanes + buf * kPairBN, half,
+                    (long long)row * 256 + rank * 128 + quarter * 32 + lane,
+                    (long long)col * kPairBN,
+                    [&]() { return wait_warp(&ctl->acc_full[buf], turn & 1, ctl, a); },
+                    [&]() {
+                        if (lane == 0)
+                            mbar_arrive_cluster(cluster_map(smem_u32(&ctl->acc_empty[buf]), leader));
+                    }))
+                break;
+        }
+    }
+    if constexpr (kSplit) {
+        __syncwarp();
+        cluster_sync_all();
+        if (warp >= 2 && !ctl->abort) {
+            int row, col;
+            tile_at(a, first, row, col);
+            finish_split<kPairBN, false>(a, smem_u32(smem) + kCtrlBytes, (warp & 3) * 32 + lane,
+                                         (warp - 2) >> 2, part, parts, 2, rank,
+                                         (long long)row * 256 + rank * 128,
+                                         (long long)col * kPairBN);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync_all();         // no CTA leaves while others use its barriers, operands or sums
+    if (warp == 1) tmem_dealloc_pair(tmem, 512);
+    __syncwarp();
+    cluster_sync_all();         // nor before both have freed the tensor memory they share
 }
 
 // ------------------------------------------------------------------ host
@@ -449,27 +697,45 @@ bool on_16(const void *p, long long stride, int size) {
     return ((uintptr_t)p & 15u) == 0 && (stride * size) % 16 == 0;
 }
 
-// Ranks of a split: the largest cluster of which the device holds one for every
-// tile at once (clusters do not span the SMs' groups, so that is fewer than the
-// SMs over the ranks: with 20 tiles, seven ranks took two waves), of at least two
-// k blocks a rank, at most eight (portable cluster size).
-template <typename Kernel>
-int split_ranks(Kernel kernel, cudaLaunchConfig_t cfg, long long tiles, long long kblocks) {
-    static std::atomic<int> most[9];        // clusters of r CTAs at once, plus one; 0: not asked yet
-    for (int r = 8; r > 1; --r) {
-        if (kblocks < 2 * r) continue;
-        int n = most[r].load(std::memory_order_relaxed) - 1;
-        if (n < 0) {
-            cfg.gridDim = dim3((unsigned)r);
-            cfg.attrs->val.clusterDim.x = r;
-            if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
-                (void)cudaGetLastError();
-                n = 0;
-            }
-            most[r].store(n + 1, std::memory_order_relaxed);
-        }
-        if (tiles <= n) return r;
+Args args_of(const SsdProduct &p, int bm, int bn, bool fp8, unsigned *err) {
+    Args a{};
+    a.p = p;
+    a.row_tiles = (int)((p.m + bm - 1) / bm);
+    a.col_tiles = (int)((p.n + bn - 1) / bn);
+    a.kblocks = (int)((p.k + (fp8 ? 127 : 63)) / (fp8 ? 128 : 64));
+    const int so = p.out_type == SSD_ELT_F32 ? 4 : 2;
+    a.vec = on_16(p.out, p.out_row, so) && (!p.residual || on_16(p.residual, p.residual_row, so)) &&
+            (!p.preact || on_16(p.preact, p.n, 2)) && on_16(p.bias, 0, 4) && on_16(p.b_scale, 0, 4);
+    a.err = err;
+    a.wait_ns = ssd_debug_config().wait_ns;
+    return a;
+}
+
+using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const Args);
+
+// Clusters of r CTAs that the device holds at once.  They do not span the SMs'
+// groups, so that can be fewer than the SMs over r.  Every kernel here takes an
+// SM to itself, so one answer serves them all; it is asked for once.
+int clusters_at_once(Kernel kernel, cudaLaunchConfig_t cfg, int r) {
+    static std::atomic<int> known[9];       // the answer plus one; 0: not asked yet
+    int n = known[r].load(std::memory_order_relaxed) - 1;
+    if (n >= 0) return n;
+    cfg.gridDim = dim3((unsigned)r);
+    cfg.attrs->val.clusterDim.x = r;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        n = 0;
     }
+    known[r].store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
+// Ranks of a split: the largest cluster of which there is one for every tile at
+// once (with 20 tiles, seven ranks took two waves), of at least two k blocks a
+// rank, at most eight (portable cluster size).
+int split_ranks(Kernel kernel, const cudaLaunchConfig_t &cfg, long long tiles, long long kblocks) {
+    for (int r = 8; r > 1; --r)
+        if (kblocks >= 2 * r && tiles <= clusters_at_once(kernel, cfg, r)) return r;
     return 1;
 }
 
@@ -480,16 +746,11 @@ cudaError_t launch(const SsdProduct &p, int sms, unsigned *err, cudaStream_t str
     const void *rp = kSwap ? p.b : p.a, *cp = kSwap ? p.a : p.b;
     const long long rs = kSwap ? p.b_row : (kAmn ? p.a_col : p.a_row);
     const long long cs = kSwap ? p.a_row : (kBmn ? p.b_col : p.b_row);
-    Args a{};
-    a.p = p;
-    a.row_tiles = (int)((rows + kBM - 1) / kBM);
-    a.col_tiles = (int)((cols + kBN - 1) / kBN);
-    a.kblocks = (int)((p.k + (kFp8 ? 127 : 63)) / (kFp8 ? 128 : 64));
-    const int so = p.out_type == SSD_ELT_F32 ? 4 : 2;
-    a.vec = on_16(p.out, p.out_row, so) && (!p.residual || on_16(p.residual, p.residual_row, so)) &&
-            (!p.preact || on_16(p.preact, p.n, 2)) && on_16(p.bias, 0, 4) && on_16(p.b_scale, 0, 4);
-    a.err = err;
-    a.wait_ns = ssd_debug_config().wait_ns;
+    Args a = args_of(p, kBM, kBN, kFp8, err);
+    if (kSwap) {
+        a.row_tiles = (int)((rows + kBM - 1) / kBM);
+        a.col_tiles = (int)((cols + kBN - 1) / kBN);
+    }
     CUtensorMap ma, mb;
     if (!operand_map(&ma, rp, kFp8, kAmn, rows, p.k, rs, kBM) ||
         !operand_map(&mb, cp, kFp8, kBmn, cols, p.k, cs, kBN))
@@ -513,34 +774,76 @@ cudaError_t launch(const SsdProduct &p, int sms, unsigned *err, cudaStream_t str
     return cudaLaunchKernelEx(&cfg, kernel, ma, mb, a);
 }
 
+template <bool kAmn, bool kBmn, bool kFp8, bool kSplit>
+cudaError_t launch_pair(const SsdProduct &p, unsigned *err, cudaStream_t stream) {
+    constexpr uint32_t kSmem = kCtrlBytes + kPairStages * kPairStage + kColumnBytes;
+    Args a = args_of(p, 256, kPairBN, kFp8, err);
+    CUtensorMap ma, mb;
+    if (!operand_map(&ma, p.a, kFp8, kAmn, p.m, p.k, kAmn ? p.a_col : p.a_row, kBM) ||
+        !operand_map(&mb, p.b, kFp8, kBmn, p.n, p.k, kBmn ? p.b_col : p.b_row, 128))
+        return cudaErrorInvalidValue;
+    const auto kernel = product_pair_kernel<kAmn, kBmn, kFp8, kSplit>;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const long long tiles = (long long)a.row_tiles * a.col_tiles;
+    if (kSplit) {
+        int parts = 4;
+        while (parts > 1 && (a.kblocks < 2 * parts || tiles > clusters_at_once(kernel, cfg, 2 * parts)))
+            --parts;
+        attr[0].val.clusterDim.x = 2 * parts;
+        cfg.gridDim = dim3((unsigned)(2 * parts * tiles));
+    } else {
+        const long long pairs = std::max(1, clusters_at_once(kernel, cfg, 2));
+        attr[0].val.clusterDim.x = 2;
+        cfg.gridDim = dim3((unsigned)(2 * std::min(tiles, pairs)));
+    }
+    return cudaLaunchKernelEx(&cfg, kernel, ma, mb, a);
+}
+
 template <bool kFp8>
 cudaError_t few_tokens(const SsdProduct &p, int sms, unsigned *err, cudaStream_t stream) {
     if (p.m <= 32) return launch<32, false, false, kFp8, true, true>(p, sms, err, stream);
     return launch<64, false, false, kFp8, true, true>(p, sms, err, stream);
 }
 
-// Tiles of 128 or of 256 columns, k split or not, by the time each would take: a
-// k block of the narrow tile takes 3/5 of the wide one's (0.20 and 0.34 us in
-// bf16), a split about 10 of the wide one's on top, for its barriers and the
-// exchange of sums; a split has as many ranks as 7/8 of the SMs allow (clusters
-// do not fill all of them), the others ceil(tiles / SMs) rounds.
+// Tiles of 128 x 128 or pairs' 256 x 256, whole or with k split, by the time each
+// would take, in units of 64 ns.  A k block takes as long as its operands take into
+// the SM, 32 KB for either: 4 units; the epilogue of a tile, which the next tile's
+// products hide if they last as long, about 20 and 40; a split's barriers and
+// exchange of sums 50.  Whole tiles run in rounds of as many
+// as the SMs take; a split has as many ranks as 7/8 of the SMs allow (clusters do
+// not fill all of them).
 template <bool kAmn, bool kBmn, bool kFp8>
 cudaError_t many(const SsdProduct &p, int sms, unsigned *err, cudaStream_t stream) {
-    const long long rt = (p.m + kBM - 1) / kBM;
-    const long long narrow = rt * ((p.n + 127) / 128), wide = rt * ((p.n + 255) / 256);
-    const long long kb = (p.k + (kFp8 ? 127 : 63)) / (kFp8 ? 128 : 64);
-    const auto rounds = [&](long long tiles) { return (tiles + sms - 1) / sms * kb; };
-    const auto split = [&](long long tiles) {
-        const long long r = std::min({sms * 7ll / 8 / tiles, kb / 2, 8ll});
-        return r < 2 ? std::numeric_limits<long long>::max() / 8 : (kb + r - 1) / r;
+    const auto tiles = [&](int rows, int cols) {
+        return (p.m + rows - 1) / rows * ((p.n + cols - 1) / cols);
     };
-    const long long t[4] = {3 * rounds(narrow), 5 * rounds(wide), 3 * split(narrow) + 50,
-                            5 * split(wide) + 50};
+    const long long kb = (p.k + (kFp8 ? 127 : 63)) / (kFp8 ? 128 : 64);
+    const auto whole = [&](long long n, int slots, long long epilogue) {
+        return (n + slots - 1) / slots * std::max(4 * kb, epilogue) + epilogue;
+    };
+    const auto split = [&](long long n, int ctas, int block, int most) {
+        const long long r = std::min({sms * 7ll / 8 / (ctas * n), kb / 2, (long long)most});
+        return r < 2 ? std::numeric_limits<long long>::max() : (kb + r - 1) / r * block + 50;
+    };
+    const long long t[4] = {whole(tiles(128, 128), sms, 20), whole(tiles(256, 256), sms / 2, 40),
+                            split(tiles(128, 128), 1, 4, 8), split(tiles(256, 256), 2, 4, 4)};
     const int best = (int)(std::min_element(t, t + 4) - t);
     if (best == 0) return launch<128, kAmn, kBmn, kFp8, false, false>(p, sms, err, stream);
-    if (best == 1) return launch<256, kAmn, kBmn, kFp8, false, false>(p, sms, err, stream);
+    if (best == 1) return launch_pair<kAmn, kBmn, kFp8, false>(p, err, stream);
     if (best == 2) return launch<128, kAmn, kBmn, kFp8, false, true>(p, sms, err, stream);
-    return launch<256, kAmn, kBmn, kFp8, false, true>(p, sms, err, stream);
+    return launch_pair<kAmn, kBmn, kFp8, true>(p, err, stream);
 }
 
 }  // namespace

@@ -192,7 +192,7 @@ __global__ void rmsnorm_fwd_wide_kernel(const SsdNormFwd a) {
 // ------------------------------------------------------------------ backward
 // A CTA walks the rows b, b + grid, ...; each thread keeps its columns' share
 // of dw in registers over all of them and writes it once, as row b of the
-// partial sums that rmsnorm_dw_kernel adds.
+// partial sums, which are then added in order.
 template <typename T, typename TS, int V, int kC>
 __global__ void __launch_bounds__(32 * kMostWarps)
 rmsnorm_bwd_kernel(const SsdNormBwd a, float *__restrict__ partial) {
@@ -295,22 +295,6 @@ __global__ void rmsnorm_dw_wide_kernel(const SsdNormBwd a, float *__restrict__ p
     partial[(size_t)blockIdx.x * a.width + j] = acc;
 }
 
-// out[j] = sum over the n partial rows, in a fixed order: 32 x 32 threads take
-// 32 columns, each of the 32 thread rows every 32nd partial row.
-__global__ void __launch_bounds__(1024)
-rmsnorm_dw_kernel(const float *__restrict__ partial, int n, int width, float *__restrict__ out) {
-    __shared__ float part[32][33];
-    const int j = blockIdx.x * 32 + threadIdx.x;
-    float acc = 0.f;
-    if (j < width)
-        for (int r = threadIdx.y; r < n; r += 32) acc += partial[(size_t)r * width + j];
-    part[threadIdx.y][threadIdx.x] = acc;
-    __syncthreads();
-    const float v = ssd_warp_sum(part[threadIdx.x][threadIdx.y]);
-    const int jo = blockIdx.x * 32 + threadIdx.y;
-    if (threadIdx.x == 0 && jo < width) out[jo] = v;
-}
-
 // Threads and runs a thread for one row: at most `most_runs` runs of V values a
 // thread (`want` where the warps allow it), a power of two of warps; 0 warps
 // when the row does not fit.
@@ -398,9 +382,7 @@ cudaError_t launch_bwd(const SsdNormBwd &a, float *partial, int sms, cudaStream_
     }
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    rmsnorm_dw_kernel<<<(unsigned)((a.width + 31) / 32), dim3(32, 32), 0, stream>>>(
-        partial, n, a.width, a.dweight);
-    return cudaGetLastError();
+    return ssd_launch_column_sum(partial, n, a.width, a.dweight, stream);
 }
 
 }  // namespace
