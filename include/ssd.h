@@ -601,8 +601,8 @@ const char *ssd_status_string(ssd_status s);
 ssd_status ssd_last_device_error(void);
 
 /* Test hook for the bounded device-side waits (the pages have no
- * counterpart).  Every later launch of the tensor-core scan reads the
- * setting; it is process-wide and not synchronised with calls in flight on
+ * counterpart).  Every later launch of the tensor-core scan, of the gated
+ * recurrence and (the limit) of the tensor-core product reads the setting; it is process-wide and not synchronised with calls in flight on
  * other host threads.
  *   fault          SSD_FAULT_NONE: normal operation.  SSD_FAULT_WITHHOLD_SIGNAL:
  *                  in the CTAs of each sequence's first segment, the barrier
@@ -612,6 +612,9 @@ ssd_status ssd_last_device_error(void);
  *                  tensor-core products complete, frees its tensor memory and
  *                  exits, and the device error word reads SSD_ERR_TIMEOUT.
  *                  The outputs of that call are undefined.
+ *                  In ssd_gated_scan_fwd / _bwd calls of more than one tile the
+ *                  first tile of the walk publishes nothing, so the tiles behind
+ *                  it give up after wait_limit_ns each, with the same report.
  *   wait_limit_ns  limit of every bounded wait in those kernels; 0 restores
  *                  the default (2 s).
  * Returns SSD_ERR_INVALID_ARG for an unknown fault. */

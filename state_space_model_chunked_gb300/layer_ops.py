@@ -68,6 +68,14 @@ def _full(t, name, dtype, index, shape):
     return t.data_ptr()
 
 
+def _out(t, name, dtype, index, device, shape):
+    """(array, address) of an output: the caller's, or a new one."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        return t, t.data_ptr()
+    return t, _full(t, name, dtype, index, shape)
+
+
 def _row_stride(t, name):
     """Distance of two rows of a matrix whose leading dimensions lie at one stride."""
     if t.dim() < 2:
@@ -167,32 +175,29 @@ def rmsnorm_fwd(x, weight, residual=None, *, eps=1e-5, out_dtype=None, y=None, r
     Returns (y, residual_out = s in the residual's dtype or None, rstd [...]
     f32, scale [...] f32 or None).  residual_out may be the residual itself."""
     lib = load()
-    at, dev = _cuda(x, "x"), x.device
-    shape, rows_shape, width = x.shape, x.shape[:-1], x.shape[-1]
-    out_dtype = x.dtype if out_dtype is None else out_dtype
-    xc, oc = _code(x.dtype, "x"), _code(out_dtype, "out_dtype")
-    xp, xs = x.data_ptr(), _row_stride(x, "x")
-    rp, rs, sc = None, 0, xc
+    at, dev, dtype = _cuda(x, "x"), x.device, x.dtype
+    shape = x.shape
+    rows_shape, width = shape[:-1], shape[-1]
+    out_dtype = dtype if out_dtype is None else out_dtype
+    xc, oc = _code(dtype, "x"), _code(out_dtype, "out_dtype")
+    xp, xs = _rows(x, "x", dtype, at, shape)
     if residual is not None:
-        rp, rs = _rows(residual, "residual", residual.dtype, at, shape)
-        sc = _code(residual.dtype, "residual")
-        if residual_out is None:
-            residual_out = torch.empty(shape, dtype=residual.dtype, device=dev)
+        stream = residual.dtype
+        rp, rs = _rows(residual, "residual", stream, at, shape)
+        sc = _code(stream, "residual")
+        residual_out, sp = _out(residual_out, "residual_out", stream, at, dev, shape)
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
-    if y is None:
-        y = torch.empty(shape, dtype=out_dtype, device=dev)
-    if rstd is None:
-        rstd = torch.empty(rows_shape, dtype=_F32, device=dev)
-    if out_dtype != FP8_E4M3:
-        scale = None
-    elif scale is None:
-        scale = torch.empty(rows_shape, dtype=_F32, device=dev)
+    else:
+        rp, rs, sc, sp = None, 0, xc, None
+    y, yp = _out(y, "y", out_dtype, at, dev, shape)
+    rstd, tp = _out(rstd, "rstd", _F32, at, dev, rows_shape)
+    if out_dtype is FP8_E4M3:
+        scale, cp = _out(scale, "scale", _F32, at, dev, rows_shape)
+    else:
+        scale, cp = None, None
     _call(at, lib.ssd_rmsnorm_fwd, xp, rp, _full(weight, "weight", _F32, at, (width,)), eps, xc,
-          sc, oc, _count(rows_shape), width, xs, rs, _full(y, "y", out_dtype, at, shape),
-          _full(residual_out, "residual_out", residual.dtype if residual is not None else None,
-                at, shape),
-          _full(rstd, "rstd", _F32, at, rows_shape), _full(scale, "scale", _F32, at, rows_shape))
+          sc, oc, _count(rows_shape), width, xs, rs, yp, sp, tp, cp)
     return y, residual_out, rstd, scale
 
 
@@ -269,7 +274,9 @@ def linear_fwd(x, w, bias=None, residual=None, *, activation=None, x_scale=None,
     rp, rs = _rows(residual, "residual", out_dtype, at, shape)
     if y is None:
         y = torch.empty(shape, dtype=out_dtype, device=dev)
-    yp, ys = _rows(y, "y", out_dtype, at, shape)
+        yp, ys = y.data_ptr(), features
+    else:
+        yp, ys = _rows(y, "y", out_dtype, at, shape)
     if return_preact and preact is None:
         preact = torch.empty(shape, dtype=kept, device=dev)
     tokens = _count(lead)
@@ -424,9 +431,7 @@ def gated_state_update(state, x, g, z=None, *, y=None):
     zp, zs = _rows(z, "z", x.dtype, at, shape)
     if state is None:
         raise ValueError("state is required")
-    if y is None:
-        y = torch.empty(shape, dtype=x.dtype, device=dev)
+    y, yp = _out(y, "y", x.dtype, at, dev, shape)
     _call(at, lib.ssd_gated_state_update, _full(state, "state", _F32, at, shape), x.data_ptr(),
-          gp, zp, code, _count(shape[:-1]), shape[-1], xs, gs, zs,
-          _full(y, "y", x.dtype, at, shape))
+          gp, zp, code, _count(shape[:-1]), shape[-1], xs, gs, zs, yp)
     return y
