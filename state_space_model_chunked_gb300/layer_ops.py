@@ -10,16 +10,46 @@ current stream of that device.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
+import os
 
 import torch
 
-from ._binding import FP8_E4M3, SsdError, _check, _host_offsets, load
+from ._binding import FP8_E4M3, SsdError, _check, _host_offsets, lib_path, load
 
 ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "relu": 3}
 GATED_SCAN_CHECKPOINT = 64      # tokens between the states kept for gated_scan_bwd
 _CODES = {torch.float32: 0, torch.bfloat16: 1, FP8_E4M3: 2}
 _F32 = torch.float32
 _BAD = ctypes.c_size_t(-1).value
+_INT_MAX = 2 ** 31 - 1
+
+
+_marshal_module = None
+
+
+def _marshal():
+    """The compiled marshalling of single-token calls (ssd_marshal.so, beside
+    libssd.so).  Its functions answer plain calls and return None for others; a
+    status that is not OK comes back as an int."""
+    global _marshal_module
+    if _marshal_module is None:
+        load()
+        path = os.path.join(os.path.dirname(lib_path()), "ssd_marshal.so")
+        if not os.path.exists(path):
+            raise ImportError(f"ssd_marshal.so not found at {path}; build it with "
+                              "`python -m state_space_model_chunked_gb300.build`")
+        spec = importlib.util.spec_from_file_location("ssd_marshal", path)
+        _marshal_module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_marshal_module)
+    return _marshal_module
+
+
+def _plain(fn, answer):
+    """A marshalled call's answer, an error status raised."""
+    if answer.__class__ is int:
+        _check(fn, answer)
+    return answer
 
 
 def _code(dtype, name):
@@ -45,6 +75,8 @@ def _cuda(t, name):
     index = t.get_device()
     if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() and t.shape[-1] > _INT_MAX:
+        raise ValueError(f"{name} has {t.shape[-1]} columns, more than a C int holds")
     return index
 
 
@@ -174,6 +206,11 @@ def rmsnorm_fwd(x, weight, residual=None, *, eps=1e-5, out_dtype=None, y=None, r
     float8_e4m3fn, with one scale a row (y * scale[..., None] is the value).
     Returns (y, residual_out = s in the residual's dtype or None, rstd [...]
     f32, scale [...] f32 or None).  residual_out may be the residual itself."""
+    if x is not None and y is None and residual_out is None and rstd is None and scale is None:
+        got = (_marshal_module or _marshal()).rmsnorm_fwd(
+            x, weight, residual, eps, _code(x.dtype if out_dtype is None else out_dtype, "out_dtype"))
+        if got is not None:
+            return _plain("ssd_rmsnorm_fwd", got)
     lib = load()
     at, dev, dtype = _cuda(x, "x"), x.device, x.dtype
     shape = x.shape
@@ -258,12 +295,18 @@ def linear_fwd(x, w, bias=None, residual=None, *, activation=None, x_scale=None,
     for f32 ones); activation None, "silu", "gelu" or "relu".  y may be the
     residual itself.  Returns y, or (y, preact) with return_preact: the values
     before the activation, which linear_bwd needs."""
+    act = _activation(activation)
+    if x is not None and y is None and preact is None and not return_preact:
+        out = out_dtype or (_F32 if x.dtype is _F32 else torch.bfloat16)
+        got = (_marshal_module or _marshal()).linear_fwd(x, w, bias, residual, act, x_scale, w_scale,
+                                                         _code(out, "out_dtype"))
+        if got is not None:
+            return _plain("ssd_linear_fwd", got)
     lib = load()
     at, dev = _cuda(x, "x"), x.device
-    act = _activation(activation)
     xc = _code(x.dtype, "x")
     lead, inner = x.shape[:-1], x.shape[-1]
-    if w is None or w.dim() != 2:
+    if w is None or w.dim() != 2 or w.shape[0] > _INT_MAX:
         raise ValueError("w must be [features, inner]")
     features = w.shape[0]
     xp, xs = x.data_ptr(), _row_stride(x, "x")
@@ -423,6 +466,10 @@ def gated_scan_bwd(dy, x, g, checkpoints, z=None, init_state=None, dfinal=None, 
 def gated_state_update(state, x, g, z=None, *, y=None):
     """One token of the gated recurrence: state [..., width] f32, updated in
     place; x, g, z [..., width] f32 or bf16.  Returns y in x's dtype."""
+    if y is None:
+        got = (_marshal_module or _marshal()).gated_state_update(state, x, g, z)
+        if got is not None:
+            return _plain("ssd_gated_state_update", got)
     lib = load()
     at, dev = _cuda(x, "x"), x.device
     code, shape = _code(x.dtype, "x"), x.shape
