@@ -29,7 +29,7 @@ _marshal_module = None
 
 
 def _marshal():
-    """The compiled marshalling of single-token calls (ssd_marshal.so, beside
+    """The compiled marshalling of plain calls (ssd_marshal.so, beside
     libssd.so).  Its functions answer plain calls and return None for others; a
     status that is not OK comes back as an int."""
     global _marshal_module
@@ -250,6 +250,10 @@ def rmsnorm_bwd(dy, s, weight, rstd, dresidual=None, *, dx=None, ds=None, dweigh
     residual_out from elsewhere.  Returns (dx, ds, dweight): the gradient of x
     in dy's dtype and of the residual in s's (one tensor when those agree),
     and of the weight, f32."""
+    if dx is None and ds is None and dweight is None and workspace is None:
+        got = (_marshal_module or _marshal()).rmsnorm_bwd(dy, s, weight, rstd, dresidual)
+        if got is not None:
+            return _plain("ssd_rmsnorm_bwd", got)[:3]
     lib = load()
     at, dev = _cuda(dy, "dy"), dy.device
     shape, width = dy.shape, dy.shape[-1]
@@ -337,9 +341,13 @@ def linear_bwd(dy, x, w, preact=None, *, activation=None, bias=True, need_dx=Tru
     given to it; preact as it returned (with an activation).  Returns
     (dx, dw, dbias): in dy's dtype, dy's dtype and f32; None for what is not
     wanted (need_dx, need_dw, bias).  The residual's gradient is dy."""
+    act = _activation(activation)
+    if need_dx and need_dw and dx is None and dw is None and dbias is None and workspace is None:
+        got = (_marshal_module or _marshal()).linear_bwd(dy, x, w, preact, act, bias)
+        if got is not None:
+            return _plain("ssd_linear_bwd", got)[:3]
     lib = load()
     at, dev = _cuda(dy, "dy"), dy.device
-    act = _activation(activation)
     dt, code = dy.dtype, _code(dy.dtype, "dy")
     lead, features = dy.shape[:-1], dy.shape[-1]
     inner = x.shape[-1]
@@ -398,6 +406,12 @@ def gated_scan_fwd(x, g, z=None, init_state=None, *, cu_seqlens=None, cu_seqlens
     (y, final_state [nseq, width] f32 or None), and the states
     [ceil(tokens / 64), width] f32 that gated_scan_bwd needs with
     return_checkpoints."""
+    if (y is None and final_state is None and return_final and checkpoints is None
+            and workspace is None):
+        got = (_marshal_module or _marshal()).gated_scan_fwd(x, g, z, init_state, cu_seqlens,
+                                                             cu_seqlens_dev, return_checkpoints)
+        if got is not None:
+            return _plain("ssd_gated_scan_fwd", got)[:3 if return_checkpoints else 2]
     lib = load()
     at, dev = _cuda(x, "x"), x.device
     code, shape, width = _code(x.dtype, "x"), x.shape, x.shape[-1]
@@ -429,6 +443,12 @@ def gated_scan_bwd(dy, x, g, checkpoints, z=None, init_state=None, dfinal=None, 
     final state (None: zeros); x, g, z, init_state and offsets as given to it
     and the checkpoints it returned.  dx, dg and dz may be column ranges of one
     matrix.  Returns (dx, dg, dz or None, dinit [nseq, width] f32 or None)."""
+    if (dx is None and dg is None and dz is None and dinit is None and return_dinit
+            and workspace is None):
+        got = (_marshal_module or _marshal()).gated_scan_bwd(dy, x, g, checkpoints, z, init_state,
+                                                             dfinal, cu_seqlens, cu_seqlens_dev)
+        if got is not None:
+            return _plain("ssd_gated_scan_bwd", got)
     lib = load()
     at, dev = _cuda(x, "x"), x.device
     code, shape, width = _code(x.dtype, "x"), x.shape, x.shape[-1]
