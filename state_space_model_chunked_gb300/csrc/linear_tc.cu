@@ -649,7 +649,7 @@ product_pair_kernel(const __grid_constant__ CUtensorMap map_a,
                     [&]() { return wait_warp(&ctl->acc_full[buf], turn & 1, ctl, a); },
                     [&]() {
                         if (lane == 0)
-                            mbar_arrive_cluster(cluster_map(smem_u32(&ctl->acc_empty[buf]), leader));
+                            mbar_arrive_cluster_relaxed(cluster_map(smem_u32(&ctl->acc_empty[buf]), leader));
                     }))
                 break;
         }
