@@ -52,6 +52,7 @@ constexpr uint32_t tmem_cols(int bn, bool split) {
 struct Args {
     SsdProduct p;           // rows of A are p.m, or (kSwap) p.n
     int row_tiles, col_tiles, kblocks;
+    int tile0, tile1;       // the tiles of this launch
     bool vec;               // 16-byte rows of out, preact, residual; bias and b_scale on 16 bytes
     unsigned *err;
     unsigned long long wait_ns;
@@ -549,8 +550,8 @@ product_pair_kernel(const __grid_constant__ CUtensorMap map_a,
     cluster_sync_all();         // both CTAs' barriers and tensor memory stand
     tc_fence_after();
     const uint32_t tmem = ctl->tmem;
-    const int ntiles = a.row_tiles * a.col_tiles, step = kSplit ? ntiles : (int)gridDim.x / 2;
-    const int first = blockIdx.x / (2 * parts);
+    const int ntiles = a.tile1, step = kSplit ? ntiles : (int)gridDim.x / 2;
+    const int first = a.tile0 + blockIdx.x / (2 * parts);
     const int kb0 = (int)((long long)a.kblocks * part / parts);
     const int kb1 = (int)((long long)a.kblocks * (part + 1) / parts);
 
@@ -774,10 +775,15 @@ cudaError_t launch(const SsdProduct &p, int sms, unsigned *err, cudaStream_t str
     return cudaLaunchKernelEx(&cfg, kernel, ma, mb, a);
 }
 
+// Pairs over the tiles tile0 .. tile1 - 1 (row by row of groups, as tile_at has
+// them; tile1 < 0: to the last).
 template <bool kAmn, bool kBmn, bool kFp8, bool kSplit>
-cudaError_t launch_pair(const SsdProduct &p, unsigned *err, cudaStream_t stream) {
+cudaError_t launch_pair(const SsdProduct &p, int tile0, int tile1, unsigned *err,
+                        cudaStream_t stream) {
     constexpr uint32_t kSmem = kCtrlBytes + kPairStages * kPairStage + kColumnBytes;
     Args a = args_of(p, 256, kPairBN, kFp8, err);
+    a.tile0 = tile0;
+    a.tile1 = tile1 < 0 ? a.row_tiles * a.col_tiles : tile1;
     CUtensorMap ma, mb;
     if (!operand_map(&ma, p.a, kFp8, kAmn, p.m, p.k, kAmn ? p.a_col : p.a_row, kBM) ||
         !operand_map(&mb, p.b, kFp8, kBmn, p.n, p.k, kBmn ? p.b_col : p.b_row, 128))
@@ -796,7 +802,7 @@ cudaError_t launch_pair(const SsdProduct &p, unsigned *err, cudaStream_t stream)
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const long long tiles = (long long)a.row_tiles * a.col_tiles;
+    const long long tiles = a.tile1 - a.tile0;
     if (kSplit) {
         int parts = 4;
         while (parts > 1 && (a.kblocks < 2 * parts || tiles > clusters_at_once(kernel, cfg, 2 * parts)))
@@ -823,7 +829,10 @@ cudaError_t few_tokens(const SsdProduct &p, int sms, unsigned *err, cudaStream_t
 // products hide if they last as long, about 20 and 40; a split's barriers and
 // exchange of sums 50.  Whole tiles run in rounds of as many
 // as the SMs take; a split has as many ranks as 7/8 of the SMs allow (clusters do
-// not fill all of them).
+// not fill all of them).  Or whole rounds of the pairs' tiles, and the few left over
+// split, in a launch of their own for another 100 units (gradients at 2635 x 7664 x
+// 1952: 147 against 164 us; at 16376 x 2048 x 1024, where it does not pay, 103
+// against 98).
 template <bool kAmn, bool kBmn, bool kFp8>
 cudaError_t many(const SsdProduct &p, int sms, unsigned *err, cudaStream_t stream) {
     const auto tiles = [&](int rows, int cols) {
@@ -837,13 +846,21 @@ cudaError_t many(const SsdProduct &p, int sms, unsigned *err, cudaStream_t strea
         const long long r = std::min({sms * 7ll / 8 / (ctas * n), kb / 2, (long long)most});
         return r < 2 ? std::numeric_limits<long long>::max() : (kb + r - 1) / r * block + 50;
     };
-    const long long t[4] = {whole(tiles(128, 128), sms, 20), whole(tiles(256, 256), sms / 2, 40),
-                            split(tiles(128, 128), 1, 4, 8), split(tiles(256, 256), 2, 4, 4)};
-    const int best = (int)(std::min_element(t, t + 4) - t);
+    const int pairs = sms / 2;
+    const long long large = tiles(256, 256), full = large / pairs * pairs;
+    const long long never = std::numeric_limits<long long>::max();
+    const long long rest = full > 0 && full < large ? split(large - full, 2, 4, 4) : never;
+    const long long t[5] = {whole(tiles(128, 128), sms, 20), whole(large, pairs, 40),
+                            split(tiles(128, 128), 1, 4, 8), split(large, 2, 4, 4),
+                            rest == never ? never : whole(full, pairs, 40) + rest + 100};
+    const int best = (int)(std::min_element(t, t + 5) - t);
     if (best == 0) return launch<128, kAmn, kBmn, kFp8, false, false>(p, sms, err, stream);
-    if (best == 1) return launch_pair<kAmn, kBmn, kFp8, false>(p, err, stream);
+    if (best == 1) return launch_pair<kAmn, kBmn, kFp8, false>(p, 0, -1, err, stream);
     if (best == 2) return launch<128, kAmn, kBmn, kFp8, false, true>(p, sms, err, stream);
-    return launch_pair<kAmn, kBmn, kFp8, true>(p, err, stream);
+    if (best == 3) return launch_pair<kAmn, kBmn, kFp8, true>(p, 0, -1, err, stream);
+    const cudaError_t e = launch_pair<kAmn, kBmn, kFp8, false>(p, 0, (int)full, err, stream);
+    return e != cudaSuccess ? e
+                            : launch_pair<kAmn, kBmn, kFp8, true>(p, (int)full, -1, err, stream);
 }
 
 }  // namespace
