@@ -70,6 +70,12 @@ template <int V>
 __device__ __forceinline__ Val<V> operator-(const Val<V> &a, const Val<V> &b) {
     return fma(b, all<V>(-1.f), a);
 }
+template <int V>
+__device__ __forceinline__ Val<V> minus(Val<V> a) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) a[k] = -a[k];
+    return a;
+}
 template <typename T, int V>
 __device__ __forceinline__ Val<V> value(const SsdRaw<T, V> &raw) {
     Val<V> r;
@@ -105,6 +111,27 @@ __device__ __forceinline__ Val<V> sigmoid(const Val<V> &z) {
         s[k] = ssdptx::rcp_approx(1.f + ssdptx::ex2_approx(z[k] * -kLog2e));
     return s;
 }
+
+// n / d for 0 <= n < 2^31 by one multiplication: m = ceil(2^(31 + s) / d) with
+// s = ceil(log2 d) errs by less than 2^s / d <= 1 of a quotient's last place.
+struct Divisor {
+    unsigned d, m, s;
+    Divisor() = default;
+    explicit Divisor(unsigned by) : d(by), m(0), s(0) {
+        while ((1ull << s) < by) ++s;
+        m = (unsigned)(((1ull << (31 + s)) + by - 1) / by);
+    }
+    __device__ __forceinline__ unsigned div(unsigned n) const {
+        return (unsigned)(((unsigned long long)n * m) >> (31 + s));
+    }
+};
+
+// What a launch hands its CTAs besides the arrays.
+struct Walk {
+    int blocks, tiles;
+    int ahead;              // tiles to the one whose rows a CTA asks L2 for
+    Divisor by_blocks, by_length;
+};
 
 // ------------------------------------------------------------- tiles and joins
 // The token axis is cut into tiles, one CTA a tile and block of 32 V channels:
@@ -247,7 +274,8 @@ struct Marks {
     int seq;
     unsigned starts, ends;
 };
-__device__ __forceinline__ Marks marks(const SsdGated &a, long long t0, int n) {
+__device__ __forceinline__ Marks marks(const SsdGated &a, const Divisor &by_length, long long t0,
+                                       int n) {
     const int lane = threadIdx.x & 31;
     const long long t = t0 + lane;
     const bool in = lane < n && t < a.tokens;
@@ -266,7 +294,7 @@ __device__ __forceinline__ Marks marks(const SsdGated &a, long long t0, int n) {
             start = __ldg(a.cu + lo) == t;
             end = __ldg(a.cu + lo + 1) == t + 1;
         } else {
-            m.seq = (int)t / a.length;
+            m.seq = (int)by_length.div((unsigned)t);
             const int off = (int)t - m.seq * a.length;
             start = off == 0;
             end = off == a.length - 1;
@@ -299,14 +327,14 @@ __device__ __forceinline__ void load_f32(const float *p, bool on, float (&v)[V])
 
 // The CTA's place: number in the walk, and block of channels.
 template <bool kJoin>
-__device__ __forceinline__ void place(const Joins &j, int blocks, int &at, int &block) {
+__device__ __forceinline__ void place(const Joins &j, const Walk &walk, int &at, int &block) {
     if constexpr (kJoin) {
         __shared__ unsigned ticket;
         if (threadIdx.x == 0) ticket = atomicAdd(j.ticket, 1u) + 1u;    // from all ones: 0, 1, ...
         __syncthreads();
         const unsigned t = __shfl_sync(0xffffffffu, ticket, 0);     // one value in the warp
-        at = t / blocks;
-        block = t % blocks;
+        at = (int)walk.by_blocks.div(t);
+        block = (int)(t - (unsigned)at * walk.blocks);
     } else {
         at = 0;
         block = blockIdx.x;
@@ -420,20 +448,32 @@ __device__ __forceinline__ void load_run(SsdRaw<T, V> (&raw)[kTok], const void *
     }
 }
 
-// Asks L2 for one array's rows of the tile from t0: a generation of CTAs ahead
-// of their use, so their loads find them there.  A thread takes rows in turn.
-template <typename T, int V, int kTile>
-__device__ __forceinline__ void prefetch_tile(const void *base, long long stride, long long t0,
+// Asks L2 for the rows of the tile from t0 in kArrays arrays: a generation of CTAs
+// ahead of their use, so their loads find them there.  A thread takes rows in turn.
+template <typename T, int V, int kTile, int kArrays>
+__device__ __forceinline__ void prefetch_tile(const void *const (&base)[kArrays],
+                                              const long long (&stride)[kArrays], long long t0,
                                               long long tokens, int c0, int width) {
-    const int bytes = min(32 * V, width - c0) * (int)sizeof(T);
-    for (int i = threadIdx.x; i < kTile; i += blockDim.x) {
-        if (t0 + i < 0 || t0 + i >= tokens) continue;
-        const char *p = reinterpret_cast<const char *>(static_cast<const T *>(base) +
-                                                       (t0 + i) * stride + c0);
-        for (int b = 0; b < bytes; b += 128)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(p + b));
+    static_assert((kTile & (kTile - 1)) == 0, "rows of an array");
+    constexpr int kBytes = 32 * V * (int)sizeof(T);
+    if (t0 < 0 || t0 + kTile > tokens) return;
+    for (int i = threadIdx.x; i < kArrays * kTile; i += blockDim.x) {
+        const void *b = base[0];
+        long long s = stride[0];
+#pragma unroll
+        for (int k = 1; k < kArrays; ++k)
+            if (i >= k * kTile) b = base[k], s = stride[k];
+        const char *p = reinterpret_cast<const char *>(static_cast<const T *>(b) +
+                                                       (t0 + (i & (kTile - 1))) * s + c0);
+        // whole blocks of channels: the last of a ragged width may be asked for short
+        if (c0 + 32 * V > width) {
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+            continue;
+        }
+#pragma unroll
+        for (int o = 0; o < kBytes; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + o));
         if (((uintptr_t)p & 127u) != 0)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(p + bytes - 1));
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p + kBytes - 1));
     }
 }
 
@@ -453,10 +493,10 @@ __device__ __forceinline__ void by_form(bool plain, F &&body) {
 
 template <typename T, int V, bool kGate, bool kJoin>
 __global__ void __launch_bounds__(32 * kFwdWarps, kFwdCtas)
-gated_fwd_kernel(const SsdGatedFwd a, const Joins joins, int blocks, int ahead) {
+gated_fwd_kernel(const SsdGatedFwd a, const Joins joins, const Walk walk) {
     __shared__ Runs<V, kFwdWarps> runs;
     int at, block;
-    place<kJoin>(joins, blocks, at, block);
+    place<kJoin>(joins, walk, at, block);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int width = a.in.width, c = (block * 32 + lane) * V;
     const bool on = c < width;
@@ -469,14 +509,18 @@ gated_fwd_kernel(const SsdGatedFwd a, const Joins joins, int blocks, int ahead) 
     load_run<T, V>(xraw, a.in.x, a.in.x_stride, t0, n, c, on, whole);
     if constexpr (kGate) load_run<T, V>(zraw, a.in.z, a.in.z_stride, t0, n, c, on, whole);
     if constexpr (kJoin) {
-        const long long tn = (long long)(at + ahead) * kFwdTile;
-        const int c0 = block * 32 * V;
-        prefetch_tile<T, V, kFwdTile>(a.in.g, a.in.g_stride, tn, a.in.tokens, c0, width);
-        prefetch_tile<T, V, kFwdTile>(a.in.x, a.in.x_stride, tn, a.in.tokens, c0, width);
-        if constexpr (kGate)
-            prefetch_tile<T, V, kFwdTile>(a.in.z, a.in.z_stride, tn, a.in.tokens, c0, width);
+        const long long tn = (long long)(at + walk.ahead) * kFwdTile;
+        if constexpr (kGate) {
+            const void *const base[3] = {a.in.g, a.in.x, a.in.z};
+            const long long stride[3] = {a.in.g_stride, a.in.x_stride, a.in.z_stride};
+            prefetch_tile<T, V, kFwdTile>(base, stride, tn, a.in.tokens, block * 32 * V, width);
+        } else {
+            const void *const base[2] = {a.in.g, a.in.x};
+            const long long stride[2] = {a.in.g_stride, a.in.x_stride};
+            prefetch_tile<T, V, kFwdTile>(base, stride, tn, a.in.tokens, block * 32 * V, width);
+        }
     }
-    const Marks m = marks(a.in, t0, kFwdTok);
+    const Marks m = marks(a.in, walk.by_length, t0, kFwdTok);
     const bool plain = whole && (m.starts | m.ends) == 0;
     if (at == 0) pass_empty<V>(a.in, a.in.init, a.final_state, c);
 
@@ -547,16 +591,16 @@ gated_fwd_kernel(const SsdGatedFwd a, const Joins joins, int blocks, int ahead) 
 // dz = dy h s (1 + z (1 - s)) = h (s (dy - dh) + dh).
 template <typename T, int V, bool kGate, bool kJoin>
 __global__ void __launch_bounds__(32 * kBwdWarps, kBwdCtas)
-gated_bwd_kernel(const SsdGatedBwd a, const Joins joins, int blocks, int tiles, int ahead) {
+gated_bwd_kernel(const SsdGatedBwd a, const Joins joins, const Walk walk) {
     __shared__ Runs<V, kBwdWarps> runs;
     __shared__ float fA[kBwdWarps][32 * V], fH[kBwdWarps][32 * V];
     __shared__ bool fcut[kBwdWarps];
     int at, block;
-    place<kJoin>(joins, blocks, at, block);
+    place<kJoin>(joins, walk, at, block);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int width = a.in.width, c = (block * 32 + lane) * V;
     const bool on = c < width;
-    const int tile = tiles - 1 - at;
+    const int tile = walk.tiles - 1 - at;
     const long long t0 = (long long)tile * kBwdTile + warp * kBwdTok;
     const int n = (int)max(0ll, min((long long)kBwdTok, a.in.tokens - t0));
     const bool whole = n == kBwdTok && __all_sync(0xffffffffu, on);
@@ -569,26 +613,31 @@ gated_bwd_kernel(const SsdGatedBwd a, const Joins joins, int blocks, int tiles, 
     Val<V> h;           // the state that enters the tile
     load_f32<V>(a.checkpoints + (size_t)tile * width + c, on && a.in.tokens > 0, h.v);
     if constexpr (kJoin) {
-        const long long tn = (long long)(tile - ahead) * kBwdTile;
-        const int c0 = block * 32 * V;
-        prefetch_tile<T, V, kBwdTile>(a.in.g, a.in.g_stride, tn, a.in.tokens, c0, width);
-        prefetch_tile<T, V, kBwdTile>(a.dy, a.dy_stride, tn, a.in.tokens, c0, width);
-        if constexpr (kGate)
-            prefetch_tile<T, V, kBwdTile>(a.in.z, a.in.z_stride, tn, a.in.tokens, c0, width);
-        prefetch_tile<T, V, kBwdTile>(a.in.x, a.in.x_stride, tn, a.in.tokens, c0, width);
+        const long long tn = (long long)(tile - walk.ahead) * kBwdTile;
+        if constexpr (kGate) {
+            const void *const base[4] = {a.in.g, a.dy, a.in.z, a.in.x};
+            const long long stride[4] = {a.in.g_stride, a.dy_stride, a.in.z_stride, a.in.x_stride};
+            prefetch_tile<T, V, kBwdTile>(base, stride, tn, a.in.tokens, block * 32 * V, width);
+        } else {
+            const void *const base[3] = {a.in.g, a.dy, a.in.x};
+            const long long stride[3] = {a.in.g_stride, a.dy_stride, a.in.x_stride};
+            prefetch_tile<T, V, kBwdTile>(base, stride, tn, a.in.tokens, block * 32 * V, width);
+        }
     }
-    const Marks m = marks(a.in, t0, kBwdTok);
+    const Marks m = marks(a.in, walk.by_length, t0, kBwdTok);
     const bool plain = whole && (m.starts | m.ends) == 0;
     if (at == 0) pass_empty<V>(a.in, a.dfinal, a.dinit, c);
 
     // the run forward (A, H) and backward (A, M)
-    Val<V> keep[kBwdTok], drop[kBwdTok], dh[kBwdTok], sig[kGate ? kBwdTok : 1];
+    Val<V> drop[kBwdTok], q[kBwdTok], dh[kBwdTok], sig[kGate ? kBwdTok : 1];
     Val<V> A = all<V>(1.f), H = all<V>(0.f), M = all<V>(0.f);
     by_form(plain, [&](auto form) {
         constexpr bool kPlain = decltype(form)::kOn;
 #pragma unroll
         for (int i = 0; i < kBwdTok; ++i) {
-            gate(value(graw[i]), keep[i], drop[i]);
+            Val<V> keep;
+            gate(value(graw[i]), keep, drop[i]);
+            q[i] = keep * drop[i];
             const Val<V> u = drop[i] * value(xraw[i]);
             if (!kPlain && ((m.starts >> i) & 1u)) {
                 const int seq = __shfl_sync(0xffffffffu, m.seq, i);
@@ -596,10 +645,10 @@ gated_bwd_kernel(const SsdGatedBwd a, const Joins joins, int blocks, int tiles, 
                 load_f32<V>(a.in.init + (size_t)seq * width + c, on && a.in.init != nullptr,
                             first.v);
                 A = all<V>(0.f);
-                H = fma(keep[i], first, u);
+                H = fma(keep, first, u);
             } else if (kPlain || i < n) {
-                A = A * keep[i];
-                H = fma(keep[i], H, u);
+                A = A * keep;
+                H = fma(keep, H, u);
             }
         }
 #pragma unroll
@@ -617,7 +666,7 @@ gated_bwd_kernel(const SsdGatedBwd a, const Joins joins, int blocks, int tiles, 
                 load_f32<V>(a.dfinal + (size_t)seq * width + c, on && a.dfinal != nullptr, lam.v);
                 lam = dh[i] + lam;
             }
-            M = !kPlain && ((m.starts >> i) & 1u) ? all<V>(0.f) : keep[i] * lam;
+            M = !kPlain && ((m.starts >> i) & 1u) ? all<V>(0.f) : lam - drop[i] * lam;
         }
     });
 #pragma unroll
@@ -629,14 +678,13 @@ gated_bwd_kernel(const SsdGatedBwd a, const Joins joins, int blocks, int tiles, 
     const Entering<V> e = join_begin<V, kBwdWarps, kJoin>(
         runs, joins, at, width, c, kBwdWarps - 1 - warp, m.starts != 0, A, M);
 
-    // forward: the state before each token, and dz
+    // forward: the states, f (1 - f) (x - h_{t-1}) in place of f (1 - f), and dz
     for (int w = 0; w < warp; ++w) {
         Val<V> wa, wh;
 #pragma unroll
         for (int k = 0; k < V; ++k) wa[k] = fA[w][lane * V + k], wh[k] = fH[w][lane * V + k];
         h = fcut[w] ? wh : fma(wa, h, wh);
     }
-    Val<V> before[kBwdTok];
     by_form(plain, [&](auto form) {
         constexpr bool kPlain = decltype(form)::kOn;
         [[maybe_unused]] T *dz = kGate ? static_cast<T *>(a.dz) + t0 * a.dz_stride : nullptr;
@@ -647,8 +695,9 @@ gated_bwd_kernel(const SsdGatedBwd a, const Joins joins, int blocks, int tiles, 
                 const int seq = __shfl_sync(0xffffffffu, m.seq, i);
                 load_f32<V>(a.in.init + (size_t)seq * width + c, on && a.in.init != nullptr, h.v);
             }
-            before[i] = h;
-            h = fma(keep[i], h, drop[i] * value(xraw[i]));
+            const Val<V> to = value(xraw[i]) - h;       // h_t = h_{t-1} + (1 - f) (x - h_{t-1})
+            q[i] = q[i] * to;
+            h = fma(drop[i], to, h);
             if constexpr (kGate) {
                 const Val<V> o = h * fma(sig[i], value(yraw[i]) - dh[i], dh[i]);
                 if (kPlain || on) ssd_store_vec<V>(dz + i * a.dz_stride + (unsigned)c, o.v);
@@ -672,15 +721,24 @@ gated_bwd_kernel(const SsdGatedBwd a, const Joins joins, int blocks, int tiles, 
                 lam = dh[i] + lam;
             }
             const Val<V> ox = drop[i] * lam;
-            mu = keep[i] * lam;
-            const Val<V> og = (mu * drop[i]) * (before[i] - value(xraw[i]));
+            mu = lam - ox;
+            const Val<V> og = minus(lam * q[i]);
             if (kPlain || on) {
                 ssd_store_vec<V>(dx + i * a.dx_stride + (unsigned)c, ox.v);
                 ssd_store_vec<V>(dg + i * a.dg_stride + (unsigned)c, og.v);
             }
             if (!kPlain && ((m.starts >> i) & 1u) && a.dinit) {
+                // dinit = f lam with a small f's own precision, which lam - (1 - f) lam
+                // does not have (and, added to dh, does not need)
                 const int seq = __shfl_sync(0xffffffffu, m.seq, i);
-                if (on) ssd_store_vec<V>(a.dinit + (size_t)seq * width + c, mu.v);
+                if (on) {
+                    SsdRaw<T, V> again;
+                    again.load(static_cast<const T *>(a.in.g) + (t0 + i) * a.in.g_stride + c);
+                    Val<V> keep, unused;
+                    gate(value(again), keep, unused);
+                    keep = keep * lam;
+                    ssd_store_vec<V>(a.dinit + (size_t)seq * width + c, keep.v);
+                }
             }
         }
     });
@@ -750,36 +808,36 @@ static cudaError_t joins_of(void *workspace, int tiles, int width, unsigned *err
     return cudaMemsetAsync(ws, 0xff, joins_bytes(tiles, width), stream);
 }
 
-template <typename T, int V, bool kGate>
-static cudaError_t launch_fwd(const SsdGatedFwd &a, int sms, void *ws, unsigned *err, cudaStream_t stream) {
-    const int tiles = tiles_of(a.in.tokens, kFwdTile), blocks = (a.in.width + 32 * V - 1) / (32 * V);
+// One launch: `one` for calls of a single tile, which has nothing to join.
+template <int V, typename Args>
+static cudaError_t launch(void (*one)(Args, Joins, Walk), void (*joined)(Args, Joins, Walk),
+                          const Args &a, int tile, int threads, int ctas, int sms, void *ws,
+                          unsigned *err, cudaStream_t stream) {
+    Walk w;
+    w.tiles = tiles_of(a.in.tokens, tile);
+    w.blocks = (a.in.width + 32 * V - 1) / (32 * V);
+    w.ahead = (sms * ctas + w.blocks - 1) / w.blocks;
+    w.by_blocks = Divisor((unsigned)w.blocks);
+    w.by_length = Divisor(a.in.length > 0 ? (unsigned)a.in.length : 1u);
     Joins j{};
-    if (tiles == 1) {
-        gated_fwd_kernel<T, V, kGate, false><<<blocks, 32 * kFwdWarps, 0, stream>>>(a, j, blocks, 0);
-        return cudaGetLastError();
+    if (w.tiles > 1) {
+        const cudaError_t e = joins_of(ws, w.tiles, a.in.width, err, stream, &j);
+        if (e != cudaSuccess) return e;
     }
-    const cudaError_t e = joins_of(ws, tiles, a.in.width, err, stream, &j);
-    if (e != cudaSuccess) return e;
-    gated_fwd_kernel<T, V, kGate, true>
-        <<<(unsigned)((size_t)tiles * blocks), 32 * kFwdWarps, 0, stream>>>(
-            a, j, blocks, (sms * kFwdCtas + blocks - 1) / blocks);
+    (w.tiles > 1 ? joined : one)<<<(unsigned)((size_t)w.tiles * w.blocks), threads, 0, stream>>>(a, j, w);
     return cudaGetLastError();
 }
-
 template <typename T, int V, bool kGate>
-static cudaError_t launch_bwd(const SsdGatedBwd &a, int sms, void *ws, unsigned *err, cudaStream_t stream) {
-    const int tiles = tiles_of(a.in.tokens, kBwdTile), blocks = (a.in.width + 32 * V - 1) / (32 * V);
-    Joins j{};
-    if (tiles == 1) {
-        gated_bwd_kernel<T, V, kGate, false><<<blocks, 32 * kBwdWarps, 0, stream>>>(a, j, blocks, tiles, 0);
-        return cudaGetLastError();
-    }
-    const cudaError_t e = joins_of(ws, tiles, a.in.width, err, stream, &j);
-    if (e != cudaSuccess) return e;
-    gated_bwd_kernel<T, V, kGate, true>
-        <<<(unsigned)((size_t)tiles * blocks), 32 * kBwdWarps, 0, stream>>>(
-            a, j, blocks, tiles, (sms * kBwdCtas + blocks - 1) / blocks);
-    return cudaGetLastError();
+static cudaError_t launch_fwd(const SsdGatedFwd &a, int sms, void *ws, unsigned *err,
+                              cudaStream_t stream) {
+    return launch<V>(gated_fwd_kernel<T, V, kGate, false>, gated_fwd_kernel<T, V, kGate, true>, a,
+                     kFwdTile, 32 * kFwdWarps, kFwdCtas, sms, ws, err, stream);
+}
+template <typename T, int V, bool kGate>
+static cudaError_t launch_bwd(const SsdGatedBwd &a, int sms, void *ws, unsigned *err,
+                              cudaStream_t stream) {
+    return launch<V>(gated_bwd_kernel<T, V, kGate, false>, gated_bwd_kernel<T, V, kGate, true>, a,
+                     kBwdTile, 32 * kBwdWarps, kBwdCtas, sms, ws, err, stream);
 }
 
 cudaError_t ssd_launch_gated_fwd(const SsdGatedFwd &a, int sms, void *ws, unsigned *err,
