@@ -745,23 +745,35 @@ gated_bwd_kernel(const SsdGatedBwd a, const Joins joins, const Walk walk) {
 }
 
 // One token of every (row, channel): the state is read and written in place.
-template <typename T>
+// Bound by memory (and, for few rows, by the launch): a thread takes V channels.
+template <typename T, int V, bool kGate>
 __global__ void __launch_bounds__(256) gated_step_kernel(const SsdGatedStep a) {
-    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= (size_t)a.rows * a.width) return;
-    const size_t r = i / a.width, c = i % a.width;
-    const Val<1> g{{ssd_ld(static_cast<const T *>(a.g) + r * a.g_stride + c)}};
-    const float x = ssd_ld(static_cast<const T *>(a.x) + r * a.x_stride + c);
-    Val<1> keep, drop;
-    gate(g, keep, drop);
-    const float h = keep[0] * a.state[i] + drop[0] * x;
-    a.state[i] = h;
-    float y = h;
-    if (a.z) {
-        const Val<1> z{{ssd_ld(static_cast<const T *>(a.z) + r * a.z_stride + c)}};
-        y = h * (z[0] * sigmoid(z)[0]);
+    const long long r = blockIdx.x;
+    const int c = (blockIdx.y * 256 + threadIdx.x) * V;
+    if (c >= a.width) return;
+    SsdRaw<T, V> gr, xr, zr;
+    SsdRaw<float, V> sr;
+    float *state = a.state + r * a.width + c;
+    gr.load_cs(static_cast<const T *>(a.g) + r * a.g_stride + c);
+    xr.load_cs(static_cast<const T *>(a.x) + r * a.x_stride + c);
+    sr.load_cs(state);
+    if constexpr (kGate) zr.load_cs(static_cast<const T *>(a.z) + r * a.z_stride + c);
+    float h[V], y[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        Val<1> g, keep, drop;
+        g[0] = gr.get(k);
+        gate(g, keep, drop);
+        h[k] = keep[0] * sr.get(k) + drop[0] * xr.get(k);
+        y[k] = h[k];
+        if constexpr (kGate) {
+            Val<1> z;
+            z[0] = zr.get(k);
+            y[k] *= z[0] * sigmoid(z)[0];
+        }
     }
-    ssd_st(static_cast<T *>(a.y) + i, y);
+    ssd_store_vec<V>(state, h);
+    ssd_store_vec<V>(static_cast<T *>(a.y) + r * a.width + c, y);
 }
 
 }  // namespace
@@ -879,9 +891,23 @@ cudaError_t ssd_launch_gated_bwd(const SsdGatedBwd &a, int sms, void *ws, unsign
                 : launch_bwd<float, 1, false>(a, sms, ws, err, stream);
 }
 
-cudaError_t ssd_launch_gated_step(const SsdGatedStep &a, cudaStream_t stream) {
-    const unsigned grid = (unsigned)(((size_t)a.rows * a.width + 255) / 256);
-    if (a.bf16) gated_step_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a);
-    else gated_step_kernel<float><<<grid, 256, 0, stream>>>(a);
+template <typename T, int V>
+static cudaError_t launch_step(const SsdGatedStep &a, cudaStream_t stream) {
+    const dim3 grid((unsigned)a.rows, (unsigned)((a.width + 256 * V - 1) / (256 * V)));
+    if (a.z) gated_step_kernel<T, V, true><<<grid, 256, 0, stream>>>(a);
+    else gated_step_kernel<T, V, false><<<grid, 256, 0, stream>>>(a);
     return cudaGetLastError();
+}
+
+cudaError_t ssd_launch_gated_step(const SsdGatedStep &a, cudaStream_t stream) {
+    const size_t size = a.bf16 ? 2 : 4;
+    const auto four = [&](const void *p, long long stride, size_t bytes) {
+        return !p || ((uintptr_t)p % (4 * bytes) == 0 && stride % 4 == 0);
+    };
+    const bool v4 = a.width % 4 == 0 && four(a.state, a.width, 4) && four(a.x, a.x_stride, size) &&
+                    four(a.g, a.g_stride, size) && four(a.z, a.z_stride, size) &&
+                    four(a.y, a.width, size);
+    if (a.bf16)
+        return v4 ? launch_step<__nv_bfloat16, 4>(a, stream) : launch_step<__nv_bfloat16, 1>(a, stream);
+    return v4 ? launch_step<float, 4>(a, stream) : launch_step<float, 1>(a, stream);
 }

@@ -150,14 +150,17 @@ cudaError_t launch(const SsdProduct &p, cudaStream_t stream) {
 
 // Few CTAs an SM: many warps in each, so all of the SM's loads are under way;
 // many CTAs: few warps, so each takes several steps between its start and its
-// barrier.  us for one token in bf16, 16 / 8 / 4 warps: 15360 features of 2560
-// (6.3 CTAs an SM) 20.0 / 17.4 / 15.9; 2560 of 5120 (1.05) 7.9 / 11.7 / 21.0.
+// barrier, unless k is long (64 steps and more) and a lane's loads few.  us in
+// bf16 by 16 / 8 / 4 warps for one token: 15360 features of 2560 (6.3 CTAs an SM)
+// 20.0 / 17.4 / 14.6; 10240 of 5120 (4.2) - / 19.4 / 22.6; 2560 of 5120 (1.05)
+// 7.9 / 11.7 / 21.0; for sixteen tokens 24.8 / 21.0 / 16.4, - / 33.7 / 24.0,
+// 9.8 / 14.3 / 26.4.
 template <bool kFp8, int kNT>
 cudaError_t launch_warps(const SsdProduct &p, int sms, cudaStream_t stream) {
-    const long long ctas = (p.n + kRows - 1) / kRows;
+    const long long ctas = (p.n + kRows - 1) / kRows, steps = p.k * (kFp8 ? 1 : 2) / 128;
     if (ctas <= 2ll * sms) return launch<kFp8, kNT, 16, 1>(p, stream);
-    if (ctas <= 4ll * sms) return launch<kFp8, kNT, 8, 2>(p, stream);
-    return launch<kFp8, kNT, 4, 4>(p, stream);
+    if (ctas <= 4ll * sms || (kNT == 1 && steps >= 64)) return launch<kFp8, kNT, 8, 2>(p, stream);
+    return launch<kFp8, kNT, 4, kFp8 || kNT == 1 ? 5 : 4>(p, stream);
 }
 
 }  // namespace
