@@ -53,7 +53,7 @@ struct Args {
     SsdProduct p;           // rows of A are p.m, or (kSwap) p.n
     int row_tiles, col_tiles, kblocks;
     int tile0, tile1;       // the tiles of this launch
-    bool vec;               // 16-byte rows of out, preact, residual; bias and b_scale on 16 bytes
+    bool vec;               // rows of out, preact and residual on 16 bytes
     unsigned *err;
     unsigned long long wait_ns;
 };
@@ -114,7 +114,7 @@ __device__ __forceinline__ void act_all(float (&v)[N], SsdAct act) {
 // The bias and scale of a warp's half of a tile's columns (32 of every 64), in
 // shared memory of its own, so that no barrier stands between it and the others.
 struct Columns {
-    float bias[128], scale[128];
+    alignas(16) float bias[128], scale[128];
 };
 constexpr uint32_t kColumnBytes = kEpiWarps * sizeof(Columns);
 constexpr uint32_t smem_bytes(int bn) {
@@ -138,65 +138,72 @@ __device__ __forceinline__ void fetch_columns(const Args &a, Columns *cols, int 
     __syncwarp();
 }
 
-// One value, for the edges: out of line, so the epilogue's code stays small.
-__device__ __noinline__ void finish_edge(const SsdProduct &p, long long m, long long n, float v) {
-    if (m < p.m && n < p.n) ssd_finish(p, m, n, v);
-}
-
-// N columns n .. n + N - 1 of row m, their bias and scale at `bias` and `scale`.
-// Rows of 16-byte vectors and all columns in range: whole vectors; else value by
-// value.  `r`: the residual's values, if whole.
+// N columns n .. n + N - 1 of row m: vectors of 8 where the rows of out, preact and
+// residual have 16-byte vectors, value by value where not and in the last columns.
+// `residual` holds its whole vectors.  Value by value through one out-of-line
+// function, which the last 16 of 944 columns took, was 20.5 against 7.6 us for 388 x
+// 560 -> 944, and 41 against 22 us with all rows unaligned (1000 x 1024 -> 1001).
 template <typename TO, int N>
 struct RowPart {
     SsdRaw<TO, 8> residual[N / 8];
-    bool whole;
+    int left, vectors;          // columns in range, and how many vectors of them
     __device__ __forceinline__ void ask(const Args &a, long long m, long long n) {
-        whole = a.vec && n + N <= a.p.n;
-        if (!whole || m >= a.p.m || !a.p.residual) return;
+        left = (int)max(0ll, min((long long)N, a.p.n - n));
+        vectors = a.vec ? left / 8 : 0;
+        if (m >= a.p.m || !a.p.residual) return;
         const TO *res = static_cast<const TO *>(a.p.residual) + m * a.p.residual_row + n;
 #pragma unroll
-        for (int j = 0; j < N / 8; ++j) residual[j].load(res + 8 * j);
+        for (int j = 0; j < N / 8; ++j)
+            if (j < vectors) residual[j].load(res + 8 * j);
     }
-    __device__ __forceinline__ void finish(const Args &a, long long m, long long n, float row_scale,
-                                           const float *bias, const float *scale, float (&v)[N]) {
-        const SsdProduct &p = a.p;
-        if (!whole) {
+    template <typename T>
+    __device__ __forceinline__ void store(T *out, const float (&v)[N]) const {
 #pragma unroll
-            for (int i = 0; i < N; ++i) finish_edge(p, m, n + i, v[i]);
-            return;
+        for (int j = 0; j < N / 8; ++j) {
+            float o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = v[8 * j + i];
+            if (j < vectors) ssd_store_vec<8>(out + 8 * j, o);
         }
-        if (m >= p.m) return;
+        if (8 * vectors == left) return;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float o[1] = {v[i]};
+            if (i >= 8 * vectors && i < left) ssd_store_vec<1>(out + i, o);
+        }
+    }
+    // bias(i), scale(i): column n + i's
+    template <typename B, typename S>
+    __device__ __forceinline__ void finish(const Args &a, long long m, long long n, float row_scale,
+                                           B &&bias, S &&scale, float (&v)[N]) {
+        const SsdProduct &p = a.p;
+        if (left == 0 || m >= p.m) return;
         if (p.a_scale) {
 #pragma unroll
-            for (int j = 0; j < N; j += 4) {
-                const float4 s = *reinterpret_cast<const float4 *>(scale + j);
-                v[j] *= row_scale * s.x, v[j + 1] *= row_scale * s.y;
-                v[j + 2] *= row_scale * s.z, v[j + 3] *= row_scale * s.w;
-            }
+            for (int i = 0; i < N; ++i) v[i] *= row_scale * scale(i);
         }
         if (p.bias) {
 #pragma unroll
-            for (int j = 0; j < N; j += 4) {
-                const float4 b = *reinterpret_cast<const float4 *>(bias + j);
-                v[j] += b.x, v[j + 1] += b.y, v[j + 2] += b.z, v[j + 3] += b.w;
-            }
+            for (int i = 0; i < N; ++i) v[i] += bias(i);
         }
-        const auto store = [&](auto *out) {
-#pragma unroll
-            for (int j = 0; j < N / 8; ++j) {
-                float o[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = v[8 * j + i];
-                ssd_store_vec<8>(out + 8 * j, o);
-            }
-        };
-        if (p.preact) store(static_cast<__nv_bfloat16 *>(p.preact) + m * p.n + n);
+        if (p.preact) store(static_cast<__nv_bfloat16 *>(p.preact) + m * p.n + n, v);
         act_all(v, p.act);
         if (p.residual) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] += residual[i / 8].get(i % 8);
+            for (int i = 0; i < N; ++i)
+                if (i < 8 * vectors) v[i] += residual[i / 8].get(i % 8);
+            if (8 * vectors < left) {
+                const TO *res = static_cast<const TO *>(p.residual) + m * p.residual_row + n;
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    SsdRaw<TO, 1> one;
+                    one.zero();
+                    if (i >= 8 * vectors && i < left) one.load(res + i);
+                    v[i] += one.get(0);
+                }
+            }
         }
-        store(static_cast<TO *>(p.out) + m * p.out_row + n);
+        store(static_cast<TO *>(p.out) + m * p.out_row + n, v);
     }
 };
 
@@ -229,7 +236,13 @@ __device__ __forceinline__ bool drain(const Args &a, const Columns *cols, uint32
         float v[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-        part.finish(a, m, n0 + c, scale, cols->bias + c / 64 * 32, cols->scale + c / 64 * 32, v);
+        const auto at = [&](const float *q) {
+            return [=](int i) {
+                const float4 w = reinterpret_cast<const float4 *>(q + c / 64 * 32)[i / 4];
+                return i % 4 == 0 ? w.x : i % 4 == 1 ? w.y : i % 4 == 2 ? w.z : w.w;
+            };
+        };
+        part.finish(a, m, n0 + c, scale, at(cols->bias), at(cols->scale), v);
     }
     return true;
 }
@@ -309,7 +322,10 @@ __device__ __forceinline__ void finish_split(const Args &a, uint32_t ring, int r
             float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
             const auto last = [&](auto part) {
                 part.ask(a, m, n);
-                part.finish(a, m, n, scale, a.p.bias + n, a.p.b_scale + n, v);
+                const auto at = [&](const float *q) {
+                    return [=](int i) { return i < part.left ? __ldg(q + n + i) : 0.f; };
+                };
+                part.finish(a, m, n, scale, at(a.p.bias), at(a.p.b_scale), v);
             };
             if (a.p.out_type == SSD_ELT_F32) last(RowPart<float, 8>{});
             else last(RowPart<__nv_bfloat16, 8>{});
@@ -706,7 +722,7 @@ Args args_of(const SsdProduct &p, int bm, int bn, bool fp8, unsigned *err) {
     a.kblocks = (int)((p.k + (fp8 ? 127 : 63)) / (fp8 ? 128 : 64));
     const int so = p.out_type == SSD_ELT_F32 ? 4 : 2;
     a.vec = on_16(p.out, p.out_row, so) && (!p.residual || on_16(p.residual, p.residual_row, so)) &&
-            (!p.preact || on_16(p.preact, p.n, 2)) && on_16(p.bias, 0, 4) && on_16(p.b_scale, 0, 4);
+            (!p.preact || on_16(p.preact, p.n, 2));
     a.err = err;
     a.wait_ns = ssd_debug_config().wait_ns;
     return a;
