@@ -45,6 +45,9 @@ ssd_status check_linear(ssd_dtype in, long long tokens, int features, int inner)
 bool valid_activation(ssd_activation a) { return a >= SSD_ACT_NONE && a <= SSD_ACT_RELU; }
 
 // The product on the path its types and alignments take.
+bool on_tensor_cores(const SsdProduct &p) {
+    return !ssd_product_few_handles(p) && !ssd_product_gemv_handles(p) && ssd_product_tc_handles(p);
+}
 cudaError_t launch_product(const SsdProduct &p, cudaStream_t stream) {
     if (ssd_product_few_handles(p)) return ssd_launch_product_few(p, ssd_sm_count(), stream);
     if (ssd_product_gemv_handles(p)) return ssd_launch_product_gemv(p, stream);
@@ -255,16 +258,19 @@ ssd_status ssd_linear_bwd(const void *dy, const void *x, const void *w, const vo
             ssd_launch_act_bwd(a, reinterpret_cast<float *>(ws + plan.dp), sms, stream);
         if (e != cudaSuccess) return SSD_ERR_CUDA;
     }
-    if (dx) {   // dx[m][k] = sum_n dp[m][n] w[n][k]
-        SsdProduct p{dp, w, t, tokens, inner, features, dp_stride, 1, 1, inner, nullptr, nullptr,
-                     nullptr, nullptr, 0, SsdAct::none, dx, nullptr, t, t, inner};
-        if (launch_product(p, stream) != cudaSuccess) return SSD_ERR_CUDA;
+    // dx[m][k] = sum_n dp[m][n] w[n][k], dw[n][k] = sum_m dp[m][n] x[m][k]
+    const SsdProduct px{dp, w, t, tokens, inner, features, dp_stride, 1, 1, inner, nullptr, nullptr,
+                        nullptr, nullptr, 0, SsdAct::none, dx, nullptr, t, t, inner};
+    const SsdProduct pw{dp, x, t, features, inner, tokens, 1, dp_stride, 1, x_stride, nullptr,
+                        nullptr, nullptr, nullptr, 0, SsdAct::none, dw, nullptr, t, t, inner};
+    cudaError_t e = cudaSuccess;
+    if (dx && dw && on_tensor_cores(px) && on_tensor_cores(pw)) {
+        e = ssd_launch_product_two(px, pw, sms, ssd_device_error_word(), stream);
+    } else {
+        if (dx) e = launch_product(px, stream);
+        if (dw && e == cudaSuccess) e = launch_product(pw, stream);
     }
-    if (dw) {   // dw[n][k] = sum_m dp[m][n] x[m][k]
-        SsdProduct p{dp, x, t, features, inner, tokens, 1, dp_stride, 1, x_stride, nullptr,
-                     nullptr, nullptr, nullptr, 0, SsdAct::none, dw, nullptr, t, t, inner};
-        if (launch_product(p, stream) != cudaSuccess) return SSD_ERR_CUDA;
-    }
+    if (e != cudaSuccess) return SSD_ERR_CUDA;
     return SSD_OK;
 }
 

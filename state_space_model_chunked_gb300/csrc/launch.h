@@ -228,6 +228,10 @@ cudaError_t ssd_launch_product_gemv(const SsdProduct &p, cudaStream_t stream);
 bool ssd_product_tc_handles(const SsdProduct &p);
 cudaError_t ssd_launch_product_tc(const SsdProduct &p, int sms, unsigned *err,
                                   cudaStream_t stream);
+// A gradient's two products on the tensor cores: `dx` of a K-major A and a B with its
+// rows contiguous, `dw` with both operands' rows contiguous.
+cudaError_t ssd_launch_product_two(const SsdProduct &dx, const SsdProduct &dw, int sms,
+                                   unsigned *err, cudaStream_t stream);
 
 // dp = dy act'(preact) (dp null: not stored) and the column sums of dp
 // (dbias null: none; `partial` holds ssd_act_bwd_workspace bytes).

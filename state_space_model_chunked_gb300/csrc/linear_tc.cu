@@ -527,10 +527,48 @@ constexpr uint32_t kPairStage = 2 * kABytes;
 constexpr int kPairStages = kRingBytes / kPairStage;
 static_assert(kPairStages <= kMaxStages, "stages");
 
-template <bool kAmn, bool kBmn, bool kFp8, bool kSplit>
+struct Job {
+    CUtensorMap map_a, map_b;
+    Args a;
+};
+// One product, or (kTwo) two whose tiles one launch computes: the pairs take the
+// first one's tiles in turn, then the second one's.  The first `late` pairs have one
+// more of the first product's tiles than the others, so those begin with `extra`
+// of the second's for themselves; then all take them in turn.
+template <bool kTwo>
+struct Jobs {
+    Job job[kTwo ? 2 : 1];
+    int late, extra;
+    int amn;                // kTwo: which product's A is MN-major
+};
+struct Place {
+    int job, row, col;
+};
+// Tile number j of pair `pair` of `pairs`; false past its last one.
+template <bool kTwo>
+__device__ __forceinline__ bool place(const Jobs<kTwo> &jobs, int pair, int pairs, int j, Place &at) {
+    const Args &one = jobs.job[0].a;
+    int t = one.tile0 + pair + j * pairs;
+    at.job = 0;
+    if (t >= one.tile1) {
+        if constexpr (!kTwo) return false;
+        const Args &two = jobs.job[kTwo ? 1 : 0].a;
+        at.job = 1;
+        j -= (one.tile1 - pair + pairs - 1) / pairs;
+        const int own = jobs.extra * (pairs - jobs.late);
+        if (pair < jobs.late) t = own + j * pairs + pair;
+        else if (j < jobs.extra) t = j * (pairs - jobs.late) + pair - jobs.late;
+        else t = own + (j - jobs.extra) * pairs + pair;
+        if (t >= two.tile1) return false;
+    }
+    tile_at(jobs.job[at.job].a, t, at.row, at.col);
+    return true;
+}
+
+template <bool kAmn, bool kBmn, bool kFp8, bool kSplit, bool kTwo>
 __global__ void __launch_bounds__(kThreads, 1)
-product_pair_kernel(const __grid_constant__ CUtensorMap map_a,
-                    const __grid_constant__ CUtensorMap map_b, const __grid_constant__ Args a) {
+product_pair_kernel(const __grid_constant__ Jobs<kTwo> jobs) {
+    const Args &a = jobs.job[0].a;
     extern __shared__ __align__(1024) uint8_t smem[];
     constexpr int kK = kFp8 ? 128 : 64;
     Ctrl *ctl = reinterpret_cast<Ctrl *>(smem);
@@ -566,22 +604,32 @@ product_pair_kernel(const __grid_constant__ CUtensorMap map_a,
     cluster_sync_all();         // both CTAs' barriers and tensor memory stand
     tc_fence_after();
     const uint32_t tmem = ctl->tmem;
-    const int ntiles = a.tile1, step = kSplit ? ntiles : (int)gridDim.x / 2;
-    const int first = a.tile0 + blockIdx.x / (2 * parts);
-    const int kb0 = (int)((long long)a.kblocks * part / parts);
-    const int kb1 = (int)((long long)a.kblocks * (part + 1) / parts);
+    // this pair's tiles: one with kSplit, and of that a part of the k blocks
+    const int pair = (int)blockIdx.x / (2 * parts), pairs = (int)gridDim.x / (2 * parts);
+    const auto tile = [&](int j, Place &at) {
+        return (!kSplit || j == 0) && place(jobs, pair, pairs, j, at);
+    };
+    const auto blocks = [&](const Place &at, int &kb0, int &kb1) {
+        const int n = jobs.job[at.job].a.kblocks;
+        kb0 = kSplit ? (int)((long long)n * part / parts) : 0;
+        kb1 = kSplit ? (int)((long long)n * (part + 1) / parts) : n;
+    };
 
     if (warp == 0) {
         if (lane == 0) {
-            tma_prefetch_desc(&map_a);
-            tma_prefetch_desc(&map_b);
+            for (const Job &job : jobs.job) {
+                tma_prefetch_desc(&job.map_a);
+                tma_prefetch_desc(&job.map_b);
+            }
             uint32_t n = 0;
             bool ok = true;
-            for (int t = first; ok && t < ntiles; t += step) {
-                int row, col;
-                tile_at(a, t, row, col);
-                const int ar = row * 256 + rank * 128, br = col * 256 + rank * 128;
-                for (int kb = kSplit ? kb0 : 0; kb < (kSplit ? kb1 : a.kblocks); ++kb, ++n) {
+            Place at;
+            for (int j = 0; ok && tile(j, at); ++j) {
+                const CUtensorMap *map_a = &jobs.job[at.job].map_a, *map_b = &jobs.job[at.job].map_b;
+                const int ar = at.row * 256 + rank * 128, br = at.col * 256 + rank * 128;
+                const bool amn = kTwo ? at.job == jobs.amn : kAmn;
+                int kb, kb1;
+                for (blocks(at, kb, kb1); kb < kb1; ++kb, ++n) {
                     const uint32_t s = n % kPairStages, turn = n / kPairStages;
                     if (turn > 0 && !wait(&ctl->empty[s], (turn - 1) & 1, ctl, a)) {
                         ok = false;
@@ -590,17 +638,17 @@ product_pair_kernel(const __grid_constant__ CUtensorMap map_a,
                     const uint32_t own = smem_u32(&ctl->full[s]), bar = cluster_map(own, leader);
                     const uint32_t dst = ring + s * kPairStage;
                     if (rank == 0) mbar_arrive_expect_tx(own, 2 * kPairStage);
-                    if constexpr (kAmn) {
-                        tma_load_2d_pair(dst, &map_a, bar, ar, kb * kK);
-                        tma_load_2d_pair(dst + 8192, &map_a, bar, ar + 64, kb * kK);
+                    if (amn) {
+                        tma_load_2d_pair(dst, map_a, bar, ar, kb * kK);
+                        tma_load_2d_pair(dst + 8192, map_a, bar, ar + 64, kb * kK);
                     } else {
-                        tma_load_2d_pair(dst, &map_a, bar, kb * kK, ar);
+                        tma_load_2d_pair(dst, map_a, bar, kb * kK, ar);
                     }
                     if constexpr (kBmn) {
-                        tma_load_2d_pair(dst + kABytes, &map_b, bar, br, kb * kK);
-                        tma_load_2d_pair(dst + kABytes + 8192, &map_b, bar, br + 64, kb * kK);
+                        tma_load_2d_pair(dst + kABytes, map_b, bar, br, kb * kK);
+                        tma_load_2d_pair(dst + kABytes + 8192, map_b, bar, br + 64, kb * kK);
                     } else {
-                        tma_load_2d_pair(dst + kABytes, &map_b, bar, kb * kK, br);
+                        tma_load_2d_pair(dst + kABytes, map_b, bar, kb * kK, br);
                     }
                 }
             }
@@ -611,21 +659,25 @@ product_pair_kernel(const __grid_constant__ CUtensorMap map_a,
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
-            constexpr uint32_t kId = kFp8 ? idesc_e4m3_f32(256, kPairBN)
-                                          : idesc_bf16_f32(256, kPairBN, kAmn, kBmn);
-            const uint64_t ad = smem_desc(ring, kAmn ? 8192 : 16, 1024, kSwizzle128B);
             const uint64_t bd = smem_desc(ring + kABytes, kBmn ? 8192 : 16, 1024, kSwizzle128B);
-            constexpr uint64_t kAStep = kAmn ? 2048 >> 4 : 32 >> 4;
             constexpr uint64_t kBStep = kBmn ? 2048 >> 4 : 32 >> 4;
             const uint16_t both = (uint16_t)(3u << leader);
-            uint32_t n = 0, tiles = 0;
+            uint32_t n = 0;
             bool ok = true;
-            for (int t = first; ok && t < ntiles; t += step, ++tiles) {
-                const uint32_t buf = tiles & 1, turn = tiles >> 1;
+            Place at;
+            for (int j = 0; ok && tile(j, at); ++j) {
+                const uint32_t buf = j & 1, turn = (uint32_t)j >> 1;
                 const uint32_t d = tmem + buf * kPairBN;
+                const bool amn = kTwo ? at.job == jobs.amn : kAmn;
+                const uint32_t id = kFp8 ? idesc_e4m3_f32(256, kPairBN)
+                                         : idesc_bf16_f32(256, kPairBN, amn, kBmn);
+                const uint64_t ad = smem_desc(ring, amn ? 8192 : 16, 1024, kSwizzle128B);
+                const uint64_t a_step = amn ? 2048 >> 4 : 32 >> 4;
                 if (turn > 0 && !wait(&ctl->acc_empty[buf], (turn - 1) & 1, ctl, a)) break;
                 tc_fence_after();
-                for (int kb = kSplit ? kb0 : 0; kb < (kSplit ? kb1 : a.kblocks); ++kb, ++n) {
+                int kb, kb1;
+                bool more = false;      // the tile's first product writes, the others add
+                for (blocks(at, kb, kb1); kb < kb1; ++kb, ++n) {
                     const uint32_t s = n % kPairStages;
                     if (!wait(&ctl->full[s], (n / kPairStages) & 1, ctl, a)) {
                         ok = false;
@@ -635,8 +687,9 @@ product_pair_kernel(const __grid_constant__ CUtensorMap map_a,
                     const uint64_t off = (uint64_t)(s * kPairStage) >> 4;
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        mma_ss_pair<kFp8>(d, ad + off + i * kAStep, bd + off + i * kBStep, kId,
-                                          kb > (kSplit ? kb0 : 0) || i > 0);
+                        mma_ss_pair<kFp8>(d, ad + off + i * a_step, bd + off + i * kBStep, id,
+                                          more || i > 0);
+                    more = true;
                     mma_commit_pair(smem_u32(&ctl->empty[s]), both);
                 }
                 if (ok) mma_commit_pair(smem_u32(&ctl->acc_full[buf]), both);
@@ -654,15 +707,13 @@ product_pair_kernel(const __grid_constant__ CUtensorMap map_a,
             if (wait_warp(&ctl->acc_full[0], 0, ctl, a))
                 store_sums<kPairBN>(smem + kCtrlBytes, tmem + lanes, quarter * 32 + lane, half);
         }
-        uint32_t tiles = 0;
-        for (int t = first; !kSplit && t < ntiles; t += step, ++tiles) {
-            const uint32_t buf = tiles & 1, turn = tiles >> 1;
-            int row, col;
-            tile_at(a, t, row, col);
+        Place at;
+        for (int j = 0; !kSplit && tile(j, at); ++j) {
+            const uint32_t buf = j & 1, turn = (uint32_t)j >> 1;
             if (!drain_accumulator<kPairBN>(
-                    a, cols, tmem + lanes + buf * kPairBN, half,
-                    (long long)row * 256 + rank * 128 + quarter * 32 + lane,
-                    (long long)col * kPairBN,
+                    jobs.job[at.job].a, cols, tmem + lanes + buf * kPairBN, half,
+                    (long long)at.row * 256 + rank * 128 + quarter * 32 + lane,
+                    (long long)at.col * kPairBN,
                     [&]() { return wait_warp(&ctl->acc_full[buf], turn & 1, ctl, a); },
                     [&]() {
                         if (lane == 0)
@@ -674,14 +725,12 @@ product_pair_kernel(const __grid_constant__ CUtensorMap map_a,
     if constexpr (kSplit) {
         __syncwarp();
         cluster_sync_all();
-        if (warp >= 2 && !ctl->abort) {
-            int row, col;
-            tile_at(a, first, row, col);
+        Place at;
+        if (warp >= 2 && !ctl->abort && tile(0, at))
             finish_split<kPairBN, false>(a, smem_u32(smem) + kCtrlBytes, (warp & 3) * 32 + lane,
                                          (warp - 2) >> 2, part, parts, 2, rank,
-                                         (long long)row * 256 + rank * 128,
-                                         (long long)col * kPairBN);
-        }
+                                         (long long)at.row * 256 + rank * 128,
+                                         (long long)at.col * kPairBN);
     }
     __syncwarp();
     tc_fence_before();
@@ -728,11 +777,10 @@ Args args_of(const SsdProduct &p, int bm, int bn, bool fp8, unsigned *err) {
     return a;
 }
 
-using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const Args);
-
 // Clusters of r CTAs that the device holds at once.  They do not span the SMs'
 // groups, so that can be fewer than the SMs over r.  Every kernel here takes an
 // SM to itself, so one answer serves them all; it is asked for once.
+template <typename Kernel>
 int clusters_at_once(Kernel kernel, cudaLaunchConfig_t cfg, int r) {
     static std::atomic<int> known[9];       // the answer plus one; 0: not asked yet
     int n = known[r].load(std::memory_order_relaxed) - 1;
@@ -750,6 +798,7 @@ int clusters_at_once(Kernel kernel, cudaLaunchConfig_t cfg, int r) {
 // Ranks of a split: the largest cluster of which there is one for every tile at
 // once (with 20 tiles, seven ranks took two waves), of at least two k blocks a
 // rank, at most eight (portable cluster size).
+template <typename Kernel>
 int split_ranks(Kernel kernel, const cudaLaunchConfig_t &cfg, long long tiles, long long kblocks) {
     for (int r = 8; r > 1; --r)
         if (kblocks >= 2 * r && tiles <= clusters_at_once(kernel, cfg, r)) return r;
@@ -791,46 +840,54 @@ cudaError_t launch(const SsdProduct &p, int sms, unsigned *err, cudaStream_t str
     return cudaLaunchKernelEx(&cfg, kernel, ma, mb, a);
 }
 
-// Pairs over the tiles tile0 .. tile1 - 1 (row by row of groups, as tile_at has
-// them; tile1 < 0: to the last).
+// A product's operands and tiles tile0 .. tile1 - 1 (row by row of groups, as
+// tile_at has them; tile1 < 0: to the last) for pairs.
+bool pair_job(Job *job, const SsdProduct &p, bool amn, bool bmn, bool fp8, int tile0, int tile1,
+              unsigned *err) {
+    job->a = args_of(p, 256, kPairBN, fp8, err);
+    job->a.tile0 = tile0;
+    job->a.tile1 = tile1 < 0 ? job->a.row_tiles * job->a.col_tiles : tile1;
+    return operand_map(&job->map_a, p.a, fp8, amn, p.m, p.k, amn ? p.a_col : p.a_row, kBM) &&
+           operand_map(&job->map_b, p.b, fp8, bmn, p.n, p.k, bmn ? p.b_col : p.b_row, 128);
+}
+
+// The launch of a kernel of pairs, `cfg` and its one attribute but for the grid
+// and the cluster's size.
+template <typename Kernel>
+cudaError_t pair_config(Kernel kernel, cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr,
+                        cudaStream_t stream) {
+    constexpr uint32_t kSmem = kCtrlBytes + kPairStages * kPairStage + kColumnBytes;
+    attr->id = cudaLaunchAttributeClusterDimension;
+    attr->val.clusterDim.x = 2;
+    attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+    *cfg = {};
+    cfg->blockDim = dim3(kThreads);
+    cfg->dynamicSmemBytes = kSmem;
+    cfg->stream = stream;
+    cfg->attrs = attr;
+    cfg->numAttrs = 1;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+}
+
 template <bool kAmn, bool kBmn, bool kFp8, bool kSplit>
 cudaError_t launch_pair(const SsdProduct &p, int tile0, int tile1, unsigned *err,
                         cudaStream_t stream) {
-    constexpr uint32_t kSmem = kCtrlBytes + kPairStages * kPairStage + kColumnBytes;
-    Args a = args_of(p, 256, kPairBN, kFp8, err);
-    a.tile0 = tile0;
-    a.tile1 = tile1 < 0 ? a.row_tiles * a.col_tiles : tile1;
-    CUtensorMap ma, mb;
-    if (!operand_map(&ma, p.a, kFp8, kAmn, p.m, p.k, kAmn ? p.a_col : p.a_row, kBM) ||
-        !operand_map(&mb, p.b, kFp8, kBmn, p.n, p.k, kBmn ? p.b_col : p.b_row, 128))
-        return cudaErrorInvalidValue;
-    const auto kernel = product_pair_kernel<kAmn, kBmn, kFp8, kSplit>;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    Jobs<false> jobs{};
+    if (!pair_job(&jobs.job[0], p, kAmn, kBmn, kFp8, tile0, tile1, err)) return cudaErrorInvalidValue;
+    const Args &a = jobs.job[0].a;
+    const auto kernel = product_pair_kernel<kAmn, kBmn, kFp8, kSplit, false>;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr;
+    const cudaError_t e = pair_config(kernel, &cfg, &attr, stream);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
     const long long tiles = a.tile1 - a.tile0;
-    if (kSplit) {
-        int parts = 4;
-        while (parts > 1 && (a.kblocks < 2 * parts || tiles > clusters_at_once(kernel, cfg, 2 * parts)))
-            --parts;
-        attr[0].val.clusterDim.x = 2 * parts;
-        cfg.gridDim = dim3((unsigned)(2 * parts * tiles));
-    } else {
-        const long long pairs = std::max(1, clusters_at_once(kernel, cfg, 2));
-        attr[0].val.clusterDim.x = 2;
-        cfg.gridDim = dim3((unsigned)(2 * std::min(tiles, pairs)));
-    }
-    return cudaLaunchKernelEx(&cfg, kernel, ma, mb, a);
+    int parts = kSplit ? 4 : 1;
+    while (parts > 1 && (a.kblocks < 2 * parts || tiles > clusters_at_once(kernel, cfg, 2 * parts)))
+        --parts;
+    const long long pairs = kSplit ? tiles : std::min<long long>(tiles, std::max(1, clusters_at_once(kernel, cfg, 2)));
+    attr.val.clusterDim.x = 2 * parts;
+    cfg.gridDim = dim3((unsigned)(2 * parts * pairs));
+    return cudaLaunchKernelEx(&cfg, kernel, jobs);
 }
 
 template <bool kFp8>
@@ -849,34 +906,77 @@ cudaError_t few_tokens(const SsdProduct &p, int sms, unsigned *err, cudaStream_t
 // split, in a launch of their own for another 100 units (gradients at 2635 x 7664 x
 // 1952: 147 against 164 us; at 16376 x 2048 x 1024, where it does not pay, 103
 // against 98).
-template <bool kAmn, bool kBmn, bool kFp8>
-cudaError_t many(const SsdProduct &p, int sms, unsigned *err, cudaStream_t stream) {
-    const auto tiles = [&](int rows, int cols) {
-        return (p.m + rows - 1) / rows * ((p.n + cols - 1) / cols);
-    };
-    const long long kb = (p.k + (kFp8 ? 127 : 63)) / (kFp8 ? 128 : 64);
+constexpr long long kBlockCost = 4, kPairEpilogue = 40, kLaunchCost = 100;
+enum class Way { whole, pairs, split, split_pairs, pairs_and_split };
+struct Choice {
+    Way way;
+    long long cost;
+    int full;               // tiles of whole rounds of pairs
+};
+long long tiles_of(const SsdProduct &p, int rows, int cols) {
+    return (p.m + rows - 1) / rows * ((p.n + cols - 1) / cols);
+}
+long long kblocks_of(const SsdProduct &p, bool fp8) {
+    return (p.k + (fp8 ? 127 : 63)) / (fp8 ? 128 : 64);
+}
+Choice choose(const SsdProduct &p, bool fp8, int sms) {
+    const long long kb = kblocks_of(p, fp8), never = std::numeric_limits<long long>::max();
     const auto whole = [&](long long n, int slots, long long epilogue) {
-        return (n + slots - 1) / slots * std::max(4 * kb, epilogue) + epilogue;
+        return (n + slots - 1) / slots * std::max(kBlockCost * kb, epilogue) + epilogue;
     };
-    const auto split = [&](long long n, int ctas, int block, int most) {
+    const auto split = [&](long long n, int ctas, int most) {
         const long long r = std::min({sms * 7ll / 8 / (ctas * n), kb / 2, (long long)most});
-        return r < 2 ? std::numeric_limits<long long>::max() : (kb + r - 1) / r * block + 50;
+        return r < 2 ? never : (kb + r - 1) / r * kBlockCost + 50;
     };
     const int pairs = sms / 2;
-    const long long large = tiles(256, 256), full = large / pairs * pairs;
-    const long long never = std::numeric_limits<long long>::max();
-    const long long rest = full > 0 && full < large ? split(large - full, 2, 4, 4) : never;
-    const long long t[5] = {whole(tiles(128, 128), sms, 20), whole(large, pairs, 40),
-                            split(tiles(128, 128), 1, 4, 8), split(large, 2, 4, 4),
-                            rest == never ? never : whole(full, pairs, 40) + rest + 100};
+    const long long small = tiles_of(p, 128, 128), large = tiles_of(p, 256, 256);
+    const long long full = large / pairs * pairs;
+    const long long rest = full > 0 && full < large ? split(large - full, 2, 4) : never;
+    const long long t[5] = {whole(small, sms, 20), whole(large, pairs, kPairEpilogue),
+                            split(small, 1, 8), split(large, 2, 4),
+                            rest == never ? never
+                                          : whole(full, pairs, kPairEpilogue) + rest + kLaunchCost};
     const int best = (int)(std::min_element(t, t + 5) - t);
-    if (best == 0) return launch<128, kAmn, kBmn, kFp8, false, false>(p, sms, err, stream);
-    if (best == 1) return launch_pair<kAmn, kBmn, kFp8, false>(p, 0, -1, err, stream);
-    if (best == 2) return launch<128, kAmn, kBmn, kFp8, false, true>(p, sms, err, stream);
-    if (best == 3) return launch_pair<kAmn, kBmn, kFp8, true>(p, 0, -1, err, stream);
-    const cudaError_t e = launch_pair<kAmn, kBmn, kFp8, false>(p, 0, (int)full, err, stream);
-    return e != cudaSuccess ? e
-                            : launch_pair<kAmn, kBmn, kFp8, true>(p, (int)full, -1, err, stream);
+    return {(Way)best, t[best], (int)full};
+}
+
+template <bool kAmn, bool kBmn, bool kFp8>
+cudaError_t many(const SsdProduct &p, int sms, unsigned *err, cudaStream_t stream) {
+    const Choice c = choose(p, kFp8, sms);
+    switch (c.way) {
+        case Way::whole: return launch<128, kAmn, kBmn, kFp8, false, false>(p, sms, err, stream);
+        case Way::pairs: return launch_pair<kAmn, kBmn, kFp8, false>(p, 0, -1, err, stream);
+        case Way::split: return launch<128, kAmn, kBmn, kFp8, false, true>(p, sms, err, stream);
+        case Way::split_pairs: return launch_pair<kAmn, kBmn, kFp8, true>(p, 0, -1, err, stream);
+        default: break;
+    }
+    const cudaError_t e = launch_pair<kAmn, kBmn, kFp8, false>(p, 0, c.full, err, stream);
+    return e != cudaSuccess ? e : launch_pair<kAmn, kBmn, kFp8, true>(p, c.full, -1, err, stream);
+}
+
+// Two products in one launch of `pairs` pairs: how its tiles are dealt (Jobs), and
+// its cost in the units above.
+struct Deal {
+    int late, extra;
+    long long cost;
+};
+Deal deal(const SsdProduct &one, const SsdProduct &two, long long pairs) {
+    const long long n1 = tiles_of(one, 256, 256), n2 = tiles_of(two, 256, 256);
+    const long long c1 = std::max(kBlockCost * kblocks_of(one, false), kPairEpilogue);
+    const long long c2 = std::max(kBlockCost * kblocks_of(two, false), kPairEpilogue);
+    const long long rounds = n1 / pairs, late = n1 % pairs, early = pairs - late;
+    Deal best{(int)late, 0, std::numeric_limits<long long>::max()};
+    for (long long extra = 0; extra <= (c1 + c2 - 1) / c2 && extra <= n2; ++extra) {
+        // tiles taken in turn, and those that go past the last whole turn: to the late pairs first
+        const long long shared = std::max(0ll, n2 - extra * early);
+        const long long turns = shared / pairs, over = shared % pairs;
+        const long long of_late = turns + (over > 0), of_early = turns + (over > late);
+        const long long own = extra * early <= n2 ? extra : (n2 + early - 1) / early;
+        const long long cost = std::max(late ? (rounds + 1) * c1 + of_late * c2 : 0,
+                                        rounds * c1 + (own + of_early) * c2) + kPairEpilogue;
+        if (cost < best.cost) best = {(int)late, (int)extra, cost};
+    }
+    return best;
 }
 
 }  // namespace
@@ -905,4 +1005,39 @@ cudaError_t ssd_launch_product_tc(const SsdProduct &p, int sms, unsigned *err,
                    : many<false, false, true>(p, sms, err, stream);
     return few ? few_tokens<false>(p, sms, err, stream)
                : many<false, false, false>(p, sms, err, stream);
+}
+
+// The gradients dx and dw.  In one launch, if that is cheaper than a launch each, the
+// product of the longer k first: pairs that have no tile of its last round begin with
+// the other's.  Tiles of two products at a time share less of what they read, about a
+// tenth of the time.  us of both in one launch and in two: tokens x features x inner
+// 2635 x 7664 x 1952 104 and 126, 16376 x 2048 x 1024 86 and 96, 300 x 1024 x 1024
+// 11.7 and 13.5; where it is not taken, 8000 x 10240 x 2560, 538 and 512.
+cudaError_t ssd_launch_product_two(const SsdProduct &dx, const SsdProduct &dw, int sms,
+                                   unsigned *err, cudaStream_t stream) {
+    const auto kernel = product_pair_kernel<false, true, false, false, true>;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr;
+    const cudaError_t e = pair_config(kernel, &cfg, &attr, stream);
+    if (e != cudaSuccess) return e;
+    const bool dw_first = dw.k > dx.k;
+    const SsdProduct &one = dw_first ? dw : dx, &two = dw_first ? dx : dw;
+    const long long tiles = tiles_of(one, 256, 256) + tiles_of(two, 256, 256);
+    const long long pairs = std::min<long long>(tiles, std::max(1, clusters_at_once(kernel, cfg, 2)));
+    const Deal d = deal(one, two, pairs);
+    const long long apart =
+        choose(dx, false, sms).cost + choose(dw, false, sms).cost + kLaunchCost;
+    if (apart < d.cost + d.cost / 10) {
+        const cudaError_t first = many<false, true, false>(dx, sms, err, stream);
+        return first != cudaSuccess ? first : many<true, true, false>(dw, sms, err, stream);
+    }
+    Jobs<true> jobs{};
+    jobs.late = d.late;
+    jobs.extra = d.extra;
+    jobs.amn = dw_first ? 0 : 1;
+    if (!pair_job(&jobs.job[0], one, dw_first, true, false, 0, -1, err) ||
+        !pair_job(&jobs.job[1], two, !dw_first, true, false, 0, -1, err))
+        return cudaErrorInvalidValue;
+    cfg.gridDim = dim3((unsigned)(2 * pairs));
+    return cudaLaunchKernelEx(&cfg, kernel, jobs);
 }
