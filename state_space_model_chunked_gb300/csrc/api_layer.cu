@@ -251,13 +251,15 @@ ssd_status ssd_linear_bwd(const void *dy, const void *x, const void *w, const vo
     const bool act = activation != SSD_ACT_NONE;
     const void *dp = act ? ws : dy;
     const long long dp_stride = act ? features : dy_stride;
-    if (act || dbias) {
-        SsdActBwd a{dy, preact, t, (SsdAct)(int)activation, tokens, features, dy_stride,
-                    act ? ws : nullptr, dbias};
-        const cudaError_t e =
-            ssd_launch_act_bwd(a, reinterpret_cast<float *>(ws + plan.dp), sms, stream);
-        if (e != cudaSuccess) return SSD_ERR_CUDA;
-    }
+    // The bias's gradient is summed in two passes, the second one beside the products;
+    // without an activation, the first one too (dy is its input and theirs).
+    const SsdActBwd pass{dy, preact, t, (SsdAct)(int)activation, tokens, features, dy_stride,
+                         act ? ws : nullptr};
+    float *partial = dbias ? reinterpret_cast<float *>(ws + plan.dp) : nullptr;
+    const bool products = dx || dw;
+    const bool first = act || (dbias && !products);
+    if (first && ssd_launch_act_bwd(pass, partial, sms, SsdOrder::after, stream) != cudaSuccess)
+        return SSD_ERR_CUDA;
     // dx[m][k] = sum_n dp[m][n] w[n][k], dw[n][k] = sum_m dp[m][n] x[m][k]
     const SsdProduct px{dp, w, t, tokens, inner, features, dp_stride, 1, 1, inner, nullptr, nullptr,
                         nullptr, nullptr, 0, SsdAct::none, dx, nullptr, t, t, inner};
@@ -270,6 +272,11 @@ ssd_status ssd_linear_bwd(const void *dy, const void *x, const void *w, const vo
         if (dx) e = launch_product(px, stream);
         if (dw && e == cudaSuccess) e = launch_product(pw, stream);
     }
+    if (dbias && !first && e == cudaSuccess)
+        e = ssd_launch_act_bwd(pass, partial, sms, SsdOrder::beside, stream);
+    if (dbias && e == cudaSuccess)
+        e = ssd_launch_column_sum(partial, ssd_act_bwd_rows(tokens, features, sms), features, dbias,
+                                  first && products ? SsdOrder::beside : SsdOrder::after, stream);
     if (e != cudaSuccess) return SSD_ERR_CUDA;
     return SSD_OK;
 }

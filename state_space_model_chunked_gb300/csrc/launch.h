@@ -233,8 +233,8 @@ cudaError_t ssd_launch_product_tc(const SsdProduct &p, int sms, unsigned *err,
 cudaError_t ssd_launch_product_two(const SsdProduct &dx, const SsdProduct &dw, int sms,
                                    unsigned *err, cudaStream_t stream);
 
-// dp = dy act'(preact) (dp null: not stored) and the column sums of dp
-// (dbias null: none; `partial` holds ssd_act_bwd_workspace bytes).
+// dp = dy act'(preact) (dp null: not stored) and the column sums of dp by blocks of
+// rows (`partial` holds ssd_act_bwd_workspace bytes; null: none).
 struct SsdActBwd {
     const void *dy, *preact;
     SsdElt type;
@@ -243,10 +243,15 @@ struct SsdActBwd {
     int width;
     long long dy_stride;
     void *dp;
-    float *dbias;
 };
+// How a kernel stands to the one in front of it in the stream: after it, or beside it,
+// where it reads nothing of that kernel's and only ends after it.
+enum class SsdOrder { after, beside };
 // out[j] = the sum of column j over n rows of `width` floats (linear_simt.cu).
 cudaError_t ssd_launch_column_sum(const float *partial, int n, int width, float *out,
-                                  cudaStream_t stream);
+                                  SsdOrder order, cudaStream_t stream);
 size_t ssd_act_bwd_workspace(long long rows, int width, int sms);
-cudaError_t ssd_launch_act_bwd(const SsdActBwd &a, float *partial, int sms, cudaStream_t stream);
+cudaError_t ssd_launch_act_bwd(const SsdActBwd &a, float *partial, int sms, SsdOrder order,
+                               cudaStream_t stream);
+// How many rows of sums it leaves in `partial`.
+int ssd_act_bwd_rows(long long rows, int width, int sms);

@@ -8,14 +8,17 @@
 // through shared memory, each of 256 threads a 4 x 4 block of sums.
 #include <cuda_fp8.h>
 
+#include <algorithm>
+
 #include "act.cuh"
 #include "launch.h"
+#include "ptx.cuh"
 #include "vec.cuh"
 
 namespace {
 
 constexpr int kTile = 64, kStep = 16;
-constexpr int kAhead = 4;      // rows of the gradients' pass under way in a thread
+constexpr int kActCtas = 5;     // CTAs an SM of the gradients' pass
 
 __device__ __forceinline__ float ld(const float *p) { return *p; }
 __device__ __forceinline__ float ld(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
@@ -72,9 +75,14 @@ __global__ void __launch_bounds__(256) product_simt_kernel(const SsdProduct p) {
 
 // dp = dy act'(p) and its column sums: bound by memory.  32 x 8 threads take
 // 32 V columns of the rows b, b + grid, ... ; a thread's sums stay in registers,
-// each block of rows' go to `partial`.
+// each block of rows' go to `partial`.  One wave of five CTAs an SM with two rows a
+// thread under way in bf16: 65536 x 2560 with silu 158 us (0.94 of the measured
+// bandwidth), 16376 x 2048 with gelu 40 us (0.74: the slope's arithmetic), the sums
+// alone 16.6 us; four CTAs with four rows 168, 42 and 16.2 us, six with two 174, 45 and 16.8.
 template <typename T, int V>
-__global__ void __launch_bounds__(256) act_bwd_kernel(const SsdActBwd a, float *partial) {
+__global__ void __launch_bounds__(256, kActCtas)
+act_bwd_kernel(const SsdActBwd a, float *partial, const bool beside) {
+    constexpr int kAhead = 4 / (int)sizeof(T);      // rows under way in a thread
     __shared__ float part[8][32 * V + 1];
     const int j = (blockIdx.x * 32 + threadIdx.x) * V;
     float acc[V];
@@ -109,7 +117,7 @@ __global__ void __launch_bounds__(256) act_bwd_kernel(const SsdActBwd a, float *
             }
         }
     }
-    if (!partial) return;
+    if (!partial) return;       // (and then not beside another kernel)
 #pragma unroll
     for (int k = 0; k < V; ++k) part[threadIdx.y][threadIdx.x * V + k] = acc[k];
     __syncthreads();
@@ -120,46 +128,64 @@ __global__ void __launch_bounds__(256) act_bwd_kernel(const SsdActBwd a, float *
         for (int y = 0; y < 8; ++y) s += part[y][i];
         if (col < a.width) partial[(size_t)blockIdx.y * a.width + col] = s;
     }
+    if (beside) ssdptx::griddep_wait();
 }
 
-// out[j] = the sum over n partial rows in a fixed order: 32 x 32 threads take 32
-// columns, each thread row every 32nd partial row.
-__global__ void __launch_bounds__(1024)
-column_sum_kernel(const float *__restrict__ partial, int n, int width, float *__restrict__ out) {
-    __shared__ float part[32][33];
+// out[j] = the sum over n partial rows in a fixed order: kRows x 32 threads take 32
+// columns, each thread row every kRows-th partial row.  Beside a product, which
+// leaves an SM few registers, 8 thread rows; else 32.
+template <int kRows>
+__global__ void __launch_bounds__(32 * kRows)
+column_sum_kernel(const float *partial, int n, int width, float *out, const bool beside) {
+    __shared__ float part[kRows][33];
+    if (!beside) ssdptx::griddep_wait();
     const int j = blockIdx.x * 32 + threadIdx.x;
     float acc = 0.f;
     if (j < width) {
 #pragma unroll 8
-        for (int r = threadIdx.y; r < n; r += 32) acc += partial[(size_t)r * width + j];
+        for (int r = threadIdx.y; r < n; r += kRows)
+            acc += __ldcg(partial + (size_t)r * width + j);
     }
     part[threadIdx.y][threadIdx.x] = acc;
     __syncthreads();
-    const float v = ssd_warp_sum(part[threadIdx.x][threadIdx.y]);
-    const int jo = blockIdx.x * 32 + threadIdx.y;
-    if (threadIdx.x == 0 && jo < width) out[jo] = v;
+    if (threadIdx.y == 0 && j < width) {
+        float v = 0.f;
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) v += part[r][threadIdx.x];
+        out[j] = v;
+    }
+    if (beside) ssdptx::griddep_wait();
 }
 
-// Blocks of rows: eight CTAs an SM, whatever vectors the arrays allow.
-int act_bwd_rows(long long rows, int width, int sms) {
-    const long long cols = (width + 255) / 256;
-    const long long want = (8ll * sms + cols - 1) / cols, most = (rows + 7) / 8;
-    return (int)(want < most ? want : most);
+// A launch that may start while the kernel in front of it in the stream still runs.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t stream, A... args) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <typename T>
-cudaError_t launch_act_bwd(const SsdActBwd &a, float *partial, int n, cudaStream_t stream) {
+cudaError_t launch_act_bwd(const SsdActBwd &a, float *partial, int n, SsdOrder order,
+                           cudaStream_t stream) {
     const auto on_16 = [](const void *p, long long stride) {
         return !p || (((uintptr_t)p & 15u) == 0 && (stride * sizeof(T)) % 16 == 0);
     };
     const dim3 block(32, 8);
-    if (on_16(a.dy, a.dy_stride) && on_16(a.preact, a.width) && on_16(a.dp, a.width) &&
-        a.width % 8 == 0)
-        act_bwd_kernel<T, 8><<<dim3((unsigned)((a.width + 255) / 256), (unsigned)n), block, 0,
-                               stream>>>(a, partial);
-    else
-        act_bwd_kernel<T, 1><<<dim3((unsigned)((a.width + 31) / 32), (unsigned)n), block, 0,
-                               stream>>>(a, partial);
+    const bool v8 =
+        on_16(a.dy, a.dy_stride) && on_16(a.preact, a.width) && on_16(a.dp, a.width) &&
+        a.width % 8 == 0;
+    const auto kernel = v8 ? act_bwd_kernel<T, 8> : act_bwd_kernel<T, 1>;
+    const dim3 grid((unsigned)((a.width + (v8 ? 255 : 31)) / (v8 ? 256 : 32)), (unsigned)n);
+    if (order == SsdOrder::beside) return launch_early(kernel, grid, block, stream, a, partial, true);
+    kernel<<<grid, block, 0, stream>>>(a, partial, false);
     return cudaGetLastError();
 }
 
@@ -175,23 +201,29 @@ cudaError_t ssd_launch_product_simt(const SsdProduct &p, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-size_t ssd_act_bwd_workspace(long long rows, int width, int sms) {
-    return (size_t)act_bwd_rows(rows, width, sms) * width * sizeof(float);
+// Blocks of rows: as many CTAs as the SMs hold, whatever vectors the arrays allow.
+int ssd_act_bwd_rows(long long rows, int width, int sms) {
+    const long long cols = (width + 255) / 256;
+    const long long want = std::max(1ll, kActCtas * (long long)sms / cols), most = (rows + 7) / 8;
+    return (int)std::min(want, most);
 }
 
-cudaError_t ssd_launch_act_bwd(const SsdActBwd &a, float *partial, int sms, cudaStream_t stream) {
-    const int n = act_bwd_rows(a.rows, a.width, sms);
-    float *part = a.dbias ? partial : nullptr;
-    const cudaError_t e = a.type == SSD_ELT_F32
-                              ? launch_act_bwd<float>(a, part, n, stream)
-                              : launch_act_bwd<__nv_bfloat16>(a, part, n, stream);
-    if (e != cudaSuccess || !a.dbias) return e;
-    return ssd_launch_column_sum(partial, n, a.width, a.dbias, stream);
+size_t ssd_act_bwd_workspace(long long rows, int width, int sms) {
+    return (size_t)ssd_act_bwd_rows(rows, width, sms) * width * sizeof(float);
+}
+
+cudaError_t ssd_launch_act_bwd(const SsdActBwd &a, float *partial, int sms, SsdOrder order,
+                               cudaStream_t stream) {
+    const int n = ssd_act_bwd_rows(a.rows, a.width, sms);
+    return a.type == SSD_ELT_F32 ? launch_act_bwd<float>(a, partial, n, order, stream)
+                                 : launch_act_bwd<__nv_bfloat16>(a, partial, n, order, stream);
 }
 
 cudaError_t ssd_launch_column_sum(const float *partial, int n, int width, float *out,
-                                  cudaStream_t stream) {
-    column_sum_kernel<<<(unsigned)((width + 31) / 32), dim3(32, 32), 0, stream>>>(partial, n, width,
-                                                                                out);
-    return cudaGetLastError();
+                                  SsdOrder order, cudaStream_t stream) {
+    const dim3 grid((unsigned)((width + 31) / 32));
+    return order == SsdOrder::beside
+               ? launch_early(column_sum_kernel<8>, grid, dim3(32, 8), stream, partial, n, width, out, true)
+               : launch_early(column_sum_kernel<32>, grid, dim3(32, 32), stream, partial, n, width, out,
+                              false);
 }

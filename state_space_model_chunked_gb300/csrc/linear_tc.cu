@@ -393,6 +393,7 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a,
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl->tmem;
+    griddep_launch_dependents();        // what may run beside this product may start
 
     // this CTA's tiles and, with kSplit, its part of the k blocks
     const int ntiles = a.row_tiles * a.col_tiles;
@@ -604,6 +605,7 @@ product_pair_kernel(const __grid_constant__ Jobs<kTwo> jobs) {
     cluster_sync_all();         // both CTAs' barriers and tensor memory stand
     tc_fence_after();
     const uint32_t tmem = ctl->tmem;
+    griddep_launch_dependents();        // what may run beside this product may start
     // this pair's tiles: one with kSplit, and of that a part of the k blocks
     const int pair = (int)blockIdx.x / (2 * parts), pairs = (int)gridDim.x / (2 * parts);
     const auto tile = [&](int j, Place &at) {

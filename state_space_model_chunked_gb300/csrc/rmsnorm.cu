@@ -382,7 +382,7 @@ cudaError_t launch_bwd(const SsdNormBwd &a, float *partial, int sms, cudaStream_
     }
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return ssd_launch_column_sum(partial, n, a.width, a.dweight, stream);
+    return ssd_launch_column_sum(partial, n, a.width, a.dweight, SsdOrder::after, stream);
 }
 
 }  // namespace

@@ -58,3 +58,21 @@ def test_gradients_with_an_infinite_value_elsewhere():
     rows = (~torch.isfinite(dx.float()).all(dim=1)).nonzero().flatten().tolist()
     cols = (~torch.isfinite(dw.float()).all(dim=1)).nonzero().flatten().tolist()
     assert rows == [650] and cols == [1280]
+
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+def test_calls_in_a_row_share_a_workspace(act):
+    """The bias's sum runs beside the products; the next call's writes to the same
+    workspace wait for it."""
+    rng = np.random.default_rng(8)
+    x, w = _values(rng, 1500, 264), _values(rng, 2048, 264)
+    calls = [(_values(rng, 1500, 2048), _values(rng, 1500, 2048) if act != "none" else None) for _ in range(8)]
+    alone = []
+    for dy, p in calls:
+        alone.append(ssd.linear_bwd(dy, x, w, p, activation=act))
+        torch.cuda.synchronize()
+    need = ssd.linear_bwd_workspace_bytes(torch.bfloat16, 1500, 2048, 264, act)
+    work = torch.empty(max(need, 1), dtype=torch.uint8, device="cuda")
+    together = [ssd.linear_bwd(dy, x, w, p, activation=act, workspace=work) for dy, p in calls]
+    for one, other in zip(alone, together):
+        assert all(torch.equal(a, b) for a, b in zip(one, other))
