@@ -278,6 +278,34 @@ __device__ __forceinline__ void store_sums(uint8_t *ring, uint32_t acc, int r, i
     tc_fence_before();
 }
 
+// N columns of row r (c its first one), N a multiple of 4: their sums over the ranks,
+// in order, four ranks' loads under way.
+template <int N>
+__device__ __forceinline__ void sum_ranks(const uint32_t (&peer)[8], int ranks, int r, int c,
+                                          float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = 0.f;
+#pragma unroll
+    for (int k0 = 0; k0 < 8; k0 += 4) {
+        if (k0 >= ranks) break;
+        float4 q[4][N / 4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int j = 0; j < N / 4; ++j)
+                if (k0 + k < ranks)
+                    q[k][j] = cluster_ld_f32x4(peer[k0 + k] + ((c / 4 + j) * kBM + r) * 16);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int j = 0; j < N / 4; ++j)
+                if (k0 + k < ranks) {
+                    v[4 * j] += q[k][j].x, v[4 * j + 1] += q[k][j].y;
+                    v[4 * j + 2] += q[k][j].z, v[4 * j + 3] += q[k][j].w;
+                }
+    }
+}
+
 // Rank `rank` of `ranks` adds its share of the columns over all ranks, in order,
 // and finishes them.  Rank k's sums lie at `ring` in the cluster's CTA
 // k * stride + offset.  r: this thread's row of the tile, m0 and n0 its first row
@@ -289,37 +317,27 @@ __device__ __forceinline__ void finish_split(const Args &a, uint32_t ring, int r
     uint32_t peer[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) peer[k] = cluster_map(ring, (k < ranks ? k : 0) * stride + offset);
-    const auto sum4 = [&](int c) {
-        float4 q[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (k < ranks) q[k] = cluster_ld_f32x4(peer[k] + (c / 4 * kBM + r) * 16);
-        float4 v = q[0];
-#pragma unroll
-        for (int k = 1; k < 8; ++k)
-            if (k < ranks) v.x += q[k].x, v.y += q[k].y, v.z += q[k].z, v.w += q[k].w;
-        return v;
-    };
     if constexpr (kSwap) {
         const long long n = row0 + r;
 #pragma unroll 1
         for (int c = (rank * 2 + half) * 4; c < kBN; c += 8 * ranks) {
             const long long m = col0 + c;
             if (m >= a.p.m) break;
-            const float4 s = sum4(c);
-            const float v[4] = {s.x, s.y, s.z, s.w};
+            float v[4];
+            sum_ranks(peer, ranks, r, c, v);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (m + i < a.p.m && n < a.p.n) ssd_finish(a.p, m + i, n, v[i]);
         }
     } else {
+        constexpr int kPart = 16;
         const long long m = row0 + r;
         const float scale = a.p.a_scale && m < a.p.m ? __ldg(a.p.a_scale + m) : 1.f;
 #pragma unroll 1
-        for (int c = (rank * 2 + half) * 8; c < kBN; c += 16 * ranks) {
+        for (int c = (rank * 2 + half) * kPart; c < kBN; c += 2 * kPart * ranks) {
             const long long n = col0 + c;
-            const float4 lo = sum4(c), hi = sum4(c + 4);
-            float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            float v[kPart];
+            sum_ranks(peer, ranks, r, c, v);
             const auto last = [&](auto part) {
                 part.ask(a, m, n);
                 const auto at = [&](const float *q) {
@@ -327,8 +345,8 @@ __device__ __forceinline__ void finish_split(const Args &a, uint32_t ring, int r
                 };
                 part.finish(a, m, n, scale, at(a.p.bias), at(a.p.b_scale), v);
             };
-            if (a.p.out_type == SSD_ELT_F32) last(RowPart<float, 8>{});
-            else last(RowPart<__nv_bfloat16, 8>{});
+            if (a.p.out_type == SSD_ELT_F32) last(RowPart<float, kPart>{});
+            else last(RowPart<__nv_bfloat16, kPart>{});
         }
     }
 }
@@ -385,6 +403,10 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a,
         ctl->abort = 0;
         fence_mbar_init();
     }
+    if (threadIdx.x == 64) {
+        tma_prefetch_desc(&map_a);
+        tma_prefetch_desc(&map_b);
+    }
     if (warp == 1) {
         tmem_alloc(smem_u32(&ctl->tmem), kCols);
         tmem_relinquish();
@@ -405,8 +427,6 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a,
 
     if (warp == 0) {
         if (lane == 0) {
-            tma_prefetch_desc(&map_a);
-            tma_prefetch_desc(&map_b);
             uint32_t n = 0;             // blocks issued so far
             bool ok = true;
             for (int t = first; ok && t < ntiles; t += step) {
@@ -509,7 +529,7 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a,
                                      (long long)col * kBN);
         }
         __syncwarp();
-        cluster_sync_all();     // nobody leaves while its sums are being read
+        cluster_sync_relaxed();     // nobody leaves while its sums are being read
     }
     __syncwarp();
     tc_fence_before();
@@ -596,6 +616,12 @@ product_pair_kernel(const __grid_constant__ Jobs<kTwo> jobs) {
         ctl->abort = 0;
         fence_mbar_init();
     }
+    if (threadIdx.x == 64) {
+        for (const Job &job : jobs.job) {
+            tma_prefetch_desc(&job.map_a);
+            tma_prefetch_desc(&job.map_b);
+        }
+    }
     if (warp == 1) {
         tmem_alloc_pair(smem_u32(&ctl->tmem), 512);
         tmem_relinquish_pair();
@@ -619,10 +645,6 @@ product_pair_kernel(const __grid_constant__ Jobs<kTwo> jobs) {
 
     if (warp == 0) {
         if (lane == 0) {
-            for (const Job &job : jobs.job) {
-                tma_prefetch_desc(&job.map_a);
-                tma_prefetch_desc(&job.map_b);
-            }
             uint32_t n = 0;
             bool ok = true;
             Place at;
@@ -736,10 +758,10 @@ product_pair_kernel(const __grid_constant__ Jobs<kTwo> jobs) {
     }
     __syncwarp();
     tc_fence_before();
-    cluster_sync_all();         // no CTA leaves while others use its barriers, operands or sums
+    cluster_sync_relaxed();     // no CTA leaves while others use its barriers, operands or sums
     if (warp == 1) tmem_dealloc_pair(tmem, 512);
     __syncwarp();
-    cluster_sync_all();         // nor before both have freed the tensor memory they share
+    cluster_sync_relaxed();     // nor before both have freed the tensor memory they share
 }
 
 // ------------------------------------------------------------------ host
