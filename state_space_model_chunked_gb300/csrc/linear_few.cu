@@ -9,9 +9,12 @@
 // take k in any order, so lane 4 g + t simply holds 16 consecutive bytes of
 // features g and g + 8 and the same 16 bytes of token g.  Nothing is staged in
 // shared memory and no barrier stands before the end, where the warps' sums are
-// added in order.  Against the tcgen05 tiles of linear_tc.cu, whose prologue, cluster
-// barriers and tensor-memory round trip cost about 8 us a call, see the rule
-// in ssd_product_few_handles.
+// added in order.
+//   Measured (time on the GPU): one token of 2560 to 15360 features in bf16 14.7 us
+// (5.35 TB/s, 0.79 of the measured copy bandwidth), sixteen tokens of 5120 to 2560 in
+// 8 bits 5.6 us, of which the weights' transfer is 2.  The tcgen05 tiles of
+// linear_tc.cu, with their prologue, cluster barriers and tensor-memory round trip,
+// took 18.2 and 10.9 us.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 

@@ -13,6 +13,10 @@
 // row's loads under way, and keeps its columns' weights in registers; the
 // row's sum and its largest |s w| come from one pass and one barrier:
 // max |y| = rstd max |s w|.
+//   Measured (time on the GPU): 65536 rows of 2560, bf16 with an fp32 residual in
+// place, to 8 bits 189 us (0.91 of the measured copy bandwidth); gradients of 16376
+// rows of 1024 46 us (0.86); 16 rows 2 us, all of it the launch.  Without the next
+// row's loads under way the first took 377 us and the second 89.
 #include "launch.h"
 #include "vec.cuh"
 
@@ -22,7 +26,9 @@ constexpr float kE4m3Max = 448.f;
 constexpr int kMostWarps = 16;      // a row's CTA: 128 registers a thread
 // most runs a thread: of 8 values (forward, backward) and of one
 constexpr int kRuns8 = 4, kBwdRuns8 = 2, kRuns1 = 16;
-// runs wanted a thread where there are rows enough, and warps an SM holds
+// runs wanted a thread where there are rows enough, and warps an SM holds.  us
+// forward by (runs, warps): (4, 16) 190, (4, 24) 223, (2, 16) 288, (2, 32) 216,
+// (1, 32) 262, (1, 48) 292; backward: (1, 16) 46.6, (1, 24) 51, (1, 32) 48.7, (2, 16) 47.0
 constexpr int kFwdRuns = 4, kFwdWarpsSm = 16;
 constexpr int kBwdRuns = 1, kBwdWarpsSm = 16;
 
