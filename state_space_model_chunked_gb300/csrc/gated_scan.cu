@@ -13,7 +13,7 @@
 //   Measured (time on the GPU): forward 65536 tokens of 5120 channels in bf16 with z
 // 540 us (0.73 of the measured copy bandwidth), 47 sequences of 65518 tokens in all,
 // 1536 channels, fp32 217 us (0.82); backward 8 x 2047 tokens of 2048 channels 131 us
-// (0.53); a token of 256 rows of 5120 2.8 us, its arrays in L2.  What bounds the two
+// (0.53); a token of 256 rows of 5120 2.5 us, its arrays in L2.  What bounds the two
 // directions is the instructions, about 40 and 78 a channel and token, and the wait
 // for the tile in front, which the walk's rule below keeps short: without the walk
 // (wrong results) 521, 177 and 123 us.
@@ -757,6 +757,7 @@ template <typename T, int V, bool kGate>
 __global__ void __launch_bounds__(256) gated_step_kernel(const SsdGatedStep a) {
     const long long r = blockIdx.x;
     const int c = (blockIdx.y * 256 + threadIdx.x) * V;
+    ssdptx::griddep_wait();
     if (c >= a.width) return;
     SsdRaw<T, V> gr, xr, zr;
     SsdRaw<float, V> sr;
@@ -901,9 +902,8 @@ cudaError_t ssd_launch_gated_bwd(const SsdGatedBwd &a, int sms, void *ws, unsign
 template <typename T, int V>
 static cudaError_t launch_step(const SsdGatedStep &a, cudaStream_t stream) {
     const dim3 grid((unsigned)a.rows, (unsigned)((a.width + 256 * V - 1) / (256 * V)));
-    if (a.z) gated_step_kernel<T, V, true><<<grid, 256, 0, stream>>>(a);
-    else gated_step_kernel<T, V, false><<<grid, 256, 0, stream>>>(a);
-    return cudaGetLastError();
+    return ssd_launch_early(a.z ? gated_step_kernel<T, V, true> : gated_step_kernel<T, V, false>, grid,
+                            dim3(256), stream, a);
 }
 
 cudaError_t ssd_launch_gated_step(const SsdGatedStep &a, cudaStream_t stream) {

@@ -244,6 +244,24 @@ struct SsdActBwd {
     long long dy_stride;
     void *dp;
 };
+// A launch that may start while the kernel in front of it in the stream still runs:
+// the kernel calls griddep_wait before it touches anything that one may, so what
+// overlaps is the launch and the set-up.
+template <typename... P, typename... A>
+cudaError_t ssd_launch_early(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t stream,
+                             A... args) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // How a kernel stands to the one in front of it in the stream: after it, or beside it,
 // where it reads nothing of that kernel's and only ends after it.
 enum class SsdOrder { after, beside };

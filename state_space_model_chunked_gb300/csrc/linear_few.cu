@@ -10,9 +10,9 @@
 // features g and g + 8 and the same 16 bytes of token g.  Nothing is staged in
 // shared memory and no barrier stands before the end, where the warps' sums are
 // added in order.
-//   Measured (time on the GPU): one token of 2560 to 15360 features in bf16 14.7 us
-// (5.35 TB/s, 0.79 of the measured copy bandwidth), sixteen tokens of 5120 to 2560 in
-// 8 bits 5.6 us, of which the weights' transfer is 2.  The tcgen05 tiles of
+//   Measured (time on the GPU): one token of 2560 to 15360 features in bf16 14.4 us
+// (5.45 TB/s, 0.80 of the measured copy bandwidth), sixteen tokens of 5120 to 2560 in
+// 8 bits 5.2 us, of which the weights' transfer is 2.  The tcgen05 tiles of
 // linear_tc.cu, with their prologue, cluster barriers and tensor-memory round trip,
 // took 18.2 and 10.9 us.
 #include <cuda_fp16.h>
@@ -20,6 +20,7 @@
 
 #include "act.cuh"
 #include "launch.h"
+#include "ptx.cuh"
 #include "vec.cuh"
 
 namespace {
@@ -75,6 +76,7 @@ __global__ void __launch_bounds__(32 * kWarps) product_few_kernel(const SsdProdu
     constexpr int kStep = 8 * kWord;            // values of k a warp takes at once: 128 bytes a row
     __shared__ float part[kWarps][kNT * 8][kRows];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    ssdptx::griddep_wait();
     const long long n0 = (long long)blockIdx.x * kRows;
     const char *w = static_cast<const char *>(p.b), *x = static_cast<const char *>(p.a);
     // rows past the end read the last one; their sums are not used
@@ -146,9 +148,8 @@ __global__ void __launch_bounds__(32 * kWarps) product_few_kernel(const SsdProdu
 
 template <bool kFp8, int kNT, int kWarps, int kAhead>
 cudaError_t launch(const SsdProduct &p, cudaStream_t stream) {
-    product_few_kernel<kFp8, kNT, kWarps, kAhead>
-        <<<(unsigned)((p.n + kRows - 1) / kRows), 32 * kWarps, 0, stream>>>(p);
-    return cudaGetLastError();
+    return ssd_launch_early(product_few_kernel<kFp8, kNT, kWarps, kAhead>,
+                            dim3((unsigned)((p.n + kRows - 1) / kRows)), dim3(32 * kWarps), stream, p);
 }
 
 // Few CTAs an SM: many warps in each, so all of the SM's loads are under way;

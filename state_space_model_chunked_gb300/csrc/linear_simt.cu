@@ -84,6 +84,7 @@ __global__ void __launch_bounds__(256, kActCtas)
 act_bwd_kernel(const SsdActBwd a, float *partial, const bool beside) {
     constexpr int kAhead = 4 / (int)sizeof(T);      // rows under way in a thread
     __shared__ float part[8][32 * V + 1];
+    if (!beside) ssdptx::griddep_wait();
     const int j = (blockIdx.x * 32 + threadIdx.x) * V;
     float acc[V];
 #pragma unroll
@@ -157,21 +158,6 @@ column_sum_kernel(const float *partial, int n, int width, float *out, const bool
     if (beside) ssdptx::griddep_wait();
 }
 
-// A launch that may start while the kernel in front of it in the stream still runs.
-template <typename... P, typename... A>
-cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t stream, A... args) {
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <typename T>
 cudaError_t launch_act_bwd(const SsdActBwd &a, float *partial, int n, SsdOrder order,
                            cudaStream_t stream) {
@@ -184,9 +170,7 @@ cudaError_t launch_act_bwd(const SsdActBwd &a, float *partial, int n, SsdOrder o
         a.width % 8 == 0;
     const auto kernel = v8 ? act_bwd_kernel<T, 8> : act_bwd_kernel<T, 1>;
     const dim3 grid((unsigned)((a.width + (v8 ? 255 : 31)) / (v8 ? 256 : 32)), (unsigned)n);
-    if (order == SsdOrder::beside) return launch_early(kernel, grid, block, stream, a, partial, true);
-    kernel<<<grid, block, 0, stream>>>(a, partial, false);
-    return cudaGetLastError();
+    return ssd_launch_early(kernel, grid, block, stream, a, partial, order == SsdOrder::beside);
 }
 
 }  // namespace
@@ -223,7 +207,8 @@ cudaError_t ssd_launch_column_sum(const float *partial, int n, int width, float 
                                   SsdOrder order, cudaStream_t stream) {
     const dim3 grid((unsigned)((width + 31) / 32));
     return order == SsdOrder::beside
-               ? launch_early(column_sum_kernel<8>, grid, dim3(32, 8), stream, partial, n, width, out, true)
-               : launch_early(column_sum_kernel<32>, grid, dim3(32, 32), stream, partial, n, width, out,
-                              false);
+               ? ssd_launch_early(column_sum_kernel<8>, grid, dim3(32, 8), stream, partial, n, width,
+                                  out, true)
+               : ssd_launch_early(column_sum_kernel<32>, grid, dim3(32, 32), stream, partial, n,
+                                  width, out, false);
 }

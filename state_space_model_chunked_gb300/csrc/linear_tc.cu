@@ -20,9 +20,10 @@
 //   Measured (time on the GPU): 65536 x 5120 -> 2560 in bf16 with bias, silu and
 // residual 1065 to 1090 us (1.6 PFLOP/s, under the power limit; 0.94 of a library
 // product's sustained rate), both gradients of 16376 x 1024 -> 2048 86 us (1.6 PFLOP/s),
-// 4001 x 768 -> 1536 in 8 bits 15 us.  A product of few tiles has a fixed cost: 1 us
-// before the first load, 1.2 us for its data, 0.6 us at the end, and with k split 3 to
-// 4 us for the exchange.
+// 4001 x 768 -> 1536 in 8 bits 14.3 us, 512 x 2560 -> 2560 in bf16 12.1 us.  A product of
+// few tiles has a fixed cost: 1 us before the first load, which the kernel in front
+// in the stream hides (13.3 us for the last one without that), 1.2 us for its data,
+// 0.6 us at the end, and with k split 3 to 4 us for the exchange.
 #include <cuda.h>
 
 #include <algorithm>
@@ -315,7 +316,7 @@ __device__ __forceinline__ void sum_ranks(const uint32_t (&peer)[8], int ranks, 
 
 // Rank `rank` of `ranks` adds its share of the columns over all ranks, in order,
 // and finishes them.  Rank k's sums lie at `ring` in the cluster's CTA
-// k * stride + offset.  r: this thread's row of the tile, m0 and n0 its first row
+// k * stride + offset.  r: this thread's row of the tile, row0 and col0 its first row
 // and column (with kSwap: first feature and token).
 template <int kBN, bool kSwap>
 __device__ __forceinline__ void finish_split(const Args &a, uint32_t ring, int r, int half,
@@ -394,6 +395,7 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a,
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool misplaced = (ring & 1023u) != 0u;    // the same in every CTA of the grid
     if (misplaced) {
+        griddep_wait();
         if (threadIdx.x == 0) ssd_report(a.err, SSD_DEVERR_SMEM_ALIGN);
         return;
     }
@@ -422,6 +424,7 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a,
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl->tmem;
+    griddep_wait();                     // the kernel in front: its results may be operands
     griddep_launch_dependents();        // what may run beside this product may start
 
     // this CTA's tiles and, with kSplit, its part of the k blocks
@@ -607,6 +610,7 @@ product_pair_kernel(const __grid_constant__ Jobs<kTwo> jobs) {
     const int part = in_cluster / 2, parts = kSplit ? (int)cluster_size() / 2 : 1;
     const bool misplaced = (ring & 1023u) != 0u;    // the same in every CTA of the grid
     if (misplaced) {
+        griddep_wait();
         if (threadIdx.x == 0) ssd_report(a.err, SSD_DEVERR_SMEM_ALIGN);
         return;
     }
@@ -638,6 +642,7 @@ product_pair_kernel(const __grid_constant__ Jobs<kTwo> jobs) {
     cluster_sync_all();         // both CTAs' barriers and tensor memory stand
     tc_fence_after();
     const uint32_t tmem = ctl->tmem;
+    griddep_wait();                     // the kernel in front: its results may be operands
     griddep_launch_dependents();        // what may run beside this product may start
     // this pair's tiles: one with kSplit, and of that a part of the k blocks
     const int pair = (int)blockIdx.x / (2 * parts), pairs = (int)gridDim.x / (2 * parts);
@@ -860,11 +865,13 @@ cudaError_t launch(const SsdProduct &p, int sms, unsigned *err, cudaStream_t str
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = kSplit ? 1 : 0;
+    cfg.numAttrs = 2;
     const int ranks = kSplit ? split_ranks(kernel, cfg, tiles, a.kblocks) : 1;
     attr[0].val.clusterDim.x = ranks;
     cfg.gridDim = dim3((unsigned)(kSplit ? tiles * ranks : (tiles < sms ? tiles : sms)));
@@ -882,21 +889,23 @@ bool pair_job(Job *job, const SsdProduct &p, bool amn, bool bmn, bool fp8, int t
            operand_map(&job->map_b, p.b, fp8, bmn, p.n, p.k, bmn ? p.b_col : p.b_row, 128);
 }
 
-// The launch of a kernel of pairs, `cfg` and its one attribute but for the grid
-// and the cluster's size.
+// The launch of a kernel of pairs, `cfg` and its attributes (the first: the cluster's
+// size) but for the grid.
 template <typename Kernel>
 cudaError_t pair_config(Kernel kernel, cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr,
                         cudaStream_t stream) {
     constexpr uint32_t kSmem = kCtrlBytes + kPairStages * kPairStage + kColumnBytes;
-    attr->id = cudaLaunchAttributeClusterDimension;
-    attr->val.clusterDim.x = 2;
-    attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     *cfg = {};
     cfg->blockDim = dim3(kThreads);
     cfg->dynamicSmemBytes = kSmem;
     cfg->stream = stream;
     cfg->attrs = attr;
-    cfg->numAttrs = 1;
+    cfg->numAttrs = 2;
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
 }
 
@@ -908,15 +917,15 @@ cudaError_t launch_pair(const SsdProduct &p, int tile0, int tile1, unsigned *err
     const Args &a = jobs.job[0].a;
     const auto kernel = product_pair_kernel<kAmn, kBmn, kFp8, kSplit, false>;
     cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute attr;
-    const cudaError_t e = pair_config(kernel, &cfg, &attr, stream);
+    cudaLaunchAttribute attr[2];
+    const cudaError_t e = pair_config(kernel, &cfg, attr, stream);
     if (e != cudaSuccess) return e;
     const long long tiles = a.tile1 - a.tile0;
     int parts = kSplit ? 4 : 1;
     while (parts > 1 && (a.kblocks < 2 * parts || tiles > clusters_at_once(kernel, cfg, 2 * parts)))
         --parts;
     const long long pairs = kSplit ? tiles : std::min<long long>(tiles, std::max(1, clusters_at_once(kernel, cfg, 2)));
-    attr.val.clusterDim.x = 2 * parts;
+    attr[0].val.clusterDim.x = 2 * parts;
     cfg.gridDim = dim3((unsigned)(2 * parts * pairs));
     return cudaLaunchKernelEx(&cfg, kernel, jobs);
 }
@@ -1048,8 +1057,8 @@ cudaError_t ssd_launch_product_two(const SsdProduct &dx, const SsdProduct &dw, i
                                    unsigned *err, cudaStream_t stream) {
     const auto kernel = product_pair_kernel<false, true, false, false, true>;
     cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute attr;
-    const cudaError_t e = pair_config(kernel, &cfg, &attr, stream);
+    cudaLaunchAttribute attr[2];
+    const cudaError_t e = pair_config(kernel, &cfg, attr, stream);
     if (e != cudaSuccess) return e;
     const bool dw_first = dw.k > dx.k;
     const SsdProduct &one = dw_first ? dw : dx, &two = dw_first ? dx : dw;

@@ -15,9 +15,10 @@
 // max |y| = rstd max |s w|.
 //   Measured (time on the GPU): 65536 rows of 2560, bf16 with an fp32 residual in
 // place, to 8 bits 189 us (0.91 of the measured copy bandwidth); gradients of 16376
-// rows of 1024 46 us (0.86); 16 rows 2 us, all of it the launch.  Without the next
+// rows of 1024 46 us (0.86); 16 rows 1.6 us, all of it the launch.  Without the next
 // row's loads under way the first took 377 us and the second 89.
 #include "launch.h"
+#include "ptx.cuh"
 #include "vec.cuh"
 
 namespace {
@@ -92,6 +93,7 @@ __device__ __forceinline__ void load_weight(const float *weight, int nvec, float
 
 template <typename TX, typename TR, typename TO, int V, int kC>
 __global__ void __launch_bounds__(32 * kMostWarps) rmsnorm_fwd_kernel(const SsdNormFwd a) {
+    ssdptx::griddep_wait();
     __shared__ float buf[2][2][32];
     constexpr bool kFp8 = sizeof(TO) == 1;
     const int nvec = a.width / V;
@@ -202,6 +204,7 @@ __global__ void rmsnorm_fwd_wide_kernel(const SsdNormFwd a) {
 template <typename T, typename TS, int V, int kC>
 __global__ void __launch_bounds__(32 * kMostWarps)
 rmsnorm_bwd_kernel(const SsdNormBwd a, float *__restrict__ partial) {
+    ssdptx::griddep_wait();
     __shared__ float buf[2][2][32];
     const int nvec = a.width / V;
     const bool res = a.dresidual != nullptr;
@@ -337,17 +340,18 @@ cudaError_t launch_fwd(const SsdNormFwd &a, int sms, cudaStream_t stream) {
     const unsigned rows = walkers(a.rows, sms, kFwdWarpsSm / (sh.warps ? sh.warps : 1));
     if (sh.warps == 0) {
         rmsnorm_fwd_wide_kernel<TX, TR, TO><<<(unsigned)a.rows, 1024, 0, stream>>>(a);
-    } else if (v8) {
-        switch (sh.runs) {
-            case 1: rmsnorm_fwd_kernel<TX, TR, TO, 8, 1><<<rows, 32 * sh.warps, 0, stream>>>(a); break;
-            case 2: rmsnorm_fwd_kernel<TX, TR, TO, 8, 2><<<rows, 32 * sh.warps, 0, stream>>>(a); break;
-            case 3: rmsnorm_fwd_kernel<TX, TR, TO, 8, 3><<<rows, 32 * sh.warps, 0, stream>>>(a); break;
-            default: rmsnorm_fwd_kernel<TX, TR, TO, 8, 4><<<rows, 32 * sh.warps, 0, stream>>>(a); break;
-        }
-    } else {
-        rmsnorm_fwd_kernel<TX, TR, TO, 1, kRuns1><<<rows, 32 * sh.warps, 0, stream>>>(a);
+        return cudaGetLastError();
     }
-    return cudaGetLastError();
+    auto kernel = rmsnorm_fwd_kernel<TX, TR, TO, 1, kRuns1>;
+    if (v8) {
+        switch (sh.runs) {
+            case 1: kernel = rmsnorm_fwd_kernel<TX, TR, TO, 8, 1>; break;
+            case 2: kernel = rmsnorm_fwd_kernel<TX, TR, TO, 8, 2>; break;
+            case 3: kernel = rmsnorm_fwd_kernel<TX, TR, TO, 8, 3>; break;
+            default: kernel = rmsnorm_fwd_kernel<TX, TR, TO, 8, 4>; break;
+        }
+    }
+    return ssd_launch_early(kernel, dim3(rows), dim3(32 * sh.warps), stream, a);
 }
 
 template <typename TX, typename TR>
@@ -374,19 +378,17 @@ cudaError_t launch_bwd(const SsdNormBwd &a, float *partial, int sms, cudaStream_
                     vec8(a.dx, a.width, sizeof(T)) && vec8(a.ds, a.width, sizeof(TS));
     const RowShape sh = row_shape(a.width, v8 ? 8 : 1, v8 ? kBwdRuns8 : kRuns1, v8 ? kBwdRuns : kRuns1);
     const int n = bwd_ctas(a.rows, a.width, sms);
+    cudaError_t e;
     if (sh.warps == 0) {
         rmsnorm_bwd_wide_kernel<T, TS><<<(unsigned)a.rows, 1024, 0, stream>>>(a);
         const dim3 grid((unsigned)n, (unsigned)((a.width + 255) / 256));
         rmsnorm_dw_wide_kernel<T, TS><<<grid, 256, 0, stream>>>(a, partial);
-    } else if (v8) {
-        switch (sh.runs) {
-            case 1: rmsnorm_bwd_kernel<T, TS, 8, 1><<<n, 32 * sh.warps, 0, stream>>>(a, partial); break;
-            default: rmsnorm_bwd_kernel<T, TS, 8, 2><<<n, 32 * sh.warps, 0, stream>>>(a, partial); break;
-        }
+        e = cudaGetLastError();
     } else {
-        rmsnorm_bwd_kernel<T, TS, 1, kRuns1><<<n, 32 * sh.warps, 0, stream>>>(a, partial);
+        auto kernel = rmsnorm_bwd_kernel<T, TS, 1, kRuns1>;
+        if (v8) kernel = sh.runs == 1 ? rmsnorm_bwd_kernel<T, TS, 8, 1> : rmsnorm_bwd_kernel<T, TS, 8, 2>;
+        e = ssd_launch_early(kernel, dim3((unsigned)n), dim3(32 * sh.warps), stream, a, partial);
     }
-    cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return ssd_launch_column_sum(partial, n, a.width, a.dweight, SsdOrder::after, stream);
 }
