@@ -214,8 +214,9 @@ __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The same without waiting for the threads' own writes to become visible: for a
-// cluster whose CTAs only keep each other's shared memory alive.
+// The same without ordering the threads' own accesses (nor waiting for their writes to
+// become visible).  A thread's loads from a peer's shared memory may still be on their
+// way when the peer leaves this barrier.
 __device__ __forceinline__ void cluster_sync_relaxed() {
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");

@@ -1,0 +1,66 @@
+"""The tensor-core product on each of its paths, with the whole epilogue (bias, scales,
+activation, residual, values before the activation) and last rows and columns that are
+not full, against the formulas in 64 bits.
+
+Bars, derived before the first run: an output is rounded once to bf16, by at most 2^-8
+of itself; the sums' 32 bits over k <= 5120 terms, and the residual's addition after
+them, stay below 1e-4 of the terms' size, which is the outputs': 2^-8 + 1e-4 as
+relative L2, and of the largest value for each value by itself (nothing is left out or
+computed for another place).  An fp32 output has the latter part alone, 1e-4."""
+import numpy as np
+import pytest
+import torch
+
+import state_space_model_chunked_gb300 as ssd
+from tests import layer_ref as ref
+from tests.gpu_util import host
+
+pytestmark = pytest.mark.gpu
+FP8 = torch.float8_e4m3fn
+BAR = {torch.bfloat16: 2.0 ** -8 + 1e-4, torch.float32: 1e-4}
+
+
+def _values(rng, rows, cols, std=1.0):
+    return torch.from_numpy(rng.standard_normal((rows, cols), dtype=np.float32) * np.float32(std)).cuda()
+
+
+def _operand(rng, rows, k, dtype, std=1.0):
+    t = _values(rng, rows, k, std)
+    if dtype is not FP8:
+        return t.to(dtype), None
+    scale = t.abs().amax(dim=1) / 448.0
+    return (t / scale[:, None]).to(FP8), scale
+
+
+def _close(got, want, bar):
+    wrong = np.abs(host(got) - want)
+    assert np.linalg.norm(wrong) <= bar * np.linalg.norm(want)
+    assert wrong.max() <= bar * np.abs(want).max()
+
+
+def _check(m, n, k, dtype, out_dtype=torch.bfloat16, activation="silu"):
+    rng = np.random.default_rng(m + 3 * n + k)
+    x, xs = _operand(rng, m, k, dtype)
+    w, ws = _operand(rng, n, k, dtype, k ** -0.5)
+    bias, residual = _values(rng, 1, n)[0], _values(rng, m, n).to(out_dtype)
+    y, p = ssd.linear_fwd(x, w, bias, residual, activation=activation, x_scale=xs, w_scale=ws,
+                          out_dtype=out_dtype, return_preact=True)
+    yr, pr = ref.linear_fwd(host(x), host(w), host(bias), host(residual), activation,
+                            None if xs is None else host(xs), None if ws is None else host(ws))
+    _close(y, yr, BAR[out_dtype])
+    _close(p, pr, BAR[torch.bfloat16])
+    bare = ssd.linear_fwd(x, w, x_scale=xs, w_scale=ws, out_dtype=out_dtype)
+    _close(bare, pr - host(bias), BAR[out_dtype])
+    ssd.last_device_error()
+
+
+@pytest.mark.parametrize("dtype,k", [(torch.bfloat16, 2048), (FP8, 4096)])
+@pytest.mark.parametrize("m,n", [
+    (40, 200), (17, 8), (33, 1032),     # tokens as columns: features that end in a tile's first warp
+    (200, 264), (130, 520), (100, 2560),   # one CTA's tiles: rows that end in the first warp, 8 columns in the last tile
+    (1800, 1000),                       # pairs: the second CTA of the last row of tiles has no row
+])
+def test_sums_split_over_a_cluster(m, n, dtype, k):
+    """Rows and columns past the end take no part in the exchange of sums."""
+    _check(m, n, k, dtype)
+    _check(m, n, k, dtype, torch.float32, "relu")
