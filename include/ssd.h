@@ -602,8 +602,8 @@ ssd_status ssd_last_device_error(void);
 
 /* Test hook for the bounded device-side waits (the pages have no
  * counterpart).  Every later launch of the tensor-core scan, of the gated
- * recurrence and (the limit) of the tensor-core product reads the setting; it is process-wide and not synchronised with calls in flight on
- * other host threads.
+ * recurrence and of the tensor-core product reads the setting; it is process-wide
+ * and not synchronised with calls in flight on other host threads.
  *   fault          SSD_FAULT_NONE: normal operation.  SSD_FAULT_WITHHOLD_SIGNAL:
  *                  in the CTAs of each sequence's first segment, the barrier
  *                  that signals "decay factors ready" waits for one arrival
@@ -615,8 +615,11 @@ ssd_status ssd_last_device_error(void);
  *                  In ssd_gated_scan_fwd / _bwd calls of more than one tile the
  *                  first tile of the walk publishes nothing, so the tiles behind
  *                  it give up after wait_limit_ns each, with the same report.
- *   wait_limit_ns  limit of every bounded wait in those kernels; 0 restores
- *                  the default (2 s).
+ *                  In the tensor-core product the first CTA's (or pair of CTAs')
+ *                  first accumulator is never announced, with the same end.
+ *   wait_limit_ns  limit of every bounded wait in those kernels but the
+ *                  product's waits, at its end, for its own copies and products
+ *                  in flight (always the default); 0 restores the default (2 s).
  * Returns SSD_ERR_INVALID_ARG for an unknown fault. */
 typedef enum { SSD_FAULT_NONE = 0, SSD_FAULT_WITHHOLD_SIGNAL = 1 } ssd_fault;
 ssd_status ssd_debug_inject_fault(ssd_fault fault, unsigned long long wait_limit_ns);

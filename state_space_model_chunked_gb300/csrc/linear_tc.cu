@@ -64,16 +64,20 @@ struct Args {
     bool vec;               // rows of out, preact and residual on 16 bytes
     unsigned *err;
     unsigned long long wait_ns;
+    bool withhold;          // test hook: the first CTA's (pair's) first accumulator is not announced
 };
 
 struct Ctrl {
     uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
     uint32_t tmem;
     int abort;
+    uint32_t other_abort;   // the flag of the pair's other CTA (alone: this one's) in the cluster
+    uint32_t issued;        // a pair: blocks that this CTA's producer has issued
 };
 static_assert(sizeof(Ctrl) <= kCtrlBytes, "control block");
 
-// A wait that another role's failure also ends; the first to run out reports.
+// A wait that another role's failure, in either CTA of a pair, also ends; the first to
+// run out reports.
 __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Ctrl *ctl, const Args &a) {
     const uint32_t b = smem_u32(bar);
     if (mbar_try_wait(b, parity)) return true;
@@ -83,6 +87,8 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Ctrl *ctl, 
         if (*reinterpret_cast<volatile int *>(&ctl->abort)) return false;
         if (globaltimer_ns() - t0 > a.wait_ns) {
             *reinterpret_cast<volatile int *>(&ctl->abort) = 1;
+            cluster_st_u32(ctl->other_abort, 1u);
+            cluster_fence();
             ssd_report(a.err, SSD_DEVERR_TIMEOUT);
             return false;
         }
@@ -92,6 +98,14 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Ctrl *ctl, 
 // The same by a whole warp, which goes on or gives up as one.
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Ctrl *ctl, const Args &a) {
     return __all_sync(0xffffffffu, wait(bar, parity, ctl, a));
+}
+
+// Where a role has given up, copies may be on their way that nobody has waited for.  A
+// CTA ends only after they have landed: the last blocks' of `issued`, with the default
+// limit, since the one in force may be shorter than a copy takes.
+__device__ __forceinline__ void await_copies(Ctrl *ctl, uint32_t issued, uint32_t stages) {
+    for (uint32_t i = issued > stages ? issued - stages : 0; i < issued; ++i)
+        mbar_wait(smem_u32(&ctl->full[i % stages]), (i / stages) & 1, kSsdDefaultWaitNs);
 }
 
 // Tiles in groups of 8 row tiles, column by column: the CTAs that run at one
@@ -415,6 +429,7 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a,
         }
         mbar_init(smem_u32(&ctl->drain), 1);
         ctl->abort = 0;
+        ctl->other_abort = smem_u32(&ctl->abort);
         fence_mbar_init();
     }
     if (threadIdx.x == 64) {
@@ -440,9 +455,9 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a,
     const int kb0 = kSplit ? (int)((long long)a.kblocks * rank / ranks) : 0;
     const int kb1 = kSplit ? (int)((long long)a.kblocks * (rank + 1) / ranks) : a.kblocks;
 
+    uint32_t n = 0;                     // the producer's: blocks issued so far
     if (warp == 0) {
         if (lane == 0) {
-            uint32_t n = 0;             // blocks issued so far
             bool ok = true;
             for (int t = first; ok && t < ntiles; t += step) {
                 int row, col;
@@ -456,10 +471,6 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a,
                     load_stage<kBN, kAmn, kBmn, kFp8>(&map_a, &map_b, ring + s * kStage,
                                                       smem_u32(&ctl->full[s]), kb, row, col);
                 }
-            }
-            if (!ok) {                  // let the copies in flight land before the CTA ends
-                for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i)
-                    mbar_wait(smem_u32(&ctl->full[i % kStages]), (i / kStages) & 1, a.wait_ns);
             }
         }
     } else if (warp == 1) {
@@ -499,11 +510,12 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a,
                     }
                     mma_commit(smem_u32(&ctl->empty[s]));
                 }
-                if (ok) mma_commit(smem_u32(&ctl->acc_full[buf]));
+                if (ok && !(a.withhold && blockIdx.x == 0 && tiles == 0))
+                    mma_commit(smem_u32(&ctl->acc_full[buf]));
             }
             // every product has ended before the accumulators are freed
             mma_commit(smem_u32(&ctl->drain));
-            mbar_wait(smem_u32(&ctl->drain), 0, a.wait_ns);
+            mbar_wait(smem_u32(&ctl->drain), 0, kSsdDefaultWaitNs);
         }
     } else {
         // a warp reads the 32 TMEM lanes of its number modulo 4; the two warps
@@ -549,6 +561,10 @@ product_tc_kernel(const __grid_constant__ CUtensorMap map_a,
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (ctl->abort) {
+        if (threadIdx.x == 0) await_copies(ctl, n, kStages);
+        __syncthreads();
+    }
     if (warp == 1) tmem_dealloc(tmem, kCols);
 }
 
@@ -630,6 +646,7 @@ product_pair_kernel(const __grid_constant__ Jobs<kTwo> jobs) {
         }
         mbar_init(smem_u32(&ctl->drain), 1);
         ctl->abort = 0;
+        ctl->other_abort = cluster_map(smem_u32(&ctl->abort), in_cluster ^ 1);
         fence_mbar_init();
     }
     if (threadIdx.x == 64) {
@@ -660,43 +677,50 @@ product_pair_kernel(const __grid_constant__ Jobs<kTwo> jobs) {
         kb1 = kSplit ? (int)((long long)n * (part + 1) / parts) : n;
     };
 
+    // block number i of this CTA's share of a tile's operands into its stage
+    const auto issue = [&](const Place &at, int kb, uint32_t i) {
+        const CUtensorMap *map_a = &jobs.job[at.job].map_a, *map_b = &jobs.job[at.job].map_b;
+        const int ar = at.row * 256 + rank * 128, br = at.col * 256 + rank * 128;
+        const uint32_t s = i % kPairStages;
+        const uint32_t own = smem_u32(&ctl->full[s]), bar = cluster_map(own, leader);
+        const uint32_t dst = ring + s * kPairStage;
+        if (rank == 0) mbar_arrive_expect_tx(own, 2 * kPairStage);
+        if (kTwo ? at.job == jobs.amn : kAmn) {
+            tma_load_2d_pair(dst, map_a, bar, ar, kb * kK);
+            tma_load_2d_pair(dst + 8192, map_a, bar, ar + 64, kb * kK);
+        } else {
+            tma_load_2d_pair(dst, map_a, bar, kb * kK, ar);
+        }
+        if constexpr (kBmn) {
+            tma_load_2d_pair(dst + kABytes, map_b, bar, br, kb * kK);
+            tma_load_2d_pair(dst + kABytes + 8192, map_b, bar, br + 64, kb * kK);
+        } else {
+            tma_load_2d_pair(dst + kABytes, map_b, bar, kb * kK, br);
+        }
+    };
+    uint32_t n = 0;                     // the producer's: blocks issued so far
+
     if (warp == 0) {
         if (lane == 0) {
-            uint32_t n = 0;
             bool ok = true;
             Place at;
             for (int j = 0; ok && tile(j, at); ++j) {
-                const CUtensorMap *map_a = &jobs.job[at.job].map_a, *map_b = &jobs.job[at.job].map_b;
-                const int ar = at.row * 256 + rank * 128, br = at.col * 256 + rank * 128;
-                const bool amn = kTwo ? at.job == jobs.amn : kAmn;
                 int kb, kb1;
                 for (blocks(at, kb, kb1); kb < kb1; ++kb, ++n) {
-                    const uint32_t s = n % kPairStages, turn = n / kPairStages;
-                    if (turn > 0 && !wait(&ctl->empty[s], (turn - 1) & 1, ctl, a)) {
+                    const uint32_t turn = n / kPairStages;
+                    if (turn > 0 && !wait(&ctl->empty[n % kPairStages], (turn - 1) & 1, ctl, a)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t own = smem_u32(&ctl->full[s]), bar = cluster_map(own, leader);
-                    const uint32_t dst = ring + s * kPairStage;
-                    if (rank == 0) mbar_arrive_expect_tx(own, 2 * kPairStage);
-                    if (amn) {
-                        tma_load_2d_pair(dst, map_a, bar, ar, kb * kK);
-                        tma_load_2d_pair(dst + 8192, map_a, bar, ar + 64, kb * kK);
-                    } else {
-                        tma_load_2d_pair(dst, map_a, bar, kb * kK, ar);
-                    }
-                    if constexpr (kBmn) {
-                        tma_load_2d_pair(dst + kABytes, map_b, bar, br, kb * kK);
-                        tma_load_2d_pair(dst + kABytes + 8192, map_b, bar, br + 64, kb * kK);
-                    } else {
-                        tma_load_2d_pair(dst + kABytes, map_b, bar, kb * kK, br);
-                    }
+                    issue(at, kb, n);
                 }
             }
-            if (!ok && rank == 0) {     // let both CTAs' copies in flight land
-                for (uint32_t i = n > kPairStages ? n - kPairStages : 0; i < n; ++i)
-                    mbar_wait(smem_u32(&ctl->full[i % kPairStages]), (i / kPairStages) & 1, a.wait_ns);
-            }
+            // the last stages too have been handed back: no arrival at these barriers is
+            // on its way when the CTA ends
+            for (uint32_t i = n > kPairStages ? n - kPairStages : 0; ok && i < n; ++i)
+                ok = wait(&ctl->empty[i % kPairStages], (i / kPairStages) & 1, ctl, a);
+            ctl->issued = n;
+            cluster_fence();
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
@@ -706,7 +730,8 @@ product_pair_kernel(const __grid_constant__ Jobs<kTwo> jobs) {
             uint32_t n = 0;
             bool ok = true;
             Place at;
-            for (int j = 0; ok && tile(j, at); ++j) {
+            int j = 0;
+            for (; ok && tile(j, at); ++j) {
                 const uint32_t buf = j & 1, turn = (uint32_t)j >> 1;
                 const uint32_t d = tmem + buf * kPairBN;
                 const bool amn = kTwo ? at.job == jobs.amn : kAmn;
@@ -714,7 +739,10 @@ product_pair_kernel(const __grid_constant__ Jobs<kTwo> jobs) {
                                          : idesc_bf16_f32(256, kPairBN, amn, kBmn);
                 const uint64_t ad = smem_desc(ring, amn ? 8192 : 16, 1024, kSwizzle128B);
                 const uint64_t a_step = amn ? 2048 >> 4 : 32 >> 4;
-                if (turn > 0 && !wait(&ctl->acc_empty[buf], (turn - 1) & 1, ctl, a)) break;
+                if (turn > 0 && !wait(&ctl->acc_empty[buf], (turn - 1) & 1, ctl, a)) {
+                    ok = false;
+                    break;
+                }
                 tc_fence_after();
                 int kb, kb1;
                 bool more = false;      // the tile's first product writes, the others add
@@ -733,11 +761,18 @@ product_pair_kernel(const __grid_constant__ Jobs<kTwo> jobs) {
                     more = true;
                     mma_commit_pair(smem_u32(&ctl->empty[s]), both);
                 }
-                if (ok) mma_commit_pair(smem_u32(&ctl->acc_full[buf]), both);
+                if (ok && !(a.withhold && blockIdx.x == 0 && j == 0))
+                    mma_commit_pair(smem_u32(&ctl->acc_full[buf]), both);
+            }
+            // both CTAs' epilogues have handed back the last accumulators: their arrivals
+            // at these barriers are not on their way when this CTA ends
+            if constexpr (!kSplit) {
+                for (int i = j > 2 ? j - 2 : 0; ok && i < j; ++i)
+                    ok = wait(&ctl->acc_empty[i & 1], (i >> 1) & 1, ctl, a);
             }
             // every product has ended before the accumulators are freed
             mma_commit_pair(smem_u32(&ctl->drain), both);
-            mbar_wait(smem_u32(&ctl->drain), 0, a.wait_ns);
+            mbar_wait(smem_u32(&ctl->drain), 0, kSsdDefaultWaitNs);
         }
     } else {
         const int quarter = warp & 3, half = (warp - 2) >> 2;
@@ -779,6 +814,20 @@ product_pair_kernel(const __grid_constant__ Jobs<kTwo> jobs) {
     // been read: only an arrival that releases waits for the loads of them
     if constexpr (kSplit) cluster_sync_all();
     else cluster_sync_relaxed();
+    // the issuer's last commit has arrived in the odd CTA too
+    if (warp == 1 && lane == 0 && rank == 1) mbar_wait(smem_u32(&ctl->drain), 0, kSsdDefaultWaitNs);
+    __syncwarp();
+    if (ctl->abort) {           // in both CTAs or in neither
+        // The even CTA's barriers count both CTAs' copies: each issues what the other has
+        // (any block will do, nobody reads it), and the even one waits for all.
+        if (threadIdx.x == 0) {
+            const uint32_t all =
+                max(n, cluster_ld_u32(cluster_map(smem_u32(&ctl->issued), in_cluster ^ 1)));
+            for (; n < all; ++n) issue(Place{0, 0, 0}, 0, n);
+            if (rank == 0) await_copies(ctl, all, kPairStages);
+        }
+        __syncwarp();
+    }
     if (warp == 1) tmem_dealloc_pair(tmem, 512);
     __syncwarp();
     cluster_sync_relaxed();     // nor before both have freed the tensor memory they share
@@ -817,7 +866,9 @@ Args args_of(const SsdProduct &p, int bm, int bn, bool fp8, unsigned *err) {
     a.vec = on_16(p.out, p.out_row, so) && (!p.residual || on_16(p.residual, p.residual_row, so)) &&
             (!p.preact || on_16(p.preact, p.n, 2));
     a.err = err;
-    a.wait_ns = ssd_debug_config().wait_ns;
+    const SsdDebug dbg = ssd_debug_config();
+    a.wait_ns = dbg.wait_ns;
+    a.withhold = dbg.fault == kSsdFaultWithholdSignal;
     return a;
 }
 
