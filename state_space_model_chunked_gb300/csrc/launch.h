@@ -246,7 +246,8 @@ struct SsdActBwd {
 };
 // A launch that may start while the kernel in front of it in the stream still runs:
 // the kernel calls griddep_wait before it touches anything that one may, so what
-// overlaps is the launch and the set-up.
+// overlaps is the launch and the set-up.  It reads with ordinary loads: those of the
+// read-only cache are defined for memory that nobody writes while the kernel lives.
 template <typename... P, typename... A>
 cudaError_t ssd_launch_early(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t stream,
                              A... args) {

@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(32 * kWarps) product_few_kernel(const SsdProdu
                 const Pairs<kFp8> ag(a[u][h][0]), ah(a[u][h][1]);
 #pragma unroll
                 for (int j = 0; j < kNT; ++j) {
-                    const Pairs<kFp8> b(in ? __ldg(reinterpret_cast<const uint4 *>(xt[j] + k * kSize))
+                    const Pairs<kFp8> b(in ? *reinterpret_cast<const uint4 *>(xt[j] + k * kSize)
                                            : zero);
 #pragma unroll
                     for (int i = 0; i < Pairs<kFp8>::kN; i += 2) {

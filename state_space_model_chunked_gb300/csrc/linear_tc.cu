@@ -154,8 +154,8 @@ __device__ __forceinline__ void fetch_columns(const Args &a, Columns *cols, int 
     for (int k = 0; k < kBN / 64; ++k) {
         const long long n = n0 + half * 32 + k * 64 + lane;
         const bool in = n < a.p.n;
-        cols->bias[k * 32 + lane] = a.p.bias && in ? __ldg(a.p.bias + n) : 0.f;
-        cols->scale[k * 32 + lane] = a.p.a_scale && in ? __ldg(a.p.b_scale + n) : 0.f;
+        cols->bias[k * 32 + lane] = a.p.bias && in ? a.p.bias[n] : 0.f;
+        cols->scale[k * 32 + lane] = a.p.a_scale && in ? a.p.b_scale[n] : 0.f;
     }
     __syncwarp();
 }
@@ -239,7 +239,7 @@ struct RowPart {
 template <typename TO, int kBN, typename F, typename G>
 __device__ __forceinline__ bool drain(const Args &a, const Columns *cols, uint32_t acc, int half,
                                       long long m, long long n0, F &&ready, G &&read) {
-    const float scale = a.p.a_scale && m < a.p.m ? __ldg(a.p.a_scale + m) : 1.f;
+    const float scale = a.p.a_scale && m < a.p.m ? a.p.a_scale[m] : 1.f;
     RowPart<TO, 32> part;
     part.ask(a, m, n0 + half * 32);
     if (!ready()) return false;
@@ -358,7 +358,7 @@ __device__ __forceinline__ void finish_split(const Args &a, uint32_t ring, int r
         constexpr int kPart = 16;
         const long long m = row0 + r;
         if (m >= a.p.m) return;
-        const float scale = a.p.a_scale ? __ldg(a.p.a_scale + m) : 1.f;
+        const float scale = a.p.a_scale ? a.p.a_scale[m] : 1.f;
 #pragma unroll 1
         for (int c = (rank * 2 + half) * kPart; c < kBN; c += 2 * kPart * ranks) {
             const long long n = col0 + c;
@@ -368,7 +368,7 @@ __device__ __forceinline__ void finish_split(const Args &a, uint32_t ring, int r
             const auto last = [&](auto part) {
                 part.ask(a, m, n);
                 const auto at = [&](const float *q) {
-                    return [=](int i) { return i < part.left ? __ldg(q + n + i) : 0.f; };
+                    return [=](int i) { return i < part.left ? q[n + i] : 0.f; };
                 };
                 part.finish(a, m, n, scale, at(a.p.bias), at(a.p.b_scale), v);
             };
