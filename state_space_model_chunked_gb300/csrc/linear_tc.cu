@@ -247,6 +247,7 @@ __device__ __forceinline__ bool drain(const Args &a, const Columns *cols, uint32
 #pragma unroll 1
     for (int c = half * 32; c < kBN; c += 64) {
         if (c >= 64) part.ask(a, m, n0 + c);
+        __syncwarp();           // rows past the end part here, the load is the whole warp's
         uint32_t r[32];
         tmem_ld32(acc + c, r);
         tmem_ld_wait(r);
