@@ -27,10 +27,10 @@
 #include <cuda.h>
 
 #include <algorithm>
-#include <atomic>
 #include <limits>
 
 #include "act.cuh"
+#include "answers.h"
 #include "launch.h"
 #include "ptx.cuh"
 #include "vec.cuh"
@@ -873,31 +873,34 @@ Args args_of(const SsdProduct &p, int bm, int bn, bool fp8, unsigned *err) {
     return a;
 }
 
-// Clusters of r CTAs that the device holds at once.  They do not span the SMs'
-// groups, so that can be fewer than the SMs over r.  Every kernel here takes an
-// SM to itself, so one answer serves them all; it is asked for once.
+// Clusters of r CTAs that the current device holds at once.  They do not span the SMs'
+// groups, so that can be fewer than the SMs over r, which stand in where the device
+// does not answer.  Every kernel here takes an SM to itself, so one answer of a device
+// serves them all.
 template <typename Kernel>
-int clusters_at_once(Kernel kernel, cudaLaunchConfig_t cfg, int r) {
-    static std::atomic<int> known[9];       // the answer plus one; 0: not asked yet
-    int n = known[r].load(std::memory_order_relaxed) - 1;
-    if (n >= 0) return n;
-    cfg.gridDim = dim3((unsigned)r);
-    cfg.attrs->val.clusterDim.x = r;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+int clusters_at_once(Kernel kernel, cudaLaunchConfig_t cfg, int r, int sms) {
+    static SsdAnswers<9> answers;
+    int device = -1;
+    if (cudaGetDevice(&device) != cudaSuccess) device = -1;
+    const int n = answers.get(device, r, [&]() {
+        int found = 0;
+        cfg.gridDim = dim3((unsigned)r);
+        cfg.attrs->val.clusterDim.x = r;
+        if (cudaOccupancyMaxActiveClusters(&found, kernel, &cfg) == cudaSuccess) return found;
         (void)cudaGetLastError();
-        n = 0;
-    }
-    known[r].store(n + 1, std::memory_order_relaxed);
-    return n;
+        return -1;
+    });
+    return n >= 0 ? n : sms / r;
 }
 
 // Ranks of a split: the largest cluster of which there is one for every tile at
 // once (with 20 tiles, seven ranks took two waves), of at least two k blocks a
 // rank, at most eight (portable cluster size).
 template <typename Kernel>
-int split_ranks(Kernel kernel, const cudaLaunchConfig_t &cfg, long long tiles, long long kblocks) {
+int split_ranks(Kernel kernel, const cudaLaunchConfig_t &cfg, long long tiles, long long kblocks,
+                int sms) {
     for (int r = 8; r > 1; --r)
-        if (kblocks >= 2 * r && tiles <= clusters_at_once(kernel, cfg, r)) return r;
+        if (kblocks >= 2 * r && tiles <= clusters_at_once(kernel, cfg, r, sms)) return r;
     return 1;
 }
 
@@ -932,7 +935,7 @@ cudaError_t launch(const SsdProduct &p, int sms, unsigned *err, cudaStream_t str
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    const int ranks = kSplit ? split_ranks(kernel, cfg, tiles, a.kblocks) : 1;
+    const int ranks = kSplit ? split_ranks(kernel, cfg, tiles, a.kblocks, sms) : 1;
     attr[0].val.clusterDim.x = ranks;
     cfg.gridDim = dim3((unsigned)(kSplit ? tiles * ranks : (tiles < sms ? tiles : sms)));
     return cudaLaunchKernelEx(&cfg, kernel, ma, mb, a);
@@ -970,7 +973,7 @@ cudaError_t pair_config(Kernel kernel, cudaLaunchConfig_t *cfg, cudaLaunchAttrib
 }
 
 template <bool kAmn, bool kBmn, bool kFp8, bool kSplit>
-cudaError_t launch_pair(const SsdProduct &p, int tile0, int tile1, unsigned *err,
+cudaError_t launch_pair(const SsdProduct &p, int tile0, int tile1, int sms, unsigned *err,
                         cudaStream_t stream) {
     Jobs<false> jobs{};
     if (!pair_job(&jobs.job[0], p, kAmn, kBmn, kFp8, tile0, tile1, err)) return cudaErrorInvalidValue;
@@ -982,9 +985,11 @@ cudaError_t launch_pair(const SsdProduct &p, int tile0, int tile1, unsigned *err
     if (e != cudaSuccess) return e;
     const long long tiles = a.tile1 - a.tile0;
     int parts = kSplit ? 4 : 1;
-    while (parts > 1 && (a.kblocks < 2 * parts || tiles > clusters_at_once(kernel, cfg, 2 * parts)))
+    while (parts > 1 &&
+           (a.kblocks < 2 * parts || tiles > clusters_at_once(kernel, cfg, 2 * parts, sms)))
         --parts;
-    const long long pairs = kSplit ? tiles : std::min<long long>(tiles, std::max(1, clusters_at_once(kernel, cfg, 2)));
+    const long long pairs =
+        kSplit ? tiles : std::min<long long>(tiles, std::max(1, clusters_at_once(kernel, cfg, 2, sms)));
     attr[0].val.clusterDim.x = 2 * parts;
     cfg.gridDim = dim3((unsigned)(2 * parts * pairs));
     return cudaLaunchKernelEx(&cfg, kernel, jobs);
@@ -1045,13 +1050,13 @@ cudaError_t many(const SsdProduct &p, int sms, unsigned *err, cudaStream_t strea
     const Choice c = choose(p, kFp8, sms);
     switch (c.way) {
         case Way::whole: return launch<128, kAmn, kBmn, kFp8, false, false>(p, sms, err, stream);
-        case Way::pairs: return launch_pair<kAmn, kBmn, kFp8, false>(p, 0, -1, err, stream);
+        case Way::pairs: return launch_pair<kAmn, kBmn, kFp8, false>(p, 0, -1, sms, err, stream);
         case Way::split: return launch<128, kAmn, kBmn, kFp8, false, true>(p, sms, err, stream);
-        case Way::split_pairs: return launch_pair<kAmn, kBmn, kFp8, true>(p, 0, -1, err, stream);
+        case Way::split_pairs: return launch_pair<kAmn, kBmn, kFp8, true>(p, 0, -1, sms, err, stream);
         default: break;
     }
-    const cudaError_t e = launch_pair<kAmn, kBmn, kFp8, false>(p, 0, c.full, err, stream);
-    return e != cudaSuccess ? e : launch_pair<kAmn, kBmn, kFp8, true>(p, c.full, -1, err, stream);
+    const cudaError_t e = launch_pair<kAmn, kBmn, kFp8, false>(p, 0, c.full, sms, err, stream);
+    return e != cudaSuccess ? e : launch_pair<kAmn, kBmn, kFp8, true>(p, c.full, -1, sms, err, stream);
 }
 
 // Two products in one launch of `pairs` pairs: how its tiles are dealt (Jobs), and
@@ -1123,7 +1128,7 @@ cudaError_t ssd_launch_product_two(const SsdProduct &dx, const SsdProduct &dw, i
     const bool dw_first = dw.k > dx.k;
     const SsdProduct &one = dw_first ? dw : dx, &two = dw_first ? dx : dw;
     const long long tiles = tiles_of(one, 256, 256) + tiles_of(two, 256, 256);
-    const long long pairs = std::min<long long>(tiles, std::max(1, clusters_at_once(kernel, cfg, 2)));
+    const long long pairs = std::min<long long>(tiles, std::max(1, clusters_at_once(kernel, cfg, 2, sms)));
     const Deal d = deal(one, two, pairs);
     const long long apart =
         choose(dx, false, sms).cost + choose(dw, false, sms).cost + kLaunchCost;
