@@ -39,9 +39,11 @@ __device__ __forceinline__ void load_tile(float (*dst)[kTile + 4], const T *p, l
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256) product_simt_kernel(const SsdProduct p) {
+__global__ void __launch_bounds__(256)
+product_simt_kernel(const SsdProduct p, const unsigned row_tiles) {
     __shared__ __align__(16) float as[kStep][kTile + 4], bs[kStep][kTile + 4];
-    const long long m0 = (long long)blockIdx.x * kTile, n0 = (long long)blockIdx.y * kTile;
+    const long long m0 = (long long)(blockIdx.x % row_tiles) * kTile;
+    const long long n0 = (long long)(blockIdx.x / row_tiles) * kTile;
     const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
     float acc[4][4] = {};
     for (long long k0 = 0; k0 < p.k; k0 += kStep) {
@@ -176,12 +178,13 @@ cudaError_t launch_act_bwd(const SsdActBwd &a, float *partial, int n, SsdOrder o
 }  // namespace
 
 cudaError_t ssd_launch_product_simt(const SsdProduct &p, cudaStream_t stream) {
-    const dim3 grid((unsigned)((p.m + kTile - 1) / kTile), (unsigned)((p.n + kTile - 1) / kTile));
-    switch (p.in) {
-        case SSD_ELT_F32: product_simt_kernel<float><<<grid, 256, 0, stream>>>(p); break;
-        case SSD_ELT_BF16: product_simt_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(p); break;
-        default: product_simt_kernel<__nv_fp8_e4m3><<<grid, 256, 0, stream>>>(p); break;
-    }
+    // one dimension of tiles: the others of a grid end at 65535, which 2^22 features pass
+    const long long rows = (p.m + kTile - 1) / kTile, tiles = rows * ((p.n + kTile - 1) / kTile);
+    if (tiles >= (1ll << 31)) return cudaErrorInvalidValue;     // more than any memory holds
+    const auto kernel = p.in == SSD_ELT_F32    ? product_simt_kernel<float>
+                        : p.in == SSD_ELT_BF16 ? product_simt_kernel<__nv_bfloat16>
+                                               : product_simt_kernel<__nv_fp8_e4m3>;
+    kernel<<<(unsigned)tiles, 256, 0, stream>>>(p, (unsigned)rows);
     return cudaGetLastError();
 }
 

@@ -13,7 +13,7 @@ import torch
 
 import state_space_model_chunked_gb300 as ssd
 from tests import layer_ref as ref
-from tests.gpu_util import host
+from tests.gpu_util import host, rel
 
 pytestmark = pytest.mark.gpu
 FP8 = torch.float8_e4m3fn
@@ -64,3 +64,17 @@ def test_sums_split_over_a_cluster(m, n, dtype, k):
     """Rows and columns past the end take no part in the exchange of sums."""
     _check(m, n, k, dtype)
     _check(m, n, k, dtype, torch.float32, "relu")
+
+
+@pytest.mark.parametrize("wide", [4194240, 4194241, 4194303])
+def test_most_columns_in_32_bits(wide):
+    """Tiles of 64 columns past 65535: the last sizes below the limit of 2^22."""
+    rng = np.random.default_rng(wide)
+    x, w = _values(rng, 5, 3), _values(rng, wide, 3)
+    y = ssd.linear_fwd(x, w)
+    assert rel(host(y), host(x) @ host(w).T) <= 1e-5
+    # the gradients of a product of as many inner values
+    dy, x, w = _values(rng, 5, 2), _values(rng, 5, wide), _values(rng, 2, wide)
+    dx, dw, _ = ssd.linear_bwd(dy, x, w, bias=False)
+    assert rel(host(dx), host(dy) @ host(w)) <= 1e-5 and rel(host(dw), host(dy).T @ host(x)) <= 1e-5
+    ssd.last_device_error()
