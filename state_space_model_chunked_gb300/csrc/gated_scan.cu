@@ -636,15 +636,13 @@ gated_bwd_kernel(const SsdGatedBwd a, const Joins joins, const Walk walk) {
     if (at == 0) pass_empty<V>(a.in, a.dfinal, a.dinit, c);
 
     // the run forward (A, H) and backward (A, M)
-    Val<V> drop[kBwdTok], q[kBwdTok], dh[kBwdTok], sig[kGate ? kBwdTok : 1];
+    Val<V> keep[kBwdTok], drop[kBwdTok], dh[kBwdTok], sig[kGate ? kBwdTok : 1];
     Val<V> A = all<V>(1.f), H = all<V>(0.f), M = all<V>(0.f);
     by_form(plain, [&](auto form) {
         constexpr bool kPlain = decltype(form)::kOn;
 #pragma unroll
         for (int i = 0; i < kBwdTok; ++i) {
-            Val<V> keep;
-            gate(value(graw[i]), keep, drop[i]);
-            q[i] = keep * drop[i];
+            gate(value(graw[i]), keep[i], drop[i]);
             const Val<V> u = drop[i] * value(xraw[i]);
             if (!kPlain && ((m.starts >> i) & 1u)) {
                 const int seq = __shfl_sync(0xffffffffu, m.seq, i);
@@ -652,10 +650,10 @@ gated_bwd_kernel(const SsdGatedBwd a, const Joins joins, const Walk walk) {
                 load_f32<V>(a.in.init + (size_t)seq * width + c, on && a.in.init != nullptr,
                             first.v);
                 A = all<V>(0.f);
-                H = fma(keep, first, u);
+                H = fma(keep[i], first, u);
             } else if (kPlain || i < n) {
-                A = A * keep;
-                H = fma(keep, H, u);
+                A = A * keep[i];
+                H = fma(keep[i], H, u);
             }
         }
 #pragma unroll
@@ -673,7 +671,7 @@ gated_bwd_kernel(const SsdGatedBwd a, const Joins joins, const Walk walk) {
                 load_f32<V>(a.dfinal + (size_t)seq * width + c, on && a.dfinal != nullptr, lam.v);
                 lam = dh[i] + lam;
             }
-            M = !kPlain && ((m.starts >> i) & 1u) ? all<V>(0.f) : lam - drop[i] * lam;
+            M = !kPlain && ((m.starts >> i) & 1u) ? all<V>(0.f) : keep[i] * lam;
         }
     });
 #pragma unroll
@@ -685,7 +683,8 @@ gated_bwd_kernel(const SsdGatedBwd a, const Joins joins, const Walk walk) {
     const Entering<V> e = join_begin<V, kBwdWarps, kJoin>(
         runs, joins, at, width, c, kBwdWarps - 1 - warp, m.starts != 0, A, M);
 
-    // forward: the states, f (1 - f) (x - h_{t-1}) in place of f (1 - f), and dz
+    // forward: the states, f (1 - f) (x - h_{t-1}), and dz
+    Val<V> q[kBwdTok];
     for (int w = 0; w < warp; ++w) {
         Val<V> wa, wh;
 #pragma unroll
@@ -703,7 +702,7 @@ gated_bwd_kernel(const SsdGatedBwd a, const Joins joins, const Walk walk) {
                 load_f32<V>(a.in.init + (size_t)seq * width + c, on && a.in.init != nullptr, h.v);
             }
             const Val<V> to = value(xraw[i]) - h;       // h_t = h_{t-1} + (1 - f) (x - h_{t-1})
-            q[i] = q[i] * to;
+            q[i] = keep[i] * drop[i] * to;
             h = fma(drop[i], to, h);
             if constexpr (kGate) {
                 const Val<V> o = h * fma(sig[i], value(yraw[i]) - dh[i], dh[i]);
@@ -727,25 +726,18 @@ gated_bwd_kernel(const SsdGatedBwd a, const Joins joins, const Walk walk) {
                 load_f32<V>(a.dfinal + (size_t)seq * width + c, on && a.dfinal != nullptr, lam.v);
                 lam = dh[i] + lam;
             }
+            // f lam by f, not as lam - (1 - f) lam: where dy is zero, f lam is all that the
+            // tokens in front receive, and the difference has no digits of a small f
             const Val<V> ox = drop[i] * lam;
-            mu = lam - ox;
+            mu = keep[i] * lam;
             const Val<V> og = minus(lam * q[i]);
             if (kPlain || on) {
                 ssd_store_vec<V>(dx + i * a.dx_stride + (unsigned)c, ox.v);
                 ssd_store_vec<V>(dg + i * a.dg_stride + (unsigned)c, og.v);
             }
             if (!kPlain && ((m.starts >> i) & 1u) && a.dinit) {
-                // dinit = f lam with a small f's own precision, which lam - (1 - f) lam
-                // does not have (and, added to dh, does not need)
                 const int seq = __shfl_sync(0xffffffffu, m.seq, i);
-                if (on) {
-                    SsdRaw<T, V> again;
-                    again.load(static_cast<const T *>(a.in.g) + (t0 + i) * a.in.g_stride + c);
-                    Val<V> keep, unused;
-                    gate(value(again), keep, unused);
-                    keep = keep * lam;
-                    ssd_store_vec<V>(a.dinit + (size_t)seq * width + c, keep.v);
-                }
+                if (on) ssd_store_vec<V>(a.dinit + (size_t)seq * width + c, mu.v);
             }
         }
     });

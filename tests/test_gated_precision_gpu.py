@@ -1,0 +1,50 @@
+"""The recurrence where its gates nearly close: f and 1 - f each keep a precision of
+their own, also where the one that is near zero is all that a result is made of.
+
+Bars, derived before the first run.  f comes from the hardware's exponential of a
+rounded argument: |g| 2^-24 + 4 * 2^-23 of itself, and a token's multiplications add
+2 * 2^-23.  A result that is a product of j such factors errs by at most
+j (|g| 2^-24 + 6 * 2^-23), below 1e-5 for j <= 5 and |g| <= 20; every token is held to
+1e-5 of its own size."""
+import numpy as np
+import pytest
+import torch
+
+import state_space_model_chunked_gb300 as ssd
+from tests import layer_ref as ref
+from tests.gpu_util import host
+
+pytestmark = pytest.mark.gpu
+BAR = 1e-5
+
+
+def _values(rng, *shape):
+    return torch.from_numpy(rng.standard_normal(shape, dtype=np.float32)).cuda()
+
+
+def _each_row(got, want, rows):
+    for t in rows:
+        wrong = np.linalg.norm(got[t] - want[t])
+        assert wrong <= BAR * np.linalg.norm(want[t]), (t, wrong / np.linalg.norm(want[t]))
+
+
+@pytest.mark.parametrize("length", [3, 5, 10, 66, 130, 450])
+@pytest.mark.parametrize("gate", [-9.0, -12.0, -18.0])
+@pytest.mark.parametrize("width", [64, 33])
+def test_gradient_of_the_last_token_alone(length, gate, width):
+    """Earlier tokens' gradients are products of closed gates (f), across warps' and tiles' ends too."""
+    rng = np.random.default_rng(length)
+    x, init = _values(rng, length, width), _values(rng, 1, width)
+    g = gate + 0.2 * _values(rng, length, width)
+    dy = torch.zeros_like(x)
+    dy[-1] = _values(rng, width)
+    _, _, kept = ssd.gated_scan_fwd(x[None], g[None], None, init, return_checkpoints=True)
+    dx, dg, _, dinit = ssd.gated_scan_bwd(dy[None], x[None], g[None], kept, None, init)
+    dxr, dgr, _, dir_ = ref.gated_bwd(host(dy), host(x), host(g), None, host(init), np.zeros((1, width)), [0, length])
+    last = range(length - 1, max(length - 5, -1), -1)
+    _each_row(host(dx)[0], dxr, last)
+    # x and the state before it are of one size here, so their difference is exact to a few 2^-23 of it
+    _each_row(host(dg)[0], dgr, last)
+    if length <= 4:
+        _each_row(host(dinit), dir_, [0])
+    ssd.last_device_error()
