@@ -701,9 +701,9 @@ gated_bwd_kernel(const SsdGatedBwd a, const Joins joins, const Walk walk) {
                 const int seq = __shfl_sync(0xffffffffu, m.seq, i);
                 load_f32<V>(a.in.init + (size_t)seq * width + c, on && a.in.init != nullptr, h.v);
             }
-            const Val<V> to = value(xraw[i]) - h;       // h_t = h_{t-1} + (1 - f) (x - h_{t-1})
-            q[i] = keep[i] * drop[i] * to;
-            h = fma(drop[i], to, h);
+            const Val<V> x = value(xraw[i]);
+            q[i] = keep[i] * drop[i] * (x - h);
+            h = fma(keep[i], h, drop[i] * x);   // as the forward pass has it
             if constexpr (kGate) {
                 const Val<V> o = h * fma(sig[i], value(yraw[i]) - dh[i], dh[i]);
                 if (kPlain || on) ssd_store_vec<V>(dz + i * a.dz_stride + (unsigned)c, o.v);

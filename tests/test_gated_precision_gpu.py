@@ -48,3 +48,26 @@ def test_gradient_of_the_last_token_alone(length, gate, width):
     if length <= 4:
         _each_row(host(dinit), dir_, [0])
     ssd.last_device_error()
+
+
+@pytest.mark.parametrize("start", [0, 1, 5, 60, 63])
+@pytest.mark.parametrize("gate", [-9.0, -12.0, -18.0])
+@pytest.mark.parametrize("width", [64, 33])
+def test_state_that_outweighs_the_inputs(start, gate, width):
+    """Inputs of zero behind a state: what is left of it is a product of closed gates, in y, dz and dg alike."""
+    rng = np.random.default_rng(start)
+    length, after = start + 5, slice(start, start + 4)
+    x, z, dy = (_values(rng, length, width) for _ in range(3))
+    g = _values(rng, length, width)
+    x[after], g[after] = 0.0, gate + 0.2 * g[after]
+    init = _values(rng, 1, width)
+    y, _, kept = ssd.gated_scan_fwd(x[None], g[None], z[None], init, return_checkpoints=True)
+    _, dg, dz, _ = ssd.gated_scan_bwd(dy[None], x[None], g[None], kept, z[None], init)
+    hx, hg, hz, hi = host(x), host(g), host(z), host(init)
+    yr = ref.gated_fwd(hx, hg, hz, hi, [0, length])[0]
+    _, dgr, dzr, _ = ref.gated_bwd(host(dy), hx, hg, hz, hi, np.zeros((1, width)), [0, length])
+    rows = range(start, start + 4)
+    _each_row(host(y)[0], yr, rows)
+    _each_row(host(dz)[0], dzr, rows)
+    _each_row(host(dg)[0], dgr, rows)
+    ssd.last_device_error()
