@@ -312,17 +312,27 @@ __device__ __forceinline__ Marks marks(const SsdGated &a, const Divisor &by_leng
     return m;
 }
 
-// Empty sequences hand `in` (zeros without one) on to `out`; the CTAs of one
-// tile do this for all of them.
+// Empty sequences hand `in` (zeros without one) on to `out`.  Each of the walk's tiles
+// looks at its share of the sequences, a lane at one, behind all that others wait for:
+// in front of the first tile's run, a million of them held the tiles behind it up for
+// more than the limit of a wait.
 template <int V>
-__device__ __forceinline__ void pass_empty(const SsdGated &a, const float *in, float *out, int c) {
-    if (!out || c >= a.width) return;
-    for (int s = threadIdx.x >> 5; s < a.nseq; s += blockDim.x >> 5) {
-        const bool empty = a.cu ? __ldg(a.cu + s) == __ldg(a.cu + s + 1) : a.length == 0;
-        if (!empty) continue;
+__device__ __forceinline__ void pass_empty(const SsdGated &a, const float *in, float *out, int at,
+                                           int tiles, int c) {
+    if (!out || (!a.cu && a.length > 0)) return;
+    const int lane = threadIdx.x & 31;
+    const long long step = (long long)tiles * blockDim.x;
+    for (long long s0 = (long long)at * blockDim.x + threadIdx.x - lane; s0 < a.nseq; s0 += step) {
+        const long long mine = s0 + lane;
+        const bool empty =
+            mine < a.nseq && (!a.cu || __ldg(a.cu + mine) == __ldg(a.cu + mine + 1));
+        for (unsigned left = __ballot_sync(0xffffffffu, empty); left; left &= left - 1) {
+            const size_t s = (size_t)(s0 + __ffs((int)left) - 1);
+            if (c >= a.width) continue;
 #pragma unroll
-        for (int k = 0; k < V; ++k)
-            out[(size_t)s * a.width + c + k] = in ? in[(size_t)s * a.width + c + k] : 0.f;
+            for (int k = 0; k < V; ++k)
+                out[s * a.width + c + k] = in ? in[s * a.width + c + k] : 0.f;
+        }
     }
 }
 
@@ -529,7 +539,6 @@ gated_fwd_kernel(const SsdGatedFwd a, const Joins joins, const Walk walk) {
     }
     const Marks m = marks(a.in, walk.by_length, t0, kFwdTok);
     const bool plain = whole && (m.starts | m.ends) == 0;
-    if (at == 0) pass_empty<V>(a.in, a.in.init, a.final_state, c);
 
     Val<V> keep[kFwdTok], u[kFwdTok], A = all<V>(1.f), H = all<V>(0.f);
     by_form(plain, [&](auto form) {
@@ -589,6 +598,7 @@ gated_fwd_kernel(const SsdGatedFwd a, const Joins joins, const Walk walk) {
             }
         }
     });
+    pass_empty<V>(a.in, a.in.init, a.final_state, at, walk.tiles, c);
 }
 
 // Backward: the same joins from the last tile to the first, on the gradient
@@ -633,7 +643,6 @@ gated_bwd_kernel(const SsdGatedBwd a, const Joins joins, const Walk walk) {
     }
     const Marks m = marks(a.in, walk.by_length, t0, kBwdTok);
     const bool plain = whole && (m.starts | m.ends) == 0;
-    if (at == 0) pass_empty<V>(a.in, a.dfinal, a.dinit, c);
 
     // the run forward (A, H) and backward (A, M)
     Val<V> keep[kBwdTok], drop[kBwdTok], dh[kBwdTok], sig[kGate ? kBwdTok : 1];
@@ -741,6 +750,7 @@ gated_bwd_kernel(const SsdGatedBwd a, const Joins joins, const Walk walk) {
             }
         }
     });
+    pass_empty<V>(a.in, a.dfinal, a.dinit, at, walk.tiles, c);
 }
 
 // One token of every (row, channel): the state is read and written in place.
