@@ -5,8 +5,9 @@
 #include "launch.h"
 #include "ptx.cuh"
 
-// 1 / (1 + e^-p) by the hardware's exponential and reciprocal (a few 2^-23);
-// e^-p past fp32's range gives 0.
+// 1 / (1 + e^-p) by the hardware's exponential and reciprocal, to (1.25 |p| + 8) 2^-24
+// of itself (the exponential's argument is one rounded product); below p = -87 it
+// runs out of fp32's normal range and is 0.
 __device__ __forceinline__ float ssd_sigmoid(float p) {
     return ssdptx::rcp_approx(1.f + ssdptx::ex2_approx(p * -1.44269504f));
 }

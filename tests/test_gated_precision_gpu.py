@@ -71,3 +71,32 @@ def test_state_that_outweighs_the_inputs(start, gate, width):
     _each_row(host(dz)[0], dzr, rows)
     _each_row(host(dg)[0], dgr, rows)
     ssd.last_device_error()
+
+
+def _bound(v, more=0):
+    """What sigmoid(v) may err by, of itself: |v| log2 e is one rounded product with a
+    rounded constant (1.22 |v| 2^-24 of the exponential), the hardware's exponential errs by
+    2^-22, its reciprocal by 2^-23, and two roundings come after; `more` of 2^-24."""
+    return (1.25 * np.abs(v) + 8 + more) * 2.0 ** -24
+
+
+def test_gates_value_by_value():
+    g = torch.cat([torch.linspace(-80, 80, 40001), torch.linspace(-1, 1, 4001)]).cuda()[None]
+    one, zero = torch.ones_like(g), torch.zeros_like(g)
+    keep, drop = one.clone(), zero.clone()
+    ssd.gated_state_update(keep, zero, g)              # f * 1 + (1 - f) * 0
+    ssd.gated_state_update(drop, one, g)               # f * 0 + (1 - f) * 1
+    v = host(g)
+    assert np.all(np.abs(host(keep) - ref.sigmoid(v)) <= _bound(v) * ref.sigmoid(v))
+    assert np.all(np.abs(host(drop) - ref.sigmoid(-v)) <= _bound(v) * ref.sigmoid(-v))
+
+
+def test_silu_value_by_value():
+    p = torch.linspace(-80, 80, 40001).cuda()[:, None]
+    y = ssd.linear_fwd(p, torch.ones((1, 1), device="cuda"), activation="silu")
+    v = host(p)
+    assert np.all(np.abs(host(y) - ref.silu(v)) <= _bound(v, 1) * np.abs(ref.silu(v)))
+    z, h = p.T.contiguous(), torch.ones((1, 40001), device="cuda")
+    big = torch.full_like(z, 80.0)                     # f = 1: the state stays 1
+    y = ssd.gated_state_update(h, torch.zeros_like(z), big, z)
+    assert np.all(np.abs(host(y) - ref.silu(v.T)) <= _bound(v.T, 1) * np.abs(ref.silu(v.T)))
