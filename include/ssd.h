@@ -527,6 +527,32 @@ ssd_status ssd_linear_bwd(const void *dy, const void *x, const void *w, const vo
 size_t ssd_linear_bwd_workspace_bytes(ssd_dtype dtype, ssd_activation activation,
                                       long long tokens, int features, int inner);
 
+/* The kernel that a product takes on the CURRENT device, whose SM count the choice
+ * depends on, when its operands are contiguous and 16-byte aligned. */
+typedef enum {
+    SSD_PRODUCT_FORWARD = 0,        /* ssd_linear_fwd */
+    SSD_PRODUCT_DX = 1,             /* ssd_linear_bwd, dx alone */
+    SSD_PRODUCT_DW = 2,             /* dw alone */
+    SSD_PRODUCT_GRADIENTS = 3       /* both */
+} ssd_product;
+typedef enum {
+    SSD_PATH_FP32 = 0,              /* fp32 multiply-adds, 64 x 64 tiles */
+    SSD_PATH_FP32_FEW = 1,          /* the same for at most 4 tokens */
+    SSD_PATH_FEW = 2,               /* warp products, at most 16 tokens */
+    SSD_PATH_FEW_SPLIT = 3,         /* tcgen05 with the tokens as columns, k split over a cluster */
+    SSD_PATH_WHOLE = 4,             /* tcgen05, 128 x 128 tiles */
+    SSD_PATH_PAIRS = 5,             /* 256 x 256 tiles of CTA pairs */
+    SSD_PATH_SPLIT = 6,             /* 128 x 128 tiles, k split over a cluster */
+    SSD_PATH_SPLIT_PAIRS = 7,       /* 256 x 256 tiles, k split over pairs */
+    SSD_PATH_PAIRS_AND_SPLIT = 8,   /* whole rounds of pairs' tiles, those left over split */
+    SSD_PATH_TOGETHER = 9,          /* both gradients in one launch of pairs */
+    SSD_PATH_APART = 10             /* the gradients one after the other, each on its own path */
+} ssd_path;
+/* An ssd_path (for launch accounting and tests); -1 for invalid sizes or enums,
+ * gradients of 8-bit inputs, or without a device. */
+int ssd_linear_path(ssd_product product, ssd_dtype in_dtype, long long tokens, int features,
+                    int inner);
+
 /* Gated linear recurrence, elementwise over `width` channels:
  *     f_t = sigmoid(g_t)
  *     h_t = f_t h_{t-1} + (1 - f_t) x_t

@@ -64,6 +64,7 @@ from .layer_ops import (  # noqa: F401
     linear_bwd,
     linear_bwd_workspace_bytes,
     linear_fwd,
+    linear_path,
     rmsnorm_bwd,
     rmsnorm_bwd_workspace_bytes,
     rmsnorm_fwd,

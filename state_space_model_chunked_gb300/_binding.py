@@ -39,6 +39,7 @@ EXPORTED_SYMBOLS = (
     "ssd_linear_fwd",
     "ssd_linear_bwd",
     "ssd_linear_bwd_workspace_bytes",
+    "ssd_linear_path",
     "ssd_gated_scan_fwd",
     "ssd_gated_scan_bwd",
     "ssd_gated_scan_workspace_bytes",
@@ -149,6 +150,7 @@ def load():
             "ssd_linear_bwd": [_vp] * 4 + [_int, _int, ll, _int, _int, ll, ll] + [_vp] * 4 +
                               [_sz, _vp],
             "ssd_linear_bwd_workspace_bytes": [_int, _int, ll, _int, _int],
+            "ssd_linear_path": [_int, _int, ll, _int, _int],
             "ssd_gated_scan_fwd": [_vp] * 3 + [_int] * 3 + [_vp, _vp, _int, ll, ll, ll, _vp, _vp,
                                                             ll, _vp, _vp, _vp, _sz, _vp],
             "ssd_gated_scan_bwd": [_vp] * 4 + [_int] * 3 + [_vp, _vp, _int, ll, ll, ll, ll, _vp,

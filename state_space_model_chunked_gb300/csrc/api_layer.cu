@@ -281,6 +281,35 @@ ssd_status ssd_linear_bwd(const void *dy, const void *x, const void *w, const vo
     return SSD_OK;
 }
 
+int ssd_linear_path(ssd_product product, ssd_dtype in_dtype, long long tokens, int features,
+                    int inner) {
+    if (check_linear(in_dtype, tokens, features, inner) != SSD_OK || tokens == 0 ||
+        product < SSD_PRODUCT_FORWARD || product > SSD_PRODUCT_GRADIENTS)
+        return -1;
+    if (product != SSD_PRODUCT_FORWARD && (!float_type(in_dtype) || inner >= (1 << 22))) return -1;
+    const int sms = ssd_sm_count();
+    if (sms <= 0) return -1;
+    // operands as the calls have them, at an address that only its alignment is read of
+    const void *at = reinterpret_cast<const void *>((uintptr_t)4096);
+    const SsdElt t = elt(in_dtype);
+    SsdProduct y{}, dx{}, dw{};
+    y.a = y.b = dx.a = dx.b = dw.a = dw.b = at;
+    y.in = dx.in = dw.in = t;
+    y.m = tokens, y.n = features, y.k = inner;
+    y.a_row = y.b_row = inner, y.a_col = y.b_col = 1;
+    dx.m = tokens, dx.n = inner, dx.k = features;
+    dx.a_row = features, dx.a_col = 1, dx.b_row = 1, dx.b_col = inner;
+    dw.m = features, dw.n = inner, dw.k = tokens;
+    dw.a_row = 1, dw.a_col = features, dw.b_row = 1, dw.b_col = inner;
+    if (product == SSD_PRODUCT_GRADIENTS)
+        return on_tensor_cores(dx) && on_tensor_cores(dw) ? ssd_product_two_path(dx, dw, sms)
+                                                          : SSD_PATH_APART;
+    const SsdProduct &p = product == SSD_PRODUCT_FORWARD ? y : product == SSD_PRODUCT_DX ? dx : dw;
+    if (ssd_product_few_handles(p)) return SSD_PATH_FEW;
+    if (ssd_product_gemv_handles(p)) return SSD_PATH_FP32_FEW;
+    return ssd_product_tc_handles(p) ? ssd_product_tc_path(p, sms) : SSD_PATH_FP32;
+}
+
 size_t ssd_gated_scan_workspace_bytes(ssd_dtype dtype, long long tokens, int width) {
     if (!float_type(dtype) || tokens < 0 || tokens >= (1ll << 31) - 2048 || width <= 0 ||
         !gated_handled(tokens, width))

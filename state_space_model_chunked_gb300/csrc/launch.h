@@ -228,6 +228,10 @@ cudaError_t ssd_launch_product_gemv(const SsdProduct &p, cudaStream_t stream);
 bool ssd_product_tc_handles(const SsdProduct &p);
 cudaError_t ssd_launch_product_tc(const SsdProduct &p, int sms, unsigned *err,
                                   cudaStream_t stream);
+// Which way it takes (the header's ssd_path): of ssd_product_tc_handles products, one
+// alone and a gradient's two.
+int ssd_product_tc_path(const SsdProduct &p, int sms);
+int ssd_product_two_path(const SsdProduct &dx, const SsdProduct &dw, int sms);
 // A gradient's two products on the tensor cores: `dx` of a K-major A and a B with its
 // rows contiguous, `dw` with both operands' rows contiguous.
 cudaError_t ssd_launch_product_two(const SsdProduct &dx, const SsdProduct &dw, int sms,

@@ -29,6 +29,7 @@
 #include <algorithm>
 #include <limits>
 
+#include "../../include/ssd.h"
 #include "act.cuh"
 #include "answers.h"
 #include "launch.h"
@@ -1012,7 +1013,13 @@ cudaError_t few_tokens(const SsdProduct &p, int sms, unsigned *err, cudaStream_t
 // 1952: 147 against 164 us; at 16376 x 2048 x 1024, where it does not pay, 103
 // against 98).
 constexpr long long kBlockCost = 4, kPairEpilogue = 40, kLaunchCost = 100;
-enum class Way { whole, pairs, split, split_pairs, pairs_and_split };
+enum class Way {
+    whole = SSD_PATH_WHOLE,
+    pairs = SSD_PATH_PAIRS,
+    split = SSD_PATH_SPLIT,
+    split_pairs = SSD_PATH_SPLIT_PAIRS,
+    pairs_and_split = SSD_PATH_PAIRS_AND_SPLIT
+};
 struct Choice {
     Way way;
     long long cost;
@@ -1042,7 +1049,7 @@ Choice choose(const SsdProduct &p, bool fp8, int sms) {
                             rest == never ? never
                                           : whole(full, pairs, kPairEpilogue) + rest + kLaunchCost};
     const int best = (int)(std::min_element(t, t + 5) - t);
-    return {(Way)best, t[best], (int)full};
+    return {(Way)((int)Way::whole + best), t[best], (int)full};
 }
 
 template <bool kAmn, bool kBmn, bool kFp8>
@@ -1099,12 +1106,21 @@ bool ssd_product_tc_handles(const SsdProduct &p) {
     return tiles < (1ll << 27) && as < (1ll << 36) && bs < (1ll << 36) && p.k < (1ll << 31);
 }
 
+// At most 64 tokens (of a forward product) are a tile's columns.
+static bool tokens_as_columns(const SsdProduct &p) {
+    return p.m <= 64 && !(p.b_row == 1 && p.b_col != 1);
+}
+
+int ssd_product_tc_path(const SsdProduct &p, int sms) {
+    return tokens_as_columns(p) ? SSD_PATH_FEW_SPLIT : (int)choose(p, p.in == SSD_ELT_E4M3, sms).way;
+}
+
 cudaError_t ssd_launch_product_tc(const SsdProduct &p, int sms, unsigned *err,
                                   cudaStream_t stream) {
     const bool amn = p.a_row == 1 && p.a_col != 1, bmn = p.b_row == 1 && p.b_col != 1;
     if (amn) return many<true, true, false>(p, sms, err, stream);
     if (bmn) return many<false, true, false>(p, sms, err, stream);
-    const bool few = p.m <= 64;
+    const bool few = tokens_as_columns(p);
     if (p.in == SSD_ELT_E4M3)
         return few ? few_tokens<true>(p, sms, err, stream)
                    : many<false, false, true>(p, sms, err, stream);
@@ -1112,7 +1128,37 @@ cudaError_t ssd_launch_product_tc(const SsdProduct &p, int sms, unsigned *err,
                : many<false, false, false>(p, sms, err, stream);
 }
 
-// The gradients dx and dw.  In one launch, if that is cheaper than a launch each, the
+// The gradients dx and dw: how one launch would deal them, and whether it is taken.
+struct Two {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    bool dw_first, together;
+    long long pairs;
+    Deal deal;
+};
+static cudaError_t plan_two(const SsdProduct &dx, const SsdProduct &dw, int sms,
+                            cudaStream_t stream, Two *t) {
+    const auto kernel = product_pair_kernel<false, true, false, false, true>;
+    const cudaError_t e = pair_config(kernel, &t->cfg, t->attr, stream);
+    if (e != cudaSuccess) return e;
+    t->dw_first = dw.k > dx.k;
+    const SsdProduct &one = t->dw_first ? dw : dx, &two = t->dw_first ? dx : dw;
+    const long long tiles = tiles_of(one, 256, 256) + tiles_of(two, 256, 256);
+    t->pairs = std::min<long long>(tiles, std::max(1, clusters_at_once(kernel, t->cfg, 2, sms)));
+    t->deal = deal(one, two, t->pairs);
+    const long long apart =
+        choose(dx, false, sms).cost + choose(dw, false, sms).cost + kLaunchCost;
+    t->together = apart >= t->deal.cost + t->deal.cost / 10;
+    return cudaSuccess;
+}
+
+int ssd_product_two_path(const SsdProduct &dx, const SsdProduct &dw, int sms) {
+    Two t;
+    if (plan_two(dx, dw, sms, nullptr, &t) != cudaSuccess) return -1;
+    return t.together ? SSD_PATH_TOGETHER : SSD_PATH_APART;
+}
+
+// In one launch, if that is cheaper than a launch each, the
 // product of the longer k first: pairs that have no tile of its last round begin with
 // the other's.  Tiles of two products at a time share less of what they read, about a
 // tenth of the time.  us of both in one launch and in two: tokens x features x inner
@@ -1120,29 +1166,20 @@ cudaError_t ssd_launch_product_tc(const SsdProduct &p, int sms, unsigned *err,
 // 11.7 and 13.5; where it is not taken, 8000 x 10240 x 2560, 538 and 512.
 cudaError_t ssd_launch_product_two(const SsdProduct &dx, const SsdProduct &dw, int sms,
                                    unsigned *err, cudaStream_t stream) {
-    const auto kernel = product_pair_kernel<false, true, false, false, true>;
-    cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute attr[2];
-    const cudaError_t e = pair_config(kernel, &cfg, attr, stream);
+    Two t;
+    const cudaError_t e = plan_two(dx, dw, sms, stream, &t);
     if (e != cudaSuccess) return e;
-    const bool dw_first = dw.k > dx.k;
-    const SsdProduct &one = dw_first ? dw : dx, &two = dw_first ? dx : dw;
-    const long long tiles = tiles_of(one, 256, 256) + tiles_of(two, 256, 256);
-    const long long pairs = std::min<long long>(tiles, std::max(1, clusters_at_once(kernel, cfg, 2, sms)));
-    const Deal d = deal(one, two, pairs);
-    const long long apart =
-        choose(dx, false, sms).cost + choose(dw, false, sms).cost + kLaunchCost;
-    if (apart < d.cost + d.cost / 10) {
+    if (!t.together) {
         const cudaError_t first = many<false, true, false>(dx, sms, err, stream);
         return first != cudaSuccess ? first : many<true, true, false>(dw, sms, err, stream);
     }
     Jobs<true> jobs{};
-    jobs.late = d.late;
-    jobs.extra = d.extra;
-    jobs.amn = dw_first ? 0 : 1;
-    if (!pair_job(&jobs.job[0], one, dw_first, true, false, 0, -1, err) ||
-        !pair_job(&jobs.job[1], two, !dw_first, true, false, 0, -1, err))
+    jobs.late = t.deal.late;
+    jobs.extra = t.deal.extra;
+    jobs.amn = t.dw_first ? 0 : 1;
+    if (!pair_job(&jobs.job[0], t.dw_first ? dw : dx, t.dw_first, true, false, 0, -1, err) ||
+        !pair_job(&jobs.job[1], t.dw_first ? dx : dw, !t.dw_first, true, false, 0, -1, err))
         return cudaErrorInvalidValue;
-    cfg.gridDim = dim3((unsigned)(2 * pairs));
-    return cudaLaunchKernelEx(&cfg, kernel, jobs);
+    t.cfg.gridDim = dim3((unsigned)(2 * t.pairs));
+    return cudaLaunchKernelEx(&t.cfg, product_pair_kernel<false, true, false, false, true>, jobs);
 }

@@ -289,6 +289,25 @@ def linear_bwd_workspace_bytes(dtype, tokens, features, inner, activation=None, 
                  _activation(activation), tokens, features, inner)
 
 
+PRODUCTS = {"forward": 0, "dx": 1, "dw": 2, "gradients": 3}
+PATHS = ("fp32", "fp32_few", "few", "few_split", "whole", "pairs", "split", "split_pairs",
+         "pairs_and_split", "together", "apart")
+
+
+def linear_path(dtype, tokens, features, inner, product="forward", device=None):
+    """The kernel (one of PATHS, see ssd_path in include/ssd.h) that linear_fwd takes for
+    these sizes on the device, or linear_bwd for its product "dx", "dw" or both
+    ("gradients"), when the operands are contiguous and aligned."""
+    if product not in PRODUCTS:
+        raise ValueError(f"product must be one of {', '.join(PRODUCTS)}, got {product!r}")
+    fn, code, index = load().ssd_linear_path, _code(dtype, "dtype"), _index(device)
+    with torch.cuda.device(index):
+        path = fn(PRODUCTS[product], code, tokens, features, inner)
+    if path < 0:
+        raise SsdError(fn.__name__, 1, "invalid sizes")
+    return PATHS[path]
+
+
 def linear_fwd(x, w, bias=None, residual=None, *, activation=None, x_scale=None, w_scale=None,
                out_dtype=None, y=None, preact=None, return_preact=False):
     """y = act(x w^T * x_scale[:, None] * w_scale + bias) + residual.
