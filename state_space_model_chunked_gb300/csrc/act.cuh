@@ -64,7 +64,7 @@ __device__ __forceinline__ void ssd_elt_store(void *p, long long i, SsdElt t, fl
     else static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
 }
 __device__ __forceinline__ void ssd_finish(const SsdProduct &p, long long m, long long n, float v) {
-    if (p.a_scale) v *= p.a_scale[m] * p.b_scale[n];
+    if (p.a_scale) v = v * p.a_scale[m] * p.b_scale[n];     // two small scales' product may underflow
     if (p.bias) v += p.bias[n];
     if (p.preact) ssd_elt_store(p.preact, m * p.n + n, p.preact_type, v);
     v = ssd_act(v, p.act);

@@ -203,7 +203,7 @@ struct RowPart {
         if (left == 0 || m >= p.m) return;
         if (p.a_scale) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] *= row_scale * scale(i);
+            for (int i = 0; i < N; ++i) v[i] = v[i] * row_scale * scale(i);
         }
         if (p.bias) {
 #pragma unroll
