@@ -330,6 +330,7 @@ PyObject *gated_scan_fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const Matrix g = matrix(args[1], dev, ok), z = matrix(args[2], dev, ok);
     const at::Tensor *init = tensor(args[3], dev, ok);
     const int keep = PyObject_IsTrue(args[6]), c = code(x.t->scalar_type());
+    if (keep < 0) return nullptr;       // no truth value: the exception is set
     Sequences q;
     if (!ok || !g.t || !like(g, *x.t) || !like(z, *x.t) || c < 0 ||
         !sequences(*x.t, args[4], args[5], q))
