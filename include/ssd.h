@@ -430,8 +430,9 @@ ssd_status ssd_chain_states(const float *contrib, const float *log_decay, const 
  *                 stream_dtype is x_dtype or SSD_F32.
  *   weight        float [width].  eps >= 0.
  *   y             out_dtype [rows][width]: SSD_F32, SSD_BF16, or SSD_FP8_E4M3
- *                 with one scale a row: scale = max_j |y_j| / 448 (1 for a row
- *                 of zeros), y holds y_j / scale rounded to nearest even.
+ *                 with one scale a row: scale = max_j |y_j| / 448 (1 where that
+ *                 is 0 in fp32), y holds y_j / scale, computed in fp32 as
+ *                 y_j (1 / scale), rounded to nearest even.
  *   residual_out  stream_dtype [rows][width]: s.  Required with a residual
  *                 (may be the residual itself), ignored without.
  *   rstd          float [rows].  scale: float [rows], required for 8-bit

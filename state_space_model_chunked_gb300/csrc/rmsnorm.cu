@@ -2,7 +2,7 @@
 // and its row scales) and backward.
 //
 //   s = x + r,  rstd = (mean_j s_j^2 + eps)^(-1/2),  y_j = s_j rstd w_j
-//   8 bits: scale = max_j |y_j| / 448 (1 for a row of zeros), q = e4m3(y / scale)
+//   8 bits: scale = max_j |y_j| / 448 (1 where that is 0), q = e4m3(y / scale)
 //   backward, with e_j = dy_j w_j:
 //     ds_j = ds_out_j + rstd (e_j - s_j rstd^2 mean_i(e_i s_i))
 //     dw_j = sum over rows of dy_j s_j rstd
@@ -57,7 +57,8 @@ struct RowScale {
     float scale, inv;
     bool tiny;
     __device__ __forceinline__ explicit RowScale(float amax) {
-        scale = amax == 0.f ? 1.f : amax / kE4m3Max;
+        scale = amax / kE4m3Max;
+        if (scale == 0.f) scale = 1.f;      // zeros, or values below 3e-43, which are 0 too
         tiny = scale < 1e-30f;
         inv = 1.f / scale;
     }
