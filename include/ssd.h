@@ -580,7 +580,10 @@ int ssd_linear_path(ssd_product product, ssd_dtype in_dtype, long long tokens, i
  * SSD_ERR_UNSUPPORTED for other types, width >= 2^21, 2^31 - 2048 tokens or
  * more, or tokens * width of about 2^42 or more.  A call of more than 64 tokens
  * joins its parts on the device by waits that are bounded in time; one that
- * runs out is reported by ssd_last_device_error(). */
+ * runs out is reported by ssd_last_device_error().  In which grouping the parts'
+ * fp32 states are joined follows their progress, so two equal calls of more than 64
+ * tokens may differ in the last fp32 bits of their results (and so in single bf16
+ * values); the same holds for ssd_gated_scan_bwd. */
 ssd_status ssd_gated_scan_fwd(const void *x, const void *g, const void *z, ssd_dtype dtype,
                               int nseq, int length, const int *cu_seqlens_host,
                               const int *cu_seqlens_dev, int width, long long x_stride,

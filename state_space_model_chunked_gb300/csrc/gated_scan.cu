@@ -11,12 +11,15 @@
 // f and 1 - f = sigmoid(-g) are each known to (1.25 |g| + 8) 2^-24 of themselves;
 // states and gradients are carried in fp32.
 //   Measured (time on the GPU): forward 65536 tokens of 5120 channels in bf16 with z
-// 540 us (0.73 of the measured copy bandwidth), 47 sequences of 65518 tokens in all,
+// 537 us (0.74 of the measured copy bandwidth), 47 sequences of 65518 tokens in all,
 // 1536 channels, fp32 217 us (0.82); backward 8 x 2047 tokens of 2048 channels 131 us
-// (0.53); a token of 256 rows of 5120 2.5 us, its arrays in L2.  What bounds the two
-// directions is the instructions, about 40 and 78 a channel and token, and the wait
-// for the tile in front, which the walk's rule below keeps short: without the walk
-// (wrong results) 521, 177 and 123 us.
+// (0.53); a token of 256 rows of 5120 2.5 us, its arrays in L2.  Neither bytes nor
+// instructions alone bound the two directions: a channel and token takes 41 and 77
+// instructions, which fill 63 and 54 % of the issue slots, and 128 registers a thread
+// leave an SM 16 warps, which most often wait at the CTA's barriers for the slowest
+// warp's loads or for the tile in front.  That wait the walk's rule below keeps short:
+// without the walk (wrong results) 521, 177 and 123 us.  The forward kernel's main form
+// spills 48 bytes a thread under that bound (fp32 80).
 #include "launch.h"
 #include "ptx.cuh"
 #include "vec.cuh"

@@ -12,7 +12,9 @@
 // added in order.
 //   Measured (time on the GPU): one token of 2560 to 15360 features in bf16 14.4 us
 // (5.45 TB/s, 0.80 of the measured copy bandwidth), sixteen tokens of 5120 to 2560 in
-// 8 bits 5.2 us, of which the weights' transfer is 2.  The tcgen05 tiles of
+// 8 bits 5.2 us, of which the weights' transfer is 2 (with at most two CTAs an SM a
+// warp loads one step at a time: three trips to memory one after another, in bf16
+// five, which take 9.4 us, and 7.0 for one token, against 3.9 for the transfer).  The tcgen05 tiles of
 // linear_tc.cu, with their prologue, cluster barriers and tensor-memory round trip,
 // took 18.2 and 10.9 us.
 #include <cuda_fp16.h>
@@ -68,8 +70,9 @@ struct Pairs {
     }
 };
 
-// kNT: groups of 8 tokens.  kAhead: steps of two 16-byte words a row under way in
-// a lane.
+// kNT: groups of 8 tokens.  kAhead: steps of two 16-byte words a row that a turn of
+// the loop loads before it uses them; the compiler keeps fewer under way (for one
+// group of tokens and five steps 54 registers, where the words alone would take 80).
 template <bool kFp8, int kNT, int kWarps, int kAhead>
 __global__ void __launch_bounds__(32 * kWarps) product_few_kernel(const SsdProduct p) {
     constexpr int kSize = kFp8 ? 1 : 2, kWord = 16 / kSize;

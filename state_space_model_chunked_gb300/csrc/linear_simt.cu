@@ -4,8 +4,12 @@
 //
 //   out[m][n] = act(sum_k A(m,k) B(n,k) a_scale[m] b_scale[n] + bias[n]) + residual[m][n]
 //
-// Bound by the fp32 pipe: a CTA's 64 x 64 tile takes 16 values of k a step
-// through shared memory, each of 256 threads a 4 x 4 block of sums.
+// A CTA's 64 x 64 tile takes 16 values of k a step through shared memory, each of
+// 256 threads a 4 x 4 block of sums.  Simple rather than fast: one buffer and two
+// barriers a step, scalar loads, no split of k.  Measured (time on the GPU): fp32
+// 2048 x 2048 -> 2048 815 us (21 TFLOP/s), both its gradients 1638; 16 x 5120 -> 2560
+// 570 us and 64 tokens 703, where 40 CTAs walk all of k; bf16 with unaligned rows 1000 x
+// 1001 -> 1024 175 us (12 TFLOP/s), gradients 354.
 #include <cuda_fp8.h>
 
 #include <algorithm>

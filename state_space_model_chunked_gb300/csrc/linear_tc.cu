@@ -20,10 +20,12 @@
 //   Measured (time on the GPU): 65536 x 5120 -> 2560 in bf16 with bias, silu and
 // residual 1065 to 1090 us (1.6 PFLOP/s, under the power limit; 0.94 of a library
 // product's sustained rate), both gradients of 16376 x 1024 -> 2048 86 us (1.6 PFLOP/s),
-// 4001 x 768 -> 1536 in 8 bits 14.3 us, 512 x 2560 -> 2560 in bf16 12.1 us.  A product of
+// 4001 x 768 -> 1536 in 8 bits 14.3 us, 512 x 2560 -> 2560 in bf16 12.9 us.  A product of
 // few tiles has a fixed cost: 1 us before the first load, which the kernel in front
-// in the stream hides (13.3 us for the last one without that), 1.2 us for its data,
-// 0.6 us at the end, and with k split 3 to 4 us for the exchange.
+// in the stream hides, 1.2 us for its data, 0.6 us at the end, and with k split about 4 us
+// for the exchange.  Where tiles take few k blocks the epilogue bounds them, with and
+// without an activation: 21375 x 688 -> 9632 263 us with silu and 275 without (a library
+// product's burst rate would make it 147), 4096 x 688 -> 4096 26 us.
 #include <cuda.h>
 
 #include <algorithm>
@@ -236,7 +238,8 @@ struct RowPart {
 // One copy of the code for all columns: unrolled, the epilogue outgrows the
 // instruction cache (1320 against 1120 us for 65536 x 5120 -> 2560).  Laying the
 // rows out in shared memory for coalesced stores took longer, not shorter (1000
-// against 977 us): the products keep shared memory busy.
+// against 977 us for the same product, whose 80 k blocks hide the epilogue; not timed
+// where k is short).
 template <typename TO, int kBN, typename F, typename G>
 __device__ __forceinline__ bool drain(const Args &a, const Columns *cols, uint32_t acc, int half,
                                       long long m, long long n0, F &&ready, G &&read) {
@@ -1005,8 +1008,13 @@ cudaError_t few_tokens(const SsdProduct &p, int sms, unsigned *err, cudaStream_t
 // Tiles of 128 x 128 or pairs' 256 x 256, whole or with k split, by the time each
 // would take, in units of 64 ns.  A k block takes as long as its operands take into
 // the SM, 32 KB for either: 4 units; the epilogue of a tile, which the next tile's
-// products hide if they last as long, about 20 and 40; a split's barriers and
-// exchange of sums 50.  Whole tiles run in rounds of as many
+// products hide if they last as long, counts for 20 and 40; a split's barriers and
+// exchange of sums 50.  These order the ways rather than tell their times: a pair
+// tile's epilogue takes two to three times the 2.6 us of its 40 units, so products of
+// few k blocks last about twice what is estimated, in either shape of tile (whole and
+// pairs: 21375 x 688 -> 9632 359 and 263 us, 16376 x 1024 -> 2048 with gelu 84 and 54,
+// 16376 x 512 -> 4096 118 and 112; 4001 x 768 -> 1536 in 8 bits 14.3 and 15.3; the better
+// one was chosen each time).  Whole tiles run in rounds of as many
 // as the SMs take; a split has as many ranks as 7/8 of the SMs allow (clusters do
 // not fill all of them).  Or whole rounds of the pairs' tiles, and the few left over
 // split, in a launch of their own for another 100 units (gradients at 2635 x 7664 x

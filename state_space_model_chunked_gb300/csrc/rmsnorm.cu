@@ -13,10 +13,16 @@
 // row's loads under way, and keeps its columns' weights in registers; the
 // row's sum and its largest |s w| come from one pass and one barrier:
 // max |y| = rstd max |s w|.
-//   Measured (time on the GPU): 65536 rows of 2560, bf16 with an fp32 residual in
-// place, to 8 bits 189 us (0.91 of the measured copy bandwidth); gradients of 16376
+//   Measured (time on the GPU): 65536 rows of 2560, bf16 with a bf16 residual,
+// to 8 bits 189 us (0.91 of the measured copy bandwidth); gradients of 16376
 // rows of 1024 46 us (0.86); 16 rows 1.6 us, all of it the launch.  Without the next
 // row's loads under way the first took 377 us and the second 89.
+//   Widths that are no multiple of 8, and unaligned rows, move value by value: 16376
+// rows of 1023 with an fp32 residual 47 us forward and 143 backward, of 2047 83 and 286
+// (0.48 and 0.14 of the bandwidth), 65536 rows of 2559 to 8 bits 696.  Rows beyond a
+// CTA's registers (above 8192 values, forward with vectors 16384) are read again for
+// each pass over them: 4096 rows of 33000 417 us forward (0.38) and 672 backward (0.24),
+// gradients at 16384 346 us (0.23).
 #include "launch.h"
 #include "ptx.cuh"
 #include "vec.cuh"

@@ -424,7 +424,8 @@ def gated_scan_fwd(x, g, z=None, init_state=None, *, cu_seqlens=None, cu_seqlens
     scan_fwd_varlen.  init_state [nseq, width] f32 or None.  Returns
     (y, final_state [nseq, width] f32 or None), and the states
     [ceil(tokens / 64), width] f32 that gated_scan_bwd needs with
-    return_checkpoints."""
+    return_checkpoints.  Equal calls of more than 64 tokens may differ in their
+    last fp32 bits: the order in which parts are joined follows their progress."""
     if (y is None and final_state is None and return_final and checkpoints is None
             and workspace is None):
         got = (_marshal_module or _marshal()).gated_scan_fwd(x, g, z, init_state, cu_seqlens,
