@@ -623,6 +623,139 @@ ssd_status ssd_gated_state_update(float *state, const void *x, const void *g, co
                                   long long g_stride, long long z_stride, void *y,
                                   cudaStream_t stream);
 
+/* Layer norm of the residual stream s = x + residual:
+ *     mean = mean_j s_j,   rstd = (mean_j (s_j - mean)^2 + eps)^(-1/2)
+ *     y_j = (s_j - mean) rstd weight_j + bias_j
+ * computed from the unrounded s.  x, residual, weight, y, residual_out, rstd, scale, types
+ * and strides as in ssd_rmsnorm_fwd (an 8-bit row's scale is that of its y); bias float
+ * [width] or NULL (zeros); mean float [rows].  A row that holds a NaN or an infinity gives
+ * NaN.  Errors as ssd_rmsnorm_fwd. */
+ssd_status ssd_layernorm_fwd(const void *x, const void *residual, const float *weight,
+                             const float *bias, float eps, ssd_dtype x_dtype,
+                             ssd_dtype stream_dtype, ssd_dtype out_dtype, long long rows, int width,
+                             long long x_stride, long long residual_stride, void *y,
+                             void *residual_out, float *mean, float *rstd, float *scale,
+                             cudaStream_t stream);
+
+/* Gradients of ssd_layernorm_fwd.  With v_j = (s_j - mean) rstd and e_j = dy_j weight_j:
+ *     ds_j = dresidual_j + rstd (e_j - mean_i(e_i) - v_j mean_i(e_i v_i))
+ *     dweight_j = sum over rows of dy_j v_j,   dbias_j = sum over rows of dy_j
+ * Arguments as in ssd_rmsnorm_bwd; mean and rstd of the forward call; dbias float [width]
+ * or NULL: not wanted; workspace ssd_layernorm_bwd_workspace_bytes() bytes, 16-byte
+ * aligned.  The sums' order is fixed for given sizes.  rows == 0 writes zeros to dweight
+ * and dbias. */
+ssd_status ssd_layernorm_bwd(const void *dy, const void *s, const float *weight, const float *mean,
+                             const float *rstd, const void *dresidual, ssd_dtype dtype,
+                             ssd_dtype stream_dtype, long long rows, int width, long long dy_stride,
+                             long long s_stride, long long dresidual_stride, void *dx, void *ds,
+                             float *dweight, float *dbias, void *workspace, size_t workspace_bytes,
+                             cudaStream_t stream);
+/* Workspace of ssd_layernorm_bwd on the current device; (size_t)-1 for invalid sizes. */
+size_t ssd_layernorm_bwd_workspace_bytes(long long rows, int width);
+
+/* Embedding: rows of a table by tokens,
+ *     y[t][j] = table[tokens[t]][j] scale
+ *   tokens   SSD_I32 or SSD_I64 [count].  A token below 0 or not below vocab stands for
+ *            padding: its row of y is zeros, and it has no part in the gradient.
+ *   table    table_dtype (SSD_F32 or SSD_BF16) [vocab][width], contiguous.
+ *   y        out_dtype (SSD_F32 or SSD_BF16) [count][width]; each value is rounded once.
+ * count == 0 enqueues nothing.  SSD_ERR_INVALID_ARG for null or misaligned pointers, sizes
+ * out of range, a scale that is not finite; SSD_ERR_UNSUPPORTED for other types, 2^31 - 2048
+ * tokens, 2^30 rows of the table or 2^24 columns or more. */
+typedef enum { SSD_I32 = 0, SSD_I64 = 1 } ssd_index;
+ssd_status ssd_embedding_fwd(const void *tokens, ssd_index token_type, const void *table,
+                             ssd_dtype table_dtype, ssd_dtype out_dtype, long long count, int vocab,
+                             int width, float scale, void *y, cudaStream_t stream);
+
+/* The table's gradient, dense:
+ *     dtable[v][j] = scale * sum over the t with tokens[t] = v of dy[t][j]
+ *   dy       dtype (SSD_F32 or SSD_BF16) [count][width], dy_stride.
+ *   dtable   out_dtype (SSD_F32 or SSD_BF16) [vocab][width]: every row is written, rows
+ *            without a token as zeros.  Sums are fp32 and rounded once.
+ *   workspace  ssd_embedding_bwd_workspace_bytes() bytes, 256-byte aligned.
+ * The tokens are sorted on the device and each row's sum runs in an order fixed for given
+ * tokens, so equal calls give equal bits.  count == 0 writes zeros.  Errors as
+ * ssd_embedding_fwd, and SSD_ERR_WORKSPACE. */
+ssd_status ssd_embedding_bwd(const void *dy, const void *tokens, ssd_index token_type,
+                             ssd_dtype dtype, ssd_dtype out_dtype, long long count, int vocab,
+                             int width, long long dy_stride, float scale, void *dtable,
+                             void *workspace, size_t workspace_bytes, cudaStream_t stream);
+/* (size_t)-1 for invalid sizes. */
+size_t ssd_embedding_bwd_workspace_bytes(long long count, int vocab, int width);
+
+/* Gated delta rule: a linear recurrence whose state is corrected towards each token's value,
+ * for every head with its state S [headdim][dstate]:
+ *     S' = exp(g_t) S_{t-1}
+ *     u_t = beta_t (v_t - S' k_t)
+ *     S_t = S' + u_t k_t^T
+ *     o_t = scale S_t q_t
+ * over nseq sequences laid end to end on one axis of `tokens` tokens (length, or
+ * cu_seqlens_host and cu_seqlens_dev, as in ssd_gated_scan_fwd).
+ *   q, k         dtype (SSD_F32 or SSD_BF16) [tokens][ngroups][dstate]; head h uses group
+ *                h / (nheads / ngroups).  q_stride and k_stride: distance of two tokens.
+ *   v, o         dtype [tokens][nheads][headdim], with v_stride and o_stride.
+ *   g            float [tokens][nheads]: the logarithm of the decay (<= 0 in use; -infinity
+ *                forgets the state, values below -200 count as that).
+ *   beta         float [tokens][nheads]: how much of the value is written (0 to 1 in use,
+ *                with keys of unit length).
+ *   init_state, final_state   float [nseq][nheads][headdim][dstate] or NULL (zeros / not
+ *                wanted).  An empty sequence's final state is its initial one.
+ *   checkpoints  float [tokens / 64 + nseq][nheads][headdim][dstate] or NULL: what
+ *                ssd_delta_scan_bwd needs of the forward call.  The state before a sequence's
+ *                tokens 0, 64, 128, ... lies at first / 64 + s + 0, 1, 2, ... (s: the
+ *                sequence, first: its first token on the axis); other places are not written.
+ * Requirements: dstate <= 256, headdim <= 2^14, nheads <= 2^16 a multiple of ngroups.
+ * SSD_ERR_INVALID_ARG for null or misaligned pointers, sizes <= 0 (length 0 is allowed),
+ * strides below a token's values, bad offsets or a scale that is not finite;
+ * SSD_ERR_UNSUPPORTED for other types and sizes beyond those, or beyond a grid (2^31
+ * runs of 64 tokens by heads by 32 rows). */
+ssd_status ssd_delta_scan_fwd(const void *q, const void *k, const void *v, const float *g,
+                              const float *beta, ssd_dtype dtype, int nseq, int length,
+                              const int *cu_seqlens_host, const int *cu_seqlens_dev, int nheads,
+                              int headdim, int dstate, int ngroups, long long q_stride,
+                              long long k_stride, long long v_stride, float scale,
+                              const float *init_state, void *o, long long o_stride,
+                              float *final_state, float *checkpoints, cudaStream_t stream);
+
+/* Gradients of ssd_delta_scan_fwd.  With L_t the gradient of S_t, which begins with dfinal
+ * behind a sequence's last token:
+ *     L_t += scale do_t q_t^T,   w_t = L_t k_t,   dv_t = beta_t w_t
+ *     L' = L_t - dv_t k_t^T,     L_{t-1} = exp(g_t) L'        (dinit: before the first token)
+ *     dbeta_t = w_t (v_t - S' k_t),   dg_t = <L', S'>
+ *     dq_t = scale S_t^T do_t,   dk_t = L_t^T u_t - S'^T dv_t     (summed over a group's heads)
+ *   dout         dtype [tokens][nheads][headdim], do_stride: the gradient of o.
+ *   q, k, v, g, beta, scale and sequences as given to the forward call; checkpoints: what
+ *                it left.
+ *   dfinal, dinit   float [nseq][nheads][headdim][dstate] or NULL (zeros / not wanted).
+ *   dq, dk, dv   dtype, laid out as q, k and v, with their own token strides.
+ *   dg, dbeta    float [tokens][nheads].
+ *   workspace    ssd_delta_scan_bwd_workspace_bytes() bytes, 256-byte aligned.
+ * Sums are fp32 in an order fixed for given sizes; each result is rounded once. */
+ssd_status ssd_delta_scan_bwd(const void *dout, const void *q, const void *k, const void *v,
+                              const float *g, const float *beta, ssd_dtype dtype, int nseq,
+                              int length, const int *cu_seqlens_host, const int *cu_seqlens_dev,
+                              int nheads, int headdim, int dstate, int ngroups, long long do_stride,
+                              long long q_stride, long long k_stride, long long v_stride, float scale,
+                              const float *checkpoints, const float *dfinal, void *dq,
+                              long long dq_stride, void *dk, long long dk_stride, void *dv,
+                              long long dv_stride, float *dg, float *dbeta, float *dinit,
+                              void *workspace, size_t workspace_bytes, cudaStream_t stream);
+/* (size_t)-1 for invalid sizes. */
+size_t ssd_delta_scan_bwd_workspace_bytes(ssd_dtype dtype, long long tokens, int nseq, int nheads,
+                                          int headdim, int dstate, int ngroups);
+
+/* One token of the delta rule: state [batch][nheads][headdim][dstate] of state_dtype (SSD_F32,
+ * or SSD_BF16 with bf16 inputs, rounded once) gives state_out, which may be the state itself;
+ * q, k [batch][ngroups][dstate], v [batch][nheads][headdim] of dtype with strides of a batch
+ * row; g, beta float [batch][nheads]; o dtype [batch][nheads][headdim].  batch == 0 enqueues
+ * nothing.  Requirements and errors as ssd_delta_scan_fwd. */
+ssd_status ssd_delta_state_update(const void *state, ssd_dtype state_dtype, void *state_out,
+                                  const void *q, const void *k, const void *v, const float *g,
+                                  const float *beta, ssd_dtype dtype, int batch, int nheads,
+                                  int headdim, int dstate, int ngroups, long long q_stride,
+                                  long long k_stride, long long v_stride, float scale, void *o,
+                                  cudaStream_t stream);
+
 /* Human-readable name of a status code (static storage). */
 const char *ssd_status_string(ssd_status s);
 

@@ -14,7 +14,19 @@ cannot load, every call raises.
     y = state_update_multi(state, x, dt, A, B, C, D)    # T tokens [b,T,H,P] in one call
     pipe = HostScanPipeline(); pipe.submit(..., out=(y_host, final_host))  # host tensors
 
+The gated delta rule, a recurrence whose state is corrected towards each value, with its
+gradients, its states in scan_fwd's layout, batched or packed:
+
+    o, final = delta_scan_fwd(q, k, v, g, beta, init_state)
+    dq, dk, dv, dg, dbeta, dinit = delta_scan_bwd(do, q, k, v, g, beta, checkpoints, dfinal)
+    o = delta_state_update(state, q, k, v, g, beta)                    # one token, state in place
+
 The steps of a layer around such a recurrence, each with its gradients:
+
+    y = embedding_fwd(tokens, table, scale=2.0)                        # tokens outside: zeros
+    dtable = embedding_bwd(dy, tokens, vocab, scale=2.0)
+    y, stream, mean, rstd, scale = layernorm_fwd(x, weight, bias, residual)
+    dx, dstream, dweight, dbias = layernorm_bwd(dy, stream, weight, mean, rstd, dstream)
 
     y, stream, rstd, scale = rmsnorm_fwd(x, weight, residual)          # scale: 8-bit outputs
     dx, dstream, dweight = rmsnorm_bwd(dy, stream, weight, rstd, dstream)
@@ -54,13 +66,27 @@ from ._binding import (  # noqa: F401
     range_log_decay,
     chain_states,
 )
+from .delta_ops import (  # noqa: F401
+    DELTA_SCAN_CHECKPOINT,
+    delta_scan_bwd,
+    delta_scan_bwd_workspace_bytes,
+    delta_scan_checkpoints,
+    delta_scan_fwd,
+    delta_state_update,
+)
 from .layer_ops import (  # noqa: F401
     ACTIVATIONS,
     GATED_SCAN_CHECKPOINT,
+    embedding_bwd,
+    embedding_bwd_workspace_bytes,
+    embedding_fwd,
     gated_scan_bwd,
     gated_scan_fwd,
     gated_scan_workspace_bytes,
     gated_state_update,
+    layernorm_bwd,
+    layernorm_bwd_workspace_bytes,
+    layernorm_fwd,
     linear_bwd,
     linear_bwd_workspace_bytes,
     linear_fwd,

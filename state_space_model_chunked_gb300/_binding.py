@@ -44,6 +44,16 @@ EXPORTED_SYMBOLS = (
     "ssd_gated_scan_bwd",
     "ssd_gated_scan_workspace_bytes",
     "ssd_gated_state_update",
+    "ssd_layernorm_fwd",
+    "ssd_layernorm_bwd",
+    "ssd_layernorm_bwd_workspace_bytes",
+    "ssd_embedding_fwd",
+    "ssd_embedding_bwd",
+    "ssd_embedding_bwd_workspace_bytes",
+    "ssd_delta_scan_fwd",
+    "ssd_delta_scan_bwd",
+    "ssd_delta_scan_bwd_workspace_bytes",
+    "ssd_delta_state_update",
 )
 
 ALGO_AUTO, ALGO_SIMT, ALGO_TCGEN05 = 0, 1, 2
@@ -158,6 +168,22 @@ def load():
                                                             _vp, _vp, _sz, _vp],
             "ssd_gated_scan_workspace_bytes": [_int, ll, _int],
             "ssd_gated_state_update": [_vp] * 4 + [_int, ll, _int, ll, ll, ll, _vp, _vp],
+            "ssd_layernorm_fwd": [_vp] * 4 + [f32, _int, _int, _int, ll, _int, ll, ll] + [_vp] * 6,
+            "ssd_layernorm_bwd": [_vp] * 6 + [_int, _int, ll, _int, ll, ll, ll] + [_vp] * 5 +
+                                 [_sz, _vp],
+            "ssd_layernorm_bwd_workspace_bytes": [ll, _int],
+            "ssd_embedding_fwd": [_vp, _int, _vp, _int, _int, ll, _int, _int, f32, _vp, _vp],
+            "ssd_embedding_bwd": [_vp, _vp, _int, _int, _int, ll, _int, _int, ll, f32, _vp, _vp,
+                                  _sz, _vp],
+            "ssd_embedding_bwd_workspace_bytes": [ll, _int, _int],
+            "ssd_delta_scan_fwd": [_vp] * 5 + [_int] * 3 + [_vp, _vp] + [_int] * 4 +
+                                  [ll, ll, ll, f32, _vp, _vp, ll, _vp, _vp, _vp],
+            "ssd_delta_scan_bwd": [_vp] * 6 + [_int] * 3 + [_vp, _vp] + [_int] * 4 +
+                                  [ll, ll, ll, ll, f32, _vp, _vp, _vp, ll, _vp, ll, _vp, ll, _vp,
+                                   _vp, _vp, _vp, _sz, _vp],
+            "ssd_delta_scan_bwd_workspace_bytes": [_int, ll] + [_int] * 5,
+            "ssd_delta_state_update": [_vp, _int] + [_vp] * 6 + [_int] * 6 +
+                                      [ll, ll, ll, f32, _vp, _vp],
         }
         for name, args in layer.items():
             fn = getattr(lib, name)

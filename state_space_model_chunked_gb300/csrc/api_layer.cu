@@ -31,6 +31,14 @@ ssd_status check_workspace(const void *ws, size_t have, size_t need, size_t alig
     return aligned(ws, align) ? SSD_OK : SSD_ERR_INVALID_ARG;
 }
 
+// The longest sequence of a call that check_sequences passed.
+int longest_of(int nseq, int length, const int *host) {
+    if (!host) return length;
+    int most = 0;
+    for (int s = 0; s < nseq; ++s) most = host[s + 1] - host[s] > most ? host[s + 1] - host[s] : most;
+    return most;
+}
+
 bool norm_sizes_ok(long long rows, int width) { return rows >= 0 && width > 0; }
 bool norm_sizes_handled(long long rows, int width) {
     return rows < (1ll << 31) && width < (1 << 24);
@@ -103,6 +111,65 @@ ssd_status gated_input(const void *x, const void *g, const void *z, ssd_dtype dt
     out->x_stride = x_stride;
     out->g_stride = g_stride;
     out->z_stride = z_stride;
+    return SSD_OK;
+}
+
+// Sizes and types of the delta rule.
+ssd_status check_delta(ssd_dtype dtype, int nheads, int headdim, int dstate, int ngroups) {
+    if (!known_type(dtype) || nheads <= 0 || headdim <= 0 || dstate <= 0 || ngroups <= 0 ||
+        nheads % ngroups != 0)
+        return SSD_ERR_INVALID_ARG;
+    if (!float_type(dtype) || dstate > 256 || headdim > (1 << 14) || nheads > (1 << 16))
+        return SSD_ERR_UNSUPPORTED;
+    return SSD_OK;
+}
+bool token_strides_ok(long long q, long long k, long long v, int nheads, int headdim, int dstate,
+                      int ngroups) {
+    const long long keys = (long long)ngroups * dstate;
+    return q >= keys && k >= keys && v >= (long long)nheads * headdim;
+}
+// Sizes the delta rule's grids can number.
+bool delta_handled(long long tokens, int nseq, int nheads, int headdim) {
+    const long long slabs = ((long long)headdim + 31) / 32;
+    return (double)(tokens / kSsdDeltaChunk + nseq) * nheads * slabs < 2147483648.0;
+}
+
+// What the delta rule's two directions share.
+ssd_status delta_input(const void *q, const void *k, const void *v, const float *g,
+                       const float *beta, ssd_dtype dtype, int nseq, int length, const int *host,
+                       const int *dev, int nheads, int headdim, int dstate, int ngroups,
+                       long long q_stride, long long k_stride, long long v_stride, float scale,
+                       SsdDelta *out) {
+    ssd_status st = check_delta(dtype, nheads, headdim, dstate, ngroups);
+    if (st != SSD_OK) return st;
+    st = check_sequences(nseq, length, host, dev, &out->tokens);
+    if (st != SSD_OK) return st;
+    if (!delta_handled(out->tokens, nseq, nheads, headdim)) return SSD_ERR_UNSUPPORTED;
+    const size_t n = size_of(dtype);
+    if (out->tokens > 0 &&
+        (!array(q, n) || !array(k, n) || !array(v, n) || !array(g, 4) || !array(beta, 4)))
+        return SSD_ERR_INVALID_ARG;
+    if (!token_strides_ok(q_stride, k_stride, v_stride, nheads, headdim, dstate, ngroups) ||
+        !isfinite(scale))
+        return SSD_ERR_INVALID_ARG;
+    out->q = q;
+    out->k = k;
+    out->v = v;
+    out->g = g;
+    out->beta = beta;
+    out->bf16 = dtype == SSD_BF16;
+    out->nseq = nseq;
+    out->length = length;
+    out->longest = longest_of(nseq, length, host);
+    out->cu = dev;
+    out->heads = nheads;
+    out->groups = ngroups;
+    out->p = headdim;
+    out->n = dstate;
+    out->q_stride = q_stride;
+    out->k_stride = k_stride;
+    out->v_stride = v_stride;
+    out->scale = scale;
     return SSD_OK;
 }
 
@@ -393,6 +460,227 @@ ssd_status ssd_gated_state_update(float *state, const void *x, const void *g, co
         return SSD_ERR_INVALID_ARG;
     SsdGatedStep a{state, x, g, z, dtype == SSD_BF16, rows, width, x_stride, g_stride, z_stride, y};
     return launched(ssd_launch_gated_step(a, stream));
+}
+
+ssd_status ssd_layernorm_fwd(const void *x, const void *residual, const float *weight,
+                             const float *bias, float eps, ssd_dtype x_dtype,
+                             ssd_dtype stream_dtype, ssd_dtype out_dtype, long long rows, int width,
+                             long long x_stride, long long residual_stride, void *y,
+                             void *residual_out, float *mean, float *rstd, float *scale,
+                             cudaStream_t stream) {
+    if (!known_type(x_dtype) || !known_type(stream_dtype) || !known_type(out_dtype))
+        return SSD_ERR_INVALID_ARG;
+    if (!norm_sizes_ok(rows, width) || !(eps >= 0.f)) return SSD_ERR_INVALID_ARG;
+    if (!float_type(x_dtype) || (stream_dtype != x_dtype && stream_dtype != SSD_F32))
+        return SSD_ERR_UNSUPPORTED;
+    if (!norm_sizes_handled(rows, width)) return SSD_ERR_UNSUPPORTED;
+    if (rows == 0) return SSD_OK;
+    const size_t nx = size_of(x_dtype), ns = size_of(stream_dtype);
+    if (!array(x, nx) || !array(weight, 4) || !maybe(bias, 4) || !array(y, size_of(out_dtype)) ||
+        !array(mean, 4) || !array(rstd, 4))
+        return SSD_ERR_INVALID_ARG;
+    if (residual && (!aligned(residual, ns) || !array(residual_out, ns) || residual_stride < width))
+        return SSD_ERR_INVALID_ARG;
+    if (out_dtype == SSD_FP8_E4M3 && !array(scale, 4)) return SSD_ERR_INVALID_ARG;
+    if (x_stride < width) return SSD_ERR_INVALID_ARG;
+    SsdLayerNormFwd a{x, residual, weight, bias, eps, elt(x_dtype), elt(stream_dtype), elt(out_dtype),
+                      rows, width, x_stride, residual_stride, y, residual ? residual_out : nullptr,
+                      mean, rstd, scale};
+    return launched(ssd_launch_layernorm_fwd(a, ssd_sm_count(), stream));
+}
+
+size_t ssd_layernorm_bwd_workspace_bytes(long long rows, int width) {
+    if (!norm_sizes_ok(rows, width) || !norm_sizes_handled(rows, width)) return kBad;
+    return ssd_layernorm_bwd_workspace(rows, width, ssd_sm_count());
+}
+
+ssd_status ssd_layernorm_bwd(const void *dy, const void *s, const float *weight, const float *mean,
+                             const float *rstd, const void *dresidual, ssd_dtype dtype,
+                             ssd_dtype stream_dtype, long long rows, int width, long long dy_stride,
+                             long long s_stride, long long dresidual_stride, void *dx, void *ds,
+                             float *dweight, float *dbias, void *workspace, size_t workspace_bytes,
+                             cudaStream_t stream) {
+    if (!known_type(dtype) || !known_type(stream_dtype)) return SSD_ERR_INVALID_ARG;
+    if (!norm_sizes_ok(rows, width)) return SSD_ERR_INVALID_ARG;
+    if (!float_type(dtype) || (stream_dtype != dtype && stream_dtype != SSD_F32))
+        return SSD_ERR_UNSUPPORTED;
+    if (!norm_sizes_handled(rows, width)) return SSD_ERR_UNSUPPORTED;
+    if (!array(dweight, 4) || !maybe(dbias, 4)) return SSD_ERR_INVALID_ARG;
+    if (rows == 0) {
+        const size_t bytes = (size_t)width * sizeof(float);
+        if (cudaMemsetAsync(dweight, 0, bytes, stream) != cudaSuccess) return SSD_ERR_CUDA;
+        return dbias ? launched(cudaMemsetAsync(dbias, 0, bytes, stream)) : SSD_OK;
+    }
+    const size_t n = size_of(dtype), ns = size_of(stream_dtype);
+    if (!array(dy, n) || !array(s, ns) || !array(weight, 4) || !array(mean, 4) || !array(rstd, 4) ||
+        !array(dx, n) || !maybe(dresidual, ns) || !maybe(ds, ns))
+        return SSD_ERR_INVALID_ARG;
+    if (dy_stride < width || s_stride < width || (dresidual && dresidual_stride < width))
+        return SSD_ERR_INVALID_ARG;
+    const int sms = ssd_sm_count();
+    const ssd_status st = check_workspace(workspace, workspace_bytes,
+                                          ssd_layernorm_bwd_workspace(rows, width, sms), 16);
+    if (st != SSD_OK) return st;
+    SsdLayerNormBwd a{dy, s, dresidual, weight, mean, rstd, elt(dtype), elt(stream_dtype), rows,
+                      width, dy_stride, s_stride, dresidual_stride, dx, ds, dweight, dbias};
+    return launched(ssd_launch_layernorm_bwd(a, static_cast<float *>(workspace), sms, stream));
+}
+
+namespace {
+ssd_status check_embedding(ssd_index index, ssd_dtype table, ssd_dtype out, long long count, int vocab,
+                           int width, float scale) {
+    if ((index != SSD_I32 && index != SSD_I64) || !known_type(table) || !known_type(out) || count < 0 ||
+        vocab <= 0 || width <= 0 || !isfinite(scale))
+        return SSD_ERR_INVALID_ARG;
+    if (!float_type(table) || !float_type(out) || count >= (1ll << 31) - 2048 ||
+        vocab >= (1 << 30) || width >= (1 << 24))
+        return SSD_ERR_UNSUPPORTED;
+    return SSD_OK;
+}
+}  // namespace
+
+ssd_status ssd_embedding_fwd(const void *tokens, ssd_index token_type, const void *table,
+                             ssd_dtype table_dtype, ssd_dtype out_dtype, long long count, int vocab,
+                             int width, float scale, void *y, cudaStream_t stream) {
+    const ssd_status st = check_embedding(token_type, table_dtype, out_dtype, count, vocab, width, scale);
+    if (st != SSD_OK) return st;
+    if (count == 0) return SSD_OK;
+    if (!array(tokens, token_type == SSD_I64 ? 8 : 4) || !array(table, size_of(table_dtype)) ||
+        !array(y, size_of(out_dtype)))
+        return SSD_ERR_INVALID_ARG;
+    SsdEmbedding a{tokens, token_type == SSD_I64, table, elt(table_dtype), elt(out_dtype), count, vocab,
+                   width, scale, y};
+    return launched(ssd_launch_embedding(a, ssd_sm_count(), stream));
+}
+
+size_t ssd_embedding_bwd_workspace_bytes(long long count, int vocab, int width) {
+    if (check_embedding(SSD_I32, SSD_F32, SSD_F32, count, vocab, width, 1.f) != SSD_OK) return kBad;
+    return count ? ssd_embedding_bwd_workspace(count, vocab, width) : 0;
+}
+
+ssd_status ssd_embedding_bwd(const void *dy, const void *tokens, ssd_index token_type,
+                             ssd_dtype dtype, ssd_dtype out_dtype, long long count, int vocab,
+                             int width, long long dy_stride, float scale, void *dtable,
+                             void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    ssd_status st = check_embedding(token_type, dtype, out_dtype, count, vocab, width, scale);
+    if (st != SSD_OK) return st;
+    if (!array(dtable, size_of(out_dtype))) return SSD_ERR_INVALID_ARG;
+    if (count == 0)
+        return launched(cudaMemsetAsync(dtable, 0, (size_t)vocab * width * size_of(out_dtype), stream));
+    if (!array(dy, size_of(dtype)) || !array(tokens, token_type == SSD_I64 ? 8 : 4) || dy_stride < width)
+        return SSD_ERR_INVALID_ARG;
+    st = check_workspace(workspace, workspace_bytes, ssd_embedding_bwd_workspace(count, vocab, width), 256);
+    if (st != SSD_OK) return st;
+    SsdEmbeddingBwd a{tokens, token_type == SSD_I64, dy, dy_stride, elt(dtype), elt(out_dtype), count, vocab,
+                      width, scale, dtable};
+    return launched(ssd_launch_embedding_bwd(a, workspace, ssd_sm_count(), stream));
+}
+
+size_t ssd_delta_scan_bwd_workspace_bytes(ssd_dtype dtype, long long tokens, int nseq, int nheads,
+                                          int headdim, int dstate, int ngroups) {
+    if (check_delta(dtype, nheads, headdim, dstate, ngroups) != SSD_OK || tokens < 0 ||
+        tokens >= (1ll << 31) - 2048 || nseq <= 0 || !delta_handled(tokens, nseq, nheads, headdim))
+        return kBad;
+    SsdDelta d{};
+    d.bf16 = dtype == SSD_BF16;
+    d.tokens = tokens;
+    d.nseq = nseq;
+    d.heads = nheads;
+    d.groups = ngroups;
+    d.p = headdim;
+    d.n = dstate;
+    return tokens ? ssd_delta_bwd_simt_workspace(d) : 0;
+}
+
+ssd_status ssd_delta_scan_fwd(const void *q, const void *k, const void *v, const float *g,
+                              const float *beta, ssd_dtype dtype, int nseq, int length,
+                              const int *cu_seqlens_host, const int *cu_seqlens_dev, int nheads,
+                              int headdim, int dstate, int ngroups, long long q_stride,
+                              long long k_stride, long long v_stride, float scale,
+                              const float *init_state, void *o, long long o_stride,
+                              float *final_state, float *checkpoints, cudaStream_t stream) {
+    SsdDeltaFwd a{};
+    const ssd_status st =
+        delta_input(q, k, v, g, beta, dtype, nseq, length, cu_seqlens_host, cu_seqlens_dev, nheads,
+                    headdim, dstate, ngroups, q_stride, k_stride, v_stride, scale, &a.in);
+    if (st != SSD_OK) return st;
+    if ((a.in.tokens > 0 && !array(o, size_of(dtype))) || o_stride < (long long)nheads * headdim ||
+        !maybe(init_state, 4) || !maybe(final_state, 4) || !maybe(checkpoints, 4))
+        return SSD_ERR_INVALID_ARG;
+    a.init = init_state;
+    a.o = o;
+    a.o_stride = o_stride;
+    a.final_state = final_state;
+    a.checkpoints = checkpoints;
+    return launched(ssd_launch_delta_fwd_simt(a, ssd_sm_count(), stream));
+}
+
+ssd_status ssd_delta_scan_bwd(const void *dout, const void *q, const void *k, const void *v,
+                              const float *g, const float *beta, ssd_dtype dtype, int nseq,
+                              int length, const int *cu_seqlens_host, const int *cu_seqlens_dev,
+                              int nheads, int headdim, int dstate, int ngroups, long long do_stride,
+                              long long q_stride, long long k_stride, long long v_stride, float scale,
+                              const float *checkpoints, const float *dfinal, void *dq,
+                              long long dq_stride, void *dk, long long dk_stride, void *dv,
+                              long long dv_stride, float *dg, float *dbeta, float *dinit,
+                              void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    SsdDeltaBwd a{};
+    ssd_status st =
+        delta_input(q, k, v, g, beta, dtype, nseq, length, cu_seqlens_host, cu_seqlens_dev, nheads,
+                    headdim, dstate, ngroups, q_stride, k_stride, v_stride, scale, &a.in);
+    if (st != SSD_OK) return st;
+    const size_t n = size_of(dtype);
+    if (a.in.tokens > 0 && (!array(dout, n) || !array(checkpoints, 4) || !array(dq, n) || !array(dk, n) ||
+                            !array(dv, n) || !array(dg, 4) || !array(dbeta, 4)))
+        return SSD_ERR_INVALID_ARG;
+    if (do_stride < (long long)nheads * headdim || !maybe(dfinal, 4) || !maybe(dinit, 4) ||
+        !token_strides_ok(dq_stride, dk_stride, dv_stride, nheads, headdim, dstate, ngroups))
+        return SSD_ERR_INVALID_ARG;
+    if (a.in.tokens == 0) {
+        const size_t bytes = (size_t)nseq * nheads * headdim * dstate * sizeof(float);
+        if (!dinit) return SSD_OK;
+        return launched(dfinal ? cudaMemcpyAsync(dinit, dfinal, bytes, cudaMemcpyDeviceToDevice, stream)
+                               : cudaMemsetAsync(dinit, 0, bytes, stream));
+    }
+    st = check_workspace(workspace, workspace_bytes, ssd_delta_bwd_simt_workspace(a.in), 256);
+    if (st != SSD_OK) return st;
+    a.dout = dout;
+    a.checkpoints = checkpoints;
+    a.dfinal = dfinal;
+    a.do_stride = do_stride;
+    a.dq_stride = dq_stride;
+    a.dk_stride = dk_stride;
+    a.dv_stride = dv_stride;
+    a.dq = dq;
+    a.dk = dk;
+    a.dv = dv;
+    a.dg = dg;
+    a.dbeta = dbeta;
+    a.dinit = dinit;
+    return launched(ssd_launch_delta_bwd_simt(a, workspace, stream));
+}
+
+ssd_status ssd_delta_state_update(const void *state, ssd_dtype state_dtype, void *state_out,
+                                  const void *q, const void *k, const void *v, const float *g,
+                                  const float *beta, ssd_dtype dtype, int batch, int nheads,
+                                  int headdim, int dstate, int ngroups, long long q_stride,
+                                  long long k_stride, long long v_stride, float scale, void *o,
+                                  cudaStream_t stream) {
+    const ssd_status st = check_delta(dtype, nheads, headdim, dstate, ngroups);
+    if (st != SSD_OK) return st;
+    if (!known_type(state_dtype) || batch < 0 || !isfinite(scale)) return SSD_ERR_INVALID_ARG;
+    if (!float_type(state_dtype) || (state_dtype == SSD_BF16 && dtype != SSD_BF16) ||
+        !delta_handled(0, batch, nheads, headdim))
+        return SSD_ERR_UNSUPPORTED;
+    if (batch == 0) return SSD_OK;
+    const size_t n = size_of(dtype), ns = size_of(state_dtype);
+    if (!array(state, ns) || !array(state_out, ns) || !array(q, n) || !array(k, n) || !array(v, n) ||
+        !array(g, 4) || !array(beta, 4) || !array(o, n) ||
+        !token_strides_ok(q_stride, k_stride, v_stride, nheads, headdim, dstate, ngroups))
+        return SSD_ERR_INVALID_ARG;
+    SsdDeltaStep a{state, state_out, state_dtype == SSD_BF16, q, k, v, g, beta, dtype == SSD_BF16, batch, nheads,
+                   ngroups, headdim, dstate, q_stride, k_stride, v_stride, scale, o};
+    return launched(ssd_launch_delta_step(a, ssd_sm_count(), stream));
 }
 
 }  // extern "C"

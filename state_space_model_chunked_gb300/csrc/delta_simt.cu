@@ -1,0 +1,615 @@
+// Gated delta rule in fp32 multiply-adds, token by token, for every size and type that the
+// tensor-core kernels do not take, forward and backward.
+//
+//   S' = exp(g_t) S_{t-1},  u_t = beta_t (v_t - S' k_t),  S_t = S' + u_t k_t^T
+//   o_t = scale S_t q_t                               S [P][N] a head
+//
+// The rows p of S do not meet but in the gradients of q and k, so a CTA takes a slab of
+// rows of one head.  Eight lanes share a row: lane l of them holds the columns
+// 32 j + 4 l + i (i < 4), which lie in shared memory as vectors of 16 bytes; a thread has
+// kR rows.  o_t = scale (exp(g_t) S_{t-1} q_t + u_t (k_t q_t)), so both of a token's
+// products with the state are taken of S_{t-1}, in one round of sums over the lanes.
+//
+// Backward, with L_t the gradient of S_t (from dfinal on, last token first):
+//   L += scale do_t q_t^T;   w_t = L k_t (the gradient of u_t);   dv_t = beta_t w_t
+//   dbeta_t = w_t (v_t - S' k_t);   L' = L - dv_t k_t^T;   L_{t-1} = exp(g_t) L'
+//   dq_t = scale S_t^T do_t;   dk_t = L^T u_t - S'^T dv_t;   dg_t = <L', S'>
+// The states are made again from those kept at every 64th token, all runs of 64 at once:
+//   1. u_t of all tokens (runs of 64 side by side)
+//   2. the walk back: w_t of all tokens, L^T u_t, and <L, S> before each run of 64
+//   3. S again, with dq_t, S'^T dv_t, dbeta_t; and dg_t from
+//      dg_{t+1} = dg_t - do_t o_t + dv_t v_t,  which starts anew at every 64th token
+//   4. the sums over a group's heads and a head's slabs, rounded once.
+// Bound by the fp32 pipe: about 4 P N multiply-adds a token forward, 12 backward, where one
+// head's tokens follow each other at the latency of a token's two sums over eight lanes.
+#include "launch.h"
+#include "ptx.cuh"
+
+namespace {
+
+constexpr int kC = kSsdDeltaChunk;
+constexpr int kThreads = 256, kLanes = 8, kRowsPass = kThreads / kLanes;
+constexpr int kTile = 16;           // tokens staged in shared memory at once
+
+// Decays below this are zero in fp32 with room to spare; infinite ones would make 0 * inf.
+__device__ __forceinline__ float decay_of(float g) { return expf(g < -200.f ? -200.f : g); }
+
+__device__ __forceinline__ float load(const void *p, size_t i, bool bf16) {
+    return bf16 ? ssd_ld(static_cast<const __nv_bfloat16 *>(p) + i) : ssd_ld(static_cast<const float *>(p) + i);
+}
+__device__ __forceinline__ void store(void *p, size_t i, bool bf16, float v) {
+    if (bf16) ssd_st(static_cast<__nv_bfloat16 *>(p) + i, v);
+    else ssd_st(static_cast<float *>(p) + i, v);
+}
+
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// A sequence's tokens on the token axis.
+__device__ __forceinline__ void range_of(const SsdDelta &d, int seq, long long &first, int &len) {
+    if (d.cu) {
+        first = d.cu[seq];
+        len = d.cu[seq + 1] - d.cu[seq];
+    } else {
+        first = (long long)seq * d.length;
+        len = d.length;
+    }
+}
+
+// A CTA's sequence, head, slab of rows and, where runs of 64 tokens go side by side, run.
+__device__ __forceinline__ void cta_place(const SsdDelta &d, int slabs, int &seq, int &head, int &slab, int &run) {
+    unsigned i = blockIdx.x;
+    slab = (int)(i % slabs);
+    i /= slabs;
+    head = (int)(i % d.heads);
+    i /= d.heads;
+    seq = (int)(i % d.nseq);
+    run = (int)(i / d.nseq);
+}
+
+// One thread's part of the state: kR rows of kV columns.
+template <int kV, int kR>
+struct State {
+    float s[kR][kV];
+    int row[kR];        // of the head, or -1
+    int lane;
+
+    __device__ __forceinline__ void place(int slab, int p) {
+        lane = threadIdx.x % kLanes;
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            const int at = slab * kRowsPass * kR + r * kRowsPass + threadIdx.x / kLanes;
+            row[r] = at < p ? at : -1;
+        }
+    }
+    __device__ __forceinline__ static int column(int lane, int i) { return i / 4 * 32 + lane * 4 + i % 4; }
+    // from / to [P][N] (null: zeros)
+    __device__ __forceinline__ void load(const float *m, int n) {
+#pragma unroll
+        for (int r = 0; r < kR; ++r)
+#pragma unroll
+            for (int i = 0; i < kV; ++i) {
+                const int c = column(lane, i);
+                s[r][i] = m && row[r] >= 0 && c < n ? m[(size_t)row[r] * n + c] : 0.f;
+            }
+    }
+    __device__ __forceinline__ void store(float *m, int n) const {
+#pragma unroll
+        for (int r = 0; r < kR; ++r)
+#pragma unroll
+            for (int i = 0; i < kV; ++i) {
+                const int c = column(lane, i);
+                if (row[r] >= 0 && c < n) m[(size_t)row[r] * n + c] = s[r][i];
+            }
+    }
+};
+
+// A lane's columns of a staged row of 8 kV values.
+template <int kV>
+__device__ __forceinline__ void columns(const float *row, int lane, float (&v)[kV]) {
+#pragma unroll
+    for (int i = 0; i < kV; i += 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(row + i * 8 + lane * 4);
+        v[i] = x.x;
+        v[i + 1] = x.y;
+        v[i + 2] = x.z;
+        v[i + 3] = x.w;
+    }
+}
+template <int kV>
+__device__ __forceinline__ float dot(const float (&a)[kV], const float (&b)[kV]) {
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < kV; ++i) v += a[i] * b[i];
+    return v;
+}
+
+// kTile tokens' rows of `width` values at `offset` of each token, zeros behind them and in
+// the columns up to `pad`.
+__device__ __forceinline__ void stage(float *to, int pad, const void *from, bool bf16, long long token,
+                                      long long stride, size_t offset, int width, int tokens) {
+    for (int i = threadIdx.x; i < kTile * pad; i += kThreads) {
+        const int t = i / pad, c = i - t * pad;
+        to[i] = t < tokens && c < width ? load(from, (size_t)(token + t) * stride + offset + c, bf16) : 0.f;
+    }
+}
+
+// ------------------------------------------------------------------- forward
+// Whole sequences (kU false: o, the final state, the kept ones), or of every run of 64
+// tokens from its kept state the u_t alone.
+struct Walk {
+    SsdDelta d;
+    const float *init, *kept;
+    void *o;
+    long long o_stride;
+    float *final_state, *checkpoints, *u;       // u [tokens][heads][P]
+    int slabs;
+};
+
+template <int kV, int kR, bool kU>
+__global__ void __launch_bounds__(kThreads) delta_walk_kernel(const Walk a) {
+    constexpr int kN = kV * kLanes, kRows = kRowsPass * kR;
+    __shared__ __align__(16) float q[kTile][kN], k[kTile][kN];
+    __shared__ float v[kTile][kRows], decay[kTile], beta[kTile];
+    const SsdDelta &d = a.d;
+    int seq, head, slab, run;
+    cta_place(d, a.slabs, seq, head, slab, run);
+    const int group = head / (d.heads / d.groups);
+    long long first;
+    int len;
+    range_of(d, seq, first, len);
+    const size_t size = (size_t)d.p * d.n, state = ((size_t)seq * d.heads + head) * size;
+    State<kV, kR> S;
+    S.place(slab, d.p);
+    int from = 0, to = len;
+    if constexpr (kU) {
+        from = run * kC;
+        if (from >= len) return;
+        to = min(len, from + kC);
+        S.load(a.kept + ((size_t)ssd_delta_slot(first, seq, run) * d.heads + head) * size, d.n);
+    } else {
+        S.load(a.init ? a.init + state : nullptr, d.n);
+    }
+    const int rows = min(kRows, d.p - slab * kRows);
+    for (int t0 = from; t0 < to; t0 += kTile) {
+        if constexpr (!kU) {
+            if (a.checkpoints && t0 % kC == 0)
+                S.store(a.checkpoints + ((size_t)ssd_delta_slot(first, seq, t0 / kC) * d.heads + head) * size, d.n);
+        }
+        const int tokens = min(kTile, to - t0);
+        __syncthreads();
+        stage(&k[0][0], kN, d.k, d.bf16, first + t0, d.k_stride, (size_t)group * d.n, d.n, tokens);
+        if constexpr (!kU)
+            stage(&q[0][0], kN, d.q, d.bf16, first + t0, d.q_stride, (size_t)group * d.n, d.n, tokens);
+        stage(&v[0][0], kRows, d.v, d.bf16, first + t0, d.v_stride, (size_t)head * d.p + slab * kRows, rows, tokens);
+        if (threadIdx.x < tokens) {
+            const size_t i = (size_t)(first + t0 + threadIdx.x) * d.heads + head;
+            decay[threadIdx.x] = decay_of(d.g[i]);
+            beta[threadIdx.x] = d.beta[i];
+        }
+        __syncthreads();
+        for (int t = 0; t < tokens; ++t) {
+            float kc[kV], qc[kV], sk[kR], sq[kR], kq = 0.f;
+            columns(k[t], S.lane, kc);
+            if constexpr (!kU) {
+                columns(q[t], S.lane, qc);
+                kq = lanes_sum(dot(kc, qc));
+            }
+            const float f = decay[t];
+#pragma unroll
+            for (int r = 0; r < kR; ++r) {
+                sk[r] = lanes_sum(dot(S.s[r], kc));
+                if constexpr (!kU) sq[r] = lanes_sum(dot(S.s[r], qc));
+            }
+#pragma unroll
+            for (int r = 0; r < kR; ++r) {
+                const float u = beta[t] * (v[t][r * kRowsPass + threadIdx.x / kLanes] - f * sk[r]);
+#pragma unroll
+                for (int i = 0; i < kV; ++i) S.s[r][i] = f * S.s[r][i] + u * kc[i];
+                if (S.lane == 0 && S.row[r] >= 0) {
+                    const size_t at = (size_t)head * d.p + S.row[r];
+                    if constexpr (kU) a.u[(size_t)(first + t0 + t) * d.heads * d.p + at] = u;
+                    else store(a.o, (size_t)(first + t0 + t) * a.o_stride + at, d.bf16, d.scale * (f * sq[r] + u * kq));
+                }
+            }
+        }
+    }
+    if constexpr (!kU) {
+        if (a.final_state) S.store(a.final_state + state, d.n);
+    }
+}
+
+// ------------------------------------------------------------------ backward
+struct Back {
+    SsdDelta d;
+    const void *dout;
+    const float *kept, *dfinal;
+    long long do_stride, dv_stride;
+    void *dv;
+    float *dinit;
+    float *u, *w;           // [tokens][heads][P]
+    float *dq, *dk;         // [tokens][heads][slabs][N], sums over a slab's rows
+    float *anchor;          // [slots][heads][slabs]: <L, S> before a run of 64 tokens
+    float *ov, *rw;         // [tokens][heads][slabs]: do_t o_t - dv_t v_t and w_t (v_t - S' k_t)
+    int slabs;
+};
+
+// The warp's sum over its rows (4 groups of lanes, kR rows each) of x_r s_r, into `part`'s
+// row of this warp.
+template <int kV, int kR>
+__device__ __forceinline__ void rows_sum(const float (&s)[kR][kV], const float (&x)[kR], float *part) {
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+        float v = 0.f;
+#pragma unroll
+        for (int r = 0; r < kR; ++r) v += s[r][i] * x[r];
+        v += __shfl_xor_sync(0xffffffffu, v, 8);
+        v += __shfl_xor_sync(0xffffffffu, v, 16);
+        if ((threadIdx.x & 31) < kLanes) part[State<kV, kR>::column(threadIdx.x % kLanes, i)] = v;
+    }
+}
+// The CTA's sum of one value a thread, in thread 0.
+__device__ __forceinline__ float cta_sum(float v, float *buf) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.f;
+    for (int w = 0; w < kThreads / 32; ++w) v += buf[w];
+    return v;
+}
+
+constexpr int kBackTile = 8;        // tokens whose sums over the warps wait in shared memory
+
+template <int kV, int kR>
+struct BackSmem {
+    static constexpr int kN = kV * kLanes, kRows = kRowsPass * kR;
+    float q[kTile][kN], k[kTile][kN];
+    float part[kBackTile][kThreads / 32][kN];
+    float x[kTile][kRows], y[kTile][kRows], z[kTile][kRows];
+    float decay[kTile], beta[kTile];
+    float sums[2][kBackTile][kThreads / 32];
+    float buf[kThreads / 32];
+};
+
+// Step 2: the walk back.
+template <int kV, int kR>
+__global__ void __launch_bounds__(kThreads) delta_back_kernel(const Back a) {
+    extern __shared__ __align__(16) unsigned char delta_smem[];
+    auto &m = *reinterpret_cast<BackSmem<kV, kR> *>(delta_smem);
+    constexpr int kN = kV * kLanes, kRows = kRowsPass * kR;
+    const SsdDelta &d = a.d;
+    int seq, head, slab, run;
+    cta_place(d, a.slabs, seq, head, slab, run);
+    const int group = head / (d.heads / d.groups);
+    long long first;
+    int len;
+    range_of(d, seq, first, len);
+    const size_t size = (size_t)d.p * d.n, state = ((size_t)seq * d.heads + head) * size;
+    State<kV, kR> L;
+    L.place(slab, d.p);
+    L.load(a.dfinal ? a.dfinal + state : nullptr, d.n);
+    const int rows = min(kRows, d.p - slab * kRows), warp = threadIdx.x >> 5;
+    const size_t wide = (size_t)d.heads * a.slabs;
+    for (int t0 = len ? (len - 1) / kTile * kTile : -1; t0 >= 0; t0 -= kTile) {
+        const int tokens = min(kTile, len - t0);
+        __syncthreads();
+        stage(&m.q[0][0], kN, d.q, d.bf16, first + t0, d.q_stride, (size_t)group * d.n, d.n, tokens);
+        stage(&m.k[0][0], kN, d.k, d.bf16, first + t0, d.k_stride, (size_t)group * d.n, d.n, tokens);
+        const size_t at = (size_t)head * d.p + slab * kRows;
+        stage(&m.x[0][0], kRows, a.dout, d.bf16, first + t0, a.do_stride, at, rows, tokens);
+        stage(&m.y[0][0], kRows, a.u, false, first + t0, (long long)d.heads * d.p, at, rows, tokens);
+        if (threadIdx.x < tokens) {
+            const size_t i = (size_t)(first + t0 + threadIdx.x) * d.heads + head;
+            m.decay[threadIdx.x] = decay_of(d.g[i]);
+            m.beta[threadIdx.x] = d.beta[i];
+        }
+        __syncthreads();
+        for (int b0 = (tokens - 1) / kBackTile * kBackTile; b0 >= 0; b0 -= kBackTile) {
+            const int part = min(kBackTile, tokens - b0);
+            for (int b = part - 1; b >= 0; --b) {
+                const int t = b0 + b;
+                float kc[kV], qc[kV], x[kR], w[kR];
+                columns(m.k[t], L.lane, kc);
+                columns(m.q[t], L.lane, qc);
+#pragma unroll
+                for (int r = 0; r < kR; ++r) {
+                    x[r] = m.y[t][r * kRowsPass + threadIdx.x / kLanes];
+                    const float dout = d.scale * m.x[t][r * kRowsPass + threadIdx.x / kLanes];
+#pragma unroll
+                    for (int i = 0; i < kV; ++i) L.s[r][i] += dout * qc[i];
+                    w[r] = lanes_sum(dot(L.s[r], kc));
+                }
+                rows_sum<kV, kR>(L.s, x, m.part[b][warp]);
+                const float f = m.decay[t];
+#pragma unroll
+                for (int r = 0; r < kR; ++r) {
+                    const float dv = m.beta[t] * w[r];
+#pragma unroll
+                    for (int i = 0; i < kV; ++i) L.s[r][i] = f * (L.s[r][i] - dv * kc[i]);
+                    if (L.lane == 0 && L.row[r] >= 0) {
+                        const size_t token = (size_t)(first + t0 + t), row = (size_t)head * d.p + L.row[r];
+                        a.w[token * d.heads * d.p + row] = w[r];
+                        store(a.dv, token * a.dv_stride + row, d.bf16, dv);
+                    }
+                }
+            }
+            __syncthreads();
+            float *const out = a.dk + ((size_t)(first + t0 + b0) * wide + head * a.slabs + slab) * d.n;
+            for (int i = threadIdx.x; i < part * kN; i += kThreads) {
+                const int t = i / kN, c = i % kN;
+                if (c >= d.n) continue;
+                float v = 0.f;
+#pragma unroll
+                for (int w = 0; w < kThreads / 32; ++w) v += m.part[t][w][c];
+                out[(size_t)t * wide * d.n + c] = v;
+            }
+            __syncthreads();
+        }
+        if (t0 % kC == 0) {
+            const size_t slot = (size_t)ssd_delta_slot(first, seq, t0 / kC);
+            State<kV, kR> S;
+            S.place(slab, d.p);
+            S.load(a.kept + (slot * d.heads + head) * size, d.n);
+            float v = 0.f;
+#pragma unroll
+            for (int r = 0; r < kR; ++r) v += dot(L.s[r], S.s[r]);
+            v = cta_sum(v, m.buf);
+            if (threadIdx.x == 0) a.anchor[slot * wide + head * a.slabs + slab] = v;
+        }
+    }
+    if (a.dinit) L.store(a.dinit + state, d.n);
+}
+
+// Step 3: a run of 64 tokens forward again.
+template <int kV, int kR>
+__global__ void __launch_bounds__(kThreads) delta_again_kernel(const Back a) {
+    extern __shared__ __align__(16) unsigned char delta_smem[];
+    auto &m = *reinterpret_cast<BackSmem<kV, kR> *>(delta_smem);
+    constexpr int kN = kV * kLanes, kRows = kRowsPass * kR;
+    const SsdDelta &d = a.d;
+    int seq, head, slab, run;
+    cta_place(d, a.slabs, seq, head, slab, run);
+    const int group = head / (d.heads / d.groups);
+    long long first;
+    int len;
+    range_of(d, seq, first, len);
+    const int from = run * kC, to = min(len, from + kC);
+    if (from >= len) return;
+    const size_t size = (size_t)d.p * d.n;
+    State<kV, kR> S;
+    S.place(slab, d.p);
+    S.load(a.kept + ((size_t)ssd_delta_slot(first, seq, run) * d.heads + head) * size, d.n);
+    const int rows = min(kRows, d.p - slab * kRows), warp = threadIdx.x >> 5;
+    const size_t wide = (size_t)d.heads * a.slabs;
+    for (int t0 = from; t0 < to; t0 += kBackTile) {
+        const int tokens = min(kBackTile, to - t0);
+        __syncthreads();
+        stage(&m.q[0][0], kN, d.q, d.bf16, first + t0, d.q_stride, (size_t)group * d.n, d.n, tokens);
+        stage(&m.k[0][0], kN, d.k, d.bf16, first + t0, d.k_stride, (size_t)group * d.n, d.n, tokens);
+        const size_t at = (size_t)head * d.p + slab * kRows;
+        stage(&m.x[0][0], kRows, a.dout, d.bf16, first + t0, a.do_stride, at, rows, tokens);
+        stage(&m.y[0][0], kRows, a.w, false, first + t0, (long long)d.heads * d.p, at, rows, tokens);
+        stage(&m.z[0][0], kRows, d.v, d.bf16, first + t0, d.v_stride, at, rows, tokens);
+        if (threadIdx.x < tokens) {
+            const size_t i = (size_t)(first + t0 + threadIdx.x) * d.heads + head;
+            m.decay[threadIdx.x] = decay_of(d.g[i]);
+            m.beta[threadIdx.x] = d.beta[i];
+        }
+        __syncthreads();
+        const size_t out = ((size_t)(first + t0) * wide + head * a.slabs + slab) * d.n;
+        // S' with S'^T dv, then S with S^T do: the sums over the warps of one token's two
+        // rows go out in turn, kBackTile / 2 tokens at a time
+        for (int b0 = 0; b0 < tokens; b0 += kBackTile / 2) {
+            const int part = min(kBackTile / 2, tokens - b0);
+            for (int b = 0; b < part; ++b) {
+                const int t = b0 + b;
+                float kc[kV], qc[kV], minus[kR], dout[kR], ov = 0.f, rw = 0.f;
+                columns(m.k[t], S.lane, kc);
+                columns(m.q[t], S.lane, qc);
+                const float f = m.decay[t], be = m.beta[t];
+                float u[kR];
+#pragma unroll
+                for (int r = 0; r < kR; ++r) {
+                    const int i0 = r * kRowsPass + threadIdx.x / kLanes;
+                    const float w = m.y[t][i0], v = m.z[t][i0];
+                    dout[r] = d.scale * m.x[t][i0];
+                    minus[r] = -be * w;
+#pragma unroll
+                    for (int i = 0; i < kV; ++i) S.s[r][i] *= f;
+                    const float miss = v - lanes_sum(dot(S.s[r], kc));
+                    u[r] = be * miss;
+                    rw += w * miss;
+                    ov += minus[r] * v;
+                }
+                rows_sum<kV, kR>(S.s, minus, m.part[2 * b][warp]);
+#pragma unroll
+                for (int r = 0; r < kR; ++r) {
+#pragma unroll
+                    for (int i = 0; i < kV; ++i) S.s[r][i] += u[r] * kc[i];
+                    ov += dout[r] * lanes_sum(dot(S.s[r], qc));
+                }
+                rows_sum<kV, kR>(S.s, dout, m.part[2 * b + 1][warp]);
+                // eight lanes hold the same sums: one of them counts
+                ov = S.lane == 0 ? ov : 0.f;
+                rw = S.lane == 0 ? rw : 0.f;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    ov += __shfl_xor_sync(0xffffffffu, ov, o);
+                    rw += __shfl_xor_sync(0xffffffffu, rw, o);
+                }
+                if ((threadIdx.x & 31) == 0) {
+                    m.sums[0][t][warp] = ov;
+                    m.sums[1][t][warp] = rw;
+                }
+            }
+            __syncthreads();
+            for (int i = threadIdx.x; i < 2 * part * kN; i += kThreads) {
+                const int t = i / kN / 2, which = i / kN % 2, c = i % kN;
+                if (c >= d.n) continue;
+                float v = 0.f;
+#pragma unroll
+                for (int w = 0; w < kThreads / 32; ++w) v += m.part[2 * t + which][w][c];
+                const size_t o = out + (size_t)(b0 + t) * wide * d.n + c;
+                if (which) a.dq[o] = v;
+                else a.dk[o] += v;
+            }
+            __syncthreads();
+        }
+        if (threadIdx.x < tokens) {
+            float ov = 0.f, rw = 0.f;
+            for (int w = 0; w < kThreads / 32; ++w) {
+                ov += m.sums[0][threadIdx.x][w];
+                rw += m.sums[1][threadIdx.x][w];
+            }
+            const size_t i = (size_t)(first + t0 + threadIdx.x) * wide + head * a.slabs + slab;
+            a.ov[i] = ov;
+            a.rw[i] = rw;
+        }
+    }
+}
+
+// Step 4: dq and dk, a group's sum over its heads and slabs.
+struct Sums {
+    const float *from;      // [tokens][groups][parts][N]
+    void *to;
+    long long tokens, stride;
+    int groups, parts, n;
+    bool bf16;
+};
+__global__ void __launch_bounds__(256) delta_group_sum_kernel(const Sums q, const Sums k) {
+    const Sums &a = blockIdx.y ? k : q;
+    const long long all = a.tokens * a.groups * a.n;
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < all; i += (long long)gridDim.x * 256) {
+        const long long row = i / a.n;
+        const int c = (int)(i - row * a.n);
+        float v = 0.f;
+        for (int s = 0; s < a.parts; ++s) v += a.from[((size_t)row * a.parts + s) * a.n + c];
+        const long long t = row / a.groups;
+        store(a.to, (size_t)t * a.stride + (size_t)(row - t * a.groups) * a.n + c, a.bf16, v);
+    }
+}
+// ... and dbeta and dg: a thread a head and run of 64 tokens.
+__global__ void __launch_bounds__(128) delta_gates_kernel(const Back a, float *dg, float *dbeta) {
+    const SsdDelta &d = a.d;
+    const size_t wide = (size_t)d.heads * a.slabs;
+    const long long runs = (d.longest + kC - 1) / kC, all = runs * d.heads * d.nseq;
+    for (long long i = (long long)blockIdx.x * 128 + threadIdx.x; i < all; i += (long long)gridDim.x * 128) {
+        const int head = (int)(i % d.heads), seq = (int)(i / d.heads % d.nseq);
+        const int chunk = (int)(i / d.heads / d.nseq);
+        long long first;
+        int len;
+        range_of(d, seq, first, len);
+        if (chunk * kC >= len) continue;
+        const float *anchor = a.anchor + (size_t)ssd_delta_slot(first, seq, chunk) * wide + head * a.slabs;
+        float at = 0.f;
+        for (int s = 0; s < a.slabs; ++s) at += anchor[s];
+        for (int t = chunk * kC; t < min(len, chunk * kC + kC); ++t) {
+            const size_t token = (size_t)(first + t);
+            float ov = 0.f, rw = 0.f;
+            for (int s = 0; s < a.slabs; ++s) {
+                ov += a.ov[token * wide + head * a.slabs + s];
+                rw += a.rw[token * wide + head * a.slabs + s];
+            }
+            dg[token * d.heads + head] = at;
+            dbeta[token * d.heads + head] = rw;
+            at -= ov;
+        }
+    }
+}
+
+template <template <int, int> class Launch, typename... A>
+cudaError_t by_shape(int p, int n, A... args) {
+    const bool one = p <= kRowsPass;
+    if (n <= 32) return one ? Launch<4, 1>::run(args...) : Launch<4, 4>::run(args...);
+    if (n <= 64) return one ? Launch<8, 1>::run(args...) : Launch<8, 4>::run(args...);
+    if (n <= 128) return one ? Launch<16, 1>::run(args...) : Launch<16, 4>::run(args...);
+    return one ? Launch<32, 1>::run(args...) : Launch<32, 2>::run(args...);
+}
+int slab_rows(int p, int n) { return p <= kRowsPass ? kRowsPass : kRowsPass * (n <= 128 ? 4 : 2); }
+
+template <int kV, int kR>
+struct LaunchFwd {
+    static cudaError_t run(Walk a, cudaStream_t stream) {
+        a.slabs = (a.d.p + kRowsPass * kR - 1) / (kRowsPass * kR);
+        const long long ctas = (long long)a.d.nseq * a.d.heads * a.slabs;
+        if (ctas >= (1ll << 31)) return cudaErrorInvalidValue;
+        delta_walk_kernel<kV, kR, false><<<(unsigned)ctas, kThreads, 0, stream>>>(a);
+        return cudaGetLastError();
+    }
+};
+template <int kV, int kR>
+struct LaunchBack {
+    static cudaError_t run(Walk u, Back a, cudaStream_t stream) {
+        const long long ctas = (long long)a.d.nseq * a.d.heads * a.slabs, runs = (a.d.longest + kC - 1) / kC;
+        if (ctas * (runs > 0 ? runs : 1) >= (1ll << 31)) return cudaErrorInvalidValue;
+        constexpr int kSmem = (int)sizeof(BackSmem<kV, kR>);
+        cudaError_t e = cudaFuncSetAttribute(delta_back_kernel<kV, kR>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(delta_again_kernel<kV, kR>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        if (runs > 0) delta_walk_kernel<kV, kR, true><<<(unsigned)(ctas * runs), kThreads, 0, stream>>>(u);
+        delta_back_kernel<kV, kR><<<(unsigned)ctas, kThreads, kSmem, stream>>>(a);
+        if (runs > 0) delta_again_kernel<kV, kR><<<(unsigned)(ctas * runs), kThreads, kSmem, stream>>>(a);
+        return cudaGetLastError();
+    }
+};
+
+// The workspace of the gradients, in bytes from its start.
+struct BackPlan {
+    size_t u, w, dq, dk, anchor, ov, rw, total;
+    int slabs;
+};
+BackPlan back_plan(const SsdDelta &d) {
+    const auto up = [](size_t n) { return (n * sizeof(float) + 255) / 256 * 256; };
+    const int rows = slab_rows(d.p, d.n);
+    BackPlan p;
+    p.slabs = (d.p + rows - 1) / rows;
+    const size_t wide = (size_t)d.heads * p.slabs, tokens = (size_t)d.tokens;
+    p.u = 0;
+    p.w = p.u + up(tokens * d.heads * d.p);
+    p.dq = p.w + up(tokens * d.heads * d.p);
+    p.dk = p.dq + up(tokens * wide * d.n);
+    p.anchor = p.dk + up(tokens * wide * d.n);
+    p.ov = p.anchor + up((size_t)ssd_delta_slots(d.tokens, d.nseq) * wide);
+    p.rw = p.ov + up(tokens * wide);
+    p.total = p.rw + up(tokens * wide);
+    return p;
+}
+
+}  // namespace
+
+cudaError_t ssd_launch_delta_fwd_simt(const SsdDeltaFwd &a, int sms, cudaStream_t stream) {
+    const Walk w{a.in, a.init, nullptr, a.o, a.o_stride, a.final_state, a.checkpoints, nullptr, 1};
+    // few CTAs: slabs of one row a thread, which make a token shorter
+    const long long most = (long long)a.in.nseq * a.in.heads * ((a.in.p + kRowsPass - 1) / kRowsPass);
+    return by_shape<LaunchFwd>(most <= 4ll * sms ? 1 : a.in.p, a.in.n, w, stream);
+}
+
+size_t ssd_delta_bwd_simt_workspace(const SsdDelta &d) { return back_plan(d).total; }
+
+cudaError_t ssd_launch_delta_bwd_simt(const SsdDeltaBwd &a, void *ws, cudaStream_t stream) {
+    const SsdDelta &d = a.in;
+    const BackPlan p = back_plan(d);
+    const auto at = [&](size_t offset) { return reinterpret_cast<float *>(static_cast<char *>(ws) + offset); };
+    const Walk u{d, nullptr, a.checkpoints, nullptr, 0, nullptr, nullptr, at(p.u), p.slabs};
+    const Back b{d, a.dout, a.checkpoints, a.dfinal, a.do_stride, a.dv_stride, a.dv, a.dinit, at(p.u), at(p.w),
+                 at(p.dq), at(p.dk), at(p.anchor), at(p.ov), at(p.rw), p.slabs};
+    cudaError_t e = by_shape<LaunchBack>(d.p, d.n, u, b, stream);
+    if (e != cudaSuccess || d.longest == 0) return e;
+    const int parts = d.heads / d.groups * p.slabs;
+    const Sums q{b.dq, a.dq, d.tokens, a.dq_stride, d.groups, parts, d.n, d.bf16};
+    const Sums k{b.dk, a.dk, d.tokens, a.dk_stride, d.groups, parts, d.n, d.bf16};
+    const auto grid = [](long long items, int per) {
+        const long long n = (items + per - 1) / per;
+        return (unsigned)(n < 8192 ? n : 8192);
+    };
+    delta_group_sum_kernel<<<dim3(grid(d.tokens * d.groups * d.n, 256), 2), 256, 0, stream>>>(q, k);
+    const long long runs = (d.longest + kC - 1) / kC * (long long)d.heads * d.nseq;
+    delta_gates_kernel<<<grid(runs, 128), 128, 0, stream>>>(b, a.dg, a.dbeta);
+    return cudaGetLastError();
+}

@@ -158,6 +158,113 @@ size_t ssd_rmsnorm_bwd_workspace(long long rows, int width, int sms);
 cudaError_t ssd_launch_rmsnorm_bwd(const SsdNormBwd &a, float *partial, int sms,
                                    cudaStream_t stream);
 
+// Layer norm (layernorm.cu), with the RMS norm's types and strides.
+struct SsdLayerNormFwd {
+    const void *x, *residual;
+    const float *weight, *bias;
+    float eps;
+    SsdElt in, stream_type, out;
+    long long rows;
+    int width;
+    long long x_stride, residual_stride;
+    void *y, *residual_out;
+    float *mean, *rstd, *scale;
+};
+cudaError_t ssd_launch_layernorm_fwd(const SsdLayerNormFwd &a, int sms, cudaStream_t stream);
+
+struct SsdLayerNormBwd {
+    const void *dy, *s, *dresidual;
+    const float *weight, *mean, *rstd;
+    SsdElt in, stream_type;
+    long long rows;
+    int width;
+    long long dy_stride, s_stride, dresidual_stride;
+    void *dx, *ds;
+    float *dweight, *dbias;
+};
+size_t ssd_layernorm_bwd_workspace(long long rows, int width, int sms);
+cudaError_t ssd_launch_layernorm_bwd(const SsdLayerNormBwd &a, float *partial, int sms,
+                                     cudaStream_t stream);
+
+// Embedding (embedding.cu): rows of a table by tokens, and its gradient.
+struct SsdEmbedding {
+    const void *tokens;
+    bool wide;                  // tokens of 64 bits
+    const void *table;
+    SsdElt table_type, out_type;
+    long long count;
+    int vocab, width;
+    float scale;
+    void *y;
+};
+cudaError_t ssd_launch_embedding(const SsdEmbedding &a, int sms, cudaStream_t stream);
+struct SsdEmbeddingBwd {
+    const void *tokens;
+    bool wide;
+    const void *dy;
+    long long dy_stride;
+    SsdElt in, out_type;
+    long long count;
+    int vocab, width;
+    float scale;
+    void *dtable;
+};
+size_t ssd_embedding_bwd_workspace(long long count, int vocab, int width);
+cudaError_t ssd_launch_embedding_bwd(const SsdEmbeddingBwd &a, void *ws, int sms,
+                                     cudaStream_t stream);
+
+// Gated delta rule over sequences as the gated recurrence has them (delta_simt.cu).
+constexpr int kSsdDeltaChunk = 64;      // tokens between the states that are kept
+struct SsdDelta {
+    const void *q, *k, *v;
+    const float *g, *beta;
+    bool bf16;
+    long long tokens;
+    int nseq, length, longest;                  // longest: the longest sequence's tokens
+    const int *cu;
+    int heads, groups, p, n;
+    long long q_stride, k_stride, v_stride;     // of a token
+    float scale;
+};
+// The place of the state before a sequence's 64 * c-th token among the kept ones, for a
+// sequence that begins at token `first`.
+__host__ __device__ inline long long ssd_delta_slot(long long first, int seq, long long c) {
+    return first / kSsdDeltaChunk + seq + c;
+}
+inline long long ssd_delta_slots(long long tokens, int nseq) { return tokens / kSsdDeltaChunk + nseq; }
+struct SsdDeltaFwd {
+    SsdDelta in;
+    const float *init;
+    void *o;
+    long long o_stride;
+    float *final_state, *checkpoints;
+};
+cudaError_t ssd_launch_delta_fwd_simt(const SsdDeltaFwd &a, int sms, cudaStream_t stream);
+struct SsdDeltaBwd {
+    SsdDelta in;
+    const void *dout;
+    const float *checkpoints, *dfinal;
+    long long do_stride, dq_stride, dk_stride, dv_stride;
+    void *dq, *dk, *dv;
+    float *dg, *dbeta, *dinit;
+};
+size_t ssd_delta_bwd_simt_workspace(const SsdDelta &d);
+cudaError_t ssd_launch_delta_bwd_simt(const SsdDeltaBwd &a, void *ws, cudaStream_t stream);
+// One token (delta_step.cu): state_out may be state.
+struct SsdDeltaStep {
+    const void *state;
+    void *state_out;
+    bool bf16_state;
+    const void *q, *k, *v;
+    const float *g, *beta;
+    bool bf16;
+    int batch, heads, groups, p, n;
+    long long q_stride, k_stride, v_stride;
+    float scale;
+    void *o;
+};
+cudaError_t ssd_launch_delta_step(const SsdDeltaStep &a, int sms, cudaStream_t stream);
+
 // Gated linear recurrence (gated_scan.cu) over `tokens` tokens laid end to
 // end: nseq sequences of `length` tokens each, or, with cu (device, nseq + 1
 // offsets), of any lengths.

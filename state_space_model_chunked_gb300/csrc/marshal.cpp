@@ -16,6 +16,7 @@
 
 #include <array>
 #include <climits>
+#include <cmath>
 
 #include "ssd.h"
 
@@ -390,6 +391,194 @@ PyObject *gated_scan_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// A tuple of five.
+PyObject *tuple5(PyObject *a, PyObject *b, PyObject *c, PyObject *d, PyObject *e) {
+    PyObject *t = PyTuple_New(5);
+    PyTuple_SET_ITEM(t, 0, a);
+    PyTuple_SET_ITEM(t, 1, b);
+    PyTuple_SET_ITEM(t, 2, c);
+    PyTuple_SET_ITEM(t, 3, d);
+    PyTuple_SET_ITEM(t, 4, e);
+    return t;
+}
+
+// x, weight, bias or None, residual or None, eps, out code
+// -> (y, residual_out or None, mean, rstd, scale or None)
+PyObject *layernorm_fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    bool ok = n == 6;
+    const Matrix x = ok ? matrix(args[0], -1, ok) : Matrix();
+    if (!ok || !x.t || x.t->get_device() != c10::cuda::current_device()) Py_RETURN_NONE;
+    const int dev = x.t->get_device();
+    const at::Tensor *w = tensor(args[1], dev, ok), *b = tensor(args[2], dev, ok);
+    const Matrix r = matrix(args[3], dev, ok);
+    const double eps = PyFloat_AsDouble(args[4]);
+    const int out_code = (int)PyLong_AsLong(args[5]), xc = code(x.t->scalar_type());
+    const int64_t width = x.t->size(-1), rows = x.t->numel() / width;
+    if (PyErr_Occurred()) return nullptr;
+    if (!ok || !w || !vector(w, width) || !vector(b, width) || xc < 0 ||
+        (r.t && r.t->sizes() != x.t->sizes()))
+        Py_RETURN_NONE;
+    const int rc = r.t ? code(r.t->scalar_type()) : xc;
+    if (rc < 0) Py_RETURN_NONE;
+    const auto lead = x.t->sizes().slice(0, x.t->dim() - 1);
+    at::Tensor y = make(x.t->sizes(), type_of(out_code), *x.t), mean = make(lead, at::kFloat, *x.t);
+    at::Tensor rstd = make(lead, at::kFloat, *x.t), so, scale;
+    if (r.t) so = make(x.t->sizes(), r.t->scalar_type(), *x.t);
+    if (out_code == SSD_FP8_E4M3) scale = make(lead, at::kFloat, *x.t);
+    const ssd_status st = ssd_layernorm_fwd(
+        ptr(x.t), ptr(r.t), fptr(w), fptr(b), (float)eps, (ssd_dtype)xc, (ssd_dtype)rc,
+        (ssd_dtype)out_code, rows, (int)width, x.stride, r.stride, out(y), out(so), out<float>(mean),
+        out<float>(rstd), out<float>(scale), c10::cuda::getCurrentCUDAStream(dev));
+    return answer(st, tuple5(wrap(y), wrap(so), wrap(mean), wrap(rstd), wrap(scale)));
+    END_HANDLE_TH_ERRORS
+}
+
+// dy, s, weight, mean, rstd, dresidual, whether dbias is wanted
+// -> (dx, ds (dx itself for one type), dweight, dbias or None)
+PyObject *layernorm_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    bool ok = n == 7;
+    const Matrix dy = ok ? matrix(args[0], -1, ok) : Matrix();
+    if (!ok || !dy.t || dy.t->get_device() != c10::cuda::current_device()) Py_RETURN_NONE;
+    const int dev = dy.t->get_device();
+    const Matrix s = matrix(args[1], dev, ok), dr = matrix(args[5], dev, ok);
+    const at::Tensor *w = tensor(args[2], dev, ok), *mean = tensor(args[3], dev, ok);
+    const at::Tensor *rstd = tensor(args[4], dev, ok);
+    const int bias = PyObject_IsTrue(args[6]);
+    if (bias < 0) return nullptr;       // no truth value: the exception is set
+    const int64_t width = dy.t->size(-1), rows = dy.t->numel() / width;
+    const auto lead = dy.t->sizes().slice(0, dy.t->dim() - 1);
+    const auto stat = [&](const at::Tensor *t) { return t && t->scalar_type() == at::kFloat && t->sizes() == lead; };
+    if (!ok || !s.t || !w || s.t->sizes() != dy.t->sizes() || !like(dr, *s.t) || !vector(w, width) ||
+        !stat(mean) || !stat(rstd))
+        Py_RETURN_NONE;
+    const int c = code(dy.t->scalar_type()), sc = code(s.t->scalar_type());
+    const size_t need = ssd_layernorm_bwd_workspace_bytes(rows, (int)width);
+    if (c < 0 || sc < 0 || need == (size_t)-1) Py_RETURN_NONE;
+    at::Tensor dx = make(dy.t->sizes(), dy.t->scalar_type(), *dy.t), ds, db;
+    if (c != sc) ds = make(dy.t->sizes(), s.t->scalar_type(), *dy.t);
+    at::Tensor dw = make({width}, at::kFloat, *dy.t), ws = scratch(need, *dy.t);
+    if (bias) db = make({width}, at::kFloat, *dy.t);
+    const ssd_status st = ssd_layernorm_bwd(
+        ptr(dy.t), ptr(s.t), fptr(w), fptr(mean), fptr(rstd), ptr(dr.t), (ssd_dtype)c, (ssd_dtype)sc,
+        rows, (int)width, dy.stride, s.stride, dr.stride, out(dx), out(ds), out<float>(dw),
+        out<float>(db), out(ws), need, c10::cuda::getCurrentCUDAStream(dev));
+    PyObject *first = wrap(dx);
+    return answer(st, tuple4(first, ds.defined() ? wrap(ds) : Py_NewRef(first), wrap(dw), wrap(db)));
+    END_HANDLE_TH_ERRORS
+}
+
+// Token numbers: -1 for other types.
+int index_code(const at::Tensor &t) {
+    return t.scalar_type() == at::kInt ? SSD_I32 : (t.scalar_type() == at::kLong ? SSD_I64 : -1);
+}
+
+// tokens, table, scale, out code -> y
+PyObject *embedding_fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    bool ok = n == 4;
+    const at::Tensor *ids = ok ? tensor(args[0], -1, ok) : nullptr;
+    if (!ids || ids->get_device() != c10::cuda::current_device()) Py_RETURN_NONE;
+    const int dev = ids->get_device();
+    const at::Tensor *table = tensor(args[1], dev, ok);
+    const double scale = PyFloat_AsDouble(args[2]);
+    const int out_code = (int)PyLong_AsLong(args[3]);
+    if (PyErr_Occurred()) return nullptr;
+    if (!ok || !table || table->dim() != 2 || index_code(*ids) < 0 || code(table->scalar_type()) < 0)
+        Py_RETURN_NONE;
+    c10::SmallVector<int64_t, 6> shape(ids->sizes().begin(), ids->sizes().end());
+    shape.push_back(table->size(1));
+    at::Tensor y = make(shape, type_of(out_code), *table);
+    const ssd_status st = ssd_embedding_fwd(
+        ptr(ids), (ssd_index)index_code(*ids), ptr(table), (ssd_dtype)code(table->scalar_type()),
+        (ssd_dtype)out_code, ids->numel(), (int)table->size(0), (int)table->size(1), (float)scale,
+        out(y), c10::cuda::getCurrentCUDAStream(dev));
+    return answer(st, wrap(y));
+    END_HANDLE_TH_ERRORS
+}
+
+// dy, tokens, vocab, scale, out code -> dtable
+PyObject *embedding_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    bool ok = n == 5;
+    const Matrix dy = ok ? matrix(args[0], -1, ok) : Matrix();
+    if (!ok || !dy.t || dy.t->get_device() != c10::cuda::current_device()) Py_RETURN_NONE;
+    const int dev = dy.t->get_device();
+    const at::Tensor *ids = tensor(args[1], dev, ok);
+    const long long vocab = PyLong_AsLongLong(args[2]);
+    const double scale = PyFloat_AsDouble(args[3]);
+    const int out_code = (int)PyLong_AsLong(args[4]);
+    if (PyErr_Occurred()) return nullptr;
+    const int64_t width = dy.t->size(-1);
+    if (!ok || !ids || index_code(*ids) < 0 || code(dy.t->scalar_type()) < 0 || vocab <= 0 ||
+        vocab > INT_MAX || ids->sizes() != dy.t->sizes().slice(0, dy.t->dim() - 1))
+        Py_RETURN_NONE;
+    const size_t need = ssd_embedding_bwd_workspace_bytes(ids->numel(), (int)vocab, (int)width);
+    if (need == (size_t)-1) Py_RETURN_NONE;
+    at::Tensor dtable = make({(int64_t)vocab, width}, type_of(out_code), *dy.t), ws = scratch(need, *dy.t);
+    const ssd_status st = ssd_embedding_bwd(
+        ptr(dy.t), ptr(ids), (ssd_index)index_code(*ids), (ssd_dtype)code(dy.t->scalar_type()),
+        (ssd_dtype)out_code, ids->numel(), (int)vocab, (int)width, dy.stride, (float)scale, out(dtable),
+        out(ws), need, c10::cuda::getCurrentCUDAStream(dev));
+    return answer(st, wrap(dtable));
+    END_HANDLE_TH_ERRORS
+}
+
+// An array of a token's values a row: [..., a, b] with the last two dimensions contiguous
+// and the rows at one stride.
+Matrix by_token(PyObject *o, int device, bool &ok) {
+    Matrix m;
+    if (!THPVariable_Check(o)) {
+        ok = false;
+        return m;
+    }
+    const at::Tensor &t = THPVariable_Unpack(o);
+    if (!t.is_cuda() || t.dim() != 3 || t.numel() == 0 || t.size(0) > INT_MAX || t.size(1) > INT_MAX ||
+        t.size(2) > INT_MAX || (device >= 0 && t.get_device() != device) ||
+        (t.size(2) > 1 && t.stride(2) != 1) || (t.size(1) > 1 && t.stride(1) != t.size(2))) {
+        ok = false;
+        return m;
+    }
+    m.t = &t;
+    m.stride = t.size(0) == 1 ? t.size(1) * t.size(2) : t.stride(0);
+    return m;
+}
+
+// state, q, k, v, g, beta, scale or None, state_out or None -> o
+PyObject *delta_state_update(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    bool ok = n == 8;
+    const at::Tensor *state = ok ? tensor(args[0], -1, ok) : nullptr;
+    if (!state || state->dim() != 4 || state->get_device() != c10::cuda::current_device()) Py_RETURN_NONE;
+    const int dev = state->get_device();
+    const Matrix q = by_token(args[1], dev, ok), k = by_token(args[2], dev, ok), v = by_token(args[3], dev, ok);
+    const at::Tensor *g = tensor(args[4], dev, ok), *beta = tensor(args[5], dev, ok);
+    const at::Tensor *next = tensor(args[7], dev, ok);
+    if (!ok || !g || !beta) Py_RETURN_NONE;
+    const int64_t batch = state->size(0), heads = state->size(1), p = state->size(2), s = state->size(3);
+    const double scale = args[6] == Py_None ? std::pow((double)s, -0.5) : PyFloat_AsDouble(args[6]);
+    if (PyErr_Occurred()) return nullptr;
+    const std::array<int64_t, 2> gates{batch, heads};
+    const std::array<int64_t, 3> values{batch, heads, p}, keys{batch, q.t->size(1), s};
+    const auto gate = [&](const at::Tensor *t) {
+        return t->scalar_type() == at::kFloat && t->sizes() == at::IntArrayRef(gates);
+    };
+    if (heads > INT_MAX || p > INT_MAX || v.t->sizes() != at::IntArrayRef(values) ||
+        q.t->sizes() != at::IntArrayRef(keys) || !like(k, *q.t) || v.t->scalar_type() != q.t->scalar_type() ||
+        !gate(g) || !gate(beta) || code(q.t->scalar_type()) < 0 || code(state->scalar_type()) < 0 ||
+        (next && (next->sizes() != state->sizes() || next->scalar_type() != state->scalar_type())))
+        Py_RETURN_NONE;
+    at::Tensor o = make(values, q.t->scalar_type(), *q.t);
+    const ssd_status st = ssd_delta_state_update(
+        ptr(state), (ssd_dtype)code(state->scalar_type()), (next ? next : state)->mutable_data_ptr(),
+        ptr(q.t), ptr(k.t), ptr(v.t), fptr(g), fptr(beta), (ssd_dtype)code(q.t->scalar_type()), (int)batch,
+        (int)heads, (int)p, (int)s, (int)q.t->size(1), q.stride, k.stride, v.stride, (float)scale, out(o),
+        c10::cuda::getCurrentCUDAStream(dev));
+    return answer(st, wrap(o));
+    END_HANDLE_TH_ERRORS
+}
+
 #define SSD_METHOD(name) {#name, (PyCFunction)(void (*)())name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {
     SSD_METHOD(rmsnorm_fwd),
@@ -399,6 +588,11 @@ PyMethodDef methods[] = {
     SSD_METHOD(gated_scan_fwd),
     SSD_METHOD(gated_scan_bwd),
     SSD_METHOD(gated_state_update),
+    SSD_METHOD(layernorm_fwd),
+    SSD_METHOD(layernorm_bwd),
+    SSD_METHOD(embedding_fwd),
+    SSD_METHOD(embedding_bwd),
+    SSD_METHOD(delta_state_update),
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "ssd_marshal", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -23,14 +23,13 @@
 // CTA's registers (above 8192 values, forward with vectors 16384) are read again for
 // each pass over them: 4096 rows of 33000 417 us forward (0.38) and 672 backward (0.24),
 // gradients at 16384 346 us (0.23).
-#include "launch.h"
+#include "norm_rows.cuh"
 #include "ptx.cuh"
-#include "vec.cuh"
 
 namespace {
 
-constexpr float kE4m3Max = 448.f;
-constexpr int kMostWarps = 16;      // a row's CTA: 128 registers a thread
+using namespace ssdnorm;
+
 // most runs a thread: of 8 values (forward, backward) and of one
 constexpr int kRuns8 = 4, kBwdRuns8 = 2, kRuns1 = 16;
 // runs wanted a thread where there are rows enough, and warps an SM holds.  us
@@ -38,65 +37,6 @@ constexpr int kRuns8 = 4, kBwdRuns8 = 2, kRuns1 = 16;
 // (1, 32) 262, (1, 48) 292; backward: (1, 16) 46.6, (1, 24) 51, (1, 32) 48.7, (2, 16) 47.0
 constexpr int kFwdRuns = 4, kFwdWarpsSm = 16;
 constexpr int kBwdRuns = 1, kBwdWarpsSm = 16;
-
-// The CTA's sum, and with kMax its maximum, over its warps (any number of them up to 32).
-template <bool kMax>
-__device__ __forceinline__ void cta_sum_max(float &sum, float &mx, float (*buf)[32]) {
-    sum = ssd_warp_sum(sum);
-    if constexpr (kMax) mx = ssd_warp_max(mx);
-    const int warps = blockDim.x >> 5;
-    if (warps == 1) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (lane == 0) {
-        buf[0][warp] = sum;
-        if constexpr (kMax) buf[1][warp] = mx;
-    }
-    __syncthreads();
-    sum = ssd_warp_sum(lane < warps ? buf[0][lane] : 0.f);
-    if constexpr (kMax) mx = ssd_warp_max(lane < warps ? buf[1][lane] : 0.f);
-}
-
-// The scale of an 8-bit row and the rounding of one of its values.  Below
-// 1e-30 the reciprocal of the scale would leave fp32's range, so those rows
-// divide.
-struct RowScale {
-    float scale, inv;
-    bool tiny;
-    __device__ __forceinline__ explicit RowScale(float amax) {
-        scale = amax / kE4m3Max;
-        if (scale == 0.f) scale = 1.f;      // zeros, or values below 3e-43, which are 0 too
-        tiny = scale < 1e-30f;
-        inv = 1.f / scale;
-    }
-    __device__ __forceinline__ float apply(float y) const { return tiny ? y / scale : y * inv; }
-};
-
-// kC runs of V values of a row: run c of this thread starts at value
-// (threadIdx.x + c * blockDim.x) * V; runs past the row read as zero.
-template <typename T, int V, int kC>
-struct Row {
-    SsdRaw<T, V> run[kC];
-    __device__ __forceinline__ void load(const T *row, int nvec, bool on) {
-#pragma unroll
-        for (int c = 0; c < kC; ++c) {
-            const int i = threadIdx.x + c * blockDim.x;
-            run[c].zero();
-            if (on && i < nvec) run[c].load_cs(row + (size_t)i * V);
-        }
-    }
-};
-template <int V, int kC>
-__device__ __forceinline__ void load_weight(const float *weight, int nvec, float (&w)[kC][V]) {
-#pragma unroll
-    for (int c = 0; c < kC; ++c) {
-        const int i = threadIdx.x + c * blockDim.x;
-        SsdRaw<float, V> r;
-        r.zero();
-        if (i < nvec) r.load(weight + (size_t)i * V);
-#pragma unroll
-        for (int k = 0; k < V; ++k) w[c][k] = r.get(k);
-    }
-}
 
 template <typename TX, typename TR, typename TO, int V, int kC>
 __global__ void __launch_bounds__(32 * kMostWarps) rmsnorm_fwd_kernel(const SsdNormFwd a) {
@@ -309,30 +249,6 @@ __global__ void rmsnorm_dw_wide_kernel(const SsdNormBwd a, float *__restrict__ p
         acc += ssd_ld(static_cast<const T *>(a.dy) + row * a.dy_stride + j) *
                (ssd_ld(static_cast<const TS *>(a.s) + row * a.s_stride + j) * a.rstd[row]);
     partial[(size_t)blockIdx.x * a.width + j] = acc;
-}
-
-// Threads and runs a thread for one row: at most `most_runs` runs of V values a
-// thread (`want` where the warps allow it), a power of two of warps; 0 warps
-// when the row does not fit.
-struct RowShape {
-    int warps, runs;
-};
-RowShape row_shape(int width, int V, int most_runs, int want) {
-    const int nvec = (width + V - 1) / V;
-    int w = 1;
-    while (w < kMostWarps && (long long)w * 32 * want < nvec) w *= 2;
-    const int runs = (nvec + w * 32 - 1) / (w * 32);
-    return {runs <= most_runs ? w : 0, runs};
-}
-
-// CTAs of a walk over rows: as many as the SMs hold at once.
-unsigned walkers(long long rows, int sms, int ctas) {
-    const long long n = (long long)sms * ctas;
-    return (unsigned)(rows < n ? rows : n);
-}
-
-bool vec8(const void *p, long long stride, int size) {
-    return p == nullptr || (((uintptr_t)p & 15u) == 0 && (stride * size) % 16 == 0);
 }
 
 template <typename TX, typename TR, typename TO>

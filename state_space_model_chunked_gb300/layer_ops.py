@@ -1,6 +1,7 @@
-"""ctypes binding of the layer's steps around the scan: the RMS norm with the
-residual's addition, the matrix product with its epilogue and the gated linear
-recurrence (argument marshalling only; contracts in include/ssd.h).
+"""ctypes binding of the layer's steps around the scan: the RMS norm and the layer
+norm with the residual's addition, the embedding, the matrix product with its
+epilogue and the gated linear recurrence (argument marshalling only; contracts in
+include/ssd.h).
 
 Matrices may be column ranges of wider ones: unit-stride columns, and leading
 dimensions that lie at one row stride.  Outputs, and workspaces that are not
@@ -280,6 +281,175 @@ def rmsnorm_bwd(dy, s, weight, rstd, dresidual=None, *, dx=None, ds=None, dweigh
           None if one else _full(ds, "ds", s.dtype, at, shape),
           _full(dweight, "dweight", _F32, at, (width,)), wp, wb)
     return dx, dx if one else ds, dweight
+
+
+# ----------------------------------------------------------------- layer norm
+def layernorm_fwd(x, weight, bias=None, residual=None, *, eps=1e-5, out_dtype=None, y=None,
+                  residual_out=None, mean=None, rstd=None, scale=None):
+    """Layer norm of s = x + residual over the last dimension:
+    y = (s - mean) * rstd * weight + bias, rstd = (mean((s - mean)^2) + eps)^(-1/2).
+
+    Arguments as in rmsnorm_fwd; bias [width] f32 or None.  Returns
+    (y, residual_out = s in the residual's dtype or None, mean [...] f32,
+    rstd [...] f32, scale [...] f32 of 8-bit rows or None).  residual_out may be
+    the residual itself."""
+    if (x is not None and y is None and residual_out is None and mean is None and rstd is None
+            and scale is None):
+        got = (_marshal_module or _marshal()).layernorm_fwd(
+            x, weight, bias, residual, eps,
+            _code(x.dtype if out_dtype is None else out_dtype, "out_dtype"))
+        if got is not None:
+            return _plain("ssd_layernorm_fwd", got)
+    lib = load()
+    at, dev, dtype = _cuda(x, "x"), x.device, x.dtype
+    shape = x.shape
+    rows_shape, width = shape[:-1], shape[-1]
+    out_dtype = dtype if out_dtype is None else out_dtype
+    xc, oc = _code(dtype, "x"), _code(out_dtype, "out_dtype")
+    xp, xs = _rows(x, "x", dtype, at, shape)
+    if residual is not None:
+        stream = residual.dtype
+        rp, rs = _rows(residual, "residual", stream, at, shape)
+        sc = _code(stream, "residual")
+        residual_out, sp = _out(residual_out, "residual_out", stream, at, dev, shape)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    else:
+        rp, rs, sc, sp = None, 0, xc, None
+    y, yp = _out(y, "y", out_dtype, at, dev, shape)
+    mean, mp = _out(mean, "mean", _F32, at, dev, rows_shape)
+    rstd, tp = _out(rstd, "rstd", _F32, at, dev, rows_shape)
+    if out_dtype is FP8_E4M3:
+        scale, cp = _out(scale, "scale", _F32, at, dev, rows_shape)
+    else:
+        scale, cp = None, None
+    _call(at, lib.ssd_layernorm_fwd, xp, rp, _full(weight, "weight", _F32, at, (width,)),
+          _full(bias, "bias", _F32, at, (width,)), eps, xc, sc, oc, _count(rows_shape), width, xs,
+          rs, yp, sp, mp, tp, cp)
+    return y, residual_out, mean, rstd, scale
+
+
+def layernorm_bwd_workspace_bytes(rows, width, device=None):
+    """Workspace bytes of layernorm_bwd on the device."""
+    return _size(_index(device), load().ssd_layernorm_bwd_workspace_bytes, rows, width)
+
+
+def layernorm_bwd(dy, s, weight, mean, rstd, dresidual=None, *, bias=True, dx=None, ds=None,
+                  dweight=None, dbias=None, workspace=None):
+    """Gradients of layernorm_fwd: dy [..., width] of y; s, mean, rstd: its
+    residual_out (or x), mean and rstd; dresidual (s's dtype): the gradient that
+    reached residual_out from elsewhere.  Returns (dx, ds, dweight, dbias): the
+    gradient of x in dy's dtype and of the residual in s's (one tensor when those
+    agree), of the weight and of the bias (None without), f32."""
+    if dx is None and ds is None and dweight is None and dbias is None and workspace is None:
+        got = (_marshal_module or _marshal()).layernorm_bwd(dy, s, weight, mean, rstd, dresidual,
+                                                            bias)
+        if got is not None:
+            return _plain("ssd_layernorm_bwd", got)
+    lib = load()
+    at, dev = _cuda(dy, "dy"), dy.device
+    shape, width = dy.shape, dy.shape[-1]
+    yc = _code(dy.dtype, "dy")
+    yp, ys = dy.data_ptr(), _row_stride(dy, "dy")
+    _cuda(s, "s")
+    sp, ss = _rows(s, "s", s.dtype, at, shape)
+    dp, dstride = _rows(dresidual, "dresidual", s.dtype, at, shape)
+    rows = _count(shape[:-1])
+    if dx is None:
+        dx = torch.empty(shape, dtype=dy.dtype, device=dev)
+    one = s.dtype == dy.dtype
+    if one:
+        if ds is not None and ds is not dx:
+            raise ValueError("ds is dx when dy and s have one dtype")
+    elif ds is None:
+        ds = torch.empty(shape, dtype=s.dtype, device=dev)
+    if dweight is None:
+        dweight = torch.empty((width,), dtype=_F32, device=dev)
+    if not bias:
+        if dbias is not None:
+            raise ValueError("dbias is given but not wanted (bias=False)")
+    elif dbias is None:
+        dbias = torch.empty((width,), dtype=_F32, device=dev)
+    need = _size(at, lib.ssd_layernorm_bwd_workspace_bytes, rows, width)
+    _keep, wp, wb = _scratch(workspace, need, dev)
+    lead = shape[:-1]
+    _call(at, lib.ssd_layernorm_bwd, yp, sp, _full(weight, "weight", _F32, at, (width,)),
+          _full(mean, "mean", _F32, at, lead), _full(rstd, "rstd", _F32, at, lead), dp, yc,
+          _code(s.dtype, "s"), rows, width, ys, ss, dstride, _full(dx, "dx", dy.dtype, at, shape),
+          None if one else _full(ds, "ds", s.dtype, at, shape),
+          _full(dweight, "dweight", _F32, at, (width,)), _full(dbias, "dbias", _F32, at, (width,)),
+          wp, wb)
+    return dx, dx if one else ds, dweight, dbias
+
+
+# ------------------------------------------------------------------ embedding
+_INDEX = {torch.int32: 0, torch.int64: 1}
+
+
+def _tokens(tokens, index=None):
+    """(device index, address, type code) of a contiguous array of token numbers."""
+    at = _cuda(tokens, "tokens")
+    code = _INDEX.get(tokens.dtype)
+    if code is None:
+        raise TypeError(f"tokens must be int32 or int64, got {tokens.dtype}")
+    if index is not None and at != index:
+        raise ValueError(f"tokens is on {tokens.device}, expected cuda:{index}")
+    if not tokens.is_contiguous():
+        raise ValueError("tokens must be contiguous")
+    return at, tokens.data_ptr(), code
+
+
+def embedding_fwd(tokens, table, *, scale=1.0, out_dtype=None, y=None):
+    """y = table[tokens] * scale: tokens [...] int32 or int64, table [vocab, width]
+    f32 or bf16.  A token outside 0 .. vocab - 1 stands for padding and gives a row
+    of zeros.  Returns y [..., width] in out_dtype (default: the table's)."""
+    if table is not None and y is None:
+        got = (_marshal_module or _marshal()).embedding_fwd(
+            tokens, table, scale, _code(table.dtype if out_dtype is None else out_dtype, "out_dtype"))
+        if got is not None:
+            return _plain("ssd_embedding_fwd", got)
+    lib = load()
+    at = _cuda(table, "table")
+    if table.dim() != 2 or table.shape[0] > _INT_MAX:
+        raise ValueError(f"table has shape {tuple(table.shape)}, expected [vocab, width]")
+    _, tp, tc = _tokens(tokens, at)
+    out_dtype = table.dtype if out_dtype is None else out_dtype
+    y, yp = _out(y, "y", out_dtype, at, table.device, tuple(tokens.shape) + (table.shape[1],))
+    _call(at, lib.ssd_embedding_fwd, tp, tc, _full(table, "table", table.dtype, at, table.shape),
+          _code(table.dtype, "table"), _code(out_dtype, "out_dtype"), tokens.numel(), table.shape[0],
+          table.shape[1], scale, yp)
+    return y
+
+
+def embedding_bwd_workspace_bytes(tokens, vocab, width, device=None):
+    """Workspace bytes of embedding_bwd on the device (tokens: their number)."""
+    return _size(_index(device), load().ssd_embedding_bwd_workspace_bytes, tokens, vocab, width)
+
+
+def embedding_bwd(dy, tokens, vocab, *, scale=1.0, dtype=None, dtable=None, workspace=None):
+    """The table's gradient of embedding_fwd: dy [..., width] f32 or bf16, tokens
+    as given to it.  Returns dtable [vocab, width] in `dtype` (default: dy's), all
+    rows written: zeros for those that no token names.  Equal calls give equal bits."""
+    if dy is not None and dtable is None and workspace is None:
+        got = (_marshal_module or _marshal()).embedding_bwd(
+            dy, tokens, vocab, scale, _code(dy.dtype if dtype is None else dtype, "dtype"))
+        if got is not None:
+            return _plain("ssd_embedding_bwd", got)
+    lib = load()
+    at, dev = _cuda(dy, "dy"), dy.device
+    yc = _code(dy.dtype, "dy")
+    dtype = dy.dtype if dtype is None else dtype
+    oc = _code(dtype, "dtype")
+    _, tp, tc = _tokens(tokens, at)
+    width, count = dy.shape[-1], tokens.numel()
+    yp, ys = _rows(dy, "dy", dy.dtype, at, tuple(tokens.shape) + (width,))
+    if not 0 < vocab <= _INT_MAX:
+        raise ValueError(f"vocab must be positive and an int, got {vocab}")
+    need = _size(at, lib.ssd_embedding_bwd_workspace_bytes, count, vocab, width)
+    dtable, op = _out(dtable, "dtable", dtype, at, dev, (vocab, width))
+    _keep, wp, wb = _scratch(workspace, need, dev)
+    _call(at, lib.ssd_embedding_bwd, yp, tp, tc, yc, oc, count, vocab, width, ys, scale, op, wp, wb)
+    return dtable
 
 
 # -------------------------------------------------------------------- product
