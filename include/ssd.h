@@ -704,18 +704,29 @@ size_t ssd_embedding_bwd_workspace_bytes(long long count, int vocab, int width);
  *                ssd_delta_scan_bwd needs of the forward call.  The state before a sequence's
  *                tokens 0, 64, 128, ... lies at first / 64 + s + 0, 1, 2, ... (s: the
  *                sequence, first: its first token on the axis); other places are not written.
+ *   workspace    ssd_delta_scan_workspace_bytes() bytes, 256-byte aligned (may be NULL
+ *                when that is 0); no initialisation needed.
+ * bf16 inputs with dstate <= 128, dstate and headdim multiples of 8 and tokens that start on
+ * 16-byte boundaries run on the tensor cores, in chunks of 64 tokens, with factors that are
+ * no bf16 values held to 16 bits (states are about 7e-6 of their size off); others in fp32
+ * multiply-adds, token by token.
  * Requirements: dstate <= 256, headdim <= 2^14, nheads <= 2^16 a multiple of ngroups.
  * SSD_ERR_INVALID_ARG for null or misaligned pointers, sizes <= 0 (length 0 is allowed),
  * strides below a token's values, bad offsets or a scale that is not finite;
  * SSD_ERR_UNSUPPORTED for other types and sizes beyond those, or beyond a grid (2^31
- * runs of 64 tokens by heads by 32 rows). */
+ * runs of 64 tokens by heads by 32 rows); SSD_ERR_WORKSPACE.  The tensor-core kernels' waits
+ * are bounded in time; one that runs out is reported by ssd_last_device_error(). */
 ssd_status ssd_delta_scan_fwd(const void *q, const void *k, const void *v, const float *g,
                               const float *beta, ssd_dtype dtype, int nseq, int length,
                               const int *cu_seqlens_host, const int *cu_seqlens_dev, int nheads,
                               int headdim, int dstate, int ngroups, long long q_stride,
                               long long k_stride, long long v_stride, float scale,
                               const float *init_state, void *o, long long o_stride,
-                              float *final_state, float *checkpoints, cudaStream_t stream);
+                              float *final_state, float *checkpoints, void *workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
+/* 0 where the call needs none; (size_t)-1 for invalid sizes. */
+size_t ssd_delta_scan_workspace_bytes(ssd_dtype dtype, long long tokens, int nseq, int nheads,
+                                      int headdim, int dstate, int ngroups);
 
 /* Gradients of ssd_delta_scan_fwd.  With L_t the gradient of S_t, which begins with dfinal
  * behind a sequence's last token:
@@ -765,7 +776,7 @@ ssd_status ssd_last_device_error(void);
 
 /* Test hook for the bounded device-side waits (the pages have no
  * counterpart).  Every later launch of the tensor-core scan, of the gated
- * recurrence and of the tensor-core product reads the setting; it is process-wide
+ * recurrence, of the tensor-core product and of the tensor-core delta rule reads the setting; it is process-wide
  * and not synchronised with calls in flight on other host threads.
  *   fault          SSD_FAULT_NONE: normal operation.  SSD_FAULT_WITHHOLD_SIGNAL:
  *                  in the CTAs of each sequence's first segment, the barrier

@@ -72,6 +72,7 @@ from .delta_ops import (  # noqa: F401
     delta_scan_bwd_workspace_bytes,
     delta_scan_checkpoints,
     delta_scan_fwd,
+    delta_scan_workspace_bytes,
     delta_state_update,
 )
 from .layer_ops import (  # noqa: F401

@@ -51,6 +51,7 @@ EXPORTED_SYMBOLS = (
     "ssd_embedding_bwd",
     "ssd_embedding_bwd_workspace_bytes",
     "ssd_delta_scan_fwd",
+    "ssd_delta_scan_workspace_bytes",
     "ssd_delta_scan_bwd",
     "ssd_delta_scan_bwd_workspace_bytes",
     "ssd_delta_state_update",
@@ -177,7 +178,8 @@ def load():
                                   _sz, _vp],
             "ssd_embedding_bwd_workspace_bytes": [ll, _int, _int],
             "ssd_delta_scan_fwd": [_vp] * 5 + [_int] * 3 + [_vp, _vp] + [_int] * 4 +
-                                  [ll, ll, ll, f32, _vp, _vp, ll, _vp, _vp, _vp],
+                                  [ll, ll, ll, f32, _vp, _vp, ll, _vp, _vp, _vp, _sz, _vp],
+            "ssd_delta_scan_workspace_bytes": [_int, ll] + [_int] * 5,
             "ssd_delta_scan_bwd": [_vp] * 6 + [_int] * 3 + [_vp, _vp] + [_int] * 4 +
                                   [ll, ll, ll, ll, f32, _vp, _vp, _vp, ll, _vp, ll, _vp, ll, _vp,
                                    _vp, _vp, _vp, _sz, _vp],

@@ -576,19 +576,34 @@ ssd_status ssd_embedding_bwd(const void *dy, const void *tokens, ssd_index token
     return launched(ssd_launch_embedding_bwd(a, workspace, ssd_sm_count(), stream));
 }
 
-size_t ssd_delta_scan_bwd_workspace_bytes(ssd_dtype dtype, long long tokens, int nseq, int nheads,
-                                          int headdim, int dstate, int ngroups) {
+namespace {
+bool delta_sizes(ssd_dtype dtype, long long tokens, int nseq, int nheads, int headdim, int dstate, int ngroups,
+                 SsdDelta *d) {
     if (check_delta(dtype, nheads, headdim, dstate, ngroups) != SSD_OK || tokens < 0 ||
         tokens >= (1ll << 31) - 2048 || nseq <= 0 || !delta_handled(tokens, nseq, nheads, headdim))
-        return kBad;
+        return false;
+    d->bf16 = dtype == SSD_BF16;
+    d->tokens = tokens;
+    d->nseq = nseq;
+    d->heads = nheads;
+    d->groups = ngroups;
+    d->p = headdim;
+    d->n = dstate;
+    return true;
+}
+}  // namespace
+
+size_t ssd_delta_scan_workspace_bytes(ssd_dtype dtype, long long tokens, int nseq, int nheads, int headdim,
+                                      int dstate, int ngroups) {
     SsdDelta d{};
-    d.bf16 = dtype == SSD_BF16;
-    d.tokens = tokens;
-    d.nseq = nseq;
-    d.heads = nheads;
-    d.groups = ngroups;
-    d.p = headdim;
-    d.n = dstate;
+    if (!delta_sizes(dtype, tokens, nseq, nheads, headdim, dstate, ngroups, &d)) return kBad;
+    return ssd_delta_tc_workspace(d);
+}
+
+size_t ssd_delta_scan_bwd_workspace_bytes(ssd_dtype dtype, long long tokens, int nseq, int nheads,
+                                          int headdim, int dstate, int ngroups) {
+    SsdDelta d{};
+    if (!delta_sizes(dtype, tokens, nseq, nheads, headdim, dstate, ngroups, &d)) return kBad;
     return tokens ? ssd_delta_bwd_simt_workspace(d) : 0;
 }
 
@@ -598,20 +613,25 @@ ssd_status ssd_delta_scan_fwd(const void *q, const void *k, const void *v, const
                               int headdim, int dstate, int ngroups, long long q_stride,
                               long long k_stride, long long v_stride, float scale,
                               const float *init_state, void *o, long long o_stride,
-                              float *final_state, float *checkpoints, cudaStream_t stream) {
+                              float *final_state, float *checkpoints, void *workspace,
+                              size_t workspace_bytes, cudaStream_t stream) {
     SsdDeltaFwd a{};
-    const ssd_status st =
+    ssd_status st =
         delta_input(q, k, v, g, beta, dtype, nseq, length, cu_seqlens_host, cu_seqlens_dev, nheads,
                     headdim, dstate, ngroups, q_stride, k_stride, v_stride, scale, &a.in);
     if (st != SSD_OK) return st;
     if ((a.in.tokens > 0 && !array(o, size_of(dtype))) || o_stride < (long long)nheads * headdim ||
         !maybe(init_state, 4) || !maybe(final_state, 4) || !maybe(checkpoints, 4))
         return SSD_ERR_INVALID_ARG;
+    st = check_workspace(workspace, workspace_bytes, ssd_delta_tc_workspace(a.in), 256);
+    if (st != SSD_OK) return st;
     a.init = init_state;
     a.o = o;
     a.o_stride = o_stride;
     a.final_state = final_state;
     a.checkpoints = checkpoints;
+    if (ssd_delta_tc_handles(a.in))
+        return launched(ssd_launch_delta_fwd_tc(a, workspace, ssd_device_error_word(), stream));
     return launched(ssd_launch_delta_fwd_simt(a, ssd_sm_count(), stream));
 }
 

@@ -1,0 +1,91 @@
+// What the tensor-core kernels of the gated delta rule share: the chunk's record in the
+// workspace, its layout in shared memory, and small device helpers.
+#pragma once
+
+#include "launch.h"
+#include "ptx.cuh"
+
+namespace ssddelta {
+
+using namespace ssdptx;
+
+constexpr int kC = kSsdDeltaChunk;          // tokens a chunk
+static_assert(kC == 64, "a chunk's matrices are one 128-byte-swizzled panel wide");
+constexpr uint32_t kPanel = 64 * 128;       // 64 rows of 64 bf16 values
+
+// A chunk's record, for every head: the matrices T diag(beta) and P, each in two bf16
+// parts and each an image of a 128-byte-swizzled panel (row: the later token), then for
+// every token the decay from the chunk's start up to it and from it to the chunk's end.
+constexpr uint32_t kRecT = 0, kRecP = 2 * kPanel, kRecGates = 4 * kPanel;
+constexpr uint32_t kRecord = kRecGates + 2 * kC * 4;
+
+// Byte of element (row, col) in a panel.
+__device__ __forceinline__ uint32_t panel_at(uint32_t row, uint32_t col) {
+    return (row >> 3) * 1024u + (row & 7u) * 128u + ((((col >> 3) ^ row) & 7u) << 4) + (col & 7u) * 2u;
+}
+
+// One lane of the warp, chosen so that what it issues needs no reconvergence: a thread picked
+// by its lane number issues a tcgen05.mma every 45 to 60 cycles, one elected so as often as
+// the tensor core takes them (N = 64: 32 cycles).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// Two values as bf16 pairs: the rounded ones and what rounding left.
+struct Split {
+    uint32_t hi, lo;
+};
+__device__ __forceinline__ Split split2(float a, float b) {
+    Split s;
+    s.hi = pack_bf16x2(a, b);
+    s.lo = pack_bf16x2(a - __uint_as_float(s.hi << 16), b - __uint_as_float(s.hi & 0xffff0000u));
+    return s;
+}
+
+// A bounded wait.  After any wait of the CTA has run out, every later one returns false at
+// once; the roles then leave their loops, and the CTA lets its copies and products in
+// flight complete before it ends.
+struct Waiter {
+    volatile int *abort;
+    unsigned *err;
+    unsigned long long limit;
+    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+        if (*abort) return false;
+        if (mbar_wait(bar, parity, limit)) return true;
+        *abort = 1;
+        ssd_report(err, SSD_DEVERR_TIMEOUT);
+        return false;
+    }
+    // of a whole warp
+    __device__ __forceinline__ bool warp(uint32_t bar, uint32_t parity) const {
+        return __all_sync(0xffffffffu, (*this)(bar, parity));
+    }
+};
+
+// Which chunk a slot of the kept states (ssd_delta_slot) stands for.
+struct ChunkAt {
+    long long first;    // the sequence's first token
+    int seq, len, chunk;
+    bool live;
+};
+__device__ __forceinline__ ChunkAt chunk_at(const SsdDelta &d, long long slot) {
+    int lo = 0, hi = d.nseq;        // the last sequence whose first slot is at or before it
+    while (hi - lo > 1) {
+        const int mid = lo + (hi - lo) / 2;
+        const long long first = d.cu ? d.cu[mid] : (long long)mid * d.length;
+        if (ssd_delta_slot(first, mid, 0) <= slot) lo = mid;
+        else hi = mid;
+    }
+    ChunkAt c;
+    c.seq = lo;
+    c.first = d.cu ? d.cu[lo] : (long long)lo * d.length;
+    c.len = d.cu ? d.cu[lo + 1] - d.cu[lo] : d.length;
+    const long long chunk = slot - ssd_delta_slot(c.first, lo, 0);
+    c.chunk = (int)chunk;
+    c.live = chunk * kC < c.len;
+    return c;
+}
+
+}  // namespace ssddelta

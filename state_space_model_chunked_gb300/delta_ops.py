@@ -67,9 +67,15 @@ def delta_scan_checkpoints(tokens, nseq):
     return tokens // DELTA_SCAN_CHECKPOINT + nseq
 
 
+def delta_scan_workspace_bytes(dtype, tokens, nseq, heads, headdim, dstate, groups, device=None):
+    """Workspace bytes of delta_scan_fwd on the device."""
+    return _size(_index(device), load().ssd_delta_scan_workspace_bytes, _code(dtype, "dtype"), tokens,
+                 nseq, heads, headdim, dstate, groups)
+
+
 def delta_scan_fwd(q, k, v, g, beta, init_state=None, *, scale=None, cu_seqlens=None,
                    cu_seqlens_dev=None, o=None, final_state=None, return_final=True,
-                   checkpoints=None, return_checkpoints=False):
+                   checkpoints=None, return_checkpoints=False, workspace=None):
     """Gated delta rule, for every head with its state S [headdim, dstate]:
     S' = exp(g_t) S_{t-1}, u_t = beta_t (v_t - S' k_t), S_t = S' + u_t k_t^T,
     o_t = scale S_t q_t (scale: dstate^-0.5 by default).
@@ -97,12 +103,15 @@ def delta_scan_fwd(q, k, v, g, beta, init_state=None, *, scale=None, cu_seqlens=
     kept = (delta_scan_checkpoints(tokens, nseq),) + states[1:]
     if checkpoints is None and return_checkpoints:
         checkpoints = torch.empty(kept, dtype=_F32, device=dev)
+    need = _size(at, lib.ssd_delta_scan_workspace_bytes, code, tokens, nseq, heads, headdim, dstate,
+                 groups)
+    _keep, wp, wb = _scratch(workspace, need, dev)
     _call(at, lib.ssd_delta_scan_fwd, qp, kp, vp, _full(g, "g", _F32, at, lead + (heads,)),
           _full(beta, "beta", _F32, at, lead + (heads,)), code, nseq, length, cu_ptr, cu_dev, heads,
           headdim, dstate, groups, qs, ks, vs, _scale(scale, dstate),
           _full(init_state, "init_state", _F32, at, states), op, os_,
           _full(final_state, "final_state", _F32, at, states),
-          _full(checkpoints, "checkpoints", _F32, at, kept))
+          _full(checkpoints, "checkpoints", _F32, at, kept), wp, wb)
     return (o, final_state, checkpoints) if return_checkpoints else (o, final_state)
 
 

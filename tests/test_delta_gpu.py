@@ -49,7 +49,8 @@ def batched(x, nseq):
 SHAPES = [  # tokens a sequence, sequences, groups, heads, headdim, dstate
     (1, 1, 1, 1, 1, 1), (3, 2, 1, 2, 5, 7), (64, 1, 2, 4, 16, 32), (65, 2, 1, 1, 64, 64), (130, 1, 2, 2, 128, 128),
     (127, 3, 2, 4, 128, 64), (200, 2, 1, 3, 64, 128), (300, 1, 1, 1, 40, 200), (63, 1, 1, 2, 130, 20), (257, 1, 1, 2, 33, 256),
-    (192, 2, 1, 2, 96, 112), (577, 1, 1, 1, 128, 128)]
+    (192, 2, 1, 2, 96, 112), (577, 1, 1, 1, 128, 128),
+    (100, 1, 1, 2, 136, 8), (129, 1, 2, 2, 256, 72), (2, 3, 1, 1, 8, 128)]
 
 
 @pytest.mark.parametrize("length,nseq,groups,heads,p,n", SHAPES)
