@@ -37,21 +37,27 @@ __device__ __forceinline__ bool elect_one() {
 struct Split {
     uint32_t hi, lo;
 };
+__device__ __forceinline__ uint32_t rest2(float a, float b, uint32_t hi) {
+    const float2 l = ffma2(make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)),
+                           make_float2(-1.f, -1.f), make_float2(a, b));
+    return pack_bf16x2(l.x, l.y);
+}
 __device__ __forceinline__ Split split2(float a, float b) {
     Split s;
     s.hi = pack_bf16x2(a, b);
-    s.lo = pack_bf16x2(a - __uint_as_float(s.hi << 16), b - __uint_as_float(s.hi & 0xffff0000u));
+    s.lo = rest2(a, b, s.hi);
     return s;
 }
 
-// A bounded wait.  After any wait of the CTA has run out, every later one returns false at
-// once; the roles then leave their loops, and the CTA lets its copies and products in
+// A bounded wait.  After any wait of the CTA has run out, every later one that would have
+// to wait returns false at once; the roles then leave their loops, and the CTA lets its copies and products in
 // flight complete before it ends.
 struct Waiter {
     volatile int *abort;
     unsigned *err;
     unsigned long long limit;
     __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+        if (mbar_try_wait(bar, parity)) return true;
         if (*abort) return false;
         if (mbar_wait(bar, parity, limit)) return true;
         *abort = 1;
