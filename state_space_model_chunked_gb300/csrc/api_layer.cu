@@ -631,7 +631,7 @@ ssd_status ssd_delta_scan_fwd(const void *q, const void *k, const void *v, const
     a.final_state = final_state;
     a.checkpoints = checkpoints;
     if (ssd_delta_tc_handles(a.in))
-        return launched(ssd_launch_delta_fwd_tc(a, workspace, ssd_device_error_word(), stream));
+        return launched(ssd_launch_delta_fwd_tc(a, workspace, ssd_sm_count(), ssd_device_error_word(), stream));
     return launched(ssd_launch_delta_fwd_simt(a, ssd_sm_count(), stream));
 }
 

@@ -27,28 +27,32 @@ namespace {
 using namespace ssddelta;
 
 // ------------------------------------------------------------- chunk matrices
-// One CTA a chunk and key group, all of the group's heads after each other.  The 64 queries
+// One CTA a chunk and key group, the group's heads after each other (or, where that would
+// be few CTAs, a share of them).  The 64 queries
 // over the 64 keys, times the keys, are one product of M = 128, N = 64: a thread's lane is
 // then a row of Q K^T (threads 0 .. 63) or of K K^T (64 .. 127).  The triangle is inverted
-// in fp32: blocks of 16 by substitution, a thread a column, then twice
+// to fp32's precision: blocks of 16 by substitution, a thread a column, then twice
 //     (T11  0; T21  T22),   T21 = -T22 (A21 T11)
-// for blocks of 32 and of 64 (substituting all 64 rows in one thread took five times as
-// long: 2016 dependent steps, and more code than the instruction cache holds).
+// for blocks of 32 (in fp32) and of 64 (TF32 products of two parts each, 22 bits).
 constexpr int kPrepThreads = 128;
 constexpr int kTw = 36;         // floats a row of a 32 x 32 block
+constexpr int kAw = 68;         // and a column of A
 struct PrepSmem {
-    // at 0: Q over K by panels, then the images
-    static constexpr uint32_t kA = 4 * kPanel;              // A's columns, fp32 (W above the diagonal)
-    static constexpr uint32_t kRows = kA + kC * kC * 4;     // T11 and T22 by rows
-    static constexpr uint32_t kCols = kRows + 2 * 32 * kTw * 4;     // and by columns
-    static constexpr uint32_t kSums = kCols + 2 * 32 * kTw * 4;     // G in two floats, beta, decay to token 31
+    // At 0 the tiles, Q over K by panels; then A by columns (and W above its diagonal
+    // blocks), and in its place at last T's images; P's images behind them.
+    static constexpr uint32_t kP = kC * kAw * 4;
+    static constexpr uint32_t kRows = kP + 2 * kPanel;              // T11 and T22 by rows
+    static constexpr uint32_t kSums = kRows + 2 * 32 * kTw * 4;     // of g, beta, decay to token 31
     static constexpr uint32_t kBars = kSums + 4 * kC * 4;
     static constexpr uint32_t kBytes = kBars + 64;
 };
+static_assert(PrepSmem::kP % 1024 == 0 && PrepSmem::kRows >= 4 * kPanel, "images and tiles");
 
 struct Prep {
     SsdDelta d;
     uint8_t *records;
+    int split;          // CTAs that share a group's heads
+    bool least_beta;
     unsigned *err;
 };
 
@@ -60,21 +64,61 @@ __device__ __forceinline__ float2 add_two(float2 a, float2 b) {
     return make_float2(hi, e - (hi - s));
 }
 
-// (1 + A)^-1 of `columns` (A[r][c] at 64 c + r), all 128 threads: its diagonal blocks of 32
-// to `rows` and `cols`, and rows 32 + r0, + 1 by columns c0 .. c0 + 3 of the block below.
-__device__ __forceinline__ void invert(float *columns, float *rows, float *cols, int r0, int c0, float (&below)[2][4]) {
+// D += A B for tiles of 16 x 8 and 8 x 8, each in two TF32 parts, without the product of
+// both second ones.
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+template <int kCount>
+__device__ __forceinline__ void split_tf32(const float (&x)[kCount], uint32_t (&hi)[kCount], uint32_t (&lo)[kCount]) {
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) {
+        asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi[i]) : "f"(x[i]));
+        lo[i] = __float_as_uint(x[i] - __uint_as_float(hi[i]));
+    }
+}
+// d = a b for the warp's 16 x 16 of 32 x 32 matrices, over k from 8 k0 to 8 k1; a(r, k), b(k, c).
+template <typename A, typename B>
+__device__ __forceinline__ void product_tf32(float (&d)[2][4], int m0, int n0, int k0, int k1, A a, B b) {
+    const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[j][i] = 0.f;
+#pragma unroll 2
+    for (int k = 8 * k0; k < 8 * k1; k += 8) {
+        const float x[4] = {a(m0 + g, k + t), a(m0 + g + 8, k + t), a(m0 + g, k + t + 4), a(m0 + g + 8, k + t + 4)};
+        uint32_t ah[4], al[4];
+        split_tf32(x, ah, al);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float y[2] = {b(k + t, n0 + 8 * j + g), b(k + t + 4, n0 + 8 * j + g)};
+            uint32_t bh[2], bl[2];
+            split_tf32(y, bh, bl);
+            mma_tf32(d[j], al, bh);
+            mma_tf32(d[j], ah, bl);
+            mma_tf32(d[j], ah, bh);
+        }
+    }
+}
+
+// (1 + A)^-1 of `columns` (A[r][c] at kAw c + r), by all 128 threads: its diagonal blocks of
+// 32 to `rows`, and of the block below the warp's 16 x 16 (rows m0, columns n0 of it).
+__device__ __forceinline__ void invert(float *columns, float *rows, int m0, int n0, float (&below)[2][4]) {
     const int t = threadIdx.x;
     if (t < 64) {       // blocks of 16
         const int b = t >> 4, c = t & 15;
         float acc[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-        float *const row = rows + (b >> 1) * 32 * kTw, *const col = cols + (b >> 1) * 32 * kTw;
-        const int off = (b & 1) * 16;
+        float *const row = rows + ((b >> 1) * 32 + (b & 1) * 16) * kTw + (b & 1) * 16 + c;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const float x = i == c ? 1.f : -acc[i];
-            const float4 *a = reinterpret_cast<const float4 *>(columns + (16 * b + i) * kC + 16 * b);
+            const float4 *a = reinterpret_cast<const float4 *>(columns + (16 * b + i) * kAw + 16 * b);
 #pragma unroll
             for (int v = (i + 1) / 4; v < 4; ++v) {
                 const float4 y = a[v];
@@ -83,91 +127,61 @@ __device__ __forceinline__ void invert(float *columns, float *rows, float *cols,
                 if (4 * v + 2 > i) acc[4 * v + 2] += y.z * x;
                 acc[4 * v + 3] += y.w * x;
             }
-            row[(off + i) * kTw + off + c] = x;
-            col[(off + c) * kTw + off + i] = x;
+            row[i * kTw] = x;
         }
     } else {            // above them nothing
-        for (int i = t - 64; i < 2 * 256; i += 64) {
-            const int b = i >> 8, r = (i >> 4) & 15, c = i & 15;
-            rows[b * 32 * kTw + r * kTw + 16 + c] = 0.f;
-            cols[b * 32 * kTw + (16 + c) * kTw + r] = 0.f;
+        for (int i = t - 64; i < 2 * 64; i += 64) {
+            const int b = i >> 6, r = (i >> 2) & 15, c = (i & 3) * 4;
+            *reinterpret_cast<float4 *>(rows + (b * 32 + r) * kTw + 16 + c) = make_float4(0.f, 0.f, 0.f, 0.f);
         }
     }
     __syncthreads();
     {                   // blocks of 32: 64 threads each, a row's four columns
         const int b = t >> 6, r = (t >> 2) & 15, c = (t & 3) * 4;
-        float *const row = rows + b * 32 * kTw, *const col = cols + b * 32 * kTw;
-        float *const w = columns + (32 + r) * kC + 16 * b;      // a row of W
+        float *const row = rows + b * 32 * kTw;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-            const float a = columns[(32 * b + k) * kC + 32 * b + 16 + r];
+            const float a = columns[(32 * b + k) * kAw + 32 * b + 16 + r];
             const float4 y = *reinterpret_cast<const float4 *>(row + k * kTw + c);
             x.x += a * y.x;
             x.y += a * y.y;
             x.z += a * y.z;
             x.w += a * y.w;
         }
-        *reinterpret_cast<float4 *>(w + c) = x;
+        *reinterpret_cast<float4 *>(columns + (32 + r) * kAw + 16 * b + c) = x;     // W
         __syncthreads();
         float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-            const float a = -row[(16 + r) * kTw + 16 + k];
-            const float4 y = *reinterpret_cast<const float4 *>(columns + (32 + k) * kC + 16 * b + c);
-            z.x += a * y.x;
-            z.y += a * y.y;
-            z.z += a * y.z;
-            z.w += a * y.w;
+            const float a = row[(16 + r) * kTw + 16 + k];
+            const float4 y = *reinterpret_cast<const float4 *>(columns + (32 + k) * kAw + 16 * b + c);
+            z.x -= a * y.x;
+            z.y -= a * y.y;
+            z.z -= a * y.z;
+            z.w -= a * y.w;
         }
         *reinterpret_cast<float4 *>(row + (16 + r) * kTw + c) = z;
-        col[c * kTw + 16 + r] = z.x;
-        col[(c + 1) * kTw + 16 + r] = z.y;
-        col[(c + 2) * kTw + 16 + r] = z.z;
-        col[(c + 3) * kTw + 16 + r] = z.w;
     }
     __syncthreads();
-    // the block of 32 below: two rows by four columns a thread
-    float w[2][4] = {};
-#pragma unroll 8
-    for (int k = 0; k < 32; ++k) {
-        const float2 a = *reinterpret_cast<const float2 *>(columns + k * kC + 32 + r0);
-        const float4 y = *reinterpret_cast<const float4 *>(rows + k * kTw + c0);
-        w[0][0] += a.x * y.x, w[0][1] += a.x * y.y, w[0][2] += a.x * y.z, w[0][3] += a.x * y.w;
-        w[1][0] += a.y * y.x, w[1][1] += a.y * y.y, w[1][2] += a.y * y.z, w[1][3] += a.y * y.w;
-    }
+    // the block of 32 below (T11's columns from 16 on begin at row 16, T22's first 16 rows
+    // end at column 16)
+    const int g = (t & 31) >> 2, u = t & 3;
+    product_tf32(below, m0, n0, n0 / 8, 4, [&](int r, int k) { return columns[k * kAw + 32 + r]; },
+                 [&](int k, int c) { return rows[k * kTw + c]; });
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-        *reinterpret_cast<float4 *>(columns + (32 + r0 + j) * kC + c0) = make_float4(w[j][0], w[j][1], w[j][2], w[j][3]);
+    for (int j = 0; j < 2; ++j) {
+        float *const w = columns + (32 + m0 + g) * kAw + n0 + 8 * j + 2 * u;
+        *reinterpret_cast<float2 *>(w) = make_float2(below[j][0], below[j][1]);
+        *reinterpret_cast<float2 *>(w + 8 * kAw) = make_float2(below[j][2], below[j][3]);
+    }
     __syncthreads();
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) below[j][i] = 0.f;
-#pragma unroll 8
-    for (int k = 0; k < 32; ++k) {
-        const float2 a = *reinterpret_cast<const float2 *>(cols + (32 + k) * kTw + r0);
-        const float4 y = *reinterpret_cast<const float4 *>(columns + (32 + k) * kC + c0);
-        below[0][0] -= a.x * y.x, below[0][1] -= a.x * y.y, below[0][2] -= a.x * y.z, below[0][3] -= a.x * y.w;
-        below[1][0] -= a.y * y.x, below[1][1] -= a.y * y.y, below[1][2] -= a.y * y.z, below[1][3] -= a.y * y.w;
-    }
-}
-
-// Eight values of a row as the two parts' vectors in the images at `to`.
-__device__ __forceinline__ void put_parts(uint8_t *image, uint32_t at, const float *v) {
-    uint32_t hi[4], lo[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const Split s = split2(v[2 * i], v[2 * i + 1]);
-        hi[i] = s.hi;
-        lo[i] = s.lo;
-    }
-    *reinterpret_cast<uint4 *>(image + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4 *>(image + kPanel + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    product_tf32(below, m0, n0, 0, (m0 + 16) / 8, [&](int r, int k) { return rows[(32 + r) * kTw + k]; },
+                 [&](int k, int c) { return -columns[(32 + k) * kAw + c]; });
 }
 
 template <int kPanels>
-__global__ void __launch_bounds__(kPrepThreads)
+__global__ void __launch_bounds__(kPrepThreads, 5)
 delta_chunk_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK, const Prep a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const SsdDelta &d = a.d;
@@ -177,8 +191,8 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
         if (threadIdx.x == 0) ssd_report(a.err, SSD_DEVERR_SMEM_ALIGN);
         return;
     }
-    const long long slot = blockIdx.x / d.groups;
-    const int group = (int)(blockIdx.x % d.groups);
+    const int share = (int)(blockIdx.x % a.split), group = (int)(blockIdx.x / a.split % d.groups);
+    const long long slot = blockIdx.x / a.split / d.groups;
     const ChunkAt at = chunk_at(d, slot);
     if (!at.live) return;
     const int valid = min(kC, at.len - at.chunk * kC);
@@ -206,6 +220,12 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
             tma_load_3d(base + p * 2 * kPanel + kPanel, &mapK, full, 64 * p, group, (int)token);
         }
     }
+    const int all = d.heads / d.groups, row = threadIdx.x & 63;
+    const int head0 = group * all + all * share / a.split, wide = group * all + all * (share + 1) / a.split - head0;
+    // the first head's gates on their way beside the copies
+    const bool on = warp < 2 && row < valid;
+    const size_t gate0 = (size_t)(token + row) * d.heads + head0;
+    float g = on ? d.g[gate0] : 0.f, beta = on ? d.beta[gate0] : 0.f;
     // (waits for the CTA's own copies and product)
     if (!mbar_wait(full, 0, kSsdDefaultWaitNs)) ssd_report(a.err, SSD_DEVERR_TIMEOUT);
     if (warp == 1 && elect_one()) {
@@ -222,118 +242,134 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
     __syncwarp();
     if (!mbar_wait(done, 0, kSsdDefaultWaitNs)) ssd_report(a.err, SSD_DEVERR_TIMEOUT);
     tc_fence_after();
-    float *const sum_hi = reinterpret_cast<float *>(smem + PrepSmem::kSums), *const sum_lo = sum_hi + kC;
-    float *const betas = sum_lo + kC, *const to_half = betas + kC;
-    float *const columns = reinterpret_cast<float *>(smem + PrepSmem::kA);
+    float2 *const sums = reinterpret_cast<float2 *>(smem + PrepSmem::kSums);
+    float *const betas = reinterpret_cast<float *>(sums + kC), *const to_half = betas + kC;
+    float *const columns = reinterpret_cast<float *>(smem);
     float *const rows = reinterpret_cast<float *>(smem + PrepSmem::kRows);
-    float *const cols = reinterpret_cast<float *>(smem + PrepSmem::kCols);
-    const int wide = d.heads / d.groups, row = threadIdx.x & 63;
     const bool keys = warp >= 2;
+    const int upper = warp & 1;         // which half of the 64 tokens the warp's rows are
     for (int h = 0; h < wide; ++h) {
-        const int head = group * wide + h;
-        uint8_t *const record = a.records + ((size_t)slot * d.heads + head) * kRecord;
-        // sums of g in two floats: a later token's decay is the difference of two of them,
-        // which an early strong decay must not round away
+        uint8_t *const record = a.records + ((size_t)slot * d.heads + head0 + h) * kRecord;
+        // The images of the head in front have been read, its sums used.  Each half's sums of
+        // log2(e) g are held in two floats: a later token's decay is the difference of two of
+        // them, which an early strong decay must not round away.
+        if (threadIdx.x == 0 && h > 0) bulk_wait_read<0>();
+        __syncthreads();
+        float2 s = make_float2(0.f, 0.f);
         if (warp < 2) {
-            const bool on = row < valid;
-            const size_t i = (size_t)(token + row) * d.heads + head;
-            float g = on ? d.g[i] : 0.f;
+            constexpr float kLog2e = 1.4426950408889634f, kRest = 1.9259629911266175e-8f;
             g = g < -200.f ? -200.f : g;
-            float2 s = make_float2(g, 0.f);
+            s.x = g * kLog2e;
+            s.y = fmaf(g, kLog2e, -s.x) + g * kRest;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const float2 n = make_float2(__shfl_up_sync(0xffffffffu, s.x, o), __shfl_up_sync(0xffffffffu, s.y, o));
                 if (lane >= o) s = add_two(n, s);
             }
-            sum_hi[row] = s.x;
-            sum_lo[row] = s.y;
-            betas[row] = on ? d.beta[i] : 0.f;
-        }
-        // the images of the head in front have been read, its blocks used
-        if (threadIdx.x == 0 && h > 0) bulk_wait_read<0>();
-        __syncthreads();
-        const float2 half = make_float2(sum_hi[31], sum_lo[31]);
-        float2 mine = make_float2(sum_hi[row], sum_lo[row]);
-        if (row >= 32) mine = add_two(half, mine);
-        const float2 end = add_two(half, make_float2(sum_hi[63], sum_lo[63]));
-        // over the middle, decays are products: of the row's from it and the column's to it
-        const float from_half = row < 32 ? 0.f : __expf((mine.x - half.x) + (mine.y - half.y));
-        __syncthreads();
-        if (threadIdx.x < kC) {
-            float *gates = reinterpret_cast<float *>(record + kRecGates);
-            gates[row] = __expf(mine.x + mine.y);
-            gates[kC + row] = __expf((end.x - mine.x) + (end.y - mine.y));
-            if (row < 32) {
-                to_half[row] = __expf((half.x - mine.x) + (half.y - mine.y));
-            } else {
-                sum_hi[row] = mine.x;
-                sum_lo[row] = mine.y;
+            sums[row] = s;
+            if (a.least_beta && fabsf(beta) < kLeastBeta) beta = copysignf(kLeastBeta, beta);
+            betas[row] = beta;
+            if (h + 1 < wide) {
+                g = on ? d.g[gate0 + h + 1] : 0.f;
+                beta = on ? d.beta[gate0 + h + 1] : 0.f;
             }
         }
         __syncthreads();
-        const float factor = keys ? betas[row] : d.scale;
+        const float2 half = sums[31], rest = sums[63], mine = sums[row];
+        const float upto = mine.x + mine.y;
+        if (warp < 2) {
+            float *gates = reinterpret_cast<float *>(record + kRecGates);
+            const float2 whole = upper ? rest : half;
+            const float behind = (whole.x - mine.x) + (whole.y - mine.y);
+            gates[row] = ex2_approx(upper ? half.x + upto : upto);
+            gates[kGateW + row] = ex2_approx(upper ? behind : behind + rest.x);
+            gates[kGateBeta + row] = betas[row];
+            *reinterpret_cast<float2 *>(gates + kGateSums + 2 * row) = mine;
+            if (!upper) to_half[row] = ex2_approx(behind);
+        }
+        __syncthreads();
+        // rows behind the sequence's end stay empty
+        const int last = row < valid ? (keys ? row - 1 : row) : -1;
+        const float factor = keys ? betas[row] : d.scale, from_half = factor * ex2_approx(upto);
+        const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
 #pragma unroll 1
         for (int c0 = 0; c0 < kC; c0 += 16) {
             float v[16];
-            if (c0 > 16 && row < 32) {
+            if (!upper && c0 >= 32) {
+                if (keys) break;
 #pragma unroll
                 for (int j = 0; j < 16; ++j) v[j] = 0.f;
             } else {
                 uint32_t r[16];
-                tmem_ld16(tmem + ((uint32_t)(warp * 32) << 16) + c0, r);
-                const bool over = c0 < 32 && row >= 32;
-                float e[16];
+                tmem_ld16(lanes + c0, r);
+                if (upper && c0 < 32) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    e[j] = over ? from_half * to_half[c0 + j]
-                                : __expf((mine.x - sum_hi[c0 + j]) + (mine.y - sum_lo[c0 + j]));
+                    for (int j = 0; j < 16; j += 4) *reinterpret_cast<float4 *>(v + j) = *reinterpret_cast<const float4 *>(to_half + c0 + j);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] *= from_half;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        const float4 c = *reinterpret_cast<const float4 *>(sums + c0 + j);
+                        v[j] = factor * ex2_approx((mine.x - c.x) + (mine.y - c.y));
+                        v[j + 1] = factor * ex2_approx((mine.x - c.z) + (mine.y - c.w));
+                    }
+                }
                 tmem_ld_wait(r);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const bool in = row < valid && (keys ? c0 + j < row : c0 + j <= row);
-                    v[j] = in ? factor * e[j] * __uint_as_float(r[j]) : 0.f;
-                }
+                for (int j = 0; j < 16; ++j) v[j] = c0 + j <= last ? v[j] * __uint_as_float(r[j]) : 0.f;
             }
             if (keys) {
-                // (above the diagonal block the array is another's)
-                if (c0 < 32 || row >= 32) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) columns[(c0 + j) * kC + row] = v[j];
-                }
+                for (int j = 0; j < 16; ++j) columns[(c0 + j) * kAw + row] = v[j];
             } else {
-                put_parts(smem + kRecP, panel_at(row, c0), v);
-                put_parts(smem + kRecP, panel_at(row, c0 + 8), v + 8);
+                put_parts(smem + PrepSmem::kP, panel_at(row, c0), v);
+                put_parts(smem + PrepSmem::kP, panel_at(row, c0 + 8), v + 8);
             }
         }
         __syncthreads();
-        const int r0 = (threadIdx.x >> 3) * 2, c0 = (threadIdx.x & 7) * 4;
+        const int m0 = (warp >> 1) * 16, n0 = (warp & 1) * 16;
         float below[2][4];
-        invert(columns, rows, cols, r0, c0, below);
-        // T diag(beta)
+        invert(columns, rows, m0, n0, below);
+        __syncthreads();
+        // T diag(beta), in A's place
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const Split x = split2(below[j][0] * betas[c0], below[j][1] * betas[c0 + 1]);
-            const Split y = split2(below[j][2] * betas[c0 + 2], below[j][3] * betas[c0 + 3]);
-            const uint32_t to = kRecT + panel_at(32 + r0 + j, c0);
-            *reinterpret_cast<uint2 *>(smem + to) = make_uint2(x.hi, y.hi);
-            *reinterpret_cast<uint2 *>(smem + kPanel + to) = make_uint2(x.lo, y.lo);
+            const int c = n0 + 8 * j + 2 * (lane & 3), r = 32 + m0 + (lane >> 2);
+            const float2 be = *reinterpret_cast<const float2 *>(betas + c);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const Split x = split2(below[j][2 * i] * be.x, below[j][2 * i + 1] * be.y);
+                const uint32_t to = panel_at(r + 8 * i, c);
+                *reinterpret_cast<uint32_t *>(smem + to) = x.hi;
+                *reinterpret_cast<uint32_t *>(smem + kPanel + to) = x.lo;
+            }
         }
         for (int i = threadIdx.x; i < 64 * 4; i += kPrepThreads) {
-            const int r = i >> 2, c = (i & 3) * 8, b = r >> 5;
+            const int r = i >> 2, c = (i & 3) * 8, b = r & 32;
+            const float4 *from = reinterpret_cast<const float4 *>(rows + r * kTw + c);
+            const float4 *be = reinterpret_cast<const float4 *>(betas + b + c);
             float v[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = rows[(b * 32 + (r & 31)) * kTw + c + j] * betas[32 * b + c + j];
-            put_parts(smem + kRecT, panel_at(r, 32 * b + c), v);
+            for (int j = 0; j < 2; ++j) {
+                const float4 x = from[j], y = be[j];
+                v[4 * j] = x.x * y.x;
+                v[4 * j + 1] = x.y * y.y;
+                v[4 * j + 2] = x.z * y.z;
+                v[4 * j + 3] = x.w * y.w;
+            }
+            put_parts(smem, panel_at(r, b + c), v);
         }
         {
-            const uint32_t to = kRecT + panel_at(threadIdx.x >> 2, 32 + (threadIdx.x & 3) * 8);
+            const uint32_t to = panel_at(threadIdx.x >> 2, 32 + (threadIdx.x & 3) * 8);
             *reinterpret_cast<uint4 *>(smem + to) = make_uint4(0, 0, 0, 0);
             *reinterpret_cast<uint4 *>(smem + kPanel + to) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
         __syncthreads();
         if (threadIdx.x == 0) {
-            bulk_store(record, base, 4 * kPanel);
+            bulk_store(record + kRecT, base, 2 * kPanel);
+            bulk_store(record + kRecP, base + PrepSmem::kP, 2 * kPanel);
             bulk_commit();
         }
     }
@@ -678,15 +714,9 @@ delta_walk_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
             if (a.checkpoints) to_memory(a.checkpoints + ((size_t)(slot0 + c) * d.heads + head) * d.p * d.n, v);
         };
         const auto stage = [&](int c) { return smem + (c & 1) * Lay::kStage; };
-        // keys behind the sequence's end are another's, or nothing: zeros
         const auto clean = [&](int c) {
-            const int tokens = len - c * kC;
-            if (tokens >= kC) return;
-            uint4 *k = reinterpret_cast<uint4 *>(stage(c) + Lay::kK);
-            for (int i = threadIdx.x; i < kPanels * (kC - tokens) * 8; i += 32 * kChainWarps) {
-                const int panel = i / ((kC - tokens) * 8), at = i % ((kC - tokens) * 8);
-                k[panel * (kPanel / 16) + tokens * 8 + at] = make_uint4(0, 0, 0, 0);
-            }
+            if (len - c * kC >= kC) return;
+            clean_rows(stage(c) + Lay::kK, kPanel, kPanels, len - c * kC, threadIdx.x, 32 * kChainWarps);
             fence_proxy_async_smem();
         };
         bool on = wait.warp(bar(kFull), 0);
@@ -736,7 +766,7 @@ delta_walk_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
             tmem_st8(tq + kColRl + 8 * part, hi);
             ready(kRl);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) *reinterpret_cast<float4 *>(f + 4 * i) = gates[kC / 4 + i];
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<float4 *>(f + 4 * i) = gates[kGateW / 4 + i];
             if (!wait.warp(bar(kU), c & 1)) break;
             tc_fence_after();
             tmem_ld16(tq + kColX + 16 * part, r);
@@ -784,21 +814,28 @@ delta_walk_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// [tokens][heads][width] bf16 by boxes of `cols` values of one head and 64 tokens.
-bool make_map(CUtensorMap *m, const void *p, int width, int heads, long long tokens, long long stride, int cols,
-              bool swizzle) {
-    const auto enc = ssd_tensor_map_encoder();
-    if (!enc) return false;
-    const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)tokens};
-    const cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)stride * 2};
-    const cuuint32_t box[3] = {(cuuint32_t)cols, 1, (cuuint32_t)kC}, es[3] = {1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+template <int kPanels>
+cudaError_t launch_chunks_of(const SsdDelta &d, uint8_t *records, bool least_beta, int sms, unsigned *err,
+                             cudaStream_t stream) {
+    CUtensorMap q, k;
+    if (!make_map(&q, d.q, d.n, d.groups, d.tokens, d.q_stride, 64, true) ||
+        !make_map(&k, d.k, d.n, d.groups, d.tokens, d.k_stride, 64, true))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(delta_chunk_kernel<kPanels>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         PrepSmem::kBytes);
+    if (e != cudaSuccess) return e;
+    // CTAs for some rounds of five an SM
+    const long long ctas = ssd_delta_slots(d.tokens, d.nseq) * d.groups, want = 20ll * sms;
+    const int wide = d.heads / d.groups;
+    const int split = (int)(ctas >= want ? 1 : (want + ctas - 1) / ctas < wide ? (want + ctas - 1) / ctas : wide);
+    if (ctas * split >= (1ll << 31)) return cudaErrorInvalidValue;
+    delta_chunk_kernel<kPanels><<<(unsigned)(ctas * split), kPrepThreads, PrepSmem::kBytes, stream>>>(
+        q, k, Prep{d, records, split, least_beta, err});
+    return cudaGetLastError();
 }
 
 template <int kPanels>
-cudaError_t launch_fwd(const SsdDeltaFwd &f, void *ws, unsigned *err, cudaStream_t stream) {
+cudaError_t launch_fwd(const SsdDeltaFwd &f, void *ws, int sms, unsigned *err, cudaStream_t stream) {
     const SsdDelta &d = f.in;
     CUtensorMap q, k, v;
     if (!make_map(&q, d.q, d.n, d.groups, d.tokens, d.q_stride, 64, true) ||
@@ -807,13 +844,8 @@ cudaError_t launch_fwd(const SsdDeltaFwd &f, void *ws, unsigned *err, cudaStream
         return cudaErrorInvalidValue;
     const SsdDebug debug = ssd_debug_config();
     uint8_t *records = static_cast<uint8_t *>(ws);
-    const long long slots = ssd_delta_slots(d.tokens, d.nseq);
-    cudaError_t e = cudaFuncSetAttribute(delta_chunk_kernel<kPanels>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         PrepSmem::kBytes);
+    cudaError_t e = launch_chunks(d, records, false, sms, err, stream);
     if (e != cudaSuccess) return e;
-    delta_chunk_kernel<kPanels><<<(unsigned)(slots * d.groups), kPrepThreads, PrepSmem::kBytes, stream>>>(
-        q, k, Prep{d, records, err});
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     using Lay = WalkSmem<kPanels>;
     static_assert(Lay::kBytes <= 232448, "more than 227 KB of shared memory");
     e = cudaFuncSetAttribute(delta_walk_tc_kernel<kPanels>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kBytes);
@@ -827,6 +859,28 @@ cudaError_t launch_fwd(const SsdDeltaFwd &f, void *ws, unsigned *err, cudaStream
 }
 
 }  // namespace
+
+namespace ssddelta {
+
+bool make_map(CUtensorMap *m, const void *p, int width, int heads, long long tokens, long long stride, int cols,
+              bool swizzle) {
+    const auto enc = ssd_tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {(cuuint32_t)cols, 1, (cuuint32_t)kC}, es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t launch_chunks(const SsdDelta &d, uint8_t *records, bool least_beta, int sms, unsigned *err,
+                          cudaStream_t stream) {
+    return d.n <= 64 ? launch_chunks_of<1>(d, records, least_beta, sms, err, stream)
+                     : launch_chunks_of<2>(d, records, least_beta, sms, err, stream);
+}
+
+}  // namespace ssddelta
 
 // Types and sizes that these kernels take, and alignments: the copies' rows start on 16 bytes.
 bool ssd_delta_tc_sizes(const SsdDelta &d) {
@@ -842,6 +896,6 @@ size_t ssd_delta_tc_workspace(const SsdDelta &d) {
     return ssd_delta_tc_sizes(d) ? (size_t)ssd_delta_slots(d.tokens, d.nseq) * d.heads * kRecord : 0;
 }
 
-cudaError_t ssd_launch_delta_fwd_tc(const SsdDeltaFwd &a, void *ws, unsigned *err, cudaStream_t stream) {
-    return a.in.n <= 64 ? launch_fwd<1>(a, ws, err, stream) : launch_fwd<2>(a, ws, err, stream);
+cudaError_t ssd_launch_delta_fwd_tc(const SsdDeltaFwd &a, void *ws, int sms, unsigned *err, cudaStream_t stream) {
+    return a.in.n <= 64 ? launch_fwd<1>(a, ws, sms, err, stream) : launch_fwd<2>(a, ws, sms, err, stream);
 }

@@ -15,9 +15,15 @@ constexpr uint32_t kPanel = 64 * 128;       // 64 rows of 64 bf16 values
 
 // A chunk's record, for every head: the matrices T diag(beta) and P, each in two bf16
 // parts and each an image of a 128-byte-swizzled panel (row: the later token), then for
-// every token the decay from the chunk's start up to it and from it to the chunk's end.
+// every token the decay from the chunk's start up to it, from it to the chunk's end, beta,
+// and log2(e) g summed from its half's first token on, in two floats.
 constexpr uint32_t kRecT = 0, kRecP = 2 * kPanel, kRecGates = 4 * kPanel;
-constexpr uint32_t kRecord = kRecGates + 2 * kC * 4;
+constexpr int kGateW = kC, kGateBeta = 2 * kC, kGateSums = 3 * kC, kGates = 5 * kC;
+constexpr uint32_t kRecord = kRecGates + kGates * 4;
+static_assert(kRecord % 128 == 0, "records are copied to 128-byte boundaries");
+// Where beta is smaller than this the gradients' kernels take this: they divide by it, and
+// what such a token writes is far below fp32's last bit.
+constexpr float kLeastBeta = 9.094947017729282e-13f;
 
 // Byte of element (row, col) in a panel.
 __device__ __forceinline__ uint32_t panel_at(uint32_t row, uint32_t col) {
@@ -93,5 +99,35 @@ __device__ __forceinline__ ChunkAt chunk_at(const SsdDelta &d, long long slot) {
     c.live = chunk * kC < c.len;
     return c;
 }
+
+// Eight values of a row as the two parts' vectors in the images at `image`.
+__device__ __forceinline__ void put_parts(uint8_t *image, uint32_t at, const float *v) {
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const Split s = split2(v[2 * i], v[2 * i + 1]);
+        hi[i] = s.hi;
+        lo[i] = s.lo;
+    }
+    *reinterpret_cast<uint4 *>(image + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4 *>(image + kPanel + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+}
+
+// Zeros in the rows of 64-token panels behind a sequence's end: they are another sequence's,
+// or nothing's, and a NaN there would not be stopped by a factor of zero.
+__device__ __forceinline__ void clean_rows(uint8_t *panels, uint32_t stride, int count, int tokens, int thread,
+                                           int threads) {
+    if (tokens >= kC) return;
+    const int each = (kC - tokens) * 8;
+    for (int i = thread; i < count * each; i += threads)
+        *reinterpret_cast<uint4 *>(panels + (i / each) * stride + tokens * 128 + (i % each) * 16) = make_uint4(0, 0, 0, 0);
+}
+
+// The records of all chunks (delta_tc.cu); least_beta: see kLeastBeta.
+cudaError_t launch_chunks(const SsdDelta &d, uint8_t *records, bool least_beta, int sms, unsigned *err,
+                          cudaStream_t stream);
+// [tokens][heads][width] bf16 by boxes of `cols` values of one head and 64 tokens.
+bool make_map(CUtensorMap *m, const void *p, int width, int heads, long long tokens, long long stride, int cols,
+              bool swizzle);
 
 }  // namespace ssddelta

@@ -391,4 +391,5 @@ int ssd_act_bwd_rows(long long rows, int width, int sms);
 bool ssd_delta_tc_sizes(const SsdDelta &d);
 bool ssd_delta_tc_handles(const SsdDelta &d);
 size_t ssd_delta_tc_workspace(const SsdDelta &d);
-cudaError_t ssd_launch_delta_fwd_tc(const SsdDeltaFwd &a, void *ws, unsigned *err, cudaStream_t stream);
+cudaError_t ssd_launch_delta_fwd_tc(const SsdDeltaFwd &a, void *ws, int sms, unsigned *err,
+                                    cudaStream_t stream);
