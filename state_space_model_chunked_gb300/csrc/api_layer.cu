@@ -593,6 +593,15 @@ bool delta_sizes(ssd_dtype dtype, long long tokens, int nseq, int nheads, int he
 }
 }  // namespace
 
+namespace {
+// (which of the two kinds of kernels runs also depends on the addresses)
+size_t delta_bwd_workspace(const SsdDelta &d) {
+    if (d.tokens == 0) return 0;
+    const size_t tc = ssd_delta_tc_bwd_workspace(d), simt = ssd_delta_bwd_simt_workspace(d);
+    return tc > simt ? tc : simt;
+}
+}  // namespace
+
 size_t ssd_delta_scan_workspace_bytes(ssd_dtype dtype, long long tokens, int nseq, int nheads, int headdim,
                                       int dstate, int ngroups) {
     SsdDelta d{};
@@ -604,7 +613,7 @@ size_t ssd_delta_scan_bwd_workspace_bytes(ssd_dtype dtype, long long tokens, int
                                           int headdim, int dstate, int ngroups) {
     SsdDelta d{};
     if (!delta_sizes(dtype, tokens, nseq, nheads, headdim, dstate, ngroups, &d)) return kBad;
-    return tokens ? ssd_delta_bwd_simt_workspace(d) : 0;
+    return delta_bwd_workspace(d);
 }
 
 ssd_status ssd_delta_scan_fwd(const void *q, const void *k, const void *v, const float *g,
@@ -662,7 +671,7 @@ ssd_status ssd_delta_scan_bwd(const void *dout, const void *q, const void *k, co
         return launched(dfinal ? cudaMemcpyAsync(dinit, dfinal, bytes, cudaMemcpyDeviceToDevice, stream)
                                : cudaMemsetAsync(dinit, 0, bytes, stream));
     }
-    st = check_workspace(workspace, workspace_bytes, ssd_delta_bwd_simt_workspace(a.in), 256);
+    st = check_workspace(workspace, workspace_bytes, delta_bwd_workspace(a.in), 256);
     if (st != SSD_OK) return st;
     a.dout = dout;
     a.checkpoints = checkpoints;
@@ -677,6 +686,8 @@ ssd_status ssd_delta_scan_bwd(const void *dout, const void *q, const void *k, co
     a.dg = dg;
     a.dbeta = dbeta;
     a.dinit = dinit;
+    if (ssd_delta_tc_bwd_handles(a))
+        return launched(ssd_launch_delta_bwd_tc(a, workspace, ssd_sm_count(), ssd_device_error_word(), stream));
     return launched(ssd_launch_delta_bwd_simt(a, workspace, stream));
 }
 

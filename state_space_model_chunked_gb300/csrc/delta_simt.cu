@@ -581,7 +581,20 @@ BackPlan back_plan(const SsdDelta &d) {
     return p;
 }
 
+unsigned blocks_of(long long items, int per) {
+    const long long n = (items + per - 1) / per;
+    return (unsigned)(n < 8192 ? n : 8192);
+}
+
 }  // namespace
+
+cudaError_t ssd_launch_delta_group_sums(const float *dq_parts, void *dq, long long dq_stride, const float *dk_parts,
+                                        void *dk, long long dk_stride, const SsdDelta &d, int parts, cudaStream_t stream) {
+    const Sums q{dq_parts, dq, d.tokens, dq_stride, d.groups, parts, d.n, d.bf16};
+    const Sums k{dk_parts, dk, d.tokens, dk_stride, d.groups, parts, d.n, d.bf16};
+    delta_group_sum_kernel<<<dim3(blocks_of(d.tokens * d.groups * d.n, 256), 2), 256, 0, stream>>>(q, k);
+    return cudaGetLastError();
+}
 
 cudaError_t ssd_launch_delta_fwd_simt(const SsdDeltaFwd &a, int sms, cudaStream_t stream) {
     const Walk w{a.in, a.init, nullptr, a.o, a.o_stride, a.final_state, a.checkpoints, nullptr, 1};
@@ -601,15 +614,9 @@ cudaError_t ssd_launch_delta_bwd_simt(const SsdDeltaBwd &a, void *ws, cudaStream
                  at(p.dq), at(p.dk), at(p.anchor), at(p.ov), at(p.rw), p.slabs};
     cudaError_t e = by_shape<LaunchBack>(d.p, d.n, u, b, stream);
     if (e != cudaSuccess || d.longest == 0) return e;
-    const int parts = d.heads / d.groups * p.slabs;
-    const Sums q{b.dq, a.dq, d.tokens, a.dq_stride, d.groups, parts, d.n, d.bf16};
-    const Sums k{b.dk, a.dk, d.tokens, a.dk_stride, d.groups, parts, d.n, d.bf16};
-    const auto grid = [](long long items, int per) {
-        const long long n = (items + per - 1) / per;
-        return (unsigned)(n < 8192 ? n : 8192);
-    };
-    delta_group_sum_kernel<<<dim3(grid(d.tokens * d.groups * d.n, 256), 2), 256, 0, stream>>>(q, k);
+    e = ssd_launch_delta_group_sums(b.dq, a.dq, a.dq_stride, b.dk, a.dk, a.dk_stride, d, d.heads / d.groups * p.slabs, stream);
+    if (e != cudaSuccess) return e;
     const long long runs = (d.longest + kC - 1) / kC * (long long)d.heads * d.nseq;
-    delta_gates_kernel<<<grid(runs, 128), 128, 0, stream>>>(b, a.dg, a.dbeta);
+    delta_gates_kernel<<<blocks_of(runs, 128), 128, 0, stream>>>(b, a.dg, a.dbeta);
     return cudaGetLastError();
 }

@@ -418,6 +418,7 @@ enum WalkBar {
     kKs = 4, kU, kS, kQs, kPu, kDrain,              // products done
     kSh, kSl, kRh, kRl, kWh, kWl,                   // operands' parts written by the chain
     kUReady, kQsRead, kPuRead,                      // and by the output's warps, or read
+    kStaged, kStored,                               // the output in shared memory, and out of it
     kBars
 };
 
@@ -458,7 +459,7 @@ delta_walk_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         }
         for (int i : {kKs, kU, kS, kQs, kPu, kDrain}) mbar_init(bar(i), 1);
         for (int i : {kSh, kSl, kRh, kRl, kWh, kWl}) mbar_init(bar(i), kChainWarps);
-        for (int i : {kQsRead, kUReady, kPuRead}) mbar_init(bar(i), kOutWarps);
+        for (int i : {kQsRead, kUReady, kPuRead, kStaged, kStored}) mbar_init(bar(i), kOutWarps);
         fence_mbar_init();
         *abort = 0;
     }
@@ -640,7 +641,9 @@ delta_walk_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
             // by way of shared memory: a lane has a channel, memory wants a token's together
 #pragma unroll
             for (int i = 0; i < 32; ++i) out[(32 * half + i) * 128 + 32 * q + lane] = __float2bfloat16_rn(__uint_as_float(y[i]));
-            named_bar_sync(1, 32 * kOutWarps);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kStaged));
+            if (!wait.warp(bar(kStaged), c & 1)) break;
             __nv_bfloat16 *const to = a.o + (size_t)(first + (long long)c * kC) * a.o_stride + (size_t)head * d.p + p0;
             if (a.o_vectors) {
                 for (int i = tid; i < tokens * 16; i += 32 * kOutWarps) {
@@ -655,7 +658,9 @@ delta_walk_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
                     if (p0 + at < d.p) to[(size_t)t * a.o_stride + at] = out[t * 128 + at];
                 }
             }
-            named_bar_sync(1, 32 * kOutWarps);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kStored));
+            if (!wait.warp(bar(kStored), c & 1)) break;
         }
     } else {
         // the chain: a thread has a row of the state and of V^T, R^T and U^T; the four groups

@@ -1,0 +1,995 @@
+// Gradients of the gated delta rule on the tensor cores, by the chunks of 64 tokens of
+// delta_tc.cu.  With S the state before a chunk (kept by the forward pass), dS the gradient
+// of the state behind it, and T, P, R, U as there:
+//
+//   dU = P^T dO + diag(exp(G_end - G)) K dS^T
+//   Z  = (T diag(beta))^T dU                       (the gradient of V)
+//   dS <- exp(G_end) dS + (diag(scale exp G) dO)^T Q - (diag(exp G) Z)^T K
+//
+// is a walk over the chunks, from the last one on (the first kernel: one CTA a head, the
+// state's rows as the tensor core's lanes, as in the forward walk; it leaves Z and every
+// chunk's dS), and with M1 = dO U^T, M2 = Z U^T (64 x 64) and D_ij = exp(G_i - G_j)
+//
+//   dP_ij = scale D_ij M1_ij (j <= i)       dA_ij = -D_ij M2_ij (j < i)
+//   dQ = scale diag(exp G) dO S + dP K
+//   dK = -diag(exp G) Z S + diag(exp(G_end - G)) U dS + dP^T Q + dA K + dA^T K
+//   dbeta_i = M2_ii / beta_i^2
+//   dg_t = exp(G_end) <S, dS> + sum_(i >= t) (what token i reads of S, dotted with it)
+//        + sum_(j < t) (what token j leaves in dS) + sum_(i >= t > j) (dP o QK + dA o KK)_ij
+//
+// of every chunk by itself (the second kernel, a chunk and head a CTA).  Where one sum
+// over pairs i >= t > j is wanted, it is taken as the running sum of row sums less column
+// sums of the same fp32 values, so what cancels does so exactly.
+//   As forward, factors that are no bf16 values are held in two bf16 parts.
+#include "delta_tc.cuh"
+
+namespace {
+
+using namespace ssddelta;
+
+// MMA helpers: one kind::f16 product of M = 128 over 16 columns or rows of K a call.
+// A panel's descriptor moves by 32 bytes along a row (K-major) and by 16 rows (MN-major).
+constexpr uint64_t kStepK = 2, kStepMn = 128;
+
+// ------------------------------------------------------------------ the walk
+// Tensor memory: dS in fp32 and in two parts; K dS^T, then Z; P^T dO; dU, then Z weighted,
+// in two parts; dO weighted, in two parts.
+constexpr uint32_t kColS = 0, kColSh = 128, kColSl = 192, kColX = 256, kColY = 320, kColR = 384, kColRl = 416,
+                   kColD = 448, kColDl = 480;
+constexpr int kChainWarps = 16, kOutWarps = 8;
+constexpr int kLoadWarp = kChainWarps + kOutWarps, kMmaWarp = kLoadWarp + 1, kBackThreads = 32 * (kMmaWarp + 1);
+
+template <int kPanels>
+struct BackSmem {
+    static constexpr uint32_t kK = 0, kQ = kPanels * kPanel, kDo = 2 * kPanels * kPanel, kRec = kDo + 2 * kPanel;
+    static constexpr uint32_t kStage = (kRec + kRecord + 1023) / 1024 * 1024;
+    static constexpr uint32_t kOut = 2 * kStage;        // [token][128]: dV on its way
+    static constexpr uint32_t kCtl = kOut + 64 * 256;
+    static constexpr uint32_t kBytes = kCtl + 256;
+};
+
+struct BackTc {
+    SsdDelta d;
+    const uint8_t *records;
+    const float *dfinal;
+    __nv_bfloat16 *dv;
+    long long dv_stride;
+    bool dv_vectors;
+    float *dinit;
+    float *z, *dstate;      // [token][head][P], [slot][head][P][N]
+    unsigned *err;
+    unsigned long long wait_ns;
+    bool withhold;
+};
+
+enum BackBar {
+    kFull = 0, kEmpty = 2,
+    kE = 4, kZ, kS, kDrain,                 // products done
+    kSh, kSl, kRh, kRl, kWh, kWl,           // operands' parts written by the chain
+    kD, kZRead,                             // by the output's warps, and read by them
+    kStaged, kStored,                       // dV in shared memory, and out of it
+    kBars
+};
+
+template <int kPanels>
+__global__ void __launch_bounds__(kBackThreads, 1)
+delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
+                     const __grid_constant__ CUtensorMap mapDo, const BackTc a) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    using Lay = BackSmem<kPanels>;
+    constexpr int kN = 64 * kPanels;
+    const SsdDelta &d = a.d;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t base = smem_u32(smem);
+    if (base & 1023u) {
+        if (threadIdx.x == 0) ssd_report(a.err, SSD_DEVERR_SMEM_ALIGN);
+        return;
+    }
+    const int head = (int)(blockIdx.x % d.heads), seq = (int)(blockIdx.x / d.heads);
+    const int group = head / (d.heads / d.groups);
+    const long long first = d.cu ? d.cu[seq] : (long long)seq * d.length;
+    const int len = d.cu ? d.cu[seq + 1] - d.cu[seq] : d.length;
+    const int chunks = (len + kC - 1) / kC;
+    const size_t size = (size_t)d.p * d.n, state = ((size_t)seq * d.heads + head) * size;
+    if (chunks == 0) {
+        if (a.dinit)
+            for (size_t i = threadIdx.x; i < size; i += kBackThreads) a.dinit[state + i] = a.dfinal ? a.dfinal[state + i] : 0.f;
+        return;
+    }
+    const auto bar = [&](int i) { return base + Lay::kCtl + 8u * (uint32_t)i; };
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(smem + Lay::kCtl + 8 * kBars);
+    volatile int *abort = reinterpret_cast<volatile int *>(smem + Lay::kCtl + 8 * kBars + 4);
+    const Waiter wait{abort, a.err, a.wait_ns};
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(bar(kFull + s), 1);
+            mbar_init(bar(kEmpty + s), 1 + kChainWarps + kOutWarps);
+        }
+        for (int i : {kE, kZ, kS, kDrain}) mbar_init(bar(i), 1);
+        for (int i : {kSh, kSl, kRh, kRl, kWh, kWl}) mbar_init(bar(i), kChainWarps);
+        for (int i : {kD, kZRead, kStaged, kStored}) mbar_init(bar(i), kOutWarps);
+        fence_mbar_init();
+        *abort = 0;
+    }
+    if (warp == 0) {
+        tmem_alloc(smem_u32(tslot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+    const long long slot0 = ssd_delta_slot(first, seq, 0);
+    int loaded = 0;
+
+    // step `it` of the walk is chunk chunks - 1 - it, in stage it & 1
+    if (warp == kLoadWarp) {
+        for (int it = 0; it < chunks; ++it) {
+            const int s = it & 1, c = chunks - 1 - it;
+            if (it >= 2 && !wait.warp(bar(kEmpty + s), ((it >> 1) - 1) & 1)) break;
+            if (elect_one()) {
+                const uint32_t to = base + s * Lay::kStage;
+                const int token = (int)(first + (long long)c * kC);
+                mbar_arrive_expect_tx(bar(kFull + s), (2 * kPanels + 2) * kPanel + kRecord);
+#pragma unroll
+                for (int p = 0; p < kPanels; ++p) {
+                    tma_load_3d(to + Lay::kK + p * kPanel, &mapK, bar(kFull + s), 64 * p, group, token);
+                    tma_load_3d(to + Lay::kQ + p * kPanel, &mapQ, bar(kFull + s), 64 * p, group, token);
+                }
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+                    tma_load_3d(to + Lay::kDo + p * kPanel, &mapDo, bar(kFull + s), 64 * p, head, token);
+                bulk_load(to + Lay::kRec, a.records + ((size_t)(slot0 + c) * d.heads + head) * kRecord, kRecord,
+                          bar(kFull + s));
+            }
+            __syncwarp();
+            loaded = it + 1;
+        }
+    } else if (warp == kMmaWarp) {
+        constexpr uint32_t kId64 = idesc_bf16_f32(128, 64, false, false);
+        constexpr uint32_t kIdS = idesc_bf16_f32(128, kN, false, true);
+        const bool one = elect_one();
+        const auto keys = [&](uint32_t acol, uint32_t tile, bool add) {
+#pragma unroll
+            for (int p = 0; p < kPanels; ++p) {
+                const uint64_t bd = smem_desc(tile + p * kPanel, 16, 1024, kSwizzle128B);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_ts(tmem + kColX, tmem + acol + 32 * p + 8 * k, bd + kStepK * k, kId64, add || p + k > 0);
+            }
+        };
+        // D (+)= A . M of a lower triangular M, whose rows from 16 k on end at column 16 k + 15
+        const auto triangle = [&](uint32_t acol, uint32_t tile, bool add) {
+            const uint64_t bd = smem_desc(tile, kPanel, 1024, kSwizzle128B);
+#pragma unroll
+            for (int k = 3; k >= 0; --k)
+                mma_ts(tmem + kColX, tmem + acol + 8 * k, bd + kStepMn * k, idesc_bf16_f32(128, 16 * k + 16, false, true),
+                       add || k < 3);
+        };
+        const auto state_update = [&](uint32_t acol, uint32_t tile) {
+            const uint64_t bd = smem_desc(tile, kPanel, 1024, kSwizzle128B);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_ts(tmem + kColS, tmem + acol + 8 * k, bd + kStepMn * k, kIdS, 1);
+        };
+        const auto from_output = [&](uint32_t at) {
+            const uint64_t ad = smem_desc(at + Lay::kDo, kPanel, 1024, kSwizzle128B);
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+                const uint64_t bd = smem_desc(at + Lay::kRec + kRecP + part * kPanel, kPanel, 1024, kSwizzle128B);
+#pragma unroll
+                for (int k = 3; k >= 0; --k)
+                    mma_ss(tmem + kColY, ad + kStepMn * k, bd + kStepMn * k, idesc_bf16_f32(128, 16 * k + 16, true, true),
+                           part > 0 || k < 3);
+            }
+        };
+        for (int it = 0; it < chunks; ++it) {
+            const int s = it & 1;
+            const uint32_t at = base + s * Lay::kStage;
+            if (!wait.warp(bar(kFull + s), (it >> 1) & 1) || !wait.warp(bar(kSh), it & 1)) break;
+            // (Z of the step in front has been read)
+            if (it > 0 && !wait.warp(bar(kZRead), (it - 1) & 1)) break;
+            tc_fence_after();
+            if (one) {
+                // the last chunk's rows behind the sequence's end are clean only now
+                if (it == 0) from_output(at);
+                keys(kColSh, at + Lay::kK, false);
+            }
+            __syncwarp();
+            if (!wait.warp(bar(kSl), it & 1)) break;
+            tc_fence_after();
+            if (one) {
+                keys(kColSl, at + Lay::kK, true);
+                if (!(a.withhold && blockIdx.x == 0 && it == 0)) mma_commit(bar(kE));
+            }
+            __syncwarp();
+            if (!wait.warp(bar(kRh), it & 1)) break;
+            tc_fence_after();
+            if (one) {
+                triangle(kColR, at + Lay::kRec + kRecT, false);
+                triangle(kColR, at + Lay::kRec + kRecT + kPanel, true);
+            }
+            __syncwarp();
+            if (!wait.warp(bar(kRl), it & 1)) break;
+            tc_fence_after();
+            if (one) {
+                triangle(kColRl, at + Lay::kRec + kRecT, true);
+                mma_commit(bar(kZ));
+            }
+            __syncwarp();
+            if (!wait.warp(bar(kD), it & 1)) break;
+            tc_fence_after();
+            if (one) {
+                state_update(kColD, at + Lay::kQ);
+                state_update(kColDl, at + Lay::kQ);
+            }
+            __syncwarp();
+            if (!wait.warp(bar(kWh), it & 1)) break;
+            tc_fence_after();
+            if (one) state_update(kColR, at + Lay::kK);
+            __syncwarp();
+            if (!wait.warp(bar(kWl), it & 1)) break;
+            tc_fence_after();
+            if (one) {
+                state_update(kColRl, at + Lay::kK);
+                mma_commit(bar(kS));
+                mma_commit(bar(kEmpty + s));
+            }
+            __syncwarp();
+            if (it + 1 < chunks) {
+                if (!wait.warp(bar(kFull + (s ^ 1)), ((it + 1) >> 1) & 1)) break;
+                if (one) from_output(base + (s ^ 1) * Lay::kStage);
+                __syncwarp();
+            }
+        }
+        // what was issued completes before the CTA gives its tensor memory back
+        if (one) mma_commit(bar(kDrain));
+        __syncwarp();
+        if (!mbar_wait(bar(kDrain), 0, kSsdDefaultWaitNs)) ssd_report(a.err, SSD_DEVERR_TIMEOUT);
+    } else if (warp >= kChainWarps) {
+        // dO's weighted parts, and Z on its way out: half of the tokens each
+        const int q = warp & 3, half = (warp - kChainWarps) >> 2, row = 32 * q + lane;
+        const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16);
+        __nv_bfloat16 *const out = reinterpret_cast<__nv_bfloat16 *>(smem + Lay::kOut);
+        const int tid = threadIdx.x - 32 * kChainWarps;
+        for (int it = 0; it < chunks; ++it) {
+            const int s = it & 1, c = chunks - 1 - it, tokens = min(kC, len - c * kC);
+            const uint8_t *stage = smem + s * Lay::kStage;
+            const float *gates = reinterpret_cast<const float *>(stage + Lay::kRec + kRecGates) + 32 * half;
+            if (!wait.warp(bar(kFull + s), (it >> 1) & 1)) break;
+            // (the step in front has used its parts)
+            if (it > 0 && !wait.warp(bar(kS), (it - 1) & 1)) break;
+            tc_fence_after();
+            {
+                const uint8_t *from = stage + Lay::kDo + (row >> 6) * kPanel;
+                uint32_t hi[16], lo[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float x[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int t = 32 * half + 2 * i + j;
+                        const float o = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(from + panel_at(t, row & 63)));
+                        x[j] = t < tokens ? o * (d.scale * gates[2 * i + j]) : 0.f;
+                    }
+                    const Split y = split2(x[0], x[1]);
+                    hi[i] = y.hi;
+                    lo[i] = y.lo;
+                }
+                tmem_st16(tq + kColD + 16 * half, hi);
+                tmem_st16(tq + kColDl + 16 * half, lo);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(kD));
+                mbar_arrive(bar(kEmpty + s));
+            }
+            if (!wait.warp(bar(kZ), it & 1)) break;
+            tc_fence_after();
+            uint32_t z[32];
+            tmem_ld32(tq + kColX + 32 * half, z);
+            tmem_ld_wait(z);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kZRead));
+            if (row < d.p) {
+                float *to = a.z + ((size_t)(first + (long long)c * kC + 32 * half) * d.heads + head) * d.p + row;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (32 * half + i < tokens) to[(size_t)i * d.heads * d.p] = __uint_as_float(z[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) out[(32 * half + i) * 128 + row] = __float2bfloat16_rn(__uint_as_float(z[i]));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kStaged));
+            if (!wait.warp(bar(kStaged), it & 1)) break;
+            __nv_bfloat16 *const to = a.dv + (size_t)(first + (long long)c * kC) * a.dv_stride + (size_t)head * d.p;
+            if (a.dv_vectors) {
+                for (int i = tid; i < tokens * 16; i += 32 * kOutWarps) {
+                    const int t = i >> 4, at = (i & 15) * 8;
+                    if (at < d.p)
+                        *reinterpret_cast<uint4 *>(to + (size_t)t * a.dv_stride + at) =
+                            *reinterpret_cast<const uint4 *>(out + t * 128 + at);
+                }
+            } else {
+                for (int i = tid; i < tokens * 128; i += 32 * kOutWarps) {
+                    const int t = i >> 7, at = i & 127;
+                    if (at < d.p) to[(size_t)t * a.dv_stride + at] = out[t * 128 + at];
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kStored));
+            if (!wait.warp(bar(kStored), it & 1)) break;
+        }
+    } else {
+        // the chain: a thread has a row of dS and of dU^T and Z^T
+        const int q = warp & 3, part = warp >> 2, p = 32 * q + lane;
+        const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16);
+        constexpr int kMine = kN / 4;
+        const int n0 = part * kMine;
+        const bool vec = d.n % 4 == 0;
+        const auto to_memory = [&](float *m, const float (&v)[kMine]) {
+            if (p >= d.p) return;
+            float *to = m + (size_t)p * d.n;
+#pragma unroll
+            for (int i = 0; i < kMine; i += 4) {
+                const int n = n0 + i;
+                if (vec) {
+                    if (n < d.n) *reinterpret_cast<float4 *>(to + n) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                } else {
+                    for (int j = 0; j < 4; ++j)
+                        if (n + j < d.n) to[n + j] = v[i + j];
+                }
+            }
+        };
+        const auto ready = [&](int which) {
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(which));
+        };
+        // the gradient of the state behind chunk c: its parts, in fp32 decayed over the
+        // chunk, and for the chunk's other gradients as it is
+        const auto put = [&](int c, const float (&v)[kMine], float decay) {
+            uint32_t hi[kMine / 2];
+#pragma unroll
+            for (int i = 0; i < kMine / 2; ++i) hi[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+            if constexpr (kMine == 32) tmem_st16(tq + kColSh + n0 / 2, hi);
+            else tmem_st8(tq + kColSh + n0 / 2, hi);
+            ready(kSh);
+#pragma unroll
+            for (int i = 0; i < kMine / 2; ++i) hi[i] = rest2(v[2 * i], v[2 * i + 1], hi[i]);
+            if constexpr (kMine == 32) tmem_st16(tq + kColSl + n0 / 2, hi);
+            else tmem_st8(tq + kColSl + n0 / 2, hi);
+            ready(kSl);
+            // (waited for before the chunk's kRh)
+#pragma unroll
+            for (int h = 0; h < kMine / 16; ++h) {
+                uint32_t f[16];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 x = fmul2(make_float2(v[16 * h + 2 * i], v[16 * h + 2 * i + 1]), make_float2(decay, decay));
+                    f[2 * i] = __float_as_uint(x.x);
+                    f[2 * i + 1] = __float_as_uint(x.y);
+                }
+                tmem_st16(tq + kColS + n0 + 16 * h, f);
+            }
+            to_memory(a.dstate + ((size_t)(slot0 + c) * d.heads + head) * size, v);
+        };
+        const auto stage = [&](int it) { return smem + (it & 1) * Lay::kStage; };
+        const auto decay_of = [&](int it) { return reinterpret_cast<const float *>(stage(it) + Lay::kRec + kRecGates)[kC - 1]; };
+        bool on = wait.warp(bar(kFull), 0);
+        if (on) {
+            const int tokens = len - (chunks - 1) * kC;
+            if (tokens < kC) {
+                clean_rows(smem, kPanel, 2 * kPanels + 2, tokens, threadIdx.x, 32 * kChainWarps);
+                fence_proxy_async_smem();
+            }
+            float v[kMine];
+#pragma unroll
+            for (int i = 0; i < kMine; ++i)
+                v[i] = a.dfinal && p < d.p && n0 + i < d.n ? a.dfinal[state + (size_t)p * d.n + n0 + i] : 0.f;
+            put(chunks - 1, v, decay_of(0));
+        }
+        for (int it = 0; on && it < chunks; ++it) {
+            const int s = it & 1, c = chunks - 1 - it, tokens = min(kC, len - c * kC) - 16 * part;
+            const float4 *gates = reinterpret_cast<const float4 *>(stage(it) + Lay::kRec + kRecGates) + 4 * part;
+            float x[16], f[16];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<float4 *>(f + 4 * i) = gates[kGateW / 4 + i];
+            if (!wait.warp(bar(kE), it & 1)) break;
+            tc_fence_after();
+            uint32_t r[16], y[16], hi[8];
+            tmem_ld16(tq + kColX + 16 * part, r);
+            tmem_ld16(tq + kColY + 16 * part, y);
+            tmem_ld_wait(r);
+            tmem_ld_wait(y);
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+                const float2 u = ffma2(make_float2(f[i], f[i + 1]), make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])),
+                                       make_float2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])));
+                x[i] = u.x;
+                x[i + 1] = u.y;
+            }
+            if (tokens < 16) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (i >= tokens) x[i] = 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) hi[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+            tmem_st8(tq + kColR + 8 * part, hi);
+            ready(kRh);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) hi[i] = rest2(x[2 * i], x[2 * i + 1], hi[i]);
+            tmem_st8(tq + kColRl + 8 * part, hi);
+            ready(kRl);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<float4 *>(f + 4 * i) = gates[i];
+            if (!wait.warp(bar(kZ), it & 1)) break;
+            tc_fence_after();
+            tmem_ld16(tq + kColX + 16 * part, r);
+            tmem_ld_wait(r);
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+                const float2 u = fmul2(make_float2(-f[i], -f[i + 1]), make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])));
+                x[i] = u.x;
+                x[i + 1] = u.y;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) hi[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+            tmem_st8(tq + kColR + 8 * part, hi);
+            ready(kWh);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) hi[i] = rest2(x[2 * i], x[2 * i + 1], hi[i]);
+            tmem_st8(tq + kColRl + 8 * part, hi);
+            ready(kWl);
+            if (lane == 0) mbar_arrive(bar(kEmpty + s));
+            const bool more = it + 1 < chunks;
+            if (more && !wait.warp(bar(kFull + (s ^ 1)), ((it + 1) >> 1) & 1)) break;
+            const float decay = more ? decay_of(it + 1) : 1.f;
+            if (!wait.warp(bar(kS), it & 1)) break;
+            tc_fence_after();
+            uint32_t m[kMine];
+            if constexpr (kMine == 32) tmem_ld32(tq + kColS + n0, m);
+            else tmem_ld16(tq + kColS + n0, m);
+            tmem_ld_wait(m);
+            float v[kMine];
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) v[i] = __uint_as_float(m[i]);
+            if (more) put(c - 1, v, decay);
+            else if (a.dinit) to_memory(a.dinit + state, v);
+        }
+    }
+    // copies in flight land before the CTA ends
+    if (warp == kLoadWarp) {
+        for (int it = loaded > 2 ? loaded - 2 : 0; it < loaded; ++it)
+            if (!mbar_wait(bar(kFull + (it & 1)), (it >> 1) & 1, kSsdDefaultWaitNs)) ssd_report(a.err, SSD_DEVERR_TIMEOUT);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------ a chunk's other gradients
+// Steps of products and of elementwise work by turns, all warps together: with 224 KB of
+// tiles one CTA an SM, whose products (about 150 of M = 128, N = 64) take longest.
+constexpr int kGradThreads = 256;
+constexpr uint32_t kTall = 2 * kPanel;      // a panel of 128 rows
+template <int kPanels>
+struct GradSmem {
+    static constexpr uint32_t kQk = 0;                          // panels of queries over keys
+    static constexpr uint32_t kAh = kQk + kPanels * kTall;      // dO over Z's rounded part, then scratch
+    static constexpr uint32_t kAl = kAh + 2 * kTall;            // nothing over what rounding left of Z
+    static constexpr uint32_t kU = kAl + 2 * kTall;             // U's parts
+    static constexpr uint32_t kSs = kU + 4 * kPanel;            // the parts of S, then of dS: [P][N]
+    static constexpr uint32_t kW = kSs + 4 * kTall;             // V and T; then the parts of dP and of dA
+    static constexpr uint32_t kCtl = kW + 4 * kPanel;
+    static constexpr uint32_t kGatesAt = kCtl + 64;
+    static constexpr uint32_t kBytes = kGatesAt + kGates * 4;
+    // scratch, where dO and Z were (floats)
+    static constexpr int kRowSum = 0, kColSum = 256, kAhead = 512, kBehind = 768, kWhole = 1024, kDbeta = 1040;
+};
+
+struct GradTc {
+    SsdDelta d;
+    const uint8_t *records;
+    const float *checkpoints, *z, *dstate;
+    __nv_bfloat16 *dq, *dk;             // where a group is one head; else sums by head:
+    float *dq_heads, *dk_heads;         // [token][head][N]
+    long long dq_stride, dk_stride;
+    float *dg, *dbeta;
+    unsigned *err;
+};
+
+// The sums over the warp's lanes of 32 values a lane, lane l's answer that of value l.
+__device__ __forceinline__ float lanes_transposed_sum(float (&v)[32], int lane) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const float keep = up ? v[i + o] : v[i], give = up ? v[i] : v[i + o];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+    }
+    return v[0];
+}
+
+template <int kPanels>
+__global__ void __launch_bounds__(kGradThreads, 1)
+delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
+                     const __grid_constant__ CUtensorMap mapV, const __grid_constant__ CUtensorMap mapDo, const GradTc a) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    using Lay = GradSmem<kPanels>;
+    const SsdDelta &d = a.d;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int q = warp & 3, half = warp >> 2;       // lanes of tensor memory, half of the columns
+    const uint32_t base = smem_u32(smem);
+    if (base & 1023u) {
+        if (threadIdx.x == 0) ssd_report(a.err, SSD_DEVERR_SMEM_ALIGN);
+        return;
+    }
+    const long long slot = blockIdx.x / d.heads;
+    const int head = (int)(blockIdx.x % d.heads), group = head / (d.heads / d.groups);
+    const ChunkAt at = chunk_at(d, slot);
+    if (!at.live) return;
+    const int valid = min(kC, at.len - at.chunk * kC);
+    const long long token = at.first + (long long)at.chunk * kC;
+    const size_t record = (size_t)slot * d.heads + head, size = (size_t)d.p * d.n;
+    const uint32_t full = base + Lay::kCtl, done = full + 8;
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(smem + Lay::kCtl + 16);
+    if (threadIdx.x == 0) {
+        mbar_init(full, 1);
+        mbar_init(done, 1);
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(smem_u32(tslot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot, tq = tmem + ((uint32_t)(32 * q) << 16);
+    if (threadIdx.x == 0) {
+        mbar_arrive_expect_tx(full, kPanels * kTall + 2 * kPanel + 64 * 256 + 2 * kPanel + kGates * 4);
+        const int t = (int)token;
+#pragma unroll
+        for (int p = 0; p < kPanels; ++p) {
+            tma_load_3d(base + Lay::kQk + p * kTall, &mapQ, full, 64 * p, group, t);
+            tma_load_3d(base + Lay::kQk + p * kTall + kPanel, &mapK, full, 64 * p, group, t);
+        }
+#pragma unroll
+        for (int p = 0; p < 2; ++p) tma_load_3d(base + Lay::kAh + p * kTall, &mapDo, full, 64 * p, head, t);
+        tma_load_3d(base + Lay::kW, &mapV, full, 0, head, t);
+        bulk_load(base + Lay::kW + 2 * kPanel, a.records + record * kRecord + kRecT, 2 * kPanel, full);
+        bulk_load(base + Lay::kGatesAt, a.records + record * kRecord + kRecGates, kGates * 4, full);
+    }
+    // a state's row by a warp: lane l has the columns 4 l .. 4 l + 3; a part's panel is tall
+    const bool vec = d.n % 4 == 0;
+    const auto load_state = [&](const float *m, int row) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int n = 4 * lane;
+        if (row < d.p && n < d.n) {
+            const float *from = m + (size_t)row * d.n + n;
+            if (vec) {
+                v = __ldcs(reinterpret_cast<const float4 *>(from));
+            } else {
+                v.x = from[0];
+                if (n + 1 < d.n) v.y = from[1];
+                if (n + 2 < d.n) v.z = from[2];
+                if (n + 3 < d.n) v.w = from[3];
+            }
+        }
+        return v;
+    };
+    const uint32_t state_panel = Lay::kSs + (uint32_t)(lane >> 4) * kTall;
+    const auto store_state = [&](int row, float4 v) {
+        if (64 * kPanels <= 4 * lane) return;
+        const uint32_t to = state_panel + panel_at(row, (4 * lane) & 63);
+        const Split x = split2(v.x, v.y), y = split2(v.z, v.w);
+        *reinterpret_cast<uint2 *>(smem + to) = make_uint2(x.hi, y.hi);
+        *reinterpret_cast<uint2 *>(smem + to + kPanels * kTall) = make_uint2(x.lo, y.lo);
+    };
+    {
+        const float *from = a.checkpoints + record * size;
+#pragma unroll 1
+        for (int r0 = 16 * warp; r0 < 16 * warp + 16; r0 += 8) {
+            float4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = load_state(from, r0 + i);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) store_state(r0 + i, v[i]);
+        }
+        // Z, a token a row
+        float4 z[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int t = 8 * warp + i, p = 4 * lane;
+            z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (t < valid && p < d.p)       // (P is a multiple of 8)
+                z[i] = __ldcs(reinterpret_cast<const float4 *>(a.z + ((size_t)(token + t) * d.heads + head) * d.p + p));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t to = (uint32_t)(lane >> 4) * kTall + panel_at(64 + 8 * warp + i, (4 * lane) & 63);
+            const Split x = split2(z[i].x, z[i].y), y = split2(z[i].z, z[i].w);
+            *reinterpret_cast<uint2 *>(smem + Lay::kAh + to) = make_uint2(x.hi, y.hi);
+            *reinterpret_cast<uint2 *>(smem + Lay::kAl + to) = make_uint2(x.lo, y.lo);
+        }
+        for (int i = threadIdx.x; i < 1024; i += kGradThreads)
+            *reinterpret_cast<uint4 *>(smem + Lay::kAl + (i >> 9) * kTall + (i & 511) * 16) = make_uint4(0, 0, 0, 0);
+    }
+    // (waits for the CTA's own copies and products)
+    if (!mbar_wait(full, 0, kSsdDefaultWaitNs)) ssd_report(a.err, SSD_DEVERR_TIMEOUT);
+    clean_rows(smem + Lay::kQk, kPanel, 2 * kPanels, valid, threadIdx.x, kGradThreads);
+    clean_rows(smem + Lay::kAh, kTall, 2, valid, threadIdx.x, kGradThreads);
+    const bool issuer = warp == 0;
+    uint32_t phase = 0;
+    // what all threads wrote is there for the products, and what the products leave for all
+    const auto before = [&] {
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+    };
+    const auto after = [&] {
+        __syncwarp();
+        if (!mbar_wait(done, phase, kSsdDefaultWaitNs)) ssd_report(a.err, SSD_DEVERR_TIMEOUT);
+        phase ^= 1;
+        tc_fence_after();
+    };
+    constexpr uint32_t kId = idesc_bf16_f32(128, 64, false, false), kIdMn = idesc_bf16_f32(128, 64, true, false);
+    constexpr uint32_t kColU = 0, kColQk = 64, kColM = 128, kColDoS = 192, kColZs = 256, kColPk = 320, kColSum = 384,
+                       kColUs = 448, kColR = 448, kColRl = 480;
+    const uint32_t sh = base + Lay::kSs, sl = sh + kPanels * kTall, ah = base + Lay::kAh, al = base + Lay::kAl;
+    const uint32_t uh = base + Lay::kU, ul = uh + 2 * kPanel, w = base + Lay::kW, qk = base + Lay::kQk;
+    // D (+)= A B^T over `panels` of 64 columns: A by tall panels, B by panels `bstep` apart
+    const auto rows_rows = [&](uint32_t dcol, uint32_t at_a, uint32_t at_b, uint32_t bstep, int panels, bool add) {
+        for (int p = 0; p < panels; ++p) {
+            const uint64_t ad = smem_desc(at_a + p * kTall, 16, 1024, kSwizzle128B);
+            const uint64_t bd = smem_desc(at_b + p * bstep, 16, 1024, kSwizzle128B);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_ss(tmem + dcol, ad + kStepK * k, bd + kStepK * k, kId, add || p + k > 0);
+        }
+    };
+    // D (+)= A^T B^T: A [128 of P][N] by tall panels of N, B [64][P] by panels `bstep` apart
+    const auto cols_rows = [&](uint32_t dcol, uint32_t at_a, uint32_t at_b, uint32_t bstep, bool add) {
+        const uint64_t ad = smem_desc(at_a, kTall, 1024, kSwizzle128B);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const uint64_t bd = smem_desc(at_b + p * bstep, 16, 1024, kSwizzle128B);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                mma_ss(tmem + dcol, ad + kStepMn * (4 * p + k), bd + kStepK * k, kIdMn, add || p + k > 0);
+        }
+    };
+    // D (+)= A^T M^T (columns of D from 16 k on) and A^T M (up to 16 k + 15) of a lower
+    // triangular M [64][64], A [64][N]
+    const auto tokens_lower = [&](uint32_t dcol, uint32_t at_a, uint32_t at_m, bool add) {
+        const uint64_t ad = smem_desc(at_a, kTall, 1024, kSwizzle128B), bd = smem_desc(at_m, 16, 1024, kSwizzle128B);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            mma_ss(tmem + dcol + 16 * k, ad + kStepMn * k, bd + kStepK * k + kStepMn * k,
+                   idesc_bf16_f32(128, 64 - 16 * k, true, false), add || k > 0);
+    };
+    const auto tokens_upper = [&](uint32_t dcol, uint32_t at_a, uint32_t at_m, bool add) {
+        const uint64_t ad = smem_desc(at_a, kTall, 1024, kSwizzle128B), bd = smem_desc(at_m, kPanel, 1024, kSwizzle128B);
+#pragma unroll
+        for (int k = 3; k >= 0; --k)
+            mma_ss(tmem + dcol, ad + kStepMn * k, bd + kStepMn * k, idesc_bf16_f32(128, 16 * k + 16, true, true), add || k < 3);
+    };
+    const float *gates = reinterpret_cast<const float *>(smem + Lay::kGatesAt);
+    float *const scratch = reinterpret_cast<float *>(smem + Lay::kAh);
+
+    // K S^T by the state's rows; Q K^T over K K^T
+    before();
+    if (issuer && elect_one()) {
+        rows_rows(kColU, sh, qk + kPanel, kTall, kPanels, false);
+        rows_rows(kColU, sl, qk + kPanel, kTall, kPanels, true);
+        rows_rows(kColQk, qk, qk + kPanel, kTall, kPanels, false);
+        mma_commit(done);
+    }
+    after();
+    // R, as the left operand of U
+    const int row = 32 * q + lane;
+    {
+        uint32_t r[32], hi[16], lo[16];
+        tmem_ld32(tq + kColU + 32 * half, r);
+        tmem_ld_wait(r);
+        const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(smem + Lay::kW) + 32 * half * 128 + row;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float x[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int t = 2 * i + j;
+                x[j] = __bfloat162float(v[t * 128]) - gates[32 * half + t] * __uint_as_float(r[t]);
+                if (32 * half + t >= valid) x[j] = 0.f;
+            }
+            const Split y = split2(x[0], x[1]);
+            hi[i] = y.hi;
+            lo[i] = y.lo;
+        }
+        tmem_st16(tq + kColR + 16 * half, hi);
+        tmem_st16(tq + kColRl + 16 * half, lo);
+        tmem_st_wait();
+    }
+    before();
+    if (issuer && elect_one()) {
+        const auto triangle = [&](uint32_t acol, uint32_t tile, bool add) {
+            const uint64_t bd = smem_desc(tile, 16, 1024, kSwizzle128B);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                mma_ts(tmem + kColU + 16 * k, tmem + acol + 8 * k, bd + kStepK * k + kStepMn * k,
+                       idesc_bf16_f32(128, 64 - 16 * k, false, false), add || k > 0);
+        };
+        triangle(kColR, w + 2 * kPanel, false);
+        triangle(kColR, w + 3 * kPanel, true);
+        triangle(kColRl, w + 2 * kPanel, true);
+        mma_commit(done);
+    }
+    after();
+    // U by tokens
+    {
+        uint32_t r[32];
+        tmem_ld32(tq + kColU + 32 * half, r);
+        tmem_ld_wait(r);
+        uint8_t *const to = smem + Lay::kU + (row >> 6) * kPanel;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const float x = __uint_as_float(r[i]);
+            const __nv_bfloat16 h = __float2bfloat16_rn(x);
+            const uint32_t o = panel_at(32 * half + i, row & 63);
+            *reinterpret_cast<__nv_bfloat16 *>(to + o) = h;
+            *reinterpret_cast<__nv_bfloat16 *>(to + 2 * kPanel + o) = __float2bfloat16_rn(x - __bfloat162float(h));
+        }
+    }
+    before();
+    if (issuer && elect_one()) {
+        // M1 over M2
+        rows_rows(kColM, ah, uh, kPanel, 2, false);
+        rows_rows(kColM, ah, ul, kPanel, 2, true);
+        rows_rows(kColM, al, uh, kPanel, 2, true);
+        // (dO S)^T and (Z S)^T
+        cols_rows(kColDoS, sh, ah, kTall, false);
+        cols_rows(kColDoS, sl, ah, kTall, true);
+        cols_rows(kColZs, sh, ah + kPanel, kTall, false);
+        cols_rows(kColZs, sl, ah + kPanel, kTall, true);
+        cols_rows(kColZs, sh, al + kPanel, kTall, true);
+        mma_commit(done);
+    }
+    // dS on its way beside the products
+    const float *const dstate = a.dstate + record * size;
+    float4 ds[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ds[i] = load_state(dstate, 16 * warp + i);
+    after();
+    // dP (lanes 0 .. 63) and dA (64 .. 127), a row a lane; and what pairs of tokens add to dg
+    {
+        const int r = row & 63, j0 = 32 * half;
+        const bool keys = q >= 2;
+        uint32_t m[32], x[32];
+        tmem_ld32(tq + kColM + j0, m);
+        tmem_ld32(tq + kColQk + j0, x);
+        const float2 *sums = reinterpret_cast<const float2 *>(gates + kGateSums);
+        const float2 mine = sums[r], whole = sums[31];
+        const bool over = r >= 32 && half == 0;
+        const int last = r < valid ? (keys ? r - 1 : r) : -1;
+        const float factor = keys ? -1.f : d.scale;
+        tmem_ld_wait(m);
+        tmem_ld_wait(x);
+        float v[32], e[32], sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const float2 c = sums[j0 + j];
+            float g = (mine.x - c.x) + (mine.y - c.y);
+            if (over) g = (mine.x + mine.y) + ((whole.x - c.x) + (whole.y - c.y));
+            const bool in = j0 + j <= last;
+            v[j] = in ? factor * ex2_approx(g) * __uint_as_float(m[j]) : 0.f;
+            e[j] = in && j0 + j < r ? v[j] * __uint_as_float(x[j]) : 0.f;
+            sum += e[j];
+            if (keys && j0 + j == r) {
+                const float be = gates[kGateBeta + r];
+                scratch[Lay::kDbeta + r] = __uint_as_float(m[j]) / be / be;
+            }
+        }
+        uint8_t *const to = smem + Lay::kW + (keys ? 2 * kPanel : 0);
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) put_parts(to, panel_at(r, j0 + j), v + j);
+        scratch[Lay::kRowSum + (keys ? 128 : 0) + 64 * half + r] = sum;
+        const float col = lanes_transposed_sum(e, lane);
+        scratch[Lay::kColSum + (keys ? 128 : 0) + 64 * (q & 1) + j0 + lane] = col;
+    }
+    // dS in S's place, and <S, dS>
+    {
+        float dot = 0.f;
+        const auto swap = [&](int r, float4 v) {
+            if (64 * kPanels <= 4 * lane) return;
+            const uint32_t to = state_panel + panel_at(r, (4 * lane) & 63);
+            const uint2 h = *reinterpret_cast<const uint2 *>(smem + to);
+            const uint2 l = *reinterpret_cast<const uint2 *>(smem + to + kPanels * kTall);
+            const auto low = [](uint32_t x) { return __uint_as_float(x << 16); };
+            const auto high = [](uint32_t x) { return __uint_as_float(x & 0xffff0000u); };
+            dot += (low(h.x) + low(l.x)) * v.x + (high(h.x) + high(l.x)) * v.y + (low(h.y) + low(l.y)) * v.z +
+                   (high(h.y) + high(l.y)) * v.w;
+            store_state(r, v);
+        };
+#pragma unroll
+        for (int i = 0; i < 8; ++i) swap(16 * warp + i, ds[i]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ds[i] = load_state(dstate, 16 * warp + 8 + i);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) swap(16 * warp + 8 + i, ds[i]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        if (lane == 0) scratch[Lay::kWhole + warp] = dot;
+    }
+    before();
+    if (issuer && elect_one()) {
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+            const uint32_t dp = w + part * kPanel, da = w + (2 + part) * kPanel;
+            tokens_lower(kColPk, qk + kPanel, dp, part > 0);
+            tokens_upper(kColSum, qk, dp, part > 0);
+            tokens_lower(kColSum, qk + kPanel, da, true);
+            tokens_upper(kColSum, qk + kPanel, da, true);
+        }
+        cols_rows(kColUs, sh, uh, kPanel, false);
+        cols_rows(kColUs, sl, uh, kPanel, true);
+        cols_rows(kColUs, sh, ul, kPanel, true);
+        mma_commit(done);
+    }
+    after();
+    // a lane is a column of dQ and dK; what a token reads of S and leaves in dS
+    {
+        const bool on = row < d.n;
+        const bool heads = a.dq == nullptr;
+        const uint8_t *const keys = smem + Lay::kQk + (row >> 6) * kTall;
+#pragma unroll 1
+        for (int b = 0; b < 2; ++b) {
+            const int t0 = 32 * half + 16 * b;
+            uint32_t x[16], y[16];
+            float dots[32], dq[16], dk[16];
+            tmem_ld16(tq + kColDoS + t0, x);
+            tmem_ld16(tq + kColPk + t0, y);
+            tmem_ld_wait(x);
+            tmem_ld_wait(y);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float from = d.scale * gates[t0 + i] * __uint_as_float(x[i]);
+                const float qv = on ? __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(keys + panel_at(t0 + i, row & 63))) : 0.f;
+                dots[i] = on ? from * qv : 0.f;
+                dq[i] = from + __uint_as_float(y[i]);
+            }
+            tmem_ld16(tq + kColZs + t0, x);
+            tmem_ld16(tq + kColUs + t0, y);
+            tmem_ld_wait(x);
+            tmem_ld_wait(y);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float from = -gates[t0 + i] * __uint_as_float(x[i]), into = gates[kGateW + t0 + i] * __uint_as_float(y[i]);
+                const float kv = on ? __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(keys + kPanel + panel_at(t0 + i, row & 63))) : 0.f;
+                dots[i] = on ? dots[i] + from * kv : 0.f;
+                dots[16 + i] = on ? into * kv : 0.f;
+                dk[i] = from + into;
+            }
+            tmem_ld16(tq + kColSum + t0, x);
+            tmem_ld_wait(x);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) dk[i] += __uint_as_float(x[i]);
+            if (on) {
+                if (heads) {
+                    const size_t o = ((size_t)(token + t0) * d.heads + head) * d.n + row;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (t0 + i < valid) {
+                            a.dq_heads[o + (size_t)i * d.heads * d.n] = dq[i];
+                            a.dk_heads[o + (size_t)i * d.heads * d.n] = dk[i];
+                        }
+                } else {
+                    __nv_bfloat16 *const tq_ = a.dq + (size_t)(token + t0) * a.dq_stride + group * d.n + row;
+                    __nv_bfloat16 *const tk_ = a.dk + (size_t)(token + t0) * a.dk_stride + group * d.n + row;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (t0 + i < valid) {
+                            tq_[(size_t)i * a.dq_stride] = __float2bfloat16_rn(dq[i]);
+                            tk_[(size_t)i * a.dk_stride] = __float2bfloat16_rn(dk[i]);
+                        }
+                }
+            }
+            const float sum = lanes_transposed_sum(dots, lane);
+            scratch[(lane < 16 ? Lay::kAhead : Lay::kBehind) + 64 * q + t0 + (lane & 15)] = sum;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x < valid) {
+        const int t = threadIdx.x;
+        float whole = 0.f, dg = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) whole += scratch[Lay::kWhole + i];
+        for (int i = 0; i < valid; ++i) {
+            const float *s = scratch + i;
+            if (i >= t) {
+                const float rows = (s[Lay::kRowSum] + s[Lay::kRowSum + 64]) + (s[Lay::kRowSum + 128] + s[Lay::kRowSum + 192]);
+                const float cols = (s[Lay::kColSum] + s[Lay::kColSum + 64]) + (s[Lay::kColSum + 128] + s[Lay::kColSum + 192]);
+                dg += (rows - cols) + ((s[Lay::kAhead] + s[Lay::kAhead + 64]) + (s[Lay::kAhead + 128] + s[Lay::kAhead + 192]));
+            } else {
+                dg += (s[Lay::kBehind] + s[Lay::kBehind + 64]) + (s[Lay::kBehind + 128] + s[Lay::kBehind + 192]);
+            }
+        }
+        const size_t o = (size_t)(token + t) * d.heads + head;
+        a.dg[o] = dg + gates[kC - 1] * whole;
+        a.dbeta[o] = scratch[Lay::kDbeta + t];
+    }
+    if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+struct Plan {
+    size_t records, z, dstate, dq, dk, total;
+};
+Plan plan_of(const SsdDelta &d) {
+    const auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+    const size_t slots = (size_t)ssd_delta_slots(d.tokens, d.nseq), tokens = (size_t)d.tokens;
+    Plan p;
+    p.records = 0;
+    p.z = up(slots * d.heads * kRecord);
+    p.dstate = p.z + up(tokens * d.heads * d.p * 4);
+    p.dq = p.dstate + up(slots * d.heads * d.p * d.n * 4);
+    p.dk = p.dq + (d.heads == d.groups ? 0 : up(tokens * d.heads * d.n * 4));
+    p.total = p.dk + (d.heads == d.groups ? 0 : up(tokens * d.heads * d.n * 4));
+    return p;
+}
+
+template <int kPanels>
+cudaError_t launch(const SsdDeltaBwd &b, void *ws, int sms, unsigned *err, cudaStream_t stream) {
+    const SsdDelta &d = b.in;
+    CUtensorMap q, k, v, o;
+    if (!make_map(&q, d.q, d.n, d.groups, d.tokens, d.q_stride, 64, true) ||
+        !make_map(&k, d.k, d.n, d.groups, d.tokens, d.k_stride, 64, true) ||
+        !make_map(&v, d.v, d.p, d.heads, d.tokens, d.v_stride, 128, false) ||
+        !make_map(&o, b.dout, d.p, d.heads, d.tokens, b.do_stride, 64, true))
+        return cudaErrorInvalidValue;
+    const SsdDebug debug = ssd_debug_config();
+    const Plan plan = plan_of(d);
+    const auto at = [&](size_t offset) { return static_cast<char *>(ws) + offset; };
+    uint8_t *records = reinterpret_cast<uint8_t *>(at(plan.records));
+    float *z = reinterpret_cast<float *>(at(plan.z)), *dstate = reinterpret_cast<float *>(at(plan.dstate));
+    cudaError_t e = launch_chunks(d, records, true, sms, err, stream);
+    if (e != cudaSuccess) return e;
+    using Back = BackSmem<kPanels>;
+    using Grad = GradSmem<kPanels>;
+    static_assert(Back::kBytes <= 232448 && Grad::kBytes <= 232448, "more than 227 KB of shared memory");
+    e = cudaFuncSetAttribute(delta_back_tc_kernel<kPanels>, cudaFuncAttributeMaxDynamicSharedMemorySize, Back::kBytes);
+    if (e != cudaSuccess) return e;
+    const BackTc w{d, records, b.dfinal, static_cast<__nv_bfloat16 *>(b.dv), b.dv_stride,
+                   ((uintptr_t)b.dv & 15u) == 0 && b.dv_stride % 8 == 0, b.dinit, z, dstate, err, debug.wait_ns,
+                   debug.fault == kSsdFaultWithholdSignal};
+    delta_back_tc_kernel<kPanels><<<(unsigned)((long long)d.nseq * d.heads), kBackThreads, Back::kBytes, stream>>>(q, k, o, w);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(delta_grad_tc_kernel<kPanels>, cudaFuncAttributeMaxDynamicSharedMemorySize, Grad::kBytes);
+    if (e != cudaSuccess) return e;
+    const bool one = d.heads == d.groups;
+    const GradTc g{d, records, b.checkpoints, z, dstate, one ? static_cast<__nv_bfloat16 *>(b.dq) : nullptr,
+                   one ? static_cast<__nv_bfloat16 *>(b.dk) : nullptr, reinterpret_cast<float *>(at(plan.dq)),
+                   reinterpret_cast<float *>(at(plan.dk)), b.dq_stride, b.dk_stride, b.dg, b.dbeta, err};
+    const long long ctas = ssd_delta_slots(d.tokens, d.nseq) * d.heads;
+    delta_grad_tc_kernel<kPanels><<<(unsigned)ctas, kGradThreads, Grad::kBytes, stream>>>(q, k, v, o, g);
+    if ((e = cudaGetLastError()) != cudaSuccess || one) return e;
+    return ssd_launch_delta_group_sums(g.dq_heads, b.dq, b.dq_stride, g.dk_heads, b.dk, b.dk_stride, d, d.heads / d.groups, stream);
+}
+
+}  // namespace
+
+bool ssd_delta_tc_bwd_sizes(const SsdDelta &d) { return ssd_delta_tc_sizes(d) && d.p <= 128; }
+bool ssd_delta_tc_bwd_handles(const SsdDeltaBwd &b) {
+    return ssd_delta_tc_bwd_sizes(b.in) && ssd_delta_tc_handles(b.in) && ((uintptr_t)b.dout & 15u) == 0 && b.do_stride % 8 == 0;
+}
+size_t ssd_delta_tc_bwd_workspace(const SsdDelta &d) { return ssd_delta_tc_bwd_sizes(d) ? plan_of(d).total : 0; }
+
+cudaError_t ssd_launch_delta_bwd_tc(const SsdDeltaBwd &a, void *ws, int sms, unsigned *err, cudaStream_t stream) {
+    return a.in.n <= 64 ? launch<1>(a, ws, sms, err, stream) : launch<2>(a, ws, sms, err, stream);
+}

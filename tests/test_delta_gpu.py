@@ -150,6 +150,38 @@ def test_without_states():
         assert torch.equal(a, c)
 
 
+def test_tokens_that_write_nothing():
+    """beta 0 (padding by value): the state passes, and what would be written has a gradient."""
+    x, init, do, dfinal = inputs(17, 140, 1, 1, 2, 64, 128, "bf16")
+    x["beta"][20:40] = 0.0
+    x["beta"][139] = 0.0
+    x["beta"][60, 0] = 1e-30
+    o, final, kept = ssd.delta_scan_fwd(*batched(x, 1).values(), init, return_checkpoints=True)
+    got = ssd.delta_scan_bwd(do[None], *batched(x, 1).values(), kept, dfinal)
+    want, last, _ = ref.delta_fwd(*map(host, x.values()), host(init), [0, 140], 128 ** -0.5)
+    grad = ref.delta_bwd(host(do), *map(host, x.values()), host(init), host(dfinal), [0, 140], 128 ** -0.5)
+    assert rel(host(o)[0], want) <= BAR["bf16"] and rel(host(final), last) <= STATE["bf16"]
+    for name, g, w in zip(("dq", "dk", "dv", "dg", "dbeta", "dinit"), got, grad):
+        assert rel(host(g).reshape(w.shape), w) <= (BAR["bf16"] if name in ("dq", "dk", "dv") else STATE["bf16"]), name
+    assert rel(host(got[4])[0, 20:40], grad[4][20:40]) <= STATE["bf16"]
+
+
+def test_what_lies_behind_a_sequence_stays_there():
+    """NaN in the next sequence's tokens reaches nothing of this one."""
+    cu = [0, 70, 140]
+    x, init, do, dfinal = inputs(18, 140, 2, 1, 2, 128, 128, "bf16")
+    clean = ssd.delta_scan_fwd(*x.values(), init, cu_seqlens=cu, return_checkpoints=True)
+    grads = ssd.delta_scan_bwd(do, *x.values(), clean[2], dfinal, cu_seqlens=cu)
+    for t in (*x.values(), do):
+        t[70:] = float("nan")
+    o, final, kept = ssd.delta_scan_fwd(*x.values(), init, cu_seqlens=cu, return_checkpoints=True)
+    assert torch.equal(o[:70], clean[0][:70]) and torch.equal(final[0], clean[1][0]) and torch.isnan(final[1]).all()
+    got = ssd.delta_scan_bwd(do, *x.values(), clean[2], dfinal, cu_seqlens=cu)
+    for g, w in zip(got[:5], grads):
+        assert torch.equal(g[:70], w[:70])
+    assert torch.equal(got[5][0], grads[5][0])
+
+
 def test_the_first_part_then_the_rest():
     """A sequence cut in two gives what it gives whole: states are handed on in 32 bits."""
     x, init, _, _ = inputs(13, 320, 1, 2, 4, 128, 128, "bf16")

@@ -15,15 +15,20 @@ pytestmark = pytest.mark.gpu
 TIMEOUT = 4   # SSD_ERR_TIMEOUT
 
 
-@pytest.mark.parametrize("limit_ns", [1, 20_000, 2_000_000])
+@pytest.mark.parametrize("backward", [False, True])
+@pytest.mark.parametrize("limit_ns", [1, 3_000, 20_000, 2_000_000])
 @pytest.mark.parametrize("length,p,n", [(300, 128, 128), (40, 64, 64)])
-def test_withheld_product_times_out_then_next_call_is_correct(length, p, n, limit_ns):
-    x, init, _, _ = inputs(length, length, 1, 1, 3, p, n, "bf16")
+def test_withheld_product_times_out_then_next_call_is_correct(length, p, n, limit_ns, backward):
+    x, init, do, dfinal = inputs(length, length, 1, 1, 3, p, n, "bf16")
     b = batched(x, 1)
+    o, final, kept = ssd.delta_scan_fwd(*b.values(), init, return_checkpoints=True)
     ssd.last_device_error()                           # start from a clear error word
     ssd.debug_inject_fault(ssd.FAULT_WITHHOLD_SIGNAL, limit_ns)
     try:
-        ssd.delta_scan_fwd(*b.values(), init)         # outputs undefined
+        if backward:                                  # outputs undefined
+            ssd.delta_scan_bwd(do[None], *b.values(), kept, dfinal)
+        else:
+            ssd.delta_scan_fwd(*b.values(), init)
         torch.cuda.synchronize()
     finally:
         ssd.debug_inject_fault(ssd.FAULT_NONE, 0)
@@ -31,7 +36,12 @@ def test_withheld_product_times_out_then_next_call_is_correct(length, p, n, limi
         ssd.last_device_error()
     assert err.value.code == TIMEOUT
     ssd.last_device_error()                           # read once, then clear
-    o, final = ssd.delta_scan_fwd(*b.values(), init)
+    if backward:
+        got = ssd.delta_scan_bwd(do[None], *b.values(), kept, dfinal)
+        grads = ref.delta_bwd(host(do), *map(host, x.values()), host(init), host(dfinal), [0, length], n ** -0.5)
+        assert all(rel(host(g).reshape(w.shape), w) <= max(BAR["bf16"], STATE["bf16"]) for g, w in zip(got, grads))
+    else:
+        o, final = ssd.delta_scan_fwd(*b.values(), init)
     want, last, _ = ref.delta_fwd(*map(host, x.values()), host(init), [0, length], n ** -0.5)
     assert rel(host(o)[0], want) <= BAR["bf16"] and rel(host(final), last) <= STATE["bf16"]
     ssd.last_device_error()
