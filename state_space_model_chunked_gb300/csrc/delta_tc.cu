@@ -8,6 +8,8 @@
 //   O = scale diag(exp G) Q S^T + P U
 //   S <- exp(G_end) S + U^T diag(exp(G_end - G)) K
 //
+// (U's largest part is beta_i r_i, from T's diagonal: that is added in fp32.)
+//
 // Two kernels.  The first makes T diag(beta) and P of every chunk, all of them side by
 // side.  The second walks a sequence's chunks, one CTA a head and 128 rows of its state,
 // with the state's rows as the tensor core's lanes: S, R and U are transposed products'
@@ -332,7 +334,7 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
         float below[2][4];
         invert(columns, rows, m0, n0, below);
         __syncthreads();
-        // T diag(beta), in A's place
+        // T diag(beta) without its diagonal, in A's place
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int c = n0 + 8 * j + 2 * (lane & 3), r = 32 + m0 + (lane >> 2);
@@ -358,6 +360,9 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
                 v[4 * j + 2] = x.z * y.z;
                 v[4 * j + 3] = x.w * y.w;
             }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c + j == (r & 31)) v[j] = 0.f;
             put_parts(smem, panel_at(r, b + c), v);
         }
         {
@@ -540,7 +545,7 @@ delta_walk_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
             if (!wait.warp(bar(kRh), c & 1)) break;
             tc_fence_after();
             if (one) {
-                triangle(kColX, kColR, at + Lay::kRec + kRecT, false);
+                triangle(kColX, kColR, at + Lay::kRec + kRecT, true);
                 triangle(kColX, kColR, at + Lay::kRec + kRecT + kPanel, true);
             }
             __syncwarp();
@@ -765,6 +770,16 @@ delta_walk_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
 #pragma unroll
             for (int i = 0; i < 8; ++i) hi[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
             tmem_st8(tq + kColR + 8 * part, hi);
+            // U's own term, beta R, where the product adds the earlier tokens'
+#pragma unroll
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<float4 *>(f + 4 * i) = gates[kGateBeta / 4 + i];
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+                const float2 y = fmul2(make_float2(x[i], x[i + 1]), make_float2(f[i], f[i + 1]));
+                r[i] = __float_as_uint(y.x);
+                r[i + 1] = __float_as_uint(y.y);
+            }
+            tmem_st16(tq + kColX + 16 * part, r);
             ready(kRh);
 #pragma unroll
             for (int i = 0; i < 8; ++i) hi[i] = rest2(x[2 * i], x[2 * i + 1], hi[i]);

@@ -13,9 +13,9 @@ constexpr int kC = kSsdDeltaChunk;          // tokens a chunk
 static_assert(kC == 64, "a chunk's matrices are one 128-byte-swizzled panel wide");
 constexpr uint32_t kPanel = 64 * 128;       // 64 rows of 64 bf16 values
 
-// A chunk's record, for every head: the matrices T diag(beta) and P, each in two bf16
-// parts and each an image of a 128-byte-swizzled panel (row: the later token), then for
-// every token the decay from the chunk's start up to it, from it to the chunk's end, beta,
+// A chunk's record, for every head: the matrices T diag(beta) without its diagonal (which is
+// beta, and is multiplied in fp32) and P, each in two bf16 parts and each an image of a
+// 128-byte-swizzled panel (row: the later token), then for every token the decay from the chunk's start up to it, from it to the chunk's end, beta,
 // and log2(e) g summed from its half's first token on, in two floats.
 constexpr uint32_t kRecT = 0, kRecP = 2 * kPanel, kRecGates = 4 * kPanel;
 constexpr int kGateW = kC, kGateBeta = 2 * kC, kGateSums = 3 * kC, kGates = 5 * kC;

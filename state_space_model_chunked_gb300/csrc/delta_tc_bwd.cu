@@ -3,7 +3,7 @@
 // of the state behind it, and T, P, R, U as there:
 //
 //   dU = P^T dO + diag(exp(G_end - G)) K dS^T
-//   Z  = (T diag(beta))^T dU                       (the gradient of V)
+//   Z  = (T diag(beta))^T dU                       (the gradient of V; its diagonal's part in fp32)
 //   dS <- exp(G_end) dS + (diag(scale exp G) dO)^T Q - (diag(exp G) Z)^T K
 //
 // is a walk over the chunks, from the last one on (the first kernel: one CTA a head, the
@@ -13,7 +13,7 @@
 //   dP_ij = scale D_ij M1_ij (j <= i)       dA_ij = -D_ij M2_ij (j < i)
 //   dQ = scale diag(exp G) dO S + dP K
 //   dK = -diag(exp G) Z S + diag(exp(G_end - G)) U dS + dP^T Q + dA K + dA^T K
-//   dbeta_i = M2_ii / beta_i^2
+//   dbeta_i = z_i . u_i / beta_i^2
 //   dg_t = exp(G_end) <S, dS> + sum_(i >= t) (what token i reads of S, dotted with it)
 //        + sum_(j < t) (what token j leaves in dS) + sum_(i >= t > j) (dP o QK + dA o KK)_ij
 //
@@ -205,7 +205,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
             if (!wait.warp(bar(kRh), it & 1)) break;
             tc_fence_after();
             if (one) {
-                triangle(kColR, at + Lay::kRec + kRecT, false);
+                triangle(kColR, at + Lay::kRec + kRecT, true);
                 triangle(kColR, at + Lay::kRec + kRecT + kPanel, true);
             }
             __syncwarp();
@@ -420,6 +420,16 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
 #pragma unroll
             for (int i = 0; i < 8; ++i) hi[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
             tmem_st8(tq + kColR + 8 * part, hi);
+            // Z's own term, beta dU, where the product adds the later tokens'
+#pragma unroll
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<float4 *>(f + 4 * i) = gates[kGateBeta / 4 + i];
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+                const float2 u = fmul2(make_float2(x[i], x[i + 1]), make_float2(f[i], f[i + 1]));
+                r[i] = __float_as_uint(u.x);
+                r[i + 1] = __float_as_uint(u.y);
+            }
+            tmem_st16(tq + kColX + 16 * part, r);
             ready(kRh);
 #pragma unroll
             for (int i = 0; i < 8; ++i) hi[i] = rest2(x[2 * i], x[2 * i + 1], hi[i]);
@@ -708,6 +718,7 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
                 const int t = 2 * i + j;
                 x[j] = __bfloat162float(v[t * 128]) - gates[32 * half + t] * __uint_as_float(r[t]);
                 if (32 * half + t >= valid) x[j] = 0.f;
+                r[t] = __float_as_uint(x[j] * gates[kGateBeta + 32 * half + t]);
             }
             const Split y = split2(x[0], x[1]);
             hi[i] = y.hi;
@@ -715,21 +726,29 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         }
         tmem_st16(tq + kColR + 16 * half, hi);
         tmem_st16(tq + kColRl + 16 * half, lo);
+        tmem_st32(tq + kColU + 32 * half, r);
         tmem_st_wait();
     }
     before();
     if (issuer && elect_one()) {
-        const auto triangle = [&](uint32_t acol, uint32_t tile, bool add) {
+        const auto triangle = [&](uint32_t acol, uint32_t tile) {
             const uint64_t bd = smem_desc(tile, 16, 1024, kSwizzle128B);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 mma_ts(tmem + kColU + 16 * k, tmem + acol + 8 * k, bd + kStepK * k + kStepMn * k,
-                       idesc_bf16_f32(128, 64 - 16 * k, false, false), add || k > 0);
+                       idesc_bf16_f32(128, 64 - 16 * k, false, false), 1);
         };
-        triangle(kColR, w + 2 * kPanel, false);
-        triangle(kColR, w + 3 * kPanel, true);
-        triangle(kColRl, w + 2 * kPanel, true);
+        triangle(kColR, w + 2 * kPanel);
+        triangle(kColR, w + 3 * kPanel);
+        triangle(kColRl, w + 2 * kPanel);
         mma_commit(done);
+    }
+    // Z as it is, for its products with U: dbeta (their parts' product would lose some of it)
+    float zu[32], own;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const int t = 32 * half + i;
+        zu[i] = t < valid && row < d.p ? __ldcs(a.z + ((size_t)(token + t) * d.heads + head) * d.p + row) : 0.f;
     }
     after();
     // U by tokens
@@ -737,6 +756,9 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         uint32_t r[32];
         tmem_ld32(tq + kColU + 32 * half, r);
         tmem_ld_wait(r);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) zu[i] *= __uint_as_float(r[i]);
+        own = lanes_transposed_sum(zu, lane);
         uint8_t *const to = smem + Lay::kU + (row >> 6) * kPanel;
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
@@ -791,15 +813,12 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
             v[j] = in ? factor * ex2_approx(g) * __uint_as_float(m[j]) : 0.f;
             e[j] = in && j0 + j < r ? v[j] * __uint_as_float(x[j]) : 0.f;
             sum += e[j];
-            if (keys && j0 + j == r) {
-                const float be = gates[kGateBeta + r];
-                scratch[Lay::kDbeta + r] = __uint_as_float(m[j]) / be / be;
-            }
         }
         uint8_t *const to = smem + Lay::kW + (keys ? 2 * kPanel : 0);
 #pragma unroll
         for (int j = 0; j < 32; j += 8) put_parts(to, panel_at(r, j0 + j), v + j);
         scratch[Lay::kRowSum + (keys ? 128 : 0) + 64 * half + r] = sum;
+        scratch[Lay::kDbeta + 64 * q + j0 + lane] = own;
         const float col = lanes_transposed_sum(e, lane);
         scratch[Lay::kColSum + (keys ? 128 : 0) + 64 * (q & 1) + j0 + lane] = col;
     }
@@ -923,7 +942,8 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         }
         const size_t o = (size_t)(token + t) * d.heads + head;
         a.dg[o] = dg + gates[kC - 1] * whole;
-        a.dbeta[o] = scratch[Lay::kDbeta + t];
+        const float *own = scratch + Lay::kDbeta + t, be = gates[kGateBeta + t];
+        a.dbeta[o] = ((own[0] + own[64]) + (own[128] + own[192])) / be / be;
     }
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
