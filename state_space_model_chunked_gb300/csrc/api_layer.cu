@@ -639,7 +639,7 @@ ssd_status ssd_delta_scan_fwd(const void *q, const void *k, const void *v, const
     a.o_stride = o_stride;
     a.final_state = final_state;
     a.checkpoints = checkpoints;
-    if (ssd_delta_tc_handles(a.in))
+    if (ssd_delta_tc_handles(a))
         return launched(ssd_launch_delta_fwd_tc(a, workspace, ssd_sm_count(), ssd_device_error_word(), stream));
     return launched(ssd_launch_delta_fwd_simt(a, ssd_sm_count(), stream));
 }

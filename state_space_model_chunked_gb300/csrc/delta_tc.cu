@@ -400,7 +400,8 @@ struct WalkSmem {
     static constexpr uint32_t kV = kRec + kRecord;      // [token][128], as they lie
     static constexpr uint32_t kStage = (kV + 64 * 256 + 1023) / 1024 * 1024;
     static constexpr uint32_t kO = 2 * kStage;          // [token][128]: the output on its way
-    static constexpr uint32_t kCtl = kO + 64 * 256;
+    static constexpr uint32_t kRows = kO + 64 * 256;    // states on their way, by warps
+    static constexpr uint32_t kCtl = kRows + kChainWarps * kStageRows;
     static constexpr uint32_t kBytes = kCtl + 256;
 };
 
@@ -674,20 +675,9 @@ delta_walk_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16);
         constexpr int kMine = kN / 4;
         const int n0 = part * kMine;
-        const bool vec = d.n % 4 == 0;
         const auto to_memory = [&](float *m, const float (&v)[kMine]) {
-            if (p >= d.p) return;
-            float *to = m + (size_t)p * d.n;
-#pragma unroll
-            for (int i = 0; i < kMine; i += 4) {
-                const int n = n0 + i;
-                if (vec) {
-                    if (n < d.n) *reinterpret_cast<float4 *>(to + n) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-                } else {
-                    for (int j = 0; j < 4; ++j)
-                        if (n + j < d.n) to[n + j] = v[i + j];
-                }
-            }
+            store_rows<kMine>(reinterpret_cast<float *>(smem + Lay::kRows + warp * kStageRows), v,
+                              m + (size_t)(p0 + 32 * q) * d.n + n0, d.n, d.p - (p0 + 32 * q), d.n - n0);
         };
         // what this thread wrote to tensor memory is there for the products
         const auto ready = [&](int which) {
@@ -906,10 +896,13 @@ cudaError_t launch_chunks(const SsdDelta &d, uint8_t *records, bool least_beta, 
 bool ssd_delta_tc_sizes(const SsdDelta &d) {
     return d.bf16 && d.n <= 128 && d.n % 8 == 0 && d.p % 8 == 0 && d.tokens > 0;
 }
-bool ssd_delta_tc_handles(const SsdDelta &d) {
-    const auto rows_ok = [](const void *p, long long stride) { return ((uintptr_t)p & 15u) == 0 && stride % 8 == 0; };
+bool ssd_delta_tc_inputs(const SsdDelta &d) {
+    const auto rows_ok = [](const void *p, long long stride) { return on_16(p) && stride % 8 == 0; };
     return ssd_delta_tc_sizes(d) && rows_ok(d.q, d.q_stride) && rows_ok(d.k, d.k_stride) && rows_ok(d.v, d.v_stride) &&
            ssd_tensor_map_encoder() != nullptr;
+}
+bool ssd_delta_tc_handles(const SsdDeltaFwd &a) {
+    return ssd_delta_tc_inputs(a.in) && on_16(a.init) && on_16(a.final_state) && on_16(a.checkpoints);
 }
 
 size_t ssd_delta_tc_workspace(const SsdDelta &d) {

@@ -2,6 +2,8 @@
 // workspace, its layout in shared memory, and small device helpers.
 #pragma once
 
+#include <stdint.h>
+
 #include "launch.h"
 #include "ptx.cuh"
 
@@ -122,6 +124,33 @@ __device__ __forceinline__ void clean_rows(uint8_t *panels, uint32_t stride, int
     for (int i = thread; i < count * each; i += threads)
         *reinterpret_cast<uint4 *>(panels + (i / each) * stride + tokens * 128 + (i % each) * 16) = make_uint4(0, 0, 0, 0);
 }
+
+// A warp's 32 rows of kMine fp32 values, a row a lane, to rows `n` apart (those below
+// `rows`, columns below `cols`), by way of 2 KB of the warp's own: a lane that wrote its own
+// row would touch a line for every 16 bytes (a state of 128 x 128 took 8000 cycles).
+template <int kMine>
+__device__ __forceinline__ void store_rows(float *stage, const float (&v)[kMine], float *to, int n, int rows, int cols) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int h = 0; h < kMine / 16; ++h) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float4 *>(stage + lane * 16 + ((i ^ (lane >> 1)) & 3) * 4) =
+                make_float4(v[16 * h + 4 * i], v[16 * h + 4 * i + 1], v[16 * h + 4 * i + 2], v[16 * h + 4 * i + 3]);
+        __syncwarp();
+        const int c = (lane & 3) * 4 + 16 * h;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = 8 * j + (lane >> 2);
+            const float4 x = *reinterpret_cast<const float4 *>(stage + r * 16 + ((lane ^ (r >> 1)) & 3) * 4);
+            if (r < rows && c < cols) *reinterpret_cast<float4 *>(to + (size_t)r * n + c) = x;
+        }
+    }
+}
+constexpr uint32_t kStageRows = 2048;       // bytes a warp
+
+inline bool on_16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
 // The records of all chunks (delta_tc.cu); least_beta: see kLeastBeta.
 cudaError_t launch_chunks(const SsdDelta &d, uint8_t *records, bool least_beta, int sms, unsigned *err,

@@ -44,7 +44,8 @@ struct BackSmem {
     static constexpr uint32_t kK = 0, kQ = kPanels * kPanel, kDo = 2 * kPanels * kPanel, kRec = kDo + 2 * kPanel;
     static constexpr uint32_t kStage = (kRec + kRecord + 1023) / 1024 * 1024;
     static constexpr uint32_t kOut = 2 * kStage;        // [token][128]: dV on its way
-    static constexpr uint32_t kCtl = kOut + 64 * 256;
+    static constexpr uint32_t kRows = kOut + 64 * 256;  // dS on its way, by warps
+    static constexpr uint32_t kCtl = kRows + kChainWarps * kStageRows;
     static constexpr uint32_t kBytes = kCtl + 256;
 };
 
@@ -328,20 +329,9 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16);
         constexpr int kMine = kN / 4;
         const int n0 = part * kMine;
-        const bool vec = d.n % 4 == 0;
         const auto to_memory = [&](float *m, const float (&v)[kMine]) {
-            if (p >= d.p) return;
-            float *to = m + (size_t)p * d.n;
-#pragma unroll
-            for (int i = 0; i < kMine; i += 4) {
-                const int n = n0 + i;
-                if (vec) {
-                    if (n < d.n) *reinterpret_cast<float4 *>(to + n) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-                } else {
-                    for (int j = 0; j < 4; ++j)
-                        if (n + j < d.n) to[n + j] = v[i + j];
-                }
-            }
+            store_rows<kMine>(reinterpret_cast<float *>(smem + Lay::kRows + warp * kStageRows), v,
+                              m + (size_t)(32 * q) * d.n + n0, d.n, d.p - 32 * q, d.n - n0);
         };
         const auto ready = [&](int which) {
             tmem_st_wait();
@@ -484,8 +474,9 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
 
 // ------------------------------------------------------ a chunk's other gradients
 // Steps of products and of elementwise work by turns, all warps together: with 224 KB of
-// tiles one CTA an SM, whose products (about 150 of M = 128, N = 64) take longest.
-constexpr int kGradThreads = 256;
+// tiles one CTA an SM.  What is loaded first (a state, Z) is asked for at once, and what the
+// CTA that comes next on this SM will load is brought into L2 meanwhile.
+constexpr int kGradWarps = 16, kGradThreads = 32 * kGradWarps;
 constexpr uint32_t kTall = 2 * kPanel;      // a panel of 128 rows
 template <int kPanels>
 struct GradSmem {
@@ -499,7 +490,7 @@ struct GradSmem {
     static constexpr uint32_t kGatesAt = kCtl + 64;
     static constexpr uint32_t kBytes = kGatesAt + kGates * 4;
     // scratch, where dO and Z were (floats)
-    static constexpr int kRowSum = 0, kColSum = 256, kAhead = 512, kBehind = 768, kWhole = 1024, kDbeta = 1040;
+    static constexpr int kRowSum = 0, kColSum = 512, kAhead = 768, kBehind = 1024, kDbeta = 1280, kWhole = 1536;
 };
 
 struct GradTc {
@@ -510,13 +501,20 @@ struct GradTc {
     float *dq_heads, *dk_heads;         // [token][head][N]
     long long dq_stride, dk_stride;
     float *dg, *dbeta;
+    int ahead;                          // how many CTAs on the next on an SM is
     unsigned *err;
 };
 
-// The sums over the warp's lanes of 32 values a lane, lane l's answer that of value l.
-__device__ __forceinline__ float lanes_transposed_sum(float (&v)[32], int lane) {
+// The sums over the warp's lanes of kCount (16 or 32) values a lane: lane l's answer is that
+// of value l % kCount.
+template <int kCount>
+__device__ __forceinline__ float lanes_transposed_sum(float (&v)[kCount], int lane) {
+    if constexpr (kCount == 16) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+        for (int i = 0; i < 16; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
+    }
+#pragma unroll
+    for (int o = kCount / 2; o > 0; o >>= 1) {
         const bool up = lane & o;
 #pragma unroll
         for (int i = 0; i < o; ++i) {
@@ -535,7 +533,7 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
     using Lay = GradSmem<kPanels>;
     const SsdDelta &d = a.d;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int q = warp & 3, half = warp >> 2;       // lanes of tensor memory, half of the columns
+    const int q = warp & 3, c0 = 16 * (warp >> 2);      // lanes of tensor memory, and the warp's columns
     const uint32_t base = smem_u32(smem);
     if (base & 1023u) {
         if (threadIdx.x == 0) ssd_report(a.err, SSD_DEVERR_SMEM_ALIGN);
@@ -554,16 +552,6 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         mbar_init(full, 1);
         mbar_init(done, 1);
         fence_mbar_init();
-    }
-    if (warp == 0) {
-        tmem_alloc(smem_u32(tslot), 512);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tslot, tq = tmem + ((uint32_t)(32 * q) << 16);
-    if (threadIdx.x == 0) {
         mbar_arrive_expect_tx(full, kPanels * kTall + 2 * kPanel + 64 * 256 + 2 * kPanel + kGates * 4);
         const int t = (int)token;
 #pragma unroll
@@ -578,22 +566,10 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         bulk_load(base + Lay::kGatesAt, a.records + record * kRecord + kRecGates, kGates * 4, full);
     }
     // a state's row by a warp: lane l has the columns 4 l .. 4 l + 3; a part's panel is tall
-    const bool vec = d.n % 4 == 0;
+    const bool mine = 4 * lane < d.n;
     const auto load_state = [&](const float *m, int row) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int n = 4 * lane;
-        if (row < d.p && n < d.n) {
-            const float *from = m + (size_t)row * d.n + n;
-            if (vec) {
-                v = __ldcs(reinterpret_cast<const float4 *>(from));
-            } else {
-                v.x = from[0];
-                if (n + 1 < d.n) v.y = from[1];
-                if (n + 2 < d.n) v.z = from[2];
-                if (n + 3 < d.n) v.w = from[3];
-            }
-        }
-        return v;
+        return mine && row < d.p ? __ldcs(reinterpret_cast<const float4 *>(m + (size_t)row * d.n + 4 * lane))
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
     };
     const uint32_t state_panel = Lay::kSs + (uint32_t)(lane >> 4) * kTall;
     const auto store_state = [&](int row, float4 v) {
@@ -604,34 +580,40 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         *reinterpret_cast<uint2 *>(smem + to + kPanels * kTall) = make_uint2(x.lo, y.lo);
     };
     {
-        const float *from = a.checkpoints + record * size;
-#pragma unroll 1
-        for (int r0 = 16 * warp; r0 < 16 * warp + 16; r0 += 8) {
-            float4 v[8];
+        float4 v[8], z[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = load_state(from, r0 + i);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) store_state(r0 + i, v[i]);
-        }
+        for (int i = 0; i < 8; ++i) v[i] = load_state(a.checkpoints + record * size, 8 * warp + i);
         // Z, a token a row
-        float4 z[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int t = 8 * warp + i, p = 4 * lane;
+        for (int i = 0; i < 4; ++i) {
+            const int t = 4 * warp + i, p = 4 * lane;
             z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (t < valid && p < d.p)       // (P is a multiple of 8)
-                z[i] = __ldcs(reinterpret_cast<const float4 *>(a.z + ((size_t)(token + t) * d.heads + head) * d.p + p));
+                z[i] = *reinterpret_cast<const float4 *>(a.z + ((size_t)(token + t) * d.heads + head) * d.p + p);
         }
+        if (warp == 1) {
+            tmem_alloc(smem_u32(tslot), 512);
+            tmem_relinquish();
+        }
+        const long long next = (long long)blockIdx.x + a.ahead;
+        if (warp == 2 && lane < 2 && next < gridDim.x)
+            bulk_prefetch_l2((lane ? a.dstate : a.checkpoints) + (size_t)next * size, (uint32_t)(size * 4));
+        for (int i = threadIdx.x; i < 1024; i += kGradThreads)
+            *reinterpret_cast<uint4 *>(smem + Lay::kAl + (i >> 9) * kTall + (i & 511) * 16) = make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t to = (uint32_t)(lane >> 4) * kTall + panel_at(64 + 8 * warp + i, (4 * lane) & 63);
+        for (int i = 0; i < 8; ++i) store_state(8 * warp + i, v[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t to = (uint32_t)(lane >> 4) * kTall + panel_at(64 + 4 * warp + i, (4 * lane) & 63);
             const Split x = split2(z[i].x, z[i].y), y = split2(z[i].z, z[i].w);
             *reinterpret_cast<uint2 *>(smem + Lay::kAh + to) = make_uint2(x.hi, y.hi);
             *reinterpret_cast<uint2 *>(smem + Lay::kAl + to) = make_uint2(x.lo, y.lo);
         }
-        for (int i = threadIdx.x; i < 1024; i += kGradThreads)
-            *reinterpret_cast<uint4 *>(smem + Lay::kAl + (i >> 9) * kTall + (i & 511) * 16) = make_uint4(0, 0, 0, 0);
     }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot, tq = tmem + ((uint32_t)(32 * q) << 16);
     // (waits for the CTA's own copies and products)
     if (!mbar_wait(full, 0, kSsdDefaultWaitNs)) ssd_report(a.err, SSD_DEVERR_TIMEOUT);
     clean_rows(smem + Lay::kQk, kPanel, 2 * kPanels, valid, threadIdx.x, kGradThreads);
@@ -651,9 +633,10 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         phase ^= 1;
         tc_fence_after();
     };
-    constexpr uint32_t kId = idesc_bf16_f32(128, 64, false, false), kIdMn = idesc_bf16_f32(128, 64, true, false);
+    constexpr uint32_t kId = idesc_bf16_f32(128, 64, false, false);
     constexpr uint32_t kColU = 0, kColQk = 64, kColM = 128, kColDoS = 192, kColZs = 256, kColPk = 320, kColSum = 384,
                        kColUs = 448, kColR = 448, kColRl = 480;
+    static_assert(kColZs == kColDoS + 64, "one product of 128 columns");
     const uint32_t sh = base + Lay::kSs, sl = sh + kPanels * kTall, ah = base + Lay::kAh, al = base + Lay::kAl;
     const uint32_t uh = base + Lay::kU, ul = uh + 2 * kPanel, w = base + Lay::kW, qk = base + Lay::kQk;
     // D (+)= A B^T over `panels` of 64 columns: A by tall panels, B by panels `bstep` apart
@@ -665,17 +648,17 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
             for (int k = 0; k < 4; ++k) mma_ss(tmem + dcol, ad + kStepK * k, bd + kStepK * k, kId, add || p + k > 0);
         }
     };
-    // D (+)= A^T B^T: A [128 of P][N] by tall panels of N, B [64][P] by panels `bstep` apart
-    const auto cols_rows = [&](uint32_t dcol, uint32_t at_a, uint32_t at_b, uint32_t bstep, bool add) {
+    // D (+)= A^T B^T: A [128 of P][N] by tall panels of N, B [rows][P] by panels `bstep` apart
+    const auto cols_rows = [&](uint32_t dcol, uint32_t at_a, uint32_t at_b, uint32_t bstep, uint32_t id, bool add) {
         const uint64_t ad = smem_desc(at_a, kTall, 1024, kSwizzle128B);
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
             const uint64_t bd = smem_desc(at_b + p * bstep, 16, 1024, kSwizzle128B);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                mma_ss(tmem + dcol, ad + kStepMn * (4 * p + k), bd + kStepK * k, kIdMn, add || p + k > 0);
+            for (int k = 0; k < 4; ++k) mma_ss(tmem + dcol, ad + kStepMn * (4 * p + k), bd + kStepK * k, id, add || p + k > 0);
         }
     };
+    constexpr uint32_t kIdMn = idesc_bf16_f32(128, 64, true, false), kIdMnWide = idesc_bf16_f32(128, 128, true, false);
     // D (+)= A^T M^T (columns of D from 16 k on) and A^T M (up to 16 k + 15) of a lower
     // triangular M [64][64], A [64][N]
     const auto tokens_lower = [&](uint32_t dcol, uint32_t at_a, uint32_t at_m, bool add) {
@@ -702,31 +685,36 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         rows_rows(kColQk, qk, qk + kPanel, kTall, kPanels, false);
         mma_commit(done);
     }
-    after();
-    // R, as the left operand of U
     const int row = 32 * q + lane;
-    {
-        uint32_t r[32], hi[16], lo[16];
-        tmem_ld32(tq + kColU + 32 * half, r);
-        tmem_ld_wait(r);
-        const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(smem + Lay::kW) + 32 * half * 128 + row;
+    // Z as it is, for its products with U: dbeta (their parts' product would lose some of it)
+    float zu[16], own;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < 16; ++i)
+        zu[i] = c0 + i < valid && row < d.p ? a.z[((size_t)(token + c0 + i) * d.heads + head) * d.p + row] : 0.f;
+    after();
+    // R, as the left operand of U, and beta R, to which that product is added
+    {
+        uint32_t r[16], hi[8], lo[8];
+        tmem_ld16(tq + kColU + c0, r);
+        tmem_ld_wait(r);
+        const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(smem + Lay::kW) + c0 * 128 + row;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
             float x[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int t = 2 * i + j;
-                x[j] = __bfloat162float(v[t * 128]) - gates[32 * half + t] * __uint_as_float(r[t]);
-                if (32 * half + t >= valid) x[j] = 0.f;
-                r[t] = __float_as_uint(x[j] * gates[kGateBeta + 32 * half + t]);
+                x[j] = __bfloat162float(v[t * 128]) - gates[c0 + t] * __uint_as_float(r[t]);
+                if (c0 + t >= valid) x[j] = 0.f;
+                r[t] = __float_as_uint(x[j] * gates[kGateBeta + c0 + t]);
             }
             const Split y = split2(x[0], x[1]);
             hi[i] = y.hi;
             lo[i] = y.lo;
         }
-        tmem_st16(tq + kColR + 16 * half, hi);
-        tmem_st16(tq + kColRl + 16 * half, lo);
-        tmem_st32(tq + kColU + 32 * half, r);
+        tmem_st8(tq + kColR + c0 / 2, hi);
+        tmem_st8(tq + kColRl + c0 / 2, lo);
+        tmem_st16(tq + kColU + c0, r);
         tmem_st_wait();
     }
     before();
@@ -742,32 +730,31 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         triangle(kColR, w + 3 * kPanel);
         triangle(kColRl, w + 2 * kPanel);
         mma_commit(done);
-    }
-    // Z as it is, for its products with U: dbeta (their parts' product would lose some of it)
-    float zu[32], own;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const int t = 32 * half + i;
-        zu[i] = t < valid && row < d.p ? __ldcs(a.z + ((size_t)(token + t) * d.heads + head) * d.p + row) : 0.f;
+        // (dO S)^T beside (Z S)^T, while U goes to shared memory
+        cols_rows(kColDoS, sh, ah, kTall, kIdMnWide, false);
+        cols_rows(kColDoS, sl, ah, kTall, kIdMnWide, true);
+        cols_rows(kColZs, sh, al + kPanel, kTall, kIdMn, true);
     }
     after();
     // U by tokens
     {
-        uint32_t r[32];
-        tmem_ld32(tq + kColU + 32 * half, r);
+        uint32_t r[16];
+        tmem_ld16(tq + kColU + c0, r);
         tmem_ld_wait(r);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) zu[i] *= __uint_as_float(r[i]);
-        own = lanes_transposed_sum(zu, lane);
         uint8_t *const to = smem + Lay::kU + (row >> 6) * kPanel;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const float x = __uint_as_float(r[i]);
-            const __nv_bfloat16 h = __float2bfloat16_rn(x);
-            const uint32_t o = panel_at(32 * half + i, row & 63);
-            *reinterpret_cast<__nv_bfloat16 *>(to + o) = h;
-            *reinterpret_cast<__nv_bfloat16 *>(to + 2 * kPanel + o) = __float2bfloat16_rn(x - __bfloat162float(h));
+        for (int i = 0; i < 16; i += 2) {
+            const Split x = split2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+            zu[i] *= __uint_as_float(r[i]);
+            zu[i + 1] *= __uint_as_float(r[i + 1]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t o = panel_at(c0 + i + j, row & 63);
+                *reinterpret_cast<uint16_t *>(to + o) = (uint16_t)(x.hi >> (16 * j));
+                *reinterpret_cast<uint16_t *>(to + 2 * kPanel + o) = (uint16_t)(x.lo >> (16 * j));
+            }
         }
+        own = lanes_transposed_sum(zu, lane);
     }
     before();
     if (issuer && elect_one()) {
@@ -775,73 +762,65 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         rows_rows(kColM, ah, uh, kPanel, 2, false);
         rows_rows(kColM, ah, ul, kPanel, 2, true);
         rows_rows(kColM, al, uh, kPanel, 2, true);
-        // (dO S)^T and (Z S)^T
-        cols_rows(kColDoS, sh, ah, kTall, false);
-        cols_rows(kColDoS, sl, ah, kTall, true);
-        cols_rows(kColZs, sh, ah + kPanel, kTall, false);
-        cols_rows(kColZs, sl, ah + kPanel, kTall, true);
-        cols_rows(kColZs, sh, al + kPanel, kTall, true);
         mma_commit(done);
     }
     // dS on its way beside the products
     const float *const dstate = a.dstate + record * size;
     float4 ds[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ds[i] = load_state(dstate, 16 * warp + i);
+    for (int i = 0; i < 8; ++i) ds[i] = load_state(dstate, 8 * warp + i);
     after();
     // dP (lanes 0 .. 63) and dA (64 .. 127), a row a lane; and what pairs of tokens add to dg
     {
-        const int r = row & 63, j0 = 32 * half;
+        const int r = row & 63;
         const bool keys = q >= 2;
-        uint32_t m[32], x[32];
-        tmem_ld32(tq + kColM + j0, m);
-        tmem_ld32(tq + kColQk + j0, x);
+        uint32_t m[16], x[16];
+        tmem_ld16(tq + kColM + c0, m);
+        tmem_ld16(tq + kColQk + c0, x);
         const float2 *sums = reinterpret_cast<const float2 *>(gates + kGateSums);
-        const float2 mine = sums[r], whole = sums[31];
-        const bool over = r >= 32 && half == 0;
+        const float2 mine_ = sums[r], whole = sums[31];
+        const bool over = r >= 32 && c0 < 32;       // from the first half of the tokens to the second
         const int last = r < valid ? (keys ? r - 1 : r) : -1;
         const float factor = keys ? -1.f : d.scale;
         tmem_ld_wait(m);
         tmem_ld_wait(x);
-        float v[32], e[32], sum = 0.f;
+        float v[16], e[16], sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            const float2 c = sums[j0 + j];
-            float g = (mine.x - c.x) + (mine.y - c.y);
-            if (over) g = (mine.x + mine.y) + ((whole.x - c.x) + (whole.y - c.y));
-            const bool in = j0 + j <= last;
+        for (int j = 0; j < 16; ++j) {
+            const float2 c = sums[c0 + j];
+            const float g = over ? (mine_.x + mine_.y) + ((whole.x - c.x) + (whole.y - c.y))
+                                 : (mine_.x - c.x) + (mine_.y - c.y);
+            const bool in = c0 + j <= last;
             v[j] = in ? factor * ex2_approx(g) * __uint_as_float(m[j]) : 0.f;
-            e[j] = in && j0 + j < r ? v[j] * __uint_as_float(x[j]) : 0.f;
+            e[j] = in && c0 + j < r ? v[j] * __uint_as_float(x[j]) : 0.f;
             sum += e[j];
         }
         uint8_t *const to = smem + Lay::kW + (keys ? 2 * kPanel : 0);
-#pragma unroll
-        for (int j = 0; j < 32; j += 8) put_parts(to, panel_at(r, j0 + j), v + j);
-        scratch[Lay::kRowSum + (keys ? 128 : 0) + 64 * half + r] = sum;
-        scratch[Lay::kDbeta + 64 * q + j0 + lane] = own;
+        put_parts(to, panel_at(r, c0), v);
+        put_parts(to, panel_at(r, c0 + 8), v + 8);
+        scratch[Lay::kRowSum + (keys ? 256 : 0) + 4 * c0 + r] = sum;
         const float col = lanes_transposed_sum(e, lane);
-        scratch[Lay::kColSum + (keys ? 128 : 0) + 64 * (q & 1) + j0 + lane] = col;
+        if (lane < 16) {
+            scratch[Lay::kColSum + (keys ? 128 : 0) + 64 * (q & 1) + c0 + lane] = col;
+            scratch[Lay::kDbeta + 64 * q + c0 + lane] = own;
+        }
     }
     // dS in S's place, and <S, dS>
     {
         float dot = 0.f;
-        const auto swap = [&](int r, float4 v) {
-            if (64 * kPanels <= 4 * lane) return;
-            const uint32_t to = state_panel + panel_at(r, (4 * lane) & 63);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (64 * kPanels <= 4 * lane) continue;
+            const float4 v = ds[i];
+            const uint32_t to = state_panel + panel_at(8 * warp + i, (4 * lane) & 63);
             const uint2 h = *reinterpret_cast<const uint2 *>(smem + to);
             const uint2 l = *reinterpret_cast<const uint2 *>(smem + to + kPanels * kTall);
             const auto low = [](uint32_t x) { return __uint_as_float(x << 16); };
             const auto high = [](uint32_t x) { return __uint_as_float(x & 0xffff0000u); };
             dot += (low(h.x) + low(l.x)) * v.x + (high(h.x) + high(l.x)) * v.y + (low(h.y) + low(l.y)) * v.z +
                    (high(h.y) + high(l.y)) * v.w;
-            store_state(r, v);
-        };
-#pragma unroll
-        for (int i = 0; i < 8; ++i) swap(16 * warp + i, ds[i]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ds[i] = load_state(dstate, 16 * warp + 8 + i);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) swap(16 * warp + 8 + i, ds[i]);
+            store_state(8 * warp + i, v);
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
         if (lane == 0) scratch[Lay::kWhole + warp] = dot;
@@ -856,96 +835,116 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
             tokens_lower(kColSum, qk + kPanel, da, true);
             tokens_upper(kColSum, qk + kPanel, da, true);
         }
-        cols_rows(kColUs, sh, uh, kPanel, false);
-        cols_rows(kColUs, sl, uh, kPanel, true);
-        cols_rows(kColUs, sh, ul, kPanel, true);
+        cols_rows(kColUs, sh, uh, kPanel, kIdMn, false);
+        cols_rows(kColUs, sl, uh, kPanel, kIdMn, true);
+        cols_rows(kColUs, sh, ul, kPanel, kIdMn, true);
         mma_commit(done);
     }
-    after();
-    // a lane is a column of dQ and dK; what a token reads of S and leaves in dS
+    // meanwhile what tokens read of S, dotted with them: a lane is a column of dQ and dK
+    const bool on = row < d.n;
+    const uint8_t *const keys = smem + Lay::kQk + (row >> 6) * kTall;
+    float dots[32], dq[16], dk[16];
     {
-        const bool on = row < d.n;
-        const bool heads = a.dq == nullptr;
-        const uint8_t *const keys = smem + Lay::kQk + (row >> 6) * kTall;
-#pragma unroll 1
-        for (int b = 0; b < 2; ++b) {
-            const int t0 = 32 * half + 16 * b;
-            uint32_t x[16], y[16];
-            float dots[32], dq[16], dk[16];
-            tmem_ld16(tq + kColDoS + t0, x);
-            tmem_ld16(tq + kColPk + t0, y);
-            tmem_ld_wait(x);
-            tmem_ld_wait(y);
+        uint32_t x[16], y[16];
+        tmem_ld16(tq + kColDoS + c0, x);
+        tmem_ld16(tq + kColZs + c0, y);
+        tmem_ld_wait(x);
+        tmem_ld_wait(y);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float from = d.scale * gates[t0 + i] * __uint_as_float(x[i]);
-                const float qv = on ? __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(keys + panel_at(t0 + i, row & 63))) : 0.f;
-                dots[i] = on ? from * qv : 0.f;
-                dq[i] = from + __uint_as_float(y[i]);
-            }
-            tmem_ld16(tq + kColZs + t0, x);
-            tmem_ld16(tq + kColUs + t0, y);
-            tmem_ld_wait(x);
-            tmem_ld_wait(y);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float from = -gates[t0 + i] * __uint_as_float(x[i]), into = gates[kGateW + t0 + i] * __uint_as_float(y[i]);
-                const float kv = on ? __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(keys + kPanel + panel_at(t0 + i, row & 63))) : 0.f;
-                dots[i] = on ? dots[i] + from * kv : 0.f;
-                dots[16 + i] = on ? into * kv : 0.f;
-                dk[i] = from + into;
-            }
-            tmem_ld16(tq + kColSum + t0, x);
-            tmem_ld_wait(x);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) dk[i] += __uint_as_float(x[i]);
+        for (int i = 0; i < 16; ++i) {
+            dq[i] = d.scale * gates[c0 + i] * __uint_as_float(x[i]);
+            dk[i] = -gates[c0 + i] * __uint_as_float(y[i]);
+            dots[i] = dots[16 + i] = 0.f;
             if (on) {
-                if (heads) {
-                    const size_t o = ((size_t)(token + t0) * d.heads + head) * d.n + row;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (t0 + i < valid) {
-                            a.dq_heads[o + (size_t)i * d.heads * d.n] = dq[i];
-                            a.dk_heads[o + (size_t)i * d.heads * d.n] = dk[i];
-                        }
-                } else {
-                    __nv_bfloat16 *const tq_ = a.dq + (size_t)(token + t0) * a.dq_stride + group * d.n + row;
-                    __nv_bfloat16 *const tk_ = a.dk + (size_t)(token + t0) * a.dk_stride + group * d.n + row;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (t0 + i < valid) {
-                            tq_[(size_t)i * a.dq_stride] = __float2bfloat16_rn(dq[i]);
-                            tk_[(size_t)i * a.dk_stride] = __float2bfloat16_rn(dk[i]);
-                        }
-                }
+                const uint32_t o = panel_at(c0 + i, row & 63);
+                const float qv = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(keys + o));
+                const float kv = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(keys + kPanel + o));
+                dots[i] = dq[i] * qv + dk[i] * kv;
+                dots[16 + i] = gates[kGateW + c0 + i] * kv;
             }
-            const float sum = lanes_transposed_sum(dots, lane);
-            scratch[(lane < 16 ? Lay::kAhead : Lay::kBehind) + 64 * q + t0 + (lane & 15)] = sum;
         }
+    }
+    after();
+    {
+        uint32_t x[16], y[16];
+        tmem_ld16(tq + kColUs + c0, x);
+        tmem_ld16(tq + kColPk + c0, y);
+        tmem_ld_wait(x);
+        tmem_ld_wait(y);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            dk[i] += gates[kGateW + c0 + i] * __uint_as_float(x[i]);
+            dots[16 + i] = on ? dots[16 + i] * __uint_as_float(x[i]) : 0.f;
+            dq[i] += __uint_as_float(y[i]);
+        }
+        tmem_ld16(tq + kColSum + c0, x);
+        tmem_ld_wait(x);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dk[i] += __uint_as_float(x[i]);
+        if (on) {
+            if (a.dq == nullptr) {
+                const size_t o = ((size_t)(token + c0) * d.heads + head) * d.n + row;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (c0 + i < valid) {
+                        a.dq_heads[o + (size_t)i * d.heads * d.n] = dq[i];
+                        a.dk_heads[o + (size_t)i * d.heads * d.n] = dk[i];
+                    }
+            } else {
+                __nv_bfloat16 *const to_q = a.dq + (size_t)(token + c0) * a.dq_stride + group * d.n + row;
+                __nv_bfloat16 *const to_k = a.dk + (size_t)(token + c0) * a.dk_stride + group * d.n + row;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (c0 + i < valid) {
+                        to_q[(size_t)i * a.dq_stride] = __float2bfloat16_rn(dq[i]);
+                        to_k[(size_t)i * a.dk_stride] = __float2bfloat16_rn(dk[i]);
+                    }
+            }
+        }
+        const float sum = lanes_transposed_sum(dots, lane);
+        scratch[(lane < 16 ? Lay::kAhead : Lay::kBehind) + 64 * q + c0 + (lane & 15)] = sum;
     }
     tc_fence_before();
     __syncthreads();
-    if (threadIdx.x < valid) {
-        const int t = threadIdx.x;
-        float whole = 0.f, dg = 0.f;
+    if (warp == 0) {
+        // lane l: tokens 2 l and 2 l + 1
+        float whole = lane < kGradWarps ? scratch[Lay::kWhole + lane] : 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) whole += scratch[Lay::kWhole + i];
-        for (int i = 0; i < valid; ++i) {
-            const float *s = scratch + i;
-            if (i >= t) {
-                const float rows = (s[Lay::kRowSum] + s[Lay::kRowSum + 64]) + (s[Lay::kRowSum + 128] + s[Lay::kRowSum + 192]);
-                const float cols = (s[Lay::kColSum] + s[Lay::kColSum + 64]) + (s[Lay::kColSum + 128] + s[Lay::kColSum + 192]);
-                dg += (rows - cols) + ((s[Lay::kAhead] + s[Lay::kAhead + 64]) + (s[Lay::kAhead + 128] + s[Lay::kAhead + 192]));
-            } else {
-                dg += (s[Lay::kBehind] + s[Lay::kBehind + 64]) + (s[Lay::kBehind + 128] + s[Lay::kBehind + 192]);
-            }
+        for (int o = 16; o > 0; o >>= 1) whole += __shfl_xor_sync(0xffffffffu, whole, o);
+        float from[2], into[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float *s = scratch + 2 * lane + i;
+            float rows = 0.f, cols = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) rows += s[Lay::kRowSum + 64 * j];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) cols += s[Lay::kColSum + 64 * j];
+            from[i] = (rows - cols) + ((s[Lay::kAhead] + s[Lay::kAhead + 64]) + (s[Lay::kAhead + 128] + s[Lay::kAhead + 192]));
+            into[i] = (s[Lay::kBehind] + s[Lay::kBehind + 64]) + (s[Lay::kBehind + 128] + s[Lay::kBehind + 192]);
         }
-        const size_t o = (size_t)(token + t) * d.heads + head;
-        a.dg[o] = dg + gates[kC - 1] * whole;
-        const float *own = scratch + Lay::kDbeta + t, be = gates[kGateBeta + t];
-        a.dbeta[o] = ((own[0] + own[64]) + (own[128] + own[192])) / be / be;
+        // of `from` the sum from the token on, of `into` that of the tokens before it
+        float ahead = from[0] + from[1], behind = into[0] + into[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float x = __shfl_down_sync(0xffffffffu, ahead, o), y = __shfl_up_sync(0xffffffffu, behind, o);
+            if (lane + o < 32) ahead += x;
+            if (lane >= o) behind += y;
+        }
+        const float next = __shfl_down_sync(0xffffffffu, ahead, 1), before_ = __shfl_up_sync(0xffffffffu, behind, 1);
+        const float past = lane ? before_ : 0.f, rest = lane < 31 ? next : 0.f;
+        const float dg[2] = {ahead + past, (rest + from[1]) + (past + into[0])};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = 2 * lane + i;
+            if (t >= valid) continue;
+            const size_t o = (size_t)(token + t) * d.heads + head;
+            const float *b = scratch + Lay::kDbeta + t, be = gates[kGateBeta + t];
+            a.dg[o] = dg[i] + gates[kC - 1] * whole;
+            a.dbeta[o] = ((b[0] + b[64]) + (b[128] + b[192])) / be / be;
+        }
     }
-    if (warp == 0) tmem_dealloc(tmem, 512);
+    if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
 struct Plan {
@@ -995,7 +994,7 @@ cudaError_t launch(const SsdDeltaBwd &b, void *ws, int sms, unsigned *err, cudaS
     const bool one = d.heads == d.groups;
     const GradTc g{d, records, b.checkpoints, z, dstate, one ? static_cast<__nv_bfloat16 *>(b.dq) : nullptr,
                    one ? static_cast<__nv_bfloat16 *>(b.dk) : nullptr, reinterpret_cast<float *>(at(plan.dq)),
-                   reinterpret_cast<float *>(at(plan.dk)), b.dq_stride, b.dk_stride, b.dg, b.dbeta, err};
+                   reinterpret_cast<float *>(at(plan.dk)), b.dq_stride, b.dk_stride, b.dg, b.dbeta, sms, err};
     const long long ctas = ssd_delta_slots(d.tokens, d.nseq) * d.heads;
     delta_grad_tc_kernel<kPanels><<<(unsigned)ctas, kGradThreads, Grad::kBytes, stream>>>(q, k, v, o, g);
     if ((e = cudaGetLastError()) != cudaSuccess || one) return e;
@@ -1006,7 +1005,8 @@ cudaError_t launch(const SsdDeltaBwd &b, void *ws, int sms, unsigned *err, cudaS
 
 bool ssd_delta_tc_bwd_sizes(const SsdDelta &d) { return ssd_delta_tc_sizes(d) && d.p <= 128; }
 bool ssd_delta_tc_bwd_handles(const SsdDeltaBwd &b) {
-    return ssd_delta_tc_bwd_sizes(b.in) && ssd_delta_tc_handles(b.in) && ((uintptr_t)b.dout & 15u) == 0 && b.do_stride % 8 == 0;
+    return ssd_delta_tc_bwd_sizes(b.in) && ssd_delta_tc_inputs(b.in) && on_16(b.dout) && b.do_stride % 8 == 0 &&
+           on_16(b.checkpoints) && on_16(b.dfinal) && on_16(b.dinit);
 }
 size_t ssd_delta_tc_bwd_workspace(const SsdDelta &d) { return ssd_delta_tc_bwd_sizes(d) ? plan_of(d).total : 0; }
 

@@ -389,7 +389,8 @@ int ssd_act_bwd_rows(long long rows, int width, int sms);
 // The delta rule on the tensor cores (delta_tc.cu): whether the sizes allow it, and the
 // addresses too; ws: ssd_delta_tc_workspace bytes (0 for other sizes).
 bool ssd_delta_tc_sizes(const SsdDelta &d);
-bool ssd_delta_tc_handles(const SsdDelta &d);
+bool ssd_delta_tc_inputs(const SsdDelta &d);
+bool ssd_delta_tc_handles(const SsdDeltaFwd &a);
 size_t ssd_delta_tc_workspace(const SsdDelta &d);
 cudaError_t ssd_launch_delta_fwd_tc(const SsdDeltaFwd &a, void *ws, int sms, unsigned *err,
                                     cudaStream_t stream);

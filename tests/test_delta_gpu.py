@@ -182,6 +182,40 @@ def test_what_lies_behind_a_sequence_stays_there():
     assert torch.equal(got[5][0], grads[5][0])
 
 
+@pytest.mark.parametrize("p,n", [(128, 128), (64, 64)])
+def test_any_alignment(p, n):
+    """Arrays that begin at any multiple of their element's size, and rows at odd strides."""
+    x, init, do, dfinal = inputs(19, 70, 1, 1, 2, p, n, "bf16")
+    b = batched(x, 1)
+    want = ssd.delta_scan_fwd(*b.values(), init, return_checkpoints=True)
+    grads = ssd.delta_scan_bwd(do[None], *b.values(), want[2], dfinal)
+
+    def shifted(t):
+        buf = torch.zeros(t.numel() + 1, dtype=t.dtype, device="cuda")
+        buf[1:] = t.reshape(-1)
+        return buf[1:].view(t.shape)
+    close = lambda got, ref_, bar: rel(host(got), host(ref_)) <= bar   # noqa: E731
+    for which in (*b, "init", "o", "final_state", "checkpoints"):
+        args = {name: shifted(t) if name == which else t for name, t in b.items()}
+        out = {name: shifted(torch.zeros_like(t)) for name, t in (("o", want[0]), ("final_state", want[1]), ("checkpoints", want[2])) if name == which}
+        got = ssd.delta_scan_fwd(*args.values(), shifted(init) if which == "init" else init, return_checkpoints=True, **out)
+        assert close(got[0], want[0], 2 * BAR["bf16"]) and close(got[1], want[1], 2 * STATE["bf16"])
+        assert close(got[2][:2], want[2][:2], 2 * STATE["bf16"]), which
+    names = ("dq", "dk", "dv", "dg", "dbeta", "dinit")
+    for which in (*b, "do", "kept", "dfinal", *names):
+        args = {name: shifted(t) if name == which else t for name, t in b.items()}
+        out = {which: shifted(torch.zeros_like(grads[names.index(which)]))} if which in names else {}
+        got = ssd.delta_scan_bwd(shifted(do[None]) if which == "do" else do[None], *args.values(), shifted(want[2]) if which == "kept" else want[2],
+                                 shifted(dfinal) if which == "dfinal" else dfinal, **out)
+        for name, g, w in zip(names, got, grads):
+            assert close(g, w, 2 * BAR["bf16"] if name in ("dq", "dk", "dv") else 2 * STATE["bf16"]), (which, name)
+    wide = torch.zeros((1, 70, 2 * p + 3), dtype=torch.bfloat16, device="cuda")
+    v = wide[..., 1:1 + 2 * p].unflatten(-1, (2, p))
+    v.copy_(b["v"])
+    o = torch.zeros_like(wide)[..., 2:2 + 2 * p].unflatten(-1, (2, p))
+    assert close(ssd.delta_scan_fwd(**dict(b, v=v), o=o)[0], ssd.delta_scan_fwd(*b.values())[0], 2 * BAR["bf16"])
+
+
 def test_the_first_part_then_the_rest():
     """A sequence cut in two gives what it gives whole: states are handed on in 32 bits."""
     x, init, _, _ = inputs(13, 320, 1, 2, 4, 128, 128, "bf16")
