@@ -39,13 +39,19 @@ constexpr uint32_t kColS = 0, kColSh = 128, kColSl = 192, kColX = 256, kColY = 3
 constexpr int kChainWarps = 16, kOutWarps = 8;
 constexpr int kLoadWarp = kChainWarps + kOutWarps, kMmaWarp = kLoadWarp + 1, kBackThreads = 32 * (kMmaWarp + 1);
 
+constexpr uint32_t kTall = 2 * kPanel;              // a panel of 128 rows
+constexpr uint32_t kImageRows = 32 * 128;           // a warp's rows of one
+static_assert(kOutWarps * kImageRows >= kChainWarps * kStageRows, "one place for both");
+// A chunk's dS, for every head: its two parts, each [128 of P][N] by tall panels.
+constexpr uint32_t state_image(int panels) { return 2 * panels * kTall; }
+
 template <int kPanels>
 struct BackSmem {
     static constexpr uint32_t kK = 0, kQ = kPanels * kPanel, kDo = 2 * kPanels * kPanel, kRec = kDo + 2 * kPanel;
     static constexpr uint32_t kStage = (kRec + kRecord + 1023) / 1024 * 1024;
     static constexpr uint32_t kOut = 2 * kStage;        // [token][128]: dV on its way
-    static constexpr uint32_t kRows = kOut + 64 * 256;  // dS on its way, by warps
-    static constexpr uint32_t kCtl = kRows + kChainWarps * kStageRows;
+    static constexpr uint32_t kRows = kOut + 64 * 256;  // dS on its way, by warps: its images, at last dinit
+    static constexpr uint32_t kCtl = kRows + kOutWarps * kImageRows;
     static constexpr uint32_t kBytes = kCtl + 256;
 };
 
@@ -57,7 +63,8 @@ struct BackTc {
     long long dv_stride;
     bool dv_vectors;
     float *dinit;
-    float *z, *dstate;      // [token][head][P], [slot][head][P][N]
+    float *z;               // [token][head][P]
+    uint8_t *dstate;        // [slot][head] images
     unsigned *err;
     unsigned long long wait_ns;
     bool withhold;
@@ -67,7 +74,7 @@ enum BackBar {
     kFull = 0, kEmpty = 2,
     kE = 4, kZ, kS, kDrain,                 // products done
     kSh, kSl, kRh, kRl, kWh, kWl,           // operands' parts written by the chain
-    kD, kZRead,                             // by the output's warps, and read by them
+    kD, kZRead, kSRead,                     // by the output's warps, and read by them
     kStaged, kStored,                       // dV in shared memory, and out of it
     kBars
 };
@@ -108,7 +115,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         }
         for (int i : {kE, kZ, kS, kDrain}) mbar_init(bar(i), 1);
         for (int i : {kSh, kSl, kRh, kRl, kWh, kWl}) mbar_init(bar(i), kChainWarps);
-        for (int i : {kD, kZRead, kStaged, kStored}) mbar_init(bar(i), kOutWarps);
+        for (int i : {kD, kZRead, kSRead, kStaged, kStored}) mbar_init(bar(i), kOutWarps);
         fence_mbar_init();
         *abort = 0;
     }
@@ -286,6 +293,35 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
                 mbar_arrive(bar(kD));
                 mbar_arrive(bar(kEmpty + s));
             }
+            // dS, as the products have it, for the chunk's other gradients: a panel's 32 rows
+            // of a part are 4 KB in one piece
+            if (!wait.warp(bar(kSl), it & 1)) break;
+            tc_fence_after();
+            uint8_t *const rows = smem + Lay::kRows + (warp - kChainWarps) * kImageRows;
+            if (half < kPanels) {
+                uint8_t *const image = a.dstate + ((size_t)(slot0 + c) * d.heads + head) * state_image(kPanels);
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    uint32_t r[32];
+                    tmem_ld32(tq + (part ? kColSl : kColSh) + 32 * half, r);
+                    tmem_ld_wait(r);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint4 *>(rows + lane * 128 + ((i ^ lane) & 7) * 16) =
+                            make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        bulk_store(image + (part * kPanels + half) * kTall + q * kImageRows, smem_u32(rows), kImageRows);
+                        bulk_commit();
+                        bulk_wait_read<0>();
+                    }
+                    __syncwarp();
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kSRead));
             if (!wait.warp(bar(kZ), it & 1)) break;
             tc_fence_after();
             uint32_t z[32];
@@ -323,6 +359,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
             if (lane == 0) mbar_arrive(bar(kStored));
             if (!wait.warp(bar(kStored), it & 1)) break;
         }
+        if (lane == 0) bulk_wait_all();
     } else {
         // the chain: a thread has a row of dS and of dU^T and Z^T
         const int q = warp & 3, part = warp >> 2, p = 32 * q + lane;
@@ -339,9 +376,8 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(which));
         };
-        // the gradient of the state behind chunk c: its parts, in fp32 decayed over the
-        // chunk, and for the chunk's other gradients as it is
-        const auto put = [&](int c, const float (&v)[kMine], float decay) {
+        // the gradient of the state behind a chunk: its parts, and in fp32 decayed over the chunk
+        const auto put = [&](const float (&v)[kMine], float decay) {
             uint32_t hi[kMine / 2];
 #pragma unroll
             for (int i = 0; i < kMine / 2; ++i) hi[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
@@ -365,7 +401,6 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
                 }
                 tmem_st16(tq + kColS + n0 + 16 * h, f);
             }
-            to_memory(a.dstate + ((size_t)(slot0 + c) * d.heads + head) * size, v);
         };
         const auto stage = [&](int it) { return smem + (it & 1) * Lay::kStage; };
         const auto decay_of = [&](int it) { return reinterpret_cast<const float *>(stage(it) + Lay::kRec + kRecGates)[kC - 1]; };
@@ -380,7 +415,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
 #pragma unroll
             for (int i = 0; i < kMine; ++i)
                 v[i] = a.dfinal && p < d.p && n0 + i < d.n ? a.dfinal[state + (size_t)p * d.n + n0 + i] : 0.f;
-            put(chunks - 1, v, decay_of(0));
+            put(v, decay_of(0));
         }
         for (int it = 0; on && it < chunks; ++it) {
             const int s = it & 1, c = chunks - 1 - it, tokens = min(kC, len - c * kC) - 16 * part;
@@ -449,7 +484,8 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
             const bool more = it + 1 < chunks;
             if (more && !wait.warp(bar(kFull + (s ^ 1)), ((it + 1) >> 1) & 1)) break;
             const float decay = more ? decay_of(it + 1) : 1.f;
-            if (!wait.warp(bar(kS), it & 1)) break;
+            // (dS's parts have been read by the output's warps)
+            if (!wait.warp(bar(kS), it & 1) || !wait.warp(bar(kSRead), it & 1)) break;
             tc_fence_after();
             uint32_t m[kMine];
             if constexpr (kMine == 32) tmem_ld32(tq + kColS + n0, m);
@@ -458,7 +494,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
             float v[kMine];
 #pragma unroll
             for (int i = 0; i < kMine; ++i) v[i] = __uint_as_float(m[i]);
-            if (more) put(c - 1, v, decay);
+            if (more) put(v, decay);
             else if (a.dinit) to_memory(a.dinit + state, v);
         }
     }
@@ -477,26 +513,26 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
 // tiles one CTA an SM.  What is loaded first (a state, Z) is asked for at once, and what the
 // CTA that comes next on this SM will load is brought into L2 meanwhile.
 constexpr int kGradWarps = 16, kGradThreads = 32 * kGradWarps;
-constexpr uint32_t kTall = 2 * kPanel;      // a panel of 128 rows
 template <int kPanels>
 struct GradSmem {
     static constexpr uint32_t kQk = 0;                          // panels of queries over keys
-    static constexpr uint32_t kAh = kQk + kPanels * kTall;      // dO over Z's rounded part, then scratch
-    static constexpr uint32_t kAl = kAh + 2 * kTall;            // nothing over what rounding left of Z
+    static constexpr uint32_t kAh = kQk + kPanels * kTall;      // dO over Z's rounded part, then dS's
+    static constexpr uint32_t kAl = kAh + 2 * kTall;            // nothing over what rounding left of Z, or of dS
     static constexpr uint32_t kU = kAl + 2 * kTall;             // U's parts
-    static constexpr uint32_t kSs = kU + 4 * kPanel;            // the parts of S, then of dS: [P][N]
+    static constexpr uint32_t kSs = kU + 4 * kPanel;            // the parts of S, [P][N]; then scratch
     static constexpr uint32_t kW = kSs + 4 * kTall;             // V and T; then the parts of dP and of dA
     static constexpr uint32_t kCtl = kW + 4 * kPanel;
     static constexpr uint32_t kGatesAt = kCtl + 64;
     static constexpr uint32_t kBytes = kGatesAt + kGates * 4;
-    // scratch, where dO and Z were (floats)
+    // scratch, where S was (floats)
     static constexpr int kRowSum = 0, kColSum = 512, kAhead = 768, kBehind = 1024, kDbeta = 1280, kWhole = 1536;
 };
 
 struct GradTc {
     SsdDelta d;
     const uint8_t *records;
-    const float *checkpoints, *z, *dstate;
+    const float *checkpoints, *z;
+    const uint8_t *dstate;
     __nv_bfloat16 *dq, *dk;             // where a group is one head; else sums by head:
     float *dq_heads, *dk_heads;         // [token][head][N]
     long long dq_stride, dk_stride;
@@ -546,11 +582,12 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
     const int valid = min(kC, at.len - at.chunk * kC);
     const long long token = at.first + (long long)at.chunk * kC;
     const size_t record = (size_t)slot * d.heads + head, size = (size_t)d.p * d.n;
-    const uint32_t full = base + Lay::kCtl, done = full + 8;
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(smem + Lay::kCtl + 16);
+    const uint32_t full = base + Lay::kCtl, done = full + 8, second = full + 16;
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(smem + Lay::kCtl + 24);
     if (threadIdx.x == 0) {
         mbar_init(full, 1);
         mbar_init(done, 1);
+        mbar_init(second, 1);
         fence_mbar_init();
         mbar_arrive_expect_tx(full, kPanels * kTall + 2 * kPanel + 64 * 256 + 2 * kPanel + kGates * 4);
         const int t = (int)token;
@@ -596,8 +633,26 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
             tmem_relinquish();
         }
         const long long next = (long long)blockIdx.x + a.ahead;
-        if (warp == 2 && lane < 2 && next < gridDim.x)
-            bulk_prefetch_l2((lane ? a.dstate : a.checkpoints) + (size_t)next * size, (uint32_t)(size * 4));
+        if (warp == 2 && next < gridDim.x) {
+            const long long slot2 = next / d.heads;
+            const int head2 = (int)(next % d.heads), group2 = head2 / (d.heads / d.groups);
+            const ChunkAt at2 = chunk_at(d, slot2);
+            if (at2.live && elect_one()) {
+                const int t = (int)(at2.first + (long long)at2.chunk * kC);
+                bulk_prefetch_l2(a.checkpoints + (size_t)next * size, (uint32_t)(size * 4));
+                bulk_prefetch_l2(a.dstate + (size_t)next * state_image(kPanels), state_image(kPanels));
+                bulk_prefetch_l2(a.records + (size_t)next * kRecord, kRecord);
+#pragma unroll
+                for (int p = 0; p < kPanels; ++p) {
+                    tma_prefetch_l2_3d(&mapQ, 64 * p, group2, t);
+                    tma_prefetch_l2_3d(&mapK, 64 * p, group2, t);
+                }
+#pragma unroll
+                for (int p = 0; p < 2; ++p) tma_prefetch_l2_3d(&mapDo, 64 * p, head2, t);
+                tma_prefetch_l2_3d(&mapV, 0, head2, t);
+            }
+            __syncwarp();
+        }
         for (int i = threadIdx.x; i < 1024; i += kGradThreads)
             *reinterpret_cast<uint4 *>(smem + Lay::kAl + (i >> 9) * kTall + (i & 511) * 16) = make_uint4(0, 0, 0, 0);
 #pragma unroll
@@ -675,7 +730,7 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
             mma_ss(tmem + dcol, ad + kStepMn * k, bd + kStepMn * k, idesc_bf16_f32(128, 16 * k + 16, true, true), add || k < 3);
     };
     const float *gates = reinterpret_cast<const float *>(smem + Lay::kGatesAt);
-    float *const scratch = reinterpret_cast<float *>(smem + Lay::kAh);
+    float *const scratch = reinterpret_cast<float *>(smem + Lay::kSs);
 
     // K S^T by the state's rows; Q K^T over K K^T
     before();
@@ -764,13 +819,16 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         rows_rows(kColM, al, uh, kPanel, 2, true);
         mma_commit(done);
     }
-    // dS on its way beside the products
-    const float *const dstate = a.dstate + record * size;
-    float4 ds[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ds[i] = load_state(dstate, 8 * warp + i);
     after();
+    // dS in the place of dO and Z
+    if (threadIdx.x == 0) {
+        const uint8_t *from = a.dstate + record * state_image(kPanels);
+        mbar_arrive_expect_tx(second, state_image(kPanels));
+        bulk_load(ah, from, kPanels * kTall, second);
+        bulk_load(al, from + kPanels * kTall, kPanels * kTall, second);
+    }
     // dP (lanes 0 .. 63) and dA (64 .. 127), a row a lane; and what pairs of tokens add to dg
+    float sum = 0.f, col, dot = 0.f;
     {
         const int r = row & 63;
         const bool keys = q >= 2;
@@ -784,7 +842,7 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         const float factor = keys ? -1.f : d.scale;
         tmem_ld_wait(m);
         tmem_ld_wait(x);
-        float v[16], e[16], sum = 0.f;
+        float v[16], e[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
             const float2 c = sums[c0 + j];
@@ -798,33 +856,28 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         uint8_t *const to = smem + Lay::kW + (keys ? 2 * kPanel : 0);
         put_parts(to, panel_at(r, c0), v);
         put_parts(to, panel_at(r, c0 + 8), v + 8);
-        scratch[Lay::kRowSum + (keys ? 256 : 0) + 4 * c0 + r] = sum;
-        const float col = lanes_transposed_sum(e, lane);
-        if (lane < 16) {
-            scratch[Lay::kColSum + (keys ? 128 : 0) + 64 * (q & 1) + c0 + lane] = col;
-            scratch[Lay::kDbeta + 64 * q + c0 + lane] = own;
-        }
+        col = lanes_transposed_sum(e, lane);
     }
-    // dS in S's place, and <S, dS>
-    {
-        float dot = 0.f;
+    // <S, dS>: both lie alike
+    if (!mbar_wait(second, 0, kSsdDefaultWaitNs)) ssd_report(a.err, SSD_DEVERR_TIMEOUT);
+    for (uint32_t i = threadIdx.x * 16; i < kPanels * kTall; i += kGradThreads * 16) {
+        const auto pairs = [&](uint32_t hi, uint32_t lo, float (&x)[8]) {
+            const uint4 h = *reinterpret_cast<const uint4 *>(smem + hi + i), l = *reinterpret_cast<const uint4 *>(smem + lo + i);
+            const uint32_t a_[4] = {h.x, h.y, h.z, h.w}, b_[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (64 * kPanels <= 4 * lane) continue;
-            const float4 v = ds[i];
-            const uint32_t to = state_panel + panel_at(8 * warp + i, (4 * lane) & 63);
-            const uint2 h = *reinterpret_cast<const uint2 *>(smem + to);
-            const uint2 l = *reinterpret_cast<const uint2 *>(smem + to + kPanels * kTall);
-            const auto low = [](uint32_t x) { return __uint_as_float(x << 16); };
-            const auto high = [](uint32_t x) { return __uint_as_float(x & 0xffff0000u); };
-            dot += (low(h.x) + low(l.x)) * v.x + (high(h.x) + high(l.x)) * v.y + (low(h.y) + low(l.y)) * v.z +
-                   (high(h.y) + high(l.y)) * v.w;
-            store_state(8 * warp + i, v);
-        }
+            for (int j = 0; j < 4; ++j) {
+                x[2 * j] = __uint_as_float(a_[j] << 16) + __uint_as_float(b_[j] << 16);
+                x[2 * j + 1] = __uint_as_float(a_[j] & 0xffff0000u) + __uint_as_float(b_[j] & 0xffff0000u);
+            }
+        };
+        float x[8], y[8];
+        pairs(Lay::kSs, Lay::kSs + kPanels * kTall, x);
+        pairs(Lay::kAh, Lay::kAl, y);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        if (lane == 0) scratch[Lay::kWhole + warp] = dot;
+        for (int j = 0; j < 8; ++j) dot += x[j] * y[j];
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
     before();
     if (issuer && elect_one()) {
 #pragma unroll
@@ -835,11 +888,18 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
             tokens_lower(kColSum, qk + kPanel, da, true);
             tokens_upper(kColSum, qk + kPanel, da, true);
         }
-        cols_rows(kColUs, sh, uh, kPanel, kIdMn, false);
-        cols_rows(kColUs, sl, uh, kPanel, kIdMn, true);
-        cols_rows(kColUs, sh, ul, kPanel, kIdMn, true);
+        cols_rows(kColUs, ah, uh, kPanel, kIdMn, false);
+        cols_rows(kColUs, al, uh, kPanel, kIdMn, true);
+        cols_rows(kColUs, ah, ul, kPanel, kIdMn, true);
         mma_commit(done);
     }
+    // (S is used up: scratch)
+    scratch[Lay::kRowSum + (q >= 2 ? 256 : 0) + 4 * c0 + (row & 63)] = sum;
+    if (lane < 16) {
+        scratch[Lay::kColSum + (q >= 2 ? 128 : 0) + 64 * (q & 1) + c0 + lane] = col;
+        scratch[Lay::kDbeta + 64 * q + c0 + lane] = own;
+    }
+    if (lane == 0) scratch[Lay::kWhole + warp] = dot;
     // meanwhile what tokens read of S, dotted with them: a lane is a column of dQ and dK
     const bool on = row < d.n;
     const uint8_t *const keys = smem + Lay::kQk + (row >> 6) * kTall;
@@ -957,7 +1017,7 @@ Plan plan_of(const SsdDelta &d) {
     p.records = 0;
     p.z = up(slots * d.heads * kRecord);
     p.dstate = p.z + up(tokens * d.heads * d.p * 4);
-    p.dq = p.dstate + up(slots * d.heads * d.p * d.n * 4);
+    p.dq = p.dstate + up(slots * d.heads * state_image(d.n <= 64 ? 1 : 2));
     p.dk = p.dq + (d.heads == d.groups ? 0 : up(tokens * d.heads * d.n * 4));
     p.total = p.dk + (d.heads == d.groups ? 0 : up(tokens * d.heads * d.n * 4));
     return p;
@@ -976,7 +1036,8 @@ cudaError_t launch(const SsdDeltaBwd &b, void *ws, int sms, unsigned *err, cudaS
     const Plan plan = plan_of(d);
     const auto at = [&](size_t offset) { return static_cast<char *>(ws) + offset; };
     uint8_t *records = reinterpret_cast<uint8_t *>(at(plan.records));
-    float *z = reinterpret_cast<float *>(at(plan.z)), *dstate = reinterpret_cast<float *>(at(plan.dstate));
+    float *z = reinterpret_cast<float *>(at(plan.z));
+    uint8_t *dstate = reinterpret_cast<uint8_t *>(at(plan.dstate));
     cudaError_t e = launch_chunks(d, records, true, sms, err, stream);
     if (e != cudaSuccess) return e;
     using Back = BackSmem<kPanels>;
