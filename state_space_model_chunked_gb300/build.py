@@ -27,7 +27,8 @@ MARSHAL = os.path.join(OUT_DIR, "ssd_marshal.so")
 OBJ_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.cu", "decode.cu", "scan_simt.cu", "scan_tc.cu", "scan_static.cu", "widen.cu",
            "seqshard.cu", "api_layer.cu", "rmsnorm.cu", "gated_scan.cu", "linear_simt.cu",
-           "linear_tc.cu", "linear_gemv.cu", "linear_few.cu", "layernorm.cu", "embedding.cu",
+           "linear_tc.cu", "linear_gemv.cu", "linear_few.cu", "layernorm.cu", "layernorm_rows.cu",
+           "embedding.cu",
            "delta_simt.cu", "delta_step.cu", "delta_tc.cu",
            "delta_tc_bwd.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

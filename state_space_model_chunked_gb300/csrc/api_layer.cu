@@ -486,7 +486,10 @@ ssd_status ssd_layernorm_fwd(const void *x, const void *residual, const float *w
     SsdLayerNormFwd a{x, residual, weight, bias, eps, elt(x_dtype), elt(stream_dtype), elt(out_dtype),
                       rows, width, x_stride, residual_stride, y, residual ? residual_out : nullptr,
                       mean, rstd, scale};
-    return launched(ssd_launch_layernorm_fwd(a, ssd_sm_count(), stream));
+    const int sms = ssd_sm_count();
+    if (ssd_layernorm_rows_handles(a, sms))
+        return launched(ssd_launch_layernorm_rows(a, sms, ssd_device_error_word(), stream));
+    return launched(ssd_launch_layernorm_fwd(a, sms, stream));
 }
 
 size_t ssd_layernorm_bwd_workspace_bytes(long long rows, int width) {

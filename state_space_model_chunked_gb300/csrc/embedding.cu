@@ -6,12 +6,14 @@
 // Both are bound by memory.  The gradient is dense: rows that no token names are zeros.
 // It is found without atomic additions, so equal calls give equal bits:
 //   1. the tokens are sorted, stably, with their places (a radix sort of at most 9 bits a
-//      pass, by one cluster whose CTAs exchange their digits' counts through distributed
-//      shared memory; keys and places go through the workspace, that is, L2);
-//   2. pieces of kPiece sorted tokens each add up their rows of dy in order.  A token whose
+//      pass, by one cluster whose CTAs exchange their digits' counts, and where they fit
+//      their keys too, through distributed shared memory).  Beside the sort, which takes
+//      eight SMs, others write zeros to all of the table, named rows or not: that takes
+//      longer than the sort for most tables, where looking for the rows that no token names
+//      would have to wait for it;
+//   2. pieces of some sorted tokens each add up their rows of dy in order.  A token whose
 //      rows lie in one piece is written at once; the sums of one that goes on beyond its
-//      piece are kept as parts.  Beside that, other CTAs write the zeros of the rows
-//      that no token names;
+//      piece are kept as parts;
 //   3. the parts of such tokens are added in the pieces' order.
 #include "launch.h"
 #include "ptx.cuh"
@@ -85,61 +87,98 @@ struct Sort {
     const void *tokens;
     bool wide;
     int count, vocab, passes, bits;
+    int run;                    // a warp's keys, whole 32s
     int *key[2], *at[2];        // the last pass writes key[0], at[0]
+    // beside the sort, by the clusters behind the first: zeros, from byte to byte (even)
+    uint8_t *zero;
+    size_t bytes;
 };
+// Shared memory: counts [warp][digit], their sums [digit], the warps' sums; then, where keys
+// stay on chip, two buffers of the CTA's keys with their places.
+constexpr int kSortWords = kSortWarps * (1 << kMostBits) + (1 << kMostBits) + kSortWarps;
+constexpr int kMostLocal = (232448 - 4 * kSortWords) / (16 * 32 * kSortWarps) * 32;        // longest run that fits
 
-// What a lane reads of the pass's input: the key (vocab: outside the table) and its place.
-__device__ __forceinline__ void sort_input(const Sort &a, int pass, int from, int i, int &key, int &at) {
-    if (pass == 0) {
-        const int row = row_of(a.tokens, a.wide, i, a.vocab);
-        key = row < 0 ? a.vocab : row;
-        at = i;
-    } else {
-        key = __ldcg(a.key[from] + i);
-        at = __ldcg(a.at[from] + i);
-    }
-}
-
+// kLocal: between passes the keys lie in the CTAs' shared memory, else in the workspace.
+template <bool kLocal>
 __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(32 * kSortWarps)
 sort_tokens_kernel(const Sort a) {
+    if (blockIdx.x >= kSortCtas) {
+        const size_t head = (size_t)(-(intptr_t)a.zero & 15) < a.bytes ? (size_t)(-(intptr_t)a.zero & 15) : a.bytes;
+        const size_t vectors = (a.bytes - head) / 16;
+        uint4 *const to = reinterpret_cast<uint4 *>(a.zero + head);
+        const size_t step = (size_t)(gridDim.x - kSortCtas) * 32 * kSortWarps;
+        const size_t first = (size_t)(blockIdx.x - kSortCtas) * 32 * kSortWarps + threadIdx.x;
+        for (size_t i = first; i < vectors; i += 4 * step) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (i + u * step < vectors) __stcs(to + i + u * step, make_uint4(0, 0, 0, 0));
+        }
+        if (first < head / 2) reinterpret_cast<uint16_t *>(a.zero)[first] = 0;
+        const size_t tail = head + 16 * vectors + 2 * first;
+        if (tail < a.bytes) *reinterpret_cast<uint16_t *>(a.zero + tail) = 0;
+        return;
+    }
     extern __shared__ int sort_smem[];
     constexpr int kMost = 1 << kMostBits;
     int *const counts = sort_smem;                          // [warp][digit]
     int *const total = sort_smem + kSortWarps * kMost;      // [digit], read by the other CTAs
     int *const scan = total + kMost;                        // [warp]
+    uint2 *const local = reinterpret_cast<uint2 *>(sort_smem + kSortWords);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)ssdptx::cluster_rank();
-    const int digits = 1 << a.bits;
-    // a warp's keys: a run of whole 32s
-    const int run = (int)(((long long)a.count + 32ll * kSortCtas * kSortWarps - 1) / (32ll * kSortCtas * kSortWarps)) * 32;
-    const long long begin = (long long)(rank * kSortWarps + warp) * run;
-    const int end = (int)(begin + run < a.count ? begin + run : a.count);
+    const int digits = 1 << a.bits, slice = a.run * kSortWarps;
+    const long long begin = (long long)(rank * kSortWarps + warp) * a.run;
+    const int end = (int)(begin + a.run < a.count ? begin + a.run : a.count);
     constexpr int kAhead = 4;
+    const bool few = a.run <= 32 * kAhead;      // a lane's keys stay in its registers
+    int key[kAhead], at[kAhead];
+    // the keys of a pass (vocab: outside the table) and their places
+    const auto load = [&](int pass, int from, long long i0) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const long long i = i0 + 32 * u + lane;
+            key[u] = -1;
+            if (i >= end) continue;
+            if (pass == 0) {
+                const int row = row_of(a.tokens, a.wide, i, a.vocab);
+                key[u] = row < 0 ? a.vocab : row;
+                at[u] = (int)i;
+            } else if constexpr (kLocal) {
+                const uint2 x = local[from * slice + (int)(i - (long long)rank * slice)];
+                key[u] = (int)x.x;
+                at[u] = (int)x.y;
+            } else {
+                key[u] = __ldcg(a.key[from] + i);
+                at[u] = __ldcg(a.at[from] + i);
+            }
+        }
+    };
     for (int pass = 0; pass < a.passes; ++pass) {
         const int to = (a.passes - 1 - pass) & 1, from = to ^ 1, shift = pass * a.bits;
+        const bool last = pass == a.passes - 1;
         int *const mine = counts + warp * kMost;
         for (int d = lane; d < digits; d += 32) mine[d] = 0;
         __syncwarp();
         for (long long i0 = begin; i0 < end; i0 += 32 * kAhead) {
-            int key[kAhead], at;
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const long long i = i0 + 32 * u + lane;
-                key[u] = -1;
-                if (i < end) sort_input(a, pass, from, (int)i, key[u], at);
-            }
+            load(pass, from, i0);
 #pragma unroll
             for (int u = 0; u < kAhead; ++u)
                 if (key[u] >= 0) atomicAdd(mine + ((key[u] >> shift) & (digits - 1)), 1);
         }
         __syncthreads();
         // counts become, by digit, the number in the CTA's warps in front
-        int all = 0;
         if (threadIdx.x < digits) {
-            for (int w = 0; w < kSortWarps; ++w) {
-                const int n = counts[w * kMost + threadIdx.x];
-                counts[w * kMost + threadIdx.x] = all;
-                all += n;
+            int all = 0;
+#pragma unroll
+            for (int w0 = 0; w0 < kSortWarps; w0 += 8) {
+                int n[8];
+#pragma unroll
+                for (int w = 0; w < 8; ++w) n[w] = counts[(w0 + w) * kMost + threadIdx.x];
+#pragma unroll
+                for (int w = 0; w < 8; ++w) {
+                    counts[(w0 + w) * kMost + threadIdx.x] = all;
+                    all += n[w];
+                }
             }
             total[threadIdx.x] = all;
         }
@@ -148,11 +187,14 @@ sort_tokens_kernel(const Sort a) {
         // the CTAs in front
         int front = 0, sum = 0;
         if (threadIdx.x < digits) {
+            int n[kSortCtas];
+#pragma unroll
+            for (int c = 0; c < kSortCtas; ++c)
+                n[c] = (int)ssdptx::cluster_ld_u32(ssdptx::cluster_map(ssdptx::smem_u32(total + threadIdx.x), (uint32_t)c));
+#pragma unroll
             for (int c = 0; c < kSortCtas; ++c) {
-                const int n = (int)ssdptx::cluster_ld_u32(
-                    ssdptx::cluster_map(ssdptx::smem_u32(total + threadIdx.x), (uint32_t)c));
-                if (c < rank) front += n;
-                sum += n;
+                if (c < rank) front += n[c];
+                sum += n[c];
             }
         }
         int upto = sum;
@@ -163,19 +205,17 @@ sort_tokens_kernel(const Sort a) {
         }
         if (lane == 31) scan[warp] = upto;
         __syncthreads();
-        int base = upto - sum + front;
-        for (int w = 0; w < warp; ++w) base += scan[w];
-        if (threadIdx.x < digits)
+        int below = lane < warp ? scan[lane] : 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) below += __shfl_xor_sync(0xffffffffu, below, o);
+        const int base = upto - sum + front + below;
+        if (threadIdx.x < digits) {
+#pragma unroll 8
             for (int w = 0; w < kSortWarps; ++w) counts[w * kMost + threadIdx.x] += base;
+        }
         __syncthreads();
         for (long long i0 = begin; i0 < end; i0 += 32 * kAhead) {
-            int key[kAhead], at[kAhead];
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const long long i = i0 + 32 * u + lane;
-                key[u] = -1;
-                if (i < end) sort_input(a, pass, from, (int)i, key[u], at[u]);
-            }
+            if (!few) load(pass, from, i0);
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 const bool on = key[u] >= 0;
@@ -186,7 +226,13 @@ sort_tokens_kernel(const Sort a) {
                 __syncwarp();
                 if (on && lane == __ffs(same) - 1) mine[d] += __popc(same);
                 __syncwarp();
-                if (on) {
+                if (!on) continue;
+                if (kLocal && !last) {
+                    const int cta = place / slice;
+                    ssdptx::cluster_st_u32x2(
+                        ssdptx::cluster_map(ssdptx::smem_u32(local + to * slice + place - cta * slice), (uint32_t)cta),
+                        (uint32_t)key[u], (uint32_t)at[u]);
+                } else {
                     a.key[to][place] = key[u];
                     a.at[to][place] = at[u];
                 }
@@ -197,9 +243,11 @@ sort_tokens_kernel(const Sort a) {
 }
 
 // ------------------------------------------------------------------ gradient
-constexpr int kPiece = 32;          // sorted tokens a CTA adds up
-constexpr int kZeroRows = 64;       // table rows a CTA looks through for those without tokens
-constexpr int kSumThreads = 128;
+// Sorted tokens a CTA adds up: few enough for some hundred CTAs, many enough that parts are
+// few.  us by (16, 32, 64): 2048 tokens 45 49 56, 16376 80 58 66, 65536 165 103 95.
+constexpr int kMostPiece = 64;
+int piece_of(long long count) { return count < 4096 ? 16 : count < 32768 ? 32 : kMostPiece; }
+constexpr int kSumThreads = 512;
 
 struct Gradient {
     const int *key, *at;            // sorted
@@ -210,57 +258,26 @@ struct Gradient {
     void *dtable;
     float *parts;                   // [piece][2][width]: what its first and its last token's
                                     // run keep for the pieces beside it
-    int pieces, blocks;             // column blocks
+    int piece, pieces, blocks;      // tokens a piece, pieces, column blocks
 };
-
-// The number of sorted keys below `v`.
-__device__ __forceinline__ int keys_below(const int *key, int count, int v) {
-    int lo = 0, hi = count;
-    while (lo < hi) {
-        const int mid = lo + (hi - lo) / 2;
-        if (__ldcg(key + mid) < v) lo = mid + 1;
-        else hi = mid;
-    }
-    return lo;
-}
 
 template <typename T, typename TO, int V>
 __global__ void __launch_bounds__(kSumThreads) embedding_bwd_kernel(const Gradient a) {
     ssdptx::griddep_wait();
     const int nvec = a.width / V;
-    if ((long long)blockIdx.x >= (long long)a.pieces * a.blocks) {
-        // the zeros of rows without tokens
-        __shared__ unsigned char named[kZeroRows];
-        __shared__ int ends[2];
-        const long long r0 = ((long long)blockIdx.x - (long long)a.pieces * a.blocks) * kZeroRows;
-        const int rows = (int)(a.vocab - r0 < kZeroRows ? a.vocab - r0 : kZeroRows);
-        if (threadIdx.x < kZeroRows) named[threadIdx.x] = 0;
-        if (threadIdx.x < 2) ends[threadIdx.x] = keys_below(a.key, a.count, (int)(threadIdx.x ? r0 + rows : r0));
-        __syncthreads();
-        for (int i = ends[0] + threadIdx.x; i < ends[1]; i += kSumThreads) named[__ldcg(a.key + i) - r0] = 1;
-        __syncthreads();
-        TO *out = static_cast<TO *>(a.dtable);
-        const float zero[V] = {};
-        for (int r = threadIdx.x >> 5; r < rows; r += kSumThreads / 32) {
-            if (named[r]) continue;
-            for (int i = threadIdx.x & 31; i < nvec; i += 32)
-                ssd_store_vec<V>(out + (size_t)(r0 + r) * a.width + (size_t)i * V, zero);
-        }
-        return;
-    }
-    __shared__ int key[kPiece + 2], at[kPiece];     // key[0], key[n + 1]: the neighbours'
+    __shared__ int key[kMostPiece + 2], at[kMostPiece];     // key[0], key[n + 1]: the neighbours'
     const int piece = (int)(blockIdx.x / a.blocks), block = (int)(blockIdx.x % a.blocks);
-    const int first = piece * kPiece, n = min(kPiece, a.count - first);
-    if (threadIdx.x < n + 2) {
-        const int i = first + (int)threadIdx.x - 1;
-        key[threadIdx.x] = i >= 0 && i < a.count ? __ldcg(a.key + i) : -1;
-        if (threadIdx.x >= 1 && threadIdx.x <= n) at[threadIdx.x - 1] = __ldcg(a.at + i);
+    const int first = piece * a.piece, n = min(a.piece, a.count - first);
+    for (int t = threadIdx.x; t < n + 2; t += blockDim.x) {
+        const int i = first + t - 1;
+        key[t] = i >= 0 && i < a.count ? __ldcg(a.key + i) : -1;
+        if (t >= 1 && t <= n) at[t - 1] = __ldcg(a.at + i);
     }
     __syncthreads();
-    const int vec = block * kSumThreads + threadIdx.x;
+    const int vec = block * (int)blockDim.x + (int)threadIdx.x;
     if (vec >= nvec) return;
     const T *dy = static_cast<const T *>(a.dy) + (size_t)vec * V;
-    constexpr int kAhead = 8;
+    constexpr int kAhead = 16;
     float acc[V] = {};
     bool whole = key[0] != key[1];      // whether the token's run began in this piece
     for (int i0 = 0; i0 < n; i0 += kAhead) {
@@ -301,22 +318,30 @@ template <typename TO, int V>
 __global__ void __launch_bounds__(kSumThreads) embedding_join_kernel(const Gradient a) {
     ssdptx::griddep_wait();
     const int piece = (int)(blockIdx.x / a.blocks), block = (int)(blockIdx.x % a.blocks);
-    const int first = piece * kPiece, last = first + kPiece - 1;
+    const long long first = (long long)piece * a.piece, last = first + a.piece - 1;
     if (last + 1 >= a.count) return;
     const int v = __ldcg(a.key + last);
     if (v >= a.vocab || __ldcg(a.key + last + 1) != v) return;
     // a run that fills the piece and began in front of it belongs to another CTA
     if (first > 0 && __ldcg(a.key + first) == v && __ldcg(a.key + first - 1) == v) return;
-    const int vec = block * kSumThreads + threadIdx.x;
+    // the run's last piece: those behind begin with its token too
+    int behind = piece;
+    for (const int lane = threadIdx.x & 31;;) {
+        const long long next = (long long)(behind + 1 + lane) * a.piece;
+        const unsigned goes_on = __ballot_sync(0xffffffffu, next < a.count && __ldcg(a.key + next) == v);
+        const int n = goes_on == 0xffffffffu ? 32 : __ffs(~goes_on) - 1;
+        behind += n;
+        if (n < 32) break;
+    }
+    const int vec = block * (int)blockDim.x + (int)threadIdx.x;
     if (vec >= a.width / V) return;
-    const int behind = (keys_below(a.key, a.count, v + 1) - 1) / kPiece;    // the run's last piece
     const float *parts = a.parts + (size_t)vec * V;
     SsdRaw<float, V> r;
     r.load(parts + ((size_t)piece * 2 + 1) * a.width);
     float acc[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) acc[k] = r.get(k);
-    constexpr int kAhead = 8;
+    constexpr int kAhead = 16;
     for (int p0 = piece + 1; p0 <= behind; p0 += kAhead) {
         SsdRaw<float, V> part[kAhead];
 #pragma unroll
@@ -336,12 +361,13 @@ __global__ void __launch_bounds__(kSumThreads) embedding_join_kernel(const Gradi
 
 struct BwdPlan {
     size_t keys, parts, total;      // bytes of one array of keys, where the parts begin, all
-    int pieces;
+    int piece, pieces;
 };
 BwdPlan bwd_plan(long long count, int width) {
     const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     BwdPlan p;
-    p.pieces = (int)((count + kPiece - 1) / kPiece);
+    p.piece = piece_of(count);
+    p.pieces = (int)((count + p.piece - 1) / p.piece);
     p.keys = up((size_t)count * 4);
     p.parts = 4 * p.keys;
     p.total = p.parts + (p.pieces > 1 ? (size_t)p.pieces * 2 * width * 4 : 0);
@@ -350,13 +376,14 @@ BwdPlan bwd_plan(long long count, int width) {
 
 template <typename T, typename TO, int V>
 cudaError_t launch_sums(Gradient g, cudaStream_t stream) {
-    g.blocks = (g.width / V + kSumThreads - 1) / kSumThreads;
-    const long long sums = (long long)g.pieces * g.blocks, zeros = ((long long)g.vocab + kZeroRows - 1) / kZeroRows;
-    if (sums + zeros >= (1ll << 31)) return cudaErrorInvalidValue;
-    cudaError_t e = ssd_launch_early(embedding_bwd_kernel<T, TO, V>, dim3((unsigned)(sums + zeros)),
-                                     dim3(kSumThreads), stream, g);
+    const int nvec = g.width / V;
+    g.blocks = (nvec + kSumThreads - 1) / kSumThreads;
+    const dim3 block((unsigned)(((nvec + g.blocks - 1) / g.blocks + 31) / 32 * 32));
+    const long long sums = (long long)g.pieces * g.blocks;
+    if (sums >= (1ll << 31)) return cudaErrorInvalidValue;
+    cudaError_t e = ssd_launch_early(embedding_bwd_kernel<T, TO, V>, dim3((unsigned)sums), block, stream, g);
     if (e != cudaSuccess || g.pieces < 2) return e;
-    return ssd_launch_early(embedding_join_kernel<TO, V>, dim3((unsigned)sums), dim3(kSumThreads), stream, g);
+    return ssd_launch_early(embedding_join_kernel<TO, V>, dim3((unsigned)sums), block, stream, g);
 }
 
 template <typename T, typename TO>
@@ -383,25 +410,39 @@ size_t ssd_embedding_bwd_workspace(long long count, int vocab, int width) {
 
 cudaError_t ssd_launch_embedding_bwd(const SsdEmbeddingBwd &a, void *ws, int sms,
                                      cudaStream_t stream) {
-    (void)sms;
     const BwdPlan plan = bwd_plan(a.count, a.width);
     char *at = static_cast<char *>(ws);
-    Sort s{a.tokens, a.wide, (int)a.count, a.vocab, 1, 1, {}, {}};
+    Sort s{};
+    s.tokens = a.tokens;
+    s.wide = a.wide;
+    s.count = (int)a.count;
+    s.vocab = a.vocab;
     int bits = 1;
     while (a.vocab >> bits) ++bits;
     s.passes = (bits + kMostBits - 1) / kMostBits;
     s.bits = (bits + s.passes - 1) / s.passes;
+    s.run = (int)((a.count + 32ll * kSortCtas * kSortWarps - 1) / (32ll * kSortCtas * kSortWarps)) * 32;
     for (int i = 0; i < 2; ++i) {
         s.key[i] = reinterpret_cast<int *>(at + 2 * i * plan.keys);
         s.at[i] = reinterpret_cast<int *>(at + (2 * i + 1) * plan.keys);
     }
-    constexpr int kSmem = (kSortWarps * (1 << kMostBits) + (1 << kMostBits) + kSortWarps) * 4;
-    cudaError_t e = cudaFuncSetAttribute(sort_tokens_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    s.zero = static_cast<uint8_t *>(a.dtable);
+    s.bytes = (size_t)a.vocab * a.width * (a.out_type == SSD_ELT_F32 ? 4 : 2);
+    // As many clusters beside the sort's as the device holds at once with it: SMs come in
+    // groups of no multiple of eight, so it is fewer than its SMs over eight, and one more
+    // would wait for the sort's end (50 us for 205 MB with 18 of them, 35 with 14)
+    const size_t per = (size_t)kSortCtas * 32 * kSortWarps * 64;        // bytes a cluster takes at once
+    const size_t want = (s.bytes + per - 1) / per, most = sms / kSortCtas > 6 ? sms / kSortCtas - 5 : 1;
+    const unsigned ctas = kSortCtas * (1 + (unsigned)(want < most ? want : most));
+    const bool local = s.run <= kMostLocal;
+    const auto kernel = local ? sort_tokens_kernel<true> : sort_tokens_kernel<false>;
+    const int smem = 4 * kSortWords + (local && s.passes > 1 ? 16 * s.run * kSortWarps : 0);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    sort_tokens_kernel<<<kSortCtas, 32 * kSortWarps, kSmem, stream>>>(s);
+    kernel<<<ctas, 32 * kSortWarps, smem, stream>>>(s);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const Gradient g{s.key[0], s.at[0], (int)a.count, a.vocab, a.width, a.dy, a.dy_stride, a.scale, a.dtable,
-                     reinterpret_cast<float *>(at + plan.parts), plan.pieces, 0};
+                     reinterpret_cast<float *>(at + plan.parts), plan.piece, plan.pieces, 0};
     if (a.in == SSD_ELT_F32)
         return a.out_type == SSD_ELT_F32 ? launch_sums_of<float, float>(g, stream)
                                          : launch_sums_of<float, __nv_bfloat16>(g, stream);

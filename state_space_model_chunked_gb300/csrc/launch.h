@@ -171,6 +171,9 @@ struct SsdLayerNormFwd {
     float *mean, *rstd, *scale;
 };
 cudaError_t ssd_launch_layernorm_fwd(const SsdLayerNormFwd &a, int sms, cudaStream_t stream);
+// Many rows, a row a warp (layernorm_rows.cu).
+bool ssd_layernorm_rows_handles(const SsdLayerNormFwd &a, int sms);
+cudaError_t ssd_launch_layernorm_rows(const SsdLayerNormFwd &a, int sms, unsigned *err, cudaStream_t stream);
 
 struct SsdLayerNormBwd {
     const void *dy, *s, *dresidual;

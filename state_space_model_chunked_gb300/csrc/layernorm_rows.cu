@@ -1,0 +1,202 @@
+// Layer norm forward of many rows, a row a warp (the formulas: layernorm.cu).
+//
+// With a CTA a row, a row waits for two or three barriers, and what an SM has under way does
+// not cover that: 65536 rows of 2560 to 8 bits took 282 us, with a third barrier (a second
+// pass for the squares) 365.  A warp needs none.  Its next row is copied to shared memory
+// while the present one is in registers (kC runs of 8 values a lane), from which the mean,
+// the squares around it, the largest value and the output are taken by turns; weight and
+// bias lie in shared memory too.  Bound by memory: each value is read and written once.
+#include "norm_rows.cuh"
+#include "ptx.cuh"
+
+namespace {
+
+using namespace ssdnorm;
+using namespace ssdptx;
+
+constexpr int kWarps = 8;
+constexpr int kCtasSm(int runs) { return runs <= 4 ? 4 : runs <= 10 ? 2 : 1; }
+
+struct RowsLayout {
+    uint32_t weight, x, r, row, bytes;      // row: bytes of a warp's row, x in front of r
+};
+RowsLayout rows_layout(const SsdLayerNormFwd &a) {
+    const auto up = [](uint32_t n) { return (n + 127) / 128 * 128; };
+    const uint32_t nx = a.in == SSD_ELT_F32 ? 4 : 2, nr = a.stream_type == SSD_ELT_F32 ? 4 : 2;
+    RowsLayout l;
+    l.weight = 128;
+    l.x = l.weight + 2 * up(a.width * 4);
+    l.r = up(a.width * nx);
+    l.row = l.r + (a.residual ? up(a.width * nr) : 0);
+    l.bytes = l.x + kWarps * l.row;
+    return l;
+}
+
+template <typename TX, typename TR, typename TO, int kC>
+__global__ void __launch_bounds__(32 * kWarps, kCtasSm(kC))
+layernorm_rows_kernel(const SsdLayerNormFwd a, const RowsLayout l, unsigned *err) {
+    extern __shared__ __align__(128) uint8_t rows_smem[];
+    constexpr bool kFp8 = sizeof(TO) == 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nvec = a.width / 8;
+    const uint32_t bar = smem_u32(rows_smem) + 8 * warp;
+    uint8_t *const mine = rows_smem + l.x + warp * l.row;
+    float *const weight = reinterpret_cast<float *>(rows_smem + l.weight), *const bias = weight + (l.x - l.weight) / 8;
+    const bool res = a.residual != nullptr;
+    if (lane == 0) {
+        mbar_init(bar, 1);
+        fence_mbar_init();
+    }
+    griddep_wait();
+    const auto fetch = [&](long long row) {
+        const uint32_t bx = a.width * sizeof(TX), br = res ? a.width * sizeof(TR) : 0;
+        mbar_arrive_expect_tx(bar, bx + br);
+        bulk_load(smem_u32(mine), static_cast<const TX *>(a.x) + row * a.x_stride, bx, bar);
+        if (res) bulk_load(smem_u32(mine + l.r), static_cast<const TR *>(a.residual) + row * a.residual_stride, br, bar);
+    };
+    const long long step = (long long)gridDim.x * kWarps;
+    long long row = (long long)blockIdx.x * kWarps + warp;
+    if (lane == 0 && row < a.rows) fetch(row);
+    for (int i = threadIdx.x; i < a.width; i += 32 * kWarps) {
+        weight[i] = a.weight[i];
+        bias[i] = a.bias ? a.bias[i] : 0.f;
+    }
+    __syncthreads();
+    const float share = 1.f / (float)a.width;
+    for (uint32_t turn = 0; row < a.rows; turn ^= 1, row += step) {
+        if (!mbar_wait(bar, turn, kSsdDefaultWaitNs)) ssd_report(err, SSD_DEVERR_TIMEOUT);
+        float s[kC][8], sum = 0.f;
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+            const int i = lane + 32 * c;
+            SsdRaw<TX, 8> x;
+            SsdRaw<TR, 8> r;
+            x.zero();
+            r.zero();
+            if (i < nvec) {
+                x.load(reinterpret_cast<const TX *>(mine) + 8 * i);
+                if (res) r.load(reinterpret_cast<const TR *>(mine + l.r) + 8 * i);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                s[c][k] = res ? x.get(k) + r.get(k) : x.get(k);
+                sum += s[c][k];
+            }
+        }
+        __syncwarp();
+        if (lane == 0 && row + step < a.rows) fetch(row + step);
+        if (res) {
+            TR *const so = static_cast<TR *>(a.residual_out) + row * a.width;
+#pragma unroll
+            for (int c = 0; c < kC; ++c)
+                if (lane + 32 * c < nvec) ssd_store_vec<8>(so + 8 * (lane + 32 * c), s[c]);
+        }
+        const float mean = ssd_warp_sum(sum) * share;
+        float squares = 0.f;
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+            if (lane + 32 * c >= nvec) continue;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                s[c][k] -= mean;
+                squares += s[c][k] * s[c][k];
+            }
+        }
+        const float rstd = rsqrtf(ssd_warp_sum(squares) * share + a.eps);
+        float mx = 0.f;
+        TO *const y = static_cast<TO *>(a.y) + row * a.width;
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+            const int i = lane + 32 * c;
+            if (i >= nvec) continue;
+            SsdRaw<float, 8> w, b;
+            w.load(weight + 8 * i);
+            b.load(bias + 8 * i);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                s[c][k] = s[c][k] * rstd * w.get(k) + b.get(k);
+                if constexpr (kFp8) mx = fmaxf(mx, fabsf(s[c][k]));
+            }
+            if constexpr (!kFp8) ssd_store_vec<8>(y + 8 * i, s[c]);
+        }
+        if constexpr (kFp8) {
+            mx = ssd_warp_max(mx);
+            if (rstd != rstd) mx = rstd;
+            const RowScale q(mx);
+#pragma unroll
+            for (int c = 0; c < kC; ++c) {
+                const int i = lane + 32 * c;
+                if (i >= nvec) continue;
+                if (q.tiny) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) s[c][k] = q.apply(s[c][k]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) s[c][k] *= q.inv;
+                }
+                ssd_store_vec<8>(y + 8 * i, s[c]);
+            }
+            if (lane == 0) a.scale[row] = q.scale;
+        }
+        if (lane == 0) {
+            a.mean[row] = mean;
+            a.rstd[row] = rstd;
+        }
+    }
+}
+
+template <typename TX, typename TR, typename TO, int kC>
+cudaError_t launch(const SsdLayerNormFwd &a, int sms, unsigned *err, cudaStream_t stream) {
+    const RowsLayout l = rows_layout(a);
+    const auto kernel = layernorm_rows_kernel<TX, TR, TO, kC>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)l.bytes);
+    if (e != cudaSuccess) return e;
+    int ctas = (int)(233472 / (l.bytes + 1024));
+    if (ctas > kCtasSm(kC)) ctas = kCtasSm(kC);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(walkers((a.rows + kWarps - 1) / kWarps, sms, ctas));
+    cfg.blockDim = dim3(32 * kWarps);
+    cfg.dynamicSmemBytes = l.bytes;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a, l, err);
+}
+
+template <typename TX, typename TR, typename TO>
+cudaError_t launch_runs(const SsdLayerNormFwd &a, int sms, unsigned *err, cudaStream_t stream) {
+    const int runs = (a.width + 255) / 256;
+    if (runs <= 2) return launch<TX, TR, TO, 2>(a, sms, err, stream);
+    if (runs <= 4) return launch<TX, TR, TO, 4>(a, sms, err, stream);
+    if (runs <= 6) return launch<TX, TR, TO, 6>(a, sms, err, stream);
+    if (runs <= 8) return launch<TX, TR, TO, 8>(a, sms, err, stream);
+    if (runs <= 10) return launch<TX, TR, TO, 10>(a, sms, err, stream);
+    return launch<TX, TR, TO, 16>(a, sms, err, stream);
+}
+template <typename TX, typename TR>
+cudaError_t launch_out(const SsdLayerNormFwd &a, int sms, unsigned *err, cudaStream_t stream) {
+    switch (a.out) {
+        case SSD_ELT_F32: return launch_runs<TX, TR, float>(a, sms, err, stream);
+        case SSD_ELT_BF16: return launch_runs<TX, TR, __nv_bfloat16>(a, sms, err, stream);
+        default: return launch_runs<TX, TR, __nv_fp8_e4m3>(a, sms, err, stream);
+    }
+}
+
+}  // namespace
+
+// Rows enough for a warp each on every SM, in vectors, and few enough values for its registers.
+bool ssd_layernorm_rows_handles(const SsdLayerNormFwd &a, int sms) {
+    const int nx = a.in == SSD_ELT_F32 ? 4 : 2, nr = a.stream_type == SSD_ELT_F32 ? 4 : 2;
+    const int no = a.out == SSD_ELT_F32 ? 4 : a.out == SSD_ELT_BF16 ? 2 : 0;
+    return a.rows >= 4ll * sms && a.width % 8 == 0 && a.width <= 4096 && rows_layout(a).bytes <= 232448 &&
+           vec8(a.x, a.x_stride, nx) && vec8(a.residual, a.residual_stride, nr) && vec8(a.residual_out, a.width, nr) &&
+           ((uintptr_t)a.y & 7u) == 0 && (no == 0 || vec8(a.y, a.width, no));
+}
+
+cudaError_t ssd_launch_layernorm_rows(const SsdLayerNormFwd &a, int sms, unsigned *err, cudaStream_t stream) {
+    if (a.in == SSD_ELT_F32) return launch_out<float, float>(a, sms, err, stream);
+    if (a.stream_type == SSD_ELT_F32) return launch_out<__nv_bfloat16, float>(a, sms, err, stream);
+    return launch_out<__nv_bfloat16, __nv_bfloat16>(a, sms, err, stream);
+}

@@ -241,6 +241,9 @@ __device__ __forceinline__ uint32_t cluster_ld_u32(uint32_t addr) {
 __device__ __forceinline__ void cluster_st_u32(uint32_t addr, uint32_t v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
+__device__ __forceinline__ void cluster_st_u32x2(uint32_t addr, uint32_t x, uint32_t y) {
+    asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
+}
 // This thread's accesses so far, in front of its later ones, for the cluster's threads.
 __device__ __forceinline__ void cluster_fence() {
     asm volatile("fence.acq_rel.cluster;" ::: "memory");

@@ -53,7 +53,8 @@ def test_lookup_without_scale_is_exact():
 @pytest.mark.parametrize("shape,vocab,width,kind", [((1,), 1, 1, "spread"), ((3, 5), 7, 33, "spread"), ((31,), 5, 64, "one"),
                                                     ((33,), 5, 64, "one"), ((64,), 3, 1032, "spread"), ((5000,), 300, 264, "few"),
                                                     ((4, 1031), 600, 40, "spread"), ((9000,), 70000, 16, "few"),
-                                                    ((2049,), 9, 100, "one"), ((70,), 513, 8, "none"), ((40000,), 250001, 8, "spread")])
+                                                    ((2049,), 9, 100, "one"), ((70,), 513, 8, "none"), ((40000,), 250001, 8, "spread"),
+                                                    ((90000,), 3000, 8, "few"), ((90001,), 300000, 4, "spread"), ((2000,), 30000, 640, "few")])
 @pytest.mark.parametrize("d,od", [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16"), ("f32", "bf16")])
 def test_gradient(shape, vocab, width, kind, d, od):
     rng = np.random.default_rng(vocab + width)
