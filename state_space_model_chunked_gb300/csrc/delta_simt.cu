@@ -119,12 +119,13 @@ __device__ __forceinline__ void columns(const float *row, int lane, float (&v)[k
         v[i + 3] = x.w;
     }
 }
+// (in four sums: one would be a chain of kV additions)
 template <int kV>
 __device__ __forceinline__ float dot(const float (&a)[kV], const float (&b)[kV]) {
-    float v = 0.f;
+    float v[4] = {};
 #pragma unroll
-    for (int i = 0; i < kV; ++i) v += a[i] * b[i];
-    return v;
+    for (int i = 0; i < kV; ++i) v[i & 3] += a[i] * b[i];
+    return (v[0] + v[1]) + (v[2] + v[3]);
 }
 
 // kTile tokens' rows of `width` values at `offset` of each token, zeros behind them and in
@@ -149,11 +150,38 @@ struct Walk {
     int slabs;
 };
 
+template <int kV, int kR>
+struct WalkTile {
+    static constexpr int kN = kV * kLanes, kRows = kRowsPass * kR;
+    float q[kTile][kN], k[kTile][kN], v[kTile][kRows];
+    float decay[kTile], beta[kTile], kq[kTile];
+};
+// kTile tokens' rows of `pad` values, in the registers of kThreads threads on their way.
+template <int kCount>
+struct Ahead {
+    static constexpr int kEach = (kCount + kThreads - 1) / kThreads;
+    float x[kEach];
+    __device__ __forceinline__ void fetch(int pad, const void *from, bool bf16, long long token, long long stride,
+                                          size_t offset, int width, int tokens) {
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+            const int i = threadIdx.x + j * kThreads, t = i / pad, c = i % pad;
+            x[j] = i < kCount && t < tokens && c < width ? load(from, (size_t)(token + t) * stride + offset + c, bf16) : 0.f;
+        }
+    }
+    __device__ __forceinline__ void put(float *to) const {
+#pragma unroll
+        for (int j = 0; j < kEach; ++j)
+            if (threadIdx.x + j * kThreads < kCount) to[threadIdx.x + j * kThreads] = x[j];
+    }
+};
+
 template <int kV, int kR, bool kU>
 __global__ void __launch_bounds__(kThreads) delta_walk_kernel(const Walk a) {
+    extern __shared__ __align__(16) unsigned char delta_smem[];
+    using Tile = WalkTile<kV, kR>;
+    Tile *const tiles = reinterpret_cast<Tile *>(delta_smem);
     constexpr int kN = kV * kLanes, kRows = kRowsPass * kR;
-    __shared__ __align__(16) float q[kTile][kN], k[kTile][kN];
-    __shared__ float v[kTile][kRows], decay[kTile], beta[kTile];
     const SsdDelta &d = a.d;
     int seq, head, slab, run;
     cta_place(d, a.slabs, seq, head, slab, run);
@@ -173,46 +201,75 @@ __global__ void __launch_bounds__(kThreads) delta_walk_kernel(const Walk a) {
     } else {
         S.load(a.init ? a.init + state : nullptr, d.n);
     }
-    const int rows = min(kRows, d.p - slab * kRows);
+    const int rows = min(kRows, d.p - slab * kRows), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // the next tile is loaded while the present one is used
+    Ahead<kTile * kN> qa, ka;
+    Ahead<kTile * kRows> va;
+    float ga = 0.f, ba = 0.f;
+    const auto fetch = [&](int t0) {
+        const int tokens = min(kTile, to - t0);
+        ka.fetch(kN, d.k, d.bf16, first + t0, d.k_stride, (size_t)group * d.n, d.n, tokens);
+        if constexpr (!kU) qa.fetch(kN, d.q, d.bf16, first + t0, d.q_stride, (size_t)group * d.n, d.n, tokens);
+        va.fetch(kRows, d.v, d.bf16, first + t0, d.v_stride, (size_t)head * d.p + slab * kRows, rows, tokens);
+        if (threadIdx.x < tokens) {
+            const size_t i = (size_t)(first + t0 + threadIdx.x) * d.heads + head;
+            ga = d.g[i];
+            ba = d.beta[i];
+        }
+    };
+    if (from < to) fetch(from);
     for (int t0 = from; t0 < to; t0 += kTile) {
+        Tile &m = tiles[(t0 - from) / kTile & 1];
+        ka.put(&m.k[0][0]);
+        if constexpr (!kU) qa.put(&m.q[0][0]);
+        va.put(&m.v[0][0]);
+        if (threadIdx.x < kTile) {
+            m.decay[threadIdx.x] = decay_of(ga);
+            m.beta[threadIdx.x] = ba;
+        }
+        // (one barrier a tile: the other buffer is written only behind the next one)
+        __syncthreads();
+        const int tokens = min(kTile, to - t0);
+        if (t0 + kTile < to) fetch(t0 + kTile);
         if constexpr (!kU) {
+            // k_t q_t, a token a warp
+            for (int t = warp; t < tokens; t += kThreads / 32) {
+                float v = 0.f;
+                for (int c = lane; c < kN; c += 32) v += m.k[t][c] * m.q[t][c];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                if (lane == 0) m.kq[t] = v;
+            }
+            __syncthreads();
             if (a.checkpoints && t0 % kC == 0)
                 S.store(a.checkpoints + ((size_t)ssd_delta_slot(first, seq, t0 / kC) * d.heads + head) * size, d.n);
         }
-        const int tokens = min(kTile, to - t0);
-        __syncthreads();
-        stage(&k[0][0], kN, d.k, d.bf16, first + t0, d.k_stride, (size_t)group * d.n, d.n, tokens);
-        if constexpr (!kU)
-            stage(&q[0][0], kN, d.q, d.bf16, first + t0, d.q_stride, (size_t)group * d.n, d.n, tokens);
-        stage(&v[0][0], kRows, d.v, d.bf16, first + t0, d.v_stride, (size_t)head * d.p + slab * kRows, rows, tokens);
-        if (threadIdx.x < tokens) {
-            const size_t i = (size_t)(first + t0 + threadIdx.x) * d.heads + head;
-            decay[threadIdx.x] = decay_of(d.g[i]);
-            beta[threadIdx.x] = d.beta[i];
-        }
-        __syncthreads();
         for (int t = 0; t < tokens; ++t) {
-            float kc[kV], qc[kV], sk[kR], sq[kR], kq = 0.f;
-            columns(k[t], S.lane, kc);
-            if constexpr (!kU) {
-                columns(q[t], S.lane, qc);
-                kq = lanes_sum(dot(kc, qc));
-            }
-            const float f = decay[t];
+            float kc[kV], qc[kV], sk[kR], sq[kR];
+            columns(m.k[t], S.lane, kc);
+            if constexpr (!kU) columns(m.q[t], S.lane, qc);
+            const float f = m.decay[t], be = m.beta[t];
 #pragma unroll
             for (int r = 0; r < kR; ++r) {
-                sk[r] = lanes_sum(dot(S.s[r], kc));
-                if constexpr (!kU) sq[r] = lanes_sum(dot(S.s[r], qc));
+                sk[r] = dot(S.s[r], kc);
+                if constexpr (!kU) sq[r] = dot(S.s[r], qc);
             }
 #pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1)
+#pragma unroll
+                for (int r = 0; r < kR; ++r) {
+                    sk[r] += __shfl_xor_sync(0xffffffffu, sk[r], o);
+                    if constexpr (!kU) sq[r] += __shfl_xor_sync(0xffffffffu, sq[r], o);
+                }
+#pragma unroll
             for (int r = 0; r < kR; ++r) {
-                const float u = beta[t] * (v[t][r * kRowsPass + threadIdx.x / kLanes] - f * sk[r]);
+                const float u = be * (m.v[t][r * kRowsPass + threadIdx.x / kLanes] - f * sk[r]);
 #pragma unroll
                 for (int i = 0; i < kV; ++i) S.s[r][i] = f * S.s[r][i] + u * kc[i];
                 if (S.lane == 0 && S.row[r] >= 0) {
                     const size_t at = (size_t)head * d.p + S.row[r];
                     if constexpr (kU) a.u[(size_t)(first + t0 + t) * d.heads * d.p + at] = u;
-                    else store(a.o, (size_t)(first + t0 + t) * a.o_stride + at, d.bf16, d.scale * (f * sq[r] + u * kq));
+                    else store(a.o, (size_t)(first + t0 + t) * a.o_stride + at, d.bf16, d.scale * (f * sq[r] + u * m.kq[t]));
                 }
             }
         }
@@ -522,15 +579,18 @@ __global__ void __launch_bounds__(128) delta_gates_kernel(const Back a, float *d
     }
 }
 
+// Rows of the state a thread has: one for heads of few rows (and forward where there are few
+// CTAs), else two: four leave an SM one CTA backward (8 x 2047 tokens, 16 heads of 128 x 128:
+// 10.7 against 8.6 ms).
 template <template <int, int> class Launch, typename... A>
-cudaError_t by_shape(int p, int n, A... args) {
-    const bool one = p <= kRowsPass;
-    if (n <= 32) return one ? Launch<4, 1>::run(args...) : Launch<4, 4>::run(args...);
-    if (n <= 64) return one ? Launch<8, 1>::run(args...) : Launch<8, 4>::run(args...);
-    if (n <= 128) return one ? Launch<16, 1>::run(args...) : Launch<16, 4>::run(args...);
-    return one ? Launch<32, 1>::run(args...) : Launch<32, 2>::run(args...);
+cudaError_t by_shape(bool one, int n, A... args) {
+    if (n <= 32) return one ? Launch<4, 1>::run(args...) : Launch<4, 2>::run(args...);
+    if (n <= 64) return one ? Launch<8, 1>::run(args...) : Launch<8, 2>::run(args...);
+    if (n <= 128) return one ? Launch<16, 1>::run(args...) : Launch<16, 2>::run(args...);
+    return Launch<32, 1>::run(args...);
 }
-int slab_rows(int p, int n) { return p <= kRowsPass ? kRowsPass : kRowsPass * (n <= 128 ? 4 : 2); }
+bool one_row(int p) { return p <= kRowsPass; }
+int slab_rows(int p, int n) { return one_row(p) || n > 128 ? kRowsPass : 2 * kRowsPass; }
 
 template <int kV, int kR>
 struct LaunchFwd {
@@ -538,7 +598,10 @@ struct LaunchFwd {
         a.slabs = (a.d.p + kRowsPass * kR - 1) / (kRowsPass * kR);
         const long long ctas = (long long)a.d.nseq * a.d.heads * a.slabs;
         if (ctas >= (1ll << 31)) return cudaErrorInvalidValue;
-        delta_walk_kernel<kV, kR, false><<<(unsigned)ctas, kThreads, 0, stream>>>(a);
+        constexpr int kSmem = 2 * (int)sizeof(WalkTile<kV, kR>);
+        const cudaError_t e = cudaFuncSetAttribute(delta_walk_kernel<kV, kR, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        delta_walk_kernel<kV, kR, false><<<(unsigned)ctas, kThreads, kSmem, stream>>>(a);
         return cudaGetLastError();
     }
 };
@@ -552,7 +615,10 @@ struct LaunchBack {
         if (e != cudaSuccess) return e;
         e = cudaFuncSetAttribute(delta_again_kernel<kV, kR>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
-        if (runs > 0) delta_walk_kernel<kV, kR, true><<<(unsigned)(ctas * runs), kThreads, 0, stream>>>(u);
+        constexpr int kWalk = 2 * (int)sizeof(WalkTile<kV, kR>);
+        e = cudaFuncSetAttribute(delta_walk_kernel<kV, kR, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWalk);
+        if (e != cudaSuccess) return e;
+        if (runs > 0) delta_walk_kernel<kV, kR, true><<<(unsigned)(ctas * runs), kThreads, kWalk, stream>>>(u);
         delta_back_kernel<kV, kR><<<(unsigned)ctas, kThreads, kSmem, stream>>>(a);
         if (runs > 0) delta_again_kernel<kV, kR><<<(unsigned)(ctas * runs), kThreads, kSmem, stream>>>(a);
         return cudaGetLastError();
@@ -600,7 +666,7 @@ cudaError_t ssd_launch_delta_fwd_simt(const SsdDeltaFwd &a, int sms, cudaStream_
     const Walk w{a.in, a.init, nullptr, a.o, a.o_stride, a.final_state, a.checkpoints, nullptr, 1};
     // few CTAs: slabs of one row a thread, which make a token shorter
     const long long most = (long long)a.in.nseq * a.in.heads * ((a.in.p + kRowsPass - 1) / kRowsPass);
-    return by_shape<LaunchFwd>(most <= 4ll * sms ? 1 : a.in.p, a.in.n, w, stream);
+    return by_shape<LaunchFwd>(one_row(a.in.p) || most <= 4ll * sms, a.in.n, w, stream);
 }
 
 size_t ssd_delta_bwd_simt_workspace(const SsdDelta &d) { return back_plan(d).total; }
@@ -612,7 +678,7 @@ cudaError_t ssd_launch_delta_bwd_simt(const SsdDeltaBwd &a, void *ws, cudaStream
     const Walk u{d, nullptr, a.checkpoints, nullptr, 0, nullptr, nullptr, at(p.u), p.slabs};
     const Back b{d, a.dout, a.checkpoints, a.dfinal, a.do_stride, a.dv_stride, a.dv, a.dinit, at(p.u), at(p.w),
                  at(p.dq), at(p.dk), at(p.anchor), at(p.ov), at(p.rw), p.slabs};
-    cudaError_t e = by_shape<LaunchBack>(d.p, d.n, u, b, stream);
+    cudaError_t e = by_shape<LaunchBack>(one_row(d.p), d.n, u, b, stream);
     if (e != cudaSuccess || d.longest == 0) return e;
     e = ssd_launch_delta_group_sums(b.dq, a.dq, a.dq_stride, b.dk, a.dk, a.dk_stride, d, d.heads / d.groups * p.slabs, stream);
     if (e != cudaSuccess) return e;

@@ -443,7 +443,9 @@ delta_walk_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         return;
     }
     const int head = (int)(blockIdx.x % d.heads), block = (int)(blockIdx.x / d.heads % a.blocks);
-    const int seq = (int)(blockIdx.x / d.heads / a.blocks), group = head / (d.heads / d.groups);
+    const int seq = sequence_of(d, (int)(blockIdx.x / d.heads / a.blocks),
+                                reinterpret_cast<volatile int *>(smem + Lay::kCtl + 8 * kBars + 8));
+    const int group = head / (d.heads / d.groups);
     const long long first = d.cu ? d.cu[seq] : (long long)seq * d.length;
     const int len = d.cu ? d.cu[seq + 1] - d.cu[seq] : d.length;
     const int chunks = (len + kC - 1) / kC, p0 = block * 128;

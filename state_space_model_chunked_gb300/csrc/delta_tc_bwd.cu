@@ -93,8 +93,8 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         if (threadIdx.x == 0) ssd_report(a.err, SSD_DEVERR_SMEM_ALIGN);
         return;
     }
-    const int head = (int)(blockIdx.x % d.heads), seq = (int)(blockIdx.x / d.heads);
-    const int group = head / (d.heads / d.groups);
+    const int head = (int)(blockIdx.x % d.heads), group = head / (d.heads / d.groups);
+    const int seq = sequence_of(d, (int)(blockIdx.x / d.heads), reinterpret_cast<volatile int *>(smem + Lay::kCtl + 8 * kBars + 8));
     const long long first = d.cu ? d.cu[seq] : (long long)seq * d.length;
     const int len = d.cu ? d.cu[seq + 1] - d.cu[seq] : d.length;
     const int chunks = (len + kC - 1) / kC;
