@@ -609,7 +609,7 @@ size_t ssd_delta_scan_workspace_bytes(ssd_dtype dtype, long long tokens, int nse
                                       int dstate, int ngroups) {
     SsdDelta d{};
     if (!delta_sizes(dtype, tokens, nseq, nheads, headdim, dstate, ngroups, &d)) return kBad;
-    return ssd_delta_tc_workspace(d);
+    return ssd_delta_tc_workspace(d, ssd_sm_count());
 }
 
 size_t ssd_delta_scan_bwd_workspace_bytes(ssd_dtype dtype, long long tokens, int nseq, int nheads,
@@ -635,7 +635,7 @@ ssd_status ssd_delta_scan_fwd(const void *q, const void *k, const void *v, const
     if ((a.in.tokens > 0 && !array(o, size_of(dtype))) || o_stride < (long long)nheads * headdim ||
         !maybe(init_state, 4) || !maybe(final_state, 4) || !maybe(checkpoints, 4))
         return SSD_ERR_INVALID_ARG;
-    st = check_workspace(workspace, workspace_bytes, ssd_delta_tc_workspace(a.in), 256);
+    st = check_workspace(workspace, workspace_bytes, ssd_delta_tc_workspace(a.in, ssd_sm_count()), 256);
     if (st != SSD_OK) return st;
     a.init = init_state;
     a.o = o;

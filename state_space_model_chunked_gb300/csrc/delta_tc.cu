@@ -405,6 +405,14 @@ struct WalkSmem {
     static constexpr uint32_t kBytes = kCtl + 256;
 };
 
+// A part's first token within its sequence of `len`: parts are whole chunks, but for the end,
+// and all as long, but for a first one of half that length where `half` is 1.
+__device__ __forceinline__ int part_start(int len, int part, int parts, int half) {
+    if (part == 0) return 0;
+    const long long at = (long long)((len + kC - 1) / kC) * (2 * part - half) / (2 * parts - half) * kC;
+    return at < len ? (int)at : len;
+}
+
 struct WalkTc {
     SsdDelta d;
     const uint8_t *records;
@@ -414,6 +422,13 @@ struct WalkTc {
     float *final_state, *checkpoints;
     int blocks;                 // of 128 rows a head
     bool o_vectors;             // whether the output's rows start on 16 bytes
+    // A sequence in parts that are walked side by side (segments > 1): `d` has the parts for
+    // sequences.  For the states they start from, `starts` [seq][segment][head][P][N], come
+    // first: every part but the last from a state of zeros (the first from its own), for its
+    // end; and for all of these but the first what they make of the rows of a unit matrix,
+    // `maps` [seq][segment - 1][head][N][N].
+    int segments, half;
+    float *starts, *maps;
     unsigned *err;
     unsigned long long wait_ns;
     bool withhold;
@@ -428,7 +443,7 @@ enum WalkBar {
     kBars
 };
 
-template <int kPanels>
+template <int kPanels, bool kEnds>
 __global__ void __launch_bounds__(kWalkThreads, 1)
 delta_walk_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                      const __grid_constant__ CUtensorMap mapV, const WalkTc a) {
@@ -442,18 +457,46 @@ delta_walk_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         if (threadIdx.x == 0) ssd_report(a.err, SSD_DEVERR_SMEM_ALIGN);
         return;
     }
-    const int head = (int)(blockIdx.x % d.heads), block = (int)(blockIdx.x / d.heads % a.blocks);
-    const int seq = sequence_of(d, (int)(blockIdx.x / d.heads / a.blocks),
-                                reinterpret_cast<volatile int *>(smem + Lay::kCtl + 8 * kBars + 8));
+    // kEnds: parts for their ends or (map) for their maps, without output
+    // (first parts last, for where there are too many jobs for the SMs)
+    const unsigned maps = kEnds ? (unsigned)d.nseq * (a.segments - 2) * d.heads : 0;
+    const bool map = kEnds && blockIdx.x < maps;
+    const unsigned job = blockIdx.x - (map ? 0 : maps);
+    const int blocks = map ? 1 : a.blocks, rows = map ? d.n : d.p;
+    const int head = (int)(job % d.heads), block = (int)(job / d.heads % blocks);
+    int seq = (int)(job / d.heads / blocks), segment = 0;
+    if constexpr (kEnds) {
+        segment = a.segments - 2 - seq / d.nseq;
+        seq %= d.nseq;
+    } else {
+        seq = sequence_of(d, seq, reinterpret_cast<volatile int *>(smem + Lay::kCtl + 8 * kBars + 8));
+    }
     const int group = head / (d.heads / d.groups);
-    const long long first = d.cu ? d.cu[seq] : (long long)seq * d.length;
-    const int len = d.cu ? d.cu[seq + 1] - d.cu[seq] : d.length;
+    long long first = d.cu ? d.cu[seq] : (long long)seq * d.length;
+    int len = d.cu ? d.cu[seq + 1] - d.cu[seq] : d.length;
+    if constexpr (kEnds) {
+        const int at = part_start(len, segment, a.segments, a.half);
+        len = part_start(len, segment + 1, a.segments, a.half) - at;
+        first += at;
+    }
     const int chunks = (len + kC - 1) / kC, p0 = block * 128;
-    const size_t state = ((size_t)seq * d.heads + head) * d.p * d.n;
+    const size_t one = (size_t)rows * d.n;
+    // where the state comes from (null: zeros, or a map's unit matrix) and goes to
+    const auto source = [&]() -> const float * {
+        return a.init && segment == 0 ? a.init + ((size_t)seq * d.heads + head) * one : nullptr;
+    };
+    const auto target = [&]() -> float * {
+        if (map) return a.maps + (((size_t)seq * (a.segments - 2) + segment - 1) * d.heads + head) * one;
+        if (kEnds) return a.starts + (((size_t)seq * a.segments + segment + 1) * d.heads + head) * one;
+        if (!a.final_state || (seq + 1) % a.segments) return nullptr;
+        return a.final_state + ((size_t)(seq / a.segments) * d.heads + head) * one;
+    };
     if (chunks == 0) {
-        if (a.final_state)
-            for (long long i = threadIdx.x; i < (long long)min(128, d.p - p0) * d.n; i += kWalkThreads)
-                a.final_state[state + (size_t)p0 * d.n + i] = a.init ? a.init[state + (size_t)p0 * d.n + i] : 0.f;
+        const float *init = source();
+        if (float *const final_state = target())
+            for (long long i = threadIdx.x; i < (long long)min(128, rows - p0) * d.n; i += kWalkThreads)
+                final_state[(size_t)p0 * d.n + i] = init ? init[(size_t)p0 * d.n + i]
+                                                    : map && i / d.n == i % d.n ? 1.f : 0.f;
         return;
     }
     const auto bar = [&](int i) { return base + Lay::kCtl + 8u * (uint32_t)i; };
@@ -479,7 +522,7 @@ delta_walk_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot;
-    const long long slot0 = ssd_delta_slot(first, seq, 0);
+    const long long slot0 = ssd_delta_slot(first, kEnds ? seq : seq / a.segments, 0);
     int loaded = 0;
 
     if (warp == kLoadWarp) {
@@ -489,15 +532,15 @@ delta_walk_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
             if (elect_one()) {
                 const uint32_t to = base + s * Lay::kStage;
                 const int token = (int)(first + (long long)c * kC);
-                mbar_arrive_expect_tx(bar(kFull + s), 2 * kPanels * kPanel + kRecord + 64 * 256);
+                mbar_arrive_expect_tx(bar(kFull + s), (kEnds ? 1 : 2) * kPanels * kPanel + kRecord + (map ? 0 : 64 * 256));
 #pragma unroll
                 for (int p = 0; p < kPanels; ++p) {
                     tma_load_3d(to + Lay::kK + p * kPanel, &mapK, bar(kFull + s), 64 * p, group, token);
-                    tma_load_3d(to + Lay::kQ + p * kPanel, &mapQ, bar(kFull + s), 64 * p, group, token);
+                    if (!kEnds) tma_load_3d(to + Lay::kQ + p * kPanel, &mapQ, bar(kFull + s), 64 * p, group, token);
                 }
                 bulk_load(to + Lay::kRec, a.records + ((size_t)(slot0 + c) * d.heads + head) * kRecord, kRecord,
                           bar(kFull + s));
-                tma_load_3d(to + Lay::kV, &mapV, bar(kFull + s), p0, head, token);
+                if (!map) tma_load_3d(to + Lay::kV, &mapV, bar(kFull + s), p0, head, token);
             }
             __syncwarp();
             loaded = c + 1;
@@ -541,10 +584,12 @@ delta_walk_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
                 if (!(a.withhold && blockIdx.x == 0 && c == 0)) mma_commit(bar(kKs));
             }
             __syncwarp();
-            if (c > 0 && !wait.warp(bar(kPuRead), (c - 1) & 1)) break;
-            tc_fence_after();
-            if (one) over_n(kColO, kColSh, at + Lay::kQ, false);
-            __syncwarp();
+            if (!kEnds) {
+                if (c > 0 && !wait.warp(bar(kPuRead), (c - 1) & 1)) break;
+                tc_fence_after();
+                if (one) over_n(kColO, kColSh, at + Lay::kQ, false);
+                __syncwarp();
+            }
             if (!wait.warp(bar(kRh), c & 1)) break;
             tc_fence_after();
             if (one) {
@@ -557,8 +602,10 @@ delta_walk_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
             if (one) {
                 triangle(kColX, kColRl, at + Lay::kRec + kRecT, true);
                 mma_commit(bar(kU));
-                over_n(kColO, kColSl, at + Lay::kQ, true);
-                mma_commit(bar(kQs));
+                if (!kEnds) {
+                    over_n(kColO, kColSl, at + Lay::kQ, true);
+                    mma_commit(bar(kQs));
+                }
             }
             __syncwarp();
             const uint64_t keys = smem_desc(at + Lay::kK, kPanel, 1024, kSwizzle128B);
@@ -575,8 +622,10 @@ delta_walk_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
 #pragma unroll
                 for (int k = 0; k < 4; ++k) mma_ts(tmem + kColS, tmem + kColWl + 8 * k, keys + 128 * k, kIdS, 1);
                 mma_commit(bar(kS));
+                if (kEnds) mma_commit(bar(kEmpty + s));
             }
             __syncwarp();
+            if (kEnds) continue;
             if (!wait.warp(bar(kUReady), c & 1) || !wait.warp(bar(kQsRead), c & 1)) break;
             tc_fence_after();
             if (one) {
@@ -601,7 +650,12 @@ delta_walk_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         for (int c = 0; c < chunks; ++c) {
             const int s = c & 1, tokens = min(kC, len - c * kC);
             const float *gates = reinterpret_cast<const float *>(smem + s * Lay::kStage + Lay::kRec + kRecGates) + 32 * half;
-            if (!wait.warp(bar(kFull + s), (c >> 1) & 1) || !wait.warp(bar(kU), c & 1)) break;
+            if (!wait.warp(bar(kFull + s), (c >> 1) & 1)) break;
+            if (kEnds) {
+                if (lane == 0) mbar_arrive(bar(kEmpty + s));
+                continue;
+            }
+            if (!wait.warp(bar(kU), c & 1)) break;
             tc_fence_after();
             {
                 uint32_t r[32], hi[16], lo[16];
@@ -679,7 +733,7 @@ delta_walk_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         const int n0 = part * kMine;
         const auto to_memory = [&](float *m, const float (&v)[kMine]) {
             store_rows<kMine>(reinterpret_cast<float *>(smem + Lay::kRows + warp * kStageRows), v,
-                              m + (size_t)(p0 + 32 * q) * d.n + n0, d.n, d.p - (p0 + 32 * q), d.n - n0);
+                              m + (size_t)(p0 + 32 * q) * d.n + n0, d.n, rows - (p0 + 32 * q), d.n - n0);
         };
         // what this thread wrote to tensor memory is there for the products
         const auto ready = [&](int which) {
@@ -713,7 +767,7 @@ delta_walk_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
                 }
                 tmem_st16(tq + kColS + n0 + 16 * h, f);
             }
-            if (a.checkpoints) to_memory(a.checkpoints + ((size_t)(slot0 + c) * d.heads + head) * d.p * d.n, v);
+            if (!kEnds && a.checkpoints) to_memory(a.checkpoints + ((size_t)(slot0 + c) * d.heads + head) * one, v);
         };
         const auto stage = [&](int c) { return smem + (c & 1) * Lay::kStage; };
         const auto clean = [&](int c) {
@@ -724,10 +778,12 @@ delta_walk_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         bool on = wait.warp(bar(kFull), 0);
         if (on) {
             clean(0);
+            const float *init = source();
             float v[kMine];
 #pragma unroll
             for (int i = 0; i < kMine; ++i)
-                v[i] = a.init && p < d.p && n0 + i < d.n ? a.init[state + (size_t)p * d.n + n0 + i] : 0.f;
+                v[i] = init ? (p < rows && n0 + i < d.n ? init[(size_t)p * d.n + n0 + i] : 0.f)
+                            : map && n0 + i == p ? 1.f : 0.f;
             put(0, v, reinterpret_cast<const float *>(stage(0) + Lay::kRec + kRecGates)[kC - 1]);
         }
         for (int c = 0; on && c < chunks; ++c) {
@@ -737,7 +793,7 @@ delta_walk_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
             {
                 const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(stage(c) + Lay::kV) + 16 * part * 128 + row;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = __bfloat162float(v[i * 128]);
+                for (int i = 0; i < 16; ++i) x[i] = map ? 0.f : __bfloat162float(v[i * 128]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) *reinterpret_cast<float4 *>(f + 4 * i) = gates[i];
             }
@@ -813,7 +869,7 @@ delta_walk_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
 #pragma unroll
             for (int i = 0; i < kMine; ++i) y[i] = __uint_as_float(m[i]);
             if (more) put(c + 1, y, decay);
-            else if (a.final_state) to_memory(a.final_state + state, y);
+            else if (float *const final_state = target()) to_memory(final_state, y);
         }
     }
     // copies in flight land before the CTA ends
@@ -824,6 +880,89 @@ delta_walk_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
     tc_fence_before();
     __syncthreads();
     if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// The states that a sequence's parts start from: of the first what its own is; of the second
+// that one's end; E_s <- E_s + E_(s-1) M_(s-1) from there on.  16 rows of a state a CTA, a
+// thread a column of eight of them.  And the offsets of the parts.
+constexpr int kJoinRows = 16;
+__global__ void __launch_bounds__(256)
+delta_join_kernel(const SsdDelta d, const float *init, int segments, int half_first, int *cu, float *starts, const float *maps) {
+    __shared__ float e[kJoinRows][129];
+    const int seq = (int)(blockIdx.x / d.heads), head = (int)(blockIdx.x % d.heads), n = d.n;
+    const int r0 = blockIdx.y * kJoinRows, col = threadIdx.x & 127, half = threadIdx.x >> 7;
+    const size_t one = (size_t)d.p * n;
+    if (head == 0 && blockIdx.y == 0 && threadIdx.x <= segments) {
+        const int first = d.cu ? d.cu[seq] : seq * d.length, len = d.cu ? d.cu[seq + 1] - first : d.length;
+        cu[seq * segments + threadIdx.x] = first + part_start(len, threadIdx.x, segments, half_first);     // (a sequence's end twice)
+    }
+    float *const own = starts + ((size_t)seq * segments * d.heads + head) * one + (size_t)r0 * n;
+    for (int i = threadIdx.x; i < min(kJoinRows, d.p - r0) * n; i += 256)
+        own[i] = init ? init[((size_t)seq * d.heads + head) * one + (size_t)r0 * n + i] : 0.f;
+    for (int s = 2; s < segments; ++s) {
+        const float *from = own + (size_t)(s - 1) * d.heads * one;
+        float *const to = own + (size_t)s * d.heads * one;
+        const float *map = maps + (((size_t)seq * (segments - 2) + s - 2) * d.heads + head) * n * n;
+        for (int i = threadIdx.x; i < kJoinRows * 128; i += 256) {
+            const int r = i >> 7, c = i & 127;
+            e[r][c] = r0 + r < d.p && c < n ? from[(size_t)r * n + c] : 0.f;
+        }
+        __syncthreads();
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = col < n && r0 + 8 * half + i < d.p ? to[(size_t)(8 * half + i) * n + col] : 0.f;
+        if (col < n) {
+#pragma unroll 8
+            for (int k = 0; k < n; ++k) {
+                const float m = map[(size_t)k * n + col];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] += e[8 * half + i][k] * m;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (r0 + 8 * half + i < d.p) to[(size_t)(8 * half + i) * n + col] = v[i];
+        }
+        __syncthreads();        // (this CTA alone reads these rows again)
+    }
+}
+
+// In how many parts a sequence is walked.  One walk a head leaves most SMs idle where there
+// are few heads and sequences, and a part's end depends on its beginning by a map of N x N:
+// the parts' own ends and their maps, side by side, then all parts again, which pays from
+// three parts on.  Parts of 16 chunks at least, all at the same time on an SM each; a first
+// part, which has no map, of half the others' length lets two of them have an SM after each
+// other.  65536 tokens through 32 heads of 128 x 128: 2200 us in one walk, 1580 in three parts, 1390 in
+// four with the first of half the length.
+struct InParts { int parts, half; };
+InParts segments_of(const SsdDelta &d, int sms) {
+    const long long walks = (long long)d.nseq * d.heads, blocks = (d.p + 127) / 128;
+    const long long chunks = d.tokens / kC / d.nseq;
+    InParts best{1, 0};
+    for (int s = 3; s <= 16 && s * 16 <= chunks && walks * blocks * s <= sms; ++s) {
+        const long long others = walks * (blocks + 1) * (s - 2), firsts = walks * blocks;
+        if (others + firsts <= sms) best = {s, 0};
+        else if (others + (firsts + 1) / 2 <= sms) best = {s, 1};
+    }
+    return best;
+}
+size_t records_bytes(const SsdDelta &d) {
+    return ((size_t)ssd_delta_slots(d.tokens, d.nseq) * d.heads * kRecord + 255) / 256 * 256;
+}
+struct Parts {
+    float *starts, *maps;
+    int *cu;
+    size_t bytes;
+};
+Parts parts_of(const SsdDelta &d, int segments, uint8_t *at) {
+    Parts p{};
+    if (segments <= 1) return p;
+    const size_t starts = (size_t)segments * d.nseq * d.heads * d.p * d.n * 4;
+    const size_t maps = (size_t)(segments - 2) * d.nseq * d.heads * d.n * d.n * 4;
+    p.bytes = starts + maps + (size_t)(segments * d.nseq + 1) * 4;
+    p.starts = reinterpret_cast<float *>(at);
+    p.maps = reinterpret_cast<float *>(at + starts);
+    p.cu = reinterpret_cast<int *>(at + starts + maps);
+    return p;
 }
 
 template <int kPanels>
@@ -860,13 +999,32 @@ cudaError_t launch_fwd(const SsdDeltaFwd &f, void *ws, int sms, unsigned *err, c
     if (e != cudaSuccess) return e;
     using Lay = WalkSmem<kPanels>;
     static_assert(Lay::kBytes <= 232448, "more than 227 KB of shared memory");
-    e = cudaFuncSetAttribute(delta_walk_tc_kernel<kPanels>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kBytes);
+    e = cudaFuncSetAttribute(delta_walk_tc_kernel<kPanels, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kBytes);
     if (e != cudaSuccess) return e;
     const int blocks = (d.p + 127) / 128;
-    const WalkTc w{d, records, f.init, static_cast<__nv_bfloat16 *>(f.o), f.o_stride, f.final_state, f.checkpoints, blocks,
-                   ((uintptr_t)f.o & 15u) == 0 && f.o_stride % 8 == 0, err, debug.wait_ns, debug.fault == kSsdFaultWithholdSignal};
-    delta_walk_tc_kernel<kPanels><<<(unsigned)((long long)d.nseq * d.heads * blocks), kWalkThreads, Lay::kBytes, stream>>>(
-        q, k, v, w);
+    const InParts segments = segments_of(d, sms);
+    WalkTc w{d, records, f.init, static_cast<__nv_bfloat16 *>(f.o), f.o_stride, f.final_state, f.checkpoints, blocks,
+             on_16(f.o) && f.o_stride % 8 == 0, segments.parts, segments.half, nullptr, nullptr, err, debug.wait_ns,
+             debug.fault == kSsdFaultWithholdSignal};
+    if (w.segments > 1) {
+        const Parts parts = parts_of(d, w.segments, records + records_bytes(d));
+        w.starts = parts.starts;
+        w.maps = parts.maps;
+        e = cudaFuncSetAttribute(delta_walk_tc_kernel<kPanels, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kBytes);
+        if (e != cudaSuccess) return e;
+        const long long walks = (long long)d.nseq * d.heads;
+        const long long jobs = walks * blocks * (w.segments - 1) + walks * (w.segments - 2);
+        delta_walk_tc_kernel<kPanels, true><<<(unsigned)jobs, kWalkThreads, Lay::kBytes, stream>>>(q, k, v, w);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        const dim3 grid((unsigned)walks, (unsigned)((d.p + kJoinRows - 1) / kJoinRows));
+        delta_join_kernel<<<grid, 256, 0, stream>>>(d, f.init, w.segments, w.half, parts.cu, w.starts, w.maps);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        w.d.cu = parts.cu;
+        w.d.nseq *= w.segments;
+        w.init = w.starts;
+    }
+    const long long ctas = (long long)w.d.nseq * d.heads * blocks;
+    delta_walk_tc_kernel<kPanels, false><<<(unsigned)ctas, kWalkThreads, Lay::kBytes, stream>>>(q, k, v, w);
     return cudaGetLastError();
 }
 
@@ -907,8 +1065,9 @@ bool ssd_delta_tc_handles(const SsdDeltaFwd &a) {
     return ssd_delta_tc_inputs(a.in) && on_16(a.init) && on_16(a.final_state) && on_16(a.checkpoints);
 }
 
-size_t ssd_delta_tc_workspace(const SsdDelta &d) {
-    return ssd_delta_tc_sizes(d) ? (size_t)ssd_delta_slots(d.tokens, d.nseq) * d.heads * kRecord : 0;
+size_t ssd_delta_tc_workspace(const SsdDelta &d, int sms) {
+    if (!ssd_delta_tc_sizes(d)) return 0;
+    return records_bytes(d) + parts_of(d, segments_of(d, sms).parts, nullptr).bytes;
 }
 
 cudaError_t ssd_launch_delta_fwd_tc(const SsdDeltaFwd &a, void *ws, int sms, unsigned *err, cudaStream_t stream) {

@@ -394,7 +394,7 @@ int ssd_act_bwd_rows(long long rows, int width, int sms);
 bool ssd_delta_tc_sizes(const SsdDelta &d);
 bool ssd_delta_tc_inputs(const SsdDelta &d);
 bool ssd_delta_tc_handles(const SsdDeltaFwd &a);
-size_t ssd_delta_tc_workspace(const SsdDelta &d);
+size_t ssd_delta_tc_workspace(const SsdDelta &d, int sms);
 cudaError_t ssd_launch_delta_fwd_tc(const SsdDeltaFwd &a, void *ws, int sms, unsigned *err,
                                     cudaStream_t stream);
 // Its gradients (delta_tc_bwd.cu); ws: ssd_delta_tc_bwd_workspace bytes.

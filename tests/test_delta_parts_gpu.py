@@ -1,0 +1,71 @@
+"""Long sequences of few heads through the gated delta rule: they are walked in parts side by
+side, and the states between the parts are joined by what a part makes of a unit matrix.
+Against tests/model_ref.py, with memories that reach over the parts (little decay, small beta).
+Bars as in test_delta_gpu.py: the state is held in fp32, and what a chunk adds to it, or a
+joining product, is off by at most 3e-5 of what it adds.
+"""
+import pytest
+import torch
+
+import state_space_model_chunked_gb300 as ssd
+from tests import model_ref as ref
+from tests.gpu_util import host, rel
+from tests.test_delta_gpu import BAR, STATE, inputs
+
+pytestmark = pytest.mark.gpu
+
+
+def sequences(lengths):
+    cu = [0]
+    for n in lengths:
+        cu.append(cu[-1] + n)
+    return cu
+
+
+def remembered(*args):
+    x, init, do, dfinal = inputs(*args, forget=0.001)
+    x["beta"] *= 0.1
+    return x, init, do, dfinal
+
+
+PARTS = [  # lengths, groups, heads, headdim, dstate
+    ([3100], 1, 1, 128, 128), ([5000], 1, 2, 64, 64), ([16 * 1024 + 5], 1, 1, 24, 72), ([3200], 1, 2, 136, 128),
+    ([0, 4100, 64, 12300, 1], 1, 2, 72, 40), ([3136, 3136], 2, 2, 64, 104), ([4200], 16, 32, 8, 16)]
+
+
+@pytest.mark.parametrize("lengths,groups,heads,p,n", PARTS)
+@pytest.mark.parametrize("start", [False, True])
+def test_forward_in_parts(lengths, groups, heads, p, n, start):
+    cu = sequences(lengths)
+    x, init, _, _ = remembered(sum(lengths) + p, cu[-1], len(lengths), groups, heads, p, n, "bf16")
+    run = lambda: ssd.delta_scan_fwd(*x.values(), init if start else None, cu_seqlens=cu,     # noqa: E731
+                                     return_checkpoints=True)
+    o, final, kept = run()
+    want, last, before = ref.delta_fwd(*map(host, x.values()), host(init) * start, cu, n ** -0.5)
+    assert rel(host(o), want) <= BAR["bf16"]
+    assert rel(host(final), last) <= STATE["bf16"]
+    for place, state in ref.delta_kept(before, cu):
+        assert rel(host(kept[place]), state) <= STATE["bf16"]
+    again = run()
+    assert all(torch.equal(a, b) for a, b in zip((o, final), again[:2]))
+
+
+def test_growth_and_resets_in_parts():
+    """Parts that reset the state altogether, and parts in which it grows."""
+    x, init, _, _ = remembered(5, 4096, 1, 1, 2, 128, 128, "bf16")
+    x["g"][1500, 0] = float("-inf")
+    x["g"][2900:3000] = 0.01
+    o, final = ssd.delta_scan_fwd(*(t[None] for t in x.values()), init)
+    want, last, _ = ref.delta_fwd(*map(host, x.values()), host(init), [0, 4096], 128 ** -0.5)
+    assert rel(host(o[0]), want) <= BAR["bf16"]
+    assert rel(host(final), last) <= STATE["bf16"]
+
+
+def test_gradients_of_a_long_sequence():
+    x, init, do, dfinal = remembered(6, 3200, 1, 1, 2, 64, 64, "bf16")
+    b = [t[None] for t in x.values()]
+    _, _, kept = ssd.delta_scan_fwd(*b, init, return_checkpoints=True)
+    got = ssd.delta_scan_bwd(do[None], *b, kept, dfinal)
+    want = ref.delta_bwd(host(do), *map(host, x.values()), host(init), host(dfinal), [0, 3200], 64 ** -0.5)
+    for a, w in zip(got, want):
+        assert rel(host(a).reshape(w.shape), w) <= (BAR["bf16"] if a.dtype == torch.bfloat16 else STATE["bf16"])
