@@ -775,15 +775,17 @@ delta_walk_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
             clean_rows(stage(c) + Lay::kK, kPanel, kPanels, len - c * kC, threadIdx.x, 32 * kChainWarps);
             fence_proxy_async_smem();
         };
-        bool on = wait.warp(bar(kFull), 0);
+        float v[kMine];
+        if (const float *init = source()) {
+            load_rows<kMine>(reinterpret_cast<float *>(smem + Lay::kRows + warp * kStageRows), v,
+                             init + (size_t)(p0 + 32 * q) * d.n + n0, d.n, rows - (p0 + 32 * q), d.n - n0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) v[i] = map && n0 + i == p ? 1.f : 0.f;
+        }
+        const bool on = wait.warp(bar(kFull), 0);
         if (on) {
             clean(0);
-            const float *init = source();
-            float v[kMine];
-#pragma unroll
-            for (int i = 0; i < kMine; ++i)
-                v[i] = init ? (p < rows && n0 + i < d.n ? init[(size_t)p * d.n + n0 + i] : 0.f)
-                            : map && n0 + i == p ? 1.f : 0.f;
             put(0, v, reinterpret_cast<const float *>(stage(0) + Lay::kRec + kRecGates)[kC - 1]);
         }
         for (int c = 0; on && c < chunks; ++c) {

@@ -168,6 +168,36 @@ __device__ __forceinline__ void store_rows(float *stage, const float (&v)[kMine]
         }
     }
 }
+// And from there.
+template <int kMine>
+__device__ __forceinline__ void load_rows(float *stage, float (&v)[kMine], const float *from, int n, int rows, int cols) {
+    const int lane = threadIdx.x & 31;
+    float4 x[kMine / 4];
+#pragma unroll
+    for (int i = 0; i < kMine / 4; ++i) {
+        const int r = 8 * (i & 3) + (lane >> 2), c = (lane & 3) * 4 + 16 * (i >> 2);
+        x[i] = r < rows && c < cols ? *reinterpret_cast<const float4 *>(from + (size_t)r * n + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int h = 0; h < kMine / 16; ++h) {
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = 8 * j + (lane >> 2);
+            *reinterpret_cast<float4 *>(stage + r * 16 + ((lane ^ (r >> 1)) & 3) * 4) = x[4 * h + j];
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 y = *reinterpret_cast<const float4 *>(stage + lane * 16 + ((i ^ (lane >> 1)) & 3) * 4);
+            v[16 * h + 4 * i] = y.x;
+            v[16 * h + 4 * i + 1] = y.y;
+            v[16 * h + 4 * i + 2] = y.z;
+            v[16 * h + 4 * i + 3] = y.w;
+        }
+    }
+    __syncwarp();
+}
 constexpr uint32_t kStageRows = 2048;       // bytes a warp
 
 inline bool on_16(const void *p) { return ((uintptr_t)p & 15u) == 0; }

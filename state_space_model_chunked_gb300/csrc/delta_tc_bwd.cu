@@ -404,17 +404,21 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         };
         const auto stage = [&](int it) { return smem + (it & 1) * Lay::kStage; };
         const auto decay_of = [&](int it) { return reinterpret_cast<const float *>(stage(it) + Lay::kRec + kRecGates)[kC - 1]; };
-        bool on = wait.warp(bar(kFull), 0);
+        float v[kMine];
+        if (a.dfinal) {
+            load_rows<kMine>(reinterpret_cast<float *>(smem + Lay::kRows + warp * kStageRows), v,
+                             a.dfinal + state + (size_t)(32 * q) * d.n + n0, d.n, d.p - 32 * q, d.n - n0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) v[i] = 0.f;
+        }
+        const bool on = wait.warp(bar(kFull), 0);
         if (on) {
             const int tokens = len - (chunks - 1) * kC;
             if (tokens < kC) {
                 clean_rows(smem, kPanel, 2 * kPanels + 2, tokens, threadIdx.x, 32 * kChainWarps);
                 fence_proxy_async_smem();
             }
-            float v[kMine];
-#pragma unroll
-            for (int i = 0; i < kMine; ++i)
-                v[i] = a.dfinal && p < d.p && n0 + i < d.n ? a.dfinal[state + (size_t)p * d.n + n0 + i] : 0.f;
             put(v, decay_of(0));
         }
         for (int it = 0; on && it < chunks; ++it) {
