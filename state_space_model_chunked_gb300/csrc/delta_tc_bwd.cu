@@ -41,16 +41,21 @@ constexpr int kLoadWarp = kChainWarps + kOutWarps, kMmaWarp = kLoadWarp + 1, kBa
 
 constexpr uint32_t kTall = 2 * kPanel;              // a panel of 128 rows
 constexpr uint32_t kImageRows = 32 * 128;           // a warp's rows of one
-static_assert(kOutWarps * kImageRows >= kChainWarps * kStageRows, "one place for both");
+static_assert(kOutWarps * kImageRows >= kChainWarps * kStageRows && 4 * kPanel >= kChainWarps * kStageRows, "one place for both");
 // A chunk's dS, for every head: its two parts, each [128 of P][N] by tall panels.
 constexpr uint32_t state_image(int panels) { return 2 * panels * kTall; }
+// And its Z in fp32, by tiles of 32 tokens x 32 rows of a state, as the warps have them.
+constexpr size_t kZTile = 64 * 128;
+__device__ __forceinline__ size_t z_at(size_t record, int token, int row) {
+    return record * kZTile + (size_t)((token >> 5) * 4 + (row >> 5)) * 1024 + (token & 31) * 32 + (row & 31);
+}
 
 template <int kPanels>
 struct BackSmem {
     static constexpr uint32_t kK = 0, kQ = kPanels * kPanel, kDo = 2 * kPanels * kPanel, kRec = kDo + 2 * kPanel;
     static constexpr uint32_t kStage = (kRec + kRecord + 1023) / 1024 * 1024;
     static constexpr uint32_t kOut = 2 * kStage;        // [token][128]: dV on its way
-    static constexpr uint32_t kRows = kOut + 64 * 256;  // dS on its way, by warps: its images, at last dinit
+    static constexpr uint32_t kRows = kOut + 64 * 256;  // by warps: dfinal, then images of dS and Z on their way out
     static constexpr uint32_t kCtl = kRows + kOutWarps * kImageRows;
     static constexpr uint32_t kBytes = kCtl + 256;
 };
@@ -305,6 +310,8 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
                     uint32_t r[32];
                     tmem_ld32(tq + (part ? kColSl : kColSh) + 32 * half, r);
                     tmem_ld_wait(r);
+                    if (lane == 0) bulk_wait_read<0>();
+                    __syncwarp();
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         *reinterpret_cast<uint4 *>(rows + lane * 128 + ((i ^ lane) & 7) * 16) =
@@ -314,9 +321,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
                     if (lane == 0) {
                         bulk_store(image + (part * kPanels + half) * kTall + q * kImageRows, smem_u32(rows), kImageRows);
                         bulk_commit();
-                        bulk_wait_read<0>();
                     }
-                    __syncwarp();
                 }
             }
             tc_fence_before();
@@ -330,11 +335,18 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kZRead));
-            if (row < d.p) {
-                float *to = a.z + ((size_t)(first + (long long)c * kC + 32 * half) * d.heads + head) * d.p + row;
+            if (32 * q < d.p) {
+                // (the image's last part has left this place)
+                if (lane == 0) bulk_wait_read<0>();
+                __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (32 * half + i < tokens) to[(size_t)i * d.heads * d.p] = __uint_as_float(z[i]);
+                for (int i = 0; i < 32; ++i) reinterpret_cast<uint32_t *>(rows)[32 * i + lane] = z[i];
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    bulk_store(a.z + z_at((size_t)(slot0 + c) * d.heads + head, 32 * half, 32 * q), smem_u32(rows), kImageRows);
+                    bulk_commit();
+                }
             }
 #pragma unroll
             for (int i = 0; i < 32; ++i) out[(32 * half + i) * 128 + row] = __float2bfloat16_rn(__uint_as_float(z[i]));
@@ -366,10 +378,6 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16);
         constexpr int kMine = kN / 4;
         const int n0 = part * kMine;
-        const auto to_memory = [&](float *m, const float (&v)[kMine]) {
-            store_rows<kMine>(reinterpret_cast<float *>(smem + Lay::kRows + warp * kStageRows), v,
-                              m + (size_t)(32 * q) * d.n + n0, d.n, d.p - 32 * q, d.n - n0);
-        };
         const auto ready = [&](int which) {
             tmem_st_wait();
             tc_fence_before();
@@ -499,7 +507,9 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
 #pragma unroll
             for (int i = 0; i < kMine; ++i) v[i] = __uint_as_float(m[i]);
             if (more) put(v, decay);
-            else if (a.dinit) to_memory(a.dinit + state, v);
+            else if (a.dinit)       // (by way of the last chunk's keys, queries and dO, which are used up)
+                store_rows<kMine>(reinterpret_cast<float *>(stage(it) + warp * kStageRows), v,
+                                  a.dinit + state + (size_t)(32 * q) * d.n + n0, d.n, d.p - 32 * q, d.n - n0);
         }
     }
     // copies in flight land before the CTA ends
@@ -630,7 +640,7 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
             const int t = 4 * warp + i, p = 4 * lane;
             z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (t < valid && p < d.p)       // (P is a multiple of 8)
-                z[i] = *reinterpret_cast<const float4 *>(a.z + ((size_t)(token + t) * d.heads + head) * d.p + p);
+                z[i] = *reinterpret_cast<const float4 *>(a.z + z_at(record, t, p));
         }
         if (warp == 1) {
             tmem_alloc(smem_u32(tslot), 512);
@@ -749,7 +759,7 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
     float zu[16], own;
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-        zu[i] = c0 + i < valid && row < d.p ? a.z[((size_t)(token + c0 + i) * d.heads + head) * d.p + row] : 0.f;
+        zu[i] = c0 + i < valid && row < d.p ? a.z[z_at(record, c0 + i, row)] : 0.f;
     after();
     // R, as the left operand of U, and beta R, to which that product is added
     {
@@ -1020,7 +1030,7 @@ Plan plan_of(const SsdDelta &d) {
     Plan p;
     p.records = 0;
     p.z = up(slots * d.heads * kRecord);
-    p.dstate = p.z + up(tokens * d.heads * d.p * 4);
+    p.dstate = p.z + up(slots * d.heads * kZTile * 4);
     p.dq = p.dstate + up(slots * d.heads * state_image(d.n <= 64 ? 1 : 2));
     p.dk = p.dq + (d.heads == d.groups ? 0 : up(tokens * d.heads * d.n * 4));
     p.total = p.dk + (d.heads == d.groups ? 0 : up(tokens * d.heads * d.n * 4));
