@@ -550,6 +550,7 @@ struct GradTc {
     __nv_bfloat16 *dq, *dk;             // where a group is one head; else sums by head:
     float *dq_heads, *dk_heads;         // [token][head][N]
     long long dq_stride, dk_stride;
+    bool vectors;                       // whether their rows start on 16 bytes
     float *dg, *dbeta;
     int ahead;                          // how many CTAs on the next on an SM is
     unsigned *err;
@@ -656,6 +657,7 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
                 bulk_prefetch_l2(a.checkpoints + (size_t)next * size, (uint32_t)(size * 4));
                 bulk_prefetch_l2(a.dstate + (size_t)next * state_image(kPanels), state_image(kPanels));
                 bulk_prefetch_l2(a.records + (size_t)next * kRecord, kRecord);
+                bulk_prefetch_l2(a.z + (size_t)next * kZTile, kZTile * 4);
 #pragma unroll
                 for (int p = 0; p < kPanels; ++p) {
                     tma_prefetch_l2_3d(&mapQ, 64 * p, group2, t);
@@ -744,6 +746,12 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
             mma_ss(tmem + dcol, ad + kStepMn * k, bd + kStepMn * k, idesc_bf16_f32(128, 16 * k + 16, true, true), add || k < 3);
     };
     const float *gates = reinterpret_cast<const float *>(smem + Lay::kGatesAt);
+    // the gates of the warp's 16 tokens
+    const auto gates_of = [&](int which, float (&f)[16]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float4 *>(f + 4 * i) = *reinterpret_cast<const float4 *>(gates + which + c0 + 4 * i);
+    };
     float *const scratch = reinterpret_cast<float *>(smem + Lay::kSs);
 
     // K S^T by the state's rows; Q K^T over K K^T
@@ -767,15 +775,18 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         tmem_ld16(tq + kColU + c0, r);
         tmem_ld_wait(r);
         const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(smem + Lay::kW) + c0 * 128 + row;
+        float gamma[16], beta[16];
+        gates_of(0, gamma);
+        gates_of(kGateBeta, beta);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             float x[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int t = 2 * i + j;
-                x[j] = __bfloat162float(v[t * 128]) - gates[c0 + t] * __uint_as_float(r[t]);
+                x[j] = __bfloat162float(v[t * 128]) - gamma[t] * __uint_as_float(r[t]);
                 if (c0 + t >= valid) x[j] = 0.f;
-                r[t] = __float_as_uint(x[j] * gates[kGateBeta + c0 + t]);
+                r[t] = __float_as_uint(x[j] * beta[t]);
             }
             const Split y = split2(x[0], x[1]);
             hi[i] = y.hi;
@@ -920,66 +931,92 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
     float dots[32], dq[16], dk[16];
     {
         uint32_t x[16], y[16];
+        float gamma[16];
+        gates_of(0, gamma);
         tmem_ld16(tq + kColDoS + c0, x);
         tmem_ld16(tq + kColZs + c0, y);
         tmem_ld_wait(x);
         tmem_ld_wait(y);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            dq[i] = d.scale * gates[c0 + i] * __uint_as_float(x[i]);
-            dk[i] = -gates[c0 + i] * __uint_as_float(y[i]);
+            dq[i] = d.scale * gamma[i] * __uint_as_float(x[i]);
+            dk[i] = -gamma[i] * __uint_as_float(y[i]);
             dots[i] = dots[16 + i] = 0.f;
             if (on) {
                 const uint32_t o = panel_at(c0 + i, row & 63);
                 const float qv = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(keys + o));
                 const float kv = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(keys + kPanel + o));
                 dots[i] = dq[i] * qv + dk[i] * kv;
-                dots[16 + i] = gates[kGateW + c0 + i] * kv;
+                dots[16 + i] = kv;
             }
         }
     }
     after();
     {
         uint32_t x[16], y[16];
+        float w[16];
+        gates_of(kGateW, w);
         tmem_ld16(tq + kColUs + c0, x);
         tmem_ld16(tq + kColPk + c0, y);
         tmem_ld_wait(x);
         tmem_ld_wait(y);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            dk[i] += gates[kGateW + c0 + i] * __uint_as_float(x[i]);
-            dots[16 + i] = on ? dots[16 + i] * __uint_as_float(x[i]) : 0.f;
+            const float u = w[i] * __uint_as_float(x[i]);
+            dk[i] += u;
+            dots[16 + i] = on ? dots[16 + i] * u : 0.f;
             dq[i] += __uint_as_float(y[i]);
         }
         tmem_ld16(tq + kColSum + c0, x);
         tmem_ld_wait(x);
 #pragma unroll
         for (int i = 0; i < 16; ++i) dk[i] += __uint_as_float(x[i]);
-        if (on) {
-            if (a.dq == nullptr) {
-                const size_t o = ((size_t)(token + c0) * d.heads + head) * d.n + row;
+        // by way of shared memory, in the places of dS's parts, which are used up
+        if (on && a.dq == nullptr) {
+            float *const to = reinterpret_cast<float *>(smem + Lay::kAh) + c0 * 128 + row;
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (c0 + i < valid) {
-                        a.dq_heads[o + (size_t)i * d.heads * d.n] = dq[i];
-                        a.dk_heads[o + (size_t)i * d.heads * d.n] = dk[i];
-                    }
-            } else {
-                __nv_bfloat16 *const to_q = a.dq + (size_t)(token + c0) * a.dq_stride + group * d.n + row;
-                __nv_bfloat16 *const to_k = a.dk + (size_t)(token + c0) * a.dk_stride + group * d.n + row;
+            for (int i = 0; i < 16; ++i) {
+                to[i * 128] = dq[i];
+                to[i * 128 + kTall / 2] = dk[i];
+            }
+        } else if (on) {
+            __nv_bfloat16 *const to = reinterpret_cast<__nv_bfloat16 *>(smem + Lay::kAh) + c0 * 128 + row;
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (c0 + i < valid) {
-                        to_q[(size_t)i * a.dq_stride] = __float2bfloat16_rn(dq[i]);
-                        to_k[(size_t)i * a.dk_stride] = __float2bfloat16_rn(dk[i]);
-                    }
+            for (int i = 0; i < 16; ++i) {
+                to[i * 128] = __float2bfloat16_rn(dq[i]);
+                to[i * 128 + kTall / 2] = __float2bfloat16_rn(dk[i]);
             }
         }
         const float sum = lanes_transposed_sum(dots, lane);
         scratch[(lane < 16 ? Lay::kAhead : Lay::kBehind) + 64 * q + c0 + (lane & 15)] = sum;
     }
+    fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
+    if (warp >= kGradWarps - 4) {
+        // the rows of dQ, then of dK
+        const auto rows = [&](int i, auto store) {
+            const int t = i & 63;
+            if (t >= valid) return;
+            if (a.dq == nullptr)
+                store((i < 64 ? a.dq_heads : a.dk_heads) + ((size_t)(token + t) * d.heads + head) * d.n,
+                      Lay::kAh + (uint32_t)i * 512, d.n * 4);
+            else
+                store((i < 64 ? a.dq + (size_t)(token + t) * a.dq_stride : a.dk + (size_t)(token + t) * a.dk_stride) + group * d.n,
+                      Lay::kAh + (uint32_t)i * 256, d.n * 2);
+        };
+        if (a.vectors) {
+            rows(threadIdx.x & 127, [&](void *to, uint32_t from, uint32_t bytes) { bulk_store(to, base + from, bytes); });
+            bulk_commit();
+            bulk_wait_read<0>();
+        } else {
+            for (int i = warp & 3; i < 128; i += 4)
+                rows(i, [&](void *to, uint32_t from, uint32_t bytes) {
+                    for (uint32_t j = lane; j < bytes / 2; j += 32)
+                        static_cast<uint16_t *>(to)[j] = reinterpret_cast<const uint16_t *>(smem + from)[j];
+                });
+        }
+    }
     if (warp == 0) {
         // lane l: tokens 2 l and 2 l + 1
         float whole = lane < kGradWarps ? scratch[Lay::kWhole + lane] : 0.f;
@@ -1069,7 +1106,8 @@ cudaError_t launch(const SsdDeltaBwd &b, void *ws, int sms, unsigned *err, cudaS
     const bool one = d.heads == d.groups;
     const GradTc g{d, records, b.checkpoints, z, dstate, one ? static_cast<__nv_bfloat16 *>(b.dq) : nullptr,
                    one ? static_cast<__nv_bfloat16 *>(b.dk) : nullptr, reinterpret_cast<float *>(at(plan.dq)),
-                   reinterpret_cast<float *>(at(plan.dk)), b.dq_stride, b.dk_stride, b.dg, b.dbeta, sms, err};
+                   reinterpret_cast<float *>(at(plan.dk)), b.dq_stride, b.dk_stride,
+                   !one || (on_16(b.dq) && on_16(b.dk) && b.dq_stride % 8 == 0 && b.dk_stride % 8 == 0), b.dg, b.dbeta, sms, err};
     const long long ctas = ssd_delta_slots(d.tokens, d.nseq) * d.heads;
     delta_grad_tc_kernel<kPanels><<<(unsigned)ctas, kGradThreads, Grad::kBytes, stream>>>(q, k, v, o, g);
     if ((e = cudaGetLastError()) != cudaSuccess || one) return e;
