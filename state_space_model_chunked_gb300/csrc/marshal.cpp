@@ -284,8 +284,8 @@ PyObject *linear_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// The sequences of a recurrence over x: [batch, length, width], or [tokens, width]
-// with offsets as a list of ints and their device copy.
+// The sequences of a recurrence over tokens [batch, length], or [tokens] with offsets as a
+// list of ints and their device copy.
 struct Sequences {
     int nseq = 0, length = 0;
     int64_t tokens = 0;
@@ -293,17 +293,17 @@ struct Sequences {
     const int *device = nullptr;
     const int *offsets() const { return host.empty() ? nullptr : host.data(); }
 };
-bool sequences(const at::Tensor &x, PyObject *cu, PyObject *cu_dev, Sequences &s) {
-    s.tokens = x.numel() / x.size(-1);
+bool sequences(at::IntArrayRef lead, int device, PyObject *cu, PyObject *cu_dev, Sequences &s) {
+    s.tokens = c10::multiply_integers(lead);
     if (s.tokens > INT_MAX) return false;
     if (cu == Py_None) {
-        if (x.dim() != 3) return false;
-        s.nseq = (int)x.size(0);
-        s.length = (int)x.size(1);
+        if (lead.size() != 2) return false;
+        s.nseq = (int)lead[0];
+        s.length = (int)lead[1];
         return true;
     }
-    bool ok = x.dim() == 2 && PyList_Check(cu) && PyList_GET_SIZE(cu) >= 2;
-    const at::Tensor *d = ok ? tensor(cu_dev, x.get_device(), ok) : nullptr;
+    bool ok = lead.size() == 1 && PyList_Check(cu) && PyList_GET_SIZE(cu) >= 2;
+    const at::Tensor *d = ok ? tensor(cu_dev, device, ok) : nullptr;
     if (!ok || !d || d->scalar_type() != at::kInt || d->dim() != 1 ||
         d->size(0) != PyList_GET_SIZE(cu))
         return false;
@@ -334,7 +334,7 @@ PyObject *gated_scan_fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (keep < 0) return nullptr;       // no truth value: the exception is set
     Sequences q;
     if (!ok || !g.t || !like(g, *x.t) || !like(z, *x.t) || c < 0 ||
-        !sequences(*x.t, args[4], args[5], q))
+        !sequences(x.t->sizes().slice(0, x.t->dim() - 1), dev, args[4], args[5], q))
         Py_RETURN_NONE;
     const int64_t width = x.t->size(-1);
     const std::array<int64_t, 2> states{q.nseq, width};
@@ -368,7 +368,7 @@ PyObject *gated_scan_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const int c = code(x.t->scalar_type());
     Sequences q;
     if (!ok || !dy.t || !g.t || !kept || !like(dy, *x.t) || !like(g, *x.t) || !like(z, *x.t) ||
-        c < 0 || !sequences(*x.t, args[7], args[8], q))
+        c < 0 || !sequences(x.t->sizes().slice(0, x.t->dim() - 1), dev, args[7], args[8], q))
         Py_RETURN_NONE;
     const int64_t width = x.t->size(-1);
     const std::array<int64_t, 2> states{q.nseq, width}, keeps{(q.tokens + 63) / 64, width};
@@ -526,7 +526,7 @@ PyObject *embedding_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
 }
 
 // An array of a token's values a row: [..., a, b] with the last two dimensions contiguous
-// and the rows at one stride.
+// and the rows at one stride (never None).
 Matrix by_token(PyObject *o, int device, bool &ok) {
     Matrix m;
     if (!THPVariable_Check(o)) {
@@ -534,15 +534,129 @@ Matrix by_token(PyObject *o, int device, bool &ok) {
         return m;
     }
     const at::Tensor &t = THPVariable_Unpack(o);
-    if (!t.is_cuda() || t.dim() != 3 || t.numel() == 0 || t.size(0) > INT_MAX || t.size(1) > INT_MAX ||
-        t.size(2) > INT_MAX || (device >= 0 && t.get_device() != device) ||
-        (t.size(2) > 1 && t.stride(2) != 1) || (t.size(1) > 1 && t.stride(1) != t.size(2))) {
+    if (!t.is_cuda() || t.dim() < 3 || t.numel() == 0 || t.size(0) > INT_MAX || t.size(-2) > INT_MAX ||
+        t.size(-1) > INT_MAX || (device >= 0 && t.get_device() != device) ||
+        (t.size(-1) > 1 && t.stride(-1) != 1) || (t.size(-2) > 1 && t.stride(-2) != t.size(-1))) {
         ok = false;
         return m;
     }
+    int64_t row = -1, step = 0;
+    for (int64_t d = t.dim() - 3; d >= 0; --d) {
+        if (t.size(d) == 1) continue;
+        if (row < 0) row = t.stride(d);
+        else if (t.stride(d) != step) ok = false;
+        step = t.stride(d) * t.size(d);
+    }
     m.t = &t;
-    m.stride = t.size(0) == 1 ? t.size(1) * t.size(2) : t.stride(0);
+    m.stride = row < 0 ? t.size(-2) * t.size(-1) : row;
     return m;
+}
+
+// What the passes over sequences of the delta rule have in common: q, k, v, g, beta, init or
+// final state's gradient, scale or None, offsets, device offsets.
+struct DeltaInputs {
+    Matrix q, k, v;
+    const at::Tensor *g = nullptr, *beta = nullptr, *state = nullptr;
+    Sequences s;
+    int dev = 0, code = -1, heads = 0, p = 0, n = 0, groups = 0;
+    float scale = 0;
+    std::array<int64_t, 4> states{}, kept{};
+};
+// Whether they are such; false with an exception set where Python raised one.
+bool delta_inputs(PyObject *const *args, PyObject *scale, PyObject *cu, PyObject *cu_dev, DeltaInputs &d) {
+    bool ok = true;
+    d.q = by_token(args[0], -1, ok);
+    if (!ok || d.q.t->get_device() != c10::cuda::current_device()) return false;
+    const at::Tensor &q = *d.q.t;
+    d.dev = q.get_device();
+    d.k = by_token(args[1], d.dev, ok);
+    d.v = by_token(args[2], d.dev, ok);
+    d.g = tensor(args[3], d.dev, ok);
+    d.beta = tensor(args[4], d.dev, ok);
+    d.state = tensor(args[5], d.dev, ok);
+    if (!ok || !d.g || !d.beta) return false;
+    const at::Tensor &v = *d.v.t;
+    const auto lead = q.sizes().slice(0, q.dim() - 2);
+    const auto gate = [&](const at::Tensor *t) {
+        return t->scalar_type() == at::kFloat && t->sizes() == v.sizes().slice(0, v.dim() - 1);
+    };
+    if (!like(d.k, q) || v.scalar_type() != q.scalar_type() || v.sizes().slice(0, v.dim() - 2) != lead ||
+        !gate(d.g) || !gate(d.beta) || !sequences(lead, d.dev, cu, cu_dev, d.s))
+        return false;
+    d.code = code(q.scalar_type());
+    d.groups = (int)q.size(-2);
+    d.n = (int)q.size(-1);
+    d.heads = (int)v.size(-2);
+    d.p = (int)v.size(-1);
+    d.scale = (float)(scale == Py_None ? std::pow((double)d.n, -0.5) : PyFloat_AsDouble(scale));
+    if (PyErr_Occurred()) return false;
+    d.states = {d.s.nseq, d.heads, d.p, d.n};
+    d.kept = {d.s.tokens / 64 + d.s.nseq, d.heads, d.p, d.n};
+    return d.code >= 0 && (!d.state || (d.state->scalar_type() == at::kFloat && d.state->sizes() == at::IntArrayRef(d.states)));
+}
+
+// q, k, v, g, beta, init_state, scale or None, offsets, device offsets, whether the final
+// state and the checkpoints are wanted -> (o, final_state or None, checkpoints or None, None)
+PyObject *delta_scan_fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    DeltaInputs d;
+    if (n != 11 || !delta_inputs(args, args[6], args[7], args[8], d)) {
+        if (PyErr_Occurred()) return nullptr;
+        Py_RETURN_NONE;
+    }
+    const int last = PyObject_IsTrue(args[9]), keep = last < 0 ? -1 : PyObject_IsTrue(args[10]);
+    if (keep < 0) return nullptr;       // no truth value: the exception is set
+    const size_t need = ssd_delta_scan_workspace_bytes((ssd_dtype)d.code, d.s.tokens, d.s.nseq, d.heads, d.p, d.n, d.groups);
+    if (need == (size_t)-1) Py_RETURN_NONE;
+    const at::Tensor &q = *d.q.t;
+    at::Tensor o = make(d.v.t->sizes(), q.scalar_type(), q), final_state, kept, ws = scratch(need, q);
+    if (last) final_state = make(d.states, at::kFloat, q);
+    if (keep) kept = make(d.kept, at::kFloat, q);
+    const ssd_status st = ssd_delta_scan_fwd(
+        ptr(d.q.t), ptr(d.k.t), ptr(d.v.t), fptr(d.g), fptr(d.beta), (ssd_dtype)d.code, d.s.nseq, d.s.length,
+        d.s.offsets(), d.s.device, d.heads, d.p, d.n, d.groups, d.q.stride, d.k.stride, d.v.stride, d.scale,
+        fptr(d.state), out(o), (int64_t)d.heads * d.p, out<float>(final_state), out<float>(kept), out(ws), need,
+        c10::cuda::getCurrentCUDAStream(d.dev));
+    return answer(st, tuple4(wrap(o), wrap(final_state), wrap(kept), Py_NewRef(Py_None)));
+    END_HANDLE_TH_ERRORS
+}
+
+// q, k, v, g, beta, dfinal, do, checkpoints, scale or None, offsets, device offsets, whether
+// dinit is wanted -> (dq, dk, dv, dg, dbeta, dinit or None)
+PyObject *delta_scan_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    DeltaInputs d;
+    if (n != 12 || !delta_inputs(args, args[8], args[9], args[10], d)) {
+        if (PyErr_Occurred()) return nullptr;
+        Py_RETURN_NONE;
+    }
+    bool ok = true;
+    const Matrix dout = by_token(args[6], d.dev, ok);
+    const at::Tensor *kept = tensor(args[7], d.dev, ok);
+    const int init = PyObject_IsTrue(args[11]);
+    if (init < 0) return nullptr;       // no truth value: the exception is set
+    const at::Tensor &q = *d.q.t, &v = *d.v.t;
+    if (!ok || !like(dout, v) || !kept || kept->scalar_type() != at::kFloat || kept->sizes() != at::IntArrayRef(d.kept))
+        Py_RETURN_NONE;
+    const size_t need =
+        ssd_delta_scan_bwd_workspace_bytes((ssd_dtype)d.code, d.s.tokens, d.s.nseq, d.heads, d.p, d.n, d.groups);
+    if (need == (size_t)-1) Py_RETURN_NONE;
+    const auto type = q.scalar_type();
+    at::Tensor dq = make(q.sizes(), type, q), dk = make(q.sizes(), type, q), dv = make(v.sizes(), type, q);
+    at::Tensor dg = make(d.g->sizes(), at::kFloat, q), dbeta = make(d.g->sizes(), at::kFloat, q), dinit;
+    if (init) dinit = make(d.states, at::kFloat, q);
+    at::Tensor ws = scratch(need, q);
+    const int64_t keys = (int64_t)d.groups * d.n, values = (int64_t)d.heads * d.p;
+    const ssd_status st = ssd_delta_scan_bwd(
+        ptr(dout.t), ptr(d.q.t), ptr(d.k.t), ptr(d.v.t), fptr(d.g), fptr(d.beta), (ssd_dtype)d.code, d.s.nseq,
+        d.s.length, d.s.offsets(), d.s.device, d.heads, d.p, d.n, d.groups, dout.stride, d.q.stride, d.k.stride,
+        d.v.stride, d.scale, fptr(kept), fptr(d.state), out(dq), keys, out(dk), keys, out(dv), values,
+        out<float>(dg), out<float>(dbeta), out<float>(dinit), out(ws), need, c10::cuda::getCurrentCUDAStream(d.dev));
+    PyObject *t = PyTuple_New(6);
+    int at = 0;
+    for (const at::Tensor *x : {&dq, &dk, &dv, &dg, &dbeta, &dinit}) PyTuple_SET_ITEM(t, at++, wrap(*x));
+    return answer(st, t);
+    END_HANDLE_TH_ERRORS
 }
 
 // state, q, k, v, g, beta, scale or None, state_out or None -> o
@@ -593,6 +707,8 @@ PyMethodDef methods[] = {
     SSD_METHOD(embedding_fwd),
     SSD_METHOD(embedding_bwd),
     SSD_METHOD(delta_state_update),
+    SSD_METHOD(delta_scan_fwd),
+    SSD_METHOD(delta_scan_bwd),
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "ssd_marshal", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

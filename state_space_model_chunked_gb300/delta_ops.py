@@ -87,6 +87,12 @@ def delta_scan_fwd(q, k, v, g, beta, init_state=None, *, scale=None, cu_seqlens=
     Returns (o in v's layout, final_state f32 or None), and with return_checkpoints
     the states [delta_scan_checkpoints(tokens, nseq), heads, headdim, dstate] f32
     that delta_scan_bwd needs."""
+    if o is None and final_state is None and checkpoints is None and workspace is None:
+        got = (_ops._marshal_module or _ops._marshal()).delta_scan_fwd(
+            q, k, v, g, beta, init_state, scale, cu_seqlens, cu_seqlens_dev, return_final,
+            return_checkpoints)
+        if got is not None:
+            return _plain("ssd_delta_scan_fwd", got)[:3 if return_checkpoints else 2]
     lib = load()
     at, code, lead, groups, dstate, heads, headdim = _sizes(q, v)
     dev, dtype = q.device, q.dtype
@@ -128,6 +134,12 @@ def delta_scan_bwd(do, q, k, v, g, beta, checkpoints, dfinal=None, *, scale=None
     f32 of the final state (None: zeros); q, k, v, g, beta, scale and offsets as
     given to it and the checkpoints it returned.  dq, dk and dv may be column ranges
     of one matrix.  Returns (dq, dk, dv, dg, dbeta, dinit f32 or None)."""
+    if (dq is None and dk is None and dv is None and dg is None and dbeta is None and dinit is None
+            and workspace is None):
+        got = (_ops._marshal_module or _ops._marshal()).delta_scan_bwd(
+            q, k, v, g, beta, dfinal, do, checkpoints, scale, cu_seqlens, cu_seqlens_dev, return_dinit)
+        if got is not None:
+            return _plain("ssd_delta_scan_bwd", got)
     lib = load()
     at, code, lead, groups, dstate, heads, headdim = _sizes(q, v)
     dev, dtype = q.device, q.dtype
