@@ -699,7 +699,8 @@ size_t ssd_embedding_bwd_workspace_bytes(long long count, int vocab, int width);
  *   beta         float [tokens][nheads]: how much of the value is written (0 to 1 in use,
  *                with keys of unit length).
  *   init_state, final_state   float [nseq][nheads][headdim][dstate] or NULL (zeros / not
- *                wanted).  An empty sequence's final state is its initial one.
+ *                wanted); they may be the same array.  An empty sequence's final state is its
+ *                initial one.
  *   checkpoints  float [tokens / 64 + nseq][nheads][headdim][dstate] or NULL: what
  *                ssd_delta_scan_bwd needs of the forward call.  The state before a sequence's
  *                tokens 0, 64, 128, ... lies at first / 64 + s + 0, 1, 2, ... (s: the
@@ -708,8 +709,10 @@ size_t ssd_embedding_bwd_workspace_bytes(long long count, int vocab, int width);
  *                when that is 0); no initialisation needed.
  * bf16 inputs with dstate <= 128, dstate and headdim multiples of 8 and tokens that start on
  * 16-byte boundaries run on the tensor cores, in chunks of 64 tokens, with factors that are
- * no bf16 values held to 16 bits (states are about 7e-6 of their size off); others in fp32
- * multiply-adds, token by token.
+ * no bf16 values held to 16 bits (states are about 4e-6 of their size off); others in fp32
+ * multiply-adds, token by token.  On the tensor cores a long sequence of few heads goes in
+ * parts side by side, whose number follows from the sizes and the device's SMs.  Equal calls
+ * give equal bits.
  * Requirements: dstate <= 256, headdim <= 2^14, nheads <= 2^16 a multiple of ngroups.
  * SSD_ERR_INVALID_ARG for null or misaligned pointers, sizes <= 0 (length 0 is allowed),
  * strides below a token's values, bad offsets or a scale that is not finite;

@@ -69,3 +69,41 @@ def test_gradients_of_a_long_sequence():
     want = ref.delta_bwd(host(do), *map(host, x.values()), host(init), host(dfinal), [0, 3200], 64 ** -0.5)
     for a, w in zip(got, want):
         assert rel(host(a).reshape(w.shape), w) <= (BAR["bf16"] if a.dtype == torch.bfloat16 else STATE["bf16"])
+
+
+def test_the_final_state_in_the_initial_one_s_place():
+    for length, heads in ((3200, 1), (200, 2)):
+        x, init, _, _ = remembered(7, length, 1, 1, heads, 128, 64, "bf16")
+        b = [t[None] for t in x.values()]
+        o, final = ssd.delta_scan_fwd(*b, init)
+        state = init.clone()
+        o2, same = ssd.delta_scan_fwd(*b, state, final_state=state)
+        assert same is state and torch.equal(o, o2) and torch.equal(final, state)
+
+
+def test_two_graphs_with_one_workspace():
+    """Captured on another stream and replayed in turns, with new inputs in the old places."""
+    x, init, _, _ = remembered(8, 3300, 1, 1, 2, 64, 128, "bf16")
+    y, init2, _, _ = remembered(9, 3300, 1, 1, 2, 64, 128, "bf16")
+    both = [([t[None].clone() for t in x.values()], init.clone()), ([t[None].clone() for t in y.values()], init2.clone())]
+    want = [ssd.delta_scan_fwd(*b, i) for b, i in both]
+    need = ssd.delta_scan_workspace_bytes(torch.bfloat16, 3300, 1, 2, 64, 128, 1)
+    ws = torch.full((need,), 0xff, dtype=torch.uint8, device="cuda")
+    graphs, got = [], []
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for b, i in both:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            got.append(ssd.delta_scan_fwd(*b, i, workspace=ws))
+        graphs.append(graph)
+    torch.cuda.current_stream().wait_stream(side)
+    for turn in (0, 1, 0, 1):
+        for t in got[turn]:
+            t.fill_(7.0)
+        graphs[turn].replay()
+        assert all(torch.equal(a, w) for a, w in zip(got[turn], want[turn]))
+    for old, new in zip(both[0][0] + [both[0][1]], both[1][0] + [both[1][1]]):
+        old.copy_(new)
+    graphs[0].replay()
+    assert all(torch.equal(a, w) for a, w in zip(got[0], want[1]))
