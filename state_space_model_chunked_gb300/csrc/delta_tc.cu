@@ -885,62 +885,108 @@ delta_walk_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
 }
 
 // The states that a sequence's parts start from: of the first what its own is; of the second
-// that one's end; E_s <- E_s + E_(s-1) M_(s-1) from there on.  16 rows of a state a CTA, a
-// thread a column of eight of them.  And the offsets of the parts.
-constexpr int kJoinRows = 16;
+// that one's end; E_s <- E_s + E_(s-1) M_(s-1) from there on.  A thread has a column of kR of a
+// CTA's 2 kR rows; the maps are copied to shared memory one ahead.  Bound by that memory's
+// reads, with few rows by each step's latency.  And the offsets of the parts.
+constexpr uint32_t kJoinMap = 128 * 128 * 4;
+constexpr uint32_t join_bytes(int r) { return 2 * kJoinMap + 2 * 128 * 2 * r * 4 + 16; }
+template <int kR>
 __global__ void __launch_bounds__(256)
-delta_join_kernel(const SsdDelta d, const float *init, int segments, int half_first, int *cu, float *starts, const float *maps) {
-    __shared__ float e[kJoinRows][129];
+delta_join_kernel(const SsdDelta d, const float *init, int segments, int half_first, int *cu, float *starts,
+                  const float *maps, unsigned *err) {
+    extern __shared__ __align__(128) uint8_t join_smem[];
     const int seq = (int)(blockIdx.x / d.heads), head = (int)(blockIdx.x % d.heads), n = d.n;
+    constexpr int kJoinRows = 2 * kR;
     const int r0 = blockIdx.y * kJoinRows, col = threadIdx.x & 127, half = threadIdx.x >> 7;
     const size_t one = (size_t)d.p * n;
+    const uint32_t bars = smem_u32(join_smem) + join_bytes(kR) - 16;
+    if (threadIdx.x == 0) {
+        mbar_init(bars, 1);
+        mbar_init(bars + 8, 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    const auto fetch = [&](int s) {     // the map of part s - 1
+        if (threadIdx.x != 0 || s >= segments) return;
+        const float *map = maps + (((size_t)seq * (segments - 2) + s - 2) * d.heads + head) * n * n;
+        mbar_arrive_expect_tx(bars + 8 * (s & 1), n * n * 4);
+        bulk_load(smem_u32(join_smem) + (s & 1) * kJoinMap, map, n * n * 4, bars + 8 * (s & 1));
+    };
+    fetch(2);
+    fetch(3);
     if (head == 0 && blockIdx.y == 0 && threadIdx.x <= segments) {
         const int first = d.cu ? d.cu[seq] : seq * d.length, len = d.cu ? d.cu[seq + 1] - first : d.length;
-        cu[seq * segments + threadIdx.x] = first + part_start(len, threadIdx.x, segments, half_first);     // (a sequence's end twice)
+        cu[seq * segments + threadIdx.x] =
+            first + part_start(len, threadIdx.x, segments, half_first);     // (a sequence's end twice)
     }
-    float *const own = starts + ((size_t)seq * segments * d.heads + head) * one + (size_t)r0 * n;
-    for (int i = threadIdx.x; i < min(kJoinRows, d.p - r0) * n; i += 256)
-        own[i] = init ? init[((size_t)seq * d.heads + head) * one + (size_t)r0 * n + i] : 0.f;
-    for (int s = 2; s < segments; ++s) {
-        const float *from = own + (size_t)(s - 1) * d.heads * one;
-        float *const to = own + (size_t)s * d.heads * one;
-        const float *map = maps + (((size_t)seq * (segments - 2) + s - 2) * d.heads + head) * n * n;
-        for (int i = threadIdx.x; i < kJoinRows * 128; i += 256) {
-            const int r = i >> 7, c = i & 127;
-            e[r][c] = r0 + r < d.p && c < n ? from[(size_t)r * n + c] : 0.f;
-        }
-        __syncthreads();
-        float v[8];
+    // states by columns, 2 kR rows each, of a part and of the one in front of it
+    float *const states = reinterpret_cast<float *>(join_smem + 2 * kJoinMap);
+    const int row = r0 + kR * half;
+    float *const own = starts + ((size_t)seq * segments * d.heads + head) * one + (size_t)row * n + col;
+    const float *const from = init ? init + ((size_t)seq * d.heads + head) * one + (size_t)row * n + col : nullptr;
+    const auto on = [&](int i) { return col < n && row + i < d.p; };
+    {
+        float first[kR], second[kR];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = col < n && r0 + 8 * half + i < d.p ? to[(size_t)(8 * half + i) * n + col] : 0.f;
+        for (int i = 0; i < kR; ++i) {
+            first[i] = from && on(i) ? from[(size_t)i * n] : 0.f;
+            second[i] = on(i) ? own[(size_t)d.heads * one + (size_t)i * n] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kR; ++i) {
+            if (on(i)) own[(size_t)i * n] = first[i];
+            states[128 * kJoinRows + col * kJoinRows + kR * half + i] = second[i];
+        }
+    }
+    for (int s = 2; s < segments; ++s) {
+        float *const to = own + (size_t)s * d.heads * one;
+        float v[kR];
+#pragma unroll
+        for (int i = 0; i < kR; ++i) v[i] = on(i) ? to[(size_t)i * n] : 0.f;
+        __syncthreads();
+        if (!mbar_wait(bars + 8 * (s & 1), ((s >> 1) - 1) & 1, kSsdDefaultWaitNs)) ssd_report(err, SSD_DEVERR_TIMEOUT);
+        const float *map = reinterpret_cast<const float *>(join_smem + (s & 1) * kJoinMap) + col;
+        const float *e = states + ((s - 1) & 1) * 128 * kJoinRows + kR * half;
         if (col < n) {
 #pragma unroll 8
             for (int k = 0; k < n; ++k) {
-                const float m = map[(size_t)k * n + col];
+                const float m = map[k * n];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] += e[8 * half + i][k] * m;
+                for (int i = 0; i < kR; i += 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(e + k * kJoinRows + i);
+                    v[i] += x.x * m;
+                    v[i + 1] += x.y * m;
+                    v[i + 2] += x.z * m;
+                    v[i + 3] += x.w * m;
+                }
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (r0 + 8 * half + i < d.p) to[(size_t)(8 * half + i) * n + col] = v[i];
         }
-        __syncthreads();        // (this CTA alone reads these rows again)
+#pragma unroll
+        for (int i = 0; i < kR; ++i) {
+            if (on(i)) to[(size_t)i * n] = v[i];
+            states[(s & 1) * 128 * kJoinRows + col * kJoinRows + kR * half + i] = v[i];
+        }
+        __syncthreads();        // (the map has been read)
+        fetch(s + 2);
     }
 }
 
 // In how many parts a sequence is walked.  One walk a head leaves most SMs idle where there
 // are few heads and sequences, and a part's end depends on its beginning by a map of N x N:
 // the parts' own ends and their maps, side by side, then all parts again, which pays from
-// three parts on.  Parts of 16 chunks at least, all at the same time on an SM each; a first
-// part, which has no map, of half the others' length lets two of them have an SM after each
-// other.  65536 tokens through 32 heads of 128 x 128: 2200 us in one walk, 1580 in three parts, 1390 in
-// four with the first of half the length.
+// three parts on, all at the same time on an SM each; a first part, which has no map, of half
+// the others' length lets two of them have an SM after each other.  65536 tokens through 32
+// heads of 128 x 128: 2200 us in one walk, 1580 in three parts, 1370 in four with the first of
+// half the length.  Parts have 8 chunks at least (one head, 24 chunks: 70 us in one, 62 in
+// three; 47 chunks: 123 in one, 76 in five), 12 where they fill more than half of the SMs (48
+// heads, 24 chunks: 84 us in one, 94 in three; 47 chunks: 153 in one, 147 in three).
 struct InParts { int parts, half; };
 InParts segments_of(const SsdDelta &d, int sms) {
     const long long walks = (long long)d.nseq * d.heads, blocks = (d.p + 127) / 128;
     const long long chunks = d.tokens / kC / d.nseq;
+    const int least = 6 * walks * blocks > sms ? 12 : 8;
     InParts best{1, 0};
-    for (int s = 3; s <= 16 && s * 16 <= chunks && walks * blocks * s <= sms; ++s) {
+    for (int s = 3; s <= 16 && s * least <= chunks && walks * blocks * s <= sms; ++s) {
         const long long others = walks * (blocks + 1) * (s - 2), firsts = walks * blocks;
         if (others + firsts <= sms) best = {s, 0};
         else if (others + (firsts + 1) / 2 <= sms) best = {s, 1};
@@ -1018,8 +1064,17 @@ cudaError_t launch_fwd(const SsdDeltaFwd &f, void *ws, int sms, unsigned *err, c
         const long long jobs = walks * blocks * (w.segments - 1) + walks * (w.segments - 2);
         delta_walk_tc_kernel<kPanels, true><<<(unsigned)jobs, kWalkThreads, Lay::kBytes, stream>>>(q, k, v, w);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        const dim3 grid((unsigned)walks, (unsigned)((d.p + kJoinRows - 1) / kJoinRows));
-        delta_join_kernel<<<grid, 256, 0, stream>>>(d, f.init, w.segments, w.half, parts.cu, w.starts, w.maps);
+        // (four rows a thread for as long as that is a CTA an SM: 8 heads in 16 parts 25 us, with eight
+        // rows 34; 16 heads in 6 parts 23 and 17)
+        const auto join = [&](auto kernel, int r) {
+            const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, join_bytes(r));
+            const dim3 grid((unsigned)walks, (unsigned)((d.p + 2 * r - 1) / (2 * r)));
+            if (set == cudaSuccess)
+                kernel<<<grid, 256, join_bytes(r), stream>>>(d, f.init, w.segments, w.half, parts.cu, w.starts, w.maps, err);
+            return set;
+        };
+        const bool few = walks * ((d.p + 7) / 8) <= sms;
+        if ((e = few ? join(delta_join_kernel<4>, 4) : join(delta_join_kernel<8>, 8)) != cudaSuccess) return e;
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         w.d.cu = parts.cu;
         w.d.nseq *= w.segments;

@@ -158,3 +158,23 @@ def test_refusals():
                 lambda: ssd.layernorm_fwd(x.to(DT["fp8"]), w)):
         with pytest.raises(ssd.SsdError):
             bad()
+
+
+@pytest.mark.parametrize("rows,width", [(2431, 264), (2432, 8), (2432, 512), (2433, 776), (3000, 1024), (2440, 1544),
+                                        (5003, 2048), (2600, 2560), (2450, 4096), (2450, 4104), (2450, 1001)])
+@pytest.mark.parametrize("xd,rd,pad", [("bf16", None, 0), ("bf16", "bf16", 8), ("bf16", "f32", 0), ("f32", "f32", 4),
+                                       ("f32", None, 2), ("bf16", "bf16", 2)])
+def test_many_rows_to_8_bits(rows, width, xd, rd, pad):
+    """Around the number of rows from which on a row is a warp's; rows whose addresses and
+    strides rule that out among them (pad 2)."""
+    rng = np.random.default_rng(rows + width)
+    x, w = cols(rng, rows, width, pad, xd, mean=0.5), tens(rng, (width,), std=0.3, mean=1.0)
+    b, r = tens(rng, (width,), std=0.5), cols(rng, rows, width, pad, rd, std=3.0) if rd else None
+    y, s, mean, rstd, scale = ssd.layernorm_fwd(x, w, b, r, eps=1e-5, out_dtype=DT["fp8"])
+    yr, sr, mr, rr = ref.layernorm_fwd(host(x), None if r is None else host(r), host(w), host(b), 1e-5)
+    assert np.linalg.norm(host(mean) - mr) <= BAR["f32"] * np.linalg.norm(np.sqrt((sr * sr).mean(axis=-1)))
+    assert rel(host(rstd), rr) <= BAR["f32"]
+    assert s is None if r is None else rel(host(s), sr) <= BAR[rd]
+    top, sc = np.abs(yr).max(axis=-1), host(scale)[:, None]
+    assert rel(host(scale), top / 448.0) <= BAR["f32"]
+    assert np.all(np.abs(host(y) * sc - yr) <= np.abs(yr) * 2.0 ** -4 + 1e-5 * top[:, None] + sc * 2.0 ** -10)
