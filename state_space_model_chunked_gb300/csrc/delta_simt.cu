@@ -22,6 +22,8 @@
 //   4. the sums over a group's heads and a head's slabs, rounded once.
 // Bound by the fp32 pipe: about 4 P N multiply-adds a token forward, 12 backward, where one
 // head's tokens follow each other at the latency of a token's two sums over eight lanes.
+// 4 x 77 tokens, 8 heads of 64 x 64: 22 us, 0.29 a token.  8 x 2047 tokens, 16 heads of
+// 128 x 128: 2.25 ms (15 TFLOP/s), gradients 8.65 ms.
 #include "launch.h"
 #include "ptx.cuh"
 

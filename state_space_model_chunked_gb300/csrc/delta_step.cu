@@ -5,7 +5,9 @@
 // Bound by memory: a state is read once and written once.  Both of its products are taken
 // of the state as it is read, S k and S q, since o = scale (exp(g) S q + u (k q)): one round
 // of sums over the lanes between the loads and the stores.  Eight lanes share a row, a
-// thread has kR rows of kV columns in registers, all their loads under way together.
+// thread has kR rows of kV columns in registers, all their loads under way together.  16
+// sequences, 32 heads of 128 x 128 in fp32: 13.5 us, 0.74 of a copy's rate; 2 are the launch
+// and the first loads' latency.
 #include "launch.h"
 #include "ptx.cuh"
 

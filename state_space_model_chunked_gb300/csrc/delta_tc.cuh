@@ -116,7 +116,7 @@ __device__ __forceinline__ void put_parts(uint8_t *image, uint32_t at, const flo
 }
 
 // The sequence that a walk's CTA takes as number `rank`: packed ones by falling length, so
-// that the longest do not begin last (47 sequences of 4 to 5000 tokens: 580 -> 420 us).  All
+// that the longest do not begin last (47 sequences of 4 to 5000 tokens: 580 -> 487 us).  All
 // threads of the CTA; `place` in shared memory.
 __device__ __forceinline__ int sequence_of(const SsdDelta &d, int rank, volatile int *place) {
     constexpr int kMost = 512;          // above this each CTA's count would take too long

@@ -21,6 +21,10 @@
 // over pairs i >= t > j is wanted, it is taken as the running sum of row sums less column
 // sums of the same fp32 values, so what cancels does so exactly.
 //   As forward, factors that are no bf16 values are held in two bf16 parts.
+//   8 x 2047 tokens, 16 heads of 128 x 128: 570 us, of which the chunk matrices 60, the walk 137
+// (dS and Z leave at 3.0 TB/s beside 2.4 TB/s of loads) and the second kernel 367: 25000 cycles a
+// chunk and head for six products in turn, each between two barriers, with 47% of the issue
+// slots, and 220 KB of tiles an SM that leave no room for a second CTA.
 #include "delta_tc.cuh"
 
 namespace {

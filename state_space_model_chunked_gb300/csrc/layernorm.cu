@@ -17,6 +17,8 @@
 //     n = n1 + n2,  d = m2 - m1,  m = m1 + d n2 / n,  q = q1 + q2 + d^2 n1 n2 / n,
 // which loses nothing where the mean is large against the spread, as sums of s^2 would,
 // nor where one value is far from the others, as sums around a chosen value would.
+//   16 rows of 2560: 2.6 us (latency: launch, one trip of loads, one barrier).  Gradients of
+// 16376 rows of 1024: 46 us, 0.85 of a copy's rate, 2 of them the partial sums' second pass.
 #include "norm_rows.cuh"
 #include "ptx.cuh"
 
