@@ -116,28 +116,30 @@ __device__ __forceinline__ void product_tf32(float (&d)[2][4], int m0, int n0, i
     }
 }
 
+// s + a y of four values, by pairs.
+__device__ __forceinline__ void fma4(float4 &s, float a, const float4 &y) {
+    const float2 aa = make_float2(a, a);
+    const float2 lo = ffma2(aa, make_float2(y.x, y.y), make_float2(s.x, s.y));
+    const float2 hi = ffma2(aa, make_float2(y.z, y.w), make_float2(s.z, s.w));
+    s = make_float4(lo.x, lo.y, hi.x, hi.y);
+}
 // (1 + A)^-1 of `columns` (A[r][c] at kAw c + r), by all 128 threads: its diagonal blocks of
 // 32 to `rows`, and of the block below the warp's 16 x 16 (rows m0, columns n0 of it).
 __device__ __forceinline__ void invert(float *columns, float *rows, int m0, int n0, float (&below)[2][4]) {
     const int t = threadIdx.x;
     if (t < 64) {       // blocks of 16
         const int b = t >> 4, c = t & 15;
-        float acc[16];
+        float4 acc[4];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+        for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         float *const row = rows + ((b >> 1) * 32 + (b & 1) * 16) * kTw + (b & 1) * 16 + c;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const float x = i == c ? 1.f : -acc[i];
+            const float at[4] = {acc[i / 4].x, acc[i / 4].y, acc[i / 4].z, acc[i / 4].w};
+            const float x = i == c ? 1.f : -at[i % 4];
             const float4 *a = reinterpret_cast<const float4 *>(columns + (16 * b + i) * kAw + 16 * b);
 #pragma unroll
-            for (int v = (i + 1) / 4; v < 4; ++v) {
-                const float4 y = a[v];
-                if (4 * v > i) acc[4 * v] += y.x * x;
-                if (4 * v + 1 > i) acc[4 * v + 1] += y.y * x;
-                if (4 * v + 2 > i) acc[4 * v + 2] += y.z * x;
-                acc[4 * v + 3] += y.w * x;
-            }
+            for (int v = (i + 1) / 4; v < 4; ++v) fma4(acc[v], x, a[v]);      // (used sums get more, unread)
             row[i * kTw] = x;
         }
     } else {            // above them nothing
@@ -154,11 +156,7 @@ __device__ __forceinline__ void invert(float *columns, float *rows, int m0, int 
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
             const float a = columns[(32 * b + k) * kAw + 32 * b + 16 + r];
-            const float4 y = *reinterpret_cast<const float4 *>(row + k * kTw + c);
-            x.x += a * y.x;
-            x.y += a * y.y;
-            x.z += a * y.z;
-            x.w += a * y.w;
+            fma4(x, a, *reinterpret_cast<const float4 *>(row + k * kTw + c));
         }
         *reinterpret_cast<float4 *>(columns + (32 + r) * kAw + 16 * b + c) = x;     // W
         __syncthreads();
@@ -166,11 +164,7 @@ __device__ __forceinline__ void invert(float *columns, float *rows, int m0, int 
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
             const float a = row[(16 + r) * kTw + 16 + k];
-            const float4 y = *reinterpret_cast<const float4 *>(columns + (32 + k) * kAw + 16 * b + c);
-            z.x -= a * y.x;
-            z.y -= a * y.y;
-            z.z -= a * y.z;
-            z.w -= a * y.w;
+            fma4(z, -a, *reinterpret_cast<const float4 *>(columns + (32 + k) * kAw + 16 * b + c));
         }
         *reinterpret_cast<float4 *>(row + (16 + r) * kTw + c) = z;
     }
@@ -259,6 +253,10 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
     float *const rows = reinterpret_cast<float *>(smem + PrepSmem::kRows);
     const bool keys = warp >= 2;
     const int upper = warp & 1;         // which half of the 64 tokens the warp's rows are
+    // P's upper right quarter, for all heads
+    for (int i = threadIdx.x; i < 2 * 32 * 4; i += kPrepThreads)
+        *reinterpret_cast<uint4 *>(smem + PrepSmem::kP + (i >> 7) * kPanel + panel_at((i >> 2) & 31, 32 + (i & 3) * 8)) =
+            make_uint4(0, 0, 0, 0);
     for (int h = 0; h < wide; ++h) {
         uint8_t *const record = a.records + ((size_t)slot * d.heads + head0 + h) * kRecord;
         // The images of the head in front have been read, its sums used.  Each half's sums of
@@ -306,29 +304,32 @@ delta_chunk_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
 #pragma unroll 1
         for (int c0 = 0; c0 < kC; c0 += 16) {
             float v[16];
-            if (!upper && c0 >= 32) {
-                if (keys) break;
+            if (!upper && c0 >= 32) break;      // (zeros)
+            uint32_t r[16];
+            tmem_ld16(lanes + c0, r);
+            float2 by;
+            if (upper && c0 < 32) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = 0.f;
+                for (int j = 0; j < 16; j += 4) *reinterpret_cast<float4 *>(v + j) = *reinterpret_cast<const float4 *>(to_half + c0 + j);
+                by = make_float2(from_half, from_half);
             } else {
-                uint32_t r[16];
-                tmem_ld16(lanes + c0, r);
-                if (upper && c0 < 32) {
 #pragma unroll
-                    for (int j = 0; j < 16; j += 4) *reinterpret_cast<float4 *>(v + j) = *reinterpret_cast<const float4 *>(to_half + c0 + j);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] *= from_half;
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        const float4 c = *reinterpret_cast<const float4 *>(sums + c0 + j);
-                        v[j] = factor * ex2_approx((mine.x - c.x) + (mine.y - c.y));
-                        v[j + 1] = factor * ex2_approx((mine.x - c.z) + (mine.y - c.w));
-                    }
+                for (int j = 0; j < 16; j += 2) {
+                    const float4 c = *reinterpret_cast<const float4 *>(sums + c0 + j);
+                    const float2 less = make_float2(-1.f, -1.f);
+                    const float2 x = ffma2(make_float2(c.x, c.y), less, mine), y = ffma2(make_float2(c.z, c.w), less, mine);
+                    v[j] = ex2_approx(x.x + x.y);
+                    v[j + 1] = ex2_approx(y.x + y.y);
                 }
-                tmem_ld_wait(r);
+                by = make_float2(factor, factor);
+            }
+            tmem_ld_wait(r);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = c0 + j <= last ? v[j] * __uint_as_float(r[j]) : 0.f;
+            for (int j = 0; j < 16; j += 2) {
+                const float2 x = fmul2(fmul2(make_float2(v[j], v[j + 1]), by),
+                                       make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])));
+                v[j] = c0 + j <= last ? x.x : 0.f;
+                v[j + 1] = c0 + j + 1 <= last ? x.y : 0.f;
             }
             if (keys) {
 #pragma unroll
