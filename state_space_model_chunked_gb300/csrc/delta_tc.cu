@@ -22,10 +22,10 @@
 // (16 bits), the product of two second parts left out: with one part the state, which is
 // handed on in fp32, would be off by 3e-3 of itself, with two it is by 4e-6.
 //
-// 65536 tokens, 32 heads of 128 x 128: 1755 us, of which the chunk matrices 375 (their records
+// 65536 tokens, 32 heads of 128 x 128: 1746 us, of which the chunk matrices 368 (their records
 // of 34 KB a chunk and head are written at 3.0 TB/s; 50% of the issue slots, ten barriers a
 // head, five CTAs an SM), the parts' ends and maps 650, their joining 18, the walks 700.  47
-// sequences of 1394 on average, 24 heads of 64 x 128: 723 us, of which 270 and 450.  A walk is
+// sequences of 1394 on average, 24 heads of 64 x 128: 717 us, of which 262 and 450.  A walk is
 // bound by latency: a chunk takes 2.1 us without output and 2.4 with it, for five products that
 // wait for one another (1300 cycles of them) and the steps between them.
 #include <mutex>

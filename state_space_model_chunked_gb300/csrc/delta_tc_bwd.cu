@@ -378,7 +378,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         if (lane == 0) bulk_wait_all();
     } else {
         // the chain: a thread has a row of dS and of dU^T and Z^T
-        const int q = warp & 3, part = warp >> 2, p = 32 * q + lane;
+        const int q = warp & 3, part = warp >> 2;
         const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16);
         constexpr int kMine = kN / 4;
         const int n0 = part * kMine;
