@@ -107,3 +107,15 @@ def test_two_graphs_with_one_workspace():
         old.copy_(new)
     graphs[0].replay()
     assert all(torch.equal(a, w) for a, w in zip(got[0], want[1]))
+
+
+def test_offsets_beyond_32_bits():
+    """Values past the 2^31st: a sequence behind a long one, against the same by itself."""
+    tokens, tail, heads = 270000, 700, 64
+    unit = lambda *s: torch.nn.functional.normalize(torch.randn(*s, device="cuda"), dim=-1).bfloat16()  # noqa: E731
+    x = [unit(tokens, 2, 64), unit(tokens, 2, 64), torch.randn((tokens, heads, 128), device="cuda", dtype=torch.bfloat16),
+         -0.1 * torch.rand((tokens, heads), device="cuda"), torch.rand((tokens, heads), device="cuda")]
+    assert x[2].numel() > 2 ** 31
+    o, final = ssd.delta_scan_fwd(*x, cu_seqlens=[0, tokens - tail, tokens])
+    o2, final2 = ssd.delta_scan_fwd(*(t[None, tokens - tail:].clone() for t in x))
+    assert torch.equal(o[tokens - tail:], o2[0]) and torch.equal(final[1], final2[0])
