@@ -744,7 +744,8 @@ size_t ssd_delta_scan_workspace_bytes(ssd_dtype dtype, long long tokens, int nse
  *   dq, dk, dv   dtype, laid out as q, k and v, with their own token strides.
  *   dg, dbeta    float [tokens][nheads].
  *   workspace    ssd_delta_scan_bwd_workspace_bytes() bytes, 256-byte aligned.
- * Sums are fp32 in an order fixed for given sizes; each result is rounded once. */
+ * Sums are fp32 in an order fixed for given sizes and the device's SMs; each result is
+ * rounded once.  dq, dk and dv overlap none of the inputs. */
 ssd_status ssd_delta_scan_bwd(const void *dout, const void *q, const void *k, const void *v,
                               const float *g, const float *beta, ssd_dtype dtype, int nseq,
                               int length, const int *cu_seqlens_host, const int *cu_seqlens_dev,

@@ -600,7 +600,7 @@ namespace {
 // (which of the two kinds of kernels runs also depends on the addresses)
 size_t delta_bwd_workspace(const SsdDelta &d) {
     if (d.tokens == 0) return 0;
-    const size_t tc = ssd_delta_tc_bwd_workspace(d), simt = ssd_delta_bwd_simt_workspace(d);
+    const size_t tc = ssd_delta_tc_bwd_workspace(d, ssd_sm_count()), simt = ssd_delta_bwd_simt_workspace(d);
     return tc > simt ? tc : simt;
 }
 }  // namespace

@@ -417,14 +417,6 @@ struct WalkSmem {
     static constexpr uint32_t kBytes = kCtl + 256;
 };
 
-// A part's first token within its sequence of `len`: parts are whole chunks, but for the end,
-// and all as long, but for a first one of half that length where `half` is 1.
-__device__ __forceinline__ int part_start(int len, int part, int parts, int half) {
-    if (part == 0) return 0;
-    const long long at = (long long)((len + kC - 1) / kC) * (2 * part - half) / (2 * parts - half) * kC;
-    return at < len ? (int)at : len;
-}
-
 struct WalkTc {
     SsdDelta d;
     const uint8_t *records;
@@ -904,7 +896,7 @@ constexpr uint32_t kJoinMap = 128 * 128 * 4;
 constexpr uint32_t join_bytes(int r) { return 2 * kJoinMap + 2 * 128 * 2 * r * 4 + 16; }
 template <int kR>
 __global__ void __launch_bounds__(256)
-delta_join_kernel(const SsdDelta d, const float *init, int segments, int half_first, int *cu, float *starts,
+delta_join_kernel(const SsdDelta d, const float *init, int segments, int part_half, int *cu, float *starts,
                   const float *maps, unsigned *err) {
     extern __shared__ __align__(128) uint8_t join_smem[];
     const int seq = (int)(blockIdx.x / d.heads), head = (int)(blockIdx.x % d.heads), n = d.n;
@@ -929,7 +921,7 @@ delta_join_kernel(const SsdDelta d, const float *init, int segments, int half_fi
     if (head == 0 && blockIdx.y == 0 && threadIdx.x <= segments) {
         const int first = d.cu ? d.cu[seq] : seq * d.length, len = d.cu ? d.cu[seq + 1] - first : d.length;
         cu[seq * segments + threadIdx.x] =
-            first + part_start(len, threadIdx.x, segments, half_first);     // (a sequence's end twice)
+            first + part_start(len, threadIdx.x, segments, part_half);     // (a sequence's end twice)
     }
     // states by columns, 2 kR rows each, of a part and of the one in front of it
     float *const states = reinterpret_cast<float *>(join_smem + 2 * kJoinMap);
@@ -983,46 +975,8 @@ delta_join_kernel(const SsdDelta d, const float *init, int segments, int half_fi
     }
 }
 
-// In how many parts a sequence is walked.  One walk a head leaves most SMs idle where there
-// are few heads and sequences, and a part's end depends on its beginning by a map of N x N:
-// the parts' own ends and their maps, side by side, then all parts again, which pays from
-// three parts on, all at the same time on an SM each; a first part, which has no map, of half
-// the others' length lets two of them have an SM after each other.  65536 tokens through 32
-// heads of 128 x 128: 2200 us in one walk, 1580 in three parts, 1370 in four with the first of
-// half the length.  Parts have 8 chunks at least (one head, 24 chunks: 70 us in one, 62 in
-// three; 47 chunks: 123 in one, 76 in five), 12 where they fill more than half of the SMs (48
-// heads, 24 chunks: 84 us in one, 94 in three; 47 chunks: 153 in one, 147 in three).
-struct InParts { int parts, half; };
-InParts segments_of(const SsdDelta &d, int sms) {
-    const long long walks = (long long)d.nseq * d.heads, blocks = (d.p + 127) / 128;
-    const long long chunks = d.tokens / kC / d.nseq;
-    const int least = 6 * walks * blocks > sms ? 12 : 8;
-    InParts best{1, 0};
-    for (int s = 3; s <= 16 && s * least <= chunks && walks * blocks * s <= sms; ++s) {
-        const long long others = walks * (blocks + 1) * (s - 2), firsts = walks * blocks;
-        if (others + firsts <= sms) best = {s, 0};
-        else if (others + (firsts + 1) / 2 <= sms) best = {s, 1};
-    }
-    return best;
-}
 size_t records_bytes(const SsdDelta &d) {
     return ((size_t)ssd_delta_slots(d.tokens, d.nseq) * d.heads * kRecord + 255) / 256 * 256;
-}
-struct Parts {
-    float *starts, *maps;
-    int *cu;
-    size_t bytes;
-};
-Parts parts_of(const SsdDelta &d, int segments, uint8_t *at) {
-    Parts p{};
-    if (segments <= 1) return p;
-    const size_t starts = (size_t)segments * d.nseq * d.heads * d.p * d.n * 4;
-    const size_t maps = (size_t)(segments - 2) * d.nseq * d.heads * d.n * d.n * 4;
-    p.bytes = starts + maps + (size_t)(segments * d.nseq + 1) * 4;
-    p.starts = reinterpret_cast<float *>(at);
-    p.maps = reinterpret_cast<float *>(at + starts);
-    p.cu = reinterpret_cast<int *>(at + starts + maps);
-    return p;
 }
 
 template <int kPanels>
@@ -1076,18 +1030,7 @@ cudaError_t launch_fwd(const SsdDeltaFwd &f, void *ws, int sms, unsigned *err, c
         const long long jobs = walks * blocks * (w.segments - 1) + walks * (w.segments - 2);
         delta_walk_tc_kernel<kPanels, true><<<(unsigned)jobs, kWalkThreads, Lay::kBytes, stream>>>(q, k, v, w);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        // (four rows a thread for as long as that is a CTA an SM: 8 heads in 16 parts 25 us, with eight
-        // rows 34; 16 heads in 6 parts 23 and 17)
-        const auto join = [&](auto kernel, int r) {
-            const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, join_bytes(r));
-            const dim3 grid((unsigned)walks, (unsigned)((d.p + 2 * r - 1) / (2 * r)));
-            if (set == cudaSuccess)
-                kernel<<<grid, 256, join_bytes(r), stream>>>(d, f.init, w.segments, w.half, parts.cu, w.starts, w.maps, err);
-            return set;
-        };
-        const bool few = walks * ((d.p + 7) / 8) <= sms;
-        if ((e = few ? join(delta_join_kernel<4>, 4) : join(delta_join_kernel<8>, 8)) != cudaSuccess) return e;
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if ((e = launch_join(d, f.init, segments, w.half, parts, sms, err, stream)) != cudaSuccess) return e;
         w.d.cu = parts.cu;
         w.d.nseq *= w.segments;
         w.init = w.starts;
@@ -1100,6 +1043,54 @@ cudaError_t launch_fwd(const SsdDeltaFwd &f, void *ws, int sms, unsigned *err, c
 }  // namespace
 
 namespace ssddelta {
+
+// In how many parts a sequence is walked.  One walk a head leaves most SMs idle where there
+// are few heads and sequences, and a part's end depends on its beginning by a map of N x N:
+// the parts' own ends and their maps, side by side, then all parts again, which pays from
+// three parts on, all at the same time on an SM each; a first part, which has no map, of half
+// the others' length lets two of them have an SM after each other.  65536 tokens through 32
+// heads of 128 x 128: 2200 us in one walk, 1580 in three parts, 1370 in four with the first of
+// half the length.  Parts have 8 chunks at least (one head, 24 chunks: 70 us in one, 62 in
+// three; 47 chunks: 123 in one, 76 in five), 12 where they fill more than half of the SMs (48
+// heads, 24 chunks: 84 us in one, 94 in three; 47 chunks: 153 in one, 147 in three).  The walk
+// back is split by the same rule (48 heads, 47 chunks: 423 us in one, 391 in three).
+InParts segments_of(const SsdDelta &d, int sms) {
+    const long long walks = (long long)d.nseq * d.heads, blocks = (d.p + 127) / 128;
+    const long long chunks = d.tokens / kC / d.nseq;
+    const int least = 6 * walks * blocks > sms ? 12 : 8;
+    InParts best{1, 0};
+    for (int s = 3; s <= 16 && s * least <= chunks && walks * blocks * s <= sms; ++s) {
+        const long long others = walks * (blocks + 1) * (s - 2), firsts = walks * blocks;
+        if (others + firsts <= sms) best = {s, 0};
+        else if (others + (firsts + 1) / 2 <= sms) best = {s, 1};
+    }
+    return best;
+}
+Parts parts_of(const SsdDelta &d, int segments, uint8_t *at) {
+    Parts p{};
+    if (segments <= 1) return p;
+    const size_t starts = (size_t)segments * d.nseq * d.heads * d.p * d.n * 4;
+    const size_t maps = (size_t)(segments - 2) * d.nseq * d.heads * d.n * d.n * 4;
+    p.bytes = starts + maps + (size_t)(segments * d.nseq + 1) * 4;
+    p.starts = reinterpret_cast<float *>(at);
+    p.maps = reinterpret_cast<float *>(at + starts);
+    p.cu = reinterpret_cast<int *>(at + starts + maps);
+    return p;
+}
+cudaError_t launch_join(const SsdDelta &d, const float *init, InParts parts, int half, const Parts &p, int sms,
+                        unsigned *err, cudaStream_t stream) {
+    const long long walks = (long long)d.nseq * d.heads;
+    // (four rows a thread for as long as that is a CTA an SM: 8 heads in 16 parts 25 us, with eight
+    // rows 34; 16 heads in 6 parts 23 and 17)
+    const auto run = [&](auto kernel, int r) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, join_bytes(r));
+        if (e != cudaSuccess) return e;
+        const dim3 grid((unsigned)walks, (unsigned)((d.p + 2 * r - 1) / (2 * r)));
+        kernel<<<grid, 256, join_bytes(r), stream>>>(d, init, parts.parts, half, p.cu, p.starts, p.maps, err);
+        return cudaGetLastError();
+    };
+    return walks * ((d.p + 7) / 8) <= sms ? run(delta_join_kernel<4>, 4) : run(delta_join_kernel<8>, 8);
+}
 
 bool make_map(CUtensorMap *m, const void *p, int width, int heads, long long tokens, long long stride, int cols,
               bool swizzle) {

@@ -200,6 +200,32 @@ __device__ __forceinline__ void load_rows(float *stage, float (&v)[kMine], const
 }
 constexpr uint32_t kStageRows = 2048;       // bytes a warp
 
+// A part's first token within its sequence of `len`: parts are whole chunks, but for the end,
+// and all as long, but for one of half that length: the first where `half` is 1, the last
+// where it is -1.
+__device__ __forceinline__ int part_start(int len, int part, int parts, int half) {
+    if (part == 0) return 0;
+    const int all = 2 * parts - (half ? 1 : 0);
+    const long long at = (long long)((len + kC - 1) / kC) * (2 * part - (half > 0 ? 1 : 0)) / all * kC;
+    return at < len ? (int)at : len;
+}
+// In how many parts a sequence is walked, whether one of them has half the others' length,
+// and what lies in the workspace for them (delta_tc.cu).
+struct InParts {
+    int parts, half;
+};
+InParts segments_of(const SsdDelta &d, int sms);
+struct Parts {
+    float *starts, *maps;
+    int *cu;
+    size_t bytes;
+};
+Parts parts_of(const SsdDelta &d, int segments, uint8_t *at);
+// The states that parts start from, by their ends and maps, in the order of the walk; `half`
+// as for part_start.
+cudaError_t launch_join(const SsdDelta &d, const float *init, InParts parts, int half, const Parts &p, int sms,
+                        unsigned *err, cudaStream_t stream);
+
 inline bool on_16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
 // The records of all chunks (delta_tc.cu); least_beta: see kLeastBeta.

@@ -21,6 +21,8 @@
 // over pairs i >= t > j is wanted, it is taken as the running sum of row sums less column
 // sums of the same fp32 values, so what cancels does so exactly.
 //   As forward, factors that are no bf16 values are held in two bf16 parts.
+//   A long sequence of few heads is walked in parts, as forward but from the last one on: 25600
+// tokens, one head 1626 -> 284 us, 32 heads 2790 -> 2130.
 //   8 x 2047 tokens, 16 heads of 128 x 128: 570 us, of which the chunk matrices 60, the walk 137
 // (dS and Z leave at 3.0 TB/s beside 2.4 TB/s of loads) and the second kernel 367: 25000 cycles a
 // chunk and head for six products in turn, each between two barriers, with 47% of the issue
@@ -72,8 +74,12 @@ struct BackTc {
     long long dv_stride;
     bool dv_vectors;
     float *dinit;
-    float *z;               // [token][head][P]
+    float *z;               // [slot][head] tiles
     uint8_t *dstate;        // [slot][head] images
+    // in parts (segments > 1), as the forward walk: `d` has them for sequences; before that, from
+    // the last one on, their ends for `starts` [seq][segment from the last][head][P][N], and maps
+    int segments, half;
+    float *starts, *maps;
     unsigned *err;
     unsigned long long wait_ns;
     bool withhold;
@@ -88,7 +94,7 @@ enum BackBar {
     kBars
 };
 
-template <int kPanels>
+template <int kPanels, bool kEnds>
 __global__ void __launch_bounds__(kBackThreads, 1)
 delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                      const __grid_constant__ CUtensorMap mapDo, const BackTc a) {
@@ -102,15 +108,45 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         if (threadIdx.x == 0) ssd_report(a.err, SSD_DEVERR_SMEM_ALIGN);
         return;
     }
-    const int head = (int)(blockIdx.x % d.heads), group = head / (d.heads / d.groups);
-    const int seq = sequence_of(d, (int)(blockIdx.x / d.heads), reinterpret_cast<volatile int *>(smem + Lay::kCtl + 8 * kBars + 8));
-    const long long first = d.cu ? d.cu[seq] : (long long)seq * d.length;
-    const int len = d.cu ? d.cu[seq + 1] - d.cu[seq] : d.length;
+    // kEnds: parts for their ends or (map) for their maps, without output
+    const unsigned maps = kEnds ? (unsigned)d.nseq * (a.segments - 2) * d.heads : 0;
+    const bool map = kEnds && blockIdx.x < maps;
+    const unsigned job = blockIdx.x - (map ? 0 : maps);
+    const int head = (int)(job % d.heads), group = head / (d.heads / d.groups), rows = map ? d.n : d.p;
+    int seq = (int)(job / d.heads), back = 0;       // back: the part's number from the last one
+    if constexpr (kEnds) {
+        back = a.segments - 2 - seq / d.nseq;
+        seq %= d.nseq;
+    } else {
+        seq = sequence_of(d, seq, reinterpret_cast<volatile int *>(smem + Lay::kCtl + 8 * kBars + 8));
+    }
+    long long first = d.cu ? d.cu[seq] : (long long)seq * d.length;
+    int len = d.cu ? d.cu[seq + 1] - d.cu[seq] : d.length;
+    if constexpr (kEnds) {
+        const int at = part_start(len, a.segments - 1 - back, a.segments, a.half);
+        len = part_start(len, a.segments - back, a.segments, a.half) - at;
+        first += at;
+    }
     const int chunks = (len + kC - 1) / kC;
-    const size_t size = (size_t)d.p * d.n, state = ((size_t)seq * d.heads + head) * size;
+    const size_t size = (size_t)rows * d.n;
+    // where dS comes from (null: zeros, or a map's unit matrix) and goes to
+    const auto source = [&]() -> const float * {
+        if (kEnds) return back == 0 && a.dfinal ? a.dfinal + ((size_t)seq * d.heads + head) * size : nullptr;
+        if (a.segments == 1) return a.dfinal ? a.dfinal + ((size_t)seq * d.heads + head) * size : nullptr;
+        const int whole = seq / a.segments, i = a.segments - 1 - seq % a.segments;
+        return a.starts + (((size_t)whole * a.segments + i) * d.heads + head) * size;
+    };
+    const auto target = [&]() -> float * {
+        if (map) return a.maps + (((size_t)seq * (a.segments - 2) + back - 1) * d.heads + head) * size;
+        if (kEnds) return a.starts + (((size_t)seq * a.segments + back + 1) * d.heads + head) * size;
+        if (!a.dinit || seq % a.segments) return nullptr;
+        return a.dinit + ((size_t)(seq / a.segments) * d.heads + head) * size;
+    };
     if (chunks == 0) {
-        if (a.dinit)
-            for (size_t i = threadIdx.x; i < size; i += kBackThreads) a.dinit[state + i] = a.dfinal ? a.dfinal[state + i] : 0.f;
+        const float *from = source();
+        if (float *const to = target())
+            for (int i = threadIdx.x; i < (int)size; i += kBackThreads)
+                to[i] = from ? from[i] : map && i / d.n == i % d.n ? 1.f : 0.f;
         return;
     }
     const auto bar = [&](int i) { return base + Lay::kCtl + 8u * (uint32_t)i; };
@@ -136,7 +172,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot;
-    const long long slot0 = ssd_delta_slot(first, seq, 0);
+    const long long slot0 = ssd_delta_slot(first, kEnds ? seq : seq / a.segments, 0);
     int loaded = 0;
 
     // step `it` of the walk is chunk chunks - 1 - it, in stage it & 1
@@ -147,15 +183,15 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
             if (elect_one()) {
                 const uint32_t to = base + s * Lay::kStage;
                 const int token = (int)(first + (long long)c * kC);
-                mbar_arrive_expect_tx(bar(kFull + s), (2 * kPanels + 2) * kPanel + kRecord);
+                mbar_arrive_expect_tx(bar(kFull + s), (map ? kPanels : 2 * kPanels + 2) * kPanel + kRecord);
 #pragma unroll
                 for (int p = 0; p < kPanels; ++p) {
                     tma_load_3d(to + Lay::kK + p * kPanel, &mapK, bar(kFull + s), 64 * p, group, token);
-                    tma_load_3d(to + Lay::kQ + p * kPanel, &mapQ, bar(kFull + s), 64 * p, group, token);
+                    if (!map) tma_load_3d(to + Lay::kQ + p * kPanel, &mapQ, bar(kFull + s), 64 * p, group, token);
                 }
 #pragma unroll
                 for (int p = 0; p < 2; ++p)
-                    tma_load_3d(to + Lay::kDo + p * kPanel, &mapDo, bar(kFull + s), 64 * p, head, token);
+                    if (!map) tma_load_3d(to + Lay::kDo + p * kPanel, &mapDo, bar(kFull + s), 64 * p, head, token);
                 bulk_load(to + Lay::kRec, a.records + ((size_t)(slot0 + c) * d.heads + head) * kRecord, kRecord,
                           bar(kFull + s));
             }
@@ -204,11 +240,11 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
             const uint32_t at = base + s * Lay::kStage;
             if (!wait.warp(bar(kFull + s), (it >> 1) & 1) || !wait.warp(bar(kSh), it & 1)) break;
             // (Z of the step in front has been read)
-            if (it > 0 && !wait.warp(bar(kZRead), (it - 1) & 1)) break;
+            if (!kEnds && it > 0 && !wait.warp(bar(kZRead), (it - 1) & 1)) break;
             tc_fence_after();
             if (one) {
                 // the last chunk's rows behind the sequence's end are clean only now
-                if (it == 0) from_output(at);
+                if (it == 0 && !map) from_output(at);
                 keys(kColSh, at + Lay::kK, false);
             }
             __syncwarp();
@@ -233,13 +269,15 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
                 mma_commit(bar(kZ));
             }
             __syncwarp();
-            if (!wait.warp(bar(kD), it & 1)) break;
-            tc_fence_after();
-            if (one) {
-                state_update(kColD, at + Lay::kQ);
-                state_update(kColDl, at + Lay::kQ);
+            if (!map) {
+                if (!wait.warp(bar(kD), it & 1)) break;
+                tc_fence_after();
+                if (one) {
+                    state_update(kColD, at + Lay::kQ);
+                    state_update(kColDl, at + Lay::kQ);
+                }
+                __syncwarp();
             }
-            __syncwarp();
             if (!wait.warp(bar(kWh), it & 1)) break;
             tc_fence_after();
             if (one) state_update(kColR, at + Lay::kK);
@@ -252,7 +290,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
                 mma_commit(bar(kEmpty + s));
             }
             __syncwarp();
-            if (it + 1 < chunks) {
+            if (it + 1 < chunks && !map) {
                 if (!wait.warp(bar(kFull + (s ^ 1)), ((it + 1) >> 1) & 1)) break;
                 if (one) from_output(base + (s ^ 1) * Lay::kStage);
                 __syncwarp();
@@ -273,6 +311,10 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
             const uint8_t *stage = smem + s * Lay::kStage;
             const float *gates = reinterpret_cast<const float *>(stage + Lay::kRec + kRecGates) + 32 * half;
             if (!wait.warp(bar(kFull + s), (it >> 1) & 1)) break;
+            if (map) {
+                if (lane == 0) mbar_arrive(bar(kEmpty + s));
+                continue;
+            }
             // (the step in front has used its parts)
             if (it > 0 && !wait.warp(bar(kS), (it - 1) & 1)) break;
             tc_fence_after();
@@ -302,6 +344,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
                 mbar_arrive(bar(kD));
                 mbar_arrive(bar(kEmpty + s));
             }
+            if (kEnds) continue;
             // dS, as the products have it, for the chunk's other gradients: a panel's 32 rows
             // of a part are 4 KB in one piece
             if (!wait.warp(bar(kSl), it & 1)) break;
@@ -417,18 +460,18 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         const auto stage = [&](int it) { return smem + (it & 1) * Lay::kStage; };
         const auto decay_of = [&](int it) { return reinterpret_cast<const float *>(stage(it) + Lay::kRec + kRecGates)[kC - 1]; };
         float v[kMine];
-        if (a.dfinal) {
+        if (const float *from = source()) {
             load_rows<kMine>(reinterpret_cast<float *>(smem + Lay::kRows + warp * kStageRows), v,
-                             a.dfinal + state + (size_t)(32 * q) * d.n + n0, d.n, d.p - 32 * q, d.n - n0);
+                             from + (size_t)(32 * q) * d.n + n0, d.n, rows - 32 * q, d.n - n0);
         } else {
 #pragma unroll
-            for (int i = 0; i < kMine; ++i) v[i] = 0.f;
+            for (int i = 0; i < kMine; ++i) v[i] = map && n0 + i == 32 * q + lane ? 1.f : 0.f;
         }
         const bool on = wait.warp(bar(kFull), 0);
         if (on) {
             const int tokens = len - (chunks - 1) * kC;
             if (tokens < kC) {
-                clean_rows(smem, kPanel, 2 * kPanels + 2, tokens, threadIdx.x, 32 * kChainWarps);
+                clean_rows(smem, kPanel, 2 * kPanels + 2, tokens, threadIdx.x, 32 * kChainWarps);     // (never a map's)
                 fence_proxy_async_smem();
             }
             put(v, decay_of(0));
@@ -443,9 +486,13 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
             tc_fence_after();
             uint32_t r[16], y[16], hi[8];
             tmem_ld16(tq + kColX + 16 * part, r);
-            tmem_ld16(tq + kColY + 16 * part, y);
+            if (!map) tmem_ld16(tq + kColY + 16 * part, y);
             tmem_ld_wait(r);
             tmem_ld_wait(y);
+            if (map) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) y[i] = 0;
+            }
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
                 const float2 u = ffma2(make_float2(f[i], f[i + 1]), make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])),
@@ -501,7 +548,7 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
             if (more && !wait.warp(bar(kFull + (s ^ 1)), ((it + 1) >> 1) & 1)) break;
             const float decay = more ? decay_of(it + 1) : 1.f;
             // (dS's parts have been read by the output's warps)
-            if (!wait.warp(bar(kS), it & 1) || !wait.warp(bar(kSRead), it & 1)) break;
+            if (!wait.warp(bar(kS), it & 1) || (!kEnds && !wait.warp(bar(kSRead), it & 1))) break;
             tc_fence_after();
             uint32_t m[kMine];
             if constexpr (kMine == 32) tmem_ld32(tq + kColS + n0, m);
@@ -511,9 +558,9 @@ delta_back_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
 #pragma unroll
             for (int i = 0; i < kMine; ++i) v[i] = __uint_as_float(m[i]);
             if (more) put(v, decay);
-            else if (a.dinit)       // (by way of the last chunk's keys, queries and dO, which are used up)
+            else if (float *const to = target())        // (by way of the last chunk's keys, queries and dO, which are used up)
                 store_rows<kMine>(reinterpret_cast<float *>(stage(it) + warp * kStageRows), v,
-                                  a.dinit + state + (size_t)(32 * q) * d.n + n0, d.n, d.p - 32 * q, d.n - n0);
+                                  to + (size_t)(32 * q) * d.n + n0, d.n, rows - 32 * q, d.n - n0);
         }
     }
     // copies in flight land before the CTA ends
@@ -1063,9 +1110,9 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
 }
 
 struct Plan {
-    size_t records, z, dstate, dq, dk, total;
+    size_t records, z, dstate, dq, dk, parts, total;
 };
-Plan plan_of(const SsdDelta &d) {
+Plan plan_of(const SsdDelta &d, int sms) {
     const auto up = [](size_t n) { return (n + 255) / 256 * 256; };
     const size_t slots = (size_t)ssd_delta_slots(d.tokens, d.nseq), tokens = (size_t)d.tokens;
     Plan p;
@@ -1074,7 +1121,8 @@ Plan plan_of(const SsdDelta &d) {
     p.dstate = p.z + up(slots * d.heads * kZTile * 4);
     p.dq = p.dstate + up(slots * d.heads * state_image(d.n <= 64 ? 1 : 2));
     p.dk = p.dq + (d.heads == d.groups ? 0 : up(tokens * d.heads * d.n * 4));
-    p.total = p.dk + (d.heads == d.groups ? 0 : up(tokens * d.heads * d.n * 4));
+    p.parts = p.dk + (d.heads == d.groups ? 0 : up(tokens * d.heads * d.n * 4));
+    p.total = p.parts + parts_of(d, segments_of(d, sms).parts, nullptr).bytes;
     return p;
 }
 
@@ -1088,7 +1136,7 @@ cudaError_t launch(const SsdDeltaBwd &b, void *ws, int sms, unsigned *err, cudaS
         !make_map(&o, b.dout, d.p, d.heads, d.tokens, b.do_stride, 64, true))
         return cudaErrorInvalidValue;
     const SsdDebug debug = ssd_debug_config();
-    const Plan plan = plan_of(d);
+    const Plan plan = plan_of(d, sms);
     const auto at = [&](size_t offset) { return static_cast<char *>(ws) + offset; };
     uint8_t *records = reinterpret_cast<uint8_t *>(at(plan.records));
     float *z = reinterpret_cast<float *>(at(plan.z));
@@ -1098,12 +1146,26 @@ cudaError_t launch(const SsdDeltaBwd &b, void *ws, int sms, unsigned *err, cudaS
     using Back = BackSmem<kPanels>;
     using Grad = GradSmem<kPanels>;
     static_assert(Back::kBytes <= 232448 && Grad::kBytes <= 232448, "more than 227 KB of shared memory");
-    e = cudaFuncSetAttribute(delta_back_tc_kernel<kPanels>, cudaFuncAttributeMaxDynamicSharedMemorySize, Back::kBytes);
+    e = cudaFuncSetAttribute(delta_back_tc_kernel<kPanels, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Back::kBytes);
     if (e != cudaSuccess) return e;
-    const BackTc w{d, records, b.dfinal, static_cast<__nv_bfloat16 *>(b.dv), b.dv_stride,
-                   ((uintptr_t)b.dv & 15u) == 0 && b.dv_stride % 8 == 0, b.dinit, z, dstate, err, debug.wait_ns,
-                   debug.fault == kSsdFaultWithholdSignal};
-    delta_back_tc_kernel<kPanels><<<(unsigned)((long long)d.nseq * d.heads), kBackThreads, Back::kBytes, stream>>>(q, k, o, w);
+    const InParts segments = segments_of(d, sms);
+    const Parts parts = parts_of(d, segments.parts, reinterpret_cast<uint8_t *>(at(plan.parts)));
+    BackTc w{d, records, b.dfinal, static_cast<__nv_bfloat16 *>(b.dv), b.dv_stride,
+             ((uintptr_t)b.dv & 15u) == 0 && b.dv_stride % 8 == 0, b.dinit, z, dstate,
+             segments.parts, -segments.half, parts.starts, parts.maps, err, debug.wait_ns,
+             debug.fault == kSsdFaultWithholdSignal};
+    const long long walks = (long long)d.nseq * d.heads;
+    if (segments.parts > 1) {
+        e = cudaFuncSetAttribute(delta_back_tc_kernel<kPanels, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Back::kBytes);
+        if (e != cudaSuccess) return e;
+        const long long jobs = walks * (2 * segments.parts - 3);
+        delta_back_tc_kernel<kPanels, true><<<(unsigned)jobs, kBackThreads, Back::kBytes, stream>>>(q, k, o, w);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if ((e = launch_join(d, b.dfinal, segments, w.half, parts, sms, err, stream)) != cudaSuccess) return e;
+        w.d.cu = parts.cu;
+        w.d.nseq *= segments.parts;
+    }
+    delta_back_tc_kernel<kPanels, false><<<(unsigned)(walks * segments.parts), kBackThreads, Back::kBytes, stream>>>(q, k, o, w);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     e = cudaFuncSetAttribute(delta_grad_tc_kernel<kPanels>, cudaFuncAttributeMaxDynamicSharedMemorySize, Grad::kBytes);
     if (e != cudaSuccess) return e;
@@ -1125,7 +1187,9 @@ bool ssd_delta_tc_bwd_handles(const SsdDeltaBwd &b) {
     return ssd_delta_tc_bwd_sizes(b.in) && ssd_delta_tc_inputs(b.in) && on_16(b.dout) && b.do_stride % 8 == 0 &&
            on_16(b.checkpoints) && on_16(b.dfinal) && on_16(b.dinit);
 }
-size_t ssd_delta_tc_bwd_workspace(const SsdDelta &d) { return ssd_delta_tc_bwd_sizes(d) ? plan_of(d).total : 0; }
+size_t ssd_delta_tc_bwd_workspace(const SsdDelta &d, int sms) {
+    return ssd_delta_tc_bwd_sizes(d) ? plan_of(d, sms).total : 0;
+}
 
 cudaError_t ssd_launch_delta_bwd_tc(const SsdDeltaBwd &a, void *ws, int sms, unsigned *err, cudaStream_t stream) {
     return a.in.n <= 64 ? launch<1>(a, ws, sms, err, stream) : launch<2>(a, ws, sms, err, stream);

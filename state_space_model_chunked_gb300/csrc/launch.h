@@ -399,7 +399,7 @@ cudaError_t ssd_launch_delta_fwd_tc(const SsdDeltaFwd &a, void *ws, int sms, uns
                                     cudaStream_t stream);
 // Its gradients (delta_tc_bwd.cu); ws: ssd_delta_tc_bwd_workspace bytes.
 bool ssd_delta_tc_bwd_handles(const SsdDeltaBwd &b);
-size_t ssd_delta_tc_bwd_workspace(const SsdDelta &d);
+size_t ssd_delta_tc_bwd_workspace(const SsdDelta &d, int sms);
 cudaError_t ssd_launch_delta_bwd_tc(const SsdDeltaBwd &a, void *ws, int sms, unsigned *err, cudaStream_t stream);
 // dq and dk from the sums of `parts` neighbours of [token][groups * parts][N] (delta_simt.cu).
 cudaError_t ssd_launch_delta_group_sums(const float *dq_parts, void *dq, long long dq_stride, const float *dk_parts,

@@ -61,14 +61,22 @@ def test_growth_and_resets_in_parts():
     assert rel(host(final), last) <= STATE["bf16"]
 
 
-def test_gradients_of_a_long_sequence():
-    x, init, do, dfinal = remembered(6, 3200, 1, 1, 2, 64, 64, "bf16")
-    b = [t[None] for t in x.values()]
-    _, _, kept = ssd.delta_scan_fwd(*b, init, return_checkpoints=True)
-    got = ssd.delta_scan_bwd(do[None], *b, kept, dfinal)
-    want = ref.delta_bwd(host(do), *map(host, x.values()), host(init), host(dfinal), [0, 3200], 64 ** -0.5)
-    for a, w in zip(got, want):
-        assert rel(host(a).reshape(w.shape), w) <= (BAR["bf16"] if a.dtype == torch.bfloat16 else STATE["bf16"])
+BACK = [([1700], 1, 1, 128, 128), ([1540], 2, 4, 64, 64), ([3000], 1, 1, 24, 72), ([0, 1600, 64, 4500, 1], 1, 2, 40, 40),
+        ([3100], 16, 32, 8, 16), ([3200], 1, 2, 64, 64), ([700, 2500, 900], 2, 2, 128, 64)]
+
+
+@pytest.mark.parametrize("lengths,groups,heads,p,n", BACK)
+@pytest.mark.parametrize("behind", [False, True])
+def test_gradients_in_parts(lengths, groups, heads, p, n, behind):
+    cu = sequences(lengths)
+    x, init, do, dfinal = remembered(sum(lengths) + n, cu[-1], len(lengths), groups, heads, p, n, "bf16")
+    _, _, kept = ssd.delta_scan_fwd(*x.values(), init, cu_seqlens=cu, return_checkpoints=True)
+    run = lambda: ssd.delta_scan_bwd(do, *x.values(), kept, dfinal if behind else None, cu_seqlens=cu)   # noqa: E731
+    got = run()
+    want = ref.delta_bwd(host(do), *map(host, x.values()), host(init), host(dfinal) * behind, cu, n ** -0.5)
+    for name, a, w in zip(("dq", "dk", "dv", "dg", "dbeta", "dinit"), got, want):
+        assert rel(host(a).reshape(w.shape), w) <= (BAR["bf16"] if a.dtype == torch.bfloat16 else STATE["bf16"]), name
+    assert all(torch.equal(a, b) for a, b in zip(got, run()))
 
 
 def test_the_final_state_in_the_initial_one_s_place():
