@@ -17,7 +17,7 @@ TIMEOUT = 4   # SSD_ERR_TIMEOUT
 
 @pytest.mark.parametrize("backward", [False, True])
 @pytest.mark.parametrize("limit_ns", [1, 3_000, 20_000, 2_000_000])
-@pytest.mark.parametrize("length,p,n", [(300, 128, 128), (40, 64, 64)])
+@pytest.mark.parametrize("length,p,n", [(300, 128, 128), (40, 64, 64), (1700, 64, 64)])      # the last one in parts
 def test_withheld_product_times_out_then_next_call_is_correct(length, p, n, limit_ns, backward):
     x, init, do, dfinal = inputs(length, length, 1, 1, 3, p, n, "bf16")
     b = batched(x, 1)
