@@ -23,7 +23,7 @@
 // Bound by the fp32 pipe: about 4 P N multiply-adds a token forward, 12 backward, where one
 // head's tokens follow each other at the latency of a token's two sums over eight lanes.
 // 4 x 77 tokens, 8 heads of 64 x 64: 22 us, 0.29 a token.  8 x 2047 tokens, 16 heads of
-// 128 x 128: 2.25 ms (15 TFLOP/s), gradients 8.65 ms.
+// 128 x 128: 2.15 ms (16 TFLOP/s), gradients 8.6 ms.
 #include "launch.h"
 #include "ptx.cuh"
 
@@ -246,16 +246,29 @@ __global__ void __launch_bounds__(kThreads) delta_walk_kernel(const Walk a) {
             if (a.checkpoints && t0 % kC == 0)
                 S.store(a.checkpoints + ((size_t)ssd_delta_slot(first, seq, t0 / kC) * d.heads + head) * size, d.n);
         }
+        // Where a lane has many columns and one row, a token's keys and queries are read while the
+        // one in front is in its sums (16384 tokens, 32 heads of 128 x 128: 6.8 -> 5.9 ms; with 8
+        // columns, 77 tokens of 64 x 64, 22 -> 24 us; with two rows and all SMs full 2.8 -> 2.9 ms).
+        constexpr bool kEarly = kV > 8 && kR == 1;
+        float kc[kV], qc[kV], f, be, v[kR];
+        const auto read = [&](int t, float (&kt)[kV], float (&qt)[kV], float &ft, float &bt, float (&vt)[kR]) {
+            columns(m.k[t], S.lane, kt);
+            if constexpr (!kU) columns(m.q[t], S.lane, qt);
+            ft = m.decay[t];
+            bt = m.beta[t];
+#pragma unroll
+            for (int r = 0; r < kR; ++r) vt[r] = m.v[t][r * kRowsPass + threadIdx.x / kLanes];
+        };
+        if constexpr (kEarly) read(0, kc, qc, f, be, v);
         for (int t = 0; t < tokens; ++t) {
-            float kc[kV], qc[kV], sk[kR], sq[kR];
-            columns(m.k[t], S.lane, kc);
-            if constexpr (!kU) columns(m.q[t], S.lane, qc);
-            const float f = m.decay[t], be = m.beta[t];
+            float sk[kR], sq[kR], kn[kV], qn[kV], fn, bn, vn[kR];
+            if constexpr (!kEarly) read(t, kc, qc, f, be, v);
 #pragma unroll
             for (int r = 0; r < kR; ++r) {
                 sk[r] = dot(S.s[r], kc);
                 if constexpr (!kU) sq[r] = dot(S.s[r], qc);
             }
+            if constexpr (kEarly) read(t + 1 < kTile ? t + 1 : t, kn, qn, fn, bn, vn);
 #pragma unroll
             for (int o = kLanes / 2; o > 0; o >>= 1)
 #pragma unroll
@@ -265,7 +278,7 @@ __global__ void __launch_bounds__(kThreads) delta_walk_kernel(const Walk a) {
                 }
 #pragma unroll
             for (int r = 0; r < kR; ++r) {
-                const float u = be * (m.v[t][r * kRowsPass + threadIdx.x / kLanes] - f * sk[r]);
+                const float u = be * (v[r] - f * sk[r]);
 #pragma unroll
                 for (int i = 0; i < kV; ++i) S.s[r][i] = f * S.s[r][i] + u * kc[i];
                 if (S.lane == 0 && S.row[r] >= 0) {
@@ -273,6 +286,16 @@ __global__ void __launch_bounds__(kThreads) delta_walk_kernel(const Walk a) {
                     if constexpr (kU) a.u[(size_t)(first + t0 + t) * d.heads * d.p + at] = u;
                     else store(a.o, (size_t)(first + t0 + t) * a.o_stride + at, d.bf16, d.scale * (f * sq[r] + u * m.kq[t]));
                 }
+                if constexpr (kEarly) v[r] = vn[r];
+            }
+            if constexpr (kEarly) {
+#pragma unroll
+                for (int i = 0; i < kV; ++i) {
+                    kc[i] = kn[i];
+                    if constexpr (!kU) qc[i] = qn[i];
+                }
+                f = fn;
+                be = bn;
             }
         }
     }
