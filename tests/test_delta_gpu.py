@@ -353,3 +353,36 @@ def test_refusals():
                 lambda: ssd.delta_state_update(init.bfloat16(), *(x[i][:2].float() for i in x))):
         with pytest.raises(ssd.SsdError):
             bad()
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_short_and_long_way_of_a_call_agree(packed, dtype):
+    """Calls that leave everything to be allocated go through compiled marshalling, others
+    through Python: equal bits, with column ranges of one matrix and an outer dimension of one."""
+    groups, heads, p, n = 2, 4, 64, 32
+    lead = (150,) if packed else (3, 50)
+    x, init, do, dfinal = inputs(21, 150, 3, groups, heads, p, n, dtype)
+    wide = torch.zeros((*lead, 2 * groups * n + heads * p), dtype=DT[dtype], device="cuda")
+    cuts = {"q": wide[..., :groups * n].unflatten(-1, (groups, n)),
+            "k": wide[..., groups * n:2 * groups * n].unflatten(-1, (groups, n)),
+            "v": wide[..., 2 * groups * n:].unflatten(-1, (heads, p))}
+    for name, t in cuts.items():
+        t.copy_(x[name].view(t.shape))
+        x[name] = t
+    for name in ("g", "beta"):
+        x[name] = x[name].view(*lead, heads)
+    do = do.view(*lead, heads, p)
+    cu = [0, 20, 20, 150] if packed else None
+    cud = torch.tensor(cu, dtype=torch.int32, device="cuda") if packed else None
+    kw = dict(cu_seqlens=cu, cu_seqlens_dev=cud)
+    short = ssd.delta_scan_fwd(*x.values(), init, scale=0.5, return_checkpoints=True, **kw)
+    o = torch.empty_like(short[0])
+    long = ssd.delta_scan_fwd(*x.values(), init, scale=0.5, return_checkpoints=True, o=o, **kw)
+    assert long[0] is o and torch.equal(o, short[0]) and torch.equal(short[1], long[1])
+    assert ssd.delta_scan_fwd(*x.values(), None, return_final=False, **kw)[1] is None
+    back = ssd.delta_scan_bwd(do, *x.values(), short[2], dfinal, scale=0.5, **kw)
+    dq = torch.empty_like(back[0])
+    others = ssd.delta_scan_bwd(do, *x.values(), short[2], dfinal, scale=0.5, dq=dq, **kw)
+    assert others[0] is dq and all(torch.equal(a, b) for a, b in zip(back, others))
+    assert ssd.delta_scan_bwd(do, *x.values(), short[2], return_dinit=False, **kw)[5] is None
