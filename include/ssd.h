@@ -780,8 +780,9 @@ ssd_status ssd_last_device_error(void);
 
 /* Test hook for the bounded device-side waits (the pages have no
  * counterpart).  Every later launch of the tensor-core scan, of the gated
- * recurrence, of the tensor-core product and of the tensor-core delta rule reads the setting; it is process-wide
- * and not synchronised with calls in flight on other host threads.
+ * recurrence, of the tensor-core product and of the tensor-core delta rule
+ * reads the setting; it is process-wide and not synchronised with calls in
+ * flight on other host threads.
  *   fault          SSD_FAULT_NONE: normal operation.  SSD_FAULT_WITHHOLD_SIGNAL:
  *                  in the CTAs of each sequence's first segment, the barrier
  *                  that signals "decay factors ready" waits for one arrival

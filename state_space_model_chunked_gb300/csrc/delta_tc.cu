@@ -39,10 +39,10 @@ using namespace ssddelta;
 
 // ------------------------------------------------------------- chunk matrices
 // One CTA a chunk and key group, the group's heads after each other (or, where that would
-// be few CTAs, a share of them).  The 64 queries
-// over the 64 keys, times the keys, are one product of M = 128, N = 64: a thread's lane is
-// then a row of Q K^T (threads 0 .. 63) or of K K^T (64 .. 127).  The triangle is inverted
-// to fp32's precision: blocks of 16 by substitution, a thread a column, then twice
+// be few CTAs, a share of them).  The 64 queries over the 64 keys, times the keys, are one
+// product of M = 128, N = 64: a thread's lane is then a row of Q K^T (threads 0 .. 63) or of
+// K K^T (64 .. 127).  The triangle is inverted to fp32's precision: blocks of 16 by
+// substitution, a thread a column, then twice
 //     (T11  0; T21  T22),   T21 = -T22 (A21 T11)
 // for blocks of 32 (in fp32) and of 64 (TF32 products of two parts each, 22 bits).
 constexpr int kPrepThreads = 128;

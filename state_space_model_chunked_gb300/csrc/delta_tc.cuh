@@ -58,8 +58,10 @@ __device__ __forceinline__ Split split2(float a, float b) {
 }
 
 // A bounded wait.  After any wait of the CTA has run out, every later one that would have
-// to wait returns false at once; the roles then leave their loops, and the CTA lets its copies and products in
-// flight complete before it ends.
+// to wait returns false at once; the roles then leave their loops, and the CTA lets its
+// copies and products in flight complete before it ends.  (Polls that sleep up to 20 us, or
+// that never sleep, make the forward walk 14 and 22% slower: the waiting warps wake late, or
+// take the working ones' issue slots.)
 struct Waiter {
     volatile int *abort;
     unsigned *err;
