@@ -23,8 +23,8 @@
 //   As forward, factors that are no bf16 values are held in two bf16 parts.
 //   A long sequence of few heads is walked in parts, as forward but from the last one on: 25600
 // tokens, one head 1626 -> 284 us, 32 heads 2790 -> 2130.
-//   8 x 2047 tokens, 16 heads of 128 x 128: 570 us, of which the chunk matrices 60, the walk 137
-// (dS and Z leave at 3.0 TB/s beside 2.4 TB/s of loads) and the second kernel 367: 25000 cycles a
+//   8 x 2047 tokens, 16 heads of 128 x 128: 567 us, of which the chunk matrices 59, the walk 137
+// (dS and Z leave at 3.0 TB/s beside 2.4 TB/s of loads) and the second kernel 363: 25000 cycles a
 // chunk and head for six products in turn, each between two barriers, with 47% of the issue
 // slots, and 220 KB of tiles an SM that leave no room for a second CTA.
 #include "delta_tc.cuh"
@@ -904,7 +904,8 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         bulk_load(al, from + kPanels * kTall, kPanels * kTall, second);
     }
     // dP (lanes 0 .. 63) and dA (64 .. 127), a row a lane; and what pairs of tokens add to dg
-    float sum = 0.f, col, dot = 0.f;
+    float sum = 0.f, col;
+    float2 both = make_float2(0.f, 0.f);
     {
         const int r = row & 63;
         const bool keys = q >= 2;
@@ -919,15 +920,23 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         tmem_ld_wait(m);
         tmem_ld_wait(x);
         float v[16], e[16];
+        const float4 *const columns = reinterpret_cast<const float4 *>(sums + c0);
+        const float2 less = make_float2(-1.f, -1.f), by = make_float2(factor, factor);
+        // (over: what the row has summed up and what is left of the first half behind the column)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const float2 c = sums[c0 + j];
-            const float g = over ? (mine_.x + mine_.y) + ((whole.x - c.x) + (whole.y - c.y))
-                                 : (mine_.x - c.x) + (mine_.y - c.y);
-            const bool in = c0 + j <= last;
-            v[j] = in ? factor * ex2_approx(g) * __uint_as_float(m[j]) : 0.f;
-            e[j] = in && c0 + j < r ? v[j] * __uint_as_float(x[j]) : 0.f;
-            sum += e[j];
+        for (int j = 0; j < 16; j += 2) {
+            const float4 c = columns[j / 2];
+            const float2 from = over ? whole : mine_;
+            float2 g0 = ffma2(make_float2(c.x, c.y), less, from), g1 = ffma2(make_float2(c.z, c.w), less, from);
+            const float more = over ? mine_.x + mine_.y : 0.f;
+            const float2 m2 = fmul2(fmul2(make_float2(ex2_approx(more + (g0.x + g0.y)), ex2_approx(more + (g1.x + g1.y))), by),
+                                    make_float2(__uint_as_float(m[j]), __uint_as_float(m[j + 1])));
+            const float2 e2 = fmul2(m2, make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])));
+            v[j] = c0 + j <= last ? m2.x : 0.f;
+            v[j + 1] = c0 + j + 1 <= last ? m2.y : 0.f;
+            e[j] = c0 + j <= last && c0 + j < r ? e2.x : 0.f;
+            e[j + 1] = c0 + j + 1 <= last && c0 + j + 1 < r ? e2.y : 0.f;
+            sum += e[j] + e[j + 1];
         }
         uint8_t *const to = smem + Lay::kW + (keys ? 2 * kPanel : 0);
         put_parts(to, panel_at(r, c0), v);
@@ -937,21 +946,21 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
     // <S, dS>: both lie alike
     if (!mbar_wait(second, 0, kSsdDefaultWaitNs)) ssd_report(a.err, SSD_DEVERR_TIMEOUT);
     for (uint32_t i = threadIdx.x * 16; i < kPanels * kTall; i += kGradThreads * 16) {
-        const auto pairs = [&](uint32_t hi, uint32_t lo, float (&x)[8]) {
+        const auto pairs = [&](uint32_t hi, uint32_t lo, float2 (&x)[4]) {
             const uint4 h = *reinterpret_cast<const uint4 *>(smem + hi + i), l = *reinterpret_cast<const uint4 *>(smem + lo + i);
             const uint32_t a_[4] = {h.x, h.y, h.z, h.w}, b_[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[2 * j] = __uint_as_float(a_[j] << 16) + __uint_as_float(b_[j] << 16);
-                x[2 * j + 1] = __uint_as_float(a_[j] & 0xffff0000u) + __uint_as_float(b_[j] & 0xffff0000u);
-            }
+            for (int j = 0; j < 4; ++j)
+                x[j] = fadd2(make_float2(__uint_as_float(a_[j] << 16), __uint_as_float(a_[j] & 0xffff0000u)),
+                             make_float2(__uint_as_float(b_[j] << 16), __uint_as_float(b_[j] & 0xffff0000u)));
         };
-        float x[8], y[8];
+        float2 x[4], y[4];
         pairs(Lay::kSs, Lay::kSs + kPanels * kTall, x);
         pairs(Lay::kAh, Lay::kAl, y);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dot += x[j] * y[j];
+        for (int j = 0; j < 4; ++j) both = ffma2(x[j], y[j], both);
     }
+    float dot = both.x + both.y;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
     before();
