@@ -23,8 +23,9 @@ constexpr uint32_t kRecT = 0, kRecP = 2 * kPanel, kRecGates = 4 * kPanel;
 constexpr int kGateW = kC, kGateBeta = 2 * kC, kGateSums = 3 * kC, kGates = 5 * kC;
 constexpr uint32_t kRecord = kRecGates + kGates * 4;
 static_assert(kRecord % 128 == 0, "records are copied to 128-byte boundaries");
-// Where beta is smaller than this the gradients' kernels take this: they divide by it, and
-// what such a token writes is far below fp32's last bit.
+// Where beta is smaller than this the gradients' records have this: dbeta is Z U over its square.
+// Elsewhere such a token's U counts by its beta's share of this (its value may be any size); its Z,
+// which is a gradient times this, is below fp32's last bit of those for keys of some length.
 constexpr float kLeastBeta = 9.094947017729282e-13f;
 
 // Byte of element (row, col) in a panel.

@@ -588,7 +588,8 @@ struct GradSmem {
     static constexpr uint32_t kW = kSs + 4 * kTall;             // V and T; then the parts of dP and of dA
     static constexpr uint32_t kCtl = kW + 4 * kPanel;
     static constexpr uint32_t kGatesAt = kCtl + 64;
-    static constexpr uint32_t kBytes = kGatesAt + kGates * 4;
+    static constexpr uint32_t kShareAt = kGatesAt + kGates * 4;     // of beta in the record's (kLeastBeta), by tokens
+    static constexpr uint32_t kBytes = kShareAt + kC * 4;
     // scratch, where S was (floats)
     static constexpr int kRowSum = 0, kColSum = 512, kAhead = 768, kBehind = 1024, kDbeta = 1280, kWhole = 1536;
 };
@@ -667,6 +668,12 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         tma_load_3d(base + Lay::kW, &mapV, full, 0, head, t);
         bulk_load(base + Lay::kW + 2 * kPanel, a.records + record * kRecord + kRecT, 2 * kPanel, full);
         bulk_load(base + Lay::kGatesAt, a.records + record * kRecord + kRecGates, kGates * 4, full);
+    }
+    // A token whose beta is below kLeastBeta has that in its record, so that dbeta can be had of
+    // Z and U; what reaches other tokens and the gradients of q, k and g is its beta's share of U.
+    if (threadIdx.x < kC) {
+        const float beta = threadIdx.x < valid ? d.beta[(size_t)(token + threadIdx.x) * d.heads + head] : 1.f;
+        reinterpret_cast<float *>(smem + Lay::kShareAt)[threadIdx.x] = fabsf(beta) < kLeastBeta ? fabsf(beta) / kLeastBeta : 1.f;
     }
     // a state's row by a warp: lane l has the columns 4 l .. 4 l + 3; a part's panel is tall
     const bool mine = 4 * lane < d.n;
@@ -797,7 +804,8 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
             mma_ss(tmem + dcol, ad + kStepMn * k, bd + kStepMn * k, idesc_bf16_f32(128, 16 * k + 16, true, true), add || k < 3);
     };
     const float *gates = reinterpret_cast<const float *>(smem + Lay::kGatesAt);
-    // the gates of the warp's 16 tokens
+    // the gates of the warp's 16 tokens (kGates: their betas' shares)
+    static_assert(Lay::kShareAt == Lay::kGatesAt + kGates * 4, "behind the gates");
     const auto gates_of = [&](int which, float (&f)[16]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -820,15 +828,16 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
     for (int i = 0; i < 16; ++i)
         zu[i] = c0 + i < valid && row < d.p ? a.z[z_at(record, c0 + i, row)] : 0.f;
     after();
-    // R, as the left operand of U, and beta R, to which that product is added
+    // R, as the left operand of U (a token's share of it), and beta R, to which that product is added
     {
         uint32_t r[16], hi[8], lo[8];
         tmem_ld16(tq + kColU + c0, r);
         tmem_ld_wait(r);
         const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(smem + Lay::kW) + c0 * 128 + row;
-        float gamma[16], beta[16];
+        float gamma[16], beta[16], share[16];
         gates_of(0, gamma);
         gates_of(kGateBeta, beta);
+        gates_of(kGates, share);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             float x[2];
@@ -839,7 +848,7 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
                 if (c0 + t >= valid) x[j] = 0.f;
                 r[t] = __float_as_uint(x[j] * beta[t]);
             }
-            const Split y = split2(x[0], x[1]);
+            const Split y = split2(x[0] * share[2 * i], x[1] * share[2 * i + 1]);
             hi[i] = y.hi;
             lo[i] = y.lo;
         }
@@ -873,9 +882,11 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_cons
         tmem_ld16(tq + kColU + c0, r);
         tmem_ld_wait(r);
         uint8_t *const to = smem + Lay::kU + (row >> 6) * kPanel;
+        float share[16];
+        gates_of(kGates, share);
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
-            const Split x = split2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+            const Split x = split2(__uint_as_float(r[i]) * share[i], __uint_as_float(r[i + 1]) * share[i + 1]);
             zu[i] *= __uint_as_float(r[i]);
             zu[i + 1] *= __uint_as_float(r[i + 1]);
 #pragma unroll
