@@ -494,6 +494,9 @@ cudaError_t launch_t(S *state, const void *x, const float *dt, const float *A,
     if (num_sms > 0 && stages >= 3 && units >= (size_t)num_sms * 4 && lay.x_bytes % 16 == 0 &&
         lay.bc_bytes % 16 == 0 && lay.state_bytes % 16 == 0) {
         const size_t smem = (size_t)stages * lay.stage_bytes + 16 * stages + 16;
+        // the most of any headdim: the attribute is the kernel's, and another thread may be
+        // about to launch it with more than this call needs
+        constexpr int kStreamMost = (int)kStreamRing + 16 * 8 + 16;
         // programmatic launch hides a launch only where that is worth it: a
         // short call (its griddepcontrol instructions are no-ops otherwise);
         // on stacks of hundreds of states per SM it cost ~1 %
@@ -502,7 +505,7 @@ cudaError_t launch_t(S *state, const void *x, const float *dt, const float *A,
 #define SSD_STREAM_N(NN)                                                                   \
     case NN:                                                                               \
         e = cudaFuncSetAttribute(ssd_decode_stream_kernel<T, S, NN, kFuse>,               \
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);   \
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamMost);  \
         if (e != cudaSuccess) return e;                                                    \
         if (pdl) {                                                                         \
             e = launch_pdl(ssd_decode_stream_kernel<T, S, NN, kFuse>, dim3(num_sms),         \
@@ -916,8 +919,10 @@ cudaError_t launch_multi_k(S *state, const void *x, const float *dt, const float
                            int ntok, int H, int P, int G, int num_sms, const SsdFuse &fuse,
                            cudaStream_t stream) {
     const size_t smem = multi_smem_floats(P, N, kFuse && fuse.z != nullptr) * sizeof(float);
+    // (as for the streaming kernel)
+    const int kMost = (int)(multi_smem_floats(multi_rows(N), N, true) * sizeof(float));
     cudaError_t e = cudaFuncSetAttribute(ssd_decode_multi_kernel<T, S, N, kFuse>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
     if (e != cudaSuccess) return e;
     const size_t units = (size_t)batch * H;
     // programmatic launch for short calls only, as for the streaming kernel

@@ -100,7 +100,8 @@ struct Sort {
 // Shared memory: counts [warp][digit], their sums [digit], the warps' sums; then, where keys
 // stay on chip, two buffers of the CTA's keys with their places.
 constexpr int kSortWords = kSortWarps * (1 << kMostBits) + (1 << kMostBits) + kSortWarps;
-constexpr int kMostLocal = (232448 - 4 * kSortWords) / (16 * 32 * kSortWarps) * 32;        // longest run that fits
+constexpr int kSortMostBytes = 232448;
+constexpr int kMostLocal = (kSortMostBytes - 4 * kSortWords) / (16 * 32 * kSortWarps) * 32;        // longest run that fits
 
 // kLocal: between passes the keys lie in the CTAs' shared memory, else in the workspace.
 template <bool kLocal>
@@ -441,7 +442,9 @@ cudaError_t ssd_launch_embedding_bwd(const SsdEmbeddingBwd &a, void *ws, int sms
     const bool local = s.run <= kMostLocal;
     const auto kernel = local ? sort_tokens_kernel<true> : sort_tokens_kernel<false>;
     const int smem = 4 * kSortWords + (local && s.passes > 1 ? 16 * s.run * kSortWarps : 0);
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // (the most that any call takes: the attribute is the kernel's, and another thread may be
+    // about to launch it with more than this call needs)
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortMostBytes);
     if (e != cudaSuccess) return e;
     kernel<<<ctas, 32 * kSortWarps, smem, stream>>>(s);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;

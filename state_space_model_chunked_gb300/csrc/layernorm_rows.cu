@@ -15,6 +15,7 @@ using namespace ssdnorm;
 using namespace ssdptx;
 
 constexpr int kWarps = 8;
+constexpr int kMostBytes = 232448;      // of shared memory a CTA
 constexpr int kCtasSm(int runs) { return runs <= 4 ? 4 : runs <= 10 ? 2 : 1; }
 
 struct RowsLayout {
@@ -146,7 +147,9 @@ template <typename TX, typename TR, int kC>
 cudaError_t launch(const SsdLayerNormFwd &a, int sms, unsigned *err, cudaStream_t stream) {
     const RowsLayout l = rows_layout(a);
     const auto kernel = layernorm_rows_kernel<TX, TR, kC>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)l.bytes);
+    // (the most that any call takes: the attribute is the kernel's, and another thread may be
+    // about to launch it with more than this call needs)
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostBytes);
     if (e != cudaSuccess) return e;
     int ctas = (int)(233472 / (l.bytes + 1024));
     if (ctas > kCtasSm(kC)) ctas = kCtasSm(kC);
@@ -181,7 +184,7 @@ cudaError_t launch_runs(const SsdLayerNormFwd &a, int sms, unsigned *err, cudaSt
 // CTA is as fast or faster (38912 rows: 126 against 133 us).
 bool ssd_layernorm_rows_handles(const SsdLayerNormFwd &a, int sms) {
     const int nx = a.in == SSD_ELT_F32 ? 4 : 2, nr = a.stream_type == SSD_ELT_F32 ? 4 : 2;
-    return a.out != SSD_ELT_F32 && a.out != SSD_ELT_BF16 && a.rows >= 16ll * sms && a.width % 8 == 0 && a.width <= 4096 && rows_layout(a).bytes <= 232448 &&
+    return a.out != SSD_ELT_F32 && a.out != SSD_ELT_BF16 && a.rows >= 16ll * sms && a.width % 8 == 0 && a.width <= 4096 && rows_layout(a).bytes <= kMostBytes &&
            vec8(a.x, a.x_stride, nx) && vec8(a.residual, a.residual_stride, nr) && vec8(a.residual_out, a.width, nr) &&
            ((uintptr_t)a.y & 7u) == 0;
 }

@@ -29,6 +29,7 @@ constexpr int kT = 64;          // tokens per tile
 constexpr int kPB = 16;         // state rows (headdim columns) per CTA
 constexpr int kThreads = 256;
 constexpr int kMS = kT + 16;    // row stride of the mask tile (bank spread)
+constexpr int kMostStates = 256;
 
 struct SimtSmem {
     int np;                     // padded row stride of the C/B/H tiles (floats)
@@ -226,8 +227,10 @@ cudaError_t launch_t(const void *x, const float *dt, const float *A, const void 
                      const SsdFuse &fuse, const int *cu, SsdProfileEvents prof,
                      cudaStream_t stream) {
     const size_t smem = simt_smem_bytes(N);
+    // (the widest state's: another thread may be about to launch the kernel with more than N's)
     cudaError_t e = cudaFuncSetAttribute(ssd_scan_simt_kernel<T, kFuse>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)simt_smem_bytes(kMostStates));
     if (e != cudaSuccess) return e;
     dim3 grid((P + kPB - 1) / kPB, H, batch);
     if (prof.before && prof.after && (e = ssd_record_event(prof.before, stream)) != cudaSuccess)
