@@ -11,6 +11,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/impl/LocalDispatchKeySet.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -101,9 +102,11 @@ const void *ptr(const at::Tensor *t) { return t ? t->const_data_ptr() : nullptr;
 const float *fptr(const at::Tensor *t) { return t ? t->const_data_ptr<float>() : nullptr; }
 
 // A new array.  Past torch's dispatcher, which takes half a microsecond of the host's time
-// (a layer norm of a few tokens makes four: 10.1 -> 7.9 us a call), unless it has to fill it.
+// (a layer norm of a few tokens makes four: 10.1 -> 7.9 us a call), unless it has to fill the
+// array, or a dispatch mode (or another layer that is on in this thread) is to see it.
 at::Tensor make(at::IntArrayRef shape, at::ScalarType type, const at::Tensor &like) {
-    if (at::globalContext().deterministicAlgorithms())
+    if (at::globalContext().deterministicAlgorithms() ||
+        c10::impl::tls_local_dispatch_key_set().included_ != c10::default_included_set)
         return at::empty(shape, at::TensorOptions().dtype(type).device(like.device()));
     return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
 }
