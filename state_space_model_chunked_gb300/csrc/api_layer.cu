@@ -31,14 +31,6 @@ ssd_status check_workspace(const void *ws, size_t have, size_t need, size_t alig
     return aligned(ws, align) ? SSD_OK : SSD_ERR_INVALID_ARG;
 }
 
-// The longest sequence of a call that check_sequences passed.
-int longest_of(int nseq, int length, const int *host) {
-    if (!host) return length;
-    int most = 0;
-    for (int s = 0; s < nseq; ++s) most = host[s + 1] - host[s] > most ? host[s + 1] - host[s] : most;
-    return most;
-}
-
 bool norm_sizes_ok(long long rows, int width) { return rows >= 0 && width > 0; }
 bool norm_sizes_handled(long long rows, int width) {
     return rows < (1ll << 31) && width < (1 << 24);
@@ -160,7 +152,6 @@ ssd_status delta_input(const void *q, const void *k, const void *v, const float 
     out->bf16 = dtype == SSD_BF16;
     out->nseq = nseq;
     out->length = length;
-    out->longest = longest_of(nseq, length, host);
     out->cu = dev;
     out->heads = nheads;
     out->groups = ngroups;

@@ -24,10 +24,12 @@
 // head's tokens follow each other at the latency of a token's two sums over eight lanes.
 // 4 x 77 tokens, 8 heads of 64 x 64: 22 us, 0.29 a token.  8 x 2047 tokens, 16 heads of
 // 128 x 128: 2.15 ms (16 TFLOP/s), gradients 8.6 ms.
-#include "launch.h"
-#include "ptx.cuh"
+#include "delta_tc.cuh"
 
 namespace {
+
+using ssddelta::chunk_at;
+using ssddelta::ChunkAt;
 
 constexpr int kC = kSsdDeltaChunk;
 constexpr int kThreads = 256, kLanes = 8, kRowsPass = kThreads / kLanes;
@@ -61,15 +63,47 @@ __device__ __forceinline__ void range_of(const SsdDelta &d, int seq, long long &
     }
 }
 
-// A CTA's sequence, head, slab of rows and, where runs of 64 tokens go side by side, run.
-__device__ __forceinline__ void cta_place(const SsdDelta &d, int slabs, int &seq, int &head, int &slab, int &run) {
-    unsigned i = blockIdx.x;
-    slab = (int)(i % slabs);
-    i /= slabs;
-    head = (int)(i % d.heads);
-    i /= d.heads;
-    seq = (int)(i % d.nseq);
-    run = (int)(i / d.nseq);
+// A CTA's head, slab of rows and, where it walks a sequence, that.
+struct Place {
+    int seq, head, slab, len, run;      // run: of 64 tokens, of a sequence's
+    long long first;
+};
+__device__ __forceinline__ Place sequence_place(const SsdDelta &d, int slabs) {
+    Place p{};
+    p.slab = (int)(blockIdx.x % slabs);
+    p.head = (int)(blockIdx.x / slabs % d.heads);
+    p.seq = (int)(blockIdx.x / slabs / d.heads);
+    range_of(d, p.seq, p.first, p.len);
+    return p;
+}
+// Runs of 64 tokens side by side, numbered: sequences of one length have as many runs each;
+// packed ones go by the kept states' slots, at most one more than runs a sequence, whatever the
+// lengths.  (32 sequences of 500 by slots too: 2150 -> 2250 us.)
+__host__ __device__ inline long long runs_of(const SsdDelta &d) {
+    return d.cu ? ssd_delta_slots(d.tokens, d.nseq) : (long long)d.nseq * ((d.length + kC - 1) / kC);
+}
+__device__ __forceinline__ ChunkAt run_at(const SsdDelta &d, long long number) {
+    if (d.cu) return chunk_at(d, number);
+    ChunkAt at;
+    at.seq = (int)(number % d.nseq);
+    at.chunk = (int)(number / d.nseq);
+    at.first = (long long)at.seq * d.length;
+    at.len = d.length;
+    at.live = true;
+    return at;
+}
+// A CTA's run; false: none.
+__device__ __forceinline__ bool run_place(const SsdDelta &d, int slabs, Place &p) {
+    const ChunkAt at = run_at(d, blockIdx.x / slabs / d.heads);
+    p.slab = (int)(blockIdx.x % slabs);
+    p.head = (int)(blockIdx.x / slabs % d.heads);
+    // (the same in every thread, which the compiler cannot see behind a search)
+    const auto same = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    p.seq = same(at.seq);
+    p.first = same((int)at.first);      // (tokens are counted by ints)
+    p.len = same(at.len);
+    p.run = same(at.chunk);
+    return same(at.live);
 }
 
 // One thread's part of the state: kR rows of kV columns.
@@ -185,19 +219,21 @@ __global__ void __launch_bounds__(kThreads) delta_walk_kernel(const Walk a) {
     Tile *const tiles = reinterpret_cast<Tile *>(delta_smem);
     constexpr int kN = kV * kLanes, kRows = kRowsPass * kR;
     const SsdDelta &d = a.d;
-    int seq, head, slab, run;
-    cta_place(d, a.slabs, seq, head, slab, run);
+    Place place;
+    if constexpr (kU) {
+        if (!run_place(d, a.slabs, place)) return;
+    } else {
+        place = sequence_place(d, a.slabs);
+    }
+    const int seq = place.seq, head = place.head, slab = place.slab, run = place.run, len = place.len;
+    const long long first = place.first;
     const int group = head / (d.heads / d.groups);
-    long long first;
-    int len;
-    range_of(d, seq, first, len);
     const size_t size = (size_t)d.p * d.n, state = ((size_t)seq * d.heads + head) * size;
     State<kV, kR> S;
     S.place(slab, d.p);
     int from = 0, to = len;
     if constexpr (kU) {
         from = run * kC;
-        if (from >= len) return;
         to = min(len, from + kC);
         S.load(a.kept + ((size_t)ssd_delta_slot(first, seq, run) * d.heads + head) * size, d.n);
     } else {
@@ -365,12 +401,10 @@ __global__ void __launch_bounds__(kThreads) delta_back_kernel(const Back a) {
     auto &m = *reinterpret_cast<BackSmem<kV, kR> *>(delta_smem);
     constexpr int kN = kV * kLanes, kRows = kRowsPass * kR;
     const SsdDelta &d = a.d;
-    int seq, head, slab, run;
-    cta_place(d, a.slabs, seq, head, slab, run);
+    const Place place = sequence_place(d, a.slabs);
+    const int seq = place.seq, head = place.head, slab = place.slab, len = place.len;
+    const long long first = place.first;
     const int group = head / (d.heads / d.groups);
-    long long first;
-    int len;
-    range_of(d, seq, first, len);
     const size_t size = (size_t)d.p * d.n, state = ((size_t)seq * d.heads + head) * size;
     State<kV, kR> L;
     L.place(slab, d.p);
@@ -454,14 +488,12 @@ __global__ void __launch_bounds__(kThreads) delta_again_kernel(const Back a) {
     auto &m = *reinterpret_cast<BackSmem<kV, kR> *>(delta_smem);
     constexpr int kN = kV * kLanes, kRows = kRowsPass * kR;
     const SsdDelta &d = a.d;
-    int seq, head, slab, run;
-    cta_place(d, a.slabs, seq, head, slab, run);
+    Place place;
+    if (!run_place(d, a.slabs, place)) return;
+    const int seq = place.seq, head = place.head, slab = place.slab, run = place.run, len = place.len;
+    const long long first = place.first;
     const int group = head / (d.heads / d.groups);
-    long long first;
-    int len;
-    range_of(d, seq, first, len);
     const int from = run * kC, to = min(len, from + kC);
-    if (from >= len) return;
     const size_t size = (size_t)d.p * d.n;
     State<kV, kR> S;
     S.place(slab, d.p);
@@ -579,15 +611,14 @@ __global__ void __launch_bounds__(256) delta_group_sum_kernel(const Sums q, cons
 __global__ void __launch_bounds__(128) delta_gates_kernel(const Back a, float *dg, float *dbeta) {
     const SsdDelta &d = a.d;
     const size_t wide = (size_t)d.heads * a.slabs;
-    const long long runs = (d.longest + kC - 1) / kC, all = runs * d.heads * d.nseq;
+    const long long all = runs_of(d) * d.heads;
     for (long long i = (long long)blockIdx.x * 128 + threadIdx.x; i < all; i += (long long)gridDim.x * 128) {
-        const int head = (int)(i % d.heads), seq = (int)(i / d.heads % d.nseq);
-        const int chunk = (int)(i / d.heads / d.nseq);
-        long long first;
-        int len;
-        range_of(d, seq, first, len);
-        if (chunk * kC >= len) continue;
-        const float *anchor = a.anchor + (size_t)ssd_delta_slot(first, seq, chunk) * wide + head * a.slabs;
+        const int head = (int)(i % d.heads);
+        const ChunkAt run = run_at(d, i / d.heads);
+        if (!run.live) continue;
+        const long long first = run.first;
+        const int len = run.len, chunk = run.chunk;
+        const float *anchor = a.anchor + (size_t)ssd_delta_slot(first, run.seq, chunk) * wide + head * a.slabs;
         float at = 0.f;
         for (int s = 0; s < a.slabs; ++s) at += anchor[s];
         for (int t = chunk * kC; t < min(len, chunk * kC + kC); ++t) {
@@ -633,8 +664,10 @@ struct LaunchFwd {
 template <int kV, int kR>
 struct LaunchBack {
     static cudaError_t run(Walk u, Back a, cudaStream_t stream) {
-        const long long ctas = (long long)a.d.nseq * a.d.heads * a.slabs, runs = (a.d.longest + kC - 1) / kC;
-        if (ctas * (runs > 0 ? runs : 1) >= (1ll << 31)) return cudaErrorInvalidValue;
+        // (both below 2^31 for the sizes that the C entry lets pass)
+        const long long ctas = (long long)a.d.nseq * a.d.heads * a.slabs;
+        const long long runs = runs_of(a.d) * a.d.heads * a.slabs;
+        if (runs >= (1ll << 31)) return cudaErrorInvalidValue;
         constexpr int kSmem = (int)sizeof(BackSmem<kV, kR>);
         cudaError_t e = cudaFuncSetAttribute(delta_back_kernel<kV, kR>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
@@ -643,9 +676,9 @@ struct LaunchBack {
         constexpr int kWalk = 2 * (int)sizeof(WalkTile<kV, kR>);
         e = cudaFuncSetAttribute(delta_walk_kernel<kV, kR, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWalk);
         if (e != cudaSuccess) return e;
-        if (runs > 0) delta_walk_kernel<kV, kR, true><<<(unsigned)(ctas * runs), kThreads, kWalk, stream>>>(u);
+        delta_walk_kernel<kV, kR, true><<<(unsigned)runs, kThreads, kWalk, stream>>>(u);
         delta_back_kernel<kV, kR><<<(unsigned)ctas, kThreads, kSmem, stream>>>(a);
-        if (runs > 0) delta_again_kernel<kV, kR><<<(unsigned)(ctas * runs), kThreads, kSmem, stream>>>(a);
+        delta_again_kernel<kV, kR><<<(unsigned)runs, kThreads, kSmem, stream>>>(a);
         return cudaGetLastError();
     }
 };
@@ -704,10 +737,10 @@ cudaError_t ssd_launch_delta_bwd_simt(const SsdDeltaBwd &a, void *ws, cudaStream
     const Back b{d, a.dout, a.checkpoints, a.dfinal, a.do_stride, a.dv_stride, a.dv, a.dinit, at(p.u), at(p.w),
                  at(p.dq), at(p.dk), at(p.anchor), at(p.ov), at(p.rw), p.slabs};
     cudaError_t e = by_shape<LaunchBack>(one_row(d.p), d.n, u, b, stream);
-    if (e != cudaSuccess || d.longest == 0) return e;
+    if (e != cudaSuccess) return e;
     e = ssd_launch_delta_group_sums(b.dq, a.dq, a.dq_stride, b.dk, a.dk, a.dk_stride, d, d.heads / d.groups * p.slabs, stream);
     if (e != cudaSuccess) return e;
-    const long long runs = (d.longest + kC - 1) / kC * (long long)d.heads * d.nseq;
+    const long long runs = runs_of(d) * d.heads;
     delta_gates_kernel<<<blocks_of(runs, 128), 128, 0, stream>>>(b, a.dg, a.dbeta);
     return cudaGetLastError();
 }

@@ -223,7 +223,7 @@ struct SsdDelta {
     const float *g, *beta;
     bool bf16;
     long long tokens;
-    int nseq, length, longest;                  // longest: the longest sequence's tokens
+    int nseq, length;
     const int *cu;
     int heads, groups, p, n;
     long long q_stride, k_stride, v_stride;     // of a token
@@ -234,7 +234,9 @@ struct SsdDelta {
 __host__ __device__ inline long long ssd_delta_slot(long long first, int seq, long long c) {
     return first / kSsdDeltaChunk + seq + c;
 }
-inline long long ssd_delta_slots(long long tokens, int nseq) { return tokens / kSsdDeltaChunk + nseq; }
+__host__ __device__ inline long long ssd_delta_slots(long long tokens, int nseq) {
+    return tokens / kSsdDeltaChunk + nseq;
+}
 struct SsdDeltaFwd {
     SsdDelta in;
     const float *init;
