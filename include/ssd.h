@@ -83,8 +83,9 @@ typedef enum {
 
 typedef enum { SSD_F32 = 0, SSD_BF16 = 1, SSD_FP8_E4M3 = 2 } ssd_dtype;
 
-/* Which kernels ssd_scan_fwd_algo uses.  AUTO takes the tensor-core path when
- * the shape allows it and the SIMT path otherwise; both run on the GPU. */
+/* Which kernels ssd_scan_fwd_algo uses, and the delta rule's calls that end in
+ * _algo.  AUTO takes the tensor-core path when the shape allows it and the SIMT
+ * path otherwise; both run on the GPU. */
 typedef enum {
     SSD_ALGO_AUTO = 0,
     SSD_ALGO_SIMT = 1,      /* exact-fp32 FFMA chunked scan, any shape */
@@ -709,8 +710,9 @@ size_t ssd_embedding_bwd_workspace_bytes(long long count, int vocab, int width);
  *                when that is 0); no initialisation needed.
  * bf16 inputs with dstate <= 128, dstate and headdim multiples of 8 and tokens that start on
  * 16-byte boundaries run on the tensor cores, in chunks of 64 tokens, with factors that are
- * no bf16 values held to 16 bits (states are about 4e-6 of their size off); others in fp32
- * multiply-adds, token by token.  On the tensor cores a long sequence of few heads goes in
+ * no bf16 values held to 16 bits (final states, checkpoints and the fp32 gradients are 3e-6 to
+ * 6e-6 of their size off); others in fp32 multiply-adds, token by token (2e-7), which
+ * ssd_delta_scan_fwd_algo asks for whatever the sizes.  On the tensor cores a long sequence of few heads goes in
  * parts side by side, whose number follows from the sizes and the device's SMs.  Equal calls
  * give equal bits.
  * Requirements: dstate <= 256, headdim <= 2^14, nheads <= 2^16 a multiple of ngroups.
@@ -731,6 +733,21 @@ ssd_status ssd_delta_scan_fwd(const void *q, const void *k, const void *v, const
 size_t ssd_delta_scan_workspace_bytes(ssd_dtype dtype, long long tokens, int nseq, int nheads,
                                       int headdim, int dstate, int ngroups);
 
+/* Same as ssd_delta_scan_fwd with an explicit kernel choice: SSD_ALGO_SIMT takes the fp32
+ * multiply-adds for every size and alignment (no workspace); SSD_ALGO_TCGEN05 returns
+ * SSD_ERR_UNSUPPORTED for types, sizes and alignments that the tensor-core kernels do not
+ * take (0 as the workspace of such sizes). */
+ssd_status ssd_delta_scan_fwd_algo(ssd_algo algo, const void *q, const void *k, const void *v,
+                                   const float *g, const float *beta, ssd_dtype dtype, int nseq,
+                                   int length, const int *cu_seqlens_host, const int *cu_seqlens_dev,
+                                   int nheads, int headdim, int dstate, int ngroups, long long q_stride,
+                                   long long k_stride, long long v_stride, float scale,
+                                   const float *init_state, void *o, long long o_stride,
+                                   float *final_state, float *checkpoints, void *workspace,
+                                   size_t workspace_bytes, cudaStream_t stream);
+size_t ssd_delta_scan_workspace_bytes_algo(ssd_algo algo, ssd_dtype dtype, long long tokens, int nseq,
+                                           int nheads, int headdim, int dstate, int ngroups);
+
 /* Gradients of ssd_delta_scan_fwd.  With L_t the gradient of S_t, which begins with dfinal
  * behind a sequence's last token:
  *     L_t += scale do_t q_t^T,   w_t = L_t k_t,   dv_t = beta_t w_t
@@ -745,7 +762,8 @@ size_t ssd_delta_scan_workspace_bytes(ssd_dtype dtype, long long tokens, int nse
  *   dg, dbeta    float [tokens][nheads].
  *   workspace    ssd_delta_scan_bwd_workspace_bytes() bytes, 256-byte aligned.
  * Sums are fp32 in an order fixed for given sizes and the device's SMs; each result is
- * rounded once.  dq, dk and dv overlap none of the inputs. */
+ * rounded once.  bf16 inputs as for ssd_delta_scan_fwd with headdim <= 128 run on the tensor
+ * cores, others in fp32 multiply-adds.  dq, dk and dv overlap none of the inputs. */
 ssd_status ssd_delta_scan_bwd(const void *dout, const void *q, const void *k, const void *v,
                               const float *g, const float *beta, ssd_dtype dtype, int nseq,
                               int length, const int *cu_seqlens_host, const int *cu_seqlens_dev,
@@ -758,6 +776,22 @@ ssd_status ssd_delta_scan_bwd(const void *dout, const void *q, const void *k, co
 /* (size_t)-1 for invalid sizes. */
 size_t ssd_delta_scan_bwd_workspace_bytes(ssd_dtype dtype, long long tokens, int nseq, int nheads,
                                           int headdim, int dstate, int ngroups);
+
+/* Same as ssd_delta_scan_bwd with an explicit kernel choice, as ssd_delta_scan_fwd_algo; the
+ * checkpoints may be of either choice. */
+ssd_status ssd_delta_scan_bwd_algo(ssd_algo algo, const void *dout, const void *q, const void *k,
+                                   const void *v, const float *g, const float *beta, ssd_dtype dtype,
+                                   int nseq, int length, const int *cu_seqlens_host,
+                                   const int *cu_seqlens_dev, int nheads, int headdim, int dstate,
+                                   int ngroups, long long do_stride, long long q_stride,
+                                   long long k_stride, long long v_stride, float scale,
+                                   const float *checkpoints, const float *dfinal, void *dq,
+                                   long long dq_stride, void *dk, long long dk_stride, void *dv,
+                                   long long dv_stride, float *dg, float *dbeta, float *dinit,
+                                   void *workspace, size_t workspace_bytes, cudaStream_t stream);
+size_t ssd_delta_scan_bwd_workspace_bytes_algo(ssd_algo algo, ssd_dtype dtype, long long tokens,
+                                               int nseq, int nheads, int headdim, int dstate,
+                                               int ngroups);
 
 /* One token of the delta rule: state [batch][nheads][headdim][dstate] of state_dtype (SSD_F32,
  * or SSD_BF16 with bf16 inputs, rounded once) gives state_out, which may be the state itself;

@@ -51,9 +51,13 @@ EXPORTED_SYMBOLS = (
     "ssd_embedding_bwd",
     "ssd_embedding_bwd_workspace_bytes",
     "ssd_delta_scan_fwd",
+    "ssd_delta_scan_fwd_algo",
     "ssd_delta_scan_workspace_bytes",
+    "ssd_delta_scan_workspace_bytes_algo",
     "ssd_delta_scan_bwd",
+    "ssd_delta_scan_bwd_algo",
     "ssd_delta_scan_bwd_workspace_bytes",
+    "ssd_delta_scan_bwd_workspace_bytes_algo",
     "ssd_delta_state_update",
 )
 
@@ -187,9 +191,12 @@ def load():
             "ssd_delta_state_update": [_vp, _int] + [_vp] * 6 + [_int] * 6 +
                                       [ll, ll, ll, f32, _vp, _vp],
         }
+        for name in ("ssd_delta_scan_fwd", "ssd_delta_scan_workspace_bytes", "ssd_delta_scan_bwd",
+                     "ssd_delta_scan_bwd_workspace_bytes"):
+            layer[name + "_algo"] = [_int] + layer[name]
         for name, args in layer.items():
             fn = getattr(lib, name)
-            fn.restype = _sz if name.endswith("_bytes") else _int
+            fn.restype = _sz if "_workspace_bytes" in name else _int
             fn.argtypes = args
         _lib = lib
         return lib

@@ -588,26 +588,71 @@ bool delta_sizes(ssd_dtype dtype, long long tokens, int nseq, int nheads, int he
 }  // namespace
 
 namespace {
-// (which of the two kinds of kernels runs also depends on the addresses)
-size_t delta_bwd_workspace(const SsdDelta &d) {
+bool known_algo(ssd_algo algo) {
+    return algo == SSD_ALGO_AUTO || algo == SSD_ALGO_SIMT || algo == SSD_ALGO_TCGEN05;
+}
+// (which of the two kinds of kernels AUTO takes also depends on the addresses)
+size_t delta_bwd_workspace(ssd_algo algo, const SsdDelta &d) {
     if (d.tokens == 0) return 0;
-    const size_t tc = ssd_delta_tc_bwd_workspace(d, ssd_sm_count()), simt = ssd_delta_bwd_simt_workspace(d);
+    const size_t tc = algo == SSD_ALGO_SIMT ? 0 : ssd_delta_tc_bwd_workspace(d, ssd_sm_count());
+    const size_t simt = algo == SSD_ALGO_TCGEN05 ? 0 : ssd_delta_bwd_simt_workspace(d);
     return tc > simt ? tc : simt;
 }
 }  // namespace
 
+size_t ssd_delta_scan_workspace_bytes_algo(ssd_algo algo, ssd_dtype dtype, long long tokens, int nseq,
+                                           int nheads, int headdim, int dstate, int ngroups) {
+    SsdDelta d{};
+    if (!known_algo(algo) || !delta_sizes(dtype, tokens, nseq, nheads, headdim, dstate, ngroups, &d)) return kBad;
+    return algo == SSD_ALGO_SIMT ? 0 : ssd_delta_tc_workspace(d, ssd_sm_count());
+}
 size_t ssd_delta_scan_workspace_bytes(ssd_dtype dtype, long long tokens, int nseq, int nheads, int headdim,
                                       int dstate, int ngroups) {
-    SsdDelta d{};
-    if (!delta_sizes(dtype, tokens, nseq, nheads, headdim, dstate, ngroups, &d)) return kBad;
-    return ssd_delta_tc_workspace(d, ssd_sm_count());
+    return ssd_delta_scan_workspace_bytes_algo(SSD_ALGO_AUTO, dtype, tokens, nseq, nheads, headdim, dstate, ngroups);
 }
 
+size_t ssd_delta_scan_bwd_workspace_bytes_algo(ssd_algo algo, ssd_dtype dtype, long long tokens, int nseq,
+                                               int nheads, int headdim, int dstate, int ngroups) {
+    SsdDelta d{};
+    if (!known_algo(algo) || !delta_sizes(dtype, tokens, nseq, nheads, headdim, dstate, ngroups, &d)) return kBad;
+    return delta_bwd_workspace(algo, d);
+}
 size_t ssd_delta_scan_bwd_workspace_bytes(ssd_dtype dtype, long long tokens, int nseq, int nheads,
                                           int headdim, int dstate, int ngroups) {
-    SsdDelta d{};
-    if (!delta_sizes(dtype, tokens, nseq, nheads, headdim, dstate, ngroups, &d)) return kBad;
-    return delta_bwd_workspace(d);
+    return ssd_delta_scan_bwd_workspace_bytes_algo(SSD_ALGO_AUTO, dtype, tokens, nseq, nheads, headdim, dstate,
+                                                   ngroups);
+}
+
+ssd_status ssd_delta_scan_fwd_algo(ssd_algo algo, const void *q, const void *k, const void *v,
+                                   const float *g, const float *beta, ssd_dtype dtype, int nseq,
+                                   int length, const int *cu_seqlens_host, const int *cu_seqlens_dev,
+                                   int nheads, int headdim, int dstate, int ngroups, long long q_stride,
+                                   long long k_stride, long long v_stride, float scale,
+                                   const float *init_state, void *o, long long o_stride,
+                                   float *final_state, float *checkpoints, void *workspace,
+                                   size_t workspace_bytes, cudaStream_t stream) {
+    if (!known_algo(algo)) return SSD_ERR_INVALID_ARG;
+    SsdDeltaFwd a{};
+    ssd_status st =
+        delta_input(q, k, v, g, beta, dtype, nseq, length, cu_seqlens_host, cu_seqlens_dev, nheads,
+                    headdim, dstate, ngroups, q_stride, k_stride, v_stride, scale, &a.in);
+    if (st != SSD_OK) return st;
+    if ((a.in.tokens > 0 && !array(o, size_of(dtype))) || o_stride < (long long)nheads * headdim ||
+        !maybe(init_state, 4) || !maybe(final_state, 4) || !maybe(checkpoints, 4))
+        return SSD_ERR_INVALID_ARG;
+    a.init = init_state;
+    a.o = o;
+    a.o_stride = o_stride;
+    a.final_state = final_state;
+    a.checkpoints = checkpoints;
+    const bool tc = algo != SSD_ALGO_SIMT && ssd_delta_tc_handles(a);
+    if (algo == SSD_ALGO_TCGEN05 && !tc && a.in.tokens > 0) return SSD_ERR_UNSUPPORTED;
+    const size_t need = algo == SSD_ALGO_SIMT ? 0 : ssd_delta_tc_workspace(a.in, ssd_sm_count());
+    st = check_workspace(workspace, workspace_bytes, need, 256);
+    if (st != SSD_OK) return st;
+    if (tc)
+        return launched(ssd_launch_delta_fwd_tc(a, workspace, ssd_sm_count(), ssd_device_error_word(), stream));
+    return launched(ssd_launch_delta_fwd_simt(a, ssd_sm_count(), stream));
 }
 
 ssd_status ssd_delta_scan_fwd(const void *q, const void *k, const void *v, const float *g,
@@ -618,35 +663,23 @@ ssd_status ssd_delta_scan_fwd(const void *q, const void *k, const void *v, const
                               const float *init_state, void *o, long long o_stride,
                               float *final_state, float *checkpoints, void *workspace,
                               size_t workspace_bytes, cudaStream_t stream) {
-    SsdDeltaFwd a{};
-    ssd_status st =
-        delta_input(q, k, v, g, beta, dtype, nseq, length, cu_seqlens_host, cu_seqlens_dev, nheads,
-                    headdim, dstate, ngroups, q_stride, k_stride, v_stride, scale, &a.in);
-    if (st != SSD_OK) return st;
-    if ((a.in.tokens > 0 && !array(o, size_of(dtype))) || o_stride < (long long)nheads * headdim ||
-        !maybe(init_state, 4) || !maybe(final_state, 4) || !maybe(checkpoints, 4))
-        return SSD_ERR_INVALID_ARG;
-    st = check_workspace(workspace, workspace_bytes, ssd_delta_tc_workspace(a.in, ssd_sm_count()), 256);
-    if (st != SSD_OK) return st;
-    a.init = init_state;
-    a.o = o;
-    a.o_stride = o_stride;
-    a.final_state = final_state;
-    a.checkpoints = checkpoints;
-    if (ssd_delta_tc_handles(a))
-        return launched(ssd_launch_delta_fwd_tc(a, workspace, ssd_sm_count(), ssd_device_error_word(), stream));
-    return launched(ssd_launch_delta_fwd_simt(a, ssd_sm_count(), stream));
+    return ssd_delta_scan_fwd_algo(SSD_ALGO_AUTO, q, k, v, g, beta, dtype, nseq, length, cu_seqlens_host,
+                                   cu_seqlens_dev, nheads, headdim, dstate, ngroups, q_stride, k_stride, v_stride,
+                                   scale, init_state, o, o_stride, final_state, checkpoints, workspace,
+                                   workspace_bytes, stream);
 }
 
-ssd_status ssd_delta_scan_bwd(const void *dout, const void *q, const void *k, const void *v,
-                              const float *g, const float *beta, ssd_dtype dtype, int nseq,
-                              int length, const int *cu_seqlens_host, const int *cu_seqlens_dev,
-                              int nheads, int headdim, int dstate, int ngroups, long long do_stride,
-                              long long q_stride, long long k_stride, long long v_stride, float scale,
-                              const float *checkpoints, const float *dfinal, void *dq,
-                              long long dq_stride, void *dk, long long dk_stride, void *dv,
-                              long long dv_stride, float *dg, float *dbeta, float *dinit,
-                              void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+ssd_status ssd_delta_scan_bwd_algo(ssd_algo algo, const void *dout, const void *q, const void *k,
+                                   const void *v, const float *g, const float *beta, ssd_dtype dtype,
+                                   int nseq, int length, const int *cu_seqlens_host,
+                                   const int *cu_seqlens_dev, int nheads, int headdim, int dstate,
+                                   int ngroups, long long do_stride, long long q_stride,
+                                   long long k_stride, long long v_stride, float scale,
+                                   const float *checkpoints, const float *dfinal, void *dq,
+                                   long long dq_stride, void *dk, long long dk_stride, void *dv,
+                                   long long dv_stride, float *dg, float *dbeta, float *dinit,
+                                   void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    if (!known_algo(algo)) return SSD_ERR_INVALID_ARG;
     SsdDeltaBwd a{};
     ssd_status st =
         delta_input(q, k, v, g, beta, dtype, nseq, length, cu_seqlens_host, cu_seqlens_dev, nheads,
@@ -665,8 +698,6 @@ ssd_status ssd_delta_scan_bwd(const void *dout, const void *q, const void *k, co
         return launched(dfinal ? cudaMemcpyAsync(dinit, dfinal, bytes, cudaMemcpyDeviceToDevice, stream)
                                : cudaMemsetAsync(dinit, 0, bytes, stream));
     }
-    st = check_workspace(workspace, workspace_bytes, delta_bwd_workspace(a.in), 256);
-    if (st != SSD_OK) return st;
     a.dout = dout;
     a.checkpoints = checkpoints;
     a.dfinal = dfinal;
@@ -680,9 +711,28 @@ ssd_status ssd_delta_scan_bwd(const void *dout, const void *q, const void *k, co
     a.dg = dg;
     a.dbeta = dbeta;
     a.dinit = dinit;
-    if (ssd_delta_tc_bwd_handles(a))
+    const bool tc = algo != SSD_ALGO_SIMT && ssd_delta_tc_bwd_handles(a);
+    if (algo == SSD_ALGO_TCGEN05 && !tc) return SSD_ERR_UNSUPPORTED;
+    st = check_workspace(workspace, workspace_bytes, delta_bwd_workspace(algo, a.in), 256);
+    if (st != SSD_OK) return st;
+    if (tc)
         return launched(ssd_launch_delta_bwd_tc(a, workspace, ssd_sm_count(), ssd_device_error_word(), stream));
     return launched(ssd_launch_delta_bwd_simt(a, workspace, stream));
+}
+
+ssd_status ssd_delta_scan_bwd(const void *dout, const void *q, const void *k, const void *v,
+                              const float *g, const float *beta, ssd_dtype dtype, int nseq,
+                              int length, const int *cu_seqlens_host, const int *cu_seqlens_dev,
+                              int nheads, int headdim, int dstate, int ngroups, long long do_stride,
+                              long long q_stride, long long k_stride, long long v_stride, float scale,
+                              const float *checkpoints, const float *dfinal, void *dq,
+                              long long dq_stride, void *dk, long long dk_stride, void *dv,
+                              long long dv_stride, float *dg, float *dbeta, float *dinit,
+                              void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    return ssd_delta_scan_bwd_algo(SSD_ALGO_AUTO, dout, q, k, v, g, beta, dtype, nseq, length, cu_seqlens_host,
+                                   cu_seqlens_dev, nheads, headdim, dstate, ngroups, do_stride, q_stride, k_stride,
+                                   v_stride, scale, checkpoints, dfinal, dq, dq_stride, dk, dk_stride, dv, dv_stride,
+                                   dg, dbeta, dinit, workspace, workspace_bytes, stream);
 }
 
 ssd_status ssd_delta_state_update(const void *state, ssd_dtype state_dtype, void *state_out,

@@ -12,7 +12,7 @@ from __future__ import annotations
 import torch
 
 from . import layer_ops as _ops
-from ._binding import load
+from ._binding import ALGO_AUTO, load
 from .layer_ops import (_call, _code, _count, _cuda, _full, _index, _out, _plain, _refuse,
                         _row_stride, _scratch, _sequences, _size)
 
@@ -67,15 +67,16 @@ def delta_scan_checkpoints(tokens, nseq):
     return tokens // DELTA_SCAN_CHECKPOINT + nseq
 
 
-def delta_scan_workspace_bytes(dtype, tokens, nseq, heads, headdim, dstate, groups, device=None):
+def delta_scan_workspace_bytes(dtype, tokens, nseq, heads, headdim, dstate, groups, device=None,
+                               algo=ALGO_AUTO):
     """Workspace bytes of delta_scan_fwd on the device."""
-    return _size(_index(device), load().ssd_delta_scan_workspace_bytes, _code(dtype, "dtype"), tokens,
-                 nseq, heads, headdim, dstate, groups)
+    return _size(_index(device), load().ssd_delta_scan_workspace_bytes_algo, algo,
+                 _code(dtype, "dtype"), tokens, nseq, heads, headdim, dstate, groups)
 
 
 def delta_scan_fwd(q, k, v, g, beta, init_state=None, *, scale=None, cu_seqlens=None,
                    cu_seqlens_dev=None, o=None, final_state=None, return_final=True,
-                   checkpoints=None, return_checkpoints=False, workspace=None):
+                   checkpoints=None, return_checkpoints=False, workspace=None, algo=ALGO_AUTO):
     """Gated delta rule, for every head with its state S [headdim, dstate]:
     S' = exp(g_t) S_{t-1}, u_t = beta_t (v_t - S' k_t), S_t = S' + u_t k_t^T,
     o_t = scale S_t q_t (scale: dstate^-0.5 by default).
@@ -86,8 +87,14 @@ def delta_scan_fwd(q, k, v, g, beta, init_state=None, *, scale=None, cu_seqlens=
     multiple of groups.  init_state [nseq, heads, headdim, dstate] f32 or None.
     Returns (o in v's layout, final_state f32 or None), and with return_checkpoints
     the states [delta_scan_checkpoints(tokens, nseq), heads, headdim, dstate] f32
-    that delta_scan_bwd needs."""
-    if o is None and final_state is None and checkpoints is None and workspace is None:
+    that delta_scan_bwd needs.
+
+    algo: ALGO_AUTO runs bf16 inputs on the tensor cores where sizes and alignments
+    allow it, whose f32 results are 3e-6 to 6e-6 of their size off; ALGO_SIMT asks for
+    f32 multiply-adds throughout (2e-7), token by token; ALGO_TCGEN05 refuses what the
+    tensor cores do not take."""
+    if (algo == ALGO_AUTO and o is None and final_state is None and checkpoints is None
+            and workspace is None):
         got = (_ops._marshal_module or _ops._marshal()).delta_scan_fwd(
             q, k, v, g, beta, init_state, scale, cu_seqlens, cu_seqlens_dev, return_final,
             return_checkpoints)
@@ -109,10 +116,10 @@ def delta_scan_fwd(q, k, v, g, beta, init_state=None, *, scale=None, cu_seqlens=
     kept = (delta_scan_checkpoints(tokens, nseq),) + states[1:]
     if checkpoints is None and return_checkpoints:
         checkpoints = torch.empty(kept, dtype=_F32, device=dev)
-    need = _size(at, lib.ssd_delta_scan_workspace_bytes, code, tokens, nseq, heads, headdim, dstate,
-                 groups)
+    need = _size(at, lib.ssd_delta_scan_workspace_bytes_algo, algo, code, tokens, nseq, heads, headdim,
+                 dstate, groups)
     _keep, wp, wb = _scratch(workspace, need, dev)
-    _call(at, lib.ssd_delta_scan_fwd, qp, kp, vp, _full(g, "g", _F32, at, lead + (heads,)),
+    _call(at, lib.ssd_delta_scan_fwd_algo, algo, qp, kp, vp, _full(g, "g", _F32, at, lead + (heads,)),
           _full(beta, "beta", _F32, at, lead + (heads,)), code, nseq, length, cu_ptr, cu_dev, heads,
           headdim, dstate, groups, qs, ks, vs, _scale(scale, dstate),
           _full(init_state, "init_state", _F32, at, states), op, os_,
@@ -121,20 +128,22 @@ def delta_scan_fwd(q, k, v, g, beta, init_state=None, *, scale=None, cu_seqlens=
     return (o, final_state, checkpoints) if return_checkpoints else (o, final_state)
 
 
-def delta_scan_bwd_workspace_bytes(dtype, tokens, nseq, heads, headdim, dstate, groups, device=None):
+def delta_scan_bwd_workspace_bytes(dtype, tokens, nseq, heads, headdim, dstate, groups, device=None,
+                                   algo=ALGO_AUTO):
     """Workspace bytes of delta_scan_bwd on the device."""
-    return _size(_index(device), load().ssd_delta_scan_bwd_workspace_bytes, _code(dtype, "dtype"),
-                 tokens, nseq, heads, headdim, dstate, groups)
+    return _size(_index(device), load().ssd_delta_scan_bwd_workspace_bytes_algo, algo,
+                 _code(dtype, "dtype"), tokens, nseq, heads, headdim, dstate, groups)
 
 
 def delta_scan_bwd(do, q, k, v, g, beta, checkpoints, dfinal=None, *, scale=None, cu_seqlens=None,
                    cu_seqlens_dev=None, dq=None, dk=None, dv=None, dg=None, dbeta=None, dinit=None,
-                   return_dinit=True, workspace=None):
+                   return_dinit=True, workspace=None, algo=ALGO_AUTO):
     """Gradients of delta_scan_fwd: do of o, dfinal [nseq, heads, headdim, dstate]
     f32 of the final state (None: zeros); q, k, v, g, beta, scale and offsets as
     given to it and the checkpoints it returned.  dq, dk and dv may be column ranges
-    of one matrix.  Returns (dq, dk, dv, dg, dbeta, dinit f32 or None)."""
-    if (dq is None and dk is None and dv is None and dg is None and dbeta is None and dinit is None
+    of one matrix.  algo as for delta_scan_fwd (the checkpoints may be of either).
+    Returns (dq, dk, dv, dg, dbeta, dinit f32 or None)."""
+    if (algo == ALGO_AUTO and dq is None and dk is None and dv is None and dg is None and dbeta is None and dinit is None
             and workspace is None):
         got = (_ops._marshal_module or _ops._marshal()).delta_scan_bwd(
             q, k, v, g, beta, dfinal, do, checkpoints, scale, cu_seqlens, cu_seqlens_dev, return_dinit)
@@ -163,10 +172,10 @@ def delta_scan_bwd(do, q, k, v, g, beta, checkpoints, dfinal=None, *, scale=None
     if checkpoints is None:
         raise ValueError("checkpoints is required")
     kept = (delta_scan_checkpoints(tokens, nseq),) + states[1:]
-    need = _size(at, lib.ssd_delta_scan_bwd_workspace_bytes, code, tokens, nseq, heads, headdim,
-                 dstate, groups)
+    need = _size(at, lib.ssd_delta_scan_bwd_workspace_bytes_algo, algo, code, tokens, nseq, heads,
+                 headdim, dstate, groups)
     _keep, wp, wb = _scratch(workspace, need, dev)
-    _call(at, lib.ssd_delta_scan_bwd, dop, qp, kp, vp, _full(g, "g", _F32, at, gates),
+    _call(at, lib.ssd_delta_scan_bwd_algo, algo, dop, qp, kp, vp, _full(g, "g", _F32, at, gates),
           _full(beta, "beta", _F32, at, gates), code, nseq, length, cu_ptr, cu_dev, heads, headdim,
           dstate, groups, dos, qs, ks, vs, _scale(scale, dstate),
           _full(checkpoints, "checkpoints", _F32, at, kept),
