@@ -814,9 +814,9 @@ ssd_status ssd_last_device_error(void);
 
 /* Test hook for the bounded device-side waits (the pages have no
  * counterpart).  Every later launch of the tensor-core scan, of the gated
- * recurrence, of the tensor-core product and of the tensor-core delta rule
- * reads the setting; it is process-wide and not synchronised with calls in
- * flight on other host threads.
+ * recurrence, of the tensor-core product, of the tensor-core delta rule and of
+ * the layer norm of many rows to 8 bits reads the setting; it is process-wide
+ * and not synchronised with calls in flight on other host threads.
  *   fault          SSD_FAULT_NONE: normal operation.  SSD_FAULT_WITHHOLD_SIGNAL:
  *                  in the CTAs of each sequence's first segment, the barrier
  *                  that signals "decay factors ready" waits for one arrival
@@ -829,7 +829,9 @@ ssd_status ssd_last_device_error(void);
  *                  first tile of the walk publishes nothing, so the tiles behind
  *                  it give up after wait_limit_ns each, with the same report.
  *                  In the tensor-core product the first CTA's (or pair of CTAs')
- *                  first accumulator is never announced, with the same end.
+ *                  first accumulator is never announced, with the same end.  In
+ *                  the layer norm of many rows the first row's copy is never
+ *                  complete: its warp gives up, waits once more and ends.
  *   wait_limit_ns  limit of every bounded wait in those kernels but the
  *                  product's waits, at its end, for its own copies and products
  *                  in flight (always the default); 0 restores the default (2 s).

@@ -947,8 +947,13 @@ delta_join_kernel(const SsdDelta d, const float *init, int segments, int part_ha
         float v[kR];
 #pragma unroll
         for (int i = 0; i < kR; ++i) v[i] = on(i) ? to[(size_t)i * n] : 0.f;
-        __syncthreads();
-        if (!mbar_wait(bars + 8 * (s & 1), ((s >> 1) - 1) & 1, kSsdDefaultWaitNs)) ssd_report(err, SSD_DEVERR_TIMEOUT);
+        // (the states in front are there; a CTA that gives up asks for no more maps, and those under
+        // way land before it ends)
+        if (!__syncthreads_and(mbar_wait(bars + 8 * (s & 1), ((s >> 1) - 1) & 1, kSsdDefaultWaitNs))) {
+            if (threadIdx.x == 0) ssd_report(err, SSD_DEVERR_TIMEOUT);
+            for (int t = s; t < segments && t < s + 2; ++t) mbar_wait(bars + 8 * (t & 1), ((t >> 1) - 1) & 1, kSsdDefaultWaitNs);
+            return;
+        }
         const float *map = reinterpret_cast<const float *>(join_smem + (s & 1) * kJoinMap) + col;
         const float *e = states + ((s - 1) & 1) * 128 * kJoinRows + kR * half;
         if (col < n) {

@@ -33,9 +33,16 @@ RowsLayout rows_layout(const SsdLayerNormFwd &a) {
     return l;
 }
 
+// (withhold: the first warp's first copy is never complete)
+struct Waits {
+    unsigned long long limit;
+    bool withhold;
+    unsigned *err;
+};
+
 template <typename TX, typename TR, int kC>
 __global__ void __launch_bounds__(32 * kWarps, kCtasSm(kC))
-layernorm_rows_kernel(const SsdLayerNormFwd a, const RowsLayout l, unsigned *err) {
+layernorm_rows_kernel(const SsdLayerNormFwd a, const RowsLayout l, const Waits wait) {
     extern __shared__ __align__(128) uint8_t rows_smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nvec = a.width / 8;
     const uint32_t bar = smem_u32(rows_smem) + 8 * warp;
@@ -50,7 +57,7 @@ layernorm_rows_kernel(const SsdLayerNormFwd a, const RowsLayout l, unsigned *err
     const uint64_t once = l2_evict_first_policy();      // (207 -> 202 us at the size above)
     const auto fetch = [&](long long row) {
         const uint32_t bx = a.width * sizeof(TX), br = res ? a.width * sizeof(TR) : 0;
-        mbar_arrive_expect_tx(bar, bx + br);
+        mbar_arrive_expect_tx(bar, bx + br + (wait.withhold && row == 0 ? 16 : 0));
         bulk_load_evict_first(smem_u32(mine), static_cast<const TX *>(a.x) + row * a.x_stride, bx, bar, once);
         if (res)
             bulk_load_evict_first(smem_u32(mine + l.r), static_cast<const TR *>(a.residual) + row * a.residual_stride, br, bar, once);
@@ -65,7 +72,12 @@ layernorm_rows_kernel(const SsdLayerNormFwd a, const RowsLayout l, unsigned *err
     __syncthreads();
     const float share = 1.f / (float)a.width;
     for (uint32_t turn = 0; row < a.rows; turn ^= 1, row += step) {
-        if (!mbar_wait(bar, turn, kSsdDefaultWaitNs)) ssd_report(err, SSD_DEVERR_TIMEOUT);
+        // (a warp that gives up asks for no more, and its copy lands before the CTA ends)
+        if (!__all_sync(0xffffffffu, mbar_wait(bar, turn, wait.limit))) {
+            ssd_report(wait.err, SSD_DEVERR_TIMEOUT);
+            mbar_wait(bar, turn, kSsdDefaultWaitNs);
+            return;
+        }
         float s[kC][8], sum = 0.f;
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
@@ -163,7 +175,8 @@ cudaError_t launch(const SsdLayerNormFwd &a, int sms, unsigned *err, cudaStream_
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a, l, err);
+    const SsdDebug debug = ssd_debug_config();
+    return cudaLaunchKernelEx(&cfg, kernel, a, l, Waits{debug.wait_ns, debug.fault == kSsdFaultWithholdSignal, err});
 }
 
 template <typename TX, typename TR>
