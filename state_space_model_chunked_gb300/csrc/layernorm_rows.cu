@@ -15,7 +15,7 @@ using namespace ssdnorm;
 using namespace ssdptx;
 
 constexpr int kWarps = 8;
-constexpr int kMostBytes = 232448;      // of shared memory a CTA
+constexpr int kMostBytes = 232448, kSmBytes = 233472;      // shared memory of a CTA, and of an SM with 1 KB a CTA
 constexpr int kCtasSm(int runs) { return runs <= 4 ? 4 : runs <= 10 ? 2 : 1; }
 
 struct RowsLayout {
@@ -163,7 +163,7 @@ cudaError_t launch(const SsdLayerNormFwd &a, int sms, unsigned *err, cudaStream_
     // about to launch it with more than this call needs)
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostBytes);
     if (e != cudaSuccess) return e;
-    int ctas = (int)(233472 / (l.bytes + 1024));
+    int ctas = (int)(kSmBytes / (l.bytes + 1024));
     if (ctas > kCtasSm(kC)) ctas = kCtasSm(kC);
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -195,10 +195,22 @@ cudaError_t launch_runs(const SsdLayerNormFwd &a, int sms, unsigned *err, cudaSt
 // Rows of 2560 to 8 bits, a warp each against a CTA each: 1216 rows 8.5 against 7.7 us, 2432 rows
 // 11.6 against 12.9, 38912 rows 124 against 169.  To bf16, where no largest value is wanted, a
 // CTA is as fast or faster (38912 rows: 126 against 133 us).
+//   Other widths, us of 65536 rows (above 2560 columns, of as many values as those have), a warp
+// each against a CTA each.  bf16 with a bf16 residual: 256 columns 29 and 30, 776 67 and 112,
+// 1544 117 and 253, 2048 156 and 249, 2560 196 and 283, 2816 315 and 264, 3200 293 and 388, 4096
+// 256 and 315.  In fp32: 512 72 and 71, 1024 142 and 175, 2048 280 and 365, 2560 360 and 409, 2816
+// 404 and 398, 3200 397 and 503.  bf16 with an fp32 residual: 2048 242 and 301, 2560 367 and 317, 2816
+// 421 and 302, 3200 398 and 436.  So a warp each where two CTAs of them fit on an SM; where only one
+// does, if a CTA's row would take four runs a thread, which makes it slow, or the rows are fp32 of
+// up to 2560 columns.
 bool ssd_layernorm_rows_handles(const SsdLayerNormFwd &a, int sms) {
+    if (a.out == SSD_ELT_F32 || a.out == SSD_ELT_BF16 || a.rows < 16ll * sms || a.width % 8 != 0 || a.width > 4096)
+        return false;
     const int nx = a.in == SSD_ELT_F32 ? 4 : 2, nr = a.stream_type == SSD_ELT_F32 ? 4 : 2;
-    return a.out != SSD_ELT_F32 && a.out != SSD_ELT_BF16 && a.rows >= 16ll * sms && a.width % 8 == 0 && a.width <= 4096 && rows_layout(a).bytes <= kMostBytes &&
-           vec8(a.x, a.x_stride, nx) && vec8(a.residual, a.residual_stride, nr) && vec8(a.residual_out, a.width, nr) &&
+    const uint32_t bytes = rows_layout(a).bytes;
+    const bool two = a.width <= 2560 && 2 * (bytes + 1024) <= kSmBytes;
+    if (bytes > kMostBytes || !(two || row_shape(a.width, 8, 4, 4).runs == 4 || (nx == 4 && a.width <= 2560))) return false;
+    return vec8(a.x, a.x_stride, nx) && vec8(a.residual, a.residual_stride, nr) && vec8(a.residual_out, a.width, nr) &&
            ((uintptr_t)a.y & 7u) == 0;
 }
 
