@@ -34,7 +34,8 @@ constexpr int kBwdRuns = 1, kBwdWarpsSm = 16;
 struct Moments {
     float n, mean, q;
     __device__ __forceinline__ void join(float n2, float mean2, float q2) {
-        const float all = n + n2, part = all > 0.f ? __fdividef(n2, all) : 0.f;
+        // (none of its own: the other's, which a quotient near 1 would not be)
+        const float all = n + n2, part = n > 0.f ? __fdividef(n2, all) : 1.f;
         const float d = mean2 - mean;
         mean += d * part;
         q += q2 + d * d * n * part;
@@ -108,11 +109,11 @@ __global__ void __launch_bounds__(32 * kMostWarps) layernorm_fwd_kernel(const Ss
     float w[kC][V], b[kC][V];
     load_weight<V, kC>(a.weight, nvec, w);
     load_weight<V, kC>(a.bias, a.bias ? nvec : 0, b);
-    // this thread's runs, and the reciprocal of its values' number
+    // this thread's runs, and its values' number
     int runs = 0;
 #pragma unroll
     for (int c = 0; c < kC; ++c) runs += (int)(threadIdx.x + c * blockDim.x) < nvec;
-    const float mine = (float)(runs * V), share = runs ? 1.f / mine : 0.f;
+    const float mine = (float)(runs * V);
     for (int turn = 0; row < a.rows; turn ^= 1) {
         float s[kC][V], sum = 0.f, mx = 0.f;
 #pragma unroll
@@ -137,7 +138,8 @@ __global__ void __launch_bounds__(32 * kMostWarps) layernorm_fwd_kernel(const Ss
                 if (i < nvec) ssd_store_vec<V>(so + (size_t)i * V, s[c]);
             }
         }
-        Moments m{mine, sum * share, 0.f};
+        // (divided, not by way of the reciprocal: a row of one bf16 value is its own mean exactly)
+        Moments m{mine, runs ? sum / mine : 0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
             if ((int)(threadIdx.x + c * blockDim.x) >= nvec) continue;

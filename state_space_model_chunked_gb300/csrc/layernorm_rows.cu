@@ -104,7 +104,8 @@ layernorm_rows_kernel(const SsdLayerNormFwd a, const RowsLayout l, const Waits w
             for (int c = 0; c < kC; ++c)
                 if (lane + 32 * c < nvec) ssd_store_vec<8>(so + 8 * (lane + 32 * c), s[c]);
         }
-        const float mean = ssd_warp_sum(sum) * share;
+        // (divided, not by way of the reciprocal: a row of one bf16 value is its own mean exactly)
+        const float mean = ssd_warp_sum(sum) / (float)a.width;
         float squares = 0.f;
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
