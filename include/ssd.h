@@ -760,7 +760,14 @@ size_t ssd_delta_scan_workspace_bytes_algo(ssd_algo algo, ssd_dtype dtype, long 
  *   dfinal, dinit   float [nseq][nheads][headdim][dstate] or NULL (zeros / not wanted).
  *   dq, dk, dv   dtype, laid out as q, k and v, with their own token strides.
  *   dg, dbeta    float [tokens][nheads].
- *   workspace    ssd_delta_scan_bwd_workspace_bytes() bytes, 256-byte aligned.
+ *   workspace    ssd_delta_scan_bwd_workspace_bytes() bytes, 256-byte aligned: enough for
+ *                either kind of kernels, since those that run follow from the addresses too.
+ *                A call needs what ssd_delta_scan_bwd_workspace_bytes_algo() says of the kind
+ *                that it takes: on the tensor cores about 34 KB + 32 KB + 512 bytes a column of
+ *                the state (dstate <= 64: of 64, else of 128) for every 64 tokens of a head, and
+ *                8 dstate bytes a token and head where heads share keys; in fp32
+ *                multiply-adds 8 (headdim + dstate * ceil(headdim / 64)) bytes a token and head
+ *                (by 32 rows where headdim <= 32 or dstate > 128).
  * Sums are fp32 in an order fixed for given sizes and the device's SMs; each result is
  * rounded once.  bf16 inputs as for ssd_delta_scan_fwd with headdim <= 128 run on the tensor
  * cores, others in fp32 multiply-adds.  dq, dk and dv overlap none of the inputs. */

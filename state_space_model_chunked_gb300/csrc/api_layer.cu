@@ -713,7 +713,8 @@ ssd_status ssd_delta_scan_bwd_algo(ssd_algo algo, const void *dout, const void *
     a.dinit = dinit;
     const bool tc = algo != SSD_ALGO_SIMT && ssd_delta_tc_bwd_handles(a);
     if (algo == SSD_ALGO_TCGEN05 && !tc) return SSD_ERR_UNSUPPORTED;
-    st = check_workspace(workspace, workspace_bytes, delta_bwd_workspace(algo, a.in), 256);
+    st = check_workspace(workspace, workspace_bytes,
+                         delta_bwd_workspace(tc ? SSD_ALGO_TCGEN05 : SSD_ALGO_SIMT, a.in), 256);
     if (st != SSD_OK) return st;
     if (tc)
         return launched(ssd_launch_delta_bwd_tc(a, workspace, ssd_sm_count(), ssd_device_error_word(), stream));

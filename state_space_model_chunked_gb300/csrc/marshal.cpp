@@ -647,8 +647,15 @@ PyObject *delta_scan_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const at::Tensor &q = *d.q.t, &v = *d.v.t;
     if (!ok || !like(dout, v) || !kept || kept->scalar_type() != at::kFloat || kept->sizes() != at::IntArrayRef(d.kept))
         Py_RETURN_NONE;
-    const size_t need =
-        ssd_delta_scan_bwd_workspace_bytes((ssd_dtype)d.code, d.s.tokens, d.s.nseq, d.heads, d.p, d.n, d.groups);
+    // the workspace of the kernels that run: where everything lies on 16 bytes the tensor cores'
+    // (0: not for these sizes), else the others'
+    uintptr_t where = (uintptr_t)((dout.stride | d.q.stride | d.k.stride | d.v.stride) * q.element_size());
+    for (const at::Tensor *t : {dout.t, d.q.t, d.k.t, d.v.t, kept, d.state}) where |= (uintptr_t)ptr(t);
+    const auto size = [&](ssd_algo algo) {
+        return ssd_delta_scan_bwd_workspace_bytes_algo(algo, (ssd_dtype)d.code, d.s.tokens, d.s.nseq, d.heads, d.p, d.n, d.groups);
+    };
+    size_t need = where % 16 == 0 ? size(SSD_ALGO_TCGEN05) : 0;
+    if (need == 0) need = size(SSD_ALGO_SIMT);
     if (need == (size_t)-1) Py_RETURN_NONE;
     const auto type = q.scalar_type();
     at::Tensor dq = make(q.sizes(), type, q), dk = make(q.sizes(), type, q), dv = make(v.sizes(), type, q);

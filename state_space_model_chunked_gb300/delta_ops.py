@@ -12,7 +12,7 @@ from __future__ import annotations
 import torch
 
 from . import layer_ops as _ops
-from ._binding import ALGO_AUTO, load
+from ._binding import ALGO_AUTO, ALGO_SIMT, ALGO_TCGEN05, load
 from .layer_ops import (_call, _code, _count, _cuda, _full, _index, _out, _plain, _refuse,
                         _row_stride, _scratch, _sequences, _size)
 
@@ -130,7 +130,8 @@ def delta_scan_fwd(q, k, v, g, beta, init_state=None, *, scale=None, cu_seqlens=
 
 def delta_scan_bwd_workspace_bytes(dtype, tokens, nseq, heads, headdim, dstate, groups, device=None,
                                    algo=ALGO_AUTO):
-    """Workspace bytes of delta_scan_bwd on the device."""
+    """Workspace bytes of delta_scan_bwd on the device (ALGO_AUTO: for whatever
+    alignments)."""
     return _size(_index(device), load().ssd_delta_scan_bwd_workspace_bytes_algo, algo,
                  _code(dtype, "dtype"), tokens, nseq, heads, headdim, dstate, groups)
 
@@ -172,15 +173,22 @@ def delta_scan_bwd(do, q, k, v, g, beta, checkpoints, dfinal=None, *, scale=None
     if checkpoints is None:
         raise ValueError("checkpoints is required")
     kept = (delta_scan_checkpoints(tokens, nseq),) + states[1:]
-    need = _size(at, lib.ssd_delta_scan_bwd_workspace_bytes_algo, algo, code, tokens, nseq, heads,
-                 headdim, dstate, groups)
+    cp, fp, ip = (_full(checkpoints, "checkpoints", _F32, at, kept),
+                  _full(dfinal, "dfinal", _F32, at, states), _full(dinit, "dinit", _F32, at, states))
+    # the workspace of the kernels that run: where everything lies on 16 bytes the tensor cores'
+    # (0: not for these sizes), else the others'
+    sizes, need = (code, tokens, nseq, heads, headdim, dstate, groups), 0
+    query = lib.ssd_delta_scan_bwd_workspace_bytes_algo
+    where = dop | qp | kp | vp | cp | (fp or 0) | (ip or 0) | (dos | qs | ks | vs) * q.element_size()
+    if algo != ALGO_SIMT and where % 16 == 0:
+        need = _size(at, query, ALGO_TCGEN05, *sizes)
+    if need == 0:
+        need = _size(at, query, ALGO_SIMT, *sizes)
     _keep, wp, wb = _scratch(workspace, need, dev)
     _call(at, lib.ssd_delta_scan_bwd_algo, algo, dop, qp, kp, vp, _full(g, "g", _F32, at, gates),
           _full(beta, "beta", _F32, at, gates), code, nseq, length, cu_ptr, cu_dev, heads, headdim,
-          dstate, groups, dos, qs, ks, vs, _scale(scale, dstate),
-          _full(checkpoints, "checkpoints", _F32, at, kept),
-          _full(dfinal, "dfinal", _F32, at, states), dqp, dqs, dkp, dks, dvp, dvs, dgp, dbp,
-          _full(dinit, "dinit", _F32, at, states), wp, wb)
+          dstate, groups, dos, qs, ks, vs, _scale(scale, dstate), cp, fp, dqp, dqs, dkp, dks, dvp,
+          dvs, dgp, dbp, ip, wp, wb)
     return dq, dk, dv, dg, dbeta, dinit
 
 
