@@ -20,14 +20,12 @@ def setup(dtype):
     return b, do.unflatten(0, (NSEQ, -1)), kept, dfinal
 
 
-def peak_of(call):
-    """The most memory above what there was, less the outputs."""
-    call()
-    torch.cuda.synchronize()
-    before = torch.cuda.memory_allocated()
-    torch.cuda.reset_peak_memory_stats()
+def made_by(call):
+    """The bytes of the arrays that a call makes, less its outputs."""
+    count = lambda: torch.cuda.memory_stats()["allocated_bytes.all.allocated"]   # noqa: E731
+    before = count()
     out = call()
-    return torch.cuda.max_memory_allocated() - before - sum(t.numel() * t.element_size() for t in out)
+    return count() - before - sum(t.numel() * t.element_size() for t in out)
 
 
 @pytest.mark.parametrize("long_way", [False, True])
@@ -39,11 +37,11 @@ def test_memory_of_a_call(long_way):
     given = sum(t.numel() * t.element_size() for t in out.values())
     slack = 1 << 20         # (the allocator's rounding)
     for args, need in ((b, tc), (dict(b, k=shifted(b["k"])), simt)):
-        got = peak_of(lambda: ssd.delta_scan_bwd(do, *args.values(), kept, dfinal, **out)) + given
+        got = made_by(lambda: ssd.delta_scan_bwd(do, *args.values(), kept, dfinal, **out)) + given
         assert need - slack <= got <= need + slack, (got, need)
     full, do, kept, dfinal = setup("f32")
     need = ssd.delta_scan_bwd_workspace_bytes(torch.float32, *SIZES)
-    assert abs(peak_of(lambda: ssd.delta_scan_bwd(do, *full.values(), kept, dfinal, **out)) + given - need) <= slack
+    assert abs(made_by(lambda: ssd.delta_scan_bwd(do, *full.values(), kept, dfinal, **out)) + given - need) <= slack
 
 
 @pytest.mark.parametrize("algo", [ssd.ALGO_AUTO, ssd.ALGO_SIMT, ssd.ALGO_TCGEN05])
