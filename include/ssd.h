@@ -714,7 +714,9 @@ size_t ssd_embedding_bwd_workspace_bytes(long long count, int vocab, int width);
  * 6e-6 of their size off); others in fp32 multiply-adds, token by token (2e-7), which
  * ssd_delta_scan_fwd_algo asks for whatever the sizes.  On the tensor cores a long sequence of few heads goes in
  * parts side by side, whose number follows from the sizes and the device's SMs.  Equal calls
- * give equal bits.
+ * give equal bits.  A token's NaN or infinity reaches what the formula says, and on the tensor
+ * cores also outputs of earlier tokens of its chunk (of a sequence's tokens 64 c to 64 c + 63);
+ * nothing of earlier chunks, of other sequences, or of heads that do not read it.
  * Requirements: dstate <= 256, headdim <= 2^14, nheads <= 2^16 a multiple of ngroups.
  * SSD_ERR_INVALID_ARG for null or misaligned pointers, sizes <= 0 (length 0 is allowed),
  * strides below a token's values, bad offsets or a scale that is not finite;
@@ -770,7 +772,9 @@ size_t ssd_delta_scan_workspace_bytes_algo(ssd_algo algo, ssd_dtype dtype, long 
  *                (by 32 rows where headdim <= 32 or dstate > 128).
  * Sums are fp32 in an order fixed for given sizes and the device's SMs; each result is
  * rounded once.  bf16 inputs as for ssd_delta_scan_fwd with headdim <= 128 run on the tensor
- * cores, others in fp32 multiply-adds.  dq, dk and dv overlap none of the inputs. */
+ * cores, others in fp32 multiply-adds.  A NaN or an infinity of dout reaches all gradients
+ * of its token's 64 (as above) and what the formula says in front of them.  dq, dk and dv
+ * overlap none of the inputs. */
 ssd_status ssd_delta_scan_bwd(const void *dout, const void *q, const void *k, const void *v,
                               const float *g, const float *beta, ssd_dtype dtype, int nseq,
                               int length, const int *cu_seqlens_host, const int *cu_seqlens_dev,
