@@ -192,23 +192,27 @@ struct WalkTile {
     float q[kTile][kN], k[kTile][kN], v[kTile][kRows];
     float decay[kTile], beta[kTile], kq[kTile];
 };
-// kTile tokens' rows of `pad` values, in the registers of kThreads threads on their way.
+// kTile tokens' rows of `pad` values, in the registers of kThreads threads on their way: as they
+// lie in memory, since a conversion would wait for the load that it follows.
 template <int kCount>
 struct Ahead {
     static constexpr int kEach = (kCount + kThreads - 1) / kThreads;
-    float x[kEach];
+    uint32_t x[kEach];
     __device__ __forceinline__ void fetch(int pad, const void *from, bool bf16, long long token, long long stride,
                                           size_t offset, int width, int tokens) {
 #pragma unroll
         for (int j = 0; j < kEach; ++j) {
             const int i = threadIdx.x + j * kThreads, t = i / pad, c = i % pad;
-            x[j] = i < kCount && t < tokens && c < width ? load(from, (size_t)(token + t) * stride + offset + c, bf16) : 0.f;
+            x[j] = 0;
+            if (i >= kCount || t >= tokens || c >= width) continue;
+            const size_t at = (size_t)(token + t) * stride + offset + c;
+            x[j] = bf16 ? static_cast<const uint16_t *>(from)[at] : static_cast<const uint32_t *>(from)[at];
         }
     }
-    __device__ __forceinline__ void put(float *to) const {
+    __device__ __forceinline__ void put(float *to, bool bf16) const {
 #pragma unroll
         for (int j = 0; j < kEach; ++j)
-            if (threadIdx.x + j * kThreads < kCount) to[threadIdx.x + j * kThreads] = x[j];
+            if (threadIdx.x + j * kThreads < kCount) to[threadIdx.x + j * kThreads] = __uint_as_float(bf16 ? x[j] << 16 : x[j]);
     }
 };
 
@@ -258,9 +262,9 @@ __global__ void __launch_bounds__(kThreads) delta_walk_kernel(const Walk a) {
     if (from < to) fetch(from);
     for (int t0 = from; t0 < to; t0 += kTile) {
         Tile &m = tiles[(t0 - from) / kTile & 1];
-        ka.put(&m.k[0][0]);
-        if constexpr (!kU) qa.put(&m.q[0][0]);
-        va.put(&m.v[0][0]);
+        ka.put(&m.k[0][0], d.bf16);
+        if constexpr (!kU) qa.put(&m.q[0][0], d.bf16);
+        va.put(&m.v[0][0], d.bf16);
         if (threadIdx.x < kTile) {
             m.decay[threadIdx.x] = decay_of(ga);
             m.beta[threadIdx.x] = ba;
