@@ -708,10 +708,10 @@ size_t ssd_embedding_bwd_workspace_bytes(long long count, int vocab, int width);
  *                sequence, first: its first token on the axis); other places are not written.
  *   workspace    ssd_delta_scan_workspace_bytes() bytes, 256-byte aligned (may be NULL
  *                when that is 0); no initialisation needed.
- * bf16 inputs with dstate <= 128, dstate and headdim multiples of 8 and tokens that start on
- * 16-byte boundaries run on the tensor cores, in chunks of 64 tokens, with factors that are
+ * bf16 inputs with dstate <= 128, dstate and headdim multiples of 8, and tokens and states that
+ * start on 16-byte boundaries run on the tensor cores, in chunks of 64 tokens, with factors that are
  * no bf16 values held to 16 bits (final states, checkpoints and the fp32 gradients are 3e-6 to
- * 6e-6 of their size off); others in fp32 multiply-adds, token by token (2e-7), which
+ * 6e-6 of their size off); others in fp32 multiply-adds, token by token (1e-7), which
  * ssd_delta_scan_fwd_algo asks for whatever the sizes.  On the tensor cores a long sequence of few heads goes in
  * parts side by side, whose number follows from the sizes and the device's SMs.  Equal calls
  * give equal bits.  A token's NaN or infinity reaches what the formula says, and on the tensor
@@ -843,9 +843,10 @@ ssd_status ssd_last_device_error(void);
  *                  first accumulator is never announced, with the same end.  In
  *                  the layer norm of many rows the first row's copy is never
  *                  complete: its warp gives up, waits once more and ends.
- *   wait_limit_ns  limit of every bounded wait in those kernels but the
- *                  product's waits, at its end, for its own copies and products
- *                  in flight (always the default); 0 restores the default (2 s).
+ *   wait_limit_ns  limit of every bounded wait in those kernels but those for a
+ *                  CTA's own copies and products in flight, at its end or where
+ *                  nothing else is waited for (always the default); 0 restores
+ *                  the default (2 s).
  * Returns SSD_ERR_INVALID_ARG for an unknown fault. */
 typedef enum { SSD_FAULT_NONE = 0, SSD_FAULT_WITHHOLD_SIGNAL = 1 } ssd_fault;
 ssd_status ssd_debug_inject_fault(ssd_fault fault, unsigned long long wait_limit_ns);

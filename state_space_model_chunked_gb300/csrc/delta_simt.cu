@@ -23,7 +23,8 @@
 // Bound by the fp32 pipe: about 4 P N multiply-adds a token forward, 12 backward, where one
 // head's tokens follow each other at the latency of a token's two sums over eight lanes.
 // 4 x 77 tokens, 8 heads of 64 x 64: 22 us, 0.29 a token.  8 x 2047 tokens, 16 heads of
-// 128 x 128: 2.15 ms (16 TFLOP/s), gradients 8.6 ms.
+// 128 x 128: 2.14 ms (16 TFLOP/s), in bf16 2.16, gradients 8.7 ms.  States and fp32 gradients
+// are 1e-7 of their size off, those of g 5e-7.
 #include "delta_tc.cuh"
 
 namespace {
@@ -287,7 +288,7 @@ __global__ void __launch_bounds__(kThreads) delta_walk_kernel(const Walk a) {
                 S.store(a.checkpoints + ((size_t)ssd_delta_slot(first, seq, t0 / kC) * d.heads + head) * size, d.n);
         }
         // Where a lane has many columns and one row, a token's keys and queries are read while the
-        // one in front is in its sums (16384 tokens, 32 heads of 128 x 128: 6.8 -> 5.9 ms; with 8
+        // one in front is in its sums (16384 tokens, 32 heads of 128 x 128: 6.8 -> 5.8 ms; with 8
         // columns, 77 tokens of 64 x 64, 22 -> 24 us; with two rows and all SMs full 2.8 -> 2.9 ms).
         constexpr bool kEarly = kV > 8 && kR == 1;
         float kc[kV], qc[kV], f, be, v[kR];

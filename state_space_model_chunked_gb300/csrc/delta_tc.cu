@@ -22,7 +22,7 @@
 // (16 bits), the product of two second parts left out: with one part the state, which is
 // handed on in fp32, would be off by 3e-3 of itself, with two it is by 4e-6.
 //
-// 65536 tokens, 32 heads of 128 x 128: 1746 us, of which the chunk matrices 368 (their records
+// 65536 tokens, 32 heads of 128 x 128: 1743 us, of which the chunk matrices 368 (their records
 // of 34 KB a chunk and head are written at 3.0 TB/s; 50% of the issue slots, ten barriers a
 // head, five CTAs an SM), the parts' ends and maps 650, their joining 18, the walks 700.  47
 // sequences of 1394 on average, 24 heads of 64 x 128: 717 us, of which 262 and 450.  A walk is

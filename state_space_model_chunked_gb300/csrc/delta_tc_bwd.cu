@@ -23,8 +23,8 @@
 //   As forward, factors that are no bf16 values are held in two bf16 parts.
 //   A long sequence of few heads is walked in parts, as forward but from the last one on: 25600
 // tokens, one head 1626 -> 284 us, 32 heads 2790 -> 2130.
-//   8 x 2047 tokens, 16 heads of 128 x 128: 567 us, of which the chunk matrices 59, the walk 137
-// (dS and Z leave at 3.0 TB/s beside 2.4 TB/s of loads) and the second kernel 363: 25000 cycles a
+//   8 x 2047 tokens, 16 heads of 128 x 128: 570 us, of which the chunk matrices 59, the walk 137
+// (dS and Z leave at 3.0 TB/s beside 2.4 TB/s of loads) and the second kernel 367: 25000 cycles a
 // chunk and head for six products in turn, each between two barriers, with 47% of the issue
 // slots, and 220 KB of tiles an SM that leave no room for a second CTA.
 #include "delta_tc.cuh"

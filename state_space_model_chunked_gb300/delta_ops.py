@@ -91,7 +91,7 @@ def delta_scan_fwd(q, k, v, g, beta, init_state=None, *, scale=None, cu_seqlens=
 
     algo: ALGO_AUTO runs bf16 inputs on the tensor cores where sizes and alignments
     allow it, whose f32 results are 3e-6 to 6e-6 of their size off; ALGO_SIMT asks for
-    f32 multiply-adds throughout (2e-7), token by token; ALGO_TCGEN05 refuses what the
+    f32 multiply-adds throughout (1e-7), token by token; ALGO_TCGEN05 refuses what the
     tensor cores do not take."""
     if (algo == ALGO_AUTO and o is None and final_state is None and checkpoints is None
             and workspace is None):
