@@ -88,3 +88,27 @@ def test_single_tokens_and_scans_of_several_state_sizes():
         B, C = torch.randn((1, 64, 1, n), **dev), torch.randn((1, 64, 1, n), **dev)
         made.append(lambda _, a=(x, dt, A, B, C): ssd.scan_fwd(*a))
     assert at_once(*made, times=2000) == []
+
+
+def test_delta_rules_of_several_streams_side_by_side():
+    """Kernels that take an SM's tensor memory, and others, of calls in flight at once: equal bits."""
+    made = []
+    unit = torch.nn.functional.normalize
+    for seed, (nseq, length, groups, heads, p, n, dtype) in enumerate(((1, 3300, 1, 2, 64, 64, torch.bfloat16), (3, 500, 2, 4, 128, 128, torch.bfloat16),
+                                                                       (2, 300, 1, 2, 60, 100, torch.bfloat16), (5, 200, 2, 2, 64, 128, torch.float32))):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        new = lambda *s: torch.randn(s, device="cuda", generator=gen)   # noqa: E731
+        x = [unit(new(nseq, length, groups, n), dim=-1).to(dtype), unit(new(nseq, length, groups, n), dim=-1).to(dtype),
+             new(nseq, length, heads, p).to(dtype), -0.1 * new(nseq, length, heads).abs(), new(nseq, length, heads).sigmoid()]
+        do = new(nseq, length, heads, p).to(dtype)
+        w, wide = new(256, 512).bfloat16(), new(4096, 512).bfloat16()
+
+        def call(_, x=x, do=do, w=w, wide=wide, last=None):
+            o, final, kept = ssd.delta_scan_fwd(*x, return_checkpoints=True)
+            last[:] = [o, final, *ssd.delta_scan_bwd(do, *x, kept), ssd.linear_fwd(wide, w)]
+        want, last = [], []
+        call(None, last=want)
+        made.append((lambda s, call=call, last=last: call(s, last=last), last, want))
+    assert at_once(*(call for call, _, _ in made), times=150) == []
+    for _, last, want in made:
+        assert all(torch.equal(a, b) for a, b in zip(last, want))
