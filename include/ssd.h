@@ -771,8 +771,10 @@ size_t ssd_delta_scan_workspace_bytes_algo(ssd_algo algo, ssd_dtype dtype, long 
  *                multiply-adds 8 (headdim + dstate * ceil(headdim / 64)) bytes a token and head
  *                (by 32 rows where headdim <= 32 or dstate > 128).
  * Sums are fp32 in an order fixed for given sizes and the device's SMs; each result is
- * rounded once.  bf16 inputs as for ssd_delta_scan_fwd with headdim <= 128 run on the tensor
- * cores, others in fp32 multiply-adds.  A NaN or an infinity of dout reaches all gradients
+ * rounded once.  dg is had as sums over a token's 64, of terms as large as dout_t . o_t and
+ * dv_t . v_t: its error goes by their size (fp32 multiply-adds: 1e-7 of it), also where a strong
+ * decay leaves dg itself much smaller.  bf16 inputs as for ssd_delta_scan_fwd with
+ * headdim <= 128 run on the tensor cores, others in fp32 multiply-adds.  A NaN or an infinity of dout reaches all gradients
  * of its token's 64 (as above) and what the formula says in front of them.  dq, dk and dv
  * overlap none of the inputs. */
 ssd_status ssd_delta_scan_bwd(const void *dout, const void *q, const void *k, const void *v,
